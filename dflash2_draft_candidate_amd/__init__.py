@@ -67,12 +67,24 @@ _lib.dflash2_lmhead_topk_workspace_bytes.argtypes = [_ci] * 4
 _lib.dflash2_lmhead_topk_workspace_bytes.restype = _sz
 _lib.dflash2_lmhead_topk.argtypes = [_vp, _vp] + [_ci] * 4 + [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.dflash2_lmhead_topk.restype = _ci
+_lib.dflash2_distill_workspace_bytes.argtypes = [_ci] * 3
+_lib.dflash2_distill_workspace_bytes.restype = _sz
+_lib.dflash2_distill.argtypes = [_vp, _ci, _vp, _vp] + [_ci] * 3 + [_cf, _vp, _vp, _vp, _sz, _vp]
+_lib.dflash2_distill.restype = _ci
+_lib.dflash2_distill_backward.argtypes = [_vp, _ci, _vp, _vp, _vp, _vp] + [_ci] * 3 + \
+    [_cf, _vp, _vp]
+_lib.dflash2_distill_backward.restype = _ci
+_lib.dflash2_distill_step.argtypes = [_vp, _ci, _vp, _vp, _vp] + [_ci] * 3 + \
+    [_cf, _vp, _vp, _vp, _sz, _vp]
+_lib.dflash2_distill_step.restype = _ci
 
 EXPORTS = ("dflash2_version", "dflash2_status_string", "dflash2_workspace_bytes",
            "dflash2_select", "dflash2_select_noalloc", "dflash2_topk_lse_workspace_bytes", "dflash2_topk_lse",
            "dflash2_gate_workspace_bytes", "dflash2_gate", "dflash2_lattice", "dflash2_walk",
            "dflash2_select_ex", "dflash2_walk_ex", "dflash2_dynconv",
-           "dflash2_lmhead_topk_workspace_bytes", "dflash2_lmhead_topk")
+           "dflash2_lmhead_topk_workspace_bytes", "dflash2_lmhead_topk",
+           "dflash2_distill_workspace_bytes", "dflash2_distill", "dflash2_distill_backward",
+           "dflash2_distill_step")
 
 
 class Dflash2Error(RuntimeError):
@@ -372,3 +384,148 @@ def dynconv(x: torch.Tensor, base: torch.Tensor, dyn: torch.Tensor, group: int,
                               _ptr(y), _stream(x.device))
     _check(rc, "dflash2_dynconv")
     return y
+
+
+# ---- distillation from a teacher's top logits ------------------------------------------------
+
+class _on:
+    """Makes `device` the current one for a launch on its stream, if it is not already."""
+
+    def __init__(self, device: torch.device):
+        current = torch.cuda.current_device()
+        index = current if device.index is None else device.index
+        self.guard = None if index == current else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _same_device(device: torch.device, *ts: torch.Tensor):
+    for t in ts:
+        if t.device != device:
+            raise ValueError("tensors must share a device")
+
+
+def _distill_args(student: torch.Tensor, teacher_ids: torch.Tensor,
+                  teacher_logits: torch.Tensor):
+    _contig(student, teacher_ids, teacher_logits)
+    if student.dim() != 2 or teacher_ids.dim() != 2:
+        raise ValueError("student [R, V], teacher_ids and teacher_logits [R, K]")
+    R, V = student.shape
+    K = teacher_ids.shape[1]
+    if teacher_ids.shape != (R, K) or teacher_logits.shape != (R, K):
+        raise ValueError("inconsistent shapes")
+    if teacher_ids.dtype != torch.int32 or teacher_logits.dtype != torch.float32:
+        raise TypeError("teacher_ids int32, teacher_logits float32")
+    _same_device(student.device, teacher_ids, teacher_logits)
+    return R, V, K
+
+
+def _row_vector(t: torch.Tensor, R: int, what: str, student: torch.Tensor):
+    _contig(t)
+    if t.shape != (R,) or t.dtype != torch.float32:
+        raise ValueError(f"{what} must be [R] float32")
+    _same_device(student.device, t)
+
+
+def distill(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+            temperature: float = 1.0):
+    """tau^2 KL(teacher's top entries || student) per row: student [R,V] logits, teacher_ids [R,K]
+    int32 (-1: no entry), teacher_logits [R,K] f32 (topk_lse's cand_ids and unary) ->
+    (loss [R] f32, row_stats [R,2] f32, which distill_backward takes)."""
+    R, V, K = _distill_args(student, teacher_ids, teacher_logits)
+    dev, dt = student.device, _dtype(student)
+    loss = torch.empty((R,), dtype=torch.float32, device=dev)
+    row_stats = torch.empty((R, 2), dtype=torch.float32, device=dev)
+    ws = _workspace(_lib.dflash2_distill_workspace_bytes(R, V, dt), dev)
+    with _on(dev):
+        rc = _lib.dflash2_distill(_ptr(student), dt, _ptr(teacher_ids), _ptr(teacher_logits), R, V,
+                                  K, float(temperature), _ptr(loss), _ptr(row_stats), _ptr(ws),
+                                  ws.numel(), _stream(dev))
+    _check(rc, "dflash2_distill")
+    return loss, row_stats
+
+
+def distill_backward(student: torch.Tensor, teacher_ids: torch.Tensor,
+                     teacher_logits: torch.Tensor, row_stats: torch.Tensor,
+                     grad_loss: torch.Tensor, temperature: float = 1.0,
+                     out: torch.Tensor | None = None):
+    """The gradient of sum_i grad_loss[i] * loss[i] with respect to the student's logits, in their
+    dtype, from distill()'s row_stats. `out` must not overlap `student`."""
+    R, V, K = _distill_args(student, teacher_ids, teacher_logits)
+    _row_vector(grad_loss, R, "grad_loss", student)
+    _contig(row_stats)
+    if row_stats.shape != (R, 2) or row_stats.dtype != torch.float32:
+        raise ValueError("row_stats must be [R, 2] float32")
+    _same_device(student.device, row_stats)
+    dev = student.device
+    grad = _gradient(student, out)
+    with _on(dev):
+        rc = _lib.dflash2_distill_backward(_ptr(student), _dtype(student), _ptr(teacher_ids),
+                                           _ptr(teacher_logits), _ptr(row_stats), _ptr(grad_loss),
+                                           R, V, K, float(temperature), _ptr(grad), _stream(dev))
+    _check(rc, "dflash2_distill_backward")
+    return grad
+
+
+def _gradient(student: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
+    if out is None:
+        return torch.empty_like(student)
+    _contig(out)
+    if out.shape != student.shape or out.dtype != student.dtype:
+        raise ValueError("out must have the student's shape and dtype")
+    _same_device(student.device, out)
+    return out
+
+
+def distill_step(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                 grad_loss: torch.Tensor, temperature: float = 1.0,
+                 out: torch.Tensor | None = None):
+    """Loss and gradient in one call, for a training step that knows grad_loss [R] beforehand
+    (weights / number of rows): -> (loss [R] f32, gradient [R,V] of the student's dtype)."""
+    R, V, K = _distill_args(student, teacher_ids, teacher_logits)
+    _row_vector(grad_loss, R, "grad_loss", student)
+    dev, dt = student.device, _dtype(student)
+    loss = torch.empty((R,), dtype=torch.float32, device=dev)
+    grad = _gradient(student, out)
+    ws = _workspace(_lib.dflash2_distill_workspace_bytes(R, V, dt), dev)
+    with _on(dev):
+        rc = _lib.dflash2_distill_step(_ptr(student), dt, _ptr(teacher_ids), _ptr(teacher_logits),
+                                       _ptr(grad_loss), R, V, K, float(temperature), _ptr(loss),
+                                       _ptr(grad), _ptr(ws), ws.numel(), _stream(dev))
+    _check(rc, "dflash2_distill_step")
+    return loss, grad
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, student, teacher_ids, teacher_logits, temperature):
+        loss, row_stats = distill(student, teacher_ids, teacher_logits, temperature)
+        ctx.save_for_backward(student, teacher_ids, teacher_logits, row_stats)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        student, teacher_ids, teacher_logits, row_stats = ctx.saved_tensors
+        grad_loss = grad_loss.contiguous()
+        if grad_loss.data_ptr() % 16:  # a view into another gradient
+            grad_loss = grad_loss.clone()
+        grad = distill_backward(student, teacher_ids, teacher_logits, row_stats, grad_loss,
+                                ctx.temperature)
+        return grad, None, None, None
+
+
+def distill_loss(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                 temperature: float = 1.0) -> torch.Tensor:
+    """distill() under autograd: loss [R] f32, differentiable (once) in the student's logits. The
+    teacher's side is a constant."""
+    if teacher_logits.requires_grad:
+        raise ValueError("teacher_logits is a constant of the loss: detach it")
+    return _DistillLoss.apply(student, teacher_ids, teacher_logits, float(temperature))

@@ -249,6 +249,80 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
                                          workspace, static_cast<hipStream_t>(stream)));
 }
 
+// Sizes shared by the distillation entry points.
+static int check_distill(int dtype, int R, int V, int K, float temperature) {
+    if (!dtype_ok(dtype) || R < 1 || R > DFLASH2_MAX_DISTILL_ROWS || V < 1 || V > DFLASH2_MAX_V ||
+        K < 1 || K > DFLASH2_MAX_K || !(temperature >= FLT_MIN) || !(temperature <= FLT_MAX))
+        return DFLASH2_ERR_INVALID_ARG;
+    return DFLASH2_OK;
+}
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+static bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
+static int check_workspace(const void *workspace, size_t workspace_bytes, size_t need) {
+    if (need == 0) return DFLASH2_OK;
+    if (!workspace || workspace_bytes < need) return DFLASH2_ERR_WORKSPACE;
+    return aligned16(workspace) ? DFLASH2_OK : DFLASH2_ERR_ALIGNMENT;
+}
+
+size_t dflash2_distill_workspace_bytes(int R, int V, int student_dtype) {
+    if (check_distill(student_dtype, R, V, 1, 1.f) != DFLASH2_OK) return 0;
+    return distill_workspace_bytes(R, V, student_dtype == DFLASH2_F32 ? 4 : 2);
+}
+
+int dflash2_distill(const void *student, int student_dtype, const int32_t *teacher_ids,
+                    const float *teacher_logits, int R, int V, int K, float temperature,
+                    float *loss, float *row_stats, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+    int rc = check_distill(student_dtype, R, V, K, temperature);
+    if (rc) return rc;
+    if ((rc = check_ptrs({student, teacher_ids, teacher_logits, loss, row_stats}))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes,
+                              dflash2_distill_workspace_bytes(R, V, student_dtype))))
+        return rc;
+    return hip_status(launch_distill(student, student_dtype, teacher_ids, teacher_logits, R, V, K,
+                                     temperature, loss, row_stats, workspace,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int dflash2_distill_backward(const void *student, int student_dtype, const int32_t *teacher_ids,
+                             const float *teacher_logits, const float *row_stats,
+                             const float *grad_loss, int R, int V, int K, float temperature,
+                             void *grad_student, void *stream) {
+    int rc = check_distill(student_dtype, R, V, K, temperature);
+    if (rc) return rc;
+    if ((rc = check_ptrs({student, teacher_ids, teacher_logits, row_stats, grad_loss,
+                          grad_student})))
+        return rc;
+    const size_t bytes = (size_t)R * V * (student_dtype == DFLASH2_F32 ? 4 : 2);
+    if (overlap(student, bytes, grad_student, bytes)) return DFLASH2_ERR_INVALID_ARG;
+    return hip_status(launch_distill_backward(student, student_dtype, teacher_ids, teacher_logits,
+                                              row_stats, grad_loss, R, V, K, temperature,
+                                              grad_student, static_cast<hipStream_t>(stream)));
+}
+
+int dflash2_distill_step(const void *student, int student_dtype, const int32_t *teacher_ids,
+                         const float *teacher_logits, const float *grad_loss, int R, int V, int K,
+                         float temperature, float *loss, void *grad_student, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    int rc = check_distill(student_dtype, R, V, K, temperature);
+    if (rc) return rc;
+    if ((rc = check_ptrs({student, teacher_ids, teacher_logits, grad_loss, loss, grad_student})))
+        return rc;
+    const size_t bytes = (size_t)R * V * (student_dtype == DFLASH2_F32 ? 4 : 2);
+    if (overlap(student, bytes, grad_student, bytes)) return DFLASH2_ERR_INVALID_ARG;
+    if ((rc = check_workspace(workspace, workspace_bytes,
+                              dflash2_distill_workspace_bytes(R, V, student_dtype))))
+        return rc;
+    return hip_status(launch_distill_step(student, student_dtype, teacher_ids, teacher_logits,
+                                          grad_loss, R, V, K, temperature, loss, grad_student,
+                                          workspace, static_cast<hipStream_t>(stream)));
+}
+
 size_t dflash2_workspace_bytes(int B, int L, int V, int H, int r, int k) {
     if (B < 1 || L < 1 || H < 1 || r < 1 || r > DFLASH2_MAX_R || rows_of(B, L) > INT_MAX ||
         check_rows((int)rows_of(B, L), V, k) != DFLASH2_OK)

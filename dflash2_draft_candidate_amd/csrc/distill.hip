@@ -1,0 +1,567 @@
+// Distillation of a drafter from its target's top logits: the loss of each row, its gradient, and
+// both in one pass.
+//
+// Student logits z [R, V]; per row K teacher entries (id_j, t_j), as the top-k pass keeps them. With
+//   p_j = softmax_j(t_j / tau) over the row's entries with an id in [0, V),
+//   q_v = softmax_v(z_v / tau) over the whole vocabulary,
+// the row's loss is tau^2 KL(p || q) and its gradient, for the gradient g of the row's loss,
+//   loss = tau^2 sum_j p_j (ln p_j - ln q_{id_j}),
+//   dz_v = g tau (q_v - sum_{j: id_j = v} p_j).
+// (d ln q_j / dz_v = ([v = id_j] - q_v) / tau and the p_j add up to 1.)
+//
+// What is kept of a row between the passes is its maximum m and Sigma = sum_v exp((z_v - m) / tau):
+// relative to the maximum, a 32-bit Sigma carries q to 2^-24 at any size of the logits, where a
+// 32-bit logsumexp of large logits would not.
+//
+// Arithmetic. The row's exponentials and their sums are fp32 (base 2: v_exp_f32 of
+// z s - ref with s = log2(e) / tau in one fma); a thread keeps the reference ref = m s of the largest
+// element it has seen, moved once per batch of loads. ref is whatever fp32 number m s rounds to:
+// the sums of threads, waves and slices are joined in terms of the rounded references, and the
+// last step multiplies by 2^(ref - m s) in fp64, so that rounding cancels. Everything that happens
+// once per row or per teacher entry is fp64 (the loss is a difference of logarithms, and at the
+// teacher's ids the gradient is a difference of probabilities).
+// A row with |m s| >= 2^23 (nothing but masks of the type's lowest value, infinities) has no such
+// reference; it is summed again with exp2((z - m) s), which is exact there too.
+#include <float.h>
+
+#include "device_common.h"
+#include "kernels.h"
+#include "row_slices.h"
+
+namespace dflash2 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kU = 4;              // 16-byte vectors per thread and batch
+constexpr float kMaxRef = 8388608.f;  // 2^23: references stay within this, so each is within 0.5
+                                      // of m s and 2^(m s - ref) cannot overflow
+constexpr float kNoRef = -kMaxRef;    // reference before the first element
+constexpr int kUnitVectors = 2 * kThreads;  // a slice holds at least this many vectors
+
+// ---- element output ------------------------------------------------------------------------
+
+template <typename T> struct Pack;
+template <> struct Pack<float> {
+    static __device__ __forceinline__ u32x4 vec(const float *v) {
+        return u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3])};
+    }
+    static __device__ __forceinline__ void one(float *p, float v) { *p = v; }
+};
+template <> struct Pack<uint16_t> {  // round to nearest even, once
+    static __device__ __forceinline__ uint32_t pair(float lo, float hi) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 h = {(__bf16)lo, (__bf16)hi};
+        return __builtin_bit_cast(uint32_t, h);
+    }
+    static __device__ __forceinline__ u32x4 vec(const float *v) {
+        return u32x4{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+    }
+    static __device__ __forceinline__ void one(uint16_t *p, float v) {
+        *p = __builtin_bit_cast(uint16_t, (__bf16)v);
+    }
+};
+
+// ---- wave reductions in fp64 -----------------------------------------------------------------
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+__device__ __forceinline__ double wave_max64(double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+    return v;
+}
+
+// ---- a row's teacher entries, one per lane of a wave --------------------------------------------
+
+struct Teacher {
+    int id;    // -1: no entry on this lane
+    double p;  // the entry's share of the row's teacher mass
+    double ln_p;
+    bool any;  // wave-uniform: the row has teacher mass
+};
+
+// Entry `lane` of a row: its id (-1: none) and t / tau.
+__device__ __forceinline__ int teacher_entry(const int32_t *ids, const float *logits, int64_t row,
+                                             int K, int V, double inv_tau, int lane, double &a) {
+    a = -INFINITY;
+    if (lane >= K) return -1;
+    const int id = ids[row * K + lane];
+    if (id < 0 || id >= V) return -1;
+    a = (double)logits[row * K + lane] * inv_tau;
+    return id;
+}
+
+// Whether the row has teacher mass (wave-uniform): an entry above -inf, or a NaN.
+__device__ __forceinline__ bool teacher_any(const int32_t *ids, const float *logits, int64_t row,
+                                            int K, int V, double inv_tau, int lane) {
+    double a;
+    teacher_entry(ids, logits, row, K, V, inv_tau, lane, a);
+    return __ballot(a != -INFINITY) != 0ull;
+}
+
+__device__ __forceinline__ Teacher teacher_row(const int32_t *ids, const float *logits,
+                                               int64_t row, int K, int V, double inv_tau,
+                                               int lane) {
+    Teacher t;
+    double a;
+    t.id = teacher_entry(ids, logits, row, K, V, inv_tau, lane, a);
+    const double top = wave_max64(a);  // (ignores NaN; a NaN entry makes the sum NaN)
+    t.any = __ballot(a != -INFINITY) != 0ull;
+    const double e = t.id < 0 || !t.any ? 0.0 : exp(a - top);
+    const double sum = wave_sum64(e);
+    t.p = t.any ? e / sum : 0.0;
+    t.ln_p = a - top - log(sum);
+    return t;
+}
+
+// The row's loss from its statistics (wave-wide; the same value in every lane).
+template <typename T>
+__device__ __forceinline__ double row_loss(const Teacher &t, const T *student, int64_t row, int V,
+                                           double m, double sigma, double tau) {
+    if (!t.any) return 0.0;
+    double term = 0.0;
+    if (t.id >= 0 && t.p != 0.0) {
+        const double z = (double)Elem<T>::load(student, row * V + t.id);
+        const double ln_q = (z - m) / tau - log(sigma);
+        term = t.p * (t.ln_p - (sigma == 0.0 ? -INFINITY : ln_q));
+    }
+    return tau * tau * wave_sum64(term);
+}
+
+// ---- streaming over a unit's vectors -----------------------------------------------------------
+
+// Runs f(vector, index) over a thread's share of n vectors at p (tid, tid + nt, ...): batches of
+// kU vectors with the next batch's loads in flight, then the rest. `g` gets whole batches.
+template <int NT, typename FB, typename FV>
+__device__ __forceinline__ void stream(const u32x4 *p, int n, int tid, FB &&batch, FV &&single) {
+    const int whole = n / (NT * kU);
+    u32x4 cur[kU], nxt[kU];
+    if (whole > 0) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) cur[u] = p[tid + u * NT];
+    }
+    for (int b = 0; b < whole; ++b) {
+        const int base = (b + 1) * NT * kU + tid;
+        if (b + 1 < whole) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) nxt[u] = p[base + u * NT];
+        }
+        batch(cur, base - NT * kU);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) cur[u] = nxt[u];
+    }
+    // the rest: at most kU vectors per thread, loaded together
+    const int base = whole * NT * kU + tid;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+        if (base + u * NT < n) cur[u] = p[base + u * NT];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+        if (base + u * NT < n) single(cur[u], base + u * NT);
+}
+
+// Ragged element `tid` of a unit (its row's ends outside whole vectors): index, or -1.
+__device__ __forceinline__ int64_t ragged_element(const UnitRange &u, int tid) {
+    const int nh = (int)(u.h1 - u.h0);
+    if (tid < nh) return u.h0 + tid;
+    if (tid - nh < (int)(u.t1 - u.t0)) return u.t0 + (tid - nh);
+    return -1;
+}
+
+// ---- row statistics ------------------------------------------------------------------------
+
+struct Stat {
+    float m;    // largest element
+    float ref;  // log2-domain reference: fl(m s)
+    float sum;  // sum of 2^(z s - ref)
+};
+
+template <int N>
+__device__ __forceinline__ void stat_add(Stat &st, const float *x, float s) {
+    float c = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) c = fmaxf(c, x[i]);
+    st.m = fmaxf(st.m, c);
+    const float ref = __builtin_amdgcn_fmed3f(c * s, st.ref, kMaxRef);  // max(st.ref, c s), capped
+    float a0 = st.sum * __builtin_amdgcn_exp2f(st.ref - ref), a1 = 0.f, a2 = 0.f, a3 = 0.f;
+    st.ref = ref;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        a0 += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], s, -ref));
+        if (i + 1 < N) a1 += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i + 1], s, -ref));
+        if (i + 2 < N) a2 += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i + 2], s, -ref));
+        if (i + 3 < N) a3 += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i + 3], s, -ref));
+    }
+    st.sum = (a0 + a1) + (a2 + a3);
+}
+
+__device__ __forceinline__ void stat_join(Stat &a, const Stat &b) {
+    a.m = fmaxf(a.m, b.m);
+    const float r = fmaxf(a.ref, b.ref);
+    a.sum = a.sum * __builtin_amdgcn_exp2f(a.ref - r) + b.sum * __builtin_amdgcn_exp2f(b.ref - r);
+    a.ref = r;
+}
+
+// (a fixed tree: lane l joins l ^ 32, l ^ 16, ...)
+__device__ __forceinline__ Stat wave_stat(Stat st) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        const Stat b{__shfl_xor(st.m, o), __shfl_xor(st.ref, o), __shfl_xor(st.sum, o)};
+        stat_join(st, b);
+    }
+    return st;
+}
+
+// Statistics of a unit, in every thread. `sh` is scratch of kWaves entries; ends with a barrier.
+template <typename T, int NT>
+__device__ __forceinline__ Stat unit_stat(const T *student, const UnitRange &ur, float s, Stat *sh,
+                                          int tid) {
+    constexpr int EV = Elem<T>::kPerVec;
+    Stat st{-INFINITY, kNoRef, 0.f};
+    stream<NT>(
+        reinterpret_cast<const u32x4 *>(student) + ur.c0, ur.nv, tid,
+        [&](const u32x4 *v, int) {
+            float x[kU * EV];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) Elem<T>::unpack(v[u], x + u * EV);
+            stat_add<kU * EV>(st, x, s);
+        },
+        [&](const u32x4 &v, int) {
+            float x[EV];
+            Elem<T>::unpack(v, x);
+            stat_add<EV>(st, x, s);
+        });
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0) {
+        const float x = Elem<T>::load(student, e);
+        stat_add<1>(st, &x, s);
+    }
+    st = wave_stat(st);
+    if ((tid & (kWave - 1)) == 0) sh[tid / kWave] = st;
+    __syncthreads();
+    st = sh[0];
+#pragma unroll
+    for (int w = 1; w < NT / kWave; ++w) stat_join(st, sh[w]);
+    __syncthreads();
+    return st;
+}
+
+// Sigma of a whole row without a usable reference, by one wave: the sum of exp2((z - m) s), 64
+// elements at a time.
+template <typename T>
+__device__ __noinline__ double far_row_sum(const T *student, int64_t row, int V, float m, float s,
+                                           int lane) {
+    double sum = 0.0;
+    for (int v = lane; v < V; v += kWave)
+        sum += (double)__builtin_amdgcn_exp2f((Elem<T>::load(student, row * V + v) - m) * s);
+    return wave_sum64(sum);
+}
+
+// Sigma of a row from its joined statistics (one wave); NaN where the row holds a NaN or +inf, 0
+// where it holds nothing above -inf.
+template <typename T>
+__device__ __forceinline__ double row_sigma(const Stat &st, const T *student, int64_t row, int V,
+                                            float s, int lane) {
+    // nothing moved the reference, so the sum is a NaN only if an element is
+    if (st.m == -INFINITY) return st.sum != st.sum ? (double)st.sum : 0.0;
+    if (!(fabsf(st.m * s) < kMaxRef)) return far_row_sum<T>(student, row, V, st.m, s, lane);
+    return (double)st.sum * exp2((double)st.ref - (double)st.m * (double)s);
+}
+
+struct Args {
+    const int32_t *ids;
+    const float *teacher;
+    int R, V, K;
+    double tau, inv_tau;
+    float s;  // log2(e) / tau
+};
+
+// Forward: a unit (row, slice) per workgroup. One slice: the row's statistics and loss at once;
+// more: the slice's statistics go to `part` [R][S], joined by distill_join_kernel.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void distill_forward_kernel(const T *__restrict__ student,
+                                                                   Args a, int S,
+                                                                   float *__restrict__ loss,
+                                                                   float *__restrict__ row_stats,
+                                                                   Stat *__restrict__ part) {
+    __shared__ Stat sh[kWaves];
+    const int tid = threadIdx.x;
+    const UnitRange ur = unit_range(blockIdx.x, a.V, S, Elem<T>::kPerVec);
+    const Stat st = unit_stat<T, kThreads>(student, ur, a.s, sh, tid);
+    if (S > 1) {
+        if (tid == 0) part[blockIdx.x] = st;
+        return;
+    }
+    if (tid >= kWave) return;
+    const int64_t row = blockIdx.x;
+    const double sigma = row_sigma<T>(st, student, row, a.V, a.s, tid);
+    const Teacher t = teacher_row(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, tid);
+    const double l = row_loss<T>(t, student, row, a.V, (double)st.m, sigma, a.tau);
+    if (tid == 0) {
+        loss[row] = (float)l;
+        row_stats[2 * row] = st.m;
+        row_stats[2 * row + 1] = (float)sigma;
+    }
+}
+
+// Joins the slices of a row and computes its loss: one wave per row.
+template <typename T>
+__global__ __launch_bounds__(kWave) void distill_join_kernel(const T *__restrict__ student, Args a,
+                                                             int S, const Stat *__restrict__ part,
+                                                             float *__restrict__ loss,
+                                                             float *__restrict__ row_stats) {
+    const int lane = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const Teacher t = teacher_row(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, lane);
+    Stat st{-INFINITY, kNoRef, 0.f};
+    for (int i = lane; i < S; i += kWave) stat_join(st, part[row * S + i]);
+    st = wave_stat(st);
+    const double sigma = row_sigma<T>(st, student, row, a.V, a.s, lane);
+    const double l = row_loss<T>(t, student, row, a.V, (double)st.m, sigma, a.tau);
+    if (lane == 0) {
+        loss[row] = (float)l;
+        row_stats[2 * row] = st.m;
+        row_stats[2 * row + 1] = (float)sigma;
+    }
+}
+
+// ---- gradient ------------------------------------------------------------------------------
+
+// The gradient at the teacher's ids of one row, a value per lane; lanes whose id a lower lane
+// holds too, and lanes without an entry, get id -1. Computed in fp64 from the stored logit.
+struct Patch {
+    int id;
+    float value;
+};
+
+template <typename T>
+__device__ __forceinline__ Patch teacher_patch(const Teacher &t, const T *student, int64_t row,
+                                               int V, int K, double m, double sigma, double g,
+                                               double tau, int lane) {
+    Patch out{-1, 0.f};
+    double p = 0.0;
+    bool first = true;
+    for (int i = 0; i < K; ++i) {
+        const int id = __builtin_amdgcn_readlane(t.id, i);
+        const double pi = __shfl(t.p, i);
+        if (id == t.id) {
+            p += pi;
+            if (i < lane) first = false;
+        }
+    }
+    if (t.id >= 0 && first && t.any) {
+        const double z = (double)Elem<T>::load(student, row * V + t.id);
+        const double q = sigma == 0.0 ? 0.0 : exp((z - m) / tau) / sigma;
+        out.id = t.id;
+        out.value = sigma == 0.0 ? 0.f : (float)(g * tau * (q - p));
+    }
+    return out;
+}
+
+// dz over a unit's elements as if no teacher entry were there: coef 2^((z - m) s), coef = g tau /
+// Sigma; zeros where `live` is false. The difference to the maximum comes first: it is exact where
+// q is large.
+template <typename T, int NT>
+__device__ __forceinline__ void unit_gradient(const T *student, const UnitRange &ur, float m,
+                                              float s, float coef, bool live, T *grad, int tid) {
+    constexpr int EV = Elem<T>::kPerVec;
+    u32x4 *out = reinterpret_cast<u32x4 *>(grad) + ur.c0;
+    if (!live) {
+        for (int i = tid; i < ur.nv; i += NT) out[i] = u32x4{0u, 0u, 0u, 0u};
+        const int64_t e = ragged_element(ur, tid);
+        if (e >= 0) Pack<T>::one(grad + e, 0.f);
+        return;
+    }
+    auto one = [&](const u32x4 &v, int i) {
+        float x[EV];
+        Elem<T>::unpack(v, x);
+#pragma unroll
+        for (int k = 0; k < EV; ++k) x[k] = coef * __builtin_amdgcn_exp2f((x[k] - m) * s);
+        out[i] = Pack<T>::vec(x);
+    };
+    stream<NT>(
+        reinterpret_cast<const u32x4 *>(student) + ur.c0, ur.nv, tid,
+        [&](const u32x4 *v, int i) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) one(v[u], i + u * NT);
+        },
+        one);
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0)
+        Pack<T>::one(grad + e,
+                     coef * __builtin_amdgcn_exp2f((Elem<T>::load(student, e) - m) * s));
+}
+
+// The element range of a unit, ragged ends included.
+__device__ __forceinline__ bool unit_holds(const UnitRange &u, int64_t e, int EV) {
+    const int64_t v0 = u.c0 * EV;
+    return (e >= v0 && e < v0 + (int64_t)u.nv * EV) || (e >= u.h0 && e < u.h1) ||
+           (e >= u.t0 && e < u.t1);
+}
+
+// Backward: a unit (row, slice) per workgroup. Wave 0 prepares the values at the teacher's ids
+// while the others start to stream; after the barrier they overwrite what the stream put there.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void distill_backward_kernel(
+    const T *__restrict__ student, Args a, int S, const float *__restrict__ row_stats,
+    const float *__restrict__ grad_loss, T *__restrict__ grad) {
+    const int tid = threadIdx.x;
+    const UnitRange ur = unit_range(blockIdx.x, a.V, S, Elem<T>::kPerVec);
+    const int64_t row = (uint32_t)blockIdx.x / (uint32_t)S;
+    const float m = row_stats[2 * row], sigma = row_stats[2 * row + 1], g = grad_loss[row];
+    Patch patch{-1, 0.f};
+    const int lane = tid & (kWave - 1);
+    const bool live =
+        teacher_any(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, lane) && sigma != 0.f;
+    if (tid < kWave) {
+        const Teacher t = teacher_row(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, lane);
+        patch = teacher_patch<T>(t, student, row, a.V, a.K, (double)m, (double)sigma, (double)g,
+                                 a.tau, lane);
+    }
+    const float coef = (float)((double)g * a.tau / (double)sigma);
+    unit_gradient<T, kThreads>(student, ur, m, a.s, coef, live, grad, tid);
+    __syncthreads();
+    if (patch.id >= 0 && unit_holds(ur, row * a.V + patch.id, Elem<T>::kPerVec))
+        Pack<T>::one(grad + row * a.V + patch.id, patch.value);
+}
+
+// Loss and gradient: a row per workgroup, read twice (the second time mostly from cache).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void distill_step_kernel(
+    const T *__restrict__ student, Args a, const float *__restrict__ grad_loss,
+    float *__restrict__ loss, T *__restrict__ grad) {
+    __shared__ Stat sh[kWaves];
+    __shared__ double sh_sigma;
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const UnitRange ur = unit_range(row, a.V, 1, Elem<T>::kPerVec);
+    const Stat st = unit_stat<T, kThreads>(student, ur, a.s, sh, tid);
+    const int lane = tid & (kWave - 1);
+    const bool any = teacher_any(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, lane);
+    const float g = grad_loss[row];
+    Patch patch{-1, 0.f};
+    if (tid < kWave) {
+        const Teacher t = teacher_row(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, lane);
+        const double sigma = row_sigma<T>(st, student, row, a.V, a.s, lane);
+        const double l = row_loss<T>(t, student, row, a.V, (double)st.m, sigma, a.tau);
+        if (lane == 0) {
+            loss[row] = (float)l;
+            sh_sigma = sigma;
+        }
+        patch = teacher_patch<T>(t, student, row, a.V, a.K, (double)st.m, sigma, (double)g, a.tau,
+                                 lane);
+    }
+    __syncthreads();
+    const double sigma = sh_sigma;
+    const bool live = any && sigma != 0.0;
+    const float coef = (float)((double)g * a.tau / sigma);
+    unit_gradient<T, kThreads>(student, ur, st.m, a.s, coef, live, grad, tid);
+    __syncthreads();
+    if (patch.id >= 0) Pack<T>::one(grad + row * a.V + patch.id, patch.value);
+}
+
+Args make_args(const int32_t *ids, const float *teacher, int R, int V, int K, float tau) {
+    Args a;
+    a.ids = ids;
+    a.teacher = teacher;
+    a.R = R;
+    a.V = V;
+    a.K = K;
+    a.tau = (double)tau;
+    a.inv_tau = 1.0 / (double)tau;
+    a.s = (float)(1.4426950408889634 / (double)tau);
+    return a;
+}
+
+// Slices per row: enough units to fill the chip (1024 workgroups) when rows are few, each of at
+// least kUnitVectors vectors.
+int plan_slices(int R, int V, int elem_bytes) {
+    const int64_t nvec = (int64_t)V * elem_bytes / 16;
+    int64_t s = (1024 + R - 1) / R;
+    const int64_t most = nvec / kUnitVectors;
+    if (s > most) s = most;
+    return s < 1 ? 1 : (int)s;
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <typename T>
+hipError_t forward(const void *student, const Args &a, float *loss, float *row_stats, void *ws,
+                   hipStream_t stream) {
+    const int S = plan_slices(a.R, a.V, (int)sizeof(T));
+    const T *x = static_cast<const T *>(student);
+    Stat *part = static_cast<Stat *>(ws);
+    hipLaunchKernelGGL((distill_forward_kernel<T>), dim3((unsigned)(a.R * (int64_t)S)),
+                       dim3(kThreads), 0, stream, x, a, S, loss, row_stats, part);
+    if (S > 1)
+        hipLaunchKernelGGL((distill_join_kernel<T>), dim3((unsigned)a.R), dim3(kWave), 0, stream, x,
+                           a, S, part, loss, row_stats);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t backward(const void *student, const Args &a, const float *row_stats,
+                    const float *grad_loss, void *grad, hipStream_t stream) {
+    const int S = plan_slices(a.R, a.V, (int)sizeof(T));
+    hipLaunchKernelGGL((distill_backward_kernel<T>), dim3((unsigned)(a.R * (int64_t)S)),
+                       dim3(kThreads), 0, stream, static_cast<const T *>(student), a, S, row_stats,
+                       grad_loss, static_cast<T *>(grad));
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t step(const void *student, const Args &a, const float *grad_loss, float *loss, void *grad,
+                void *ws, hipStream_t stream) {
+    const int S = plan_slices(a.R, a.V, (int)sizeof(T));
+    if (S == 1) {
+        hipLaunchKernelGGL((distill_step_kernel<T>), dim3((unsigned)a.R), dim3(kThreads), 0, stream,
+                           static_cast<const T *>(student), a, grad_loss, loss,
+                           static_cast<T *>(grad));
+        return hipGetLastError();
+    }
+    float *row_stats = static_cast<float *>(ws);
+    char *part = static_cast<char *>(ws) + align256((size_t)a.R * 2 * sizeof(float));
+    const hipError_t e = forward<T>(student, a, loss, row_stats, part, stream);
+    if (e != hipSuccess) return e;
+    return backward<T>(student, a, row_stats, grad_loss, grad, stream);
+}
+
+}  // namespace
+
+size_t distill_workspace_bytes(int R, int V, int elem_bytes) {
+    const int S = plan_slices(R, V, elem_bytes);
+    if (S == 1) return 0;
+    return align256((size_t)R * 2 * sizeof(float)) + align256((size_t)R * S * sizeof(Stat));
+}
+
+hipError_t launch_distill(const void *student, int dtype, const int32_t *ids, const float *teacher,
+                          int R, int V, int K, float tau, float *loss, float *row_stats, void *ws,
+                          hipStream_t stream) {
+    const Args a = make_args(ids, teacher, R, V, K, tau);
+    return dtype == 0 ? forward<float>(student, a, loss, row_stats, ws, stream)
+                      : forward<uint16_t>(student, a, loss, row_stats, ws, stream);
+}
+
+hipError_t launch_distill_backward(const void *student, int dtype, const int32_t *ids,
+                                   const float *teacher, const float *row_stats,
+                                   const float *grad_loss, int R, int V, int K, float tau,
+                                   void *grad, hipStream_t stream) {
+    const Args a = make_args(ids, teacher, R, V, K, tau);
+    return dtype == 0 ? backward<float>(student, a, row_stats, grad_loss, grad, stream)
+                      : backward<uint16_t>(student, a, row_stats, grad_loss, grad, stream);
+}
+
+hipError_t launch_distill_step(const void *student, int dtype, const int32_t *ids,
+                               const float *teacher, const float *grad_loss, int R, int V, int K,
+                               float tau, float *loss, void *grad, void *ws, hipStream_t stream) {
+    const Args a = make_args(ids, teacher, R, V, K, tau);
+    return dtype == 0 ? step<float>(student, a, grad_loss, loss, grad, ws, stream)
+                      : step<uint16_t>(student, a, grad_loss, loss, grad, ws, stream);
+}
+
+}  // namespace dflash2

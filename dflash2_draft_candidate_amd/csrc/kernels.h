@@ -101,4 +101,19 @@ hipError_t launch_lmhead_topk(const void *hidden, const void *W_lm, int R, int H
 hipError_t launch_dynconv(const void *x, const void *base, const void *dyn, int dtype, int nb,
                           int Tn, int C, int K, int G, void *y, hipStream_t stream);
 
+// ---- distillation from a teacher's top logits -------------------------------------------------
+// teacher ids / logits [R, K], K <= 64; row_stats [R, 2] = (max, sum exp((z - max) / tau)).
+// workspace: distill_workspace_bytes (forward and step; may be 0).
+size_t distill_workspace_bytes(int R, int V, int elem_bytes);
+hipError_t launch_distill(const void *student, int dtype, const int32_t *ids, const float *teacher,
+                          int R, int V, int K, float tau, float *loss, float *row_stats, void *ws,
+                          hipStream_t stream);
+hipError_t launch_distill_backward(const void *student, int dtype, const int32_t *ids,
+                                   const float *teacher, const float *row_stats,
+                                   const float *grad_loss, int R, int V, int K, float tau,
+                                   void *grad, hipStream_t stream);
+hipError_t launch_distill_step(const void *student, int dtype, const int32_t *ids,
+                               const float *teacher, const float *grad_loss, int R, int V, int K,
+                               float tau, float *loss, void *grad, void *ws, hipStream_t stream);
+
 }  // namespace dflash2

@@ -50,6 +50,7 @@ extern "C" {
 #define DFLASH2_MAX_CONV_TAPS 8 /* largest kernel of dflash2_dynconv */
 #define DFLASH2_LMHEAD_MAX_K 16 /* largest k of dflash2_lmhead_topk */
 #define DFLASH2_LMHEAD_MAX_ROWS 16 /* largest R of dflash2_lmhead_topk (one 16-row tile) */
+#define DFLASH2_MAX_DISTILL_ROWS (1 << 21) /* largest R of the dflash2_distill calls */
 
 typedef enum dflash2_dtype {
     DFLASH2_F32 = 0,  /* IEEE binary32 */
@@ -270,6 +271,51 @@ size_t dflash2_lmhead_topk_workspace_bytes(int R, int H, int V, int k);
 int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int V, int k,
                         int32_t *cand_ids, float *unary, float *lse, void *workspace,
                         size_t workspace_bytes, void *stream);
+
+/*
+ * dflash2_distill, dflash2_distill_backward, dflash2_distill_step - the loss that trains a drafter
+ *   on its target's top logits, as dflash2_topk_lse or dflash2_lmhead_topk keeps them (cand_ids
+ *   and unary, or the logits themselves: a constant added to a row's teacher logits changes
+ *   nothing).
+ *
+ *   student        [R, V]  student_dtype, device. The drafter's logits z.
+ *   teacher_ids    [R, K]  int32, device. An id outside [0, V) is no entry (pad short rows with
+ *                          -1). An id that occurs twice in a row counts twice.
+ *   teacher_logits [R, K]  float, device. t; -inf is an entry without mass.
+ *   temperature    tau > 0 (finite and normal).
+ *   With p = softmax(t / tau) over the row's entries and q = softmax(z / tau) over the vocabulary:
+ *   loss           [R]     float, device, out. tau^2 sum_j p_j (ln p_j - ln q[id_j]).
+ *   row_stats      [R, 2]  float, device. Out of dflash2_distill, into dflash2_distill_backward:
+ *                          (max_v z_v, sum_v exp((z_v - max) / tau)).
+ *   grad_loss      [R]     float, device. The gradient g of each row's loss (weights, 1 / R, ...).
+ *   grad_student   [R, V]  student_dtype, device, out, written in full:
+ *                          g tau (q_v - sum_{j: id_j = v} p_j), rounded once. Must not overlap
+ *                          student (DFLASH2_ERR_INVALID_ARG).
+ *   dflash2_distill computes loss and row_stats, dflash2_distill_backward the gradient from them,
+ *   and dflash2_distill_step loss and gradient in one call (the student's logits come from HBM
+ *   once); its loss and gradient are those of the two calls up to the rounding of row_stats.
+ *   Rows without a teacher entry, or without teacher mass: loss 0, gradient 0. Student logits of
+ *   -inf (masked tokens) have q = 0 and gradient 0 where no teacher entry names them; an entry with
+ *   mass at such a token makes the loss +inf (its gradient is -g tau p). A row whose student logits
+ *   are all -inf has loss +inf and gradient 0. NaN, or +inf among the student's logits, makes the
+ *   row's loss NaN and its gradient NaN.
+ *   1 <= R <= DFLASH2_MAX_DISTILL_ROWS, 1 <= V <= DFLASH2_MAX_V, 1 <= K <= DFLASH2_MAX_K.
+ * Workspace of dflash2_distill and dflash2_distill_step: dflash2_distill_workspace_bytes(R, V,
+ * student_dtype) bytes (may be 0), contents need not be initialised.
+ */
+size_t dflash2_distill_workspace_bytes(int R, int V, int student_dtype);
+int dflash2_distill(const void *student, int student_dtype, const int32_t *teacher_ids,
+                    const float *teacher_logits, int R, int V, int K, float temperature,
+                    float *loss, float *row_stats, void *workspace, size_t workspace_bytes,
+                    void *stream);
+int dflash2_distill_backward(const void *student, int student_dtype, const int32_t *teacher_ids,
+                             const float *teacher_logits, const float *row_stats,
+                             const float *grad_loss, int R, int V, int K, float temperature,
+                             void *grad_student, void *stream);
+int dflash2_distill_step(const void *student, int student_dtype, const int32_t *teacher_ids,
+                         const float *teacher_logits, const float *grad_loss, int R, int V, int K,
+                         float temperature, float *loss, void *grad_student, void *workspace,
+                         size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
