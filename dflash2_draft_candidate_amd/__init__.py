@@ -67,6 +67,9 @@ _lib.dflash2_lmhead_topk_workspace_bytes.argtypes = [_ci] * 4
 _lib.dflash2_lmhead_topk_workspace_bytes.restype = _sz
 _lib.dflash2_lmhead_topk.argtypes = [_vp, _vp] + [_ci] * 4 + [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.dflash2_lmhead_topk.restype = _ci
+_lib.dflash2_sample.argtypes = [_vp, _ci, _ci, _ci, _vp, _cf, _vp, _ci, _vp, _cf, _vp, _cf, _vp,
+                                _vp, _vp, _vp]
+_lib.dflash2_sample.restype = _ci
 _lib.dflash2_distill_workspace_bytes.argtypes = [_ci] * 3
 _lib.dflash2_distill_workspace_bytes.restype = _sz
 _lib.dflash2_distill.argtypes = [_vp, _ci, _vp, _vp] + [_ci] * 3 + [_cf, _vp, _vp, _vp, _sz, _vp]
@@ -83,7 +86,7 @@ EXPORTS = ("dflash2_version", "dflash2_status_string", "dflash2_workspace_bytes"
            "dflash2_gate_workspace_bytes", "dflash2_gate", "dflash2_lattice", "dflash2_walk",
            "dflash2_select_ex", "dflash2_walk_ex", "dflash2_dynconv",
            "dflash2_lmhead_topk_workspace_bytes", "dflash2_lmhead_topk",
-           "dflash2_distill_workspace_bytes", "dflash2_distill", "dflash2_distill_backward",
+           "dflash2_sample", "dflash2_distill_workspace_bytes", "dflash2_distill", "dflash2_distill_backward",
            "dflash2_distill_step")
 
 
@@ -386,7 +389,7 @@ def dynconv(x: torch.Tensor, base: torch.Tensor, dyn: torch.Tensor, group: int,
     return y
 
 
-# ---- distillation from a teacher's top logits ------------------------------------------------
+# ---- sampling from whole rows of logits --------------------------------------------------------
 
 class _on:
     """Makes `device` the current one for a launch on its stream, if it is not already."""
@@ -410,6 +413,56 @@ def _same_device(device: torch.device, *ts: torch.Tensor):
         if t.device != device:
             raise ValueError("tensors must share a device")
 
+
+def _setting(value, dtype: torch.dtype, R: int, what: str, logits: torch.Tensor):
+    """A setting as (tensor or None, value for all rows)."""
+    if not isinstance(value, torch.Tensor):
+        return None, value
+    _contig(value)
+    if value.shape != (R,) or value.dtype != dtype:
+        raise ValueError(f"{what} must be a number or [R] {dtype}")
+    _same_device(logits.device, value)
+    return value, 0
+
+
+def sample(logits: torch.Tensor, uniforms: torch.Tensor,
+           temperature: float | torch.Tensor = 1.0, top_k: int | torch.Tensor = 0,
+           top_p: float | torch.Tensor = 1.0, min_p: float | torch.Tensor = 0.0,
+           out: tuple | None = None):
+    """A token per row of logits [R, V], drawn with uniforms [R] float32 in [0, 1): ->
+    (token_ids [R] int32, logprob [R] f32 of the token among those kept). Each setting is a number
+    or a tensor [R] (float32; top_k int32). temperature 0: greedy; top_k 0, top_p 1 and min_p 0:
+    no cut. `out` may be passed to reuse buffers."""
+    _contig(logits, uniforms)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [R, V]")
+    R, V = logits.shape
+    if uniforms.shape != (R,) or uniforms.dtype != torch.float32:
+        raise ValueError("uniforms must be [R] float32")
+    dev = logits.device
+    _same_device(dev, uniforms)
+    t, t_all = _setting(temperature, torch.float32, R, "temperature", logits)
+    k, k_all = _setting(top_k, torch.int32, R, "top_k", logits)
+    p, p_all = _setting(top_p, torch.float32, R, "top_p", logits)
+    m, m_all = _setting(min_p, torch.float32, R, "min_p", logits)
+    if out is None:
+        out = (torch.empty((R,), dtype=torch.int32, device=dev),
+               torch.empty((R,), dtype=torch.float32, device=dev))
+    token_ids, logprob = out
+    _contig(token_ids, logprob)
+    if token_ids.shape != (R,) or token_ids.dtype != torch.int32 or logprob.shape != (R,) or \
+            logprob.dtype != torch.float32:
+        raise ValueError("out must be ([R] int32, [R] float32)")
+    _same_device(dev, token_ids, logprob)
+    with _on(dev):
+        rc = _lib.dflash2_sample(_ptr(logits), _dtype(logits), R, V, _ptr(t), float(t_all), _ptr(k),
+                                 int(k_all), _ptr(p), float(p_all), _ptr(m), float(m_all),
+                                 _ptr(uniforms), _ptr(token_ids), _ptr(logprob), _stream(dev))
+    _check(rc, "dflash2_sample")
+    return token_ids, logprob
+
+
+# ---- distillation from a teacher's top logits ------------------------------------------------
 
 def _distill_args(student: torch.Tensor, teacher_ids: torch.Tensor,
                   teacher_logits: torch.Tensor):

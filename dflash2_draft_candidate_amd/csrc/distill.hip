@@ -26,14 +26,14 @@
 
 #include "device_common.h"
 #include "kernels.h"
-#include "row_slices.h"
+#include "row_stream.h"
 
 namespace dflash2 {
 namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kU = 4;              // 16-byte vectors per thread and batch
+constexpr int kU = kStreamVectors;
 constexpr float kMaxRef = 8388608.f;  // 2^23: references stay within this, so each is within 0.5
                                       // of m s and 2^(m s - ref) cannot overflow
 constexpr float kNoRef = -kMaxRef;    // reference before the first element
@@ -131,46 +131,6 @@ __device__ __forceinline__ double row_loss(const Teacher &t, const T *student, i
         term = t.p * (t.ln_p - (sigma == 0.0 ? -INFINITY : ln_q));
     }
     return tau * tau * wave_sum64(term);
-}
-
-// ---- streaming over a unit's vectors -----------------------------------------------------------
-
-// Runs f(vector, index) over a thread's share of n vectors at p (tid, tid + nt, ...): batches of
-// kU vectors with the next batch's loads in flight, then the rest. `g` gets whole batches.
-template <int NT, typename FB, typename FV>
-__device__ __forceinline__ void stream(const u32x4 *p, int n, int tid, FB &&batch, FV &&single) {
-    const int whole = n / (NT * kU);
-    u32x4 cur[kU], nxt[kU];
-    if (whole > 0) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u) cur[u] = p[tid + u * NT];
-    }
-    for (int b = 0; b < whole; ++b) {
-        const int base = (b + 1) * NT * kU + tid;
-        if (b + 1 < whole) {
-#pragma unroll
-            for (int u = 0; u < kU; ++u) nxt[u] = p[base + u * NT];
-        }
-        batch(cur, base - NT * kU);
-#pragma unroll
-        for (int u = 0; u < kU; ++u) cur[u] = nxt[u];
-    }
-    // the rest: at most kU vectors per thread, loaded together
-    const int base = whole * NT * kU + tid;
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-        if (base + u * NT < n) cur[u] = p[base + u * NT];
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-        if (base + u * NT < n) single(cur[u], base + u * NT);
-}
-
-// Ragged element `tid` of a unit (its row's ends outside whole vectors): index, or -1.
-__device__ __forceinline__ int64_t ragged_element(const UnitRange &u, int tid) {
-    const int nh = (int)(u.h1 - u.h0);
-    if (tid < nh) return u.h0 + tid;
-    if (tid - nh < (int)(u.t1 - u.t0)) return u.t0 + (tid - nh);
-    return -1;
 }
 
 // ---- row statistics ------------------------------------------------------------------------

@@ -101,6 +101,14 @@ hipError_t launch_lmhead_topk(const void *hidden, const void *W_lm, int R, int H
 hipError_t launch_dynconv(const void *x, const void *base, const void *dyn, int dtype, int nb,
                           int Tn, int C, int K, int G, void *y, hipStream_t stream);
 
+// ---- sampling from whole rows of logits -------------------------------------------------------
+// Settings per row (null: the value for all rows); logprob may be null.
+hipError_t launch_sample(const void *logits, int dtype, int R, int V, const float *temperature,
+                         float all_temperature, const int32_t *top_k, int all_top_k,
+                         const float *top_p, float all_top_p, const float *min_p, float all_min_p,
+                         const float *uniforms, int32_t *tokens, float *logprob,
+                         hipStream_t stream);
+
 // ---- distillation from a teacher's top logits -------------------------------------------------
 // teacher ids / logits [R, K], K <= 64; row_stats [R, 2] = (max, sum exp((z - max) / tau)).
 // workspace: distill_workspace_bytes (forward and step; may be 0).

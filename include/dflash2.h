@@ -50,6 +50,7 @@ extern "C" {
 #define DFLASH2_MAX_CONV_TAPS 8 /* largest kernel of dflash2_dynconv */
 #define DFLASH2_LMHEAD_MAX_K 16 /* largest k of dflash2_lmhead_topk */
 #define DFLASH2_LMHEAD_MAX_ROWS 16 /* largest R of dflash2_lmhead_topk (one 16-row tile) */
+#define DFLASH2_MAX_SAMPLE_ROWS (1 << 21)  /* largest R of dflash2_sample */
 #define DFLASH2_MAX_DISTILL_ROWS (1 << 21) /* largest R of the dflash2_distill calls */
 
 typedef enum dflash2_dtype {
@@ -271,6 +272,40 @@ size_t dflash2_lmhead_topk_workspace_bytes(int R, int H, int V, int k);
 int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int V, int k,
                         int32_t *cand_ids, float *unary, float *lse, void *workspace,
                         size_t workspace_bytes, void *stream);
+
+/*
+ * dflash2_sample - a token from each row of whole vocabulary logits: the target's own answers and the
+ *   anchors a draft block starts from (dflash2_walk_ex samples among a lattice's candidates).
+ *
+ *   logits       [R, V]  dtype, device. -inf (masked) and NaN logits are never drawn; +inf logits
+ *                        share all of the weight.
+ *   temperature  [R]     float, device, or NULL: all_temperature (>= 0, finite) for every row.
+ *                        <= 0 or NaN in a row: greedy, the first token of the candidate order.
+ *   top_k        [R]     int32, device, or NULL: all_top_k. < 1: no cut.
+ *   top_p        [R]     float, device, or NULL: all_top_p (not NaN). >= 1 or NaN: no cut.
+ *   min_p        [R]     float, device, or NULL: all_min_p (not NaN). <= 0 or NaN: no cut; values
+ *                        above 1 count as 1.
+ *   uniforms     [R]     float, device. u in [0, 1), the caller's random numbers (not read by greedy
+ *                        rows; values outside are clamped, NaN counts as 0).
+ *   With w_v = exp((x_v - max x) / T) and S_j the running sum of w over the candidate order (higher
+ *   logit first, equal logits by lower id): top_k keeps the first k tokens (Z = their mass),
+ *   top_p the first n with S_n >= top_p Z, min_p those with w_v >= min_p; the fewest of the three
+ *   are kept, and one at least. With W their mass:
+ *   token_ids    [R]     int32, device, out. The first token with S_j > u W; -1 for a row without
+ *                        a logit above -inf.
+ *   logprob      [R]     float, device, out, may be NULL. ln(w / W) of the token: its
+ *                        log-probability in the distribution it was drawn from (0 when greedy, -inf
+ *                        where the token is -1).
+ *   Weights and masses are held to 2^-40 of themselves; weights below 2^-64 of the row's largest
+ *   count as 0.
+ *   1 <= R <= DFLASH2_MAX_SAMPLE_ROWS, 1 <= V <= DFLASH2_MAX_V. No workspace.
+ * Errors: DFLASH2_ERR_INVALID_ARG (sizes, dtype, all_* out of range where its pointer is NULL, NULL
+ * logits, uniforms or token_ids), DFLASH2_ERR_ALIGNMENT, DFLASH2_ERR_HIP.
+ */
+int dflash2_sample(const void *logits, int dtype, int R, int V, const float *temperature,
+                   float all_temperature, const int32_t *top_k, int all_top_k, const float *top_p,
+                   float all_top_p, const float *min_p, float all_min_p, const float *uniforms,
+                   int32_t *token_ids, float *logprob, void *stream);
 
 /*
  * dflash2_distill, dflash2_distill_backward, dflash2_distill_step - the loss that trains a drafter
