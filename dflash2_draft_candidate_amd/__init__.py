@@ -67,8 +67,10 @@ _lib.dflash2_lmhead_topk_workspace_bytes.argtypes = [_ci] * 4
 _lib.dflash2_lmhead_topk_workspace_bytes.restype = _sz
 _lib.dflash2_lmhead_topk.argtypes = [_vp, _vp] + [_ci] * 4 + [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.dflash2_lmhead_topk.restype = _ci
+_lib.dflash2_sample_workspace_bytes.argtypes = [_ci] * 3
+_lib.dflash2_sample_workspace_bytes.restype = _sz
 _lib.dflash2_sample.argtypes = [_vp, _ci, _ci, _ci, _vp, _cf, _vp, _ci, _vp, _cf, _vp, _cf, _vp,
-                                _vp, _vp, _vp]
+                                _vp, _vp, _vp, _sz, _vp]
 _lib.dflash2_sample.restype = _ci
 _lib.dflash2_distill_workspace_bytes.argtypes = [_ci] * 3
 _lib.dflash2_distill_workspace_bytes.restype = _sz
@@ -86,7 +88,7 @@ EXPORTS = ("dflash2_version", "dflash2_status_string", "dflash2_workspace_bytes"
            "dflash2_gate_workspace_bytes", "dflash2_gate", "dflash2_lattice", "dflash2_walk",
            "dflash2_select_ex", "dflash2_walk_ex", "dflash2_dynconv",
            "dflash2_lmhead_topk_workspace_bytes", "dflash2_lmhead_topk",
-           "dflash2_sample", "dflash2_distill_workspace_bytes", "dflash2_distill", "dflash2_distill_backward",
+           "dflash2_sample_workspace_bytes", "dflash2_sample", "dflash2_distill_workspace_bytes", "dflash2_distill", "dflash2_distill_backward",
            "dflash2_distill_step")
 
 
@@ -454,10 +456,13 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor,
             logprob.dtype != torch.float32:
         raise ValueError("out must be ([R] int32, [R] float32)")
     _same_device(dev, token_ids, logprob)
+    dt = _dtype(logits)
+    ws = _workspace(_lib.dflash2_sample_workspace_bytes(R, V, dt), dev)
     with _on(dev):
-        rc = _lib.dflash2_sample(_ptr(logits), _dtype(logits), R, V, _ptr(t), float(t_all), _ptr(k),
+        rc = _lib.dflash2_sample(_ptr(logits), dt, R, V, _ptr(t), float(t_all), _ptr(k),
                                  int(k_all), _ptr(p), float(p_all), _ptr(m), float(m_all),
-                                 _ptr(uniforms), _ptr(token_ids), _ptr(logprob), _stream(dev))
+                                 _ptr(uniforms), _ptr(token_ids), _ptr(logprob), _ptr(ws),
+                                 ws.numel(), _stream(dev))
     _check(rc, "dflash2_sample")
     return token_ids, logprob
 

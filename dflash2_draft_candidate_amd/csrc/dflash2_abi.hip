@@ -249,26 +249,6 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
                                          workspace, static_cast<hipStream_t>(stream)));
 }
 
-int dflash2_sample(const void *logits, int dtype, int R, int V, const float *temperature,
-                   float all_temperature, const int32_t *top_k, int all_top_k, const float *top_p,
-                   float all_top_p, const float *min_p, float all_min_p, const float *uniforms,
-                   int32_t *token_ids, float *logprob, void *stream) {
-    if (!dtype_ok(dtype) || R < 1 || R > DFLASH2_MAX_SAMPLE_ROWS || V < 1 || V > DFLASH2_MAX_V)
-        return DFLASH2_ERR_INVALID_ARG;
-    if (!temperature && (!(all_temperature >= 0.f) || !(all_temperature <= FLT_MAX)))
-        return DFLASH2_ERR_INVALID_ARG;
-    if ((!top_p && all_top_p != all_top_p) || (!min_p && all_min_p != all_min_p))
-        return DFLASH2_ERR_INVALID_ARG;
-    int rc = check_ptrs({logits, uniforms, token_ids});
-    if (rc) return rc;
-    for (const void *p : {(const void *)temperature, (const void *)top_k, (const void *)top_p,
-                          (const void *)min_p, (const void *)logprob})
-        if (p && !aligned16(p)) return DFLASH2_ERR_ALIGNMENT;
-    return hip_status(launch_sample(logits, dtype, R, V, temperature, all_temperature, top_k,
-                                    all_top_k, top_p, all_top_p, min_p, all_min_p, uniforms,
-                                    token_ids, logprob, static_cast<hipStream_t>(stream)));
-}
-
 // Sizes shared by the distillation entry points.
 static int check_distill(int dtype, int R, int V, int K, float temperature) {
     if (!dtype_ok(dtype) || R < 1 || R > DFLASH2_MAX_DISTILL_ROWS || V < 1 || V > DFLASH2_MAX_V ||
@@ -287,6 +267,37 @@ static int check_workspace(const void *workspace, size_t workspace_bytes, size_t
     if (need == 0) return DFLASH2_OK;
     if (!workspace || workspace_bytes < need) return DFLASH2_ERR_WORKSPACE;
     return aligned16(workspace) ? DFLASH2_OK : DFLASH2_ERR_ALIGNMENT;
+}
+
+size_t dflash2_sample_workspace_bytes(int R, int V, int dtype) {
+    if (!dtype_ok(dtype) || R < 1 || R > DFLASH2_MAX_SAMPLE_ROWS || V < 1 || V > DFLASH2_MAX_V)
+        return 0;
+    return sample_workspace_bytes(R, V, dtype);
+}
+
+int dflash2_sample(const void *logits, int dtype, int R, int V, const float *temperature,
+                   float all_temperature, const int32_t *top_k, int all_top_k, const float *top_p,
+                   float all_top_p, const float *min_p, float all_min_p, const float *uniforms,
+                   int32_t *token_ids, float *logprob, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+    if (!dtype_ok(dtype) || R < 1 || R > DFLASH2_MAX_SAMPLE_ROWS || V < 1 || V > DFLASH2_MAX_V)
+        return DFLASH2_ERR_INVALID_ARG;
+    if (!temperature && (!(all_temperature >= 0.f) || !(all_temperature <= FLT_MAX)))
+        return DFLASH2_ERR_INVALID_ARG;
+    if ((!top_p && all_top_p != all_top_p) || (!min_p && all_min_p != all_min_p))
+        return DFLASH2_ERR_INVALID_ARG;
+    int rc = check_ptrs({logits, uniforms, token_ids});
+    if (rc) return rc;
+    for (const void *p : {(const void *)temperature, (const void *)top_k, (const void *)top_p,
+                          (const void *)min_p, (const void *)logprob})
+        if (p && !aligned16(p)) return DFLASH2_ERR_ALIGNMENT;
+    if ((rc = check_workspace(workspace, workspace_bytes,
+                              dflash2_sample_workspace_bytes(R, V, dtype))))
+        return rc;
+    return hip_status(launch_sample(logits, dtype, R, V, temperature, all_temperature, top_k,
+                                    all_top_k, top_p, all_top_p, min_p, all_min_p, uniforms,
+                                    token_ids, logprob, workspace,
+                                    static_cast<hipStream_t>(stream)));
 }
 
 size_t dflash2_distill_workspace_bytes(int R, int V, int student_dtype) {

@@ -102,11 +102,13 @@ hipError_t launch_dynconv(const void *x, const void *base, const void *dyn, int 
                           int Tn, int C, int K, int G, void *y, hipStream_t stream);
 
 // ---- sampling from whole rows of logits -------------------------------------------------------
-// Settings per row (null: the value for all rows); logprob may be null.
+// Settings per row (null: the value for all rows); logprob may be null. workspace:
+// sample_workspace_bytes (may be 0).
+size_t sample_workspace_bytes(int R, int V, int dtype);
 hipError_t launch_sample(const void *logits, int dtype, int R, int V, const float *temperature,
                          float all_temperature, const int32_t *top_k, int all_top_k,
                          const float *top_p, float all_top_p, const float *min_p, float all_min_p,
-                         const float *uniforms, int32_t *tokens, float *logprob,
+                         const float *uniforms, int32_t *tokens, float *logprob, void *ws,
                          hipStream_t stream);
 
 // ---- distillation from a teacher's top logits -------------------------------------------------

@@ -9,625 +9,44 @@
 // Each cut keeps a prefix of the order and S grows along it, so W is the smallest of the cuts' masses
 // and nothing else of a cut is needed.
 //
-// The token is a whole number that a rounding can change, and a flat row has more than 10^5 tokens
-// whose shares a 32-bit sum cannot tell apart: weights and masses are held to about 2^-40.
-// With y = 64 log2(e) (m - x) / T in fp64 and b = floor(y), a weight is 2^(-b/64) 2^(-(y-b)/64); the
-// second factor, within 1% of 1, is a polynomial of degree 5 (error 2.2e-15). b is also the
-// weight's bin: bins follow the candidate order, because y does. A bin's second factors are summed
-// as 64-bit integers (kFracBits behind the point) by LDS atomics: whole numbers have no order of
-// summation, so results do not depend on which wave came first. Bins end at b = 4096, weight 2^-64 of
-// the largest: what lies below adds less than 2^-36 of a unit in the last place of u W.
-//
-// A workgroup works on one row: maximum (and, for T = 0, where it first stands); the histogram of the
-// bins; then each cut is found among the bins' running masses and inside its bin. Where the tokens
-// from the top to the lowest cut are few (<= kCap) they are gathered once, sorted, and everything
-// is settled in that list. Otherwise each cut gathers and sorts its own bin, which is split by value
-// first if it holds more than kCap tokens; when a single value remains, its tokens are equal and
-// a division tells how many of them a cut takes.
-#include <float.h>
-
-#include "device_common.h"
+// float32 rows take the general path (sample_general.h). bf16 rows have few distinct values, so it is
+// enough to count how often each occurs: the masses of all cuts follow from the counts, a weight per
+// value, and the draw gives a value and how many of its equals come before the token. The counts
+// are whole numbers (LDS atomics in any order), there is one atomic and a handful of integer
+// instructions per logit in place of an exponential, and the pass needs no maximum first.
+//   * Counted values: 2^-20 <= |x| < 2^8, 28 binades of 128 values, a word each: positive values
+//     in its low half, negative ones in its high half. A word below takes what is smaller, one
+//     above what is larger. The row is counted in parts (words of their own), so that a half-word
+//     is enough; a part's overflow shows as a wrong total.
+//   * Smaller values are rare (one in 10^7 of a normal row): up to 64 of them are gathered and take
+//     their place between the positive and the negative values. Larger negative ones are masks,
+//     or so far below the maximum that they have no weight. Anything else (large or infinite
+//     logits, many tiny or zero ones, a row of masks) sends the row to the general path.
+//   * The token is then the n-th logit of a value, and the parts' counts say in which part: only
+//     that part is read a second time.
+// Rows that are many (kRowGroups and more) have a workgroup each, with four parts; few rows are cut
+// into slices, a part and a workgroup each, whose counts go through the workspace to a second kernel.
 #include "kernels.h"
-#include "row_stream.h"
+#include "sample_general.h"
 
 namespace dflash2 {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / kWave;
-constexpr int kBins = 4096;
-constexpr int kPer = kBins / kThreads;  // bins per thread
-constexpr int kCap = kThreads;          // gathered tokens, one per thread
-constexpr double kTwo52 = 4503599627370496.0;
+constexpr int kNT = 512;       // threads of the bf16 kernels
+constexpr int kNT32 = 1024;    // threads of the float32 kernel
+constexpr int kParts = 4;      // parts of a row that a workgroup counts by itself
+constexpr int kBase = 0x3580;  // bf16 pattern of 2^-20
+constexpr int kValues = 3584;  // counted values of a sign: up to 2^8
+constexpr int kStride = 3588;  // words of a part: below, kValues, above, two unused
+constexpr int kPerThread = 2 * kValues / kNT;
+constexpr int kRowGroups = 256;
+constexpr int kMaxSlices = 16;
+constexpr int kSmallCap = 64;  // gathered values below 2^-20
+static_assert(kCountWords == kParts * kStride, "counts in LDS");
+static_assert(kPerThread * kNT == 2 * kValues && kValues % kPerThread == 0, "bins of a thread");
 
-struct Shared {
-    uint64_t mass[kBins];
-    uint32_t count[kBins];
-    uint64_t list[kCap];
-    double wave_mass[kWaves];
-    uint32_t wave_count[kWaves];
-    int wave_first[kWaves];
-    float wave_max[kWaves];
-    uint32_t listed;
-    uint32_t key_lo, key_hi;
-    int32_t token;
-    double spot_mass;
-    uint32_t spot_count;
-    int spot_bin;
-    uint32_t spot_size;
-};
-
-// The weights of a row.
-struct Weights {
-    float m;     // row maximum (finite)
-    double c;    // 64 log2(e) / T
-    double one;  // 2^kFracBits of this vocabulary
-};
-
-__device__ __forceinline__ double weight_y(const Weights &w, float x) {
-    return ((double)w.m - (double)x) * w.c;
-}
-
-// 2^(-f/64) for f in [0, 1): the Taylor polynomial of exp(-f ln2/64); the next term is below 2.2e-15.
-__device__ __forceinline__ double fraction(double f) {
-    constexpr double a = kLn2 / 64.0;
-    double p = -a * a * a * a * a / 120.0;
-    p = __builtin_fma(p, f, a * a * a * a / 24.0);
-    p = __builtin_fma(p, f, -a * a * a / 6.0);
-    p = __builtin_fma(p, f, a * a / 2.0);
-    p = __builtin_fma(p, f, -a);
-    return __builtin_fma(p, f, 1.0);
-}
-
-// round(2^kFracBits fraction): adding 2^52 leaves the integer in the low mantissa bits.
-__device__ __forceinline__ uint64_t fixed_fraction(const Weights &w, double f) {
-    const double v = __builtin_fma(fraction(f), w.one, kTwo52);
-    return (uint64_t)__double_as_longlong(v) & 0xFFFFFFFFFFFFFull;
-}
-
-__device__ __forceinline__ double bin_scale(int b) { return exp2((double)b * (-1.0 / 64.0)); }
-
-__device__ __forceinline__ double weight_of(const Weights &w, float x) {
-    const double y = weight_y(w, x);
-    const int b = (int)y;
-    return fraction(y - (double)b) * bin_scale(b);
-}
-
-// ---- workgroup steps -------------------------------------------------------------------------
-
-// Exclusive running sum over the threads; `total` is the sum. The result of thread t + 1 is at
-// least that of thread t plus its v up to one rounding.
-__device__ __forceinline__ double scan_mass(Shared &sh, double v, int tid, double &total) {
-    const int lane = tid & (kWave - 1), wave = tid / kWave;
-    double s = v;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const double t = __shfl_up(s, o);
-        if (lane >= o) s += t;
-    }
-    if (lane == kWave - 1) sh.wave_mass[wave] = s;
-    __syncthreads();
-    double base = 0.0, all = 0.0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        if (i == wave) base = all;
-        all += sh.wave_mass[i];
-    }
-    __syncthreads();
-    total = all;
-    const double before = __shfl_up(s, 1);
-    return lane == 0 ? base : base + before;
-}
-
-__device__ __forceinline__ uint32_t scan_count(Shared &sh, uint32_t v, int tid, uint32_t &total) {
-    const int lane = tid & (kWave - 1), wave = tid / kWave;
-    uint32_t s = v;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t t = __shfl_up(s, o);
-        if (lane >= o) s += t;
-    }
-    if (lane == kWave - 1) sh.wave_count[wave] = s;
-    __syncthreads();
-    uint32_t base = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        if (i == wave) base = all;
-        all += sh.wave_count[i];
-    }
-    __syncthreads();
-    total = all;
-    return base + s - v;
-}
-
-// The first thread for which `c` holds, kThreads if none.
-__device__ __forceinline__ int first_thread(Shared &sh, bool c, int tid) {
-    const uint64_t b = __ballot(c);
-    if ((tid & (kWave - 1)) == 0)
-        sh.wave_first[tid / kWave] = b ? (tid + __builtin_ctzll(b)) : kThreads;
-    __syncthreads();
-    int first = kThreads;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) first = min(first, sh.wave_first[i]);
-    __syncthreads();
-    return first;
-}
-
-// The row: f(x, id) for each of its elements, in no particular order.
-template <typename T, typename F>
-__device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, F &&f) {
-    constexpr int EV = Elem<T>::kPerVec;
-    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
-    auto one = [&](const u32x4 &v, int i) {
-        float x[EV];
-        Elem<T>::unpack(v, x);
-#pragma unroll
-        for (int k = 0; k < EV; ++k) f(x[k], id0 + i * EV + k);
-    };
-    stream<kThreads>(
-        reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
-        [&](const u32x4 *v, int i) {
-#pragma unroll
-            for (int u = 0; u < kStreamVectors; ++u) one(v[u], i + u * kThreads);
-        },
-        one);
-    const int64_t e = ragged_element(ur, tid);
-    if (e >= 0) f(Elem<T>::load(logits, e), (int32_t)(e - ur.g0));
-}
-
-// The row's maximum over what is not NaN, in every thread; `at` is where this thread met its own
-// (a vector index; the element lies there or up to kStreamVectors - 1 strides on).
-struct Top {
-    float m;     // of the row
-    float mine;  // of this thread's vectors
-    int at;
-};
-
-template <typename T>
-__device__ __forceinline__ Top row_top(const T *logits, const UnitRange &ur, Shared &sh, int tid) {
-    constexpr int EV = Elem<T>::kPerVec;
-    Top t{-INFINITY, -INFINITY, 0};
-    stream<kThreads>(
-        reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
-        [&](const u32x4 *v, int i) {
-            float x[kStreamVectors * EV];
-#pragma unroll
-            for (int u = 0; u < kStreamVectors; ++u) Elem<T>::unpack(v[u], x + u * EV);
-            float c = x[0];
-#pragma unroll
-            for (int k = 1; k < kStreamVectors * EV; ++k) c = fmaxf(c, x[k]);
-            if (c > t.mine) {
-                t.mine = c;
-                t.at = i;
-            }
-        },
-        [&](const u32x4 &v, int i) {
-            float x[EV];
-            Elem<T>::unpack(v, x);
-            float c = x[0];
-#pragma unroll
-            for (int k = 1; k < EV; ++k) c = fmaxf(c, x[k]);
-            if (c > t.mine) {
-                t.mine = c;
-                t.at = i;
-            }
-        });
-    float m = t.mine;
-    const int64_t e = ragged_element(ur, tid);
-    if (e >= 0) m = fmaxf(m, Elem<T>::load(logits, e));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if ((tid & (kWave - 1)) == 0) sh.wave_max[tid / kWave] = m;
-    __syncthreads();
-    m = sh.wave_max[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.wave_max[w]);
-    __syncthreads();
-    t.m = m;
-    return t;
-}
-
-// The lowest id whose logit is the row's maximum.
-template <typename T>
-__device__ __forceinline__ int32_t first_of_top(const T *logits, const UnitRange &ur, const Top &t,
-                                                Shared &sh, int tid) {
-    constexpr int EV = Elem<T>::kPerVec;
-    if (tid == 0) sh.token = 0x7FFFFFFF;
-    __syncthreads();
-    int32_t id = 0x7FFFFFFF;
-    if (t.mine == t.m) {
-        for (int u = kStreamVectors - 1; u >= 0; --u) {
-            const int i = t.at + u * kThreads;
-            if (i >= ur.nv) continue;
-            float x[EV];
-            Elem<T>::unpack(reinterpret_cast<const u32x4 *>(logits)[ur.c0 + i], x);
-#pragma unroll
-            for (int k = EV - 1; k >= 0; --k)
-                if (x[k] == t.m) id = (int32_t)((ur.c0 + i) * EV + k - ur.g0);
-        }
-    }
-    const int64_t e = ragged_element(ur, tid);
-    if (e >= 0 && Elem<T>::load(logits, e) == t.m) id = min(id, (int32_t)(e - ur.g0));
-    if (id != 0x7FFFFFFF) atomicMin(&sh.token, id);
-    __syncthreads();
-    id = sh.token;
-    __syncthreads();
-    return id;
-}
-
-// How many logits equal `value`, and the id of number `nth` (from 0, by id) among them, -1 if there
-// are not so many. Wave w takes the w-th run of the row's vectors.
-template <typename T>
-__device__ __noinline__ int32_t nth_equal(const T *logits, const UnitRange &ur, Shared &sh, int tid,
-                                          float value, uint32_t nth, uint32_t &total) {
-    constexpr int EV = Elem<T>::kPerVec;
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
-    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
-    const int lane = tid & (kWave - 1), wave = tid / kWave;
-    const int v0 = (int)((int64_t)ur.nv * wave / kWaves);
-    const int v1 = (int)((int64_t)ur.nv * (wave + 1) / kWaves);
-    auto matches = [&](int i) {  // which elements of vector i match
-        uint32_t bits = 0;
-        if (i < v1) {
-            float x[EV];
-            Elem<T>::unpack(p[i], x);
-#pragma unroll
-            for (int k = 0; k < EV; ++k) bits |= x[k] == value ? 1u << k : 0u;
-        }
-        return bits;
-    };
-    uint32_t mine = 0;
-    for (int i = v0; i < v1; i += kWave) mine += __popc(matches(i + lane));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
-    if (lane == 0) sh.wave_count[wave] = mine;
-    if (tid == 0) sh.token = -1;
-    __syncthreads();
-    uint32_t head = 0, tail = 0;
-    for (int64_t e = ur.h0; e < ur.h1; ++e) head += Elem<T>::load(logits, e) == value;
-    for (int64_t e = ur.t0; e < ur.t1; ++e) tail += Elem<T>::load(logits, e) == value;
-    uint32_t before = head, base = head;
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) base = before;
-        before += sh.wave_count[w];
-    }
-    total = before + tail;
-    if (tid == 0 && (nth < head || (nth >= before && nth < total))) {
-        uint32_t left = nth < head ? nth : nth - before;
-        for (int64_t e = nth < head ? ur.h0 : ur.t0;; ++e)
-            if (Elem<T>::load(logits, e) == value && left-- == 0) {
-                sh.token = (int32_t)(e - ur.g0);
-                break;
-            }
-    }
-    if (nth >= base && nth < base + mine) {  // this wave's run holds it
-        uint32_t left = nth - base;
-        for (int i = v0; i < v1; i += kWave) {
-            const uint32_t bits = matches(i + lane);
-            uint32_t s = __popc(bits);
-            const uint32_t own = s;
-#pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) {
-                const uint32_t t = __shfl_up(s, o);
-                if (lane >= o) s += t;
-            }
-            const uint32_t all = __shfl(s, kWave - 1);
-            if (left < all) {
-                uint32_t k = left - (s - own);
-                if (left >= s - own && left < s) {
-                    uint32_t b = bits;
-                    while (k-- > 0) b &= b - 1;
-                    sh.token = id0 + (i + lane) * EV + (__ffs(b) - 1);
-                }
-                break;
-            }
-            left -= all;
-        }
-    }
-    __syncthreads();
-    const int32_t id = sh.token;
-    __syncthreads();
-    return id;
-}
-
-// ---- the gathered list --------------------------------------------------------------------------
-
-// One gathered token per thread in candidate order (threads below n), with running masses.
-struct Listed {
-    uint64_t key;
-    double w;      // 0 for threads from n on
-    double below;  // masses of the tokens before it
-    int n;
-};
-
-// Sorts sh.list[0 .. n) in candidate order, a key per thread: waves sort 64 by lane exchanges,
-// larger strides go through LDS. Keys are distinct, so the order is unique.
-__device__ __forceinline__ uint64_t sort_list(Shared &sh, int n, int tid) {
-    const int lane = tid & (kWave - 1);
-    uint64_t key = tid < n ? sh.list[tid] : 0ull;
-    key = bitonic_merge_steps<1>(key, lane, (lane & 2) == 0);
-    key = bitonic_merge_steps<2>(key, lane, (lane & 4) == 0);
-    key = bitonic_merge_steps<4>(key, lane, (lane & 8) == 0);
-    key = bitonic_merge_steps<8>(key, lane, (lane & 16) == 0);
-    key = bitonic_merge_steps<16>(key, lane, (lane & 32) == 0);
-    int size = kWave;
-    while (size < n) size <<= 1;
-    key = bitonic_merge_steps<32>(key, lane, size == kWave || (tid & kWave) == 0);
-    for (int k = 2 * kWave; k <= size; k <<= 1) {
-        const bool desc = k == size || (tid & k) == 0;
-        for (int j = k >> 1; j >= kWave; j >>= 1) {
-            __syncthreads();
-            sh.list[tid] = key;
-            __syncthreads();
-            const uint64_t other = sh.list[tid ^ j];
-            const bool keep_max = ((tid & j) == 0) == desc;
-            key = ((key > other) == keep_max) ? key : other;
-        }
-        key = bitonic_merge_steps<32>(key, lane, desc);
-    }
-    __syncthreads();
-    return key;
-}
-
-__device__ __forceinline__ Listed make_list(Shared &sh, const Weights &w, int n, int tid) {
-    Listed l;
-    l.n = n;
-    l.key = sort_list(sh, n, tid);
-    l.w = tid < n ? weight_of(w, key_logit(l.key)) : 0.0;
-    double total;
-    l.below = scan_mass(sh, l.w, tid, total);
-    return l;
-}
-
-// Gathers the tokens of bins [b0, b1] whose value keys lie in [k0, k1] (at most kCap, known from
-// the histogram). The float bounds drop nearly all others first.
-template <typename T>
-__device__ __forceinline__ Listed gather(const T *logits, const UnitRange &ur, Shared &sh,
-                                         const Weights &w, int b0, int b1, uint32_t k0, uint32_t k1,
-                                         int tid) {
-    // x of the bins' ends, a step outwards: y < b1 + 1 and y >= b0 up to roundings far below it
-    const double lo = (double)w.m - (double)(b1 + 1) / w.c * (1.0 + 0x1p-20);
-    const double hi = (double)w.m - (double)b0 / w.c * (1.0 - 0x1p-20);
-    const float slack_lo = (float)(lo - fabs(lo) * 0x1p-20), slack_hi = (float)(hi + fabs(hi) * 0x1p-20);
-    const float xlo = w.c > 0.0 ? slack_lo : -FLT_MAX, xhi = w.c > 0.0 ? slack_hi : FLT_MAX;
-    if (tid == 0) sh.listed = 0;
-    __syncthreads();
-    each(logits, ur, tid, [&](float x, int32_t id) {
-        if (x >= xlo && x <= xhi) {
-            const double y = weight_y(w, x);
-            const uint32_t vk = value_key(x);
-            if (y < (double)kBins && (int)y >= b0 && (int)y <= b1 && vk >= k0 && vk <= k1) {
-                const uint32_t at = atomicAdd(&sh.listed, 1u);
-                if (at < kCap) sh.list[at] = cand_key(x, id);
-            }
-        }
-    });
-    __syncthreads();
-    const int n = min((int)sh.listed, kCap);
-    __syncthreads();
-    return make_list(sh, w, n, tid);
-}
-
-// ---- cuts -------------------------------------------------------------------------------------
-
-enum Cut { kNumber, kReach, kPass };  // the n-th token; first S >= target; first S > target
-
-// A place in the candidate order.
-struct Place {
-    double mass;  // running mass up to and including the token
-    double w;     // its weight
-    int32_t id;   // its id, or -1: number `nth` of the tokens of logit `value`
-    float value;
-    uint32_t nth;
-};
-
-// The histogram's bins of this thread: masses and counts, and what lies before them.
-struct Bins {
-    double mass[kPer];
-    uint32_t count[kPer];
-    double below;
-    uint32_t before;
-    double total;
-    uint32_t number;
-};
-
-// Takes a histogram over bins out of LDS (their factor 2^(-b/64) for level 0; `scale` otherwise).
-__device__ __forceinline__ Bins take_bins(Shared &sh, const Weights &w, bool by_bin, double scale,
-                                          double below, uint32_t before, int tid) {
-    Bins h;
-    double sum = 0.0;
-    uint32_t number = 0;
-    const double unit = 1.0 / w.one;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int b = tid * kPer + j;
-        h.count[j] = sh.count[b];
-        h.mass[j] = (double)sh.mass[b] * unit * (by_bin ? bin_scale(b) : scale);
-        sum += h.mass[j];
-        number += h.count[j];
-    }
-    h.below = below + scan_mass(sh, sum, tid, h.total);
-    h.before = before + scan_count(sh, number, tid, h.number);
-    h.total += below;
-    h.number += before;
-    return h;
-}
-
-// The bin that holds a cut: the result is in sh.spot_*. Roundings may leave a mass cut behind the
-// last bin: it is then the last that holds anything.
-__device__ __forceinline__ void find_bin(Shared &sh, const Bins &h, Cut cut, double target,
-                                         uint32_t nth, int tid) {
-    double run = h.below, spot_mass = 0.0;
-    uint32_t num = h.before, spot_count = 0, spot_size = 0;
-    int bin = -1;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const double next = run + h.mass[j];
-        const uint32_t nnum = num + h.count[j];
-        const bool in = h.count[j] > 0 && bin < 0 &&
-                        (cut == kNumber ? nnum >= nth : cut == kReach ? next >= target : next > target);
-        if (in) {
-            bin = tid * kPer + j;
-            spot_mass = run;
-            spot_count = num;
-            spot_size = h.count[j];
-        }
-        run = next;
-        num = nnum;
-    }
-    int first = first_thread(sh, bin >= 0, tid);
-    if (first == kThreads) {  // the last bin with a token
-        run = h.below;
-        num = h.before;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            if (h.count[j] > 0) {
-                bin = tid * kPer + j;
-                spot_mass = run;
-                spot_count = num;
-                spot_size = h.count[j];
-            }
-            run += h.mass[j];
-            num += h.count[j];
-        }
-        const uint64_t b = __ballot(bin >= 0);
-        const int lane = tid & (kWave - 1), wave = tid / kWave;
-        if (lane == 0) sh.wave_first[wave] = b ? wave * kWave + 63 - __builtin_clzll(b) : -1;
-        __syncthreads();
-        first = -1;
-        for (int i = 0; i < kWaves; ++i) first = max(first, sh.wave_first[i]);
-        __syncthreads();
-    }
-    if (tid == first) {
-        sh.spot_bin = bin;
-        sh.spot_mass = spot_mass;
-        sh.spot_count = spot_count;
-        sh.spot_size = spot_size;
-    }
-    __syncthreads();
-}
-
-// The cut inside a sorted list whose first token has `below` mass and `before` tokens before it.
-__device__ __forceinline__ Place cut_list(Shared &sh, const Listed &l, Cut cut, double target,
-                                          uint32_t nth, double below, uint32_t before, int tid) {
-    const double s = below + l.below + l.w;
-    const bool in = tid < l.n && (cut == kNumber ? before + tid + 1 >= nth
-                                  : cut == kReach ? s >= target
-                                                  : s > target);
-    int at = first_thread(sh, in, tid);
-    if (at >= l.n) at = l.n - 1;
-    if (tid == at) {
-        sh.spot_mass = s;
-        sh.list[0] = l.key;
-    }
-    __syncthreads();
-    Place p;
-    p.mass = sh.spot_mass;
-    const uint64_t key = sh.list[0];
-    __syncthreads();
-    p.id = key_id(key);
-    p.value = key_logit(key);
-    p.nth = 0;
-    p.w = 0.0;
-    return p;
-}
-
-// The cut among `size` tokens of one value.
-__device__ __forceinline__ Place cut_equal(float value, double w, uint32_t size, Cut cut,
-                                           double target, uint32_t nth, double below,
-                                           uint32_t before) {
-    uint32_t n;  // how many of them are taken
-    if (cut == kNumber) {
-        n = nth - before;
-    } else {
-        double q = floor((target - below) / w);
-        q = fmin(fmax(q - 1.0, 0.0), (double)size);
-        n = (uint32_t)q;
-        if (n < 1) n = 1;
-        while (n < size && !(cut == kReach ? below + n * w >= target : below + n * w > target)) ++n;
-    }
-    if (n > size) n = size;
-    Place p;
-    p.mass = below + (double)n * w;
-    p.w = w;
-    p.id = -1;
-    p.value = value;
-    p.nth = n - 1;
-    return p;
-}
-
-// The cut inside bin `bin` of the row (size tokens, `below` mass and `before` tokens before it).
-template <typename T>
-__device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange &ur, Shared &sh,
-                                      const Weights &w, int bin, uint32_t size, Cut cut,
-                                      double target, uint32_t nth, double below, uint32_t before,
-                                      int tid) {
-    uint32_t k0 = 0u, k1 = 0xFFFFFFFFu;
-    if (size > kCap) {  // the range of the bin's values
-        if (tid == 0) {
-            sh.key_lo = 0xFFFFFFFFu;
-            sh.key_hi = 0u;
-        }
-        __syncthreads();
-        uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-        each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = weight_y(w, x);
-            if (y < (double)kBins && (int)y == bin) {
-                const uint32_t vk = value_key(x);
-                lo = min(lo, vk);
-                hi = max(hi, vk);
-            }
-        });
-        if (lo <= hi) {
-            atomicMin(&sh.key_lo, lo);
-            atomicMax(&sh.key_hi, hi);
-        }
-        __syncthreads();
-        k0 = sh.key_lo;
-        k1 = sh.key_hi;
-        __syncthreads();
-    }
-    // Split by value until a part is small or a single value; every step narrows the range to a
-    // 4096th of it or to one value.
-    while (size > kCap && k0 != k1) {
-        const int bits = 32 - __clz(k1 - k0);
-        const int shift = bits > 12 ? bits - 12 : 0;
-        for (int b = tid; b < kBins; b += kThreads) {
-            sh.mass[b] = 0ull;
-            sh.count[b] = 0u;
-        }
-        __syncthreads();
-        each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = weight_y(w, x);
-            const uint32_t vk = value_key(x);
-            if (y < (double)kBins && (int)y == bin && vk >= k0 && vk <= k1) {
-                const uint32_t part = (k1 - vk) >> shift;
-                atomicAdd((unsigned long long *)&sh.mass[part],
-                          (unsigned long long)fixed_fraction(w, y - (double)bin));
-                atomicAdd(&sh.count[part], 1u);
-            }
-        });
-        __syncthreads();
-        const Bins h = take_bins(sh, w, false, bin_scale(bin), below, before, tid);
-        find_bin(sh, h, cut, target, nth, tid);
-        const uint32_t part = (uint32_t)sh.spot_bin;
-        below = sh.spot_mass;
-        before = sh.spot_count;
-        size = sh.spot_size;
-        __syncthreads();
-        k1 -= part << shift;
-        const uint32_t width = (1u << shift) - 1u;
-        k0 = k1 - k0 > width ? k1 - width : k0;
-    }
-    if (size > kCap) {
-        const float value = key_value(k1);
-        return cut_equal(value, weight_of(w, value), size, cut, target, nth, below, before);
-    }
-    const Listed l = gather(logits, ur, sh, w, bin, bin, k0, k1, tid);
-    Place p = cut_list(sh, l, cut, target, nth, below, before, tid);
-    p.w = weight_of(w, p.value);
-    return p;
-}
+using S16 = RowSampler<uint16_t, kNT>;
+using S32 = RowSampler<float, kNT32>;
 
 struct Settings {
     const float *temperature;
@@ -641,167 +60,475 @@ struct Settings {
     float all_min_p;
 };
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_kernel(const T *__restrict__ logits, int V,
-                                                          double one, Settings st,
-                                                          int32_t *__restrict__ tokens,
-                                                          float *__restrict__ logprob) {
-    __shared__ Shared sh;
-    const int tid = threadIdx.x;
+__device__ __forceinline__ RowSettings row_settings(const Settings &st, int64_t row) {
+    RowSettings r;
+    r.temperature = st.temperature ? st.temperature[row] : st.all_temperature;
+    r.top_k = st.top_k ? st.top_k[row] : st.all_top_k;
+    r.top_p = st.top_p ? st.top_p[row] : st.all_top_p;
+    r.min_p = st.min_p ? st.min_p[row] : st.all_min_p;
+    const float u = st.uniforms[row];
+    r.u = u > 0.f ? (double)fminf(u, 0x1.fffffep-1f) : 0.0;
+    return r;
+}
+
+__global__ __launch_bounds__(kNT32) void sample_f32_kernel(const float *__restrict__ logits, int V,
+                                                           double one, Settings st,
+                                                           int32_t *__restrict__ tokens,
+                                                           float *__restrict__ logprob) {
+    __shared__ S32::Shared sh;
     const int64_t row = blockIdx.x;
-    const UnitRange ur = unit_range(row, V, 1, Elem<T>::kPerVec);
-    const float temperature = st.temperature ? st.temperature[row] : st.all_temperature;
-    const int top_k = st.top_k ? st.top_k[row] : st.all_top_k;
-    const float top_p = st.top_p ? st.top_p[row] : st.all_top_p;
-    const float min_p = st.min_p ? st.min_p[row] : st.all_min_p;
-    const float uniform = st.uniforms[row];
-    const double u = uniform > 0.f ? (double)fminf(uniform, 0x1.fffffep-1f) : 0.0;
+    const UnitRange ur = unit_range(row, V, 1, Elem<float>::kPerVec);
+    S32::run(logits, ur, sh, row_settings(st, row), one, threadIdx.x, tokens + row,
+             logprob ? logprob + row : nullptr);
+}
 
-    auto answer = [&](int32_t id, double lp) {
-        if (tid == 0) {
-            tokens[row] = id;
-            if (logprob) logprob[row] = (float)lp;
-        }
-    };
-    const Top top = row_top(logits, ur, sh, tid);
-    if (top.m == -INFINITY) {  // nothing to draw
-        answer(-1, -INFINITY);
-        return;
-    }
-    if (!(temperature > 0.f)) {
-        answer(first_of_top(logits, ur, top, sh, tid), 0.0);
-        return;
-    }
-    if (top.m == INFINITY) {  // only the infinite logits have weight, all the same
-        uint32_t n;
-        nth_equal(logits, ur, sh, tid, INFINITY, 0u, n);
-        if (top_k >= 1 && (uint32_t)top_k < n) n = (uint32_t)top_k;
-        double whole = (double)n;
-        if (top_p < 1.f)
-            whole = cut_equal(INFINITY, 1.0, n, kReach, (double)top_p * whole, 0u, 0.0, 0u).mass;
-        const Place p = cut_equal(INFINITY, 1.0, n, kPass, u * whole, 0u, 0.0, 0u);
-        answer(nth_equal(logits, ur, sh, tid, INFINITY, p.nth, n), -log(whole));
-        return;
-    }
+// The general path of a bf16 row (a call: it must not weigh on the registers of the counting pass).
+__device__ __noinline__ void general_row(const uint16_t *logits, int64_t row, int V,
+                                         S16::Shared *sh, const RowSettings *st, double one,
+                                         int32_t *token, float *logprob) {
+    const UnitRange ur = unit_range(row, V, 1, Elem<uint16_t>::kPerVec);
+    S16::run(logits, ur, *sh, *st, one, threadIdx.x, token, logprob);
+}
 
-    Weights w;
-    w.m = top.m;
-    w.c = 92.332482616893656 / (double)temperature;  // 64 log2(e) / T
-    w.one = one;
-    for (int b = tid; b < kBins; b += kThreads) {
-        sh.mass[b] = 0ull;
-        sh.count[b] = 0u;
-    }
-    __syncthreads();
-    each(logits, ur, tid, [&](float x, int32_t) {
-        const double y = weight_y(w, x);
-        if (y < (double)kBins) {  // (false for NaN and -inf)
-            const int b = (int)y;
-            atomicAdd((unsigned long long *)&sh.mass[b],
-                      (unsigned long long)fixed_fraction(w, y - (double)b));
-            atomicAdd(&sh.count[b], 1u);
-        }
-    });
-    __syncthreads();
-    const Bins h = take_bins(sh, w, true, 1.0, 0.0, 0u, tid);
+// ---- counting ----------------------------------------------------------------------------------
 
-    // The lowest bin that the cuts can reach. (A top-k beyond the counted tokens cuts only among
-    // weights below 2^-64.)
-    const bool by_number = top_k >= 1 && (uint32_t)top_k < h.number;
-    const bool by_mass = top_p < 1.f;
-    const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;
-    const bool by_weight = least > 0x1p-60;
-    const int weight_bin = by_weight ? min((int)(-64.0 * log2(least)) + 1, kBins - 1) : kBins - 1;
-    int low = by_weight ? weight_bin : kBins - 1;
-    if (by_number) {
-        find_bin(sh, h, kNumber, 0.0, (uint32_t)top_k, tid);
-        // (top-p needs the whole mass of the top-k tokens, whatever min-p leaves of them)
-        low = by_mass ? sh.spot_bin : min(low, sh.spot_bin);
-        __syncthreads();
-    } else if (by_mass) {
-        find_bin(sh, h, kReach, (double)top_p * h.total, 0u, tid);
-        low = min(low, sh.spot_bin);
-        __syncthreads();
-    }
-    // tokens in the bins up to `low`
-    uint32_t upto = 0;
-    {
+// Counts one logit: `mag` its pattern without the sign, `sign` 0 or 1.
+__device__ __forceinline__ void tally(uint32_t *words, uint32_t mag, uint32_t sign) {
+    const int at = min(max((int)mag - (kBase - 1), 0), kValues + 1);
+    __hip_atomic_fetch_add(words + at, sign * 65535u + 1u, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+__device__ __forceinline__ void tally_vector(uint32_t *words, const u32x4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (tid * kPer + j <= low) upto += h.count[j];
-        uint32_t total;
-        scan_count(sh, upto, tid, total);
-        upto = total;
+    for (int i = 0; i < 4; ++i) {
+        tally(words, w[i] & 0x7FFFu, (w[i] >> 15) & 1u);
+        tally(words, (w[i] >> 16) & 0x7FFFu, w[i] >> 31);
     }
-    if (upto <= kCap) {
-        const Listed l = gather(logits, ur, sh, w, 0, low, 0u, 0xFFFFFFFFu, tid);
-        double z = h.total;
-        if (by_number)
-            z = cut_list(sh, l, kNumber, 0.0, (uint32_t)top_k, 0.0, 0u, tid).mass;
-        double whole = z;
-        if (by_mass) {
-            const double target = (double)top_p * z;
-            // (the list may end before the nucleus does, at a min-p cut)
-            if (first_thread(sh, tid < l.n && l.below + l.w >= target, tid) < l.n)
-                whole = fmin(whole, cut_list(sh, l, kReach, target, 0u, 0.0, 0u, tid).mass);
-        }
-        if (by_weight) {
-            const int n = first_thread(sh, !(tid < l.n && l.w >= least), tid);
-            whole = fmin(whole, cut_list(sh, l, kNumber, 0.0, (uint32_t)max(n, 1), 0.0, 0u, tid).mass);
-        }
-        const Place p = cut_list(sh, l, kPass, u * whole, 0u, 0.0, 0u, tid);
-        answer(p.id, log(weight_of(w, p.value) / whole));
-        return;
-    }
+}
 
-    // Cut by cut, each in its own bin; the draw is the last.
-    double z = h.total, whole = h.total;
-    if (by_weight) {
-        // all of the bins above those that the border can fall in, and what reaches it there
-        double part = 0.0;
-        each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = weight_y(w, x);
-            if (y < (double)kBins && (int)y <= weight_bin && (int)y >= weight_bin - 2) {
-                const double v = weight_of(w, x);
-                if (v >= least) part += v;
+// Counts a part by NT threads.
+template <int NT>
+__device__ __forceinline__ void count_part(const uint16_t *logits, const UnitRange &ur,
+                                           uint32_t *words, int tid) {
+    stream<NT>(
+        reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
+        [&](const u32x4 *v, int) {
+#pragma unroll
+            for (int u = 0; u < kStreamVectors; ++u) tally_vector(words, v[u]);
+        },
+        [&](const u32x4 &v, int) { tally_vector(words, v); });
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0) {
+        const uint32_t h = logits[e];
+        tally(words, h & 0x7FFFu, h >> 15);
+    }
+}
+
+// The value at place q of the candidate order: positive values from the largest down, then the
+// negative ones.
+__device__ __forceinline__ uint32_t place_word(int q) {  // its word
+    return (uint32_t)(q < kValues ? kValues - q : q - kValues + 1);
+}
+__device__ __forceinline__ float place_value(int q) {
+    const uint32_t mag = place_word(q) + (kBase - 1);
+    return __uint_as_float((q < kValues ? mag : mag | 0x8000u) << 16);
+}
+__device__ __forceinline__ uint32_t half(uint32_t word, bool negative) {
+    return negative ? word >> 16 : word & 0xFFFFu;
+}
+
+// Where the counts of a row's parts are: in this workgroup's LDS, ...
+struct LocalCounts {
+    const uint32_t *words;  // [kParts][kStride]
+    __device__ __forceinline__ int parts() const { return kParts; }
+    __device__ __forceinline__ uint32_t part(int p, uint32_t word, bool negative) const {
+        return half(words[p * kStride + word], negative);
+    }
+    __device__ __forceinline__ uint32_t count(uint32_t word, bool negative) const {
+        uint32_t n = 0;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) n += half(words[p * kStride + word], negative);
+        return n;
+    }
+};
+
+// ... or in the workspace, with their sums in LDS (positive, then negative).
+struct SlicedCounts {
+    const uint32_t *words;  // [slices][kStride]
+    const uint32_t *sums;   // [2][kStride]
+    int slices;
+    __device__ __forceinline__ int parts() const { return slices; }
+    __device__ __forceinline__ uint32_t part(int p, uint32_t word, bool negative) const {
+        return half(words[(size_t)p * kStride + word], negative);
+    }
+    __device__ __forceinline__ uint32_t count(uint32_t word, bool negative) const {
+        return sums[(negative ? kStride : 0) + word];
+    }
+};
+
+// ---- a row from its counts -----------------------------------------------------------------------
+
+// What a thread knows of its places [tid kPerThread, + kPerThread).
+struct Run {
+    double mass, below;
+    uint32_t count, before;
+};
+
+// The gathered small values (|x| < 2^-20), in candidate order.
+struct Small {
+    int n;
+    double mass, below;
+    uint32_t before;
+};
+
+// The value a cut falls on.
+struct Spot {
+    float value;
+    double w, below;
+    uint32_t size, before;
+    int small;  // index into the gathered small values, -1 if a counted value
+    int q;
+};
+
+template <typename Counts>
+__device__ __forceinline__ Spot find_spot(S16::Shared &sh, const Counts &counts, const Weights &w,
+                                          const Run &run, const Small &small, Cut cut,
+                                          double target, uint32_t nth, int tid) {
+    auto meets = [&](double mass, uint32_t number) {
+        return cut == kNumber ? number >= nth : cut == kReach ? mass >= target : mass > target;
+    };
+    const int first = S16::first_thread(
+        sh, run.count > 0 && meets(run.below + run.mass, run.before + run.count), tid);
+    Spot s;
+    s.small = -1;
+    if (small.n > 0 && first >= kNT / 2 &&
+        meets(small.below + small.mass, small.before + small.n)) {
+        s.small = 0;
+        s.q = -1;
+        s.below = small.below;
+        s.before = small.before;
+        s.w = 0.0;
+        for (int i = 0; i < small.n; ++i) {  // few: every thread walks them
+            s.value = key_logit(sh.list[i]);
+            s.w = weight_of(w, s.value);
+            s.small = i;
+            if (i == small.n - 1 || meets(s.below + s.w, s.before + 1)) break;
+            s.below += s.w;
+            ++s.before;
+        }
+        s.size = 1;
+        return s;
+    }
+    // Roundings may leave a mass cut behind everything: it falls on the last counted value then.
+    int owner = first;
+    if (first == kNT) {
+        const uint64_t b = __ballot(run.count > 0);
+        const int wave = tid / kWave;
+        if ((tid & (kWave - 1)) == 0)
+            sh.wave_first[wave] = b ? wave * kWave + 63 - __builtin_clzll(b) : 0;
+        __syncthreads();
+        owner = 0;
+        for (int i = 0; i < S16::kWaves; ++i) owner = max(owner, sh.wave_first[i]);
+        __syncthreads();
+    }
+    if (tid == owner) {
+        sh.spot_mass = run.below;
+        sh.spot_count = run.before;
+    }
+    __syncthreads();
+    // every wave looks through the owner's places, one to a lane
+    const int lane = tid & (kWave - 1);
+    const int q = owner * kPerThread + min(lane, kPerThread - 1);
+    const float value = place_value(q);
+    const double y = weight_y(w, value);
+    const bool counted = lane < kPerThread && value <= w.m && y < (double)kBins;
+    const uint32_t n = counted ? counts.count(place_word(q), q >= kValues) : 0u;
+    const double wt = n > 0 ? weight_of(w, value) : 0.0;
+    double mass = wt * (double)n;
+    uint32_t number = n;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+        const double a = __shfl_up(mass, o);
+        const uint32_t b = __shfl_up(number, o);
+        if (lane >= o) {
+            mass += a;
+            number += b;
+        }
+    }
+    const double base = sh.spot_mass;
+    const uint32_t start = sh.spot_count;
+    __syncthreads();
+    uint64_t in = __ballot(n > 0 && meets(base + mass, start + number));
+    const uint64_t any = __ballot(n > 0);
+    const int at = in ? __builtin_ctzll(in) : any ? 63 - __builtin_clzll(any) : 0;
+    const double upto = __shfl(mass, at > 0 ? at - 1 : 0);
+    const uint32_t upto_n = __shfl(number, at > 0 ? at - 1 : 0);
+    s.below = base + (at > 0 ? upto : 0.0);
+    s.before = start + (at > 0 ? upto_n : 0u);
+    s.value = __shfl(value, at);
+    s.w = __shfl(wt, at);
+    s.size = __shfl(n, at);
+    s.q = owner * kPerThread + at;
+    return s;
+}
+static_assert(kPerThread <= 16, "a scan over 16 lanes");
+
+// Settles a row from the counts of its parts. False (in every thread) if the row is one for the
+// general path; nothing is written then.
+template <typename Counts>
+__device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int V,
+                                       const Counts &counts, S16::Shared &sh,
+                                       const RowSettings &st, int tid, int32_t *token,
+                                       float *logprob) {
+    const int lane = tid & (kWave - 1);
+    if (tid < 64) sh.scale[tid] = exp2((double)tid * (-1.0 / 64.0));
+    // counts of this thread's places
+    const bool negative = tid >= kNT / 2;
+    uint32_t c[kPerThread];
+    uint32_t mine = 0;
+    int first_q = 2 * kValues;
+#pragma unroll
+    for (int j = kPerThread - 1; j >= 0; --j) {
+        const int q = tid * kPerThread + j;
+        c[j] = counts.count(place_word(q), negative);
+        mine += c[j];
+        if (c[j] > 0) first_q = q;
+    }
+    const uint32_t small_n = counts.count(0, false) + counts.count(0, true);
+    const uint32_t large_pos = counts.count(kValues + 1, false);
+    const uint32_t large_neg = counts.count(kValues + 1, true);
+    uint32_t total;
+    S16::scan_count(sh, mine, tid, total);
+    if (total + small_n + large_pos + large_neg != (uint32_t)V || large_pos > 0 ||
+        small_n > kSmallCap || total + small_n == 0)
+        return false;
+    // the small values, gathered and sorted
+    Small small{(int)small_n, 0.0, 0.0, 0u};
+    if (small_n > 0) {
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        const UnitRange ur = unit_range(row, V, 1, Elem<uint16_t>::kPerVec);
+        S16::each(logits, ur, tid, [&](float x, int32_t id) {
+            if (fabsf(x) < 0x1p-20f) {
+                const uint32_t at = atomicAdd(&sh.listed, 1u);
+                if (at < kSmallCap) sh.list[at] = cand_key(x, id);
             }
         });
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (tid * kPer + j < weight_bin - 2) part += h.mass[j];
-        double sum;
-        scan_mass(sh, part, tid, sum);
-        whole = fmin(whole, sum);
-    }
-    Place p;
-#pragma unroll 1
-    for (int step = by_number ? 0 : by_mass ? 1 : 2; step < 3; ++step) {
-        if (step == 1 && !by_mass) continue;
-        const Cut cut = step == 0 ? kNumber : step == 1 ? kReach : kPass;
-        const double target = step == 1 ? (double)top_p * z : u * whole;
-        find_bin(sh, h, cut, target, (uint32_t)top_k, tid);
-        const int bin = sh.spot_bin;
-        const double below = sh.spot_mass;
-        const uint32_t before = sh.spot_count, size = sh.spot_size;
         __syncthreads();
-        p = cut_bin(logits, ur, sh, w, bin, size, cut, target, (uint32_t)top_k, below, before, tid);
-        if (step == 0) z = p.mass;
-        if (step < 2) whole = fmin(whole, p.mass);
+        if (tid < kWave) {
+            const uint64_t key = wave_sort_desc(lane < (int)small_n ? sh.list[lane] : 0ull, lane);
+            sh.list[lane] = key;
+        }
+        __syncthreads();
     }
-    int32_t id = p.id;
-    if (id < 0) {
+    // the maximum
+    const int owner = S16::first_thread(sh, mine > 0, tid);
+    if (tid == owner) sh.spot_bin = first_q;
+    __syncthreads();
+    const int top_q = owner == kNT ? 2 * kValues : sh.spot_bin;
+    __syncthreads();
+    const bool top_small = small_n > 0 && top_q >= kValues;
+    const float m = top_small ? key_logit(sh.list[0]) : place_value(top_q);
+
+    float value = m;
+    uint32_t nth = 0;
+    int32_t id = -1;
+    int found_q = top_q;
+    double lp = 0.0;
+    if (st.temperature > 0.f) {
+        const Weights w{m, kBinsPerE / (double)st.temperature, 1.0, sh.scale};
+        if (large_neg > 0 && !(weight_y(w, -256.f) >= (double)kBins)) return false;
+        const bool by_weight = st.min_p > 0.f;
+        const double least = by_weight ? fmin((double)st.min_p, 1.0) : 0.0;
+        Run run{0.0, 0.0, 0u, 0u};
+        double heavy = 0.0;  // mass of the weights that min_p keeps
+#pragma unroll
+        for (int j = 0; j < kPerThread; ++j) {
+            if (c[j] > 0) {
+                const float x = place_value(tid * kPerThread + j);
+                if (weight_y(w, x) < (double)kBins) {
+                    const double wt = weight_of(w, x);
+                    const double mass = wt * (double)c[j];
+                    run.mass += mass;
+                    run.count += c[j];
+                    if (wt >= least) heavy += mass;
+                }
+            }
+        }
+        for (int i = 0; i < small.n; ++i) {
+            const float x = key_logit(sh.list[i]);
+            if (!(weight_y(w, x) < (double)kBins)) {  // (they are in order: the rest has none either)
+                small.n = i;
+                break;
+            }
+            const double wt = weight_of(w, x);
+            small.mass += wt;
+            if (tid == 0 && wt >= least) heavy += wt;
+        }
+        double z, whole_heavy = 0.0;
+        uint32_t number;
+        run.below = S16::scan_mass(sh, run.mass, tid, z);
+        run.before = S16::scan_count(sh, run.count, tid, number);
+        if (by_weight) S16::scan_mass(sh, heavy, tid, whole_heavy);
+        if (small.n > 0) {  // between the positive and the negative values
+            if (tid == kNT / 2) {
+                sh.spot_mass = run.below;
+                sh.spot_count = run.before;
+            }
+            __syncthreads();
+            small.below = sh.spot_mass;
+            small.before = sh.spot_count;
+            __syncthreads();
+            if (negative) {
+                run.below += small.mass;
+                run.before += (uint32_t)small.n;
+            }
+            z += small.mass;
+            number += (uint32_t)small.n;
+        }
+        auto cut_at = [&](const Spot &s, Cut cut, double target, uint32_t k) {
+            return cut_equal(s.value, s.w, s.size, cut, target, k, s.below, s.before);
+        };
+        double whole = z;
+        if (st.top_k >= 1 && (uint32_t)st.top_k < number) {
+            const uint32_t k = (uint32_t)st.top_k;
+            const Spot s = find_spot(sh, counts, w, run, small, kNumber, 0.0, k, tid);
+            z = cut_at(s, kNumber, 0.0, k).mass;
+            whole = z;
+        }
+        if (st.top_p < 1.f) {
+            const double target = (double)st.top_p * z;
+            const Spot s = find_spot(sh, counts, w, run, small, kReach, target, 0u, tid);
+            whole = fmin(whole, cut_at(s, kReach, target, 0u).mass);
+        }
+        if (by_weight) whole = fmin(whole, whole_heavy);
+        const double target = st.u * whole;
+        const Spot s = find_spot(sh, counts, w, run, small, kPass, target, 0u, tid);
+        const Place p = cut_at(s, kPass, target, 0u);
+        value = s.value;
+        nth = p.nth;
+        found_q = s.q;
+        if (s.small >= 0) id = key_id(sh.list[s.small]);
+        lp = log(s.w / whole);
+    } else if (top_small) {
+        id = key_id(sh.list[0]);
+    }
+    if (id < 0) {  // number nth of its equals: the part that holds it, then the logit itself
+        const uint32_t word = place_word(found_q);
+        int part = 0;
+        uint32_t left = nth;
+        for (; part < counts.parts() - 1; ++part) {
+            const uint32_t n = counts.part(part, word, found_q >= kValues);
+            if (left < n) break;
+            left -= n;
+        }
+        const int64_t unit = row * counts.parts() + part;
+        const UnitRange ur = unit_range(unit, V, counts.parts(), Elem<uint16_t>::kPerVec);
         uint32_t n;
-        id = nth_equal(logits, ur, sh, tid, p.value, p.nth, n);
+        id = S16::nth_equal(logits, ur, sh, tid, value, left, n);
     }
-    answer(id, log(p.w / whole));
+    if (tid == 0) {
+        *token = id;
+        if (logprob) *logprob = (float)lp;
+    }
+    return true;
+}
+
+// A row per workgroup.
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void
+sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Settings st,
+                   int32_t *__restrict__ tokens, float *__restrict__ logprob) {
+    __shared__ S16::Shared sh;
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    constexpr int kGroup = kNT / kParts;
+    const int part = tid / kGroup;
+    const UnitRange ur = unit_range(row * kParts + part, V, kParts, Elem<uint16_t>::kPerVec);
+    u32x4 *clear = reinterpret_cast<u32x4 *>(sh.words);
+    for (int i = tid; i < kCountWords / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
+    __syncthreads();
+    count_part<kGroup>(logits, ur, sh.words + part * kStride, tid & (kGroup - 1));
+    __syncthreads();
+    const RowSettings rs = row_settings(st, row);
+    int32_t *token = tokens + row;
+    float *lp = logprob ? logprob + row : nullptr;
+    if (!settle(logits, row, V, LocalCounts{sh.words}, sh, rs, tid, token, lp)) {
+        __syncthreads();
+        general_row(logits, row, V, &sh, &rs, one, token, lp);
+    }
+}
+
+// A slice per workgroup: its counts go to the workspace, [R][slices][kStride].
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void
+sample_count_kernel(const uint16_t *__restrict__ logits, int V, int slices,
+                    uint32_t *__restrict__ words) {
+    __shared__ __attribute__((aligned(16))) uint32_t sh[kStride];
+    const int tid = threadIdx.x;
+    const UnitRange ur = unit_range(blockIdx.x, V, slices, Elem<uint16_t>::kPerVec);
+    u32x4 *clear = reinterpret_cast<u32x4 *>(sh);
+    for (int i = tid; i < kStride / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
+    __syncthreads();
+    count_part<kNT>(logits, ur, sh, tid);
+    __syncthreads();
+    u32x4 *out = reinterpret_cast<u32x4 *>(words + (size_t)blockIdx.x * kStride);
+    for (int i = tid; i < kStride / 4; i += kNT) out[i] = clear[i];
+}
+
+// Joins a row's slices and settles it.
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void
+sample_settle_kernel(const uint16_t *__restrict__ logits, int V, int slices, double one,
+                     Settings st, const uint32_t *__restrict__ words,
+                     int32_t *__restrict__ tokens, float *__restrict__ logprob) {
+    __shared__ S16::Shared sh;
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const uint32_t *mine = words + (size_t)row * slices * kStride;
+    uint32_t *sums = sh.words;  // [2][kStride]
+    for (int i = tid; i < kStride / 4; i += kNT) {
+        u32x4 lo = u32x4{0u, 0u, 0u, 0u}, hi = lo;
+#pragma unroll 8
+        for (int s = 0; s < slices; ++s) {
+            const u32x4 v = reinterpret_cast<const u32x4 *>(mine + (size_t)s * kStride)[i];
+            lo += v & 0xFFFFu;
+            hi += v >> 16;
+        }
+        reinterpret_cast<u32x4 *>(sums)[i] = lo;
+        reinterpret_cast<u32x4 *>(sums + kStride)[i] = hi;
+    }
+    __syncthreads();
+    const RowSettings rs = row_settings(st, row);
+    int32_t *token = tokens + row;
+    float *lp = logprob ? logprob + row : nullptr;
+    if (!settle(logits, row, V, SlicedCounts{mine, sums, slices}, sh, rs, tid, token, lp)) {
+        __syncthreads();
+        general_row(logits, row, V, &sh, &rs, one, token, lp);
+    }
+}
+
+// Slices per bf16 row: about 512 workgroups in all when rows are few, each of two vectors and more
+// per thread.
+int plan_slices(int R, int V) {
+    if (R >= kRowGroups) return 1;
+    int s = 2 * kRowGroups / R;
+    if (s > kMaxSlices) s = kMaxSlices;
+    const int most = V / 8 / (2 * kNT);
+    if (s > most) s = most;
+    return s < 1 ? 1 : s;
 }
 
 }  // namespace
 
+size_t sample_workspace_bytes(int R, int V, int dtype) {
+    const int slices = dtype == 0 ? 1 : plan_slices(R, V);
+    return slices == 1 ? 0 : (size_t)R * slices * kStride * sizeof(uint32_t);
+}
+
 hipError_t launch_sample(const void *logits, int dtype, int R, int V, const float *temperature,
                          float all_temperature, const int32_t *top_k, int all_top_k,
                          const float *top_p, float all_top_p, const float *min_p, float all_min_p,
-                         const float *uniforms, int32_t *tokens, float *logprob,
+                         const float *uniforms, int32_t *tokens, float *logprob, void *ws,
                          hipStream_t stream) {
     const Settings st{temperature, top_k, top_p, min_p, uniforms, all_temperature, all_top_k,
                       all_top_p, all_min_p};
@@ -810,12 +537,26 @@ hipError_t launch_sample(const void *logits, int dtype, int R, int V, const floa
     while ((1ll << bits) <= V) ++bits;
     const int frac = bits <= 22 ? 41 : 63 - bits;
     const double one = (double)(1ull << frac);
-    if (dtype == 0)
-        hipLaunchKernelGGL((sample_kernel<float>), dim3((unsigned)R), dim3(kThreads), 0, stream,
+    const dim3 rows((unsigned)R);
+    if (dtype == 0) {
+        hipLaunchKernelGGL(sample_f32_kernel, rows, dim3(kNT32), 0, stream,
                            static_cast<const float *>(logits), V, one, st, tokens, logprob);
-    else
-        hipLaunchKernelGGL((sample_kernel<uint16_t>), dim3((unsigned)R), dim3(kThreads), 0, stream,
-                           static_cast<const uint16_t *>(logits), V, one, st, tokens, logprob);
+        return hipGetLastError();
+    }
+    const uint16_t *x = static_cast<const uint16_t *>(logits);
+    const int slices = plan_slices(R, V);
+    if (slices == 1) {
+        hipLaunchKernelGGL(sample_bf16_kernel, rows, dim3(kNT), 0, stream, x, V, one, st, tokens,
+                           logprob);
+        return hipGetLastError();
+    }
+    uint32_t *words = static_cast<uint32_t *>(ws);
+    hipLaunchKernelGGL(sample_count_kernel, dim3((unsigned)(R * slices)), dim3(kNT), 0, stream, x,
+                       V, slices, words);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sample_settle_kernel, rows, dim3(kNT), 0, stream, x, V, slices, one, st,
+                       words, tokens, logprob);
     return hipGetLastError();
 }
 

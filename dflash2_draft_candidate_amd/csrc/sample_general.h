@@ -1,0 +1,792 @@
+// Sampling a token from a row of vocabulary logits, by one workgroup of NT threads: the general path
+// (any type, any values). sample.hip has the definitions and the faster path for bf16 rows.
+//
+// The token is a whole number that a rounding can change, and a flat row has more than 10^5 tokens
+// whose shares a 32-bit sum cannot tell apart: weights and masses are held to about 2^-40.
+// With y = 64 log2(e) (m - x) / T in fp64 and b = floor(y), a weight is 2^(-b/64) 2^(-(y-b)/64); the
+// second factor, within 1% of 1, is a polynomial of degree 5 (error 2.2e-15). b is also the
+// weight's bin: bins follow the candidate order, because y does. A bin's second factors are summed
+// as 64-bit integers (kFracBits behind the point) by LDS atomics: whole numbers have no order of
+// summation, so results do not depend on which wave came first. Bins end at b = 4096, weight 2^-64 of
+// the largest: what lies below adds less than 2^-36 of a unit in the last place of u W.
+//
+// The row is read for its maximum (and, for T = 0, where it first stands) and for the histogram of
+// the bins; then each cut is found among the bins' running masses and inside its bin. Where the
+// tokens from the top to the lowest cut are few (<= NT) they are gathered once, sorted, and
+// everything is settled in that list. Otherwise each cut gathers and sorts its own bin, which is
+// split by value first if it holds more than NT tokens; when a single value remains, its tokens are
+// equal and a division tells how many of them a cut takes.
+#pragma once
+
+#include <float.h>
+
+#include "device_common.h"
+#include "row_stream.h"
+
+namespace dflash2 {
+
+constexpr int kBins = 4096;
+constexpr int kCountWords = 4 * 3588;
+constexpr double kBinsPerE = 92.332482616893656;  // 64 log2(e)
+constexpr double kTwo52 = 4503599627370496.0;
+
+enum Cut { kNumber, kReach, kPass };  // the n-th token; first S >= target; first S > target
+
+
+// The settings of one row.
+struct RowSettings {
+    float temperature;
+    int top_k;
+    float top_p, min_p;
+    double u;  // in [0, 1)
+};
+
+// The weights of a row.
+struct Weights {
+    float m;              // row maximum (finite)
+    double c;             // 64 log2(e) / T
+    double one;           // 2^kFracBits of this vocabulary
+    const double *scale;  // 2^(-i/64), i < 64
+};
+
+__device__ __forceinline__ double weight_y(const Weights &w, float x) {
+    return ((double)w.m - (double)x) * w.c;
+}
+
+// 2^(-f/64) for f in [0, 1): the Taylor polynomial of exp(-f ln2/64); the next term is below 2.2e-15.
+__device__ __forceinline__ double fraction(double f) {
+    constexpr double a = kLn2 / 64.0;
+    double p = -a * a * a * a * a / 120.0;
+    p = __builtin_fma(p, f, a * a * a * a / 24.0);
+    p = __builtin_fma(p, f, -a * a * a / 6.0);
+    p = __builtin_fma(p, f, a * a / 2.0);
+    p = __builtin_fma(p, f, -a);
+    return __builtin_fma(p, f, 1.0);
+}
+
+// round(2^kFracBits fraction): adding 2^52 leaves the integer in the low mantissa bits.
+__device__ __forceinline__ uint64_t fixed_fraction(const Weights &w, double f) {
+    const double v = __builtin_fma(fraction(f), w.one, kTwo52);
+    return (uint64_t)__double_as_longlong(v) & 0xFFFFFFFFFFFFFull;
+}
+
+__device__ __forceinline__ double bin_scale(const Weights &w, int b) {
+    return ldexp(w.scale[b & 63], -(b >> 6));
+}
+
+__device__ __forceinline__ double weight_of(const Weights &w, float x) {
+    const double y = weight_y(w, x);
+    const int b = (int)y;
+    return fraction(y - (double)b) * bin_scale(w, b);
+}
+
+// A place in the candidate order.
+struct Place {
+    double mass;  // running mass up to and including the token
+    double w;     // its weight
+    int32_t id;   // its id, or -1: number `nth` of the tokens of logit `value`
+    float value;
+    uint32_t nth;
+};
+
+// The cut among `size` tokens of one value.
+__device__ __forceinline__ Place cut_equal(float value, double w, uint32_t size, Cut cut,
+                                           double target, uint32_t nth, double below,
+                                           uint32_t before) {
+    uint32_t n;  // how many of them are taken
+    if (cut == kNumber) {
+        n = nth - before;
+    } else {
+        double q = floor((target - below) / w);
+        q = fmin(fmax(q - 1.0, 0.0), (double)size);
+        n = (uint32_t)q;
+        if (n < 1) n = 1;
+        while (n < size && !(cut == kReach ? below + n * w >= target : below + n * w > target)) ++n;
+    }
+    if (n > size) n = size;
+    Place p;
+    p.mass = below + (double)n * w;
+    p.w = w;
+    p.id = -1;
+    p.value = value;
+    p.nth = n - 1;
+    return p;
+}
+
+template <typename T, int NT>
+struct RowSampler {
+static constexpr int EV = Elem<T>::kPerVec;
+static constexpr int kThreads = NT;
+static constexpr int kWaves = NT / kWave;
+static constexpr int kPer = kBins / NT;  // bins per thread
+static constexpr int kCap = NT;          // gathered tokens, one per thread
+
+struct Shared {
+    union {
+        struct {
+            uint64_t mass[kBins];
+            uint32_t count[kBins];
+        };
+        uint32_t words[sizeof(T) == 2 ? kCountWords : 1];  // sample.hip: counts of bf16 values
+    };
+    uint64_t list[kCap];
+    double scale[64];  // 2^(-i/64)
+    double wave_mass[kWaves];
+    uint32_t wave_count[kWaves];
+    int wave_first[kWaves];
+    float wave_max[kWaves];
+    uint32_t listed;
+    uint32_t key_lo, key_hi;
+    int32_t token;
+    double spot_mass;
+    uint32_t spot_count;
+    int spot_bin;
+    uint32_t spot_size;
+};
+
+// ---- workgroup steps -------------------------------------------------------------------------
+
+// Exclusive running sum over the threads; `total` is the sum. The result of thread t + 1 is at
+// least that of thread t plus its v up to one rounding.
+static __device__ __forceinline__ double scan_mass(Shared &sh, double v, int tid, double &total) {
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    double s = v;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const double t = __shfl_up(s, o);
+        if (lane >= o) s += t;
+    }
+    if (lane == kWave - 1) sh.wave_mass[wave] = s;
+    __syncthreads();
+    double base = 0.0, all = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i == wave) base = all;
+        all += sh.wave_mass[i];
+    }
+    __syncthreads();
+    total = all;
+    const double before = __shfl_up(s, 1);
+    return lane == 0 ? base : base + before;
+}
+
+static __device__ __forceinline__ uint32_t scan_count(Shared &sh, uint32_t v, int tid, uint32_t &total) {
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    uint32_t s = v;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const uint32_t t = __shfl_up(s, o);
+        if (lane >= o) s += t;
+    }
+    if (lane == kWave - 1) sh.wave_count[wave] = s;
+    __syncthreads();
+    uint32_t base = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i == wave) base = all;
+        all += sh.wave_count[i];
+    }
+    __syncthreads();
+    total = all;
+    return base + s - v;
+}
+
+// The first thread for which `c` holds, kThreads if none.
+static __device__ __forceinline__ int first_thread(Shared &sh, bool c, int tid) {
+    const uint64_t b = __ballot(c);
+    if ((tid & (kWave - 1)) == 0)
+        sh.wave_first[tid / kWave] = b ? (tid + __builtin_ctzll(b)) : kThreads;
+    __syncthreads();
+    int first = kThreads;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) first = min(first, sh.wave_first[i]);
+    __syncthreads();
+    return first;
+}
+
+// The row: f(x, id) for each of its elements, in no particular order; the next two vectors are in
+// flight while two are worked on (the passes that use this are bound by their arithmetic).
+template <typename F>
+static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, F &&f) {
+    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    auto one = [&](const u32x4 &v, int i) {
+        float x[EV];
+        Elem<T>::unpack(v, x);
+#pragma unroll
+        for (int k = 0; k < EV; ++k) f(x[k], id0 + i * EV + k);
+    };
+    u32x4 a = u32x4{}, b = u32x4{};
+    if (tid < ur.nv) a = p[tid];
+    if (tid + NT < ur.nv) b = p[tid + NT];
+#pragma unroll 1
+    for (int i = tid; i < ur.nv; i += 2 * NT) {
+        u32x4 c = u32x4{}, d = u32x4{};
+        if (i + 2 * NT < ur.nv) c = p[i + 2 * NT];
+        if (i + 3 * NT < ur.nv) d = p[i + 3 * NT];
+        one(a, i);
+        if (i + NT < ur.nv) one(b, i + NT);
+        a = c;
+        b = d;
+    }
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0) f(Elem<T>::load(logits, e), (int32_t)(e - ur.g0));
+}
+
+// The row's maximum over what is not NaN, in every thread; `at` is where this thread met its own
+// (a vector index; the element lies there or up to kStreamVectors - 1 strides on).
+struct Top {
+    float m;     // of the row
+    float mine;  // of this thread's vectors
+    int at;
+};
+
+static __device__ __forceinline__ Top row_top(const T *logits, const UnitRange &ur, Shared &sh, int tid) {
+    Top t{-INFINITY, -INFINITY, 0};
+    stream<kThreads>(
+        reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
+        [&](const u32x4 *v, int i) {
+            float x[kStreamVectors * EV];
+#pragma unroll
+            for (int u = 0; u < kStreamVectors; ++u) Elem<T>::unpack(v[u], x + u * EV);
+            float c = x[0];
+#pragma unroll
+            for (int k = 1; k < kStreamVectors * EV; ++k) c = fmaxf(c, x[k]);
+            if (c > t.mine) {
+                t.mine = c;
+                t.at = i;
+            }
+        },
+        [&](const u32x4 &v, int i) {
+            float x[EV];
+            Elem<T>::unpack(v, x);
+            float c = x[0];
+#pragma unroll
+            for (int k = 1; k < EV; ++k) c = fmaxf(c, x[k]);
+            if (c > t.mine) {
+                t.mine = c;
+                t.at = i;
+            }
+        });
+    float m = t.mine;
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0) m = fmaxf(m, Elem<T>::load(logits, e));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((tid & (kWave - 1)) == 0) sh.wave_max[tid / kWave] = m;
+    __syncthreads();
+    m = sh.wave_max[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.wave_max[w]);
+    __syncthreads();
+    t.m = m;
+    return t;
+}
+
+// The lowest id whose logit is the row's maximum.
+static __device__ __forceinline__ int32_t first_of_top(const T *logits, const UnitRange &ur, const Top &t,
+                                                Shared &sh, int tid) {
+    if (tid == 0) sh.token = 0x7FFFFFFF;
+    __syncthreads();
+    int32_t id = 0x7FFFFFFF;
+    if (t.mine == t.m) {
+        for (int u = kStreamVectors - 1; u >= 0; --u) {
+            const int i = t.at + u * kThreads;
+            if (i >= ur.nv) continue;
+            float x[EV];
+            Elem<T>::unpack(reinterpret_cast<const u32x4 *>(logits)[ur.c0 + i], x);
+#pragma unroll
+            for (int k = EV - 1; k >= 0; --k)
+                if (x[k] == t.m) id = (int32_t)((ur.c0 + i) * EV + k - ur.g0);
+        }
+    }
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0 && Elem<T>::load(logits, e) == t.m) id = min(id, (int32_t)(e - ur.g0));
+    if (id != 0x7FFFFFFF) atomicMin(&sh.token, id);
+    __syncthreads();
+    id = sh.token;
+    __syncthreads();
+    return id;
+}
+
+// How many logits equal `value`, and the id of number `nth` (from 0, by id) among them, -1 if there
+// are not so many. Wave w takes the w-th run of the row's vectors.
+static __device__ __forceinline__ int32_t nth_equal(const T *logits, const UnitRange &ur, Shared &sh, int tid,
+                                          float value, uint32_t nth, uint32_t &total) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    const int v0 = (int)((int64_t)ur.nv * wave / kWaves);
+    const int v1 = (int)((int64_t)ur.nv * (wave + 1) / kWaves);
+    auto matches = [&](int i) {  // which elements of vector i match
+        uint32_t bits = 0;
+        if (i < v1) {
+            float x[EV];
+            Elem<T>::unpack(p[i], x);
+#pragma unroll
+            for (int k = 0; k < EV; ++k) bits |= x[k] == value ? 1u << k : 0u;
+        }
+        return bits;
+    };
+    uint32_t mine = 0;
+    for (int i = v0; i < v1; i += kWave) mine += __popc(matches(i + lane));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
+    if (lane == 0) sh.wave_count[wave] = mine;
+    if (tid == 0) sh.token = -1;
+    __syncthreads();
+    uint32_t head = 0, tail = 0;
+    for (int64_t e = ur.h0; e < ur.h1; ++e) head += Elem<T>::load(logits, e) == value;
+    for (int64_t e = ur.t0; e < ur.t1; ++e) tail += Elem<T>::load(logits, e) == value;
+    uint32_t before = head, base = head;
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) base = before;
+        before += sh.wave_count[w];
+    }
+    total = before + tail;
+    if (tid == 0 && (nth < head || (nth >= before && nth < total))) {
+        uint32_t left = nth < head ? nth : nth - before;
+        for (int64_t e = nth < head ? ur.h0 : ur.t0;; ++e)
+            if (Elem<T>::load(logits, e) == value && left-- == 0) {
+                sh.token = (int32_t)(e - ur.g0);
+                break;
+            }
+    }
+    if (nth >= base && nth < base + mine) {  // this wave's run holds it
+        uint32_t left = nth - base;
+        for (int i = v0; i < v1; i += kWave) {
+            const uint32_t bits = matches(i + lane);
+            uint32_t s = __popc(bits);
+            const uint32_t own = s;
+#pragma unroll
+            for (int o = 1; o < kWave; o <<= 1) {
+                const uint32_t t = __shfl_up(s, o);
+                if (lane >= o) s += t;
+            }
+            const uint32_t all = __shfl(s, kWave - 1);
+            if (left < all) {
+                uint32_t k = left - (s - own);
+                if (left >= s - own && left < s) {
+                    uint32_t b = bits;
+                    while (k-- > 0) b &= b - 1;
+                    sh.token = id0 + (i + lane) * EV + (__ffs(b) - 1);
+                }
+                break;
+            }
+            left -= all;
+        }
+    }
+    __syncthreads();
+    const int32_t id = sh.token;
+    __syncthreads();
+    return id;
+}
+
+// ---- the gathered list --------------------------------------------------------------------------
+
+// One gathered token per thread in candidate order (threads below n), with running masses.
+struct Listed {
+    uint64_t key;
+    double w;      // 0 for threads from n on
+    double below;  // masses of the tokens before it
+    int n;
+};
+
+// Sorts sh.list[0 .. n) in candidate order, a key per thread: waves sort 64 by lane exchanges,
+// larger strides go through LDS. Keys are distinct, so the order is unique.
+static __device__ __forceinline__ uint64_t sort_list(Shared &sh, int n, int tid) {
+    const int lane = tid & (kWave - 1);
+    uint64_t key = tid < n ? sh.list[tid] : 0ull;
+    key = bitonic_merge_steps<1>(key, lane, (lane & 2) == 0);
+    key = bitonic_merge_steps<2>(key, lane, (lane & 4) == 0);
+    key = bitonic_merge_steps<4>(key, lane, (lane & 8) == 0);
+    key = bitonic_merge_steps<8>(key, lane, (lane & 16) == 0);
+    key = bitonic_merge_steps<16>(key, lane, (lane & 32) == 0);
+    int size = kWave;
+    while (size < n) size <<= 1;
+    key = bitonic_merge_steps<32>(key, lane, size == kWave || (tid & kWave) == 0);
+    for (int k = 2 * kWave; k <= size; k <<= 1) {
+        const bool desc = k == size || (tid & k) == 0;
+        for (int j = k >> 1; j >= kWave; j >>= 1) {
+            __syncthreads();
+            sh.list[tid] = key;
+            __syncthreads();
+            const uint64_t other = sh.list[tid ^ j];
+            const bool keep_max = ((tid & j) == 0) == desc;
+            key = ((key > other) == keep_max) ? key : other;
+        }
+        key = bitonic_merge_steps<32>(key, lane, desc);
+    }
+    __syncthreads();
+    return key;
+}
+
+static __device__ __forceinline__ Listed make_list(Shared &sh, const Weights &w, int n, int tid) {
+    Listed l;
+    l.n = n;
+    l.key = sort_list(sh, n, tid);
+    l.w = tid < n ? weight_of(w, key_logit(l.key)) : 0.0;
+    double total;
+    l.below = scan_mass(sh, l.w, tid, total);
+    return l;
+}
+
+// Gathers the tokens of bins [b0, b1] whose value keys lie in [k0, k1] (at most kCap, known from
+// the histogram). The float bounds drop nearly all others first.
+static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange &ur, Shared &sh,
+                                         const Weights &w, int b0, int b1, uint32_t k0, uint32_t k1,
+                                         int tid) {
+    // x of the bins' ends, a step outwards: y < b1 + 1 and y >= b0 up to roundings far below it
+    const double lo = (double)w.m - (double)(b1 + 1) / w.c * (1.0 + 0x1p-20);
+    const double hi = (double)w.m - (double)b0 / w.c * (1.0 - 0x1p-20);
+    const float slack_lo = (float)(lo - fabs(lo) * 0x1p-20), slack_hi = (float)(hi + fabs(hi) * 0x1p-20);
+    const float xlo = w.c > 0.0 ? slack_lo : -FLT_MAX, xhi = w.c > 0.0 ? slack_hi : FLT_MAX;
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
+    each(logits, ur, tid, [&](float x, int32_t id) {
+        if (x >= xlo && x <= xhi) {
+            const double y = weight_y(w, x);
+            const uint32_t vk = value_key(x);
+            if (y < (double)kBins && (int)y >= b0 && (int)y <= b1 && vk >= k0 && vk <= k1) {
+                const uint32_t at = atomicAdd(&sh.listed, 1u);
+                if (at < kCap) sh.list[at] = cand_key(x, id);
+            }
+        }
+    });
+    __syncthreads();
+    const int n = min((int)sh.listed, kCap);
+    __syncthreads();
+    return make_list(sh, w, n, tid);
+}
+
+// ---- cuts -------------------------------------------------------------------------------------
+
+// The histogram's bins of this thread: masses and counts, and what lies before them.
+struct Bins {
+    double mass[kPer];
+    uint32_t count[kPer];
+    double below;
+    uint32_t before;
+    double total;
+    uint32_t number;
+};
+
+// Takes a histogram over bins out of LDS (their factor 2^(-b/64) for level 0; `scale` otherwise).
+static __device__ __forceinline__ Bins take_bins(Shared &sh, const Weights &w, bool by_bin, double scale,
+                                          double below, uint32_t before, int tid) {
+    Bins h;
+    double sum = 0.0;
+    uint32_t number = 0;
+    const double unit = 1.0 / w.one;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int b = tid * kPer + j;
+        h.count[j] = sh.count[b];
+        h.mass[j] = (double)sh.mass[b] * unit * (by_bin ? bin_scale(w, b) : scale);
+        sum += h.mass[j];
+        number += h.count[j];
+    }
+    h.below = below + scan_mass(sh, sum, tid, h.total);
+    h.before = before + scan_count(sh, number, tid, h.number);
+    h.total += below;
+    h.number += before;
+    return h;
+}
+
+// The bin that holds a cut: the result is in sh.spot_*. Roundings may leave a mass cut behind the
+// last bin: it is then the last that holds anything.
+static __device__ __forceinline__ void find_bin(Shared &sh, const Bins &h, Cut cut, double target,
+                                         uint32_t nth, int tid) {
+    double run = h.below, spot_mass = 0.0;
+    uint32_t num = h.before, spot_count = 0, spot_size = 0;
+    int bin = -1;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const double next = run + h.mass[j];
+        const uint32_t nnum = num + h.count[j];
+        const bool in = h.count[j] > 0 && bin < 0 &&
+                        (cut == kNumber ? nnum >= nth : cut == kReach ? next >= target : next > target);
+        if (in) {
+            bin = tid * kPer + j;
+            spot_mass = run;
+            spot_count = num;
+            spot_size = h.count[j];
+        }
+        run = next;
+        num = nnum;
+    }
+    int first = first_thread(sh, bin >= 0, tid);
+    if (first == kThreads) {  // the last bin with a token
+        run = h.below;
+        num = h.before;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (h.count[j] > 0) {
+                bin = tid * kPer + j;
+                spot_mass = run;
+                spot_count = num;
+                spot_size = h.count[j];
+            }
+            run += h.mass[j];
+            num += h.count[j];
+        }
+        const uint64_t b = __ballot(bin >= 0);
+        const int lane = tid & (kWave - 1), wave = tid / kWave;
+        if (lane == 0) sh.wave_first[wave] = b ? wave * kWave + 63 - __builtin_clzll(b) : -1;
+        __syncthreads();
+        first = -1;
+        for (int i = 0; i < kWaves; ++i) first = max(first, sh.wave_first[i]);
+        __syncthreads();
+    }
+    if (tid == first) {
+        sh.spot_bin = bin;
+        sh.spot_mass = spot_mass;
+        sh.spot_count = spot_count;
+        sh.spot_size = spot_size;
+    }
+    __syncthreads();
+}
+
+// The cut inside a sorted list whose first token has `below` mass and `before` tokens before it.
+static __device__ __forceinline__ Place cut_list(Shared &sh, const Listed &l, Cut cut, double target,
+                                          uint32_t nth, double below, uint32_t before, int tid) {
+    const double s = below + l.below + l.w;
+    const bool in = tid < l.n && (cut == kNumber ? before + tid + 1 >= nth
+                                  : cut == kReach ? s >= target
+                                                  : s > target);
+    int at = first_thread(sh, in, tid);
+    if (at >= l.n) at = l.n - 1;
+    if (tid == at) {
+        sh.spot_mass = s;
+        sh.list[0] = l.key;
+    }
+    __syncthreads();
+    Place p;
+    p.mass = sh.spot_mass;
+    const uint64_t key = sh.list[0];
+    __syncthreads();
+    p.id = key_id(key);
+    p.value = key_logit(key);
+    p.nth = 0;
+    p.w = 0.0;
+    return p;
+}
+
+// The cut inside bin `bin` of the row (size tokens, `below` mass and `before` tokens before it).
+static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange &ur, Shared &sh,
+                                      const Weights &w, int bin, uint32_t size, Cut cut,
+                                      double target, uint32_t nth, double below, uint32_t before,
+                                      int tid) {
+    uint32_t k0 = 0u, k1 = 0xFFFFFFFFu;
+    if (size > kCap) {  // the range of the bin's values
+        if (tid == 0) {
+            sh.key_lo = 0xFFFFFFFFu;
+            sh.key_hi = 0u;
+        }
+        __syncthreads();
+        uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+        each(logits, ur, tid, [&](float x, int32_t) {
+            const double y = weight_y(w, x);
+            if (y < (double)kBins && (int)y == bin) {
+                const uint32_t vk = value_key(x);
+                lo = min(lo, vk);
+                hi = max(hi, vk);
+            }
+        });
+        if (lo <= hi) {
+            atomicMin(&sh.key_lo, lo);
+            atomicMax(&sh.key_hi, hi);
+        }
+        __syncthreads();
+        k0 = sh.key_lo;
+        k1 = sh.key_hi;
+        __syncthreads();
+    }
+    // Split by value until a part is small or a single value; every step narrows the range to a
+    // 4096th of it or to one value.
+    while (size > kCap && k0 != k1) {
+        const int bits = 32 - __clz(k1 - k0);
+        const int shift = bits > 12 ? bits - 12 : 0;
+        for (int b = tid; b < kBins; b += kThreads) {
+            sh.mass[b] = 0ull;
+            sh.count[b] = 0u;
+        }
+        __syncthreads();
+        each(logits, ur, tid, [&](float x, int32_t) {
+            const double y = weight_y(w, x);
+            const uint32_t vk = value_key(x);
+            if (y < (double)kBins && (int)y == bin && vk >= k0 && vk <= k1) {
+                const uint32_t part = (k1 - vk) >> shift;
+                atomicAdd((unsigned long long *)&sh.mass[part],
+                          (unsigned long long)fixed_fraction(w, y - (double)bin));
+                atomicAdd(&sh.count[part], 1u);
+            }
+        });
+        __syncthreads();
+        const Bins h = take_bins(sh, w, false, bin_scale(w, bin), below, before, tid);
+        find_bin(sh, h, cut, target, nth, tid);
+        const uint32_t part = (uint32_t)sh.spot_bin;
+        below = sh.spot_mass;
+        before = sh.spot_count;
+        size = sh.spot_size;
+        __syncthreads();
+        k1 -= part << shift;
+        const uint32_t width = (1u << shift) - 1u;
+        k0 = k1 - k0 > width ? k1 - width : k0;
+    }
+    if (size > kCap) {
+        const float value = key_value(k1);
+        return cut_equal(value, weight_of(w, value), size, cut, target, nth, below, before);
+    }
+    const Listed l = gather(logits, ur, sh, w, bin, bin, k0, k1, tid);
+    Place p = cut_list(sh, l, cut, target, nth, below, before, tid);
+    p.w = weight_of(w, p.value);
+    return p;
+}
+
+// One row: its token and log-probability, written by thread 0.
+static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur, Shared &sh,
+                                           const RowSettings &st, double one, int tid,
+                                           int32_t *token, float *logprob) {
+    const int top_k = st.top_k;
+    const float top_p = st.top_p, min_p = st.min_p, temperature = st.temperature;
+    const double u = st.u;
+    auto answer = [&](int32_t id, double lp) {
+        if (tid == 0) {
+            *token = id;
+            if (logprob) *logprob = (float)lp;
+        }
+    };
+    if (tid < 64) sh.scale[tid] = exp2((double)tid * (-1.0 / 64.0));
+    const Top top = row_top(logits, ur, sh, tid);
+    if (top.m == -INFINITY) {  // nothing to draw
+        answer(-1, -INFINITY);
+        return;
+    }
+    if (!(temperature > 0.f)) {
+        answer(first_of_top(logits, ur, top, sh, tid), 0.0);
+        return;
+    }
+    if (top.m == INFINITY) {  // only the infinite logits have weight, all the same
+        uint32_t n;
+        nth_equal(logits, ur, sh, tid, INFINITY, 0u, n);
+        if (top_k >= 1 && (uint32_t)top_k < n) n = (uint32_t)top_k;
+        double whole = (double)n;
+        if (top_p < 1.f)
+            whole = cut_equal(INFINITY, 1.0, n, kReach, (double)top_p * whole, 0u, 0.0, 0u).mass;
+        const Place p = cut_equal(INFINITY, 1.0, n, kPass, u * whole, 0u, 0.0, 0u);
+        answer(nth_equal(logits, ur, sh, tid, INFINITY, p.nth, n), -log(whole));
+        return;
+    }
+
+    const Weights w{top.m, kBinsPerE / (double)temperature, one, sh.scale};
+    for (int b = tid; b < kBins; b += kThreads) {
+        sh.mass[b] = 0ull;
+        sh.count[b] = 0u;
+    }
+    __syncthreads();
+    each(logits, ur, tid, [&](float x, int32_t) {
+        const double y = weight_y(w, x);
+        if (y < (double)kBins) {  // (false for NaN and -inf)
+            const int b = (int)y;
+            atomicAdd((unsigned long long *)&sh.mass[b],
+                      (unsigned long long)fixed_fraction(w, y - (double)b));
+            atomicAdd(&sh.count[b], 1u);
+        }
+    });
+    __syncthreads();
+    const Bins h = take_bins(sh, w, true, 1.0, 0.0, 0u, tid);
+
+    // The lowest bin that the cuts can reach. (A top-k beyond the counted tokens cuts only among
+    // weights below 2^-64.)
+    const bool by_number = top_k >= 1 && (uint32_t)top_k < h.number;
+    const bool by_mass = top_p < 1.f;
+    const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;
+    const bool by_weight = least > 0x1p-60;
+    const int weight_bin = by_weight ? min((int)(-64.0 * log2(least)) + 1, kBins - 1) : kBins - 1;
+    int low = by_weight ? weight_bin : kBins - 1;
+    if (by_number) {
+        find_bin(sh, h, kNumber, 0.0, (uint32_t)top_k, tid);
+        // (top-p needs the whole mass of the top-k tokens, whatever min-p leaves of them)
+        low = by_mass ? sh.spot_bin : min(low, sh.spot_bin);
+        __syncthreads();
+    } else if (by_mass) {
+        find_bin(sh, h, kReach, (double)top_p * h.total, 0u, tid);
+        low = min(low, sh.spot_bin);
+        __syncthreads();
+    }
+    // tokens in the bins up to `low`
+    uint32_t upto = 0;
+    {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (tid * kPer + j <= low) upto += h.count[j];
+        uint32_t total;
+        scan_count(sh, upto, tid, total);
+        upto = total;
+    }
+    if (upto <= kCap) {
+        const Listed l = gather(logits, ur, sh, w, 0, low, 0u, 0xFFFFFFFFu, tid);
+        double z = h.total;
+        if (by_number)
+            z = cut_list(sh, l, kNumber, 0.0, (uint32_t)top_k, 0.0, 0u, tid).mass;
+        double whole = z;
+        if (by_mass) {
+            const double target = (double)top_p * z;
+            // (the list may end before the nucleus does, at a min-p cut)
+            if (first_thread(sh, tid < l.n && l.below + l.w >= target, tid) < l.n)
+                whole = fmin(whole, cut_list(sh, l, kReach, target, 0u, 0.0, 0u, tid).mass);
+        }
+        if (by_weight) {
+            const int n = first_thread(sh, !(tid < l.n && l.w >= least), tid);
+            whole = fmin(whole, cut_list(sh, l, kNumber, 0.0, (uint32_t)max(n, 1), 0.0, 0u, tid).mass);
+        }
+        const Place p = cut_list(sh, l, kPass, u * whole, 0u, 0.0, 0u, tid);
+        answer(p.id, log(weight_of(w, p.value) / whole));
+        return;
+    }
+
+    // Cut by cut, each in its own bin; the draw is the last.
+    double z = h.total, whole = h.total;
+    if (by_weight) {
+        // all of the bins above those that the border can fall in, and what reaches it there
+        double part = 0.0;
+        each(logits, ur, tid, [&](float x, int32_t) {
+            const double y = weight_y(w, x);
+            if (y < (double)kBins && (int)y <= weight_bin && (int)y >= weight_bin - 2) {
+                const double v = weight_of(w, x);
+                if (v >= least) part += v;
+            }
+        });
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (tid * kPer + j < weight_bin - 2) part += h.mass[j];
+        double sum;
+        scan_mass(sh, part, tid, sum);
+        whole = fmin(whole, sum);
+    }
+    Place p;
+#pragma unroll 1
+    for (int step = by_number ? 0 : by_mass ? 1 : 2; step < 3; ++step) {
+        if (step == 1 && !by_mass) continue;
+        const Cut cut = step == 0 ? kNumber : step == 1 ? kReach : kPass;
+        const double target = step == 1 ? (double)top_p * z : u * whole;
+        find_bin(sh, h, cut, target, (uint32_t)top_k, tid);
+        const int bin = sh.spot_bin;
+        const double below = sh.spot_mass;
+        const uint32_t before = sh.spot_count, size = sh.spot_size;
+        __syncthreads();
+        p = cut_bin(logits, ur, sh, w, bin, size, cut, target, (uint32_t)top_k, below, before, tid);
+        if (step == 0) z = p.mass;
+        if (step < 2) whole = fmin(whole, p.mass);
+    }
+    int32_t id = p.id;
+    if (id < 0) {
+        uint32_t n;
+        id = nth_equal(logits, ur, sh, tid, p.value, p.nth, n);
+    }
+    answer(id, log(p.w / whole));
+}
+};
+
+}  // namespace dflash2

@@ -298,14 +298,18 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
  *                        where the token is -1).
  *   Weights and masses are held to 2^-40 of themselves; weights below 2^-64 of the row's largest
  *   count as 0.
- *   1 <= R <= DFLASH2_MAX_SAMPLE_ROWS, 1 <= V <= DFLASH2_MAX_V. No workspace.
+ *   1 <= R <= DFLASH2_MAX_SAMPLE_ROWS, 1 <= V <= DFLASH2_MAX_V.
+ * Workspace: dflash2_sample_workspace_bytes(R, V, dtype) bytes (may be 0), contents need not be
+ * initialised.
  * Errors: DFLASH2_ERR_INVALID_ARG (sizes, dtype, all_* out of range where its pointer is NULL, NULL
- * logits, uniforms or token_ids), DFLASH2_ERR_ALIGNMENT, DFLASH2_ERR_HIP.
+ * logits, uniforms or token_ids), DFLASH2_ERR_ALIGNMENT, DFLASH2_ERR_WORKSPACE, DFLASH2_ERR_HIP.
  */
+size_t dflash2_sample_workspace_bytes(int R, int V, int dtype);
 int dflash2_sample(const void *logits, int dtype, int R, int V, const float *temperature,
                    float all_temperature, const int32_t *top_k, int all_top_k, const float *top_p,
                    float all_top_p, const float *min_p, float all_min_p, const float *uniforms,
-                   int32_t *token_ids, float *logprob, void *stream);
+                   int32_t *token_ids, float *logprob, void *workspace, size_t workspace_bytes,
+                   void *stream);
 
 /*
  * dflash2_distill, dflash2_distill_backward, dflash2_distill_step - the loss that trains a drafter

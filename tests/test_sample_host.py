@@ -27,16 +27,27 @@ def d2():
     # a value for all rows is not looked at where a tensor takes its place
     (dict(t=MIS, t_all=NAN), EALIGN), (dict(p=MIS, p_all=NAN), EALIGN),
     (dict(m=MIS, m_all=NAN), EALIGN),
+    (dict(V=151936), EWS), (dict(V=151936, wsb=16), EWS), (dict(V=151936, ws=None, wsb=1 << 30), EWS),
+    (dict(V=151936, ws=MIS, wsb=1 << 30), EALIGN),
 ])
 def test_rejects(d2, kw, status):
     a = dict(logits=P, dt=BF16, R=4, V=100, t=None, t_all=1.0, k=None, k_all=0, p=None, p_all=1.0,
-             m=None, m_all=0.0, u=P, ids=P, lp=None)
+             m=None, m_all=0.0, u=P, ids=P, lp=None, ws=P, wsb=0)
     a.update(kw)
     assert d2.library().dflash2_sample(a["logits"], a["dt"], a["R"], a["V"], a["t"], a["t_all"],
                                        a["k"], a["k_all"], a["p"], a["p_all"], a["m"], a["m_all"],
-                                       a["u"], a["ids"], a["lp"], None) == status
+                                       a["u"], a["ids"], a["lp"], a["ws"], a["wsb"],
+                                       None) == status
 
 
 def test_binding_rejects_host_tensors(d2):
     with pytest.raises(ValueError):
         d2.sample(torch.zeros(2, 10), torch.zeros(2))
+
+
+def test_workspace_sizes(d2):
+    f = d2.library().dflash2_sample_workspace_bytes
+    assert f(4, 151936, BF16) > 0        # few rows: slices
+    assert f(1024, 151936, BF16) == 0
+    assert f(4, 151936, F32) == 0
+    assert f(0, 151936, BF16) == 0 and f(4, 0, BF16) == 0 and f(4, 100, 3) == 0
