@@ -309,13 +309,13 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
     if (small_n > 0) {
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        const UnitRange ur = unit_range(row, V, 1, Elem<uint16_t>::kPerVec);
-        S16::each(logits, ur, tid, [&](float x, int32_t id) {
-            if (fabsf(x) < 0x1p-20f) {
-                const uint32_t at = atomicAdd(&sh.listed, 1u);
-                if (at < kSmallCap) sh.list[at] = cand_key(x, id);
-            }
-        });
+        for (int part = 0; part < counts.parts(); ++part) {
+            if (counts.part(part, 0, false) + counts.part(part, 0, true) == 0) continue;
+            const UnitRange ur = unit_range(row * counts.parts() + part, V, counts.parts(),
+                                            Elem<uint16_t>::kPerVec);
+            S16::collect(logits, ur, sh, tid, kSmallCap,
+                         [](float x) { return fabsf(x) < 0x1p-20f; });
+        }
         __syncthreads();
         if (tid < kWave) {
             const uint64_t key = wave_sort_desc(lane < (int)small_n ? sh.list[lane] : 0ull, lane);
@@ -487,12 +487,17 @@ sample_settle_kernel(const uint16_t *__restrict__ logits, int V, int slices, dou
     const uint32_t *mine = words + (size_t)row * slices * kStride;
     uint32_t *sums = sh.words;  // [2][kStride]
     for (int i = tid; i < kStride / 4; i += kNT) {
+        u32x4 v[kMaxSlices];  // all in flight together
+#pragma unroll
+        for (int s = 0; s < kMaxSlices; ++s) {
+            v[s] = u32x4{0u, 0u, 0u, 0u};
+            if (s < slices) v[s] = reinterpret_cast<const u32x4 *>(mine + (size_t)s * kStride)[i];
+        }
         u32x4 lo = u32x4{0u, 0u, 0u, 0u}, hi = lo;
-#pragma unroll 8
-        for (int s = 0; s < slices; ++s) {
-            const u32x4 v = reinterpret_cast<const u32x4 *>(mine + (size_t)s * kStride)[i];
-            lo += v & 0xFFFFu;
-            hi += v >> 16;
+#pragma unroll
+        for (int s = 0; s < kMaxSlices; ++s) {
+            lo += v[s] & 0xFFFFu;
+            hi += v[s] >> 16;
         }
         reinterpret_cast<u32x4 *>(sums)[i] = lo;
         reinterpret_cast<u32x4 *>(sums + kStride)[i] = hi;

@@ -309,77 +309,128 @@ static __device__ __forceinline__ int32_t first_of_top(const T *logits, const Un
     return id;
 }
 
-// How many logits equal `value`, and the id of number `nth` (from 0, by id) among them, -1 if there
-// are not so many. Wave w takes the w-th run of the row's vectors.
-static __device__ __forceinline__ int32_t nth_equal(const T *logits, const UnitRange &ur, Shared &sh, int tid,
-                                          float value, uint32_t nth, uint32_t &total) {
+// Which elements of the kSweep vectors i + 64 u of a run that ends at `end` match, EV bits a vector;
+// all loads are in flight together.
+static constexpr int kSweep = 8;
+template <typename F>
+static __device__ __forceinline__ uint64_t sweep(const u32x4 *p, int i, int end, F &&match) {
+    u32x4 v[kSweep];
+#pragma unroll
+    for (int u = 0; u < kSweep; ++u) {
+        v[u] = u32x4{};
+        if (i + u * kWave < end) v[u] = p[i + u * kWave];
+    }
+    uint64_t bits = 0;
+#pragma unroll
+    for (int u = 0; u < kSweep; ++u) {
+        float x[EV];
+        Elem<T>::unpack(v[u], x);
+        uint32_t b = 0;
+#pragma unroll
+        for (int k = 0; k < EV; ++k) b |= match(x[k]) ? 1u << k : 0u;
+        if (i + u * kWave < end) bits |= (uint64_t)b << (u * EV);
+    }
+    return bits;
+}
+
+// How many logits of a unit equal `value`, and the id of number `nth` (from 0, by id) among them,
+// -1 if there are not so many. Wave w takes the w-th run of the unit's vectors.
+static __device__ __forceinline__ int32_t nth_equal(const T *logits, const UnitRange &ur, Shared &sh,
+                                                    int tid, float value, uint32_t nth,
+                                                    uint32_t &total) {
     const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
     const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
     const int lane = tid & (kWave - 1), wave = tid / kWave;
     const int v0 = (int)((int64_t)ur.nv * wave / kWaves);
     const int v1 = (int)((int64_t)ur.nv * (wave + 1) / kWaves);
-    auto matches = [&](int i) {  // which elements of vector i match
-        uint32_t bits = 0;
-        if (i < v1) {
-            float x[EV];
-            Elem<T>::unpack(p[i], x);
-#pragma unroll
-            for (int k = 0; k < EV; ++k) bits |= x[k] == value ? 1u << k : 0u;
-        }
-        return bits;
-    };
+    constexpr int kChunk = kSweep * kWave;
+    auto match = [&](float x) { return x == value; };
     uint32_t mine = 0;
-    for (int i = v0; i < v1; i += kWave) mine += __popc(matches(i + lane));
+    uint64_t bits = 0;
+    for (int i = v0; i < v1; i += kChunk) {
+        bits = sweep(p, i + lane, v1, match);
+        mine += __popcll(bits);
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
+    // the ragged ends: lanes of every wave look at one element each
+    const int nh = (int)(ur.h1 - ur.h0), nt = (int)(ur.t1 - ur.t0);
+    const int64_t e = ragged_element(ur, lane);
+    const uint64_t ends = __ballot(e >= 0 && match(Elem<T>::load(logits, e >= 0 ? e : ur.g0)));
+    const uint64_t head_mask = (1ull << nh) - 1ull;  // (fewer than 64 of them)
     if (lane == 0) sh.wave_count[wave] = mine;
     if (tid == 0) sh.token = -1;
     __syncthreads();
-    uint32_t head = 0, tail = 0;
-    for (int64_t e = ur.h0; e < ur.h1; ++e) head += Elem<T>::load(logits, e) == value;
-    for (int64_t e = ur.t0; e < ur.t1; ++e) tail += Elem<T>::load(logits, e) == value;
+    const uint32_t head = __popcll(ends & head_mask), tail = __popcll(ends & ~head_mask);
     uint32_t before = head, base = head;
     for (int w = 0; w < kWaves; ++w) {
         if (w == wave) base = before;
         before += sh.wave_count[w];
     }
     total = before + tail;
-    if (tid == 0 && (nth < head || (nth >= before && nth < total))) {
-        uint32_t left = nth < head ? nth : nth - before;
-        for (int64_t e = nth < head ? ur.h0 : ur.t0;; ++e)
-            if (Elem<T>::load(logits, e) == value && left-- == 0) {
-                sh.token = (int32_t)(e - ur.g0);
-                break;
-            }
+    if (tid == 0 && nt + nh > 0 && (nth < head || (nth >= before && nth < total))) {
+        uint64_t b = nth < head ? ends & head_mask : ends & ~head_mask;
+        for (uint32_t left = nth < head ? nth : nth - before; left > 0; --left) b &= b - 1;
+        sh.token = (int32_t)(ragged_element(ur, __builtin_ctzll(b)) - ur.g0);
     }
     if (nth >= base && nth < base + mine) {  // this wave's run holds it
         uint32_t left = nth - base;
-        for (int i = v0; i < v1; i += kWave) {
-            const uint32_t bits = matches(i + lane);
-            uint32_t s = __popc(bits);
-            const uint32_t own = s;
+        bool found = false;
+        for (int i = v0; i < v1 && !found; i += kChunk) {
+            if (v1 - v0 > kChunk) bits = sweep(p, i + lane, v1, match);
+            for (int u = 0; u < kSweep; ++u) {
+                const uint32_t b = (uint32_t)(bits >> (u * EV)) & ((1u << EV) - 1u);
+                if (__ballot(b != 0u) == 0ull) continue;
+                const uint32_t own = __popc(b);
+                uint32_t s = own;
 #pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) {
-                const uint32_t t = __shfl_up(s, o);
-                if (lane >= o) s += t;
-            }
-            const uint32_t all = __shfl(s, kWave - 1);
-            if (left < all) {
-                uint32_t k = left - (s - own);
-                if (left >= s - own && left < s) {
-                    uint32_t b = bits;
-                    while (k-- > 0) b &= b - 1;
-                    sh.token = id0 + (i + lane) * EV + (__ffs(b) - 1);
+                for (int o = 1; o < kWave; o <<= 1) {
+                    const uint32_t t = __shfl_up(s, o);
+                    if (lane >= o) s += t;
                 }
+                const uint32_t all = __shfl(s, kWave - 1);
+                if (left >= all) {
+                    left -= all;
+                    continue;
+                }
+                if (left >= s - own && left < s) {
+                    uint32_t c = b;
+                    for (uint32_t k = left - (s - own); k > 0; --k) c &= c - 1;
+                    sh.token = id0 + (i + u * kWave + lane) * EV + (__ffs(c) - 1);
+                }
+                found = true;
                 break;
             }
-            left -= all;
         }
     }
     __syncthreads();
     const int32_t id = sh.token;
     __syncthreads();
     return id;
+}
+
+// Appends the keys of a unit's matching logits to sh.list (sh.listed counts them; what does not fit
+// in `cap` is dropped).
+template <typename F>
+static __device__ __forceinline__ void collect(const T *logits, const UnitRange &ur, Shared &sh,
+                                               int tid, uint32_t cap, F &&match) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    auto append = [&](int32_t id) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < cap) sh.list[at] = cand_key(Elem<T>::load(logits, ur.g0 + id), id);
+    };
+    for (int i = wave * kSweep * kWave + lane; i - lane < ur.nv; i += NT * kSweep) {
+        uint64_t bits = sweep(p, i, ur.nv, match);
+        while (bits) {
+            const int k = __builtin_ctzll(bits);
+            append(id0 + (i + k / EV * kWave) * EV + k % EV);
+            bits &= bits - 1;
+        }
+    }
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0 && match(Elem<T>::load(logits, e))) append((int32_t)(e - ur.g0));
 }
 
 // ---- the gathered list --------------------------------------------------------------------------

@@ -186,6 +186,42 @@ def test_masks(d2, dt):
         check(d2, x, [v] * 12, k=7, p=0.6)
 
 
+def test_values_outside_the_counted_range(d2):
+    """bf16 rows with values below 2^-20 (gathered, or too many) and from 2^8 on, in rows that are
+    counted whole and rows that are cut into slices."""
+    for V in (6001, 40010):
+        x, u = rows(10, V, "bf16", V)
+        g = torch.Generator().manual_seed(V)
+        tiny = (torch.randn(V, generator=g) * 2.0 ** -22).to(torch.bfloat16)
+        at = torch.randperm(V, generator=g)
+        x[0, at[:40]] = tiny[:40]                       # a few, between the others
+        x[1] = -x[1].abs() - 0.5
+        x[1, at[:30]] = tiny[:30]                       # they are the top
+        x[2] = -x[2].abs() - 0.5
+        x[2, at[:64]] = 0.0                             # as many as are gathered, all equal
+        x[3, at[:65]] = -0.0                            # one more
+        x[4] = tiny                                     # nothing else
+        x[5, at[:7]] = 300.0                            # large
+        x[6, at[:700]] = -300.0                         # large negative: no weight, or some
+        x[7] = -1000.0 - x[7].abs()
+        x[8] = -torch.inf
+        x[8, at[:3]] = tiny[:3]
+        x[9] = 5e-324
+        for i, s in enumerate(SETTINGS + [dict(T=100.0), dict(T=50.0, k=V // 2, p=0.9)]):
+            check(d2, x, [(v + 0.29 * i) % 1.0 for v in u], **s)
+
+
+@pytest.mark.parametrize("R,V", [(256, 300000), (1, 1200000)])
+def test_a_value_more_often_than_a_half_word_counts(d2, R, V):
+    """Constant rows: a part of the row holds one value more than 65535 times."""
+    x = torch.zeros(R, V, dtype=torch.bfloat16, device=DEV)
+    x[R - 1] = 1.5
+    u = (torch.arange(R, device=DEV) + 0.5) / R
+    ids, lp = d2.sample(x, u)
+    assert ids.tolist() == [int(v * V) for v in u.double().tolist()]
+    assert float((lp.double() + math.log(V)).abs().max()) <= 2.0 ** -37 + 2.0 ** -24 * math.log(V)
+
+
 def test_extreme_settings(d2):
     x, u = rows(6, 3001, "f32", 8)
     check(d2, x, u, T=[1e-45, 1e-30, 1e30, 3e38, 100.0, 0.001])
