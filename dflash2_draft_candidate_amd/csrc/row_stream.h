@@ -9,35 +9,55 @@ namespace dflash2 {
 
 constexpr int kStreamVectors = 4;  // 16-byte vectors per thread and batch
 
-// Runs over a thread's share of n vectors at p (tid, tid + nt, ...): batches of
-// kStreamVectors vectors with the next batch's loads in flight (batch(vectors, index of the
-// first); the others follow NT apart), then the rest one by one (single(vector, index)).
+// Runs over a thread's share of n vectors at p (tid, tid + NT, ...): batches of kStreamVectors
+// vectors (batch(vectors, index of the first); the others follow NT apart), then the rest one by
+// one (single(vector, index)). Two sets of registers take turns, so that the next batch is in
+// flight while one is worked on; no load is conditional (a wait at the join of two paths must assume
+// that the later loads are missing, and then waits for the ones in flight).
 template <int NT, typename FB, typename FV>
 __device__ __forceinline__ void stream(const u32x4 *p, int n, int tid, FB &&batch, FV &&single) {
-    const int whole = n / (NT * kStreamVectors);
-    u32x4 cur[kStreamVectors], nxt[kStreamVectors];
-    if (whole > 0) {
+    constexpr int kStep = NT * kStreamVectors;
+    const int whole = n / kStep;
+    u32x4 a[kStreamVectors], c[kStreamVectors];
+    auto load = [&](u32x4 *v, int b) {
 #pragma unroll
-        for (int u = 0; u < kStreamVectors; ++u) cur[u] = p[tid + u * NT];
+        for (int u = 0; u < kStreamVectors; ++u) v[u] = p[b * kStep + tid + u * NT];
+    };
+    const int base = whole * kStep + tid;
+    auto load_rest = [&](u32x4 *v) {
+#pragma unroll
+        for (int u = 0; u < kStreamVectors; ++u)
+            if (base + u * NT < n) v[u] = p[base + u * NT];
+    };
+    auto rest = [&](const u32x4 *v) {
+#pragma unroll
+        for (int u = 0; u < kStreamVectors; ++u)
+            if (base + u * NT < n) single(v[u], base + u * NT);
+    };
+    if (whole == 0) {
+        load_rest(a);
+        rest(a);
+        return;
     }
-    for (int b = 0; b < whole; ++b) {
-        const int base = (b + 1) * NT * kStreamVectors + tid;
-        if (b + 1 < whole) {
-#pragma unroll
-            for (int u = 0; u < kStreamVectors; ++u) nxt[u] = p[base + u * NT];
-        }
-        batch(cur, base - NT * kStreamVectors);
-#pragma unroll
-        for (int u = 0; u < kStreamVectors; ++u) cur[u] = nxt[u];
+    load(a, 0);
+    int b = 0;
+    for (; b + 2 < whole; b += 2) {
+        load(c, b + 1);
+        batch(a, b * kStep + tid);
+        load(a, b + 2);
+        batch(c, (b + 1) * kStep + tid);
     }
-    // the rest: at most kStreamVectors vectors per thread, loaded together
-    const int base = whole * NT * kStreamVectors + tid;
-#pragma unroll
-    for (int u = 0; u < kStreamVectors; ++u)
-        if (base + u * NT < n) cur[u] = p[base + u * NT];
-#pragma unroll
-    for (int u = 0; u < kStreamVectors; ++u)
-        if (base + u * NT < n) single(cur[u], base + u * NT);
+    if (b + 2 == whole) {
+        load(c, b + 1);
+        batch(a, b * kStep + tid);
+        load_rest(a);
+        batch(c, (b + 1) * kStep + tid);
+        rest(a);
+    } else {
+        load_rest(c);
+        batch(a, b * kStep + tid);
+        rest(c);
+    }
 }
 
 // Ragged element `tid` of a unit (its row's ends outside whole vectors): index, or -1.

@@ -92,20 +92,34 @@ __device__ __noinline__ void general_row(const uint16_t *logits, int64_t row, in
 
 // ---- counting ----------------------------------------------------------------------------------
 
-// Counts one logit: `mag` its pattern without the sign, `sign` 0 or 1.
-__device__ __forceinline__ void tally(uint32_t *words, uint32_t mag, uint32_t sign) {
-    const int at = min(max((int)mag - (kBase - 1), 0), kValues + 1);
-    __hip_atomic_fetch_add(words + at, sign * 65535u + 1u, __ATOMIC_RELAXED,
+// Counts two logits packed in a word: the words' indexes by packed 16-bit arithmetic (a saturating
+// subtraction and a minimum), the increments 1 or 2^16 as sign mask + 1.
+__device__ __forceinline__ void tally2(uint32_t *words, uint32_t pair) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+    const u16x2 low = {(uint16_t)(kBase - 1), (uint16_t)(kBase - 1)};
+    const u16x2 high = {(uint16_t)(kValues + 1), (uint16_t)(kValues + 1)};
+    const u16x2 mag = __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu);
+    const u16x2 at = __builtin_elementwise_min(__builtin_elementwise_sub_sat(mag, low), high);
+    const u16x2 sign = __builtin_bit_cast(u16x2, __builtin_bit_cast(i16x2, pair) >> 15);
+    __hip_atomic_fetch_add(words + at.x, (uint32_t)sign.x + 1u, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WORKGROUP);
+    __hip_atomic_fetch_add(words + at.y, (uint32_t)sign.y + 1u, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// Counts one logit.
+__device__ __forceinline__ void tally(uint32_t *words, uint32_t h) {
+    const int at = min(max((int)(h & 0x7FFFu) - (kBase - 1), 0), kValues + 1);
+    __hip_atomic_fetch_add(words + at, (h >> 15) * 65535u + 1u, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
 __device__ __forceinline__ void tally_vector(uint32_t *words, const u32x4 &v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        tally(words, w[i] & 0x7FFFu, (w[i] >> 15) & 1u);
-        tally(words, (w[i] >> 16) & 0x7FFFu, w[i] >> 31);
-    }
+    tally2(words, v.x);
+    tally2(words, v.y);
+    tally2(words, v.z);
+    tally2(words, v.w);
 }
 
 // Counts a part by NT threads.
@@ -120,10 +134,7 @@ __device__ __forceinline__ void count_part(const uint16_t *logits, const UnitRan
         },
         [&](const u32x4 &v, int) { tally_vector(words, v); });
     const int64_t e = ragged_element(ur, tid);
-    if (e >= 0) {
-        const uint32_t h = logits[e];
-        tally(words, h & 0x7FFFu, h >> 15);
-    }
+    if (e >= 0) tally(words, logits[e]);
 }
 
 // The value at place q of the candidate order: positive values from the largest down, then the
