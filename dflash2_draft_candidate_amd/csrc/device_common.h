@@ -199,6 +199,40 @@ __device__ __forceinline__ float wave_sum(float v) {
     return ((r0 + r1) + r2) + r3;
 }
 
+// Inclusive running sums over the wave's lanes: steps of 1, 2, 4 and 8 lanes within each row of 16 (a
+// lane without a source adds 0), then the last lane of each even row to the row after it, and lane 31
+// to the upper half. Lane 63 holds the sum.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xF, false);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = dpp_or_zero<kCtrl, kRows>((uint32_t)b);
+    const uint32_t hi = dpp_or_zero<kCtrl, kRows>((uint32_t)(b >> 32));
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <typename T>
+__device__ __forceinline__ T wave_running_sum(T v) {
+    v += dpp_or_zero<0x111, 0xF>(v);  // row_shr:1
+    v += dpp_or_zero<0x112, 0xF>(v);
+    v += dpp_or_zero<0x114, 0xF>(v);
+    v += dpp_or_zero<0x118, 0xF>(v);
+    v += dpp_or_zero<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    v += dpp_or_zero<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+// The value of one lane (the same for the whole wave), in every lane.
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint64_t lo = lane_value((uint32_t)b, lane), hi = lane_value((uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)((hi << 32) | lo));
+}
+
 // ---- logsumexp partial state ---------------------------------------------------------------
 // (ref, sum) stands for log2-domain reference `ref` and sum = sum_i 2^(x_i*log2e - ref):
 // logsumexp = (ref + log2(sum)) * ln 2. ref = -inf with sum = 0 is the empty state.

@@ -32,20 +32,21 @@
 namespace dflash2 {
 namespace {
 
-constexpr int kNT = 512;       // threads of the bf16 kernels
-constexpr int kNT32 = 1024;    // threads of the float32 kernel
+constexpr int kNT = 512;        // threads of the bf16 kernels: two workgroups share a CU, and two
+                                // waves share a SIMD where all waves do the same
+constexpr int kNT32 = 1024;     // threads of the float32 kernel
 constexpr int kParts = 4;      // parts of a row that a workgroup counts by itself
 constexpr int kBase = 0x3580;  // bf16 pattern of 2^-20
 constexpr int kValues = 3584;  // counted values of a sign: up to 2^8
 constexpr int kStride = 3588;  // words of a part: below, kValues, above, two unused
-constexpr int kPerThread = 2 * kValues / kNT;
+constexpr int kRows = 2 * kValues / kWave;  // places in rows of 64, one to a lane
 constexpr int kRowGroups = 256;
 constexpr int kMaxSlices = 16;
 constexpr int kSmallCap = 64;  // gathered values below 2^-20
 static_assert(kCountWords == kParts * kStride, "counts in LDS");
-static_assert(kPerThread * kNT == 2 * kValues && kValues % kPerThread == 0, "bins of a thread");
+static_assert(kRows <= 2 * kWave && kValues % kWave == 0, "rows of places: two to a lane");
 
-using S16 = RowSampler<uint16_t, kNT>;
+template <int NT> using S16 = RowSampler<uint16_t, NT>;
 using S32 = RowSampler<float, kNT32>;
 
 struct Settings {
@@ -83,11 +84,12 @@ __global__ __launch_bounds__(kNT32) void sample_f32_kernel(const float *__restri
 }
 
 // The general path of a bf16 row (a call: it must not weigh on the registers of the counting pass).
+template <int NT>
 __device__ __noinline__ void general_row(const uint16_t *logits, int64_t row, int V,
-                                         S16::Shared *sh, const RowSettings *st, double one,
+                                         typename S16<NT>::Shared *sh, const RowSettings *st, double one,
                                          int32_t *token, float *logprob) {
     const UnitRange ur = unit_range(row, V, 1, Elem<uint16_t>::kPerVec);
-    S16::run(logits, ur, *sh, *st, one, threadIdx.x, token, logprob);
+    S16<NT>::run(logits, ur, *sh, *st, one, threadIdx.x, token, logprob);
 }
 
 // ---- counting ----------------------------------------------------------------------------------
@@ -180,11 +182,16 @@ struct SlicedCounts {
 };
 
 // ---- a row from its counts -----------------------------------------------------------------------
+//
+// The 7168 places are kRows rows of 64, a place to a lane. The waves take the rows in turn for their
+// counts and masses; after that every wave holds all rows' running sums (lane l: rows 2l and
+// 2l + 1) and finds each cut by itself, first among the rows, then among the row's lanes: no
+// barriers, and the waves agree because they do the same.
 
-// What a thread knows of its places [tid kPerThread, + kPerThread).
-struct Run {
-    double mass, below;
-    uint32_t count, before;
+// Two rows per lane: masses and counts, and what lies before them.
+struct Rows {
+    double mass[2], below[2];
+    uint32_t count[2], before[2];
 };
 
 // The gathered small values (|x| < 2^-20), in candidate order.
@@ -203,25 +210,36 @@ struct Spot {
     int q;
 };
 
-template <typename Counts>
-__device__ __forceinline__ Spot find_spot(S16::Shared &sh, const Counts &counts, const Weights &w,
-                                          const Run &run, const Small &small, Cut cut,
-                                          double target, uint32_t nth, int tid) {
+template <int NT, typename Counts>
+__device__ __forceinline__ Spot find_spot(const typename S16<NT>::Shared &sh, const Counts &counts,
+                                          const Weights &w, const Rows &rows, const Small &small,
+                                          Cut cut, double target, uint32_t nth, int lane) {
     auto meets = [&](double mass, uint32_t number) {
         return cut == kNumber ? number >= nth : cut == kReach ? mass >= target : mass > target;
     };
-    const int first = S16::first_thread(
-        sh, run.count > 0 && meets(run.below + run.mass, run.before + run.count), tid);
+    uint64_t in[2], any[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        any[i] = __ballot(rows.count[i] > 0);
+        in[i] = any[i] & __ballot(meets(rows.below[i] + rows.mass[i], rows.before[i] + rows.count[i]));
+    }
+    int row;
+    if (in[0] | in[1]) {
+        const int l = __builtin_ctzll(in[0] | in[1]);
+        row = 2 * l + ((in[0] >> l) & 1 ? 0 : 1);
+    } else {
+        row = 2 * kRows;
+    }
     Spot s;
     s.small = -1;
-    if (small.n > 0 && first >= kNT / 2 &&
-        meets(small.below + small.mass, small.before + small.n)) {
-        s.small = 0;
+    if (small.n > 0 && row >= kRows / 2 &&
+        (meets(small.below + small.mass, small.before + (uint32_t)small.n) ||
+         (any[0] | any[1]) == 0ull)) {
         s.q = -1;
         s.below = small.below;
         s.before = small.before;
-        s.w = 0.0;
-        for (int i = 0; i < small.n; ++i) {  // few: every thread walks them
+        s.size = 1;
+        for (int i = 0; i < small.n; ++i) {  // few
             s.value = key_logit(sh.list[i]);
             s.w = weight_of(w, s.value);
             s.small = i;
@@ -229,89 +247,89 @@ __device__ __forceinline__ Spot find_spot(S16::Shared &sh, const Counts &counts,
             s.below += s.w;
             ++s.before;
         }
-        s.size = 1;
         return s;
     }
-    // Roundings may leave a mass cut behind everything: it falls on the last counted value then.
-    int owner = first;
-    if (first == kNT) {
-        const uint64_t b = __ballot(run.count > 0);
-        const int wave = tid / kWave;
-        if ((tid & (kWave - 1)) == 0)
-            sh.wave_first[wave] = b ? wave * kWave + 63 - __builtin_clzll(b) : 0;
-        __syncthreads();
-        owner = 0;
-        for (int i = 0; i < S16::kWaves; ++i) owner = max(owner, sh.wave_first[i]);
-        __syncthreads();
+    if (row >= kRows) {  // roundings left a mass cut behind everything: the last counted value
+        const int l = 63 - __builtin_clzll(any[0] | any[1]);
+        row = 2 * l + ((any[1] >> l) & 1 ? 1 : 0);
     }
-    if (tid == owner) {
-        sh.spot_mass = run.below;
-        sh.spot_count = run.before;
-    }
-    __syncthreads();
-    // every wave looks through the owner's places, one to a lane
-    const int lane = tid & (kWave - 1);
-    const int q = owner * kPerThread + min(lane, kPerThread - 1);
+    const int owner = row >> 1;
+    const double base = lane_value(row & 1 ? rows.below[1] : rows.below[0], owner);
+    const uint32_t start = lane_value(row & 1 ? rows.before[1] : rows.before[0], owner);
+    const int q = row * kWave + lane;
     const float value = place_value(q);
-    const double y = weight_y(w, value);
-    const bool counted = lane < kPerThread && value <= w.m && y < (double)kBins;
+    const bool counted = value <= w.m && weight_y(w, value) < (double)kBins;
     const uint32_t n = counted ? counts.count(place_word(q), q >= kValues) : 0u;
     const double wt = n > 0 ? weight_of(w, value) : 0.0;
-    double mass = wt * (double)n;
-    uint32_t number = n;
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-        const double a = __shfl_up(mass, o);
-        const uint32_t b = __shfl_up(number, o);
-        if (lane >= o) {
-            mass += a;
-            number += b;
-        }
-    }
-    const double base = sh.spot_mass;
-    const uint32_t start = sh.spot_count;
-    __syncthreads();
-    uint64_t in = __ballot(n > 0 && meets(base + mass, start + number));
-    const uint64_t any = __ballot(n > 0);
-    const int at = in ? __builtin_ctzll(in) : any ? 63 - __builtin_clzll(any) : 0;
-    const double upto = __shfl(mass, at > 0 ? at - 1 : 0);
-    const uint32_t upto_n = __shfl(number, at > 0 ? at - 1 : 0);
-    s.below = base + (at > 0 ? upto : 0.0);
-    s.before = start + (at > 0 ? upto_n : 0u);
-    s.value = __shfl(value, at);
-    s.w = __shfl(wt, at);
-    s.size = __shfl(n, at);
-    s.q = owner * kPerThread + at;
+    const double mass = wave_running_sum(wt * (double)n);
+    const uint32_t number = wave_running_sum(n);
+    const uint64_t here = __ballot(n > 0);
+    const uint64_t hit = here & __ballot(meets(base + mass, start + number));
+    const int at = hit ? __builtin_ctzll(hit) : here ? 63 - __builtin_clzll(here) : 0;
+    s.below = at > 0 ? base + lane_value(mass, at - 1) : base;
+    s.before = at > 0 ? start + lane_value(number, at - 1) : start;
+    s.value = __uint_as_float(lane_value(__float_as_uint(value), at));
+    s.w = lane_value(wt, at);
+    s.size = lane_value(n, at);
+    s.q = row * kWave + at;
     return s;
 }
-static_assert(kPerThread <= 16, "a scan over 16 lanes");
+
+// Scratch of settle.
+template <int NT>
+struct SettleShared {
+    uint32_t weighed[2 * kWave];  // tokens with weight, by row
+    double mass[2 * kWave];
+    double heavy[S16<NT>::kWaves];
+    uint32_t total[S16<NT>::kWaves];  // by wave: tokens counted, and the first row that holds any
+    int first[S16<NT>::kWaves];
+};
 
 // Settles a row from the counts of its parts. False (in every thread) if the row is one for the
 // general path; nothing is written then.
-template <typename Counts>
+template <int NT, typename Counts>
 __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int V,
-                                       const Counts &counts, S16::Shared &sh,
+                                       const Counts &counts, typename S16<NT>::Shared &sh, SettleShared<NT> &ss,
                                        const RowSettings &st, int tid, int32_t *token,
                                        float *logprob) {
-    const int lane = tid & (kWave - 1);
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    constexpr int kOwn = kRows / S16<NT>::kWaves;  // rows of a wave: wave, wave + kWaves, ...
+    static_assert(kOwn * S16<NT>::kWaves == kRows, "rows of a wave");
     if (tid < 64) sh.scale[tid] = exp2((double)tid * (-1.0 / 64.0));
-    // counts of this thread's places
-    const bool negative = tid >= kNT / 2;
-    uint32_t c[kPerThread];
-    uint32_t mine = 0;
-    int first_q = 2 * kValues;
+    // (the loops over rows are loops: run once per row of logits, their code comes from memory, and
+    // fourteen copies of it took longer to fetch than to run)
+    uint32_t c[kOwn], tokens = 0;
+    uint32_t held = 0;  // which of the wave's rows hold a token
 #pragma unroll
-    for (int j = kPerThread - 1; j >= 0; --j) {
-        const int q = tid * kPerThread + j;
-        c[j] = counts.count(place_word(q), negative);
-        mine += c[j];
-        if (c[j] > 0) first_q = q;
+    for (int j = 0; j < kOwn; ++j) {
+        const int r = wave + j * S16<NT>::kWaves;
+        c[j] = counts.count(place_word(r * kWave + lane), r >= kRows / 2);
+    }
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        tokens += c[j];
+        held |= __ballot(c[j] > 0) != 0ull ? 1u << j : 0u;
+    }
+    tokens = wave_running_sum(tokens);
+    if (lane == kWave - 1) {
+        ss.total[wave] = tokens;
+        ss.first[wave] = held ? wave + __builtin_ctz(held) * S16<NT>::kWaves : kRows;
+    }
+    if (tid < 2 * kWave) {
+        ss.weighed[tid] = 0u;
+        ss.mass[tid] = 0.0;
     }
     const uint32_t small_n = counts.count(0, false) + counts.count(0, true);
     const uint32_t large_pos = counts.count(kValues + 1, false);
     const uint32_t large_neg = counts.count(kValues + 1, true);
-    uint32_t total;
-    S16::scan_count(sh, mine, tid, total);
+    __syncthreads();
+    uint32_t total = 0;
+    int first = kRows;
+#pragma unroll
+    for (int i = 0; i < S16<NT>::kWaves; ++i) {
+        total += ss.total[i];
+        first = min(first, ss.first[i]);
+    }
     if (total + small_n + large_pos + large_neg != (uint32_t)V || large_pos > 0 ||
         small_n > kSmallCap || total + small_n == 0)
         return false;
@@ -324,7 +342,7 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
             if (counts.part(part, 0, false) + counts.part(part, 0, true) == 0) continue;
             const UnitRange ur = unit_range(row * counts.parts() + part, V, counts.parts(),
                                             Elem<uint16_t>::kPerVec);
-            S16::collect(logits, ur, sh, tid, kSmallCap,
+            S16<NT>::collect(logits, ur, sh, tid, kSmallCap,
                          [](float x) { return fabsf(x) < 0x1p-20f; });
         }
         __syncthreads();
@@ -334,12 +352,12 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
         }
         __syncthreads();
     }
-    // the maximum
-    const int owner = S16::first_thread(sh, mine > 0, tid);
-    if (tid == owner) sh.spot_bin = first_q;
-    __syncthreads();
-    const int top_q = owner == kNT ? 2 * kValues : sh.spot_bin;
-    __syncthreads();
+    // the maximum: the first place with a count, unless a small value comes before it
+    int top_q = 2 * kValues;
+    if (first < kRows) {
+        const uint32_t n = counts.count(place_word(first * kWave + lane), first >= kRows / 2);
+        top_q = first * kWave + __builtin_ctzll(__ballot(n > 0));
+    }
     const bool top_small = small_n > 0 && top_q >= kValues;
     const float m = top_small ? key_logit(sh.list[0]) : place_value(top_q);
 
@@ -347,25 +365,45 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
     uint32_t nth = 0;
     int32_t id = -1;
     int found_q = top_q;
-    double lp = 0.0;
+    double share = 1.0;
     if (st.temperature > 0.f) {
         const Weights w{m, kBinsPerE / (double)st.temperature, 1.0, sh.scale};
         if (large_neg > 0 && !(weight_y(w, -256.f) >= (double)kBins)) return false;
         const bool by_weight = st.min_p > 0.f;
         const double least = by_weight ? fmin((double)st.min_p, 1.0) : 0.0;
-        Run run{0.0, 0.0, 0u, 0u};
         double heavy = 0.0;  // mass of the weights that min_p keeps
+#pragma unroll 1
+        while (held) {  // two rows at a time: their chains of dependent steps overlap
+            int r[2];
+            r[0] = __builtin_ctz(held);
+            held &= held - 1;
+            r[1] = held ? __builtin_ctz(held) : -1;
+            held &= held - 1;
+            double mass[2];
+            uint32_t n[2];
 #pragma unroll
-        for (int j = 0; j < kPerThread; ++j) {
-            if (c[j] > 0) {
-                const float x = place_value(tid * kPerThread + j);
-                if (weight_y(w, x) < (double)kBins) {
-                    const double wt = weight_of(w, x);
-                    const double mass = wt * (double)c[j];
-                    run.mass += mass;
-                    run.count += c[j];
-                    if (wt >= least) heavy += mass;
-                }
+            for (int i = 0; i < 2; ++i) {
+                const bool on = r[i] >= 0;
+                r[i] = on ? wave + r[i] * S16<NT>::kWaves : 0;
+                const float x = place_value(r[i] * kWave + lane);
+                n[i] = counts.count(place_word(r[i] * kWave + lane), r[i] >= kRows / 2);
+                if (!on || !(weight_y(w, x) < (double)kBins)) n[i] = 0;
+                const double wt = n[i] > 0 ? weight_of(w, x) : 0.0;
+                mass[i] = wt * (double)n[i];
+                if (wt >= least) heavy += mass[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mass[i] = wave_running_sum(mass[i]);
+                n[i] = wave_running_sum(n[i]);
+            }
+            if (lane == kWave - 1) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (n[i] > 0) {
+                        ss.mass[r[i]] = mass[i];
+                        ss.weighed[r[i]] = n[i];
+                    }
             }
         }
         for (int i = 0; i < small.n; ++i) {
@@ -378,71 +416,87 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
             small.mass += wt;
             if (tid == 0 && wt >= least) heavy += wt;
         }
-        double z, whole_heavy = 0.0;
-        uint32_t number;
-        run.below = S16::scan_mass(sh, run.mass, tid, z);
-        run.before = S16::scan_count(sh, run.count, tid, number);
-        if (by_weight) S16::scan_mass(sh, heavy, tid, whole_heavy);
+        if (by_weight) {
+            heavy = wave_running_sum(heavy);
+            if (lane == kWave - 1) ss.heavy[wave] = heavy;
+        }
+        __syncthreads();
+        Rows rows;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rows.mass[i] = ss.mass[2 * lane + i];
+            rows.count[i] = ss.weighed[2 * lane + i];
+        }
+        const double upto = wave_running_sum(rows.mass[0] + rows.mass[1]);
+        const uint32_t upto_n = wave_running_sum(rows.count[0] + rows.count[1]);
+        rows.below[0] = dpp_or_zero<0x138, 0xF>(upto);  // wave_shr:1
+        rows.before[0] = upto_n - rows.count[0] - rows.count[1];
+        double z = lane_value(upto, kWave - 1);
+        uint32_t number = lane_value(upto_n, kWave - 1);
         if (small.n > 0) {  // between the positive and the negative values
-            if (tid == kNT / 2) {
-                sh.spot_mass = run.below;
-                sh.spot_count = run.before;
-            }
-            __syncthreads();
-            small.below = sh.spot_mass;
-            small.before = sh.spot_count;
-            __syncthreads();
-            if (negative) {
-                run.below += small.mass;
-                run.before += (uint32_t)small.n;
+            small.below = lane_value(upto, kRows / 4 - 1);
+            small.before = lane_value(upto_n, kRows / 4 - 1);
+            if (lane >= kRows / 4) {
+                rows.below[0] += small.mass;
+                rows.before[0] += (uint32_t)small.n;
             }
             z += small.mass;
             number += (uint32_t)small.n;
         }
-        auto cut_at = [&](const Spot &s, Cut cut, double target, uint32_t k) {
-            return cut_equal(s.value, s.w, s.size, cut, target, k, s.below, s.before);
-        };
+        rows.below[1] = rows.below[0] + rows.mass[0];
+        rows.before[1] = rows.before[0] + rows.count[0];
+        // top-k, top-p and the draw, in one loop: one copy of the search
         double whole = z;
-        if (st.top_k >= 1 && (uint32_t)st.top_k < number) {
-            const uint32_t k = (uint32_t)st.top_k;
-            const Spot s = find_spot(sh, counts, w, run, small, kNumber, 0.0, k, tid);
-            z = cut_at(s, kNumber, 0.0, k).mass;
-            whole = z;
+        Spot s;
+        uint32_t taken = 0;
+#pragma unroll 1
+        for (int step = 0; step < 3; ++step) {
+            Cut cut = kNumber;
+            double target = 0.0;
+            if (step == 0) {
+                if (st.top_k < 1 || (uint32_t)st.top_k >= number) continue;
+            } else if (step == 1) {
+                if (!(st.top_p < 1.f)) continue;
+                cut = kReach;
+                target = (double)st.top_p * z;
+            } else {
+                if (by_weight) {
+                    double sum = 0.0;
+                    for (int i = 0; i < S16<NT>::kWaves; ++i) sum += ss.heavy[i];
+                    whole = fmin(whole, sum);
+                }
+                cut = kPass;
+                target = st.u * whole;
+            }
+            s = find_spot<NT>(sh, counts, w, rows, small, cut, target, (uint32_t)st.top_k, lane);
+            const Place p = cut_equal(s.value, s.w, s.size, cut, target, (uint32_t)st.top_k, s.below,
+                                      s.before);
+            if (step == 0) z = p.mass;
+            if (step < 2) whole = fmin(whole, p.mass);
+            taken = p.nth;
         }
-        if (st.top_p < 1.f) {
-            const double target = (double)st.top_p * z;
-            const Spot s = find_spot(sh, counts, w, run, small, kReach, target, 0u, tid);
-            whole = fmin(whole, cut_at(s, kReach, target, 0u).mass);
-        }
-        if (by_weight) whole = fmin(whole, whole_heavy);
-        const double target = st.u * whole;
-        const Spot s = find_spot(sh, counts, w, run, small, kPass, target, 0u, tid);
-        const Place p = cut_at(s, kPass, target, 0u);
         value = s.value;
-        nth = p.nth;
+        nth = taken;
         found_q = s.q;
         if (s.small >= 0) id = key_id(sh.list[s.small]);
-        lp = log(s.w / whole);
+        share = s.w / whole;
     } else if (top_small) {
         id = key_id(sh.list[0]);
     }
     if (id < 0) {  // number nth of its equals: the part that holds it, then the logit itself
-        const uint32_t word = place_word(found_q);
-        int part = 0;
-        uint32_t left = nth;
-        for (; part < counts.parts() - 1; ++part) {
-            const uint32_t n = counts.part(part, word, found_q >= kValues);
-            if (left < n) break;
-            left -= n;
-        }
+        const uint32_t n =
+            lane < counts.parts() ? counts.part(lane, place_word(found_q), found_q >= kValues) : 0u;
+        const uint32_t upto = wave_running_sum(n);
+        const int part = __builtin_ctzll(__ballot(upto > nth));
+        const uint32_t left = nth - (lane_value(upto, part) - lane_value(n, part));
         const int64_t unit = row * counts.parts() + part;
         const UnitRange ur = unit_range(unit, V, counts.parts(), Elem<uint16_t>::kPerVec);
-        uint32_t n;
-        id = S16::nth_equal(logits, ur, sh, tid, value, left, n);
+        uint32_t equal;
+        id = S16<NT>::nth_equal(logits, ur, sh, tid, value, left, equal);
     }
     if (tid == 0) {
         *token = id;
-        if (logprob) *logprob = (float)lp;
+        if (logprob) *logprob = (float)log(share);
     }
     return true;
 }
@@ -451,7 +505,8 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void
 sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Settings st,
                    int32_t *__restrict__ tokens, float *__restrict__ logprob) {
-    __shared__ S16::Shared sh;
+    __shared__ S16<kNT>::Shared sh;
+    __shared__ SettleShared<kNT> ss;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     constexpr int kGroup = kNT / kParts;
@@ -465,9 +520,9 @@ sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Setti
     const RowSettings rs = row_settings(st, row);
     int32_t *token = tokens + row;
     float *lp = logprob ? logprob + row : nullptr;
-    if (!settle(logits, row, V, LocalCounts{sh.words}, sh, rs, tid, token, lp)) {
+    if (!settle<kNT>(logits, row, V, LocalCounts{sh.words}, sh, ss, rs, tid, token, lp)) {
         __syncthreads();
-        general_row(logits, row, V, &sh, &rs, one, token, lp);
+        general_row<kNT>(logits, row, V, &sh, &rs, one, token, lp);
     }
 }
 
@@ -492,7 +547,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void
 sample_settle_kernel(const uint16_t *__restrict__ logits, int V, int slices, double one,
                      Settings st, const uint32_t *__restrict__ words,
                      int32_t *__restrict__ tokens, float *__restrict__ logprob) {
-    __shared__ S16::Shared sh;
+    __shared__ S16<kNT>::Shared sh;
+    __shared__ SettleShared<kNT> ss;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const uint32_t *mine = words + (size_t)row * slices * kStride;
@@ -517,9 +573,9 @@ sample_settle_kernel(const uint16_t *__restrict__ logits, int V, int slices, dou
     const RowSettings rs = row_settings(st, row);
     int32_t *token = tokens + row;
     float *lp = logprob ? logprob + row : nullptr;
-    if (!settle(logits, row, V, SlicedCounts{mine, sums, slices}, sh, rs, tid, token, lp)) {
+    if (!settle<kNT>(logits, row, V, SlicedCounts{mine, sums, slices}, sh, ss, rs, tid, token, lp)) {
         __syncthreads();
-        general_row(logits, row, V, &sh, &rs, one, token, lp);
+        general_row<kNT>(logits, row, V, &sh, &rs, one, token, lp);
     }
 }
 

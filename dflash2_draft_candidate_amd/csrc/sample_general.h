@@ -150,12 +150,7 @@ struct Shared {
 // least that of thread t plus its v up to one rounding.
 static __device__ __forceinline__ double scan_mass(Shared &sh, double v, int tid, double &total) {
     const int lane = tid & (kWave - 1), wave = tid / kWave;
-    double s = v;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const double t = __shfl_up(s, o);
-        if (lane >= o) s += t;
-    }
+    const double s = wave_running_sum(v);
     if (lane == kWave - 1) sh.wave_mass[wave] = s;
     __syncthreads();
     double base = 0.0, all = 0.0;
@@ -172,12 +167,7 @@ static __device__ __forceinline__ double scan_mass(Shared &sh, double v, int tid
 
 static __device__ __forceinline__ uint32_t scan_count(Shared &sh, uint32_t v, int tid, uint32_t &total) {
     const int lane = tid & (kWave - 1), wave = tid / kWave;
-    uint32_t s = v;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t t = __shfl_up(s, o);
-        if (lane >= o) s += t;
-    }
+    const uint32_t s = wave_running_sum(v);
     if (lane == kWave - 1) sh.wave_count[wave] = s;
     __syncthreads();
     uint32_t base = 0, all = 0;
@@ -309,54 +299,46 @@ static __device__ __forceinline__ int32_t first_of_top(const T *logits, const Un
     return id;
 }
 
-// Which elements of the kSweep vectors i + 64 u of a run that ends at `end` match, EV bits a vector;
-// all loads are in flight together.
-static constexpr int kSweep = 8;
-template <typename F>
-static __device__ __forceinline__ uint64_t sweep(const u32x4 *p, int i, int end, F &&match) {
-    u32x4 v[kSweep];
-#pragma unroll
-    for (int u = 0; u < kSweep; ++u) {
-        v[u] = u32x4{};
-        if (i + u * kWave < end) v[u] = p[i + u * kWave];
-    }
-    uint64_t bits = 0;
-#pragma unroll
-    for (int u = 0; u < kSweep; ++u) {
-        float x[EV];
-        Elem<T>::unpack(v[u], x);
-        uint32_t b = 0;
-#pragma unroll
-        for (int k = 0; k < EV; ++k) b |= match(x[k]) ? 1u << k : 0u;
-        if (i + u * kWave < end) bits |= (uint64_t)b << (u * EV);
-    }
-    return bits;
-}
-
 // How many logits of a unit equal `value`, and the id of number `nth` (from 0, by id) among them,
-// -1 if there are not so many. Wave w takes the w-th run of the unit's vectors.
+// -1 if there are not so many. Wave w takes the w-th run of the unit's vectors, kSweep vectors a lane
+// in flight. A comparison leaves a mask of lanes in a scalar register, and the scalar unit
+// counts its bits: the vector units see two instructions an element (they are what bounds this
+// otherwise: every wave of the workgroup runs here).
+static constexpr int kSweep = 8;
 static __device__ __forceinline__ int32_t nth_equal(const T *logits, const UnitRange &ur, Shared &sh,
                                                     int tid, float value, uint32_t nth,
                                                     uint32_t &total) {
     const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
     const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
-    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    const int lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int v0 = (int)((int64_t)ur.nv * wave / kWaves);
     const int v1 = (int)((int64_t)ur.nv * (wave + 1) / kWaves);
-    constexpr int kChunk = kSweep * kWave;
-    auto match = [&](float x) { return x == value; };
-    uint32_t mine = 0;
-    uint64_t bits = 0;
-    for (int i = v0; i < v1; i += kChunk) {
-        bits = sweep(p, i + lane, v1, match);
-        mine += __popcll(bits);
-    }
+    // matches among the 64 vectors at i (those below v1): of all lanes
+    auto count = [&](const u32x4 &v, int i) {
+        float x[EV];
+        Elem<T>::unpack(v, x);
+        const uint64_t on = v1 - i >= kWave ? ~0ull : (1ull << (v1 - i)) - 1ull;
+        uint32_t n = 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
+        for (int k = 0; k < EV; ++k) n += __builtin_popcountll(__ballot(x[k] == value) & on);
+        return n;
+    };
+    auto at = [&](int i) { return p[min(i + lane, v1 - 1)]; };
+    uint32_t mine = 0;
+    for (int i = v0; i < v1; i += kSweep * kWave) {
+        u32x4 v[kSweep];
+#pragma unroll
+        for (int u = 0; u < kSweep; ++u)
+            if (i + u * kWave < v1) v[u] = at(i + u * kWave);
+#pragma unroll
+        for (int u = 0; u < kSweep; ++u)
+            if (i + u * kWave < v1) mine += count(v[u], i + u * kWave);
+    }
     // the ragged ends: lanes of every wave look at one element each
-    const int nh = (int)(ur.h1 - ur.h0), nt = (int)(ur.t1 - ur.t0);
+    const int nh = (int)(ur.h1 - ur.h0);
     const int64_t e = ragged_element(ur, lane);
-    const uint64_t ends = __ballot(e >= 0 && match(Elem<T>::load(logits, e >= 0 ? e : ur.g0)));
+    const uint64_t ends = __ballot(e >= 0 && Elem<T>::load(logits, e >= 0 ? e : ur.g0) == value);
     const uint64_t head_mask = (1ull << nh) - 1ull;  // (fewer than 64 of them)
     if (lane == 0) sh.wave_count[wave] = mine;
     if (tid == 0) sh.token = -1;
@@ -368,39 +350,33 @@ static __device__ __forceinline__ int32_t nth_equal(const T *logits, const UnitR
         before += sh.wave_count[w];
     }
     total = before + tail;
-    if (tid == 0 && nt + nh > 0 && (nth < head || (nth >= before && nth < total))) {
+    if (tid == 0 && (nth < head || (nth >= before && nth < total))) {
         uint64_t b = nth < head ? ends & head_mask : ends & ~head_mask;
         for (uint32_t left = nth < head ? nth : nth - before; left > 0; --left) b &= b - 1;
         sh.token = (int32_t)(ragged_element(ur, __builtin_ctzll(b)) - ur.g0);
     }
-    if (nth >= base && nth < base + mine) {  // this wave's run holds it
+    if (nth >= base && nth < base + mine) {  // this wave's run holds it: once more, in order
         uint32_t left = nth - base;
-        bool found = false;
-        for (int i = v0; i < v1 && !found; i += kChunk) {
-            if (v1 - v0 > kChunk) bits = sweep(p, i + lane, v1, match);
-            for (int u = 0; u < kSweep; ++u) {
-                const uint32_t b = (uint32_t)(bits >> (u * EV)) & ((1u << EV) - 1u);
-                if (__ballot(b != 0u) == 0ull) continue;
-                const uint32_t own = __popc(b);
-                uint32_t s = own;
-#pragma unroll
-                for (int o = 1; o < kWave; o <<= 1) {
-                    const uint32_t t = __shfl_up(s, o);
-                    if (lane >= o) s += t;
-                }
-                const uint32_t all = __shfl(s, kWave - 1);
-                if (left >= all) {
-                    left -= all;
-                    continue;
-                }
-                if (left >= s - own && left < s) {
-                    uint32_t c = b;
-                    for (uint32_t k = left - (s - own); k > 0; --k) c &= c - 1;
-                    sh.token = id0 + (i + u * kWave + lane) * EV + (__ffs(c) - 1);
-                }
-                found = true;
-                break;
+        for (int i = v0; i < v1; i += kWave) {
+            const u32x4 v = at(i);
+            const uint32_t all = count(v, i);
+            if (left >= all) {
+                left -= all;
+                continue;
             }
+            float x[EV];
+            Elem<T>::unpack(v, x);
+            uint32_t bits = 0;
+#pragma unroll
+            for (int k = 0; k < EV; ++k) bits |= x[k] == value ? 1u << k : 0u;
+            if (i + lane >= v1) bits = 0;
+            const uint32_t own = __popc(bits);
+            const uint32_t s = wave_running_sum(own);
+            if (left >= s - own && left < s) {
+                for (uint32_t k = left - (s - own); k > 0; --k) bits &= bits - 1;
+                sh.token = id0 + (i + lane) * EV + (__ffs(bits) - 1);
+            }
+            break;
         }
     }
     __syncthreads();
@@ -416,21 +392,28 @@ static __device__ __forceinline__ void collect(const T *logits, const UnitRange 
                                                int tid, uint32_t cap, F &&match) {
     const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
     const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
-    const int lane = tid & (kWave - 1), wave = tid / kWave;
-    auto append = [&](int32_t id) {
+    auto append = [&](float x, int32_t id) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
-        if (at < cap) sh.list[at] = cand_key(Elem<T>::load(logits, ur.g0 + id), id);
+        if (at < cap) sh.list[at] = cand_key(x, id);
     };
-    for (int i = wave * kSweep * kWave + lane; i - lane < ur.nv; i += NT * kSweep) {
-        uint64_t bits = sweep(p, i, ur.nv, match);
-        while (bits) {
-            const int k = __builtin_ctzll(bits);
-            append(id0 + (i + k / EV * kWave) * EV + k % EV);
-            bits &= bits - 1;
+    for (int i = tid; i < ur.nv; i += kSweep * NT) {
+        u32x4 v[kSweep];
+#pragma unroll
+        for (int u = 0; u < kSweep; ++u)
+            if (i + u * NT < ur.nv) v[u] = p[i + u * NT];
+#pragma unroll
+        for (int u = 0; u < kSweep; ++u) {
+            if (i + u * NT >= ur.nv) continue;
+            float x[EV];
+            Elem<T>::unpack(v[u], x);
+#pragma unroll
+            for (int k = 0; k < EV; ++k)
+                if (match(x[k])) append(x[k], id0 + (i + u * NT) * EV + k);
         }
     }
     const int64_t e = ragged_element(ur, tid);
-    if (e >= 0 && match(Elem<T>::load(logits, e))) append((int32_t)(e - ur.g0));
+    if (e >= 0 && match(Elem<T>::load(logits, e)))
+        append(Elem<T>::load(logits, e), (int32_t)(e - ur.g0));
 }
 
 // ---- the gathered list --------------------------------------------------------------------------
