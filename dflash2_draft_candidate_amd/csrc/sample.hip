@@ -42,6 +42,8 @@ constexpr int kStride = 3588;  // words of a part: below, kValues, above, two un
 constexpr int kRows = 2 * kValues / kWave;  // places in rows of 64, one to a lane
 constexpr int kRowGroups = 256;
 constexpr int kMaxSlices = 16;
+constexpr int kMaxTops = 2048;  // groups of a row whose maxima are kept
+constexpr uint32_t kListed = 256;  // equal logits of a part that are listed
 constexpr int kSmallCap = 64;  // gathered values below 2^-20
 static_assert(kCountWords == kParts * kStride, "counts in LDS");
 static_assert(kRows <= 2 * kWave && kValues % kWave == 0, "rows of places: two to a lane");
@@ -94,20 +96,28 @@ __device__ __noinline__ void general_row(const uint16_t *logits, int64_t row, in
 
 // ---- counting ----------------------------------------------------------------------------------
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+
 // Counts two logits packed in a word: the words' indexes by packed 16-bit arithmetic (a saturating
-// subtraction and a minimum), the increments 1 or 2^16 as sign mask + 1.
-__device__ __forceinline__ void tally2(uint32_t *words, uint32_t pair) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+// subtraction and a minimum), the increments 1 or 2^16 as sign mask + 1. Returns the pair as integers
+// in the order of the logits (negative ones with their magnitude inverted).
+__device__ __forceinline__ i16x2 tally2(uint32_t *words, uint32_t pair) {
     const u16x2 low = {(uint16_t)(kBase - 1), (uint16_t)(kBase - 1)};
     const u16x2 high = {(uint16_t)(kValues + 1), (uint16_t)(kValues + 1)};
     const u16x2 mag = __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu);
     const u16x2 at = __builtin_elementwise_min(__builtin_elementwise_sub_sat(mag, low), high);
-    const u16x2 sign = __builtin_bit_cast(u16x2, __builtin_bit_cast(i16x2, pair) >> 15);
+    const uint32_t mask = __builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2, pair) >> 15);
+    const u16x2 sign = __builtin_bit_cast(u16x2, mask);
     __hip_atomic_fetch_add(words + at.x, (uint32_t)sign.x + 1u, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_WORKGROUP);
     __hip_atomic_fetch_add(words + at.y, (uint32_t)sign.y + 1u, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_WORKGROUP);
+    return __builtin_bit_cast(i16x2, pair ^ (mask & 0x7FFF7FFFu));
+}
+__device__ __forceinline__ int order_key(float value) {  // of a bf16 value, as tally2 returns it
+    const int h = (int)(__float_as_uint(value)) >> 16;
+    return h ^ ((h >> 15) & 0x7FFF);
 }
 
 // Counts one logit.
@@ -117,24 +127,50 @@ __device__ __forceinline__ void tally(uint32_t *words, uint32_t h) {
                            __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
-__device__ __forceinline__ void tally_vector(uint32_t *words, const u32x4 &v) {
-    tally2(words, v.x);
-    tally2(words, v.y);
-    tally2(words, v.z);
-    tally2(words, v.w);
+__device__ __forceinline__ i16x2 tally_vector(uint32_t *words, const u32x4 &v) {
+    const i16x2 a = __builtin_elementwise_max(tally2(words, v.x), tally2(words, v.y));
+    const i16x2 b = __builtin_elementwise_max(tally2(words, v.z), tally2(words, v.w));
+    return __builtin_elementwise_max(a, b);
 }
 
-// Counts a part by NT threads.
+// A group is what eight neighbouring threads load in one batch of the stream (256 logits); the rest
+// of the part, less than a batch, makes a last row of groups. The largest logit of each group tells
+// later where a value can be found. kGroupLanes lanes' maximum, in each of them:
+constexpr int kGroupLanes = 8;
+__device__ __forceinline__ int group_max(i16x2 m) {
+    int v = max((int)m.x, (int)m.y);
+    v = max(v, __builtin_amdgcn_mov_dpp(v, kDppQuadXor1, 0xF, 0xF, true));
+    v = max(v, __builtin_amdgcn_mov_dpp(v, kDppQuadXor2, 0xF, 0xF, true));
+    return max(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));  // row_half_mirror
+}
+
+// Counts a part by NT threads; the groups' maxima go to `tops` unless that is null.
 template <int NT>
 __device__ __forceinline__ void count_part(const uint16_t *logits, const UnitRange &ur,
-                                           uint32_t *words, int tid) {
+                                           uint32_t *words, int16_t *tops, int tid) {
+    constexpr int kStep = NT * kStreamVectors, kPerBatch = NT / kGroupLanes;
+    const int slot = tid / kGroupLanes;
+    const bool first = (tid & (kGroupLanes - 1)) == 0;
+    i16x2 rest = {-32768, -32768};
     stream<NT>(
         reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
-        [&](const u32x4 *v, int) {
+        [&](const u32x4 *v, int i) {
+            i16x2 m = tally_vector(words, v[0]);
 #pragma unroll
-            for (int u = 0; u < kStreamVectors; ++u) tally_vector(words, v[u]);
+            for (int u = 1; u < kStreamVectors; ++u)
+                m = __builtin_elementwise_max(m, tally_vector(words, v[u]));
+            if (tops) {
+                const int top = group_max(m);
+                if (first) tops[i / kStep * kPerBatch + slot] = (int16_t)top;
+            }
         },
-        [&](const u32x4 &v, int) { tally_vector(words, v); });
+        [&](const u32x4 &v, int) {
+            rest = __builtin_elementwise_max(rest, tally_vector(words, v));
+        });
+    if (tops) {
+        const int top = group_max(rest);
+        if (first) tops[ur.nv / kStep * kPerBatch + slot] = (int16_t)top;
+    }
     const int64_t e = ragged_element(ur, tid);
     if (e >= 0) tally(words, logits[e]);
 }
@@ -154,7 +190,12 @@ __device__ __forceinline__ uint32_t half(uint32_t word, bool negative) {
 
 // Where the counts of a row's parts are: in this workgroup's LDS, ...
 struct LocalCounts {
+    static constexpr int kPartThreads = kNT / kParts;
     const uint32_t *words;  // [kParts][kStride]
+    const int16_t *maxima;  // of the parts' groups, `stride` apart; null: not kept
+    int stride;
+    __device__ __forceinline__ bool has_tops() const { return maxima != nullptr; }
+    __device__ __forceinline__ const int16_t *tops(int p) const { return maxima + p * stride; }
     __device__ __forceinline__ int parts() const { return kParts; }
     __device__ __forceinline__ uint32_t part(int p, uint32_t word, bool negative) const {
         return half(words[p * kStride + word], negative);
@@ -169,9 +210,12 @@ struct LocalCounts {
 
 // ... or in the workspace, with their sums in LDS (positive, then negative).
 struct SlicedCounts {
+    static constexpr int kPartThreads = kNT;
     const uint32_t *words;  // [slices][kStride]
     const uint32_t *sums;   // [2][kStride]
     int slices;
+    __device__ __forceinline__ bool has_tops() const { return false; }
+    __device__ __forceinline__ const int16_t *tops(int) const { return nullptr; }
     __device__ __forceinline__ int parts() const { return slices; }
     __device__ __forceinline__ uint32_t part(int p, uint32_t word, bool negative) const {
         return half(words[(size_t)p * kStride + word], negative);
@@ -184,9 +228,10 @@ struct SlicedCounts {
 // ---- a row from its counts -----------------------------------------------------------------------
 //
 // The 7168 places are kRows rows of 64, a place to a lane. The waves take the rows in turn for their
-// counts and masses; after that every wave holds all rows' running sums (lane l: rows 2l and
-// 2l + 1) and finds each cut by itself, first among the rows, then among the row's lanes: no
-// barriers, and the waves agree because they do the same.
+// counts and masses; after that one wave holds all rows' running sums (lane l: rows 2l and 2l + 1)
+// and finds each cut by itself, first among the rows, then among the row's lanes: no barriers. (When
+// all waves did the same, to save handing the result on, that cost the many-rows pass a third of its
+// time: it is a long chain of fp64 instructions, and a SIMD issues one in four cycles.)
 
 // Two rows per lane: masses and counts, and what lies before them.
 struct Rows {
@@ -283,6 +328,14 @@ struct SettleShared {
     double heavy[S16<NT>::kWaves];
     uint32_t total[S16<NT>::kWaves];  // by wave: tokens counted, and the first row that holds any
     int first[S16<NT>::kWaves];
+    // what is drawn: a value and how many of its equals come before, or a token
+    float value;
+    uint32_t nth;
+    int q;
+    int32_t id;
+    double share;
+    uint32_t hits;  // groups to look through for it
+    uint16_t hit[kMaxTops];
 };
 
 // Settles a row from the counts of its parts. False (in every thread) if the row is one for the
@@ -361,15 +414,10 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
     const bool top_small = small_n > 0 && top_q >= kValues;
     const float m = top_small ? key_logit(sh.list[0]) : place_value(top_q);
 
-    float value = m;
-    uint32_t nth = 0;
-    int32_t id = -1;
-    int found_q = top_q;
-    double share = 1.0;
     if (st.temperature > 0.f) {
         const Weights w{m, kBinsPerE / (double)st.temperature, 1.0, sh.scale};
         if (large_neg > 0 && !(weight_y(w, -256.f) >= (double)kBins)) return false;
-        const bool by_weight = st.min_p > 0.f;
+        const bool by_number = st.top_k >= 1, by_weight = st.min_p > 0.f;
         const double least = by_weight ? fmin((double)st.min_p, 1.0) : 0.0;
         double heavy = 0.0;  // mass of the weights that min_p keeps
 #pragma unroll 1
@@ -395,7 +443,8 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 mass[i] = wave_running_sum(mass[i]);
-                n[i] = wave_running_sum(n[i]);
+                // (how many they are matters to top-k only; otherwise whether there are any)
+                n[i] = by_number ? wave_running_sum(n[i]) : (uint32_t)(__ballot(n[i] > 0) != 0ull);
             }
             if (lane == kWave - 1) {
 #pragma unroll
@@ -421,82 +470,141 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
             if (lane == kWave - 1) ss.heavy[wave] = heavy;
         }
         __syncthreads();
-        Rows rows;
+        if (wave == 0) {
+            Rows rows;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            rows.mass[i] = ss.mass[2 * lane + i];
-            rows.count[i] = ss.weighed[2 * lane + i];
-        }
-        const double upto = wave_running_sum(rows.mass[0] + rows.mass[1]);
-        const uint32_t upto_n = wave_running_sum(rows.count[0] + rows.count[1]);
-        rows.below[0] = dpp_or_zero<0x138, 0xF>(upto);  // wave_shr:1
-        rows.before[0] = upto_n - rows.count[0] - rows.count[1];
-        double z = lane_value(upto, kWave - 1);
-        uint32_t number = lane_value(upto_n, kWave - 1);
-        if (small.n > 0) {  // between the positive and the negative values
-            small.below = lane_value(upto, kRows / 4 - 1);
-            small.before = lane_value(upto_n, kRows / 4 - 1);
-            if (lane >= kRows / 4) {
-                rows.below[0] += small.mass;
-                rows.before[0] += (uint32_t)small.n;
+            for (int i = 0; i < 2; ++i) {
+                rows.mass[i] = ss.mass[2 * lane + i];
+                rows.count[i] = ss.weighed[2 * lane + i];
             }
-            z += small.mass;
-            number += (uint32_t)small.n;
-        }
-        rows.below[1] = rows.below[0] + rows.mass[0];
-        rows.before[1] = rows.before[0] + rows.count[0];
-        // top-k, top-p and the draw, in one loop: one copy of the search
-        double whole = z;
-        Spot s;
-        uint32_t taken = 0;
-#pragma unroll 1
-        for (int step = 0; step < 3; ++step) {
-            Cut cut = kNumber;
-            double target = 0.0;
-            if (step == 0) {
-                if (st.top_k < 1 || (uint32_t)st.top_k >= number) continue;
-            } else if (step == 1) {
-                if (!(st.top_p < 1.f)) continue;
-                cut = kReach;
-                target = (double)st.top_p * z;
-            } else {
-                if (by_weight) {
-                    double sum = 0.0;
-                    for (int i = 0; i < S16<NT>::kWaves; ++i) sum += ss.heavy[i];
-                    whole = fmin(whole, sum);
+            const double upto = wave_running_sum(rows.mass[0] + rows.mass[1]);
+            const uint32_t upto_n = wave_running_sum(rows.count[0] + rows.count[1]);
+            rows.below[0] = dpp_or_zero<0x138, 0xF>(upto);  // wave_shr:1
+            rows.before[0] = upto_n - rows.count[0] - rows.count[1];
+            double z = lane_value(upto, kWave - 1);
+            uint32_t number = lane_value(upto_n, kWave - 1);
+            if (small.n > 0) {  // between the positive and the negative values
+                small.below = lane_value(upto, kRows / 4 - 1);
+                small.before = lane_value(upto_n, kRows / 4 - 1);
+                if (lane >= kRows / 4) {
+                    rows.below[0] += small.mass;
+                    rows.before[0] += (uint32_t)small.n;
                 }
-                cut = kPass;
-                target = st.u * whole;
+                z += small.mass;
+                number += (uint32_t)small.n;
             }
-            s = find_spot<NT>(sh, counts, w, rows, small, cut, target, (uint32_t)st.top_k, lane);
-            const Place p = cut_equal(s.value, s.w, s.size, cut, target, (uint32_t)st.top_k, s.below,
-                                      s.before);
-            if (step == 0) z = p.mass;
-            if (step < 2) whole = fmin(whole, p.mass);
-            taken = p.nth;
+            rows.below[1] = rows.below[0] + rows.mass[0];
+            rows.before[1] = rows.before[0] + rows.count[0];
+            // top-k, top-p and the draw, in one loop: one copy of the search
+            double whole = z;
+            Spot s;
+            uint32_t taken = 0;
+#pragma unroll 1
+            for (int step = 0; step < 3; ++step) {
+                Cut cut = kNumber;
+                double target = 0.0;
+                if (step == 0) {
+                    if (!by_number || (uint32_t)st.top_k >= number) continue;
+                } else if (step == 1) {
+                    if (!(st.top_p < 1.f)) continue;
+                    cut = kReach;
+                    target = (double)st.top_p * z;
+                } else {
+                    if (by_weight) {
+                        double sum = 0.0;
+                        for (int i = 0; i < S16<NT>::kWaves; ++i) sum += ss.heavy[i];
+                        whole = fmin(whole, sum);
+                    }
+                    cut = kPass;
+                    target = st.u * whole;
+                }
+                s = find_spot<NT>(sh, counts, w, rows, small, cut, target, (uint32_t)st.top_k, lane);
+                const Place p = cut_equal(s.value, s.w, s.size, cut, target, (uint32_t)st.top_k, s.below,
+                                          s.before);
+                if (step == 0) z = p.mass;
+                if (step < 2) whole = fmin(whole, p.mass);
+                taken = p.nth;
+            }
+            if (lane == 0) {
+                ss.value = s.value;
+                ss.nth = taken;
+                ss.q = s.q;
+                ss.id = s.small >= 0 ? key_id(sh.list[s.small]) : -1;
+                ss.share = s.w / whole;
+                ss.hits = 0;
+                sh.listed = 0;
+            }
         }
-        value = s.value;
-        nth = taken;
-        found_q = s.q;
-        if (s.small >= 0) id = key_id(sh.list[s.small]);
-        share = s.w / whole;
-    } else if (top_small) {
-        id = key_id(sh.list[0]);
+    } else if (tid == 0) {
+        ss.value = m;
+        ss.nth = 0;
+        ss.q = top_q;
+        ss.id = top_small ? key_id(sh.list[0]) : -1;
+        ss.share = 1.0;
+        ss.hits = 0;
+        sh.listed = 0;
     }
-    if (id < 0) {  // number nth of its equals: the part that holds it, then the logit itself
-        const uint32_t n =
-            lane < counts.parts() ? counts.part(lane, place_word(found_q), found_q >= kValues) : 0u;
-        const uint32_t upto = wave_running_sum(n);
-        const int part = __builtin_ctzll(__ballot(upto > nth));
-        const uint32_t left = nth - (lane_value(upto, part) - lane_value(n, part));
-        const int64_t unit = row * counts.parts() + part;
-        const UnitRange ur = unit_range(unit, V, counts.parts(), Elem<uint16_t>::kPerVec);
-        uint32_t equal;
-        id = S16<NT>::nth_equal(logits, ur, sh, tid, value, left, equal);
+    __syncthreads();
+    if (tid == 0 && logprob) *logprob = (float)log(ss.share);
+    if (ss.id >= 0) {
+        if (tid == 0) *token = ss.id;
+        return true;
     }
-    if (tid == 0) {
-        *token = id;
-        if (logprob) *logprob = (float)log(share);
+    // number nth of its equals: the part that holds it, then the logit itself
+    const float value = ss.value;
+    const uint32_t nth = ss.nth;
+    const int q = ss.q;
+    const uint32_t n = lane < counts.parts() ? counts.part(lane, place_word(q), q >= kValues) : 0u;
+    const uint32_t upto = wave_running_sum(n);
+    const int part = __builtin_ctzll(__ballot(upto > nth));
+    const uint32_t equal = lane_value(n, part);
+    const uint32_t left = nth - (lane_value(upto, part) - equal);
+    const UnitRange ur =
+        unit_range(row * counts.parts() + part, V, counts.parts(), Elem<uint16_t>::kPerVec);
+    if (!counts.has_tops() || equal > kListed) {
+        uint32_t found;
+        const int32_t id = S16<NT>::nth_equal(logits, ur, sh, tid, value, left, found);
+        if (tid == 0) *token = id;
+        return true;
+    }
+    // Only groups whose maximum reaches the value can hold it: near the top, few of them.
+    constexpr int kPart = Counts::kPartThreads;
+    constexpr int kStep = kPart * kStreamVectors, kPerBatch = kPart / kGroupLanes;
+    const int key = order_key(value);
+    const int16_t *tops = counts.tops(part);
+    const int groups = (ur.nv / kStep + 1) * kPerBatch;
+    for (int g = tid; g < groups; g += NT)
+        if (tops[g] >= key) ss.hit[atomicAdd(&ss.hits, 1u)] = (uint16_t)g;
+    const int32_t id0 = (int32_t)(ur.c0 * Elem<uint16_t>::kPerVec - ur.g0);
+    const uint32_t pattern = __float_as_uint(value) >> 16;
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0 && logits[e] == pattern) sh.list[atomicAdd(&sh.listed, 1u)] = (uint32_t)(e - ur.g0);
+    __syncthreads();
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    for (int h = tid / kGroupLanes; h < (int)ss.hits; h += NT / kGroupLanes) {
+        const int g = ss.hit[h];
+        const int i = g / kPerBatch * kStep + g % kPerBatch * kGroupLanes + (tid & (kGroupLanes - 1));
+        u32x4 v[kStreamVectors];
+#pragma unroll
+        for (int u = 0; u < kStreamVectors; ++u) {
+            v[u] = u32x4{};  // (zeros match nothing: small values are not looked for here)
+            if (i + u * kPart < ur.nv) v[u] = p[i + u * kPart];
+        }
+#pragma unroll
+        for (int u = 0; u < kStreamVectors; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (((w[k / 2] >> (16 * (k & 1))) & 0xFFFFu) == pattern)
+                    sh.list[atomicAdd(&sh.listed, 1u)] = (uint32_t)(id0 + (i + u * kPart) * 8 + k);
+        }
+    }
+    __syncthreads();
+    if (tid < (int)equal) {  // all `equal` of them are listed: number `left` by id
+        const uint32_t id = (uint32_t)sh.list[tid];
+        uint32_t before = 0;
+        for (uint32_t i = 0; i < equal; ++i) before += (uint32_t)sh.list[i] < id ? 1u : 0u;
+        if (before == left) *token = (int32_t)id;
     }
     return true;
 }
@@ -507,6 +615,7 @@ sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Setti
                    int32_t *__restrict__ tokens, float *__restrict__ logprob) {
     __shared__ S16<kNT>::Shared sh;
     __shared__ SettleShared<kNT> ss;
+    __shared__ int16_t maxima[kMaxTops];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     constexpr int kGroup = kNT / kParts;
@@ -515,12 +624,16 @@ sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Setti
     u32x4 *clear = reinterpret_cast<u32x4 *>(sh.words);
     for (int i = tid; i < kCountWords / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    count_part<kGroup>(logits, ur, sh.words + part * kStride, tid & (kGroup - 1));
+    // (the longest part has at most V / 8 / kParts + 1 vectors)
+    const int stride = (V / 8 / kParts / (kGroup * kStreamVectors) + 2) * (kGroup / kGroupLanes);
+    const bool keep = kParts * stride <= kMaxTops;
+    count_part<kGroup>(logits, ur, sh.words + part * kStride, keep ? maxima + part * stride : nullptr,
+                       tid & (kGroup - 1));
     __syncthreads();
     const RowSettings rs = row_settings(st, row);
     int32_t *token = tokens + row;
     float *lp = logprob ? logprob + row : nullptr;
-    if (!settle<kNT>(logits, row, V, LocalCounts{sh.words}, sh, ss, rs, tid, token, lp)) {
+    if (!settle<kNT>(logits, row, V, LocalCounts{sh.words, keep ? maxima : nullptr, stride}, sh, ss, rs, tid, token, lp)) {
         __syncthreads();
         general_row<kNT>(logits, row, V, &sh, &rs, one, token, lp);
     }
@@ -536,7 +649,7 @@ sample_count_kernel(const uint16_t *__restrict__ logits, int V, int slices,
     u32x4 *clear = reinterpret_cast<u32x4 *>(sh);
     for (int i = tid; i < kStride / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    count_part<kNT>(logits, ur, sh, tid);
+    count_part<kNT>(logits, ur, sh, nullptr, tid);
     __syncthreads();
     u32x4 *out = reinterpret_cast<u32x4 *>(words + (size_t)blockIdx.x * kStride);
     for (int i = tid; i < kStride / 4; i += kNT) out[i] = clear[i];
