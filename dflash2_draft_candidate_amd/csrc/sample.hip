@@ -18,13 +18,13 @@
 //     in its low half, negative ones in its high half. A word below takes what is smaller, one
 //     above what is larger. The row is counted in parts (words of their own), so that a half-word
 //     is enough; a part's overflow shows as a wrong total.
-//   * Smaller values are rare (one in 10^7 of a normal row): up to 64 of them are gathered and take
+//   * Smaller values are rare (one in 10^6 of a normal row): up to 64 of them are listed and take
 //     their place between the positive and the negative values. Larger negative ones are masks,
 //     or so far below the maximum that they have no weight. Anything else (large or infinite
 //     logits, many tiny or zero ones, a row of masks) sends the row to the general path.
 //   * The token is then the n-th logit of a value, and the parts' counts say in which part: only
 //     that part is read a second time.
-// Rows that are many (kRowGroups and more) have a workgroup each, with four parts; few rows are cut
+// Rows that are many (kRowGroups and more) have a workgroup each, with two parts; few rows are cut
 // into slices, a part and a workgroup each, whose counts go through the workspace to a second kernel.
 #include "kernels.h"
 #include "sample_general.h"
@@ -34,18 +34,18 @@ namespace {
 
 constexpr int kNT = 512;        // threads of the bf16 kernels: two workgroups share a CU, and two
                                 // waves share a SIMD where all waves do the same
+constexpr int kParts = 2;       // parts of a row that a workgroup counts by itself
 constexpr int kNT32 = 1024;     // threads of the float32 kernel
-constexpr int kParts = 4;      // parts of a row that a workgroup counts by itself
 constexpr int kBase = 0x3580;  // bf16 pattern of 2^-20
 constexpr int kValues = 3584;  // counted values of a sign: up to 2^8
 constexpr int kStride = 3588;  // words of a part: below, kValues, above, two unused
 constexpr int kRows = 2 * kValues / kWave;  // places in rows of 64, one to a lane
 constexpr int kRowGroups = 256;
 constexpr int kMaxSlices = 16;
-constexpr int kMaxTops = 2048;  // groups of a row whose maxima are kept
+constexpr int kMaxTops = 1280;  // groups of a row whose maxima are kept
 constexpr uint32_t kListed = 256;  // equal logits of a part that are listed
 constexpr int kSmallCap = 64;  // gathered values below 2^-20
-static_assert(kCountWords == kParts * kStride, "counts in LDS");
+static_assert(kCountWords == 2 * kStride, "counts in LDS");
 static_assert(kRows <= 2 * kWave && kValues % kWave == 0, "rows of places: two to a lane");
 
 template <int NT> using S16 = RowSampler<uint16_t, NT>;
@@ -85,13 +85,13 @@ __global__ __launch_bounds__(kNT32) void sample_f32_kernel(const float *__restri
              logprob ? logprob + row : nullptr);
 }
 
-// The general path of a bf16 row (a call: it must not weigh on the registers of the counting pass).
+// The general path of a bf16 row.
 template <int NT>
-__device__ __noinline__ void general_row(const uint16_t *logits, int64_t row, int V,
-                                         typename S16<NT>::Shared *sh, const RowSettings *st, double one,
-                                         int32_t *token, float *logprob) {
+__device__ __forceinline__ void general_row(const uint16_t *logits, int64_t row, int V,
+                                            typename S16<NT>::Shared &sh, const RowSettings &st,
+                                            double one, int32_t *token, float *logprob) {
     const UnitRange ur = unit_range(row, V, 1, Elem<uint16_t>::kPerVec);
-    S16<NT>::run(logits, ur, *sh, *st, one, threadIdx.x, token, logprob);
+    S16<NT>::run(logits, ur, sh, st, one, threadIdx.x, token, logprob);
 }
 
 // ---- counting ----------------------------------------------------------------------------------
@@ -101,12 +101,14 @@ typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 
 // Counts two logits packed in a word: the words' indexes by packed 16-bit arithmetic (a saturating
 // subtraction and a minimum), the increments 1 or 2^16 as sign mask + 1. Returns the pair as integers
-// in the order of the logits (negative ones with their magnitude inverted).
-__device__ __forceinline__ i16x2 tally2(uint32_t *words, uint32_t pair) {
+// in the order of the logits (negative ones with their magnitude inverted); `lowest` becomes 0 in a
+// half that met a small value.
+__device__ __forceinline__ i16x2 tally2(uint32_t *words, uint32_t pair, u16x2 &lowest) {
     const u16x2 low = {(uint16_t)(kBase - 1), (uint16_t)(kBase - 1)};
     const u16x2 high = {(uint16_t)(kValues + 1), (uint16_t)(kValues + 1)};
     const u16x2 mag = __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu);
     const u16x2 at = __builtin_elementwise_min(__builtin_elementwise_sub_sat(mag, low), high);
+    lowest = __builtin_elementwise_min(lowest, at);
     const uint32_t mask = __builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2, pair) >> 15);
     const u16x2 sign = __builtin_bit_cast(u16x2, mask);
     __hip_atomic_fetch_add(words + at.x, (uint32_t)sign.x + 1u, __ATOMIC_RELAXED,
@@ -127,9 +129,9 @@ __device__ __forceinline__ void tally(uint32_t *words, uint32_t h) {
                            __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
-__device__ __forceinline__ i16x2 tally_vector(uint32_t *words, const u32x4 &v) {
-    const i16x2 a = __builtin_elementwise_max(tally2(words, v.x), tally2(words, v.y));
-    const i16x2 b = __builtin_elementwise_max(tally2(words, v.z), tally2(words, v.w));
+__device__ __forceinline__ i16x2 tally_vector(uint32_t *words, const u32x4 &v, u16x2 &lowest) {
+    const i16x2 a = __builtin_elementwise_max(tally2(words, v.x, lowest), tally2(words, v.y, lowest));
+    const i16x2 b = __builtin_elementwise_max(tally2(words, v.z, lowest), tally2(words, v.w, lowest));
     return __builtin_elementwise_max(a, b);
 }
 
@@ -144,35 +146,69 @@ __device__ __forceinline__ int group_max(i16x2 m) {
     return max(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));  // row_half_mirror
 }
 
-// Counts a part by NT threads; the groups' maxima go to `tops` unless that is null.
+// What a workgroup keeps of its stream beside the counts (null pointers: nothing).
+struct Notes {
+    int16_t *tops;         // maxima of the part's groups
+    uint64_t *small_keys;  // the row's values below 2^-20: candidate keys, at most kSmallCap
+    uint32_t *small_n;     // how many there were
+};
+
+__device__ __forceinline__ void note_small(const Notes &notes, uint32_t h, int64_t id) {
+    if ((h & 0x7FFFu) >= kBase) return;
+    const uint32_t at = atomicAdd(notes.small_n, 1u);
+    if (at < kSmallCap) notes.small_keys[at] = cand_key(__uint_as_float(h << 16), (int32_t)id);
+}
+__device__ __forceinline__ void note_small(const Notes &notes, const u32x4 &v, int64_t id) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) note_small(notes, (w[k / 2] >> (16 * (k & 1))) & 0xFFFFu, id + k);
+}
+
+// Counts a part by NT threads.
 template <int NT>
 __device__ __forceinline__ void count_part(const uint16_t *logits, const UnitRange &ur,
-                                           uint32_t *words, int16_t *tops, int tid) {
+                                           uint32_t *words, const Notes &notes, int tid) {
     constexpr int kStep = NT * kStreamVectors, kPerBatch = NT / kGroupLanes;
     const int slot = tid / kGroupLanes;
-    const bool first = (tid & (kGroupLanes - 1)) == 0;
+    const bool first = (tid & (kGroupLanes - 1)) == 0, keep = notes.tops != nullptr;
+    const int64_t id0 = ur.c0 * 8 - ur.g0;
     i16x2 rest = {-32768, -32768};
     stream<NT>(
         reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
         [&](const u32x4 *v, int i) {
-            i16x2 m = tally_vector(words, v[0]);
+            u16x2 lowest = {0xFFFF, 0xFFFF};
+            i16x2 m = tally_vector(words, v[0], lowest);
 #pragma unroll
             for (int u = 1; u < kStreamVectors; ++u)
-                m = __builtin_elementwise_max(m, tally_vector(words, v[u]));
-            if (tops) {
+                m = __builtin_elementwise_max(m, tally_vector(words, v[u], lowest));
+            if (keep) {
                 const int top = group_max(m);
-                if (first) tops[i / kStep * kPerBatch + slot] = (int16_t)top;
+                if (first) notes.tops[i / kStep * kPerBatch + slot] = (int16_t)top;
+                if (lowest.x == 0 || lowest.y == 0) {  // rare
+                    for (int u = 0; u < kStreamVectors; ++u) {
+                        // (one vector at a time, read again: the registers are not to be indexed)
+                        const int j = i + u * NT;
+                        note_small(notes, reinterpret_cast<const u32x4 *>(logits)[ur.c0 + j],
+                                   id0 + (int64_t)j * 8);
+                    }
+                }
             }
         },
-        [&](const u32x4 &v, int) {
-            rest = __builtin_elementwise_max(rest, tally_vector(words, v));
+        [&](const u32x4 &v, int i) {
+            u16x2 lowest = {0xFFFF, 0xFFFF};
+            rest = __builtin_elementwise_max(rest, tally_vector(words, v, lowest));
+            if (keep && (lowest.x == 0 || lowest.y == 0))
+                note_small(notes, v, id0 + (int64_t)i * 8);
         });
-    if (tops) {
+    if (keep) {
         const int top = group_max(rest);
-        if (first) tops[ur.nv / kStep * kPerBatch + slot] = (int16_t)top;
+        if (first) notes.tops[ur.nv / kStep * kPerBatch + slot] = (int16_t)top;
     }
     const int64_t e = ragged_element(ur, tid);
-    if (e >= 0) tally(words, logits[e]);
+    if (e >= 0) {
+        tally(words, logits[e]);
+        if (keep) note_small(notes, (uint32_t)logits[e], e - ur.g0);
+    }
 }
 
 // The value at place q of the candidate order: positive values from the largest down, then the
@@ -189,12 +225,14 @@ __device__ __forceinline__ uint32_t half(uint32_t word, bool negative) {
 }
 
 // Where the counts of a row's parts are: in this workgroup's LDS, ...
+template <int NT>
 struct LocalCounts {
-    static constexpr int kPartThreads = kNT / kParts;
+    static constexpr int kPartThreads = NT / kParts;
     const uint32_t *words;  // [kParts][kStride]
     const int16_t *maxima;  // of the parts' groups, `stride` apart; null: not kept
     int stride;
     __device__ __forceinline__ bool has_tops() const { return maxima != nullptr; }
+    __device__ __forceinline__ bool small_listed() const { return maxima != nullptr; }
     __device__ __forceinline__ const int16_t *tops(int p) const { return maxima + p * stride; }
     __device__ __forceinline__ int parts() const { return kParts; }
     __device__ __forceinline__ uint32_t part(int p, uint32_t word, bool negative) const {
@@ -215,6 +253,7 @@ struct SlicedCounts {
     const uint32_t *sums;   // [2][kStride]
     int slices;
     __device__ __forceinline__ bool has_tops() const { return false; }
+    __device__ __forceinline__ bool small_listed() const { return false; }
     __device__ __forceinline__ const int16_t *tops(int) const { return nullptr; }
     __device__ __forceinline__ int parts() const { return slices; }
     __device__ __forceinline__ uint32_t part(int p, uint32_t word, bool negative) const {
@@ -346,27 +385,34 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
                                        const RowSettings &st, int tid, int32_t *token,
                                        float *logprob) {
     const int lane = tid & (kWave - 1), wave = tid / kWave;
-    constexpr int kOwn = kRows / S16<NT>::kWaves;  // rows of a wave: wave, wave + kWaves, ...
-    static_assert(kOwn * S16<NT>::kWaves == kRows, "rows of a wave");
-    if (tid < 64) sh.scale[tid] = exp2((double)tid * (-1.0 / 64.0));
-    // (the loops over rows are loops: run once per row of logits, their code comes from memory, and
-    // fourteen copies of it took longer to fetch than to run)
-    uint32_t c[kOwn], tokens = 0;
-    uint32_t held = 0;  // which of the wave's rows hold a token
+    // A binade is four rows: two of its positive values, two of its negative ones. The waves take the
+    // binades in turn.
+    constexpr int kTurns = (kRows / 4 + S16<NT>::kWaves - 1) / S16<NT>::kWaves;
+    auto row_of = [&](int binade, int i) {  // descending values: larger magnitudes first, then last
+        return i < 2 ? kRows / 2 - 1 - 2 * binade - i : kRows / 2 + 2 * binade + (i - 2);
+    };
+    S16<NT>::fill_scale(sh, tid);
+    uint32_t tokens = 0, held = 0;  // held: which of the wave's binades hold a token
+    int first = kRows;
 #pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-        const int r = wave + j * S16<NT>::kWaves;
-        c[j] = counts.count(place_word(r * kWave + lane), r >= kRows / 2);
-    }
+    for (int k = 0; k < kTurns; ++k) {
+        const int binade = wave + k * S16<NT>::kWaves;
+        if (binade >= kRows / 4) continue;
 #pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-        tokens += c[j];
-        held |= __ballot(c[j] > 0) != 0ull ? 1u << j : 0u;
+        for (int i = 0; i < 4; ++i) {
+            const int r = row_of(binade, i);
+            const uint32_t n = counts.count(place_word(r * kWave + lane), i >= 2);
+            tokens += n;
+            if (__ballot(n > 0) != 0ull) {
+                held |= 1u << k;
+                first = min(first, r);
+            }
+        }
     }
     tokens = wave_running_sum(tokens);
     if (lane == kWave - 1) {
         ss.total[wave] = tokens;
-        ss.first[wave] = held ? wave + __builtin_ctz(held) * S16<NT>::kWaves : kRows;
+        ss.first[wave] = first;
     }
     if (tid < 2 * kWave) {
         ss.weighed[tid] = 0u;
@@ -377,7 +423,6 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
     const uint32_t large_neg = counts.count(kValues + 1, true);
     __syncthreads();
     uint32_t total = 0;
-    int first = kRows;
 #pragma unroll
     for (int i = 0; i < S16<NT>::kWaves; ++i) {
         total += ss.total[i];
@@ -386,19 +431,21 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
     if (total + small_n + large_pos + large_neg != (uint32_t)V || large_pos > 0 ||
         small_n > kSmallCap || total + small_n == 0)
         return false;
-    // the small values, gathered and sorted
+    // the small values, listed and sorted
     Small small{(int)small_n, 0.0, 0.0, 0u};
     if (small_n > 0) {
-        if (tid == 0) sh.listed = 0;
-        __syncthreads();
-        for (int part = 0; part < counts.parts(); ++part) {
-            if (counts.part(part, 0, false) + counts.part(part, 0, true) == 0) continue;
-            const UnitRange ur = unit_range(row * counts.parts() + part, V, counts.parts(),
-                                            Elem<uint16_t>::kPerVec);
-            S16<NT>::collect(logits, ur, sh, tid, kSmallCap,
-                         [](float x) { return fabsf(x) < 0x1p-20f; });
+        if (!counts.small_listed()) {
+            if (tid == 0) sh.listed = 0;
+            __syncthreads();
+            for (int part = 0; part < counts.parts(); ++part) {
+                if (counts.part(part, 0, false) + counts.part(part, 0, true) == 0) continue;
+                const UnitRange ur = unit_range(row * counts.parts() + part, V, counts.parts(),
+                                                Elem<uint16_t>::kPerVec);
+                S16<NT>::collect(logits, ur, sh, tid, kSmallCap,
+                                 [](float x) { return fabsf(x) < 0x1p-20f; });
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (tid < kWave) {
             const uint64_t key = wave_sort_desc(lane < (int)small_n ? sh.list[lane] : 0ull, lane);
             sh.list[lane] = key;
@@ -420,39 +467,49 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
         const bool by_number = st.top_k >= 1, by_weight = st.min_p > 0.f;
         const double least = by_weight ? fmin((double)st.min_p, 1.0) : 0.0;
         double heavy = 0.0;  // mass of the weights that min_p keeps
+        // A row's values are equidistant, so its weights are that of its first value times
+        // exp(-lane distance / T), which the four rows of a binade share. Lane j has the first
+        // weight of the wave's row j. The row of the maximum, which may begin above it, is weighed
+        // value by value: the maximum's weight is 1 exactly.
+        double base = 0.0;
+        if (lane < 4 * kTurns) {
+            const int binade = wave + lane / 4 * S16<NT>::kWaves;
+            const int r = row_of(min(binade, kRows / 4 - 1), lane & 3);
+            base = weight_at(w, fmax(weight_y(w, place_value(r * kWave)), 0.0));
+        }
 #pragma unroll 1
-        while (held) {  // two rows at a time: their chains of dependent steps overlap
-            int r[2];
-            r[0] = __builtin_ctz(held);
-            held &= held - 1;
-            r[1] = held ? __builtin_ctz(held) : -1;
-            held &= held - 1;
-            double mass[2];
-            uint32_t n[2];
+        for (int k = 0; k < kTurns; ++k) {
+            if (!((held >> k) & 1u)) continue;
+            const int binade = wave + k * S16<NT>::kWaves;
+            const double distance = ldexp(1.0, binade - 27);  // (128 values from 2^(binade - 20) on)
+            const double falloff = weight_at(w, distance * (double)lane * w.c);
+            double mass[4];
+            uint32_t n[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool on = r[i] >= 0;
-                r[i] = on ? wave + r[i] * S16<NT>::kWaves : 0;
-                const float x = place_value(r[i] * kWave + lane);
-                n[i] = counts.count(place_word(r[i] * kWave + lane), r[i] >= kRows / 2);
-                if (!on || !(weight_y(w, x) < (double)kBins)) n[i] = 0;
-                const double wt = n[i] > 0 ? weight_of(w, x) : 0.0;
-                mass[i] = wt * (double)n[i];
+            for (int i = 0; i < 4; ++i) {
+                const int r = row_of(binade, i);
+                n[i] = counts.count(place_word(r * kWave + lane), i >= 2);
+                double wt = lane_value(base, 4 * k + i) * falloff;
+                if (r == first) {
+                    const float x = place_value(r * kWave + lane);
+                    wt = x <= m ? weight_of(w, x) : 0.0;
+                }
+                if (!(wt >= 0x1p-64)) n[i] = 0;
+                mass[i] = n[i] > 0 ? wt * (double)n[i] : 0.0;
                 if (wt >= least) heavy += mass[i];
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 mass[i] = wave_running_sum(mass[i]);
                 // (how many they are matters to top-k only; otherwise whether there are any)
                 n[i] = by_number ? wave_running_sum(n[i]) : (uint32_t)(__ballot(n[i] > 0) != 0ull);
             }
             if (lane == kWave - 1) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (n[i] > 0) {
-                        ss.mass[r[i]] = mass[i];
-                        ss.weighed[r[i]] = n[i];
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    ss.mass[row_of(binade, i)] = mass[i];
+                    ss.weighed[row_of(binade, i)] = n[i];
+                }
             }
         }
         for (int i = 0; i < small.n; ++i) {
@@ -545,7 +602,7 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
         sh.listed = 0;
     }
     __syncthreads();
-    if (tid == 0 && logprob) *logprob = (float)log(ss.share);
+    if (tid == NT - 1 && logprob) *logprob = (float)log(ss.share);
     if (ss.id >= 0) {
         if (tid == 0) *token = ss.id;
         return true;
@@ -613,7 +670,7 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void
 sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Settings st,
                    int32_t *__restrict__ tokens, float *__restrict__ logprob) {
-    __shared__ S16<kNT>::Shared sh;
+    __shared__ typename S16<kNT>::Shared sh;
     __shared__ SettleShared<kNT> ss;
     __shared__ int16_t maxima[kMaxTops];
     const int tid = threadIdx.x;
@@ -621,21 +678,24 @@ sample_bf16_kernel(const uint16_t *__restrict__ logits, int V, double one, Setti
     constexpr int kGroup = kNT / kParts;
     const int part = tid / kGroup;
     const UnitRange ur = unit_range(row * kParts + part, V, kParts, Elem<uint16_t>::kPerVec);
+    const RowSettings rs = row_settings(st, row);
     u32x4 *clear = reinterpret_cast<u32x4 *>(sh.words);
-    for (int i = tid; i < kCountWords / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
+    for (int i = tid; i < kParts * kStride / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
+    if (tid == 0) sh.listed = 0;
     __syncthreads();
     // (the longest part has at most V / 8 / kParts + 1 vectors)
     const int stride = (V / 8 / kParts / (kGroup * kStreamVectors) + 2) * (kGroup / kGroupLanes);
     const bool keep = kParts * stride <= kMaxTops;
-    count_part<kGroup>(logits, ur, sh.words + part * kStride, keep ? maxima + part * stride : nullptr,
-                       tid & (kGroup - 1));
+    Notes notes{nullptr, sh.list, &sh.listed};
+    if (keep) notes.tops = maxima + part * stride;
+    count_part<kGroup>(logits, ur, sh.words + part * kStride, notes, tid & (kGroup - 1));
     __syncthreads();
-    const RowSettings rs = row_settings(st, row);
     int32_t *token = tokens + row;
     float *lp = logprob ? logprob + row : nullptr;
-    if (!settle<kNT>(logits, row, V, LocalCounts{sh.words, keep ? maxima : nullptr, stride}, sh, ss, rs, tid, token, lp)) {
+    const LocalCounts<kNT> counts{sh.words, keep ? maxima : nullptr, stride};
+    if (!settle<kNT>(logits, row, V, counts, sh, ss, rs, tid, token, lp)) {
         __syncthreads();
-        general_row<kNT>(logits, row, V, &sh, &rs, one, token, lp);
+        general_row<kNT>(logits, row, V, sh, rs, one, token, lp);
     }
 }
 
@@ -649,7 +709,7 @@ sample_count_kernel(const uint16_t *__restrict__ logits, int V, int slices,
     u32x4 *clear = reinterpret_cast<u32x4 *>(sh);
     for (int i = tid; i < kStride / 4; i += kNT) clear[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    count_part<kNT>(logits, ur, sh, nullptr, tid);
+    count_part<kNT>(logits, ur, sh, Notes{nullptr, nullptr, nullptr}, tid);
     __syncthreads();
     u32x4 *out = reinterpret_cast<u32x4 *>(words + (size_t)blockIdx.x * kStride);
     for (int i = tid; i < kStride / 4; i += kNT) out[i] = clear[i];
@@ -688,7 +748,7 @@ sample_settle_kernel(const uint16_t *__restrict__ logits, int V, int slices, dou
     float *lp = logprob ? logprob + row : nullptr;
     if (!settle<kNT>(logits, row, V, SlicedCounts{mine, sums, slices}, sh, ss, rs, tid, token, lp)) {
         __syncthreads();
-        general_row<kNT>(logits, row, V, &sh, &rs, one, token, lp);
+        general_row<kNT>(logits, row, V, sh, rs, one, token, lp);
     }
 }
 
@@ -731,8 +791,8 @@ hipError_t launch_sample(const void *logits, int dtype, int R, int V, const floa
     const uint16_t *x = static_cast<const uint16_t *>(logits);
     const int slices = plan_slices(R, V);
     if (slices == 1) {
-        hipLaunchKernelGGL(sample_bf16_kernel, rows, dim3(kNT), 0, stream, x, V, one, st, tokens,
-                           logprob);
+        hipLaunchKernelGGL(sample_bf16_kernel, rows, dim3(kNT), 0, stream, x, V, one,
+                           st, tokens, logprob);
         return hipGetLastError();
     }
     uint32_t *words = static_cast<uint32_t *>(ws);

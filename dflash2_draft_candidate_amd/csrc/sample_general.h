@@ -3,12 +3,12 @@
 //
 // The token is a whole number that a rounding can change, and a flat row has more than 10^5 tokens
 // whose shares a 32-bit sum cannot tell apart: weights and masses are held to about 2^-40.
-// With y = 64 log2(e) (m - x) / T in fp64 and b = floor(y), a weight is 2^(-b/64) 2^(-(y-b)/64); the
-// second factor, within 1% of 1, is a polynomial of degree 5 (error 2.2e-15). b is also the
+// With y = 32 log2(e) (m - x) / T in fp64 and b = floor(y), a weight is 2^(-b/32) 2^(-(y-b)/32); the
+// second factor, within 2.2% of 1, is a polynomial of degree 5 (error 1.5e-13). b is also the
 // weight's bin: bins follow the candidate order, because y does. A bin's second factors are summed
-// as 64-bit integers (kFracBits behind the point) by LDS atomics: whole numbers have no order of
-// summation, so results do not depend on which wave came first. Bins end at b = 4096, weight 2^-64 of
-// the largest: what lies below adds less than 2^-36 of a unit in the last place of u W.
+// as 64-bit integers (41 bits behind the point) by LDS atomics: whole numbers have no order of
+// summation, so results do not depend on which wave came first. Bins end at b = 2048, weight 2^-64 of
+// the largest: the 2^28 longest row's worth of smaller weights is 2^-36 of it.
 //
 // The row is read for its maximum (and, for T = 0, where it first stands) and for the histogram of
 // the bins; then each cut is found among the bins' running masses and inside its bin. Where the
@@ -25,9 +25,10 @@
 
 namespace dflash2 {
 
-constexpr int kBins = 4096;
-constexpr int kCountWords = 4 * 3588;
-constexpr double kBinsPerE = 92.332482616893656;  // 64 log2(e)
+constexpr int kPerOctave = 32;          // bins to a factor of two
+constexpr int kBins = 64 * kPerOctave;
+constexpr int kCountWords = 2 * 3588;
+constexpr double kBinsPerE = kPerOctave * 1.4426950408889634;
 constexpr double kTwo52 = 4503599627370496.0;
 
 enum Cut { kNumber, kReach, kPass };  // the n-th token; first S >= target; first S > target
@@ -44,18 +45,18 @@ struct RowSettings {
 // The weights of a row.
 struct Weights {
     float m;              // row maximum (finite)
-    double c;             // 64 log2(e) / T
-    double one;           // 2^kFracBits of this vocabulary
-    const double *scale;  // 2^(-i/64), i < 64
+    double c;             // kBinsPerE / T
+    double one;           // fixed-point 1 (2^41, less for very long rows)
+    const double *scale;  // 2^(-i/kPerOctave), i < kPerOctave
 };
 
 __device__ __forceinline__ double weight_y(const Weights &w, float x) {
     return ((double)w.m - (double)x) * w.c;
 }
 
-// 2^(-f/64) for f in [0, 1): the Taylor polynomial of exp(-f ln2/64); the next term is below 2.2e-15.
+// 2^(-f/kPerOctave) for f in [0, 1): the Taylor polynomial of exp(-f ln2 / kPerOctave).
 __device__ __forceinline__ double fraction(double f) {
-    constexpr double a = kLn2 / 64.0;
+    constexpr double a = kLn2 / kPerOctave;
     double p = -a * a * a * a * a / 120.0;
     p = __builtin_fma(p, f, a * a * a * a / 24.0);
     p = __builtin_fma(p, f, -a * a * a / 6.0);
@@ -64,20 +65,24 @@ __device__ __forceinline__ double fraction(double f) {
     return __builtin_fma(p, f, 1.0);
 }
 
-// round(2^kFracBits fraction): adding 2^52 leaves the integer in the low mantissa bits.
+// round(one * fraction): adding 2^52 leaves the integer in the low mantissa bits.
 __device__ __forceinline__ uint64_t fixed_fraction(const Weights &w, double f) {
     const double v = __builtin_fma(fraction(f), w.one, kTwo52);
     return (uint64_t)__double_as_longlong(v) & 0xFFFFFFFFFFFFFull;
 }
 
 __device__ __forceinline__ double bin_scale(const Weights &w, int b) {
-    return ldexp(w.scale[b & 63], -(b >> 6));
+    return ldexp(w.scale[b & (kPerOctave - 1)], -(b / kPerOctave));
 }
 
-__device__ __forceinline__ double weight_of(const Weights &w, float x) {
-    const double y = weight_y(w, x);
+// 2^(-y/kPerOctave) for y >= 0.
+__device__ __forceinline__ double weight_at(const Weights &w, double y) {
+    y = fmin(y, 1e6);
     const int b = (int)y;
     return fraction(y - (double)b) * bin_scale(w, b);
+}
+__device__ __forceinline__ double weight_of(const Weights &w, float x) {
+    return weight_at(w, weight_y(w, x));
 }
 
 // A place in the candidate order.
@@ -130,7 +135,7 @@ struct Shared {
         uint32_t words[sizeof(T) == 2 ? kCountWords : 1];  // sample.hip: counts of bf16 values
     };
     uint64_t list[kCap];
-    double scale[64];  // 2^(-i/64)
+    double scale[kPerOctave];  // 2^(-i/kPerOctave)
     double wave_mass[kWaves];
     uint32_t wave_count[kWaves];
     int wave_first[kWaves];
@@ -143,6 +148,10 @@ struct Shared {
     int spot_bin;
     uint32_t spot_size;
 };
+
+static __device__ __forceinline__ void fill_scale(Shared &sh, int tid) {
+    if (tid < kPerOctave) sh.scale[tid] = exp2((double)tid * (-1.0 / kPerOctave));
+}
 
 // ---- workgroup steps -------------------------------------------------------------------------
 
@@ -637,10 +646,10 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
         __syncthreads();
     }
     // Split by value until a part is small or a single value; every step narrows the range to a
-    // 4096th of it or to one value.
+    // 2048th of it or to one value.
     while (size > kCap && k0 != k1) {
         const int bits = 32 - __clz(k1 - k0);
-        const int shift = bits > 12 ? bits - 12 : 0;
+        const int shift = bits > 11 ? bits - 11 : 0;
         for (int b = tid; b < kBins; b += kThreads) {
             sh.mass[b] = 0ull;
             sh.count[b] = 0u;
@@ -691,7 +700,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
             if (logprob) *logprob = (float)lp;
         }
     };
-    if (tid < 64) sh.scale[tid] = exp2((double)tid * (-1.0 / 64.0));
+    fill_scale(sh, tid);
     const Top top = row_top(logits, ur, sh, tid);
     if (top.m == -INFINITY) {  // nothing to draw
         answer(-1, -INFINITY);
@@ -737,7 +746,8 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     const bool by_mass = top_p < 1.f;
     const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;
     const bool by_weight = least > 0x1p-60;
-    const int weight_bin = by_weight ? min((int)(-64.0 * log2(least)) + 1, kBins - 1) : kBins - 1;
+    const int weight_bin =
+        by_weight ? min((int)(-kPerOctave * log2(least)) + 1, kBins - 1) : kBins - 1;
     int low = by_weight ? weight_bin : kBins - 1;
     if (by_number) {
         find_bin(sh, h, kNumber, 0.0, (uint32_t)top_k, tid);
