@@ -342,7 +342,7 @@ __device__ __forceinline__ Spot find_spot(const typename S16<NT>::Shared &sh, co
     const uint32_t start = lane_value(row & 1 ? rows.before[1] : rows.before[0], owner);
     const int q = row * kWave + lane;
     const float value = place_value(q);
-    const bool counted = value <= w.m && weight_y(w, value) < (double)kBins;
+    const bool counted = value <= w.m && weight_y(w, value) < (double)kFar;
     const uint32_t n = counted ? counts.count(place_word(q), q >= kValues) : 0u;
     const double wt = n > 0 ? weight_of(w, value) : 0.0;
     const double mass = wave_running_sum(wt * (double)n);
@@ -462,8 +462,8 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
     const float m = top_small ? key_logit(sh.list[0]) : place_value(top_q);
 
     if (st.temperature > 0.f) {
-        const Weights w{m, kBinsPerE / (double)st.temperature, 1.0, sh.scale};
-        if (large_neg > 0 && !(weight_y(w, -256.f) >= (double)kBins)) return false;
+        const Weights w{m, kBinsPerE / (double)st.temperature, 1.0, sh.scale, m, 0.0, 1.0};
+        if (large_neg > 0 && !(weight_y(w, -256.f) >= (double)kFar)) return false;
         const bool by_number = st.top_k >= 1, by_weight = st.min_p > 0.f;
         const double least = by_weight ? fmin((double)st.min_p, 1.0) : 0.0;
         double heavy = 0.0;  // mass of the weights that min_p keeps
@@ -514,7 +514,7 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
         }
         for (int i = 0; i < small.n; ++i) {
             const float x = key_logit(sh.list[i]);
-            if (!(weight_y(w, x) < (double)kBins)) {  // (they are in order: the rest has none either)
+            if (!(weight_y(w, x) < (double)kFar)) {  // (they are in order: the rest has none either)
                 small.n = i;
                 break;
             }

@@ -3,19 +3,20 @@
 //
 // The token is a whole number that a rounding can change, and a flat row has more than 10^5 tokens
 // whose shares a 32-bit sum cannot tell apart: weights and masses are held to about 2^-40.
-// With y = 32 log2(e) (m - x) / T in fp64 and b = floor(y), a weight is 2^(-b/32) 2^(-(y-b)/32); the
-// second factor, within 2.2% of 1, is a polynomial of degree 5 (error 1.5e-13). b is also the
-// weight's bin: bins follow the candidate order, because y does. A bin's second factors are summed
-// as 64-bit integers (41 bits behind the point) by LDS atomics: whole numbers have no order of
-// summation, so results do not depend on which wave came first. Bins end at b = 2048, weight 2^-64 of
-// the largest: the 2^28 longest row's worth of smaller weights is 2^-36 of it.
+// With y = 32 log2(e) (ref - x) / T + shift in fp64 and b = floor(y), a weight is, but for a factor of
+// the row, 2^(-b/32) 2^(-(y-b)/32); the second factor, within 2.2% of 1, is a polynomial of degree 5
+// (error 1.5e-13). b is also the weight's bin: bins follow the candidate order, because y does. A
+// bin's second factors are summed as 64-bit integers (41 bits behind the point) by LDS atomics: whole
+// numbers have no order of summation, so results do not depend on which wave came first.
 //
-// The row is read for its maximum (and, for T = 0, where it first stands) and for the histogram of
-// the bins; then each cut is found among the bins' running masses and inside its bin. Where the
-// tokens from the top to the lowest cut are few (<= NT) they are gathered once, sorted, and
-// everything is settled in that list. Otherwise each cut gathers and sorts its own bin, which is
-// split by value first if it holds more than NT tokens; when a single value remains, its tokens are
-// equal and a division tells how many of them a cut takes.
+// One pass finds the maximum and fills the bins: ref is the largest of the first logits that the
+// workgroup loads (2 vectors a thread), with 40 octaves of bins left above it and 88 below. Only if
+// the row's maximum lies above the bins is the pass made again with the maximum itself. (For T = 0
+// the pass is for the maximum alone, and where it first stands.) Then each cut is found among the
+// bins' running masses and inside its bin. Where the tokens from the top to the lowest cut are few
+// (<= NT) they are gathered once, sorted, and everything is settled in that list. Otherwise each cut
+// gathers and sorts its own bin, which is split by value first if it holds more than NT tokens; when
+// a single value remains, its tokens are equal and a division tells how many of them a cut takes.
 #pragma once
 
 #include <float.h>
@@ -26,7 +27,9 @@
 namespace dflash2 {
 
 constexpr int kPerOctave = 32;          // bins to a factor of two
-constexpr int kBins = 64 * kPerOctave;
+constexpr int kBins = 128 * kPerOctave;
+constexpr int kHeadroom = 40 * kPerOctave;  // bins above the first estimate of the maximum
+constexpr int kFar = 64 * kPerOctave;       // weights from here on count as 0
 constexpr int kCountWords = 2 * 3588;
 constexpr double kBinsPerE = kPerOctave * 1.4426950408889634;
 constexpr double kTwo52 = 4503599627370496.0;
@@ -44,14 +47,22 @@ struct RowSettings {
 
 // The weights of a row.
 struct Weights {
-    float m;              // row maximum (finite)
+    float m;              // row maximum (finite): its weight is 1
     double c;             // kBinsPerE / T
     double one;           // fixed-point 1 (2^41, less for very long rows)
     const double *scale;  // 2^(-i/kPerOctave), i < kPerOctave
+    // general path: bins start `shift` above `ref`; a bin's weights are `unit` 2^(-b/kPerOctave)
+    // times their second factors
+    float ref;
+    double shift, unit;
 };
 
 __device__ __forceinline__ double weight_y(const Weights &w, float x) {
     return ((double)w.m - (double)x) * w.c;
+}
+
+__device__ __forceinline__ double bin_y(const Weights &w, float x) {
+    return ((double)w.ref - (double)x) * w.c + w.shift;
 }
 
 // 2^(-f/kPerOctave) for f in [0, 1): the Taylor polynomial of exp(-f ln2 / kPerOctave).
@@ -125,6 +136,7 @@ static constexpr int kThreads = NT;
 static constexpr int kWaves = NT / kWave;
 static constexpr int kPer = kBins / NT;  // bins per thread
 static constexpr int kCap = NT;          // gathered tokens, one per thread
+static constexpr int kParts = 1024;      // parts that a bin is split into
 
 struct Shared {
     union {
@@ -134,6 +146,8 @@ struct Shared {
         };
         uint32_t words[sizeof(T) == 2 ? kCountWords : 1];  // sample.hip: counts of bf16 values
     };
+    uint64_t part_mass[kParts];  // of a bin that is split
+    uint32_t part_count[kParts];
     uint64_t list[kCap];
     double scale[kPerOctave];  // 2^(-i/kPerOctave)
     double wave_mass[kWaves];
@@ -205,8 +219,16 @@ static __device__ __forceinline__ int first_thread(Shared &sh, bool c, int tid) 
 
 // The row: f(x, id) for each of its elements, in no particular order; the next two vectors are in
 // flight while two are worked on (the passes that use this are bound by their arithmetic).
+static __device__ __forceinline__ void first_vectors(const T *logits, const UnitRange &ur, int tid,
+                                                     u32x4 &a, u32x4 &b) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    a = b = u32x4{};
+    if (tid < ur.nv) a = p[tid];
+    if (tid + NT < ur.nv) b = p[tid + NT];
+}
 template <typename F>
-static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, F &&f) {
+static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, u32x4 a,
+                                            u32x4 b, F &&f) {
     const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
     const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
     auto one = [&](const u32x4 &v, int i) {
@@ -215,14 +237,10 @@ static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur
 #pragma unroll
         for (int k = 0; k < EV; ++k) f(x[k], id0 + i * EV + k);
     };
-    u32x4 a = u32x4{}, b = u32x4{};
-    if (tid < ur.nv) a = p[tid];
-    if (tid + NT < ur.nv) b = p[tid + NT];
 #pragma unroll 1
     for (int i = tid; i < ur.nv; i += 2 * NT) {
-        u32x4 c = u32x4{}, d = u32x4{};
-        if (i + 2 * NT < ur.nv) c = p[i + 2 * NT];
-        if (i + 3 * NT < ur.nv) d = p[i + 3 * NT];
+        // (past the end: the last vector once more, not looked at; the loads are not conditional)
+        const u32x4 c = p[min(i + 2 * NT, ur.nv - 1)], d = p[min(i + 3 * NT, ur.nv - 1)];
         one(a, i);
         if (i + NT < ur.nv) one(b, i + NT);
         a = c;
@@ -230,6 +248,25 @@ static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur
     }
     const int64_t e = ragged_element(ur, tid);
     if (e >= 0) f(Elem<T>::load(logits, e), (int32_t)(e - ur.g0));
+}
+template <typename F>
+static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, F &&f) {
+    u32x4 a, b;
+    first_vectors(logits, ur, tid, a, b);
+    each(logits, ur, tid, a, b, f);
+}
+
+// The largest of a value over the workgroup.
+static __device__ __forceinline__ float group_top(Shared &sh, float m, int tid) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((tid & (kWave - 1)) == 0) sh.wave_max[tid / kWave] = m;
+    __syncthreads();
+    m = sh.wave_max[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.wave_max[w]);
+    __syncthreads();
+    return m;
 }
 
 // The row's maximum over what is not NaN, in every thread; `at` is where this thread met its own
@@ -270,15 +307,7 @@ static __device__ __forceinline__ Top row_top(const T *logits, const UnitRange &
     float m = t.mine;
     const int64_t e = ragged_element(ur, tid);
     if (e >= 0) m = fmaxf(m, Elem<T>::load(logits, e));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if ((tid & (kWave - 1)) == 0) sh.wave_max[tid / kWave] = m;
-    __syncthreads();
-    m = sh.wave_max[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.wave_max[w]);
-    __syncthreads();
-    t.m = m;
+    t.m = group_top(sh, m, tid);
     return t;
 }
 
@@ -432,6 +461,7 @@ struct Listed {
     uint64_t key;
     double w;      // 0 for threads from n on
     double below;  // masses of the tokens before it
+    double total;
     int n;
 };
 
@@ -469,8 +499,7 @@ static __device__ __forceinline__ Listed make_list(Shared &sh, const Weights &w,
     l.n = n;
     l.key = sort_list(sh, n, tid);
     l.w = tid < n ? weight_of(w, key_logit(l.key)) : 0.0;
-    double total;
-    l.below = scan_mass(sh, l.w, tid, total);
+    l.below = scan_mass(sh, l.w, tid, l.total);
     return l;
 }
 
@@ -480,17 +509,19 @@ static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange
                                          const Weights &w, int b0, int b1, uint32_t k0, uint32_t k1,
                                          int tid) {
     // x of the bins' ends, a step outwards: y < b1 + 1 and y >= b0 up to roundings far below it
-    const double lo = (double)w.m - (double)(b1 + 1) / w.c * (1.0 + 0x1p-20);
-    const double hi = (double)w.m - (double)b0 / w.c * (1.0 - 0x1p-20);
-    const float slack_lo = (float)(lo - fabs(lo) * 0x1p-20), slack_hi = (float)(hi + fabs(hi) * 0x1p-20);
+    const double lo = (double)w.ref - ((double)(b1 + 1) - w.shift) / w.c;
+    const double hi = (double)w.ref - ((double)b0 - w.shift) / w.c;
+    const double slack = fabs((double)w.ref) * 0x1p-20 + ((double)kBins / w.c) * 0x1p-20;
+    const float slack_lo = (float)(lo - fabs(lo) * 0x1p-20 - slack);
+    const float slack_hi = (float)(hi + fabs(hi) * 0x1p-20 + slack);
     const float xlo = w.c > 0.0 ? slack_lo : -FLT_MAX, xhi = w.c > 0.0 ? slack_hi : FLT_MAX;
     if (tid == 0) sh.listed = 0;
     __syncthreads();
     each(logits, ur, tid, [&](float x, int32_t id) {
         if (x >= xlo && x <= xhi) {
-            const double y = weight_y(w, x);
+            const double y = bin_y(w, x);
             const uint32_t vk = value_key(x);
-            if (y < (double)kBins && (int)y >= b0 && (int)y <= b1 && vk >= k0 && vk <= k1) {
+            if (y >= 0.0 && y < (double)kBins && (int)y >= b0 && (int)y <= b1 && vk >= k0 && vk <= k1) {
                 const uint32_t at = atomicAdd(&sh.listed, 1u);
                 if (at < kCap) sh.list[at] = cand_key(x, id);
             }
@@ -504,30 +535,36 @@ static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange
 
 // ---- cuts -------------------------------------------------------------------------------------
 
-// The histogram's bins of this thread: masses and counts, and what lies before them.
+// A histogram in LDS: kPerThread bins per thread, of mass sum[b] `unit`, times 2^(-b/kPerOctave) where
+// `by_bin` is set.
+template <int kPerThread>
+struct Level {
+    const uint64_t *sum;
+    const uint32_t *counts;
+    double unit;
+    bool by_bin;
+    __device__ __forceinline__ double mass(const Weights &w, int b) const {
+        return (double)sum[b] * (by_bin ? bin_scale(w, b) * unit : unit);
+    }
+};
+// What lies before this thread's bins, and in all.
 struct Bins {
-    double mass[kPer];
-    uint32_t count[kPer];
-    double below;
-    uint32_t before;
-    double total;
-    uint32_t number;
+    double below, total;
+    uint32_t before, number;
 };
 
-// Takes a histogram over bins out of LDS (their factor 2^(-b/64) for level 0; `scale` otherwise).
-static __device__ __forceinline__ Bins take_bins(Shared &sh, const Weights &w, bool by_bin, double scale,
-                                          double below, uint32_t before, int tid) {
+template <int kPerThread>
+static __device__ __forceinline__ Bins sum_bins(Shared &sh, const Level<kPerThread> &v,
+                                                const Weights &w, double below, uint32_t before,
+                                                int tid) {
     Bins h;
     double sum = 0.0;
     uint32_t number = 0;
-    const double unit = 1.0 / w.one;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int b = tid * kPer + j;
-        h.count[j] = sh.count[b];
-        h.mass[j] = (double)sh.mass[b] * unit * (by_bin ? bin_scale(w, b) : scale);
-        sum += h.mass[j];
-        number += h.count[j];
+    for (int j = 0; j < kPerThread; ++j) {
+        const int b = tid * kPerThread + j;
+        sum += v.mass(w, b);
+        number += v.counts[b];
     }
     h.below = below + scan_mass(sh, sum, tid, h.total);
     h.before = before + scan_count(sh, number, tid, h.number);
@@ -538,41 +575,41 @@ static __device__ __forceinline__ Bins take_bins(Shared &sh, const Weights &w, b
 
 // The bin that holds a cut: the result is in sh.spot_*. Roundings may leave a mass cut behind the
 // last bin: it is then the last that holds anything.
-static __device__ __forceinline__ void find_bin(Shared &sh, const Bins &h, Cut cut, double target,
-                                         uint32_t nth, int tid) {
-    double run = h.below, spot_mass = 0.0;
-    uint32_t num = h.before, spot_count = 0, spot_size = 0;
-    int bin = -1;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const double next = run + h.mass[j];
-        const uint32_t nnum = num + h.count[j];
-        const bool in = h.count[j] > 0 && bin < 0 &&
-                        (cut == kNumber ? nnum >= nth : cut == kReach ? next >= target : next > target);
-        if (in) {
-            bin = tid * kPer + j;
-            spot_mass = run;
-            spot_count = num;
-            spot_size = h.count[j];
-        }
-        run = next;
-        num = nnum;
-    }
-    int first = first_thread(sh, bin >= 0, tid);
-    if (first == kThreads) {  // the last bin with a token
-        run = h.below;
-        num = h.before;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            if (h.count[j] > 0) {
-                bin = tid * kPer + j;
-                spot_mass = run;
-                spot_count = num;
-                spot_size = h.count[j];
+template <int kPerThread>
+static __device__ __forceinline__ void find_bin(Shared &sh, const Level<kPerThread> &v,
+                                                const Weights &w, const Bins &h, Cut cut,
+                                                double target, uint32_t nth, int tid) {
+    // the first bin of this thread that meets the cut, or (any) the last that holds a token
+    auto look = [&](bool any, double &run, uint32_t &num, uint32_t &size) {
+        int bin = -1;
+        double mass = h.below;
+        uint32_t number = h.before;
+#pragma unroll 1
+        for (int j = 0; j < kPerThread; ++j) {
+            const int b = tid * kPerThread + j;
+            const uint32_t n = v.counts[b];
+            if (n == 0) continue;
+            const double next = mass + v.mass(w, b);
+            const bool in = cut == kNumber ? number + n >= nth
+                            : cut == kReach ? next >= target
+                                            : next > target;
+            if (any || (in && bin < 0)) {
+                bin = b;
+                run = mass;
+                num = number;
+                size = n;
             }
-            run += h.mass[j];
-            num += h.count[j];
+            mass = next;
+            number += n;
         }
+        return bin;
+    };
+    double spot_mass = 0.0;
+    uint32_t spot_count = 0, spot_size = 0;
+    int bin = look(false, spot_mass, spot_count, spot_size);
+    int first = first_thread(sh, bin >= 0, tid);
+    if (first == kThreads) {
+        bin = look(true, spot_mass, spot_count, spot_size);
         const uint64_t b = __ballot(bin >= 0);
         const int lane = tid & (kWave - 1), wave = tid / kWave;
         if (lane == 0) sh.wave_first[wave] = b ? wave * kWave + 63 - __builtin_clzll(b) : -1;
@@ -629,8 +666,8 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
         __syncthreads();
         uint32_t lo = 0xFFFFFFFFu, hi = 0u;
         each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = weight_y(w, x);
-            if (y < (double)kBins && (int)y == bin) {
+            const double y = bin_y(w, x);
+            if (y >= 0.0 && y < (double)kBins && (int)y == bin) {
                 const uint32_t vk = value_key(x);
                 lo = min(lo, vk);
                 hi = max(hi, vk);
@@ -646,28 +683,30 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
         __syncthreads();
     }
     // Split by value until a part is small or a single value; every step narrows the range to a
-    // 2048th of it or to one value.
+    // kParts-th of it or to one value.
     while (size > kCap && k0 != k1) {
         const int bits = 32 - __clz(k1 - k0);
-        const int shift = bits > 11 ? bits - 11 : 0;
-        for (int b = tid; b < kBins; b += kThreads) {
-            sh.mass[b] = 0ull;
-            sh.count[b] = 0u;
+        const int shift = bits > 10 ? bits - 10 : 0;
+        for (int b = tid; b < kParts; b += kThreads) {
+            sh.part_mass[b] = 0ull;
+            sh.part_count[b] = 0u;
         }
         __syncthreads();
         each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = weight_y(w, x);
+            const double y = bin_y(w, x);
             const uint32_t vk = value_key(x);
-            if (y < (double)kBins && (int)y == bin && vk >= k0 && vk <= k1) {
+            if (y >= 0.0 && y < (double)kBins && (int)y == bin && vk >= k0 && vk <= k1) {
                 const uint32_t part = (k1 - vk) >> shift;
-                atomicAdd((unsigned long long *)&sh.mass[part],
+                atomicAdd((unsigned long long *)&sh.part_mass[part],
                           (unsigned long long)fixed_fraction(w, y - (double)bin));
-                atomicAdd(&sh.count[part], 1u);
+                atomicAdd(&sh.part_count[part], 1u);
             }
         });
         __syncthreads();
-        const Bins h = take_bins(sh, w, false, bin_scale(w, bin), below, before, tid);
-        find_bin(sh, h, cut, target, nth, tid);
+        const Level<kParts / NT> v{sh.part_mass, sh.part_count,
+                                   bin_scale(w, bin) * w.unit / w.one, false};
+        const Bins h = sum_bins(sh, v, w, below, before, tid);
+        find_bin(sh, v, w, h, cut, target, nth, tid);
         const uint32_t part = (uint32_t)sh.spot_bin;
         below = sh.spot_mass;
         before = sh.spot_count;
@@ -700,17 +739,57 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
             if (logprob) *logprob = (float)lp;
         }
     };
+    if (!(temperature > 0.f)) {
+        const Top top = row_top(logits, ur, sh, tid);
+        if (top.m == -INFINITY)
+            answer(-1, -INFINITY);
+        else
+            answer(first_of_top(logits, ur, top, sh, tid), 0.0);
+        return;
+    }
+    u32x4 a, b;
+    first_vectors(logits, ur, tid, a, b);
     fill_scale(sh, tid);
-    const Top top = row_top(logits, ur, sh, tid);
-    if (top.m == -INFINITY) {  // nothing to draw
+    float m = -INFINITY;
+    {
+        float x[2 * EV];
+        Elem<T>::unpack(a, x);
+        Elem<T>::unpack(b, x + EV);
+#pragma unroll
+        for (int k = 0; k < 2 * EV; ++k)
+            if (tid + (k < EV ? 0 : NT) < ur.nv) m = fmaxf(m, x[k]);
+    }
+    Weights w{0.f, kBinsPerE / (double)temperature, one, sh.scale, group_top(sh, m, tid),
+              (double)kHeadroom, 1.0};
+#pragma unroll 1
+    for (;;) {
+        for (int i = tid; i < kBins; i += kThreads) {
+            sh.mass[i] = 0ull;
+            sh.count[i] = 0u;
+        }
+        __syncthreads();
+        each(logits, ur, tid, a, b, [&](float x, int32_t) {
+            m = fmaxf(m, x);
+            const double y = bin_y(w, x);
+            if (y >= 0.0 && y < (double)kBins) {  // (false for NaN and -inf)
+                const int i = (int)y;
+                atomicAdd((unsigned long long *)&sh.mass[i],
+                          (unsigned long long)fixed_fraction(w, y - (double)i));
+                atomicAdd(&sh.count[i], 1u);
+            }
+        });
+        w.m = group_top(sh, m, tid);
+        // (nothing to weigh, or the maximum has its bin; a second time it always has)
+        if (!(fabsf(w.m) < INFINITY) || (w.ref > -INFINITY && bin_y(w, w.m) >= 0.0)) break;
+        w.ref = w.m;
+        w.shift = 0.0;
+        first_vectors(logits, ur, tid, a, b);
+    }
+    if (w.m == -INFINITY) {  // nothing to draw
         answer(-1, -INFINITY);
         return;
     }
-    if (!(temperature > 0.f)) {
-        answer(first_of_top(logits, ur, top, sh, tid), 0.0);
-        return;
-    }
-    if (top.m == INFINITY) {  // only the infinite logits have weight, all the same
+    if (w.m == INFINITY) {  // only the infinite logits have weight, all the same
         uint32_t n;
         nth_equal(logits, ur, sh, tid, INFINITY, 0u, n);
         if (top_k >= 1 && (uint32_t)top_k < n) n = (uint32_t)top_k;
@@ -721,24 +800,14 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         answer(nth_equal(logits, ur, sh, tid, INFINITY, p.nth, n), -log(whole));
         return;
     }
-
-    const Weights w{top.m, kBinsPerE / (double)temperature, one, sh.scale};
-    for (int b = tid; b < kBins; b += kThreads) {
-        sh.mass[b] = 0ull;
-        sh.count[b] = 0u;
+    if (w.ref == w.m) {
+        // (bins from 0 on, or `shift` on: powers of two apart, so equal tokens still weigh 1 each)
+        w.unit = ldexp(1.0, (int)w.shift / kPerOctave);
+    } else {
+        w.unit = exp2(bin_y(w, w.m) * (1.0 / kPerOctave));
     }
-    __syncthreads();
-    each(logits, ur, tid, [&](float x, int32_t) {
-        const double y = weight_y(w, x);
-        if (y < (double)kBins) {  // (false for NaN and -inf)
-            const int b = (int)y;
-            atomicAdd((unsigned long long *)&sh.mass[b],
-                      (unsigned long long)fixed_fraction(w, y - (double)b));
-            atomicAdd(&sh.count[b], 1u);
-        }
-    });
-    __syncthreads();
-    const Bins h = take_bins(sh, w, true, 1.0, 0.0, 0u, tid);
+    const Level<kPer> all{sh.mass, sh.count, w.unit / one, true};
+    const Bins h = sum_bins(sh, all, w, 0.0, 0u, tid);
 
     // The lowest bin that the cuts can reach. (A top-k beyond the counted tokens cuts only among
     // weights below 2^-64.)
@@ -747,15 +816,17 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;
     const bool by_weight = least > 0x1p-60;
     const int weight_bin =
-        by_weight ? min((int)(-kPerOctave * log2(least)) + 1, kBins - 1) : kBins - 1;
+        by_weight ? min((int)(bin_y(w, w.m) - kPerOctave * log2(least)) + 1, kBins - 1) : kBins - 1;
+    bool mass_inside = false;  // the nucleus ends in the bins up to `low`
     int low = by_weight ? weight_bin : kBins - 1;
     if (by_number) {
-        find_bin(sh, h, kNumber, 0.0, (uint32_t)top_k, tid);
+        find_bin(sh, all, w, h, kNumber, 0.0, (uint32_t)top_k, tid);
         // (top-p needs the whole mass of the top-k tokens, whatever min-p leaves of them)
         low = by_mass ? sh.spot_bin : min(low, sh.spot_bin);
         __syncthreads();
     } else if (by_mass) {
-        find_bin(sh, h, kReach, (double)top_p * h.total, 0u, tid);
+        find_bin(sh, all, w, h, kReach, (double)top_p * h.total, 0u, tid);
+        mass_inside = sh.spot_bin <= low;
         low = min(low, sh.spot_bin);
         __syncthreads();
     }
@@ -764,21 +835,28 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     {
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
-            if (tid * kPer + j <= low) upto += h.count[j];
+            if (tid * kPer + j <= low) upto += sh.count[tid * kPer + j];
         uint32_t total;
         scan_count(sh, upto, tid, total);
         upto = total;
     }
     if (upto <= kCap) {
         const Listed l = gather(logits, ur, sh, w, 0, low, 0u, 0xFFFFFFFFu, tid);
-        double z = h.total;
+        // (the list's weights are exact where equal tokens tie; the bins give only what lies below it)
+        double z = 0.0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (tid * kPer + j > low) z += all.mass(w, tid * kPer + j);
+        double tail;
+        scan_mass(sh, z, tid, tail);
+        z = l.total + tail;
         if (by_number)
             z = cut_list(sh, l, kNumber, 0.0, (uint32_t)top_k, 0.0, 0u, tid).mass;
         double whole = z;
         if (by_mass) {
             const double target = (double)top_p * z;
             // (the list may end before the nucleus does, at a min-p cut)
-            if (first_thread(sh, tid < l.n && l.below + l.w >= target, tid) < l.n)
+            if (mass_inside || first_thread(sh, tid < l.n && l.below + l.w >= target, tid) < l.n)
                 whole = fmin(whole, cut_list(sh, l, kReach, target, 0u, 0.0, 0u, tid).mass);
         }
         if (by_weight) {
@@ -796,15 +874,15 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         // all of the bins above those that the border can fall in, and what reaches it there
         double part = 0.0;
         each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = weight_y(w, x);
-            if (y < (double)kBins && (int)y <= weight_bin && (int)y >= weight_bin - 2) {
+            const double y = bin_y(w, x);
+            if (y >= 0.0 && y < (double)kBins && (int)y <= weight_bin && (int)y >= weight_bin - 2) {
                 const double v = weight_of(w, x);
                 if (v >= least) part += v;
             }
         });
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
-            if (tid * kPer + j < weight_bin - 2) part += h.mass[j];
+            if (tid * kPer + j < weight_bin - 2) part += all.mass(w, tid * kPer + j);
         double sum;
         scan_mass(sh, part, tid, sum);
         whole = fmin(whole, sum);
@@ -815,7 +893,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         if (step == 1 && !by_mass) continue;
         const Cut cut = step == 0 ? kNumber : step == 1 ? kReach : kPass;
         const double target = step == 1 ? (double)top_p * z : u * whole;
-        find_bin(sh, h, cut, target, (uint32_t)top_k, tid);
+        find_bin(sh, all, w, h, cut, target, (uint32_t)top_k, tid);
         const int bin = sh.spot_bin;
         const double below = sh.spot_mass;
         const uint32_t before = sh.spot_count, size = sh.spot_size;
