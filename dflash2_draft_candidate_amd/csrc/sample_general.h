@@ -3,11 +3,12 @@
 //
 // The token is a whole number that a rounding can change, and a flat row has more than 10^5 tokens
 // whose shares a 32-bit sum cannot tell apart: weights and masses are held to about 2^-40.
-// With y = 32 log2(e) (ref - x) / T + shift in fp64 and b = floor(y), a weight is, but for a factor of
-// the row, 2^(-b/32) 2^(-(y-b)/32); the second factor, within 2.2% of 1, is a polynomial of degree 5
-// (error 1.5e-13). b is also the weight's bin: bins follow the candidate order, because y does. A
-// bin's second factors are summed as 64-bit integers (41 bits behind the point) by LDS atomics: whole
-// numbers have no order of summation, so results do not depend on which wave came first.
+// With z = 32 log2(e) (ref - x) / T + shift in fp64 and b the integer nearest to it, a weight is, but for
+// a factor of the row, 2^(-b/32) 2^(-(z-b)/32); the second factor, within 1.1% of 1, is a polynomial
+// of degree 4 (error 1.6e-13, 1 at 0). b (counted from the middle of the bins) is also the weight's
+// bin: bins follow the candidate order, because z does. A bin's second factors are summed as 64-bit
+// integers (41 bits behind the point) by LDS atomics: whole numbers have no order of summation, so
+// results do not depend on which wave came first.
 //
 // One pass finds the maximum and fills the bins: ref is the largest of the first logits that the
 // workgroup loads (2 vectors a thread), with 40 octaves of bins left above it and 88 below. Only if
@@ -28,11 +29,13 @@ namespace dflash2 {
 
 constexpr int kPerOctave = 32;          // bins to a factor of two
 constexpr int kBins = 128 * kPerOctave;
-constexpr int kHeadroom = 40 * kPerOctave;  // bins above the first estimate of the maximum
+constexpr int kHeadroom = 40 * kPerOctave;  // the bin of the first estimate of the maximum
 constexpr int kFar = 64 * kPerOctave;       // weights from here on count as 0
 constexpr int kCountWords = 2 * 3588;
 constexpr double kBinsPerE = kPerOctave * 1.4426950408889634;
 constexpr double kTwo52 = 4503599627370496.0;
+// added to z, this leaves the bin's number in the low bits
+constexpr double kToBin = 1.5 * kTwo52 + kBins / 2;
 
 enum Cut { kNumber, kReach, kPass };  // the n-th token; first S >= target; first S > target
 
@@ -51,8 +54,7 @@ struct Weights {
     double c;             // kBinsPerE / T
     double one;           // fixed-point 1 (2^41, less for very long rows)
     const double *scale;  // 2^(-i/kPerOctave), i < kPerOctave
-    // general path: bins start `shift` above `ref`; a bin's weights are `unit` 2^(-b/kPerOctave)
-    // times their second factors
+    // general path: a bin's weights are `unit` 2^(-b/kPerOctave) times their second factors
     float ref;
     double shift, unit;
 };
@@ -61,18 +63,20 @@ __device__ __forceinline__ double weight_y(const Weights &w, float x) {
     return ((double)w.m - (double)x) * w.c;
 }
 
-__device__ __forceinline__ double bin_y(const Weights &w, float x) {
-    return ((double)w.ref - (double)x) * w.c + w.shift;
+// p f + c; c uniform, from a scalar register (the compiler copies it to a vector register first).
+__device__ __forceinline__ double fma_const(double p, double f, double c) {
+    double r;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(p), "v"(f), "s"(c));
+    return r;
 }
 
-// 2^(-f/kPerOctave) for f in [0, 1): the Taylor polynomial of exp(-f ln2 / kPerOctave).
+// 2^(-f/32) for |f| <= 1/2: 1 + f times the cubic that meets (2^(-f/32) - 1) / f at the four Chebyshev
+// nodes of the interval; relative error 1.6e-13.
 __device__ __forceinline__ double fraction(double f) {
-    constexpr double a = kLn2 / kPerOctave;
-    double p = -a * a * a * a * a / 120.0;
-    p = __builtin_fma(p, f, a * a * a * a / 24.0);
-    p = __builtin_fma(p, f, -a * a * a / 6.0);
-    p = __builtin_fma(p, f, a * a / 2.0);
-    p = __builtin_fma(p, f, -a);
+    static_assert(kPerOctave == 32, "coefficients");
+    double p = fma_const(f, 0x1.3b2b07bdf358dp-27, -0x1.c6b13c3465457p-20);
+    p = fma_const(p, f, 0x1.ebfbdff82240ap-13);
+    p = fma_const(p, f, -0x1.62e42fef8dc67p-6);
     return __builtin_fma(p, f, 1.0);
 }
 
@@ -83,18 +87,28 @@ __device__ __forceinline__ uint64_t fixed_fraction(const Weights &w, double f) {
 }
 
 __device__ __forceinline__ double bin_scale(const Weights &w, int b) {
-    return ldexp(w.scale[b & (kPerOctave - 1)], -(b / kPerOctave));
+    return ldexp(w.scale[b & (kPerOctave - 1)], -(b / kPerOctave));  // (b >= 0)
 }
 
 // 2^(-y/kPerOctave) for y >= 0.
 __device__ __forceinline__ double weight_at(const Weights &w, double y) {
     y = fmin(y, 1e6);
-    const int b = (int)y;
-    return fraction(y - (double)b) * bin_scale(w, b);
+    const double b = rint(y);
+    return fraction(y - b) * bin_scale(w, (int)b);
 }
 __device__ __forceinline__ double weight_of(const Weights &w, float x) {
     return weight_at(w, weight_y(w, x));
 }
+
+__device__ __forceinline__ double bin_z(const Weights &w, float x) {
+    return __builtin_fma((double)w.ref - (double)x, w.c, w.shift);
+}
+__device__ __forceinline__ bool has_bin(double z) { return fabs(z) < kBins / 2 - 1; }  // (no NaN has)
+__device__ __forceinline__ int bin_of(double z) {
+    return (int)(uint32_t)__double_as_longlong(z + kToBin);
+}
+// z's distance from its bin's middle.
+__device__ __forceinline__ double bin_fraction(double z) { return z - ((z + kToBin) - kToBin); }
 
 // A place in the candidate order.
 struct Place {
@@ -155,7 +169,6 @@ struct Shared {
     int wave_first[kWaves];
     float wave_max[kWaves];
     uint32_t listed;
-    uint32_t key_lo, key_hi;
     int32_t token;
     double spot_mass;
     uint32_t spot_count;
@@ -256,6 +269,45 @@ static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur
     each(logits, ur, tid, a, b, f);
 }
 
+// The row's whole vectors, f(vector, index), with more in flight, for cheap f: those passes wait for
+// memory. (One copy of the body: with stream()'s five the compiler keeps every copy's ids in
+// registers.)
+template <typename F>
+static __device__ __forceinline__ void each_vector(const T *logits, const UnitRange &ur, int tid,
+                                                   F &&f) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    constexpr int kDeep = 3;
+    u32x4 v[kDeep], next[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+        v[u] = u32x4{};
+        if (tid + u * NT < ur.nv) v[u] = p[tid + u * NT];
+    }
+#pragma unroll 1
+    for (int i = tid; i < ur.nv; i += kDeep * NT) {
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) next[u] = p[min(i + (kDeep + u) * NT, ur.nv - 1)];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            if (i + u * NT < ur.nv) f(v[u], i + u * NT);
+            v[u] = next[u];
+        }
+    }
+}
+template <typename F>
+static __device__ __forceinline__ void each_cheap(const T *logits, const UnitRange &ur, int tid,
+                                                  F &&f) {
+    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
+    each_vector(logits, ur, tid, [&](const u32x4 &v, int i) {
+        float x[EV];
+        Elem<T>::unpack(v, x);
+#pragma unroll
+        for (int k = 0; k < EV; ++k) f(x[k], id0 + i * EV + k);
+    });
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0) f(Elem<T>::load(logits, e), (int32_t)(e - ur.g0));
+}
+
 // The largest of a value over the workgroup.
 static __device__ __forceinline__ float group_top(Shared &sh, float m, int tid) {
 #pragma unroll
@@ -269,67 +321,36 @@ static __device__ __forceinline__ float group_top(Shared &sh, float m, int tid) 
     return m;
 }
 
-// The row's maximum over what is not NaN, in every thread; `at` is where this thread met its own
-// (a vector index; the element lies there or up to kStreamVectors - 1 strides on).
-struct Top {
-    float m;     // of the row
-    float mine;  // of this thread's vectors
-    int at;
-};
-
-static __device__ __forceinline__ Top row_top(const T *logits, const UnitRange &ur, Shared &sh, int tid) {
-    Top t{-INFINITY, -INFINITY, 0};
-    stream<kThreads>(
-        reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
-        [&](const u32x4 *v, int i) {
-            float x[kStreamVectors * EV];
+// The lowest id of the row's largest logit (NaN aside), -1 if nothing lies above -inf.
+static __device__ __forceinline__ int32_t first_of_top(const T *logits, const UnitRange &ur,
+                                                       Shared &sh, int tid) {
+    float mine = -INFINITY;
+    int at = -1;  // the first vector of this thread that holds its largest
+    each_vector(logits, ur, tid, [&](const u32x4 &v, int i) {
+        float x[EV];
+        Elem<T>::unpack(v, x);
+        float c = x[0];
 #pragma unroll
-            for (int u = 0; u < kStreamVectors; ++u) Elem<T>::unpack(v[u], x + u * EV);
-            float c = x[0];
-#pragma unroll
-            for (int k = 1; k < kStreamVectors * EV; ++k) c = fmaxf(c, x[k]);
-            if (c > t.mine) {
-                t.mine = c;
-                t.at = i;
-            }
-        },
-        [&](const u32x4 &v, int i) {
-            float x[EV];
-            Elem<T>::unpack(v, x);
-            float c = x[0];
-#pragma unroll
-            for (int k = 1; k < EV; ++k) c = fmaxf(c, x[k]);
-            if (c > t.mine) {
-                t.mine = c;
-                t.at = i;
-            }
-        });
-    float m = t.mine;
-    const int64_t e = ragged_element(ur, tid);
-    if (e >= 0) m = fmaxf(m, Elem<T>::load(logits, e));
-    t.m = group_top(sh, m, tid);
-    return t;
-}
-
-// The lowest id whose logit is the row's maximum.
-static __device__ __forceinline__ int32_t first_of_top(const T *logits, const UnitRange &ur, const Top &t,
-                                                Shared &sh, int tid) {
-    if (tid == 0) sh.token = 0x7FFFFFFF;
-    __syncthreads();
-    int32_t id = 0x7FFFFFFF;
-    if (t.mine == t.m) {
-        for (int u = kStreamVectors - 1; u >= 0; --u) {
-            const int i = t.at + u * kThreads;
-            if (i >= ur.nv) continue;
-            float x[EV];
-            Elem<T>::unpack(reinterpret_cast<const u32x4 *>(logits)[ur.c0 + i], x);
-#pragma unroll
-            for (int k = EV - 1; k >= 0; --k)
-                if (x[k] == t.m) id = (int32_t)((ur.c0 + i) * EV + k - ur.g0);
+        for (int k = 1; k < EV; ++k) c = fmaxf(c, x[k]);
+        if (c > mine) {
+            mine = c;
+            at = i;
         }
-    }
+    });
     const int64_t e = ragged_element(ur, tid);
-    if (e >= 0 && Elem<T>::load(logits, e) == t.m) id = min(id, (int32_t)(e - ur.g0));
+    const float end = e >= 0 ? Elem<T>::load(logits, e) : -INFINITY;
+    if (tid == 0) sh.token = 0x7FFFFFFF;
+    const float m = group_top(sh, fmaxf(mine, end), tid);
+    if (m == -INFINITY) return -1;
+    int32_t id = 0x7FFFFFFF;
+    if (mine == m) {
+        float x[EV];
+        Elem<T>::unpack(reinterpret_cast<const u32x4 *>(logits)[ur.c0 + at], x);
+#pragma unroll
+        for (int k = EV - 1; k >= 0; --k)
+            if (x[k] == m) id = (int32_t)((ur.c0 + at) * EV + k - ur.g0);
+    }
+    if (e >= 0 && end == m) id = min(id, (int32_t)(e - ur.g0));
     if (id != 0x7FFFFFFF) atomicMin(&sh.token, id);
     __syncthreads();
     id = sh.token;
@@ -342,7 +363,7 @@ static __device__ __forceinline__ int32_t first_of_top(const T *logits, const Un
 // in flight. A comparison leaves a mask of lanes in a scalar register, and the scalar unit
 // counts its bits: the vector units see two instructions an element (they are what bounds this
 // otherwise: every wave of the workgroup runs here).
-static constexpr int kSweep = 8;
+static constexpr int kSweep = sizeof(T) == 2 ? 8 : 4;
 static __device__ __forceinline__ int32_t nth_equal(const T *logits, const UnitRange &ur, Shared &sh,
                                                     int tid, float value, uint32_t nth,
                                                     uint32_t &total) {
@@ -503,28 +524,54 @@ static __device__ __forceinline__ Listed make_list(Shared &sh, const Weights &w,
     return l;
 }
 
-// Gathers the tokens of bins [b0, b1] whose value keys lie in [k0, k1] (at most kCap, known from
-// the histogram). The float bounds drop nearly all others first.
+// The smallest value key in [key(-FLT_MAX), key(FLT_MAX)] for which `holds` is true, one past the range
+// if there is none; holds(x) must not fall back to false as x grows. Every wave searches by itself,
+// 64 keys at a time.
+template <typename F>
+static __device__ __forceinline__ uint32_t first_key(int lane, F &&holds) {
+    uint32_t a = value_key(-FLT_MAX), e = value_key(FLT_MAX) + 1u;  // a <= answer <= e
+#pragma unroll 1
+    while (a < e) {
+        const uint32_t step = (e - a) / kWave + 1u;
+        const uint64_t probe = (uint64_t)a + (uint64_t)lane * step;
+        const bool yes = probe >= e || holds(key_value((uint32_t)probe));
+        const uint64_t b = __ballot(yes);
+        const uint32_t t = b ? (uint32_t)__builtin_ctzll(b) : (uint32_t)kWave;
+        const uint32_t base = a;
+        if (t > 0) a = base + (t - 1u) * step + 1u;
+        const uint64_t top = (uint64_t)base + (uint64_t)t * step;
+        if (t < kWave && top < e) e = (uint32_t)top;
+    }
+    return a;
+}
+// Value keys of the bins [b0, b1].
+struct Keys {
+    uint32_t lo, hi;  // lo <= key <= hi
+};
+static __device__ __forceinline__ Keys keys_of(const Weights &w, int b0, int b1, int lane) {
+    auto from = [&](int b) {  // the first key in bin b or above it in the order
+        const double last = (double)(b - kBins / 2);
+        return first_key(lane, [&](float x) {
+            const double z = bin_z(w, x);
+            return z - bin_fraction(z) <= last;
+        });
+    };
+    Keys k;
+    k.lo = from(b1);
+    k.hi = from(b0 - 1) - 1u;
+    return k;
+}
+
+// Gathers the tokens with these keys (at most kCap, known from the histogram).
 static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange &ur, Shared &sh,
-                                         const Weights &w, int b0, int b1, uint32_t k0, uint32_t k1,
-                                         int tid) {
-    // x of the bins' ends, a step outwards: y < b1 + 1 and y >= b0 up to roundings far below it
-    const double lo = (double)w.ref - ((double)(b1 + 1) - w.shift) / w.c;
-    const double hi = (double)w.ref - ((double)b0 - w.shift) / w.c;
-    const double slack = fabs((double)w.ref) * 0x1p-20 + ((double)kBins / w.c) * 0x1p-20;
-    const float slack_lo = (float)(lo - fabs(lo) * 0x1p-20 - slack);
-    const float slack_hi = (float)(hi + fabs(hi) * 0x1p-20 + slack);
-    const float xlo = w.c > 0.0 ? slack_lo : -FLT_MAX, xhi = w.c > 0.0 ? slack_hi : FLT_MAX;
+                                         const Weights &w, const Keys &keys, int tid) {
+    const float lo = key_value(keys.lo), hi = key_value(keys.hi);
     if (tid == 0) sh.listed = 0;
     __syncthreads();
-    each(logits, ur, tid, [&](float x, int32_t id) {
-        if (x >= xlo && x <= xhi) {
-            const double y = bin_y(w, x);
-            const uint32_t vk = value_key(x);
-            if (y >= 0.0 && y < (double)kBins && (int)y >= b0 && (int)y <= b1 && vk >= k0 && vk <= k1) {
-                const uint32_t at = atomicAdd(&sh.listed, 1u);
-                if (at < kCap) sh.list[at] = cand_key(x, id);
-            }
+    each_cheap(logits, ur, tid, [&](float x, int32_t id) {
+        if (x >= lo && x <= hi) {
+            const uint32_t at = atomicAdd(&sh.listed, 1u);
+            if (at < kCap) sh.list[at] = cand_key(x, id);
         }
     });
     __syncthreads();
@@ -657,48 +704,24 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
                                       const Weights &w, int bin, uint32_t size, Cut cut,
                                       double target, uint32_t nth, double below, uint32_t before,
                                       int tid) {
-    uint32_t k0 = 0u, k1 = 0xFFFFFFFFu;
-    if (size > kCap) {  // the range of the bin's values
-        if (tid == 0) {
-            sh.key_lo = 0xFFFFFFFFu;
-            sh.key_hi = 0u;
-        }
-        __syncthreads();
-        uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-        each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = bin_y(w, x);
-            if (y >= 0.0 && y < (double)kBins && (int)y == bin) {
-                const uint32_t vk = value_key(x);
-                lo = min(lo, vk);
-                hi = max(hi, vk);
-            }
-        });
-        if (lo <= hi) {
-            atomicMin(&sh.key_lo, lo);
-            atomicMax(&sh.key_hi, hi);
-        }
-        __syncthreads();
-        k0 = sh.key_lo;
-        k1 = sh.key_hi;
-        __syncthreads();
-    }
+    Keys keys = keys_of(w, bin, bin, tid & (kWave - 1));
     // Split by value until a part is small or a single value; every step narrows the range to a
     // kParts-th of it or to one value.
-    while (size > kCap && k0 != k1) {
-        const int bits = 32 - __clz(k1 - k0);
+#pragma unroll 1
+    while (size > kCap && keys.lo != keys.hi) {
+        const int bits = 32 - __clz(keys.hi - keys.lo);
         const int shift = bits > 10 ? bits - 10 : 0;
         for (int b = tid; b < kParts; b += kThreads) {
             sh.part_mass[b] = 0ull;
             sh.part_count[b] = 0u;
         }
         __syncthreads();
+        const float lo = key_value(keys.lo), hi = key_value(keys.hi);
         each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = bin_y(w, x);
-            const uint32_t vk = value_key(x);
-            if (y >= 0.0 && y < (double)kBins && (int)y == bin && vk >= k0 && vk <= k1) {
-                const uint32_t part = (k1 - vk) >> shift;
+            if (x >= lo && x <= hi) {
+                const uint32_t part = (keys.hi - value_key(x)) >> shift;
                 atomicAdd((unsigned long long *)&sh.part_mass[part],
-                          (unsigned long long)fixed_fraction(w, y - (double)bin));
+                          (unsigned long long)fixed_fraction(w, bin_fraction(bin_z(w, x))));
                 atomicAdd(&sh.part_count[part], 1u);
             }
         });
@@ -712,15 +735,15 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
         before = sh.spot_count;
         size = sh.spot_size;
         __syncthreads();
-        k1 -= part << shift;
+        keys.hi -= part << shift;
         const uint32_t width = (1u << shift) - 1u;
-        k0 = k1 - k0 > width ? k1 - width : k0;
+        if (keys.hi - keys.lo > width) keys.lo = keys.hi - width;
     }
     if (size > kCap) {
-        const float value = key_value(k1);
+        const float value = key_value(keys.hi);
         return cut_equal(value, weight_of(w, value), size, cut, target, nth, below, before);
     }
-    const Listed l = gather(logits, ur, sh, w, bin, bin, k0, k1, tid);
+    const Listed l = gather(logits, ur, sh, w, keys, tid);
     Place p = cut_list(sh, l, cut, target, nth, below, before, tid);
     p.w = weight_of(w, p.value);
     return p;
@@ -740,11 +763,8 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         }
     };
     if (!(temperature > 0.f)) {
-        const Top top = row_top(logits, ur, sh, tid);
-        if (top.m == -INFINITY)
-            answer(-1, -INFINITY);
-        else
-            answer(first_of_top(logits, ur, top, sh, tid), 0.0);
+        const int32_t id = first_of_top(logits, ur, sh, tid);
+        answer(id, id < 0 ? -INFINITY : 0.0);
         return;
     }
     u32x4 a, b;
@@ -760,7 +780,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
             if (tid + (k < EV ? 0 : NT) < ur.nv) m = fmaxf(m, x[k]);
     }
     Weights w{0.f, kBinsPerE / (double)temperature, one, sh.scale, group_top(sh, m, tid),
-              (double)kHeadroom, 1.0};
+              (double)(kHeadroom - kBins / 2), 1.0};
 #pragma unroll 1
     for (;;) {
         for (int i = tid; i < kBins; i += kThreads) {
@@ -770,19 +790,19 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         __syncthreads();
         each(logits, ur, tid, a, b, [&](float x, int32_t) {
             m = fmaxf(m, x);
-            const double y = bin_y(w, x);
-            if (y >= 0.0 && y < (double)kBins) {  // (false for NaN and -inf)
-                const int i = (int)y;
+            const double z = bin_z(w, x);
+            if (has_bin(z)) {  // (false for NaN and -inf)
+                const int i = bin_of(z);
                 atomicAdd((unsigned long long *)&sh.mass[i],
-                          (unsigned long long)fixed_fraction(w, y - (double)i));
+                          (unsigned long long)fixed_fraction(w, bin_fraction(z)));
                 atomicAdd(&sh.count[i], 1u);
             }
         });
         w.m = group_top(sh, m, tid);
         // (nothing to weigh, or the maximum has its bin; a second time it always has)
-        if (!(fabsf(w.m) < INFINITY) || (w.ref > -INFINITY && bin_y(w, w.m) >= 0.0)) break;
+        if (!(fabsf(w.m) < INFINITY) || (w.ref > -INFINITY && has_bin(bin_z(w, w.m)))) break;
         w.ref = w.m;
-        w.shift = 0.0;
+        w.shift = kPerOctave - kBins / 2;  // an octave of bins above it stays empty
         first_vectors(logits, ur, tid, a, b);
     }
     if (w.m == -INFINITY) {  // nothing to draw
@@ -800,12 +820,10 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         answer(nth_equal(logits, ur, sh, tid, INFINITY, p.nth, n), -log(whole));
         return;
     }
-    if (w.ref == w.m) {
-        // (bins from 0 on, or `shift` on: powers of two apart, so equal tokens still weigh 1 each)
-        w.unit = ldexp(1.0, (int)w.shift / kPerOctave);
-    } else {
-        w.unit = exp2(bin_y(w, w.m) * (1.0 / kPerOctave));
-    }
+    // The maximum's weight is 1; where it is the reference itself, its bin is a whole number of octaves
+    // down, so that equal tokens weigh 1 each exactly.
+    const double top_z = bin_z(w, w.m) + kBins / 2;
+    w.unit = w.ref == w.m ? ldexp(1.0, (int)top_z / kPerOctave) : exp2(top_z * (1.0 / kPerOctave));
     const Level<kPer> all{sh.mass, sh.count, w.unit / one, true};
     const Bins h = sum_bins(sh, all, w, 0.0, 0u, tid);
 
@@ -816,7 +834,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;
     const bool by_weight = least > 0x1p-60;
     const int weight_bin =
-        by_weight ? min((int)(bin_y(w, w.m) - kPerOctave * log2(least)) + 1, kBins - 1) : kBins - 1;
+        by_weight ? min((int)(top_z - kPerOctave * log2(least)) + 2, kBins - 1) : kBins - 1;
     bool mass_inside = false;  // the nucleus ends in the bins up to `low`
     int low = by_weight ? weight_bin : kBins - 1;
     if (by_number) {
@@ -841,7 +859,8 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         upto = total;
     }
     if (upto <= kCap) {
-        const Listed l = gather(logits, ur, sh, w, 0, low, 0u, 0xFFFFFFFFu, tid);
+        const Keys keys{keys_of(w, low, low, tid & (kWave - 1)).lo, value_key(w.m)};
+        const Listed l = gather(logits, ur, sh, w, keys, tid);
         // (the list's weights are exact where equal tokens tie; the bins give only what lies below it)
         double z = 0.0;
 #pragma unroll
@@ -871,18 +890,17 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     // Cut by cut, each in its own bin; the draw is the last.
     double z = h.total, whole = h.total;
     if (by_weight) {
-        // all of the bins above those that the border can fall in, and what reaches it there
+        // the bins above the one that the border falls in, and of that one what reaches it
+        const float border = key_value(
+            first_key(tid & (kWave - 1), [&](float x) { return x >= w.m || weight_of(w, x) >= least; }));
+        const int bin = bin_of(bin_z(w, border));
         double part = 0.0;
         each(logits, ur, tid, [&](float x, int32_t) {
-            const double y = bin_y(w, x);
-            if (y >= 0.0 && y < (double)kBins && (int)y <= weight_bin && (int)y >= weight_bin - 2) {
-                const double v = weight_of(w, x);
-                if (v >= least) part += v;
-            }
+            if (x >= border && x <= w.m && bin_of(bin_z(w, x)) == bin) part += weight_of(w, x);
         });
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
-            if (tid * kPer + j < weight_bin - 2) part += all.mass(w, tid * kPer + j);
+            if (tid * kPer + j < bin) part += all.mass(w, tid * kPer + j);
         double sum;
         scan_mass(sh, part, tid, sum);
         whole = fmin(whole, sum);
