@@ -223,6 +223,11 @@ __device__ __forceinline__ T wave_running_sum(T v) {
     v += dpp_or_zero<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
     return v;
 }
+// A lane move (a DPP pattern in which every lane has a source).
+template <int kCtrl>
+__device__ __forceinline__ float lane_move(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kCtrl, 0xF, 0xF, true));
+}
 // The value of one lane (the same for the whole wave), in every lane.
 __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);

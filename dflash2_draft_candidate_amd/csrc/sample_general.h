@@ -150,6 +150,8 @@ static constexpr int kThreads = NT;
 static constexpr int kWaves = NT / kWave;
 static constexpr int kPer = kBins / NT;  // bins per thread
 static constexpr int kCap = NT;          // gathered tokens, one per thread
+static constexpr int kTops = sizeof(T) == 4 ? 4096 : 1;  // (bf16 rows come here rarely)
+static constexpr int kGroups = NT / 8;  // groups of an iteration of each: eight threads' vectors
 static constexpr int kParts = 1024;      // parts that a bin is split into
 
 struct Shared {
@@ -163,6 +165,9 @@ struct Shared {
     uint64_t part_mass[kParts];  // of a bin that is split
     uint32_t part_count[kParts];
     uint64_t list[kCap];
+    float tops[kTops];    // the groups' maxima (see each)
+    uint16_t hit[kTops];  // groups to look through
+    uint32_t hits;
     double scale[kPerOctave];  // 2^(-i/kPerOctave)
     double wave_mass[kWaves];
     uint32_t wave_count[kWaves];
@@ -239,9 +244,10 @@ static __device__ __forceinline__ void first_vectors(const T *logits, const Unit
     if (tid < ur.nv) a = p[tid];
     if (tid + NT < ur.nv) b = p[tid + NT];
 }
-template <typename F>
+// `group` is called after each pair of vectors, with the number of the pair.
+template <typename F, typename G>
 static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, u32x4 a,
-                                            u32x4 b, F &&f) {
+                                            u32x4 b, F &&f, G &&group) {
     const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
     const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
     auto one = [&](const u32x4 &v, int i) {
@@ -251,11 +257,13 @@ static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur
         for (int k = 0; k < EV; ++k) f(x[k], id0 + i * EV + k);
     };
 #pragma unroll 1
-    for (int i = tid; i < ur.nv; i += 2 * NT) {
+    for (int i0 = 0; i0 < ur.nv; i0 += 2 * NT) {
         // (past the end: the last vector once more, not looked at; the loads are not conditional)
+        const int i = i0 + tid;
         const u32x4 c = p[min(i + 2 * NT, ur.nv - 1)], d = p[min(i + 3 * NT, ur.nv - 1)];
-        one(a, i);
+        if (i < ur.nv) one(a, i);
         if (i + NT < ur.nv) one(b, i + NT);
+        group(i0 / (2 * NT));
         a = c;
         b = d;
     }
@@ -266,7 +274,7 @@ template <typename F>
 static __device__ __forceinline__ void each(const T *logits, const UnitRange &ur, int tid, F &&f) {
     u32x4 a, b;
     first_vectors(logits, ur, tid, a, b);
-    each(logits, ur, tid, a, b, f);
+    each(logits, ur, tid, a, b, f, [](int) {});
 }
 
 // The row's whole vectors, f(vector, index), with more in flight, for cheap f: those passes wait for
@@ -294,20 +302,6 @@ static __device__ __forceinline__ void each_vector(const T *logits, const UnitRa
         }
     }
 }
-template <typename F>
-static __device__ __forceinline__ void each_cheap(const T *logits, const UnitRange &ur, int tid,
-                                                  F &&f) {
-    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
-    each_vector(logits, ur, tid, [&](const u32x4 &v, int i) {
-        float x[EV];
-        Elem<T>::unpack(v, x);
-#pragma unroll
-        for (int k = 0; k < EV; ++k) f(x[k], id0 + i * EV + k);
-    });
-    const int64_t e = ragged_element(ur, tid);
-    if (e >= 0) f(Elem<T>::load(logits, e), (int32_t)(e - ur.g0));
-}
-
 // The largest of a value over the workgroup.
 static __device__ __forceinline__ float group_top(Shared &sh, float m, int tid) {
 #pragma unroll
@@ -562,18 +556,72 @@ static __device__ __forceinline__ Keys keys_of(const Weights &w, int b0, int b1,
     return k;
 }
 
-// Gathers the tokens with these keys (at most kCap, known from the histogram).
+// Whether the pass keeps the maxima of this row's groups.
+static __device__ __forceinline__ bool keeps_tops(const UnitRange &ur) {
+    return kTops > 1 && (ur.nv + 2 * NT - 1) / (2 * NT) * kGroups <= kTops;
+}
+
+// Gathers the tokens whose keys lie in `one` or `two` (at most kCap, known from the histogram). Only
+// groups whose maximum reaches the lowest of them can hold any; where those are few, the rest of the
+// row is not read again.
 static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange &ur, Shared &sh,
-                                         const Weights &w, const Keys &keys, int tid) {
-    const float lo = key_value(keys.lo), hi = key_value(keys.hi);
-    if (tid == 0) sh.listed = 0;
+                                         const Weights &w, const Keys &one, const Keys &two,
+                                         int tid) {
+    const float lo1 = key_value(one.lo), hi1 = key_value(one.hi);
+    const float lo2 = key_value(two.lo), hi2 = key_value(two.hi);
+    const float lo = fminf(lo1, lo2);  // (finite: keys of finite logits)
+    const int groups = (ur.nv + 2 * NT - 1) / (2 * NT) * kGroups;
+    const bool keep = keeps_tops(ur);
+    if (tid == 0) sh.listed = sh.hits = 0;
     __syncthreads();
-    each_cheap(logits, ur, tid, [&](float x, int32_t id) {
-        if (x >= lo && x <= hi) {
-            const uint32_t at = atomicAdd(&sh.listed, 1u);
-            if (at < kCap) sh.list[at] = cand_key(x, id);
+    if (keep) {
+        for (int g = tid; g < groups; g += NT)
+            if (sh.tops[g] >= lo) sh.hit[atomicAdd(&sh.hits, 1u)] = (uint16_t)g;
+        __syncthreads();
+    }
+    // (x lies in a range where the median of it and the range's ends is x itself; one branch a vector)
+    auto in = [&](float x) {
+        return __builtin_amdgcn_fmed3f(x, lo1, hi1) == x || __builtin_amdgcn_fmed3f(x, lo2, hi2) == x;
+    };
+    auto append = [&](float x, int32_t id) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kCap) sh.list[at] = cand_key(x, id);
+    };
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(logits) + ur.c0;
+    const int32_t id0 = (int32_t)(ur.c0 * EV - ur.g0);
+    auto take = [&](const u32x4 &v, int i) {
+        float x[EV];
+        Elem<T>::unpack(v, x);
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < EV; ++k) any |= in(x[k]);
+        if (any) {
+#pragma unroll
+            for (int k = 0; k < EV; ++k)
+                if (in(x[k])) append(x[k], id0 + i * EV + k);
         }
-    });
+    };
+    if (keep && (int)sh.hits * 2 < groups) {
+#pragma unroll 1
+        for (int h = tid / 8; h < (int)sh.hits; h += kGroups) {
+            const int g = sh.hit[h];
+            const int i = g / kGroups * 2 * NT + g % kGroups * 8 + (tid & 7);
+            u32x4 v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (i + u * NT < ur.nv) v[u] = p[i + u * NT];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (i + u * NT < ur.nv) take(v[u], i + u * NT);
+        }
+    } else {
+        each_vector(logits, ur, tid, take);
+    }
+    const int64_t e = ragged_element(ur, tid);
+    if (e >= 0) {
+        const float x = Elem<T>::load(logits, e);
+        if (in(x)) append(x, (int32_t)(e - ur.g0));
+    }
     __syncthreads();
     const int n = min((int)sh.listed, kCap);
     __syncthreads();
@@ -743,7 +791,7 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
         const float value = key_value(keys.hi);
         return cut_equal(value, weight_of(w, value), size, cut, target, nth, below, before);
     }
-    const Listed l = gather(logits, ur, sh, w, keys, tid);
+    const Listed l = gather(logits, ur, sh, w, keys, keys, tid);
     Place p = cut_list(sh, l, cut, target, nth, below, before, tid);
     p.w = weight_of(w, p.value);
     return p;
@@ -781,6 +829,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     }
     Weights w{0.f, kBinsPerE / (double)temperature, one, sh.scale, group_top(sh, m, tid),
               (double)(kHeadroom - kBins / 2), 1.0};
+    const bool keep = keeps_tops(ur);
 #pragma unroll 1
     for (;;) {
         for (int i = tid; i < kBins; i += kThreads) {
@@ -788,16 +837,30 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
             sh.count[i] = 0u;
         }
         __syncthreads();
-        each(logits, ur, tid, a, b, [&](float x, int32_t) {
-            m = fmaxf(m, x);
-            const double z = bin_z(w, x);
-            if (has_bin(z)) {  // (false for NaN and -inf)
-                const int i = bin_of(z);
-                atomicAdd((unsigned long long *)&sh.mass[i],
-                          (unsigned long long)fixed_fraction(w, bin_fraction(z)));
-                atomicAdd(&sh.count[i], 1u);
-            }
-        });
+        float pair = -INFINITY;
+        each(
+            logits, ur, tid, a, b,
+            [&](float x, int32_t) {
+                pair = fmaxf(pair, x);
+                const double z = bin_z(w, x);
+                if (has_bin(z)) {  // (false for NaN and -inf)
+                    const int i = bin_of(z);
+                    atomicAdd((unsigned long long *)&sh.mass[i],
+                              (unsigned long long)fixed_fraction(w, bin_fraction(z)));
+                    atomicAdd(&sh.count[i], 1u);
+                }
+            },
+            [&](int number) {
+                m = fmaxf(m, pair);
+                if (keep) {
+                    pair = fmaxf(pair, lane_move<kDppQuadXor1>(pair));
+                    pair = fmaxf(pair, lane_move<kDppQuadXor2>(pair));
+                    pair = fmaxf(pair, lane_move<0x141>(pair));  // row_half_mirror
+                    if ((tid & 7) == 0) sh.tops[number * kGroups + tid / 8] = pair;
+                }
+                pair = -INFINITY;
+            });
+        m = fmaxf(m, pair);  // (of the ragged ends)
         w.m = group_top(sh, m, tid);
         // (nothing to weigh, or the maximum has its bin; a second time it always has)
         if (!(fabsf(w.m) < INFINITY) || (w.ref > -INFINITY && has_bin(bin_z(w, w.m)))) break;
@@ -860,7 +923,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     }
     if (upto <= kCap) {
         const Keys keys{keys_of(w, low, low, tid & (kWave - 1)).lo, value_key(w.m)};
-        const Listed l = gather(logits, ur, sh, w, keys, tid);
+        const Listed l = gather(logits, ur, sh, w, keys, keys, tid);
         // (the list's weights are exact where equal tokens tie; the bins give only what lies below it)
         double z = 0.0;
 #pragma unroll
@@ -904,6 +967,54 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         double sum;
         scan_mass(sh, part, tid, sum);
         whole = fmin(whole, sum);
+    }
+    if (by_mass && !by_number) {
+        // The nucleus' end and the draw, gathered in one pass: the kept mass is known to within the
+        // end's bin, and with it where the draw can fall.
+        const double target = (double)top_p * z;
+        find_bin(sh, all, w, h, kReach, target, 0u, tid);
+        const int end = sh.spot_bin;
+        const double end_below = sh.spot_mass;
+        const uint32_t end_before = sh.spot_count, end_size = sh.spot_size;
+        __syncthreads();
+        find_bin(sh, all, w, h, kPass, u * fmin(whole, end_below), 0u, tid);
+        const int from = sh.spot_bin;
+        const double from_below = sh.spot_mass;
+        const uint32_t from_before = sh.spot_count;
+        __syncthreads();
+        find_bin(sh, all, w, h, kPass, u * fmin(whole, end_below + all.mass(w, end)), 0u, tid);
+        const int to = sh.spot_bin;
+        const uint32_t to_before = sh.spot_count + sh.spot_size;
+        __syncthreads();
+        const bool apart = to < end;  // otherwise one run of bins, from `from` to `end`
+        const uint32_t drawn = apart ? to_before - from_before : 0u;  // tokens of the draw's bins
+        const uint32_t in_all =
+            apart ? drawn + end_size : end_before + end_size - min(from_before, end_before);
+        if (in_all <= kCap) {
+            const int lane = tid & (kWave - 1);
+            const Keys tail = keys_of(w, apart ? end : min(from, end), end, lane);
+            const Keys head = apart ? keys_of(w, from, to, lane) : tail;
+            const Listed l = gather(logits, ur, sh, w, head, tail, tid);
+            // the running mass of this thread's token in the row
+            if (tid == (int)drawn) sh.spot_mass = l.below;
+            __syncthreads();
+            const double split = sh.spot_mass;
+            __syncthreads();
+            const double s = apart && tid >= (int)drawn ? end_below + (l.below - split) + l.w
+                                                        : fmin(from_below, end_below) + l.below + l.w;
+            int at = min(first_thread(sh, tid >= (int)drawn && tid < l.n && s >= target, tid), l.n - 1);
+            if (tid == at) sh.spot_mass = s;
+            __syncthreads();
+            whole = fmin(whole, sh.spot_mass);
+            __syncthreads();
+            const int last = apart ? (int)drawn : l.n;
+            at = min(first_thread(sh, tid < last && s > u * whole, tid), last - 1);
+            if (tid == at) {
+                *token = key_id(l.key);
+                if (logprob) *logprob = (float)log(l.w / whole);
+            }
+            return;
+        }
     }
     Place p;
 #pragma unroll 1
