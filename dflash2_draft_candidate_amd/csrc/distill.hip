@@ -37,6 +37,7 @@ constexpr int kU = kStreamVectors;
 constexpr float kMaxRef = 8388608.f;  // 2^23: references stay within this, so each is within 0.5
                                       // of m s and 2^(m s - ref) cannot overflow
 constexpr float kNoRef = -kMaxRef;    // reference before the first element
+constexpr int kBufferWord3 = 0x00020000;  // gfx9-family buffer descriptor word 3 (raw data)
 constexpr int kUnitVectors = 2 * kThreads;  // a slice holds at least this many vectors
 
 // ---- element output ------------------------------------------------------------------------
@@ -177,6 +178,19 @@ __device__ __forceinline__ Stat wave_stat(Stat st) {
     return st;
 }
 
+// The threads' statistics joined, in every thread.
+template <int NT>
+__device__ __forceinline__ Stat group_stat(Stat st, Stat *sh, int tid) {
+    st = wave_stat(st);
+    if ((tid & (kWave - 1)) == 0) sh[tid / kWave] = st;
+    __syncthreads();
+    st = sh[0];
+#pragma unroll
+    for (int w = 1; w < NT / kWave; ++w) stat_join(st, sh[w]);
+    __syncthreads();
+    return st;
+}
+
 // Statistics of a unit, in every thread. `sh` is scratch of kWaves entries; ends with a barrier.
 template <typename T, int NT>
 __device__ __forceinline__ Stat unit_stat(const T *student, const UnitRange &ur, float s, Stat *sh,
@@ -201,14 +215,7 @@ __device__ __forceinline__ Stat unit_stat(const T *student, const UnitRange &ur,
         const float x = Elem<T>::load(student, e);
         stat_add<1>(st, &x, s);
     }
-    st = wave_stat(st);
-    if ((tid & (kWave - 1)) == 0) sh[tid / kWave] = st;
-    __syncthreads();
-    st = sh[0];
-#pragma unroll
-    for (int w = 1; w < NT / kWave; ++w) stat_join(st, sh[w]);
-    __syncthreads();
-    return st;
+    return group_stat<NT>(st, sh, tid);
 }
 
 // Sigma of a whole row without a usable reference, by one wave: the sum of exp2((z - m) s), 64
@@ -425,6 +432,145 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(
     if (patch.id >= 0) Pack<T>::one(grad + row * a.V + patch.id, patch.value);
 }
 
+// Statistics and gradient of long rows: a row per workgroup of 1024 threads, NV vectors of it per thread
+// held in registers between the two passes, so that they come from memory once. What does not fit
+// (`rest`: the row's first vectors) is streamed and read again. All fp32, and without the teacher's
+// entries: the fp64 work for those (distill_finish_kernel) would cost the registers that hold the row.
+constexpr int kHeld = 1024;
+template <typename T, int NV>
+__global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict__ student, Args a,
+                                                             const float *__restrict__ grad_loss,
+                                                             Stat *__restrict__ stats,
+                                                             T *__restrict__ grad) {
+    constexpr int EV = Elem<T>::kPerVec;
+    __shared__ Stat sh[kHeld / kWave];
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const UnitRange ur = unit_range(row, a.V, 1, EV);
+    const int rest = max(ur.nv - NV * kHeld, 0), held = ur.nv - rest;
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(student) + ur.c0 + rest;
+    u32x4 *out = reinterpret_cast<u32x4 *>(grad) + ur.c0 + rest;
+    // (buffer accesses: one offset register for all vectors, and what lies past the row's end is
+    // not stored)
+    const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<u32x4 *>(p), 0, held * 16, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t dst =
+        __builtin_amdgcn_make_buffer_rsrc(out, 0, held * 16, kBufferWord3);
+    u32x4 v[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        v[j] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, tid * 16, j * kHeld * 16, 0));
+    const int64_t e = ragged_element(ur, tid);
+    const float end = e >= 0 ? Elem<T>::load(student, e) : -INFINITY;
+    const float g = grad_loss[row];
+    const bool any = teacher_any(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, tid & (kWave - 1));
+    Stat st{-INFINITY, kNoRef, 0.f};
+    // f(elements of vectors j, j + 1; how many of the two the row has) over the held vectors
+    auto pairs = [&](auto &&f) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 2) {
+            // (a new value to the compiler: it would keep the widened logits from pass to pass, twice
+            // the registers, to save widening them again; and unpacked ahead of their turn they
+            // would not fit either)
+            asm("" : "+v"(v[j]), "+v"(v[j + 1]));
+            float x[2 * EV];
+            Elem<T>::unpack(v[j], x);
+            Elem<T>::unpack(v[j + 1], x + EV);
+            f(j, x, tid + (j + 1) * kHeld < held ? 2 : tid + j * kHeld < held ? 1 : 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    pairs([&](int, const float *x, int n) {
+        if (n == 2)
+            stat_add<2 * EV>(st, x, a.s);
+        else if (n == 1)
+            stat_add<EV>(st, x, a.s);
+    });
+    for (int i = tid - rest; i < 0; i += kHeld) {
+        float x[EV];
+        Elem<T>::unpack(p[i], x);
+        stat_add<EV>(st, x, a.s);
+    }
+    if (e >= 0) stat_add<1>(st, &end, a.s);
+    st = group_stat<kHeld>(st, sh, tid);
+    if (tid == 0) stats[row] = st;
+    const float m = st.m;
+    float sigma = st.sum * __builtin_amdgcn_exp2f(__builtin_fmaf(-m, a.s, st.ref));
+    if (m > -INFINITY && !(fabsf(m * a.s) < kMaxRef)) {  // no reference: from the differences
+        Stat far{m, 0.f, 0.f};
+        auto add = [&](float x) { far.sum += __builtin_amdgcn_exp2f((x - m) * a.s); };
+        pairs([&](int, const float *x, int n) {
+#pragma unroll
+            for (int k = 0; k < 2 * EV; ++k)
+                if (k < n * EV) add(x[k]);
+        });
+        for (int i = tid - rest; i < 0; i += kHeld) {
+            float x[EV];
+            Elem<T>::unpack(p[i], x);
+#pragma unroll
+            for (int k = 0; k < EV; ++k) add(x[k]);
+        }
+        if (e >= 0) add(end);
+        sigma = group_stat<kHeld>(far, sh, tid).sum;
+    }
+    // (nothing above -inf: the sum is 0, or NaN if the row holds one)
+    const bool live = any && (m > -INFINITY || st.sum != st.sum);
+    const float coef = live ? g * (float)a.tau / sigma : 0.f;
+    auto gradient = [&](float *x) {
+#pragma unroll
+        for (int k = 0; k < EV; ++k)
+            x[k] = live ? coef * __builtin_amdgcn_exp2f((x[k] - m) * a.s) : 0.f;
+        return Pack<T>::vec(x);
+    };
+    pairs([&](int j, float *x, int) {
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(x), dst, tid * 16, j * kHeld * 16, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(x + EV), dst, tid * 16,
+                                               (j + 1) * kHeld * 16, 0);
+    });
+    for (int i = tid - rest; i < 0; i += kHeld) {
+        float x[EV];
+        Elem<T>::unpack(p[i], x);
+        out[i] = gradient(x);
+    }
+    if (e >= 0)
+        Pack<T>::one(grad + e, live ? coef * __builtin_amdgcn_exp2f((end - m) * a.s) : 0.f);
+}
+
+// The loss of a row, and its gradient at the teacher's ids: one wave per row, after
+// distill_held_kernel.
+template <typename T>
+__global__ __launch_bounds__(kWave) void distill_finish_kernel(const T *__restrict__ student,
+                                                               Args a,
+                                                               const float *__restrict__ grad_loss,
+                                                               const Stat *__restrict__ stats,
+                                                               float *__restrict__ loss,
+                                                               T *__restrict__ grad) {
+    const int lane = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const Stat st = stats[row];
+    const Teacher t = teacher_row(a.ids, a.teacher, row, a.K, a.V, a.inv_tau, lane);
+    const double sigma = row_sigma<T>(st, student, row, a.V, a.s, lane);
+    const double l = row_loss<T>(t, student, row, a.V, (double)st.m, sigma, a.tau);
+    if (lane == 0) loss[row] = (float)l;
+    const Patch patch = teacher_patch<T>(t, student, row, a.V, a.K, (double)st.m, sigma,
+                                         (double)grad_loss[row], a.tau, lane);
+    if (patch.id >= 0) Pack<T>::one(grad + row * a.V + patch.id, patch.value);
+}
+
+template <typename T, int NV>
+hipError_t held(const T *x, const Args &a, const float *grad_loss, float *loss, T *grad, void *ws,
+                hipStream_t stream) {
+    Stat *stats = static_cast<Stat *>(ws);
+    hipLaunchKernelGGL((distill_held_kernel<T, NV>), dim3((unsigned)a.R), dim3(kHeld), 0, stream, x,
+                       a, grad_loss, stats, grad);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((distill_finish_kernel<T>), dim3((unsigned)a.R), dim3(kWave), 0, stream, x, a,
+                       grad_loss, stats, loss, grad);
+    return hipGetLastError();
+}
+
 Args make_args(const int32_t *ids, const float *teacher, int R, int V, int K, float tau) {
     Args a;
     a.ids = ids;
@@ -479,9 +625,14 @@ hipError_t step(const void *student, const Args &a, const float *grad_loss, floa
                 void *ws, hipStream_t stream) {
     const int S = plan_slices(a.R, a.V, (int)sizeof(T));
     if (S == 1) {
+        const T *x = static_cast<const T *>(student);
+        T *out = static_cast<T *>(grad);
+        const int64_t per_thread = (int64_t)a.V * (int)sizeof(T) / 16 / kHeld;  // vectors, rounded down
+        if (per_thread >= 16) return held<T, 20>(x, a, grad_loss, loss, out, ws, stream);
+        if (per_thread >= 8) return held<T, 16>(x, a, grad_loss, loss, out, ws, stream);
+        if (per_thread >= 4) return held<T, 8>(x, a, grad_loss, loss, out, ws, stream);
         hipLaunchKernelGGL((distill_step_kernel<T>), dim3((unsigned)a.R), dim3(kThreads), 0, stream,
-                           static_cast<const T *>(student), a, grad_loss, loss,
-                           static_cast<T *>(grad));
+                           x, a, grad_loss, loss, out);
         return hipGetLastError();
     }
     float *row_stats = static_cast<float *>(ws);
@@ -495,7 +646,7 @@ hipError_t step(const void *student, const Args &a, const float *grad_loss, floa
 
 size_t distill_workspace_bytes(int R, int V, int elem_bytes) {
     const int S = plan_slices(R, V, elem_bytes);
-    if (S == 1) return 0;
+    if (S == 1) return align256((size_t)R * sizeof(Stat));  // of distill_held_kernel
     return align256((size_t)R * 2 * sizeof(float)) + align256((size_t)R * S * sizeof(Stat));
 }
 

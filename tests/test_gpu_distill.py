@@ -202,6 +202,55 @@ def test_not_a_number(d2, R, V, dt):
         check(loss[good], grad[good], tuple(x[good] for x in ref), V, 1.0, g[good], dtype)
 
 
+@pytest.mark.parametrize("V,dt", [(40000, "bf16"), (70011, "bf16"), (140001, "bf16"),
+                                  (180003, "bf16"), (20003, "f32"), (40001, "f32"), (66666, "f32"),
+                                  (90007, "f32")])
+def test_long_rows(d2, V, dt):
+    """Many long rows (held in registers between the passes, wholly or in part): a few rows of each
+    kind against the formulas, the others against the two calls."""
+    log(f"distill long rows V={V} {dt}")
+    dtype = torch.float32 if dt == "f32" else torch.bfloat16
+    R, K, tau = 1024, 9, 1.5
+    gen = torch.Generator(device=DEV).manual_seed(V)
+    z = (torch.randn(R, V, generator=gen, device=DEV) * 3).to(dtype)
+    ids = (torch.arange(K, device=DEV) * (V // K) +
+           torch.randint(0, V // K, (R, K), generator=gen, device=DEV)).int()
+    t = torch.randn(R, K, generator=gen, device=DEV)
+    g = torch.rand(R, generator=gen, device=DEV) - 0.5
+    inf, low = math.inf, torch.finfo(dtype).min
+    ids[1] = -1
+    ids[2, 4:] = ids[2, 0]
+    z[3, V // 3:] = -inf
+    z[4] = -inf
+    z[5] = low
+    z[6, :V // 2] = low
+    z[7] = z[7].abs() * 1e37
+    z[8, V - 2] = math.nan
+    z[9, 1] = inf
+    z[10] = -inf
+    z[10, V // 2] = math.nan
+    ids[11, 0], ids[11, 1] = 0, V - 1
+    z[12] = z[12] * 1e7                    # no reference, but no mask either
+    loss, grad = d2.distill_step(z, ids, t, g, tau)
+    rows = [0, 1, 2, 3, 4, 5, 6, 7, 11, 12, 511, 1023]
+    ref = reference(z[rows], ids[rows], t[rows], g[rows], tau)
+    check(loss[rows], grad[rows], ref, V, tau, g[rows], dtype)
+    bad = [8, 9, 10]
+    assert bool(torch.isnan(loss[bad]).all()) and bool(torch.isnan(grad[bad]).any(dim=1).all())
+    two, stats = d2.distill(z, ids, t, tau)
+    grad2 = d2.distill_backward(z, ids, t, stats, g, tau)
+    good = [r for r in range(R) if r not in bad]
+    fin = torch.isfinite(two)
+    assert torch.equal(fin, torch.isfinite(loss))
+    tol = 2 * (tau * tau * eps_sigma(V) + U * two[fin].abs())
+    assert bool(((loss[fin] - two[fin]).abs() <= tol).all())
+    half = U if dt == "f32" else 2.0 ** -8
+    # both sides within their tolerance of the formula: |q - p| <= 1, q <= 1
+    lim = 2 * (g.abs() * tau)[:, None] * (eps_sigma(V) + 200 * U) + \
+        2 * half * torch.maximum(grad.float().abs(), grad2.float().abs())
+    assert bool(((grad.float() - grad2.float()).abs() <= lim)[good].all())
+
+
 def test_gradient_against_differences(d2):
     """Central differences of the 64-bit loss at a step of 1e-5: off by O(h^2) = 1e-10 of the third
     derivative (below tau^-1) and 1e-16 / h of the loss."""
