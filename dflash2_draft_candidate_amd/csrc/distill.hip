@@ -38,6 +38,8 @@ constexpr float kMaxRef = 8388608.f;  // 2^23: references stay within this, so e
                                       // of m s and 2^(m s - ref) cannot overflow
 constexpr float kNoRef = -kMaxRef;    // reference before the first element
 constexpr int kBufferWord3 = 0x00020000;  // gfx9-family buffer descriptor word 3 (raw data)
+constexpr int kHeldRows = 128;   // rows from which on a step holds a row in a workgroup's registers
+constexpr int kShortRow = 1024;  // vectors up to which a step reads its row twice
 constexpr int kUnitVectors = 2 * kThreads;  // a slice holds at least this many vectors
 
 // ---- element output ------------------------------------------------------------------------
@@ -432,22 +434,21 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(
     if (patch.id >= 0) Pack<T>::one(grad + row * a.V + patch.id, patch.value);
 }
 
-// Statistics and gradient of long rows: a row per workgroup of 1024 threads, NV vectors of it per thread
+// Statistics and gradient of long rows: a row per workgroup of NT threads, NV vectors of it per thread
 // held in registers between the two passes, so that they come from memory once. What does not fit
 // (`rest`: the row's first vectors) is streamed and read again. All fp32, and without the teacher's
 // entries: the fp64 work for those (distill_finish_kernel) would cost the registers that hold the row.
-constexpr int kHeld = 1024;
-template <typename T, int NV>
-__global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict__ student, Args a,
+template <typename T, int NT, int NV>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void distill_held_kernel(const T *__restrict__ student, Args a,
                                                              const float *__restrict__ grad_loss,
                                                              Stat *__restrict__ stats,
                                                              T *__restrict__ grad) {
     constexpr int EV = Elem<T>::kPerVec;
-    __shared__ Stat sh[kHeld / kWave];
+    __shared__ Stat sh[NT / kWave];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const UnitRange ur = unit_range(row, a.V, 1, EV);
-    const int rest = max(ur.nv - NV * kHeld, 0), held = ur.nv - rest;
+    const int rest = max(ur.nv - NV * NT, 0), held = ur.nv - rest;
     const u32x4 *p = reinterpret_cast<const u32x4 *>(student) + ur.c0 + rest;
     u32x4 *out = reinterpret_cast<u32x4 *>(grad) + ur.c0 + rest;
     // (buffer accesses: one offset register for all vectors, and what lies past the row's end is
@@ -460,7 +461,7 @@ __global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         v[j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, tid * 16, j * kHeld * 16, 0));
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, tid * 16, j * NT * 16, 0));
     const int64_t e = ragged_element(ur, tid);
     const float end = e >= 0 ? Elem<T>::load(student, e) : -INFINITY;
     const float g = grad_loss[row];
@@ -477,7 +478,7 @@ __global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict
             float x[2 * EV];
             Elem<T>::unpack(v[j], x);
             Elem<T>::unpack(v[j + 1], x + EV);
-            f(j, x, tid + (j + 1) * kHeld < held ? 2 : tid + j * kHeld < held ? 1 : 0);
+            f(j, x, tid + (j + 1) * NT < held ? 2 : tid + j * NT < held ? 1 : 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -487,13 +488,13 @@ __global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict
         else if (n == 1)
             stat_add<EV>(st, x, a.s);
     });
-    for (int i = tid - rest; i < 0; i += kHeld) {
+    for (int i = tid - rest; i < 0; i += NT) {
         float x[EV];
         Elem<T>::unpack(p[i], x);
         stat_add<EV>(st, x, a.s);
     }
     if (e >= 0) stat_add<1>(st, &end, a.s);
-    st = group_stat<kHeld>(st, sh, tid);
+    st = group_stat<NT>(st, sh, tid);
     if (tid == 0) stats[row] = st;
     const float m = st.m;
     float sigma = st.sum * __builtin_amdgcn_exp2f(__builtin_fmaf(-m, a.s, st.ref));
@@ -505,14 +506,14 @@ __global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict
             for (int k = 0; k < 2 * EV; ++k)
                 if (k < n * EV) add(x[k]);
         });
-        for (int i = tid - rest; i < 0; i += kHeld) {
+        for (int i = tid - rest; i < 0; i += NT) {
             float x[EV];
             Elem<T>::unpack(p[i], x);
 #pragma unroll
             for (int k = 0; k < EV; ++k) add(x[k]);
         }
         if (e >= 0) add(end);
-        sigma = group_stat<kHeld>(far, sh, tid).sum;
+        sigma = group_stat<NT>(far, sh, tid).sum;
     }
     // (nothing above -inf: the sum is 0, or NaN if the row holds one)
     const bool live = any && (m > -INFINITY || st.sum != st.sum);
@@ -524,11 +525,14 @@ __global__ __launch_bounds__(kHeld) void distill_held_kernel(const T *__restrict
         return Pack<T>::vec(x);
     };
     pairs([&](int j, float *x, int) {
-        __builtin_amdgcn_raw_buffer_store_b128(gradient(x), dst, tid * 16, j * kHeld * 16, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(gradient(x + EV), dst, tid * 16,
-                                               (j + 1) * kHeld * 16, 0);
+        // The vector's place is part of the vector offset, not a scalar offset: after a 16-byte
+        // store with a scalar offset the compiler lets the next instruction overwrite the first
+        // stored register, and stores with a logit difference in that word have been seen.
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(x), dst, (tid + j * NT) * 16, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(x + EV), dst, (tid + (j + 1) * NT) * 16, 0,
+                                               0);
     });
-    for (int i = tid - rest; i < 0; i += kHeld) {
+    for (int i = tid - rest; i < 0; i += NT) {
         float x[EV];
         Elem<T>::unpack(p[i], x);
         out[i] = gradient(x);
@@ -558,11 +562,11 @@ __global__ __launch_bounds__(kWave) void distill_finish_kernel(const T *__restri
     if (patch.id >= 0) Pack<T>::one(grad + row * a.V + patch.id, patch.value);
 }
 
-template <typename T, int NV>
+template <typename T, int NT, int NV>
 hipError_t held(const T *x, const Args &a, const float *grad_loss, float *loss, T *grad, void *ws,
                 hipStream_t stream) {
     Stat *stats = static_cast<Stat *>(ws);
-    hipLaunchKernelGGL((distill_held_kernel<T, NV>), dim3((unsigned)a.R), dim3(kHeld), 0, stream, x,
+    hipLaunchKernelGGL((distill_held_kernel<T, NT, NV>), dim3((unsigned)a.R), dim3(NT), 0, stream, x,
                        a, grad_loss, stats, grad);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -624,13 +628,20 @@ template <typename T>
 hipError_t step(const void *student, const Args &a, const float *grad_loss, float *loss, void *grad,
                 void *ws, hipStream_t stream) {
     const int S = plan_slices(a.R, a.V, (int)sizeof(T));
-    if (S == 1) {
+    if (S == 1 || a.R >= kHeldRows) {
         const T *x = static_cast<const T *>(student);
         T *out = static_cast<T *>(grad);
-        const int64_t per_thread = (int64_t)a.V * (int)sizeof(T) / 16 / kHeld;  // vectors, rounded down
-        if (per_thread >= 16) return held<T, 20>(x, a, grad_loss, loss, out, ws, stream);
-        if (per_thread >= 8) return held<T, 16>(x, a, grad_loss, loss, out, ws, stream);
-        if (per_thread >= 4) return held<T, 8>(x, a, grad_loss, loss, out, ws, stream);
+        // the smallest shape that holds the row (at most 128 registers a thread: 1024 threads a CU)
+        const int n = (int)((int64_t)a.V * (int)sizeof(T) / 16);  // vectors of a row
+        if (n > 16 * 1024) return held<T, 1024, 20>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 12 * 1024) return held<T, 1024, 16>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 20 * 512) return held<T, 1024, 12>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 16 * 512) return held<T, 512, 20>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 12 * 512) return held<T, 512, 16>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 20 * 256) return held<T, 512, 12>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 16 * 256) return held<T, 256, 20>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > 12 * 256) return held<T, 256, 16>(x, a, grad_loss, loss, out, ws, stream);
+        if (n > kShortRow) return held<T, 256, 12>(x, a, grad_loss, loss, out, ws, stream);
         hipLaunchKernelGGL((distill_step_kernel<T>), dim3((unsigned)a.R), dim3(kThreads), 0, stream,
                            x, a, grad_loss, loss, out);
         return hipGetLastError();
