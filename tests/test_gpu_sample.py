@@ -1,10 +1,11 @@
 """Sampling from whole rows of logits vs a plain implementation in 64 bits (needs an MI355X).
 
 The reference sorts a row (logit descending, id ascending), sums its weights in 64 bits and applies
-the definition. A weight on the GPU errs by at most 2^-42 of itself (half a step of its 41-bit second
-factor, which is at least 0.98) + 2^-46 (the product y < 4096 in fp64, the polynomial): below 2^-41; a
-running sum errs by no more than that of itself, and its comparison with a cut (a product with a sum
-that errs as much, or with two) by less than 2^-38 of the row's mass. So:
+the definition. A weight on the GPU errs by at most, relative to itself: half a step of its 41-bit
+second factor, which is at least 0.989 (2^-41.98), the polynomial of that factor (2^-42.5; bf16 rows
+multiply two of them and have no fixed-point step) and the fp64 roundings of its argument (below 4096,
+2^-46): below 2^-41 in all. A running sum errs by no more than that of itself, and its comparison with a
+cut (a product with a sum that errs as much, or with two) by less than 2^-38 of the row's mass. So:
   * the token is the reference's, unless a cut or the draw lies within 2^-38 of the mass of a
     running sum, where either neighbour's answer is right; the inputs below have no such place
     (asserted: `clear`), but for runs of equal largest logits, whose sums are whole numbers and exact
@@ -220,6 +221,46 @@ def test_a_value_more_often_than_a_half_word_counts(d2, R, V):
     ids, lp = d2.sample(x, u)
     assert ids.tolist() == [int(v * V) for v in u.double().tolist()]
     assert float((lp.double() + math.log(V)).abs().max()) <= 2.0 ** -37 + 2.0 ** -24 * math.log(V)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_late_maximum(d2, dt):
+    """Rows whose first logits say little of their maximum: masked, far below it, just below the bins'
+    headroom, or NaN; the bf16 rows hold a large logit, which sends them the same way."""
+    V, inf = 40000, math.inf
+    x, u = rows(8, V, "f32", 71)
+    x[0, :30000] = -inf
+    x[1, 39000] = 60.0                 # far above everything
+    x[2, 39000:39005] = 45.0
+    x[3, :20000] -= 40.0
+    x[4, :39999] = -inf
+    x[5, :9000] = math.nan
+    x[6] = -x[6].abs() * 100           # steep, all negative
+    x[7, 20000:] += 25.0
+    if dt == "bf16":
+        x = x.to(torch.bfloat16)
+        x[:, 17] = 300.0
+        x[4, 17] = -inf
+    else:
+        x = x.float()
+    for i, s in enumerate([dict(), dict(T=0.5), dict(T=0.05, p=0.9), dict(T=1.4, p=0.97),
+                           dict(T=2.0, k=2000, p=0.9), dict(T=3.0, m=0.05), dict(T=20.0, p=0.8),
+                           dict(T=40.0, m=0.2, p=0.6), dict(T=0.0)]):
+        check(d2, x, [(v + 0.31 * i) % 1.0 for v in u], **s)
+
+
+def test_very_long_rows(d2):
+    """More groups than their maxima are kept for, in both types."""
+    V = 600011
+    for dt in ("f32", "bf16"):
+        x, u = rows(2, V, dt, 91)
+        for s in (dict(), dict(p=0.9), dict(k=30), dict(T=0.0), dict(T=2.0, m=0.01)):
+            check(d2, x, u, **s)
+    x, u = rows(1, V, "bf16", 93)
+    x = x.repeat(256, 1)               # a row per workgroup
+    ids, _ = d2.sample(x.to(DEV), torch.tensor(u * 256, device=DEV), top_p=0.99)
+    want, _, clear = reference_row(x[0].double().numpy(), 1.0, 0, f32(0.99), 0.0, f32(u[0]))
+    assert clear and ids.tolist() == [want] * 256
 
 
 def test_extreme_settings(d2):
