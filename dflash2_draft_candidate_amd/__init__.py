@@ -445,6 +445,7 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor,
     _same_device(dev, uniforms)
     t, t_all = _setting(temperature, torch.float32, R, "temperature", logits)
     k, k_all = _setting(top_k, torch.int32, R, "top_k", logits)
+    k_all = max(-1, min(int(k_all), 2 ** 31 - 1))  # (as a C int: any larger value is no cut)
     p, p_all = _setting(top_p, torch.float32, R, "top_p", logits)
     m, m_all = _setting(min_p, torch.float32, R, "min_p", logits)
     if out is None:
@@ -460,7 +461,7 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor,
     ws = _workspace(_lib.dflash2_sample_workspace_bytes(R, V, dt), dev)
     with _on(dev):
         rc = _lib.dflash2_sample(_ptr(logits), dt, R, V, _ptr(t), float(t_all), _ptr(k),
-                                 int(k_all), _ptr(p), float(p_all), _ptr(m), float(m_all),
+                                 k_all, _ptr(p), float(p_all), _ptr(m), float(m_all),
                                  _ptr(uniforms), _ptr(token_ids), _ptr(logprob), _ptr(ws),
                                  ws.numel(), _stream(dev))
     _check(rc, "dflash2_sample")

@@ -220,14 +220,21 @@ __device__ __forceinline__ Stat unit_stat(const T *student, const UnitRange &ur,
     return group_stat<NT>(st, sh, tid);
 }
 
-// Sigma of a whole row without a usable reference, by one wave: the sum of exp2((z - m) s), 64
-// elements at a time.
+// Sigma of a whole row without a usable reference, by one wave: the sum of exp2((z - m) s).
 template <typename T>
 __device__ __noinline__ double far_row_sum(const T *student, int64_t row, int V, float m, float s,
                                            int lane) {
     double sum = 0.0;
-    for (int v = lane; v < V; v += kWave)
-        sum += (double)__builtin_amdgcn_exp2f((Elem<T>::load(student, row * V + v) - m) * s);
+    constexpr int kAhead = 16;  // loads in flight per lane
+    for (int v0 = lane; v0 < V; v0 += kAhead * kWave) {
+        float x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            x[u] = Elem<T>::load(student, row * V + min(v0 + u * kWave, V - 1));
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (v0 + u * kWave < V) sum += (double)__builtin_amdgcn_exp2f((x[u] - m) * s);
+    }
     return wave_sum64(sum);
 }
 
@@ -439,10 +446,9 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(
 // (`rest`: the row's first vectors) is streamed and read again. All fp32, and without the teacher's
 // entries: the fp64 work for those (distill_finish_kernel) would cost the registers that hold the row.
 template <typename T, int NT, int NV>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void distill_held_kernel(const T *__restrict__ student, Args a,
-                                                             const float *__restrict__ grad_loss,
-                                                             Stat *__restrict__ stats,
-                                                             T *__restrict__ grad) {
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void
+distill_held_kernel(const T *__restrict__ student, Args a, const float *__restrict__ grad_loss,
+                    Stat *__restrict__ stats, T *__restrict__ grad) {
     constexpr int EV = Elem<T>::kPerVec;
     __shared__ Stat sh[NT / kWave];
     const int tid = threadIdx.x;
@@ -451,8 +457,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
     const int rest = max(ur.nv - NV * NT, 0), held = ur.nv - rest;
     const u32x4 *p = reinterpret_cast<const u32x4 *>(student) + ur.c0 + rest;
     u32x4 *out = reinterpret_cast<u32x4 *>(grad) + ur.c0 + rest;
-    // (buffer accesses: one offset register for all vectors, and what lies past the row's end is
-    // not stored)
+    // (Buffer accesses: 32-bit offsets, and what lies past the row's end is neither read nor stored.
+    // A vector's place is all in the vector offset, because a scalar offset is not part of the check.)
     const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<u32x4 *>(p), 0, held * 16, kBufferWord3);
     const __amdgpu_buffer_rsrc_t dst =
@@ -461,7 +467,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         v[j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, tid * 16, j * NT * 16, 0));
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, (tid + j * NT) * 16, 0, 0));
     const int64_t e = ragged_element(ur, tid);
     const float end = e >= 0 ? Elem<T>::load(student, e) : -INFINITY;
     const float g = grad_loss[row];
@@ -524,13 +530,14 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
             x[k] = live ? coef * __builtin_amdgcn_exp2f((x[k] - m) * a.s) : 0.f;
         return Pack<T>::vec(x);
     };
+    int at = tid * 16;
+    asm("" : "+v"(at));  // (the loads' offsets would be kept for the stores otherwise)
     pairs([&](int j, float *x, int) {
-        // The vector's place is part of the vector offset, not a scalar offset: after a 16-byte
-        // store with a scalar offset the compiler lets the next instruction overwrite the first
-        // stored register, and stores with a logit difference in that word have been seen.
-        __builtin_amdgcn_raw_buffer_store_b128(gradient(x), dst, (tid + j * NT) * 16, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(gradient(x + EV), dst, (tid + (j + 1) * NT) * 16, 0,
-                                               0);
+        // (With a scalar offset, moreover, the compiler lets the instruction after a 16-byte store
+        // overwrite the first stored register, and stores with a logit difference in that word have
+        // been seen.)
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(x), dst, at + j * NT * 16, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(x + EV), dst, at + (j + 1) * NT * 16, 0, 0);
     });
     for (int i = tid - rest; i < 0; i += NT) {
         float x[EV];

@@ -285,7 +285,7 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
  *   top_p        [R]     float, device, or NULL: all_top_p (not NaN). >= 1 or NaN: no cut.
  *   min_p        [R]     float, device, or NULL: all_min_p (not NaN). <= 0 or NaN: no cut; values
  *                        above 1 count as 1.
- *   uniforms     [R]     float, device. u in [0, 1), the caller's random numbers (not read by greedy
+ *   uniforms     [R]     float, device. u in [0, 1), the caller's random numbers (no matter to greedy
  *                        rows; values outside are clamped, NaN counts as 0).
  *   With w_v = exp((x_v - max x) / T) and S_j the running sum of w over the candidate order (higher
  *   logit first, equal logits by lower id): top_k keeps the first k tokens (Z = their mass),
@@ -296,9 +296,11 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
  *   logprob      [R]     float, device, out, may be NULL. ln(w / W) of the token: its
  *                        log-probability in the distribution it was drawn from (0 when greedy, -inf
  *                        where the token is -1).
- *   Weights and masses are held to 2^-40 of themselves; weights below 2^-64 of the row's largest
- *   count as 0.
- *   1 <= R <= DFLASH2_MAX_SAMPLE_ROWS, 1 <= V <= DFLASH2_MAX_V.
+ *   Weights and masses are held to 2^-40 of themselves; weights below 2^-64 of the row's largest may
+ *   count as 0. bf16 rows take a faster path where all logits that are not masked or far below the
+ *   maximum lie in (-256, 256) and at most 64 of them within 2^-20 of 0.
+ *   1 <= R <= DFLASH2_MAX_SAMPLE_ROWS, 1 <= V <= DFLASH2_MAX_V. Outputs and workspace overlap
+ *   neither inputs nor each other.
  * Workspace: dflash2_sample_workspace_bytes(R, V, dtype) bytes (may be 0), contents need not be
  * initialised.
  * Errors: DFLASH2_ERR_INVALID_ARG (sizes, dtype, all_* out of range where its pointer is NULL, NULL
@@ -337,8 +339,10 @@ int dflash2_sample(const void *logits, int dtype, int R, int V, const float *tem
  *   -inf (masked tokens) have q = 0 and gradient 0 where no teacher entry names them; an entry with
  *   mass at such a token makes the loss +inf (its gradient is -g tau p). A row whose student logits
  *   are all -inf has loss +inf and gradient 0. NaN, or +inf among the student's logits, makes the
- *   row's loss NaN and its gradient NaN.
- *   1 <= R <= DFLASH2_MAX_DISTILL_ROWS, 1 <= V <= DFLASH2_MAX_V, 1 <= K <= DFLASH2_MAX_K.
+ *   row's loss NaN and its gradient NaN; a NaN teacher logit makes the loss NaN, and the gradient at
+ *   the row's entries.
+ *   1 <= R <= DFLASH2_MAX_DISTILL_ROWS, 1 <= V <= DFLASH2_MAX_V, 1 <= K <= DFLASH2_MAX_K. Outputs and
+ *   workspace overlap neither inputs nor each other.
  * Workspace of dflash2_distill and dflash2_distill_step: dflash2_distill_workspace_bytes(R, V,
  * student_dtype) bytes (may be 0), contents need not be initialised.
  */

@@ -142,7 +142,8 @@ def test_sizes(d2, R, V, K, dt, tau):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("R,V", [(16, 20000), (1100, 600)])  # slices; a row per workgroup
+# slices; a row per workgroup, read twice; held in registers
+@pytest.mark.parametrize("R,V", [(16, 20000), (1100, 600), (130, 20001)])
 def test_special_rows(d2, R, V, dt):
     log(f"distill special rows R={R} V={V} {dt}")
     dtype = torch.float32 if dt == "f32" else torch.bfloat16
@@ -181,7 +182,7 @@ def test_special_rows(d2, R, V, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("R,V", [(16, 20000), (1100, 600)])
+@pytest.mark.parametrize("R,V", [(16, 20000), (1100, 600), (130, 20001)])
 def test_not_a_number(d2, R, V, dt):
     dtype = torch.float32 if dt == "f32" else torch.bfloat16
     z, ids, t, g = inputs(R, V, 4, dtype, 6)
