@@ -15,8 +15,10 @@
 // are whole numbers (LDS atomics in any order), there is one atomic and a handful of integer
 // instructions per logit in place of an exponential, and the pass needs no maximum first.
 //   * Counted values: 2^-20 <= |x| < 2^8, 28 binades of 128 values, a word each: positive values
-//     in its low half, negative ones in its high half. A word below takes what is smaller, one
-//     above what is larger. The row is counted in parts (words of their own), so that a half-word
+//     in its low half, negative ones in its high half. A word below takes what is smaller, 64
+//     above what is larger (a lane has its own: the masked tokens of a row all count there, and
+//     atomics on one word take turns: 1024 rows x 151936 of which 90% are masked took 570 us with
+//     one word for them, 71 with 64). The row is counted in parts (words of their own), so that a half-word
 //     is enough; a part's overflow shows as a wrong total.
 //   * Smaller values are rare (one in 10^6 of a normal row): up to 64 of them are listed and take
 //     their place between the positive and the negative values. Larger negative ones are masks,
@@ -38,14 +40,15 @@ constexpr int kParts = 2;       // parts of a row that a workgroup counts by its
 constexpr int kNT32 = 1024;     // threads of the float32 kernel
 constexpr int kBase = 0x3580;  // bf16 pattern of 2^-20
 constexpr int kValues = 3584;  // counted values of a sign: up to 2^8
-constexpr int kStride = 3588;  // words of a part: below, kValues, above, two unused
+constexpr int kAbove = 64;      // words for what is larger, one to a lane
+constexpr int kStride = 3652;  // words of a part: below, kValues, kAbove, three unused
 constexpr int kRows = 2 * kValues / kWave;  // places in rows of 64, one to a lane
 constexpr int kRowGroups = 256;
 constexpr int kMaxSlices = 16;
 constexpr int kMaxTops = 1280;  // groups of a row whose maxima are kept
 constexpr uint32_t kListed = 256;  // equal logits of a part that are listed
 constexpr int kSmallCap = 64;  // gathered values below 2^-20
-static_assert(kCountWords == 2 * kStride, "counts in LDS");
+static_assert(kCountWords == 2 * kStride && kStride >= 1 + kValues + kAbove, "counts in LDS");
 static_assert(kRows <= 2 * kWave && kValues % kWave == 0, "rows of places: two to a lane");
 
 template <int NT> using S16 = RowSampler<uint16_t, NT>;
@@ -102,10 +105,10 @@ typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 // Counts two logits packed in a word: the words' indexes by packed 16-bit arithmetic (a saturating
 // subtraction and a minimum), the increments 1 or 2^16 as sign mask + 1. Returns the pair as integers
 // in the order of the logits (negative ones with their magnitude inverted); `lowest` becomes 0 in a
-// half that met a small value.
-__device__ __forceinline__ i16x2 tally2(uint32_t *words, uint32_t pair, u16x2 &lowest) {
+// half that met a small value. `high` has the last word that larger values may take, twice.
+__device__ __forceinline__ i16x2 tally2(uint32_t *words, uint32_t pair, u16x2 high,
+                                        u16x2 &lowest) {
     const u16x2 low = {(uint16_t)(kBase - 1), (uint16_t)(kBase - 1)};
-    const u16x2 high = {(uint16_t)(kValues + 1), (uint16_t)(kValues + 1)};
     const u16x2 mag = __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu);
     const u16x2 at = __builtin_elementwise_min(__builtin_elementwise_sub_sat(mag, low), high);
     lowest = __builtin_elementwise_min(lowest, at);
@@ -129,9 +132,12 @@ __device__ __forceinline__ void tally(uint32_t *words, uint32_t h) {
                            __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
-__device__ __forceinline__ i16x2 tally_vector(uint32_t *words, const u32x4 &v, u16x2 &lowest) {
-    const i16x2 a = __builtin_elementwise_max(tally2(words, v.x, lowest), tally2(words, v.y, lowest));
-    const i16x2 b = __builtin_elementwise_max(tally2(words, v.z, lowest), tally2(words, v.w, lowest));
+__device__ __forceinline__ i16x2 tally_vector(uint32_t *words, const u32x4 &v, u16x2 high,
+                                              u16x2 &lowest) {
+    const i16x2 a = __builtin_elementwise_max(tally2(words, v.x, high, lowest),
+                                              tally2(words, v.y, high, lowest));
+    const i16x2 b = __builtin_elementwise_max(tally2(words, v.z, high, lowest),
+                                              tally2(words, v.w, high, lowest));
     return __builtin_elementwise_max(a, b);
 }
 
@@ -172,15 +178,17 @@ __device__ __forceinline__ void count_part(const uint16_t *logits, const UnitRan
     const int slot = tid / kGroupLanes;
     const bool first = (tid & (kGroupLanes - 1)) == 0, keep = notes.tops != nullptr;
     const int64_t id0 = ur.c0 * 8 - ur.g0;
+    const uint16_t top = (uint16_t)(kValues + 1 + (tid & (kAbove - 1)));
+    const u16x2 high = {top, top};
     i16x2 rest = {-32768, -32768};
     stream<NT>(
         reinterpret_cast<const u32x4 *>(logits) + ur.c0, ur.nv, tid,
         [&](const u32x4 *v, int i) {
             u16x2 lowest = {0xFFFF, 0xFFFF};
-            i16x2 m = tally_vector(words, v[0], lowest);
+            i16x2 m = tally_vector(words, v[0], high, lowest);
 #pragma unroll
             for (int u = 1; u < kStreamVectors; ++u)
-                m = __builtin_elementwise_max(m, tally_vector(words, v[u], lowest));
+                m = __builtin_elementwise_max(m, tally_vector(words, v[u], high, lowest));
             if (keep) {
                 const int top = group_max(m);
                 if (first) notes.tops[i / kStep * kPerBatch + slot] = (int16_t)top;
@@ -196,7 +204,7 @@ __device__ __forceinline__ void count_part(const uint16_t *logits, const UnitRan
         },
         [&](const u32x4 &v, int i) {
             u16x2 lowest = {0xFFFF, 0xFFFF};
-            rest = __builtin_elementwise_max(rest, tally_vector(words, v, lowest));
+            rest = __builtin_elementwise_max(rest, tally_vector(words, v, high, lowest));
             if (keep && (lowest.x == 0 || lowest.y == 0))
                 note_small(notes, v, id0 + (int64_t)i * 8);
         });
@@ -381,9 +389,9 @@ struct SettleShared {
 // general path; nothing is written then.
 template <int NT, typename Counts>
 __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int V,
-                                       const Counts &counts, typename S16<NT>::Shared &sh, SettleShared<NT> &ss,
-                                       const RowSettings &st, int tid, int32_t *token,
-                                       float *logprob) {
+                                       const Counts &counts, typename S16<NT>::Shared &sh,
+                                       SettleShared<NT> &ss, const RowSettings &st, int tid,
+                                       int32_t *token, float *logprob) {
     const int lane = tid & (kWave - 1), wave = tid / kWave;
     // A binade is four rows: two of its positive values, two of its negative ones. The waves take the
     // binades in turn.
@@ -409,6 +417,10 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
             }
         }
     }
+    const uint32_t large_pos = counts.count(kValues + 1 + lane, false);
+    const uint32_t large_neg = counts.count(kValues + 1 + lane, true);
+    const bool any_large_neg = __ballot(large_neg > 0) != 0ull;
+    if (wave == 0) tokens += large_pos + large_neg;
     tokens = wave_running_sum(tokens);
     if (lane == kWave - 1) {
         ss.total[wave] = tokens;
@@ -419,8 +431,6 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
         ss.mass[tid] = 0.0;
     }
     const uint32_t small_n = counts.count(0, false) + counts.count(0, true);
-    const uint32_t large_pos = counts.count(kValues + 1, false);
-    const uint32_t large_neg = counts.count(kValues + 1, true);
     __syncthreads();
     uint32_t total = 0;
 #pragma unroll
@@ -428,8 +438,8 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
         total += ss.total[i];
         first = min(first, ss.first[i]);
     }
-    if (total + small_n + large_pos + large_neg != (uint32_t)V || large_pos > 0 ||
-        small_n > kSmallCap || total + small_n == 0)
+    if (total + small_n != (uint32_t)V || __ballot(large_pos > 0) != 0ull ||
+        small_n > kSmallCap || (first == kRows && small_n == 0))
         return false;
     // the small values, listed and sorted
     Small small{(int)small_n, 0.0, 0.0, 0u};
@@ -463,7 +473,7 @@ __device__ __forceinline__ bool settle(const uint16_t *logits, int64_t row, int 
 
     if (st.temperature > 0.f) {
         const Weights w{m, kBinsPerE / (double)st.temperature, 1.0, sh.scale, m, 0.0, 1.0};
-        if (large_neg > 0 && !(weight_y(w, -256.f) >= (double)kFar)) return false;
+        if (any_large_neg && !(weight_y(w, -256.f) >= (double)kFar)) return false;
         const bool by_number = st.top_k >= 1, by_weight = st.min_p > 0.f;
         const double least = by_weight ? fmin((double)st.min_p, 1.0) : 0.0;
         double heavy = 0.0;  // mass of the weights that min_p keeps

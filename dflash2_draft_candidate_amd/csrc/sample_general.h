@@ -31,7 +31,7 @@ constexpr int kPerOctave = 32;          // bins to a factor of two
 constexpr int kBins = 128 * kPerOctave;
 constexpr int kHeadroom = 40 * kPerOctave;  // the bin of the first estimate of the maximum
 constexpr int kFar = 64 * kPerOctave;       // weights from here on count as 0
-constexpr int kCountWords = 2 * 3588;
+constexpr int kCountWords = 2 * 3652;
 constexpr double kBinsPerE = kPerOctave * 1.4426950408889634;
 constexpr double kTwo52 = 4503599627370496.0;
 // added to z, this leaves the bin's number in the low bits
