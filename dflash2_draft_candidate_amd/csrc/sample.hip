@@ -43,7 +43,7 @@ constexpr int kValues = 3584;  // counted values of a sign: up to 2^8
 constexpr int kAbove = 64;      // words for what is larger, one to a lane
 constexpr int kStride = 3652;  // words of a part: below, kValues, kAbove, three unused
 constexpr int kRows = 2 * kValues / kWave;  // places in rows of 64, one to a lane
-constexpr int kRowGroups = 256;
+constexpr int kRowGroups = 128;
 constexpr int kMaxSlices = 16;
 constexpr int kMaxTops = 1280;  // groups of a row whose maxima are kept
 constexpr uint32_t kListed = 256;  // equal logits of a part that are listed
@@ -762,15 +762,21 @@ sample_settle_kernel(const uint16_t *__restrict__ logits, int V, int slices, dou
     }
 }
 
-// Slices per bf16 row: about 512 workgroups in all when rows are few, each of two vectors and more
-// per thread.
+// Slices per bf16 row: 1 (sample_bf16_kernel) where rows are many or short, otherwise about 512
+// workgroups in all, of two vectors and more per thread. Slices read a row faster, but their counts
+// go through the workspace to a second kernel, which costs more the more rows there are. Measured,
+// one workgroup per row against slices (us, N(0, 2.5) logits, top-p): V = 32000: 1 row 14.9 / 16.7,
+// 64 rows 16.4 / 20.0; V = 65536: 1 row 19.0 / 18.0, 8 rows 19.3 / 18.2, 64 rows 20.2 / 24.5;
+// V = 100001: 8 rows 23.7 / 19.0, 64 rows 24.3 / 24.8; V = 151936: 1 row 26.9 / 18.0, 64 rows
+// 29.6 / 26.7, 100 rows 30.1 / 30.0, 127 rows 30.8 / 33.2, 192 rows 31.3 / 43.7; V = 262144: 64 rows
+// 41.6 / 30.5, 127 rows 43.3 / 41.9. (256 or 1024 workgroups in place of 512: 64 rows x 151936
+// 27.9 / 28.3 against 26.7.)
 int plan_slices(int R, int V) {
-    if (R >= kRowGroups) return 1;
-    int s = 2 * kRowGroups / R;
+    if (R >= kRowGroups || V <= 60000 + 1000 * R) return 1;
+    int s = 512 / R;
     if (s > kMaxSlices) s = kMaxSlices;
     const int most = V / 8 / (2 * kNT);
-    if (s > most) s = most;
-    return s < 1 ? 1 : s;
+    return s > most ? most : s;
 }
 
 }  // namespace

@@ -135,11 +135,12 @@ def test_settings_of_each_row(d2, dt):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("spread", [0.0, 1e-4, 0.02, 0.3, 30.0])
-def test_flat_and_steep_rows(d2, spread, dt):
+@pytest.mark.parametrize("V", [40000, 80000])  # (bf16: a workgroup per row; slices)
+def test_flat_and_steep_rows(d2, V, spread, dt):
     """Many tokens in a bin: bins are split by value, down to a single value in constant rows."""
     log(f"sample spread={spread} {dt}")
     g = torch.Generator().manual_seed(9)
-    R, V = 4, 40000
+    R = 4
     x = (torch.randn(R, V, generator=g) * spread + 1.5)
     x = x.to(torch.float32 if dt == "f32" else torch.bfloat16)
     for i, s in enumerate([dict(), dict(T=0.5, p=0.7), dict(k=20000), dict(k=1500, p=0.5),
@@ -190,7 +191,7 @@ def test_masks(d2, dt):
 def test_values_outside_the_counted_range(d2):
     """bf16 rows with values below 2^-20 (gathered, or too many) and from 2^8 on, in rows that are
     counted whole and rows that are cut into slices."""
-    for V in (6001, 40010):
+    for V in (6001, 80010):
         x, u = rows(10, V, "bf16", V)
         g = torch.Generator().manual_seed(V)
         tiny = (torch.randn(V, generator=g) * 2.0 ** -22).to(torch.bfloat16)
@@ -247,6 +248,42 @@ def test_late_maximum(d2, dt):
                            dict(T=2.0, k=2000, p=0.9), dict(T=3.0, m=0.05), dict(T=20.0, p=0.8),
                            dict(T=40.0, m=0.2, p=0.6), dict(T=0.0)]):
         check(d2, x, [(v + 0.31 * i) % 1.0 for v in u], **s)
+
+
+@pytest.mark.parametrize("R,V", [(5, 150001), (130, 150001)])  # slices; a workgroup per row
+def test_mostly_masked_rows(d2, R, V):
+    """Rows of which little is left, as constrained decoding makes them: more masks than a half-word
+    counts."""
+    x, u = rows(5, V, "bf16", 101)
+    g = torch.Generator().manual_seed(102)
+    off = torch.rand(5, V, generator=g)
+    x[0, off[0] > 0.1] = -math.inf
+    x[1, off[1] > 0.001] = torch.finfo(torch.bfloat16).min
+    x[2, off[2] > 0.5] = -math.inf
+    x[2, off[2] > 0.8] = -300.0
+    x[3, :] = -math.inf
+    x[3, V - 3] = -2.0
+    x[4, off[4] > 0.0005] = math.nan
+    x = x.repeat(R // 5, 1)
+    for i, s in enumerate([dict(), dict(p=0.9), dict(T=0.7, k=40), dict(T=2.0, m=0.02, p=0.97)]):
+        v = [(a + 0.23 * i) % 1.0 for a in u]
+        ids, lp = d2.sample(x.to(DEV), torch.tensor(v * (R // 5), device=DEV),
+                            s.get("T", 1.0), s.get("k", 0), s.get("p", 1.0), s.get("m", 0.0))
+        assert torch.equal(ids, ids[:5].repeat(R // 5)) and torch.equal(lp, lp[:5].repeat(R // 5))
+        if R == 5:
+            check(d2, x, v, **s)
+        else:
+            few = d2.sample(x[:5].to(DEV), torch.tensor(v, device=DEV),
+                            s.get("T", 1.0), s.get("k", 0), s.get("p", 1.0), s.get("m", 0.0))
+            assert torch.equal(ids[:5], few[0])
+
+
+def test_any_top_k_number(d2):
+    x, u = rows(3, 500, "f32", 11)
+    x, u = x.to(DEV), torch.tensor(u, device=DEV)
+    want = d2.sample(x, u)[0]
+    for k in (0, -3, -2 ** 40, 500, 2 ** 40):
+        assert torch.equal(d2.sample(x, u, top_k=k)[0], want)
 
 
 def test_very_long_rows(d2):
@@ -331,7 +368,7 @@ def test_outputs_and_neighbours(d2):
 
 
 def test_graph_replay(d2):
-    R, V = 20, 30011
+    R, V = 20, 90011
     a, ua = rows(R, V, "bf16", 51)
     b, ub = rows(R, V, "bf16", 52)
     dev = lambda x, u: (x.to(DEV), torch.tensor(u, device=DEV))
@@ -354,7 +391,7 @@ def test_graph_replay(d2):
 
 
 def test_two_streams(d2):
-    a, ua = rows(30, 20011, "bf16", 61)
+    a, ua = rows(30, 95011, "bf16", 61)
     b, ub = rows(9, 50000, "f32", 62)
     a, b = (a.to(DEV), torch.tensor(ua, device=DEV)), (b.to(DEV), torch.tensor(ub, device=DEV))
     wa, wb = d2.sample(*a, top_p=0.95), d2.sample(*b)
