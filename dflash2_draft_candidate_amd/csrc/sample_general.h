@@ -172,6 +172,7 @@ struct Shared {
     double wave_mass[kWaves];
     uint32_t wave_count[kWaves];
     int wave_first[kWaves];
+    uint32_t first_key[4];
     float wave_max[kWaves];
     uint32_t listed;
     int32_t token;
@@ -519,8 +520,7 @@ static __device__ __forceinline__ Listed make_list(Shared &sh, const Weights &w,
 }
 
 // The smallest value key in [key(-FLT_MAX), key(FLT_MAX)] for which `holds` is true, one past the range
-// if there is none; holds(x) must not fall back to false as x grows. Every wave searches by itself,
-// 64 keys at a time.
+// if there is none; holds(x) must not fall back to false as x grows. By one wave, 64 keys at a time.
 template <typename F>
 static __device__ __forceinline__ uint32_t first_key(int lane, F &&holds) {
     uint32_t a = value_key(-FLT_MAX), e = value_key(FLT_MAX) + 1u;  // a <= answer <= e
@@ -542,18 +542,24 @@ static __device__ __forceinline__ uint32_t first_key(int lane, F &&holds) {
 struct Keys {
     uint32_t lo, hi;  // lo <= key <= hi
 };
-static __device__ __forceinline__ Keys keys_of(const Weights &w, int b0, int b1, int lane) {
-    auto from = [&](int b) {  // the first key in bin b or above it in the order
-        const double last = (double)(b - kBins / 2);
-        return first_key(lane, [&](float x) {
+// The keys of the bins [a0, a1] and of [b0, b1]: four searches, a wave each (side by side they take
+// 2 us; by every wave, one after the other, 7).
+static __device__ __forceinline__ void keys_of(Shared &sh, const Weights &w, int a0, int a1, int b0,
+                                               int b1, int tid, Keys &a, Keys &b) {
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    if (wave < 4) {  // the first key in bin `bin` or above it in the order
+        const int bin = wave == 0 ? a1 : wave == 1 ? a0 - 1 : wave == 2 ? b1 : b0 - 1;
+        const double last = (double)(bin - kBins / 2);
+        const uint32_t key = first_key(tid & (kWave - 1), [&](float x) {
             const double z = bin_z(w, x);
             return z - bin_fraction(z) <= last;
         });
-    };
-    Keys k;
-    k.lo = from(b1);
-    k.hi = from(b0 - 1) - 1u;
-    return k;
+        if ((tid & (kWave - 1)) == 0) sh.first_key[wave] = key;
+    }
+    __syncthreads();
+    a = Keys{sh.first_key[0], sh.first_key[1] - 1u};
+    b = Keys{sh.first_key[2], sh.first_key[3] - 1u};
+    __syncthreads();
 }
 
 // Whether the pass keeps the maxima of this row's groups.
@@ -579,10 +585,10 @@ static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange
             if (sh.tops[g] >= lo) sh.hit[atomicAdd(&sh.hits, 1u)] = (uint16_t)g;
         __syncthreads();
     }
+    const bool single = one.lo == two.lo && one.hi == two.hi;
     // (x lies in a range where the median of it and the range's ends is x itself; one branch a vector)
-    auto in = [&](float x) {
-        return __builtin_amdgcn_fmed3f(x, lo1, hi1) == x || __builtin_amdgcn_fmed3f(x, lo2, hi2) == x;
-    };
+    auto in_one = [&](float x) { return __builtin_amdgcn_fmed3f(x, lo1, hi1) == x; };
+    auto in = [&](float x) { return in_one(x) || __builtin_amdgcn_fmed3f(x, lo2, hi2) == x; };
     auto append = [&](float x, int32_t id) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
         if (at < kCap) sh.list[at] = cand_key(x, id);
@@ -593,8 +599,13 @@ static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange
         float x[EV];
         Elem<T>::unpack(v, x);
         bool any = false;
+        if (single) {
 #pragma unroll
-        for (int k = 0; k < EV; ++k) any |= in(x[k]);
+            for (int k = 0; k < EV; ++k) any |= in_one(x[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < EV; ++k) any |= in(x[k]);
+        }
         if (any) {
 #pragma unroll
             for (int k = 0; k < EV; ++k)
@@ -752,7 +763,8 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
                                       const Weights &w, int bin, uint32_t size, Cut cut,
                                       double target, uint32_t nth, double below, uint32_t before,
                                       int tid) {
-    Keys keys = keys_of(w, bin, bin, tid & (kWave - 1));
+    Keys keys, same;
+    keys_of(sh, w, bin, bin, bin, bin, tid, keys, same);
     // Split by value until a part is small or a single value; every step narrows the range to a
     // kParts-th of it or to one value.
 #pragma unroll 1
@@ -922,7 +934,9 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         upto = total;
     }
     if (upto <= kCap) {
-        const Keys keys{keys_of(w, low, low, tid & (kWave - 1)).lo, value_key(w.m)};
+        Keys keys, same;
+        keys_of(sh, w, low, low, low, low, tid, keys, same);
+        keys.hi = value_key(w.m);
         const Listed l = gather(logits, ur, sh, w, keys, keys, tid);
         // (the list's weights are exact where equal tokens tie; the bins give only what lies below it)
         double z = 0.0;
@@ -991,9 +1005,9 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         const uint32_t in_all =
             apart ? drawn + end_size : end_before + end_size - min(from_before, end_before);
         if (in_all <= kCap) {
-            const int lane = tid & (kWave - 1);
-            const Keys tail = keys_of(w, apart ? end : min(from, end), end, lane);
-            const Keys head = apart ? keys_of(w, from, to, lane) : tail;
+            Keys head, tail;
+            const int last_run = apart ? end : min(from, end);
+            keys_of(sh, w, apart ? from : last_run, apart ? to : end, last_run, end, tid, head, tail);
             const Listed l = gather(logits, ur, sh, w, head, tail, tid);
             // the running mass of this thread's token in the row
             if (tid == (int)drawn) sh.spot_mass = l.below;
