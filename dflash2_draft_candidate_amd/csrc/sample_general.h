@@ -672,8 +672,29 @@ static __device__ __forceinline__ Bins sum_bins(Shared &sh, const Level<kPerThre
         sum += v.mass(w, b);
         number += v.counts[b];
     }
-    h.below = below + scan_mass(sh, sum, tid, h.total);
-    h.before = before + scan_count(sh, number, tid, h.number);
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    const double upto = wave_running_sum(sum);
+    const uint32_t upto_n = wave_running_sum(number);
+    if (lane == kWave - 1) {
+        sh.wave_mass[wave] = upto;
+        sh.wave_count[wave] = upto_n;
+    }
+    __syncthreads();
+    h.below = h.total = 0.0;
+    h.before = h.number = 0u;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i == wave) {
+            h.below = h.total;
+            h.before = h.number;
+        }
+        h.total += sh.wave_mass[i];
+        h.number += sh.wave_count[i];
+    }
+    __syncthreads();
+    const double prev = __shfl_up(upto, 1);
+    h.below += below + (lane == 0 ? 0.0 : prev);
+    h.before += before + upto_n - number;
     h.total += below;
     h.number += before;
     return h;
@@ -916,16 +937,17 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         find_bin(sh, all, w, h, kNumber, 0.0, (uint32_t)top_k, tid);
         // (top-p needs the whole mass of the top-k tokens, whatever min-p leaves of them)
         low = by_mass ? sh.spot_bin : min(low, sh.spot_bin);
-        __syncthreads();
     } else if (by_mass) {
         find_bin(sh, all, w, h, kReach, (double)top_p * h.total, 0u, tid);
         mass_inside = sh.spot_bin <= low;
         low = min(low, sh.spot_bin);
-        __syncthreads();
     }
-    // tokens in the bins up to `low`
-    uint32_t upto = 0;
-    {
+    // tokens in the bins up to `low` (after a search: of which sh.spot_* still has the result)
+    uint32_t upto = h.number;
+    if ((by_number || by_mass) && low == sh.spot_bin) {
+        upto = sh.spot_count + sh.spot_size;
+    } else if (low < kBins - 1) {
+        upto = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
             if (tid * kPer + j <= low) upto += sh.count[tid * kPer + j];
@@ -986,8 +1008,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
         // The nucleus' end and the draw, gathered in one pass: the kept mass is known to within the
         // end's bin, and with it where the draw can fall.
         const double target = (double)top_p * z;
-        find_bin(sh, all, w, h, kReach, target, 0u, tid);
-        const int end = sh.spot_bin;
+        const int end = sh.spot_bin;  // (found above)
         const double end_below = sh.spot_mass;
         const uint32_t end_before = sh.spot_count, end_size = sh.spot_size;
         __syncthreads();
