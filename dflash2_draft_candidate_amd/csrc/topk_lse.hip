@@ -1084,7 +1084,10 @@ size_t topk_workspace_bytes(const TopkPlan &p, int R) {
 }
 
 uint32_t next_launch_epoch() {
-    static std::atomic<uint32_t> launches{0};
+    // (Counters lie in workspace that need not be initialised, and one that happened to hold this
+    // launch's epoch would be taken for its own: epochs start among NaN patterns, which neither
+    // logits, ids nor other counts leave behind, rather than among small integers.)
+    static std::atomic<uint32_t> launches{0x7FB10000u};
     uint32_t e = launches.fetch_add(1, std::memory_order_relaxed) + 1u;
     return e == 0u ? 1u : e;  // after 2^32 launches it wraps (the kernel then re-bases by CAS)
 }
