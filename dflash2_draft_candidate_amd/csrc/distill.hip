@@ -38,7 +38,7 @@ constexpr float kMaxRef = 8388608.f;  // 2^23: references stay within this, so e
                                       // of m s and 2^(m s - ref) cannot overflow
 constexpr float kNoRef = -kMaxRef;    // reference before the first element
 constexpr int kBufferWord3 = 0x00020000;  // gfx9-family buffer descriptor word 3 (raw data)
-constexpr int kHeldRows = 128;   // rows from which on a step holds a row in a workgroup's registers
+constexpr int kHeldRows = 128;   // rows from which on a step always holds a row in registers
 constexpr int kShortRow = 1024;  // vectors up to which a step reads its row twice
 constexpr int kUnitVectors = 2 * kThreads;  // a slice holds at least this many vectors
 
@@ -595,8 +595,8 @@ Args make_args(const int32_t *ids, const float *teacher, int R, int V, int K, fl
     return a;
 }
 
-// Slices per row: enough units to fill the chip (1024 workgroups) when rows are few, each of at
-// least kUnitVectors vectors.
+// Slices per row where rows are cut: enough units to fill the chip (1024 workgroups) when rows are
+// few, each of at least kUnitVectors vectors.
 int plan_slices(int R, int V, int elem_bytes) {
     const int64_t nvec = (int64_t)V * elem_bytes / 16;
     int64_t s = (1024 + R - 1) / R;
@@ -605,12 +605,35 @@ int plan_slices(int R, int V, int elem_bytes) {
     return s < 1 ? 1 : (int)s;
 }
 
+// Slices per row of the forward pass: 1 where the row is short for the number of rows, as a second
+// kernel has to join slices. Measured in a graph, one workgroup per row against slices (us, bf16):
+// V = 32000: 1 row 6.4 / 7.4, 128 rows 7.2 / 9.6; V = 100001: 16 rows 9.4 / 8.1, 48 rows 9.7 / 10.9;
+// V = 200003: 48 rows 13.9 / 13.7, 128 rows 15.0 / 17.1; V = 500000: 48 rows 26.3 / 17.9, 128 rows
+// 32.3 / 31.6; V = 151936: 256 rows 17.3 / 21.1, 512 rows 29.0 / 32.6 (float32: the same borders).
+// By itself the second launch also costs the host 2.6 us, more than slices save up to V = 160000:
+// 16 rows x 151936 take 12.5 us in one launch, 15.1 in two (11.3 and 9.0 in a graph).
+int forward_slices(int R, int V, int elem_bytes, bool alone) {
+    int64_t most = 50000 + 2500 * (int64_t)R;
+    if (alone && most < 160000) most = 160000;
+    return V <= most ? 1 : plan_slices(R, V, elem_bytes);
+}
+
+// Whether a step holds its rows in registers (distill_held_kernel, a workgroup per row) or runs forward
+// and backward pass one after the other (rows cut into slices, at least by the latter). Held against
+// the two passes (us, in a graph, bf16): V = 32000: 16 rows 12.2 / 11.9, 100 rows 13.4 / 14.9;
+// V = 65536: 16 rows 15.5 / 13.2, 100 rows 18.1 / 20.4; V = 151936: 100 rows 29.7 / 27.8, 128 rows
+// 31.6 / 29, 200 rows 33.8 / 41, 512 rows 82 / 103; V = 262144: 512 rows 149 / 164. float32: V = 10000:
+// 1 row 8.8 / 10.3; V = 32000: 64 rows 13.4 / 15.1; V = 151936: 127 rows 46.9 / 48.4.
+bool held_step(int R, int V, int elem_bytes) {
+    return R >= kHeldRows || V <= 40000 + 300 * R || plan_slices(R, V, elem_bytes) == 1;
+}
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <typename T>
-hipError_t forward(const void *student, const Args &a, float *loss, float *row_stats, void *ws,
-                   hipStream_t stream) {
-    const int S = plan_slices(a.R, a.V, (int)sizeof(T));
+hipError_t forward(const void *student, const Args &a, bool alone, float *loss, float *row_stats,
+                   void *ws, hipStream_t stream) {
+    const int S = forward_slices(a.R, a.V, (int)sizeof(T), alone);
     const T *x = static_cast<const T *>(student);
     Stat *part = static_cast<Stat *>(ws);
     hipLaunchKernelGGL((distill_forward_kernel<T>), dim3((unsigned)(a.R * (int64_t)S)),
@@ -634,8 +657,7 @@ hipError_t backward(const void *student, const Args &a, const float *row_stats,
 template <typename T>
 hipError_t step(const void *student, const Args &a, const float *grad_loss, float *loss, void *grad,
                 void *ws, hipStream_t stream) {
-    const int S = plan_slices(a.R, a.V, (int)sizeof(T));
-    if (S == 1 || a.R >= kHeldRows) {
+    if (held_step(a.R, a.V, (int)sizeof(T))) {
         const T *x = static_cast<const T *>(student);
         T *out = static_cast<T *>(grad);
         // the smallest shape that holds the row (at most 128 registers a thread: 1024 threads a CU)
@@ -655,7 +677,7 @@ hipError_t step(const void *student, const Args &a, const float *grad_loss, floa
     }
     float *row_stats = static_cast<float *>(ws);
     char *part = static_cast<char *>(ws) + align256((size_t)a.R * 2 * sizeof(float));
-    const hipError_t e = forward<T>(student, a, loss, row_stats, part, stream);
+    const hipError_t e = forward<T>(student, a, false, loss, row_stats, part, stream);
     if (e != hipSuccess) return e;
     return backward<T>(student, a, row_stats, grad_loss, grad, stream);
 }
@@ -665,6 +687,7 @@ hipError_t step(const void *student, const Args &a, const float *grad_loss, floa
 size_t distill_workspace_bytes(int R, int V, int elem_bytes) {
     const int S = plan_slices(R, V, elem_bytes);
     if (S == 1) return align256((size_t)R * sizeof(Stat));  // of distill_held_kernel
+    // row_stats of a step's two passes and the slices' statistics (more than the held kernel needs)
     return align256((size_t)R * 2 * sizeof(float)) + align256((size_t)R * S * sizeof(Stat));
 }
 
@@ -672,8 +695,8 @@ hipError_t launch_distill(const void *student, int dtype, const int32_t *ids, co
                           int R, int V, int K, float tau, float *loss, float *row_stats, void *ws,
                           hipStream_t stream) {
     const Args a = make_args(ids, teacher, R, V, K, tau);
-    return dtype == 0 ? forward<float>(student, a, loss, row_stats, ws, stream)
-                      : forward<uint16_t>(student, a, loss, row_stats, ws, stream);
+    return dtype == 0 ? forward<float>(student, a, true, loss, row_stats, ws, stream)
+                      : forward<uint16_t>(student, a, true, loss, row_stats, ws, stream);
 }
 
 hipError_t launch_distill_backward(const void *student, int dtype, const int32_t *ids,

@@ -141,9 +141,12 @@ def test_sizes(d2, R, V, K, dt, tau):
         check(loss, grad, ref, V, tau, g, dtype)
 
 
+# slices; a row per workgroup forward, slices backward; a row per workgroup; held in registers
+WAYS = [(16, 165000), (16, 60000), (1100, 600), (130, 20001)]
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-# slices; a row per workgroup, read twice; held in registers
-@pytest.mark.parametrize("R,V", [(16, 20000), (1100, 600), (130, 20001)])
+@pytest.mark.parametrize("R,V", WAYS)
 def test_special_rows(d2, R, V, dt):
     log(f"distill special rows R={R} V={V} {dt}")
     dtype = torch.float32 if dt == "f32" else torch.bfloat16
@@ -182,7 +185,7 @@ def test_special_rows(d2, R, V, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("R,V", [(16, 20000), (1100, 600), (130, 20001)])
+@pytest.mark.parametrize("R,V", WAYS)
 def test_not_a_number(d2, R, V, dt):
     dtype = torch.float32 if dt == "f32" else torch.bfloat16
     z, ids, t, g = inputs(R, V, 4, dtype, 6)
@@ -300,7 +303,7 @@ def test_no_gradient_needed(d2):
         assert not d2.distill_loss(z, ids, t).requires_grad
 
 
-@pytest.mark.parametrize("R,V", [(16, 40000), (1024, 700)])
+@pytest.mark.parametrize("R,V", WAYS)
 def test_graph_replay(d2, R, V):
     log(f"distill graph R={R} V={V}")
     z, ids, t, g = inputs(R, V, 8, torch.bfloat16, 21)
@@ -327,7 +330,7 @@ def test_graph_replay(d2, R, V):
 
 
 def test_other_stream_and_two_at_once(d2):
-    a = inputs(16, 40000, 8, torch.bfloat16, 31)
+    a = inputs(16, 165000, 8, torch.bfloat16, 31)
     b = inputs(700, 3001, 8, torch.float32, 32)
     wa, wb = d2.distill_step(*a), d2.distill_step(*b)
     torch.cuda.synchronize()
