@@ -18,16 +18,28 @@
 //     in its low half, negative ones in its high half. A word below takes what is smaller, 64
 //     above what is larger (a lane has its own: the masked tokens of a row all count there, and
 //     atomics on one word take turns: 1024 rows x 151936 of which 90% are masked took 570 us with
-//     one word for them, 71 with 64). The row is counted in parts (words of their own), so that a half-word
-//     is enough; a part's overflow shows as a wrong total.
+//     one word for them, 71 with 64). The row is counted in parts (words of their own), so that a
+//     half-word is enough; a part's overflow shows as a wrong total.
 //   * Smaller values are rare (one in 10^6 of a normal row): up to 64 of them are listed and take
 //     their place between the positive and the negative values. Larger negative ones are masks,
 //     or so far below the maximum that they have no weight. Anything else (large or infinite
 //     logits, many tiny or zero ones, a row of masks) sends the row to the general path.
 //   * The token is then the n-th logit of a value, and the parts' counts say in which part: only
 //     that part is read a second time.
-// Rows that are many (kRowGroups and more) have a workgroup each, with two parts; few rows are cut
-// into slices, a part and a workgroup each, whose counts go through the workspace to a second kernel.
+// Rows that are many (kRowGroups and more) or short have a workgroup each, with two parts; a few long
+// rows are cut into slices, a part and a workgroup each, whose counts go through the workspace to a
+// second kernel (plan_slices).
+//
+// What bounds it and what it takes (V = 151936, settings mixed; a row's bytes are read once, and the
+// part that holds the token for the groups that can hold it):
+//   1024 rows bf16: 82 us, 3.8 TB/s of logits; the reading and counting alone 55 us (5.6 TB/s, what a
+//     plain read reaches), the rest is the settling of a row, a chain of 11-13 us that the other
+//     workgroup of the CU hides in part;
+//   64 rows bf16: 27 us: counting 9 us, settling 18 us; 1 row: 17 us, 4 + 13 us. Latency: barriers,
+//     two dependent reads of the counts, fp64 exponentials, the second read of the part;
+//   256 rows float32: 85 us; the first pass 35 us, at the rate of a read, 64 rows 32 us: there the
+//     fp64 arithmetic of one CU per row is what it takes. Settling: 11 us a row whose cuts leave few
+//     tokens, about 25 us where 1024 tokens are gathered from most of the row.
 #include "kernels.h"
 #include "sample_general.h"
 
@@ -35,8 +47,11 @@ namespace dflash2 {
 namespace {
 
 constexpr int kNT = 512;        // threads of the bf16 kernels: two workgroups share a CU, and two
-                                // waves share a SIMD where all waves do the same
-constexpr int kParts = 2;       // parts of a row that a workgroup counts by itself
+                                // waves share a SIMD where all waves do the same (four workgroups
+                                // of 256: 1024 rows x 151936 82 us, 81 with two of 512)
+constexpr int kParts = 2;       // parts of a row that a workgroup counts by itself (with one, whose
+                                // atomics meet more often and of which all is read again, 256 rows
+                                // x 151936 took 40 us, 33 with two; 1024 rows 102, 87)
 constexpr int kNT32 = 1024;     // threads of the float32 kernel
 constexpr int kBase = 0x3580;  // bf16 pattern of 2^-20
 constexpr int kValues = 3584;  // counted values of a sign: up to 2^8
@@ -44,7 +59,7 @@ constexpr int kAbove = 64;      // words for what is larger, one to a lane
 constexpr int kStride = 3652;  // words of a part: below, kValues, kAbove, three unused
 constexpr int kRows = 2 * kValues / kWave;  // places in rows of 64, one to a lane
 constexpr int kRowGroups = 128;
-constexpr int kMaxSlices = 16;
+constexpr int kMaxSlices = 16;  // (8: 1 row 18.2 us, 18.1 with 16; 64 rows 27.3, 27.8)
 constexpr int kMaxTops = 1280;  // groups of a row whose maxima are kept
 constexpr uint32_t kListed = 256;  // equal logits of a part that are listed
 constexpr int kSmallCap = 64;  // gathered values below 2^-20

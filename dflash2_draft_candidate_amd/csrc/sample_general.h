@@ -18,6 +18,14 @@
 // (<= NT) they are gathered once, sorted, and everything is settled in that list. Otherwise each cut
 // gathers and sorts its own bin, which is split by value first if it holds more than NT tokens; when
 // a single value remains, its tokens are equal and a division tells how many of them a cut takes.
+//
+// The first pass is bound by its arithmetic where a row has a CU to itself (about 20 instructions a
+// logit, half of them fp64: 31 us for a row of 151936; 28 without the atomics) and by memory where
+// all CUs read (256 rows: 35 us, 4.4 TB/s). The rest is latency: running sums over the bins 2 us, a
+// cut's bin 2, bounds of bins 2, gathering 2 where few groups of 64 logits reach the range and up to
+// 12 where most do, sorting and sums 2-5 (by the tokens), cuts in the list 3. Groups of 32 logits
+// made the first pass 2 us longer and gained nothing; gathering with five vectors a thread in flight
+// in place of three was slower (256 rows 90 us against 86).
 #pragma once
 
 #include <float.h>
@@ -30,7 +38,7 @@ namespace dflash2 {
 constexpr int kPerOctave = 32;          // bins to a factor of two
 constexpr int kBins = 128 * kPerOctave;
 constexpr int kHeadroom = 40 * kPerOctave;  // the bin of the first estimate of the maximum
-constexpr int kFar = 64 * kPerOctave;       // weights from here on count as 0
+constexpr int kFar = 64 * kPerOctave;  // counts of bf16 values: weights from here on count as 0
 constexpr int kCountWords = 2 * 3652;
 constexpr double kBinsPerE = kPerOctave * 1.4426950408889634;
 constexpr double kTwo52 = 4503599627370496.0;
@@ -38,7 +46,6 @@ constexpr double kTwo52 = 4503599627370496.0;
 constexpr double kToBin = 1.5 * kTwo52 + kBins / 2;
 
 enum Cut { kNumber, kReach, kPass };  // the n-th token; first S >= target; first S > target
-
 
 // The settings of one row.
 struct RowSettings {
