@@ -297,6 +297,29 @@ def test_autograd(d2):
     assert bool(torch.isfinite(h.grad).all()) and bool(torch.isfinite(W.grad).all())
 
 
+def test_most_rows(d2):
+    log("distill, most rows")
+    R, V, K = 1 << 21, 3, 2
+    gen = torch.Generator(device=DEV).manual_seed(19)
+    z = torch.randn(R, V, generator=gen, device=DEV)
+    ids = torch.randint(-1, V, (R, K), generator=gen, device=DEV, dtype=torch.int32)
+    t = torch.randn(R, K, generator=gen, device=DEV)
+    g = torch.rand(R, generator=gen, device=DEV)
+    q = torch.softmax(z.double(), 1)
+    has = ids >= 0
+    p = torch.softmax(t.double().masked_fill(~has, -math.inf), 1).nan_to_num(0.0)
+    ln = torch.where(has, torch.log(p) - torch.log(q).gather(1, ids.clamp(min=0).long()), 0.0)
+    want = (p * ln).sum(1)
+    grad = q.clone().scatter_add_(1, ids.clamp(min=0).long(), torch.where(has, -p, 0.0))
+    grad = torch.where(has.any(1, keepdim=True), grad, 0.0) * g[:, None].double()
+    for loss, got in ((d2.distill_step(z, ids, t, g)),
+                      (d2.distill(z, ids, t)[0],
+                       d2.distill_backward(z, ids, t, d2.distill(z, ids, t)[1], g))):
+        assert bool(((loss.double() - want).abs() <= eps_sigma(V) + U * want.abs()).all())
+        lim = g[:, None].double() * (eps_sigma(V) + 200 * U) + U * grad.abs()
+        assert bool(((got.double() - grad).abs() <= lim).all())
+
+
 def test_no_gradient_needed(d2):
     z, ids, t, _ = inputs(3, 100, 4, torch.float32, 3)
     with torch.no_grad():

@@ -300,6 +300,32 @@ def test_very_long_rows(d2):
     assert clear and ids.tolist() == [want] * 256
 
 
+def test_most_rows_and_longest_row(d2):
+    log("sample, most rows")
+    R = 1 << 21
+    g = torch.Generator(device=DEV).manual_seed(13)
+    x = torch.randn(R, 3, generator=g, device=DEV)
+    u = torch.rand(R, generator=g, device=DEV)
+    top, order = torch.sort(x, dim=1, descending=True, stable=True)
+    w = torch.exp(top.double() - top[:, :1].double())
+    s = w.cumsum(1)
+    gap = (s - (u.double() * s[:, 2])[:, None]).abs().amin(1)
+    want = order.gather(1, (s <= (u.double() * s[:, 2])[:, None]).sum(1, keepdim=True))[:, 0]
+    ids, _ = d2.sample(x, u)
+    sure = gap > 2.0 ** -37
+    assert int((~sure).sum()) < 100 and torch.equal(ids[sure].long(), want[sure])
+    b = x.bfloat16()
+    ids, _ = d2.sample(b, u, temperature=0.0)
+    assert torch.equal(ids.long(), torch.sort(b, dim=1, descending=True, stable=True)[1][:, 0])
+    del x, b, s, w, top, order
+    V = 1 << 24
+    for dt in ("f32", "bf16"):
+        log(f"sample, longest row {dt}")
+        x, u = rows(1, V, dt, 17)
+        for kw in (dict(), dict(k=1000, p=0.9)):
+            check(d2, x, u, **kw)
+
+
 def test_extreme_settings(d2):
     x, u = rows(6, 3001, "f32", 8)
     check(d2, x, u, T=[1e-45, 1e-30, 1e30, 3e38, 100.0, 0.001])
