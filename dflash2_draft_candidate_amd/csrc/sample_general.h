@@ -110,7 +110,11 @@ __device__ __forceinline__ double weight_of(const Weights &w, float x) {
 __device__ __forceinline__ double bin_z(const Weights &w, float x) {
     return __builtin_fma((double)w.ref - (double)x, w.c, w.shift);
 }
-__device__ __forceinline__ bool has_bin(double z) { return fabs(z) < kBins / 2 - 1; }  // (no NaN has)
+// Whether the integer nearest to z is a bin's, up to kBins / 2 - 1 (a tie goes to kBins / 2): the same
+// integer decides which keys are a bin's (keys_of), so what is gathered of the last bin was counted. (With
+// |z| below that integer itself, half of the last bin was gathered without having been counted:
+// where a fill lay there, the list overflowed.) No NaN has a bin.
+__device__ __forceinline__ bool has_bin(double z) { return fabs(z) < kBins / 2 - 0.5; }
 __device__ __forceinline__ int bin_of(double z) {
     return (int)(uint32_t)__double_as_longlong(z + kToBin);
 }
@@ -574,9 +578,9 @@ static __device__ __forceinline__ bool keeps_tops(const UnitRange &ur) {
     return kTops > 1 && (ur.nv + 2 * NT - 1) / (2 * NT) * kGroups <= kTops;
 }
 
-// Gathers the tokens whose keys lie in `one` or `two` (at most kCap, known from the histogram). Only
-// groups whose maximum reaches the lowest of them can hold any; where those are few, the rest of the
-// row is not read again.
+// Gathers the tokens whose keys lie in `one` or `two`: at most kCap, known from the histogram, which
+// counted each logit by the bin or part that the keys were made from. Only groups whose maximum reaches
+// the lowest of them can hold any; where those are few, the rest of the row is not read again.
 static __device__ __forceinline__ Listed gather(const T *logits, const UnitRange &ur, Shared &sh,
                                          const Weights &w, const Keys &one, const Keys &two,
                                          int tid) {
