@@ -553,6 +553,7 @@ static __device__ __forceinline__ uint32_t first_key(int lane, F &&holds) {
 struct Keys {
     uint32_t lo, hi;  // lo <= key <= hi
 };
+static constexpr uint32_t kMinusZero = 0x7FFFFFFFu;  // key_value gives -0, value_key never this
 // The keys of the bins [a0, a1] and of [b0, b1]: four searches, a wave each (side by side they take
 // 2 us; by every wave, one after the other, 7).
 static __device__ __forceinline__ void keys_of(Shared &sh, const Weights &w, int a0, int a1, int b0,
@@ -830,6 +831,9 @@ static __device__ __forceinline__ Place cut_bin(const T *logits, const UnitRange
         keys.hi -= part << shift;
         const uint32_t width = (1u << shift) - 1u;
         if (keys.hi - keys.lo > width) keys.lo = keys.hi - width;
+        // (The key of -0 is no logit's, as zeros of both signs have that of +0. Logits are compared by
+        // value, so as an upper end it would let the zeros in, whose key lies above the range.)
+        if (keys.hi == kMinusZero) --keys.hi;
     }
     if (size > kCap) {
         const float value = key_value(keys.hi);
