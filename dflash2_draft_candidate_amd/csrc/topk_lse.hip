@@ -54,8 +54,6 @@
 //     other twelve waves absorb the delay. A gate rides along only where its tile parts fit in
 //     LDS beside the chunk sums of the pass's own plan (so select and the stage-by-stage calls
 //     sum the same chunks). Tiles are numbered XCD by XCD (see gate_tile_of).
-#include <atomic>
-
 #include "device_common.h"
 #include "gate_tile.h"
 #include "kernels.h"
@@ -1083,15 +1081,6 @@ size_t topk_workspace_bytes(const TopkPlan &p, int R) {
     return (size_t)R * p.slices * (kWave * sizeof(uint64_t) + sizeof(float2));
 }
 
-uint32_t next_launch_epoch() {
-    // (Counters lie in workspace that need not be initialised, and one that happened to hold this
-    // launch's epoch would be taken for its own: epochs start among NaN patterns, which neither
-    // logits, ids nor other counts leave behind, rather than among small integers.)
-    static std::atomic<uint32_t> launches{0x7FB10000u};
-    uint32_t e = launches.fetch_add(1, std::memory_order_relaxed) + 1u;
-    return e == 0u ? 1u : e;  // after 2^32 launches it wraps (the kernel then re-bases by CAS)
-}
-
 size_t topk_pass_workspace_bytes(int R, int V, int elem_bytes) {
     SmallPlanInfo sp;
     if (plan_small(R, V, elem_bytes, sp)) return small_workspace_bytes(sp, R);
@@ -1121,8 +1110,8 @@ hipError_t launch_topk_lse(const void *logits, int logits_dtype, int R, int V, i
                            hipStream_t stream, const FusedGate *gate) {
     SmallPlanInfo sp;
     if (plan_small(R, V, logits_dtype == 0 ? 4 : 2, sp))
-        return launch_topk_small(sp, logits, logits_dtype, R, V, k, next_launch_epoch(), cand_ids,
-                                 unary, lse, workspace, stream, gate);
+        return launch_topk_small(sp, logits, logits_dtype, R, V, k, cand_ids, unary, lse, workspace,
+                                 stream, gate);
     const int nt = gate ? fused_gate_nt(gate->r) : 0;
     if (gate && nt == 0) return hipErrorInvalidValue;
     const TopkPlan plan = plan_topk(R, V, logits_dtype == 0 ? 4 : 2);

@@ -19,20 +19,15 @@
 //     elements at or above it (one float compare each) are compacted into LDS, and sorted by
 //     waves 64 at a time, then merged. With very many (ties, flat slices) each wave's lanes offer
 //     them in rounds, largest first, one sort and merge per round, and the wave lists are merged.
-//   * slices: each slice writes its list and pair to the workspace with device-scope atomic
-//     stores (coherent across the XCDs' L2 caches), waits for them to complete and then counts
-//     itself in the row's arrival counter; the slice whose count completes the row reads the
-//     partials back with device-scope atomic loads, merges them (a tree over its waves) and writes
-//     the outputs. Device-scope release / acquire fences are not used: on gfx950 they write back
-//     or invalidate the whole L2 of the XCD, which cost more than the pass itself. The counter
-//     holds a launch epoch above the count: epochs grow from launch to launch, so an atomic max
-//     at the start re-bases a counter left by an earlier launch, and the last slice clears the
-//     count, so replays of a captured launch (same epoch) start from zero. Nothing waits on
-//     another workgroup.
+//   * slices: each slice writes its list and pair to the workspace; a second kernel, a workgroup per
+//     row, reads a row's partials back, merges them (a tree over its waves) and writes the outputs. (A
+//     slice that completes its row could do it in this launch, found by a counter; but counters
+//     would lie in workspace that need not be initialised, where a word left by other data can
+//     pass for a count of this launch whatever it is tagged with, and the row is lost.)
+//     16 rows of 151936 bf16, in a graph: 11.8 us; 12.0 with the last slice merging.
 //   * gate (optional): workgroups past the slices compute split-K tiles of hidden . W_sel with
 //     the stand-alone gate kernel's decomposition and summation order (gate_tile.h; its first
 //     four waves), so a fused selector call reproduces the stage-by-stage gate bit for bit.
-#include "arrival.h"
 #include "device_common.h"
 #include "gate_tile.h"
 #include "kernels.h"
@@ -68,7 +63,6 @@ struct SmallShared {
     uint32_t tw[kSmWaves];            // each wave's threshold (value key)
     uint32_t top4[kSmWaves * 4];      // each wave's four largest lane maxima (value keys)
     uint32_t ncand_all;
-    uint32_t last;                    // this workgroup's slice arrived last
 };
 
 // Out-of-line sort and merge (several waves call them; one copy of the code).
@@ -203,13 +197,13 @@ constexpr size_t gate_red_floats_small() {
 
 // Waves [h, 2h) hand their lists to waves [0, h), which merge them, for h = top, top / 2, ..., 1:
 // wave 0 ends with the merge of the first 2 * top waves' lists.
-__device__ __forceinline__ uint64_t tree_merge(SmallShared &sh, uint64_t list, int top, int wave,
-                                               int lane) {
+__device__ __forceinline__ uint64_t tree_merge(uint64_t (*lists)[kWave], uint64_t list, int top,
+                                               int wave, int lane) {
 #pragma unroll 1
     for (int h = top; h >= 1; h >>= 1) {
-        if (wave >= h && wave < 2 * h) sh.lists[wave][lane] = list;
+        if (wave >= h && wave < 2 * h) lists[wave][lane] = list;
         __syncthreads();
-        if (wave < h) list = merge_keys(list, sh.lists[wave + h][lane], lane);
+        if (wave < h) list = merge_keys(list, lists[wave + h][lane], lane);
     }
     return list;
 }
@@ -217,10 +211,9 @@ __device__ __forceinline__ uint64_t tree_merge(SmallShared &sh, uint64_t list, i
 // Grid: R * S slice workgroups, then (NTG > 0) gj.mtiles * gj.splits gate workgroups.
 template <typename T, int NTG>
 __global__ __launch_bounds__(kSmThreads) void topk_small_kernel(
-    const T *__restrict__ logits, int V, int k, int S, int n_units, uint32_t epoch,
+    const T *__restrict__ logits, int V, int k, int S, int n_units,
     int32_t *__restrict__ cand_ids, float *__restrict__ unary, float *__restrict__ lse_out,
-    uint64_t *__restrict__ part_keys, float2 *__restrict__ part_lse,
-    uint64_t *__restrict__ arrivals, SmallGate gj) {
+    uint64_t *__restrict__ part_keys, float2 *__restrict__ part_lse, SmallGate gj) {
     constexpr int EV = Elem<T>::kPerVec;
     __shared__ SmallShared sh;
     __shared__ float red[gate_red_floats_small<NTG>()];
@@ -249,10 +242,6 @@ __global__ __launch_bounds__(kSmThreads) void topk_small_kernel(
                 rsrc, ((int)threadIdx.x + i * kSmThreads) * 16, 0, kNonTemp);
         te.nmine += (int)threadIdx.x + i * kSmThreads < ur.nv ? 1 : 0;
     }
-    // Launch epochs grow, so an atomic max of (epoch, 0) re-bases a counter left by an earlier
-    // launch and leaves one of this launch alone; it is not waited for.
-    const int64_t row = unit / S;
-    if (S > 1 && threadIdx.x == 0) arrival_rebase(&arrivals[row], epoch);
     te.xh = te.xt = -INFINITY;
     const bool ragged = wave == 0 && (ur.h1 > ur.h0 || ur.t1 > ur.t0);
     if (ragged) {  // the ragged ends hold fewer than 2 * EV elements
@@ -348,16 +337,13 @@ __global__ __launch_bounds__(kSmThreads) void topk_small_kernel(
             lt = pick64(list, k - 1);
             cap = best;
         }
-        list = tree_merge(sh, list, kSmWaves / 2, wave, lane);
+        list = tree_merge(sh.lists, list, kSmWaves / 2, wave, lane);
     }
 
     // ---- the slice's list and pair (pairs in a fixed tree over the waves) ----
     if (wave == 0) {
-        // Publish the list first (a device-scope atomic store: coherent across the XCDs' L2
-        // caches), so that its write overlaps the pair tree.
-        if (S > 1)
-            __hip_atomic_store(&part_keys[(int64_t)unit * kWave + lane], list, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
+        // (the list's store overlaps the pair tree)
+        if (S > 1) part_keys[(int64_t)unit * kWave + lane] = list;
         float r0 = -INFINITY, s0 = 0.f;
         if (lane < kSmWaves) {
             r0 = sh.pairs[lane].x;
@@ -371,98 +357,87 @@ __global__ __launch_bounds__(kSmThreads) void topk_small_kernel(
         r0 = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(r0)));
         s0 = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(s0)));
         if (S == 1) {
+            const int64_t row = unit;
             const double lse = lse_value(r0, s0);
             if (lane < k) {
                 cand_ids[row * k + lane] = key_id(list);
                 unary[row * k + lane] = (float)((double)key_logit(list) - lse);
             }
             if (lane == 0 && lse_out) lse_out[row] = (float)lse;
-        } else {
-            // Publish the pair as the list; count the arrival only once both stores have
-            // completed, which orders them before the count without a release fence (that writes
-            // back the whole L2).
-            if (lane == 0)
-                __hip_atomic_store(reinterpret_cast<uint64_t *>(&part_lse[unit]),
-                                   ((uint64_t)__float_as_uint(s0) << 32) | __float_as_uint(r0),
-                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            stores_complete();
-            if (lane == 0) sh.last = arrive(&arrivals[row], epoch, (uint32_t)S) ? 1u : 0u;
+        } else if (lane == 0) {
+            part_lse[unit] = make_float2(r0, s0);
         }
     }
-    if (S == 1) return;
-    __syncthreads();
-    if (sh.last == 0u) return;
+}
 
-    // ---- the last slice: merge the row's S lists and pairs, write the outputs ----
-    // Every slice's partial was complete before it counted itself; the loads are device-scope
-    // atomic loads, which bypass stale lines in this XCD's L2. Lane i of wave w loads entry i < k
-    // of the lists of slices w, w + 16, ... (entries past k cannot reach the row's first k) and
-    // merges them; then the waves' lists are merged in a tree.
+// Waves of a row's merge: the power of two from S on, from 2 to 16.
+int merge_waves(int S) {
+    int n = 2;
+    while (n < S && n < kSmWaves) n *= 2;
+    return n;
+}
+
+// Merges a row's S lists and pairs and writes its outputs: a workgroup of merge_waves(S) waves per row.
+// Lane i of wave w loads entry i < k of the lists of slices w, w + 16, ... (entries past k cannot reach
+// the row's first k) and merges them; then the waves' lists are merged in a tree.
+__global__ __launch_bounds__(kSmThreads) void topk_small_merge_kernel(
+    int k, int S, const uint64_t *__restrict__ part_keys, const float2 *__restrict__ part_lse,
+    int32_t *__restrict__ cand_ids, float *__restrict__ unary, float *__restrict__ lse_out) {
+    __shared__ uint64_t lists[kSmWaves][kWave];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t row = blockIdx.x;
     constexpr int kPer = kSmMaxSlices / kSmWaves;
     const uint64_t *pk = part_keys + row * S * kWave;
     uint64_t got[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int sl = wave + i * kSmWaves;
-        got[i] = sl < S && lane < k ? __hip_atomic_load(&pk[sl * kWave + lane], __ATOMIC_RELAXED,
-                                                        __HIP_MEMORY_SCOPE_AGENT)
-                                    : 0ull;
+        got[i] = sl < S && lane < k ? pk[sl * kWave + lane] : 0ull;
     }
-    uint64_t pp = 0ull;
-    if (wave == 0 && lane < S)
-        pp = __hip_atomic_load(reinterpret_cast<uint64_t *>(&part_lse[row * S + lane]),
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    list = got[0];
+    float pr = -INFINITY, ps = 0.f;
+    if (wave == 0 && lane < S) {
+        pr = part_lse[row * S + lane].x;
+        ps = part_lse[row * S + lane].y;
+    }
+    uint64_t list = got[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i)
         if (wave + i * kSmWaves < S) list = merge_keys(list, got[i], lane);
-    int top = 1;  // the waves holding lists: min(S, 16), merged in a tree
-    while (2 * top < min(S, kSmWaves)) top *= 2;
-    list = tree_merge(sh, list, top, wave, lane);
+    list = tree_merge(lists, list, (int)blockDim.x / kWave / 2, wave, lane);
     if (wave != 0) return;
-    float pr = -INFINITY, ps = 0.f;
-    if (lane < S) {
-        pr = __uint_as_float((uint32_t)pp);
-        ps = __uint_as_float((uint32_t)(pp >> 32));
-    }
     wave_pair(pr, ps, lane);
     const double lse = lse_value(pr, ps);
     if (lane < k) {
         cand_ids[row * k + lane] = key_id(list);
         unary[row * k + lane] = (float)((double)key_logit(list) - lse);
     }
-    if (lane == 0) {
-        if (lse_out) lse_out[row] = (float)lse;
-        // every slice of this launch has counted itself: clear the count for a replay of the
-        // same launch (same epoch)
-        arrival_clear(&arrivals[row], epoch);
-    }
+    if (lane == 0 && lse_out) lse_out[row] = (float)lse;
 }
 
 template <typename T, int NTG>
 void launch_small_t(const SmallPlanInfo &p, const void *logits, int R, int V, int k,
-                    uint32_t epoch, int32_t *cand_ids, float *unary, float *lse, void *workspace,
+                    int32_t *cand_ids, float *unary, float *lse, void *workspace,
                     const SmallGate &gj, hipStream_t stream) {
     const int units = R * p.slices;
     uint64_t *keys = static_cast<uint64_t *>(workspace);
     float2 *pairs = reinterpret_cast<float2 *>(keys + (size_t)units * kWave);
-    uint64_t *arr = reinterpret_cast<uint64_t *>(pairs + units);
     const int grid = units + (NTG > 0 ? gj.mtiles * gj.splits : 0);
     hipLaunchKernelGGL((topk_small_kernel<T, NTG>), dim3((unsigned)grid), dim3(kSmThreads), 0,
-                       stream, static_cast<const T *>(logits), V, k, p.slices, units, epoch,
-                       cand_ids, unary, lse, keys, pairs, arr, gj);
+                       stream, static_cast<const T *>(logits), V, k, p.slices, units, cand_ids,
+                       unary, lse, keys, pairs, gj);
 }
 
 template <typename T>
 void launch_small_g(const SmallPlanInfo &p, int nt, const void *logits, int R, int V, int k,
-                    uint32_t epoch, int32_t *cand_ids, float *unary, float *lse, void *workspace,
+                    int32_t *cand_ids, float *unary, float *lse, void *workspace,
                     const SmallGate &gj, hipStream_t stream) {
     switch (nt) {
-    case 1: launch_small_t<T, 1>(p, logits, R, V, k, epoch, cand_ids, unary, lse, workspace, gj, stream); break;
-    case 2: launch_small_t<T, 2>(p, logits, R, V, k, epoch, cand_ids, unary, lse, workspace, gj, stream); break;
-    case 4: launch_small_t<T, 4>(p, logits, R, V, k, epoch, cand_ids, unary, lse, workspace, gj, stream); break;
-    case 8: launch_small_t<T, 8>(p, logits, R, V, k, epoch, cand_ids, unary, lse, workspace, gj, stream); break;
-    default: launch_small_t<T, 0>(p, logits, R, V, k, epoch, cand_ids, unary, lse, workspace, gj, stream); break;
+    case 1: launch_small_t<T, 1>(p, logits, R, V, k, cand_ids, unary, lse, workspace, gj, stream); break;
+    case 2: launch_small_t<T, 2>(p, logits, R, V, k, cand_ids, unary, lse, workspace, gj, stream); break;
+    case 4: launch_small_t<T, 4>(p, logits, R, V, k, cand_ids, unary, lse, workspace, gj, stream); break;
+    case 8: launch_small_t<T, 8>(p, logits, R, V, k, cand_ids, unary, lse, workspace, gj, stream); break;
+    default: launch_small_t<T, 0>(p, logits, R, V, k, cand_ids, unary, lse, workspace, gj, stream); break;
     }
 }
 
@@ -478,7 +453,7 @@ bool plan_small(int R, int V, int elem_bytes, SmallPlanInfo &p) {
     // streaming pass
     if (s_need > kSmMaxSlices || R * s_need > kSmTargetWgs) return false;
     // a row that one workgroup covers with a vector per thread stays whole: splitting it would
-    // save less than the slice merge costs (a store, an arrival and a load round trip)
+    // save less than the slice merge costs (a second launch)
     if (nvec <= kSmThreads) {
         p.slices = 1;
         return true;
@@ -495,7 +470,7 @@ bool plan_small(int R, int V, int elem_bytes, SmallPlanInfo &p) {
 size_t small_workspace_bytes(const SmallPlanInfo &p, int R) {
     if (p.slices <= 1) return 0;
     const size_t units = (size_t)R * p.slices;
-    return units * kWave * sizeof(uint64_t) + units * sizeof(float2) + (size_t)R * sizeof(uint64_t);
+    return units * kWave * sizeof(uint64_t) + units * sizeof(float2);
 }
 
 int small_gate_nt(int r) {
@@ -505,7 +480,7 @@ int small_gate_nt(int r) {
 }
 
 hipError_t launch_topk_small(const SmallPlanInfo &p, const void *logits, int logits_dtype, int R,
-                             int V, int k, uint32_t epoch, int32_t *cand_ids, float *unary,
+                             int V, int k, int32_t *cand_ids, float *unary,
                              float *lse, void *workspace, hipStream_t stream,
                              const FusedGate *gate) {
     SmallGate gj{};
@@ -523,11 +498,18 @@ hipError_t launch_topk_small(const SmallPlanInfo &p, const void *logits, int log
         gj.splits = gate_splits(R, gate->H, 1);
     }
     if (logits_dtype == 0)
-        launch_small_g<float>(p, nt, logits, R, V, k, epoch, cand_ids, unary, lse, workspace, gj,
+        launch_small_g<float>(p, nt, logits, R, V, k, cand_ids, unary, lse, workspace, gj,
                               stream);
     else
-        launch_small_g<uint16_t>(p, nt, logits, R, V, k, epoch, cand_ids, unary, lse, workspace,
+        launch_small_g<uint16_t>(p, nt, logits, R, V, k, cand_ids, unary, lse, workspace,
                                  gj, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.slices == 1) return e;
+    const uint64_t *keys = static_cast<const uint64_t *>(workspace);
+    const float2 *pairs = reinterpret_cast<const float2 *>(keys + (size_t)R * p.slices * kWave);
+    hipLaunchKernelGGL(topk_small_merge_kernel, dim3((unsigned)R),
+                       dim3((unsigned)(kWave * merge_waves(p.slices))), 0, stream, k, p.slices, keys,
+                       pairs, cand_ids, unary, lse);
     return hipGetLastError();
 }
 
