@@ -535,7 +535,13 @@ distill_held_kernel(const T *__restrict__ student, Args a, const float *__restri
     }
     // (nothing above -inf: the sum is 0, or NaN if the row holds one)
     const bool live = any && (m > -INFINITY || st.sum != st.sum);
-    const float coef = live ? g * (float)a.tau / sigma : 0.f;
+    // (g tau / sigma from mantissas and exponents: g tau alone may pass the largest number)
+    const float tau = (float)a.tau;
+    const float coef =
+        live ? __builtin_amdgcn_ldexpf(__builtin_amdgcn_frexp_mantf(g) *
+                                           __builtin_amdgcn_frexp_mantf(tau) / sigma,
+                                       __builtin_amdgcn_frexp_expf(g) + __builtin_amdgcn_frexp_expf(tau))
+             : 0.f;
     auto gradient = [&](float *x) {
 #pragma unroll
         for (int k = 0; k < EV; ++k)
