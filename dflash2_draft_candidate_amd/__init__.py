@@ -416,6 +416,12 @@ def _same_device(device: torch.device, *ts: torch.Tensor):
             raise ValueError("tensors must share a device")
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """`t`, or a copy where it does not start on 16 bytes (a slice t[1:] of a batch's numbers), as the
+    library asks of every pointer. For what has a few numbers per row; logits are not copied."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _setting(value, dtype: torch.dtype, R: int, what: str, logits: torch.Tensor):
     """A setting as (tensor or None, value for all rows)."""
     if not isinstance(value, torch.Tensor):
@@ -424,7 +430,7 @@ def _setting(value, dtype: torch.dtype, R: int, what: str, logits: torch.Tensor)
     if value.shape != (R,) or value.dtype != dtype:
         raise ValueError(f"{what} must be a number or [R] {dtype}")
     _same_device(logits.device, value)
-    return value, 0
+    return _aligned(value), 0
 
 
 def sample(logits: torch.Tensor, uniforms: torch.Tensor,
@@ -434,7 +440,8 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor,
     """A token per row of logits [R, V], drawn with uniforms [R] float32 in [0, 1): ->
     (token_ids [R] int32, logprob [R] f32 of the token among those kept). Each setting is a number
     or a tensor [R] (float32; top_k int32). temperature 0: greedy; top_k 0, top_p 1 and min_p 0:
-    no cut. `out` may be passed to reuse buffers."""
+    no cut. `out` may be passed to reuse buffers. logits must start on 16 bytes; the other tensors may
+    be slices that do not."""
     _contig(logits, uniforms)
     if logits.dim() != 2:
         raise ValueError("logits must be [R, V]")
@@ -459,12 +466,17 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor,
     _same_device(dev, token_ids, logprob)
     dt = _dtype(logits)
     ws = _workspace(_lib.dflash2_sample_workspace_bytes(R, V, dt), dev)
+    uniforms, ids, lp = _aligned(uniforms), _aligned(token_ids), _aligned(logprob)
     with _on(dev):
         rc = _lib.dflash2_sample(_ptr(logits), dt, R, V, _ptr(t), float(t_all), _ptr(k),
                                  k_all, _ptr(p), float(p_all), _ptr(m), float(m_all),
-                                 _ptr(uniforms), _ptr(token_ids), _ptr(logprob), _ptr(ws),
-                                 ws.numel(), _stream(dev))
+                                 _ptr(uniforms), _ptr(ids), _ptr(lp), _ptr(ws), ws.numel(),
+                                 _stream(dev))
     _check(rc, "dflash2_sample")
+    if ids is not token_ids:
+        token_ids.copy_(ids)
+    if lp is not logprob:
+        logprob.copy_(lp)
     return token_ids, logprob
 
 
@@ -482,29 +494,31 @@ def _distill_args(student: torch.Tensor, teacher_ids: torch.Tensor,
     if teacher_ids.dtype != torch.int32 or teacher_logits.dtype != torch.float32:
         raise TypeError("teacher_ids int32, teacher_logits float32")
     _same_device(student.device, teacher_ids, teacher_logits)
-    return R, V, K
+    return R, V, K, _aligned(teacher_ids), _aligned(teacher_logits)
 
 
-def _row_vector(t: torch.Tensor, R: int, what: str, student: torch.Tensor):
+def _row_vector(t: torch.Tensor, R: int, what: str, student: torch.Tensor) -> torch.Tensor:
     _contig(t)
     if t.shape != (R,) or t.dtype != torch.float32:
         raise ValueError(f"{what} must be [R] float32")
     _same_device(student.device, t)
+    return _aligned(t)
 
 
 def distill(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
             temperature: float = 1.0):
     """tau^2 KL(teacher's top entries || student) per row: student [R,V] logits, teacher_ids [R,K]
     int32 (-1: no entry), teacher_logits [R,K] f32 (topk_lse's cand_ids and unary) ->
-    (loss [R] f32, row_stats [R,2] f32, which distill_backward takes)."""
-    R, V, K = _distill_args(student, teacher_ids, teacher_logits)
+    (loss [R] f32, row_stats [R,2] f32, which distill_backward takes). student (and `out` of the calls
+    below) must start on 16 bytes; the other tensors may be slices that do not."""
+    R, V, K, ids, t = _distill_args(student, teacher_ids, teacher_logits)
     dev, dt = student.device, _dtype(student)
     loss = torch.empty((R,), dtype=torch.float32, device=dev)
     row_stats = torch.empty((R, 2), dtype=torch.float32, device=dev)
     ws = _workspace(_lib.dflash2_distill_workspace_bytes(R, V, dt), dev)
     with _on(dev):
-        rc = _lib.dflash2_distill(_ptr(student), dt, _ptr(teacher_ids), _ptr(teacher_logits), R, V,
-                                  K, float(temperature), _ptr(loss), _ptr(row_stats), _ptr(ws),
+        rc = _lib.dflash2_distill(_ptr(student), dt, _ptr(ids), _ptr(t), R, V, K,
+                                  float(temperature), _ptr(loss), _ptr(row_stats), _ptr(ws),
                                   ws.numel(), _stream(dev))
     _check(rc, "dflash2_distill")
     return loss, row_stats
@@ -516,18 +530,19 @@ def distill_backward(student: torch.Tensor, teacher_ids: torch.Tensor,
                      out: torch.Tensor | None = None):
     """The gradient of sum_i grad_loss[i] * loss[i] with respect to the student's logits, in their
     dtype, from distill()'s row_stats. `out` must not overlap `student`."""
-    R, V, K = _distill_args(student, teacher_ids, teacher_logits)
-    _row_vector(grad_loss, R, "grad_loss", student)
+    R, V, K, ids, t = _distill_args(student, teacher_ids, teacher_logits)
+    g = _row_vector(grad_loss, R, "grad_loss", student)
     _contig(row_stats)
     if row_stats.shape != (R, 2) or row_stats.dtype != torch.float32:
         raise ValueError("row_stats must be [R, 2] float32")
     _same_device(student.device, row_stats)
+    row_stats = _aligned(row_stats)
     dev = student.device
     grad = _gradient(student, out)
     with _on(dev):
-        rc = _lib.dflash2_distill_backward(_ptr(student), _dtype(student), _ptr(teacher_ids),
-                                           _ptr(teacher_logits), _ptr(row_stats), _ptr(grad_loss),
-                                           R, V, K, float(temperature), _ptr(grad), _stream(dev))
+        rc = _lib.dflash2_distill_backward(_ptr(student), _dtype(student), _ptr(ids), _ptr(t),
+                                           _ptr(row_stats), _ptr(g), R, V, K, float(temperature),
+                                           _ptr(grad), _stream(dev))
     _check(rc, "dflash2_distill_backward")
     return grad
 
@@ -547,16 +562,16 @@ def distill_step(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logit
                  out: torch.Tensor | None = None):
     """Loss and gradient in one call, for a training step that knows grad_loss [R] beforehand
     (weights / number of rows): -> (loss [R] f32, gradient [R,V] of the student's dtype)."""
-    R, V, K = _distill_args(student, teacher_ids, teacher_logits)
-    _row_vector(grad_loss, R, "grad_loss", student)
+    R, V, K, ids, t = _distill_args(student, teacher_ids, teacher_logits)
+    g = _row_vector(grad_loss, R, "grad_loss", student)
     dev, dt = student.device, _dtype(student)
     loss = torch.empty((R,), dtype=torch.float32, device=dev)
     grad = _gradient(student, out)
     ws = _workspace(_lib.dflash2_distill_workspace_bytes(R, V, dt), dev)
     with _on(dev):
-        rc = _lib.dflash2_distill_step(_ptr(student), dt, _ptr(teacher_ids), _ptr(teacher_logits),
-                                       _ptr(grad_loss), R, V, K, float(temperature), _ptr(loss),
-                                       _ptr(grad), _ptr(ws), ws.numel(), _stream(dev))
+        rc = _lib.dflash2_distill_step(_ptr(student), dt, _ptr(ids), _ptr(t), _ptr(g), R, V, K,
+                                       float(temperature), _ptr(loss), _ptr(grad), _ptr(ws),
+                                       ws.numel(), _stream(dev))
     _check(rc, "dflash2_distill_step")
     return loss, grad
 
@@ -573,11 +588,8 @@ class _DistillLoss(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
         student, teacher_ids, teacher_logits, row_stats = ctx.saved_tensors
-        grad_loss = grad_loss.contiguous()
-        if grad_loss.data_ptr() % 16:  # a view into another gradient
-            grad_loss = grad_loss.clone()
-        grad = distill_backward(student, teacher_ids, teacher_logits, row_stats, grad_loss,
-                                ctx.temperature)
+        grad = distill_backward(student, teacher_ids, teacher_logits, row_stats,
+                                grad_loss.contiguous(), ctx.temperature)
         return grad, None, None, None
 
 
