@@ -40,6 +40,8 @@
 //   256 rows float32: 85 us; the first pass 35 us, at the rate of a read, 64 rows 32 us: there the
 //     fp64 arithmetic of one CU per row is what it takes. Settling: 11 us a row whose cuts leave few
 //     tokens, about 25 us where 1024 tokens are gathered from most of the row.
+#include <stddef.h>
+
 #include "kernels.h"
 #include "sample_general.h"
 
@@ -65,8 +67,11 @@ constexpr uint32_t kListed = 256;  // equal logits of a part that are listed
 constexpr int kSmallCap = 64;  // gathered values below 2^-20
 static_assert(kCountWords == 2 * kStride && kStride >= 1 + kValues + kAbove, "counts in LDS");
 static_assert(kRows <= 2 * kWave && kValues % kWave == 0, "rows of places: two to a lane");
+static_assert(kStride % 4 == 0, "a part's words are whole 16-byte vectors");
 
 template <int NT> using S16 = RowSampler<uint16_t, NT>;
+static_assert(alignof(S16<kNT>::Shared) == 16 && offsetof(S16<kNT>::Shared, words) % 16 == 0,
+              "counts are accessed by 16-byte vectors");
 using S32 = RowSampler<float, kNT32>;
 
 struct Settings {

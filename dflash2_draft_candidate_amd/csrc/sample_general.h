@@ -165,7 +165,7 @@ static constexpr int kTops = sizeof(T) == 4 ? 4096 : 1;  // (bf16 rows come here
 static constexpr int kGroups = NT / 8;  // groups of an iteration of each: eight threads' vectors
 static constexpr int kParts = 1024;      // parts that a bin is split into
 
-struct Shared {
+struct alignas(16) Shared {  // (`words` is cleared and written by 16-byte vectors)
     union {
         struct {
             uint64_t mass[kBins];
