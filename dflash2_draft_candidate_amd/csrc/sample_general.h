@@ -943,7 +943,7 @@ static __device__ __forceinline__ void run(const T *logits, const UnitRange &ur,
     const bool by_number = top_k >= 1 && (uint32_t)top_k < h.number;
     const bool by_mass = top_p < 1.f;
     const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;
-    const bool by_weight = least > 0x1p-60;
+    const bool by_weight = least > 0x1p-64;  // (lower weights need not count)
     const int weight_bin =
         by_weight ? min((int)(top_z - kPerOctave * log2(least)) + 2, kBins - 1) : kBins - 1;
     bool mass_inside = false;  // the nucleus ends in the bins up to `low`
