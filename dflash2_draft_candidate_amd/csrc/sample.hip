@@ -813,7 +813,9 @@ hipError_t launch_sample(const void *logits, int dtype, int R, int V, const floa
                          hipStream_t stream) {
     const Settings st{temperature, top_k, top_p, min_p, uniforms, all_temperature, all_top_k,
                       all_top_p, all_min_p};
-    // a bin's sum of up to V factors stays below 2^63
+    // A bin's sum of up to V factors, each at most 1.011, stays below 2^64. (A weight errs by half a step
+    // of its factor: below 2^-40 of itself with 40 bits behind the point and more, below 2^-frac with
+    // fewer.)
     int bits = 0;
     while ((1ll << bits) <= V) ++bits;
     const int frac = bits <= 22 ? 41 : 63 - bits;

@@ -2,13 +2,15 @@
 // (any type, any values). sample.hip has the definitions and the faster path for bf16 rows.
 //
 // The token is a whole number that a rounding can change, and a flat row has more than 10^5 tokens
-// whose shares a 32-bit sum cannot tell apart: weights and masses are held to about 2^-40.
+// whose shares a 32-bit sum cannot tell apart: weights and masses are held to 2^-40 of themselves, up to
+// V = 2^23 - 1, and half as fine for each doubling from there, where the fixed point below moves.
 // With z = 32 log2(e) (ref - x) / T + shift in fp64 and b the integer nearest to it, a weight is, but for
 // a factor of the row, 2^(-b/32) 2^(-(z-b)/32); the second factor, within 1.1% of 1, is a polynomial
 // of degree 4 (error 1.6e-13, 1 at 0). b (counted from the middle of the bins) is also the weight's
 // bin: bins follow the candidate order, because z does. A bin's second factors are summed as 64-bit
-// integers (41 bits behind the point) by LDS atomics: whole numbers have no order of summation, so
-// results do not depend on which wave came first.
+// integers (41 bits behind the point up to V = 2^22 - 1, 62 - floor(log2 V) from there on, so that
+// V of them fit) by LDS atomics: whole numbers have no order of summation, so results do not depend on
+// which wave came first.
 //
 // One pass finds the maximum and fills the bins: ref is the largest of the first logits that the
 // workgroup loads (2 vectors a thread), with 40 octaves of bins left above it and 88 below. Only if
