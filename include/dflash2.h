@@ -280,7 +280,8 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
  *   logits       [R, V]  dtype, device. -inf (masked) and NaN logits are never drawn; +inf logits
  *                        share all of the weight.
  *   temperature  [R]     float, device, or NULL: all_temperature (>= 0, finite) for every row.
- *                        <= 0 or NaN in a row: greedy, the first token of the candidate order.
+ *                        <= 0 or NaN in a row: greedy, the first token of the candidate order;
+ *                        +inf in a row: every logit above -inf weighs the same.
  *   top_k        [R]     int32, device, or NULL: all_top_k. < 1: no cut.
  *   top_p        [R]     float, device, or NULL: all_top_p (not NaN). >= 1 or NaN: no cut.
  *   min_p        [R]     float, device, or NULL: all_min_p (not NaN). <= 0 or NaN: no cut; values
@@ -336,14 +337,16 @@ int dflash2_sample(const void *logits, int dtype, int R, int V, const float *tem
  *                          g tau (q_v - sum_{j: id_j = v} p_j), rounded once. Must not overlap
  *                          student (DFLASH2_ERR_INVALID_ARG).
  *   dflash2_distill computes loss and row_stats, dflash2_distill_backward the gradient from them,
- *   and dflash2_distill_step loss and gradient in one call (the student's logits come from HBM
- *   once); its loss and gradient are those of the two calls up to the rounding of row_stats.
+ *   and dflash2_distill_step loss and gradient in one call; its loss and gradient are those of the
+ *   two calls up to the rounding of row_stats. (From 128 rows on, rows of up to 163840 bf16 or 81920
+ *   float logits come from memory once; what longer rows have beyond that, short rows and few long
+ *   rows are read twice, the second time mostly from a cache.)
  *   Rows without a teacher entry, or without teacher mass: loss 0, gradient 0. Student logits of
  *   -inf (masked tokens) have q = 0 and gradient 0 where no teacher entry names them; an entry with
  *   mass at such a token makes the loss +inf (its gradient is -g tau p). A row whose student logits
  *   are all -inf has loss +inf and gradient 0. NaN, or +inf among the student's logits, makes the
- *   row's loss NaN and its gradient NaN; a NaN teacher logit makes the loss NaN, and the gradient at
- *   the row's entries.
+ *   row's loss NaN and its gradient NaN; a NaN or +inf teacher logit makes the loss NaN, and the
+ *   gradient at the row's entries.
  *   1 <= R <= DFLASH2_MAX_DISTILL_ROWS, 1 <= V <= DFLASH2_MAX_V, 1 <= K <= DFLASH2_MAX_K. Outputs and
  *   workspace overlap neither inputs nor each other.
  * Workspace of dflash2_distill and dflash2_distill_step: dflash2_distill_workspace_bytes(R, V,

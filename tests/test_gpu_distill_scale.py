@@ -40,3 +40,25 @@ def test_large_scale(R, V, dt):
             assert bool(torch.isfinite(grad).all())
             assert bool((grad[2, V // 2:] == 0).all()) and bool((grad[4] == 0).all())
             check(None, grad, ref, V, tau, g, dtype)
+
+
+@pytest.mark.parametrize("R,V", WAYS)
+def test_infinite_teacher_logit(R, V):
+    """+inf among the teacher's logits: the row's loss is NaN, and so is its gradient at the entries;
+    everywhere else, and in the other rows, the results are what they are without it."""
+    import dflash2_draft_candidate_amd as d2
+    K, tau = 5, 1.5
+    z, ids, t, g = inputs(R, V, K, torch.float32, 44)
+    ref = reference(z, ids, t, g, tau)
+    plain = run_all(d2, z, ids, t, g, tau)
+    t[3, 2] = math.inf
+    t[5] = math.inf
+    good = [r for r in range(R) if r not in (3, 5)]
+    for (loss, grad), (_, whole) in zip(run_all(d2, z, ids, t, g, tau), plain):
+        assert bool(torch.isnan(loss[[3, 5]]).all())
+        for r in (3, 5):
+            nan = torch.zeros(V, dtype=torch.bool, device=DEV)
+            nan[ids[r].long()] = True
+            assert torch.equal(torch.isnan(grad[r]), nan)
+            assert torch.equal(grad[r][~nan], whole[r][~nan])
+        check(loss[good], grad[good], tuple(x[good] for x in ref), V, tau, g[good], torch.float32)
