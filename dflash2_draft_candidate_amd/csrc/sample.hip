@@ -16,9 +16,10 @@
 // instructions per logit in place of an exponential, and the pass needs no maximum first.
 //   * Counted values: 2^-20 <= |x| < 2^8, 28 binades of 128 values, a word each: positive values
 //     in its low half, negative ones in its high half. A word below takes what is smaller, 64
-//     above what is larger (a lane has its own: the masked tokens of a row all count there, and
-//     atomics on one word take turns: 1024 rows x 151936 of which 90% are masked took 570 us with
-//     one word for them, 71 with 64). The row is counted in parts (words of their own), so that a
+//     above what is larger (from 382 on a lane has its own: the masked tokens of a row all count
+//     there, and atomics on one word take turns: 1024 rows x 151936 of which 90% are masked took
+//     570 us with one word for them, 71 with 64; of a finite mask nearer than that they still take
+//     320 to 590). The row is counted in parts (words of their own), so that a
 //     half-word is enough; a part's overflow shows as a wrong total.
 //   * Smaller values are rare (one in 10^6 of a normal row): up to 64 of them are listed and take
 //     their place between the positive and the negative values. Larger negative ones are masks,

@@ -301,8 +301,8 @@ int dflash2_lmhead_topk(const void *hidden, const void *W_lm, int R, int H, int 
  *   each doubling from there (2^-34 at V = 2^28; always 2^-40 on bf16's faster path); weights below
  *   2^-64 of the row's largest may count as 0. bf16 rows take a faster path where all logits that
  *   are not masked or far below the maximum lie in (-256, 256), at most 64 of them within 2^-20 of
- *   0, and no value occurs some 65536 times (masks of -256 and below may). A value that most of a
- *   row holds costs time on every path, unless it is such a mask.
+ *   0, and no value occurs some 65536 times (masks below -382 may). A value that most of a row
+ *   holds costs time, unless it is such a mask or, in float rows, has no weight.
  *   1 <= R <= DFLASH2_MAX_SAMPLE_ROWS, 1 <= V <= DFLASH2_MAX_V. Outputs and workspace overlap
  *   neither inputs nor each other.
  * Workspace: dflash2_sample_workspace_bytes(R, V, dtype) bytes (may be 0), contents need not be
