@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import torch  # loads the HIP runtime first, so libdflash2 binds to the same one
 
@@ -82,6 +83,25 @@ _lib.dflash2_distill_backward.restype = _ci
 _lib.dflash2_distill_step.argtypes = [_vp, _ci, _vp, _vp, _vp] + [_ci] * 3 + \
     [_cf, _vp, _vp, _vp, _sz, _vp]
 _lib.dflash2_distill_step.restype = _ci
+_lib.dflash2_lmhead_loss_workspace_bytes.argtypes = [_ci] * 5
+_lib.dflash2_lmhead_loss_workspace_bytes.restype = _sz
+_lib.dflash2_lmhead_ce.argtypes = [_vp, _vp, _ci, _vp] + [_ci] * 3 + [_vp, _vp, _vp, _sz, _vp]
+_lib.dflash2_lmhead_ce.restype = _ci
+_lib.dflash2_lmhead_ce_backward.argtypes = [_vp, _vp, _ci, _vp, _vp, _vp] + [_ci] * 3 + \
+    [_vp, _vp, _vp, _sz, _vp]
+_lib.dflash2_lmhead_ce_backward.restype = _ci
+_lib.dflash2_lmhead_distill.argtypes = [_vp, _vp, _ci, _vp, _vp] + [_ci] * 4 + \
+    [_cf, _vp, _vp, _vp, _sz, _vp]
+_lib.dflash2_lmhead_distill.restype = _ci
+_lib.dflash2_lmhead_distill_backward.argtypes = [_vp, _vp, _ci, _vp, _vp, _vp, _vp] + \
+    [_ci] * 4 + [_cf, _vp, _vp, _vp, _sz, _vp]
+_lib.dflash2_lmhead_distill_backward.restype = _ci
+_lib.dflash2_grad_norm_workspace_bytes.argtypes = []
+_lib.dflash2_grad_norm_workspace_bytes.restype = _sz
+_lib.dflash2_grad_norm.argtypes = [_vp, _vp, _vp, _ci, _vp, _vp, _sz, _vp]
+_lib.dflash2_grad_norm.restype = _ci
+_lib.dflash2_clip_grads.argtypes = [_vp, _vp, _vp, _ci, _vp, _cf, _vp, _vp, _sz, _vp]
+_lib.dflash2_clip_grads.restype = _ci
 
 EXPORTS = ("dflash2_version", "dflash2_status_string", "dflash2_workspace_bytes",
            "dflash2_select", "dflash2_select_noalloc", "dflash2_topk_lse_workspace_bytes", "dflash2_topk_lse",
@@ -89,7 +109,10 @@ EXPORTS = ("dflash2_version", "dflash2_status_string", "dflash2_workspace_bytes"
            "dflash2_select_ex", "dflash2_walk_ex", "dflash2_dynconv",
            "dflash2_lmhead_topk_workspace_bytes", "dflash2_lmhead_topk",
            "dflash2_sample_workspace_bytes", "dflash2_sample", "dflash2_distill_workspace_bytes", "dflash2_distill", "dflash2_distill_backward",
-           "dflash2_distill_step")
+           "dflash2_distill_step", "dflash2_lmhead_loss_workspace_bytes", "dflash2_lmhead_ce",
+           "dflash2_lmhead_ce_backward", "dflash2_lmhead_distill",
+           "dflash2_lmhead_distill_backward", "dflash2_grad_norm_workspace_bytes",
+           "dflash2_grad_norm", "dflash2_clip_grads")
 
 
 class Dflash2Error(RuntimeError):
@@ -600,3 +623,230 @@ def distill_loss(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logit
     if teacher_logits.requires_grad:
         raise ValueError("teacher_logits is a constant of the loss: detach it")
     return _DistillLoss.apply(student, teacher_ids, teacher_logits, float(temperature))
+
+
+# ---- losses of the LM head's product, without its logits --------------------------------------
+
+def _head_args(hidden: torch.Tensor, W_lm: torch.Tensor):
+    _contig(hidden, W_lm)
+    if hidden.dim() != 2 or W_lm.dim() != 2 or hidden.shape[1] != W_lm.shape[1]:
+        raise ValueError("hidden [R, H] and W_lm [V, H]")
+    if hidden.dtype != W_lm.dtype:
+        raise TypeError("hidden and W_lm must share a dtype")
+    _same_device(hidden.device, W_lm)
+    R, H = hidden.shape
+    return R, H, W_lm.shape[0], _dtype(hidden)
+
+
+def _targets(targets: torch.Tensor, R: int, hidden: torch.Tensor) -> torch.Tensor:
+    _contig(targets)
+    if targets.shape != (R,):
+        raise ValueError("targets must be [R]")
+    if targets.dtype != torch.int32:
+        raise TypeError("targets must be int32")
+    _same_device(hidden.device, targets)
+    return _aligned(targets)
+
+
+def _teacher(teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, R: int,
+             hidden: torch.Tensor):
+    _contig(teacher_ids, teacher_logits)
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != R or \
+            teacher_logits.shape != teacher_ids.shape:
+        raise ValueError("teacher_ids and teacher_logits must be [R, K]")
+    if teacher_ids.dtype != torch.int32 or teacher_logits.dtype != torch.float32:
+        raise TypeError("teacher_ids int32, teacher_logits float32")
+    _same_device(hidden.device, teacher_ids, teacher_logits)
+    return teacher_ids.shape[1], _aligned(teacher_ids), _aligned(teacher_logits)
+
+
+def _head_forward(call, what: str, hidden: torch.Tensor, W_lm: torch.Tensor, R: int, H: int,
+                  V: int, K: int, dt: int, side: tuple, sizes: tuple):
+    dev = hidden.device
+    loss = torch.empty((R,), dtype=torch.float32, device=dev)
+    row_stats = torch.empty((R, K + 2), dtype=torch.float32, device=dev)
+    ws = _workspace(_lib.dflash2_lmhead_loss_workspace_bytes(R, H, V, dt, 0), dev)
+    with _on(dev):
+        rc = call(_ptr(hidden), _ptr(W_lm), dt, *map(_ptr, side), R, H, V, *sizes, _ptr(loss),
+                  _ptr(row_stats), _ptr(ws), ws.numel(), _stream(dev))
+    _check(rc, what)
+    return loss, row_stats
+
+
+def _head_backward(call, what: str, hidden: torch.Tensor, W_lm: torch.Tensor, R: int, H: int,
+                   V: int, K: int, dt: int, side: tuple, sizes: tuple, row_stats: torch.Tensor,
+                   grad_loss: torch.Tensor, need_hidden: bool, need_weight: bool):
+    _contig(row_stats)
+    if row_stats.shape != (R, K + 2) or row_stats.dtype != torch.float32:
+        raise ValueError("row_stats must be [R, K + 2] float32")
+    _same_device(hidden.device, row_stats)
+    g = _row_vector(grad_loss, R, "grad_loss", hidden)
+    if not need_hidden and not need_weight:
+        return None, None
+    dev = hidden.device
+    stats = _aligned(row_stats)
+    grad_hidden = torch.empty_like(hidden) if need_hidden else None
+    grad_W = torch.empty_like(W_lm) if need_weight else None
+    ws = _workspace(_lib.dflash2_lmhead_loss_workspace_bytes(R, H, V, dt, 1), dev)
+    with _on(dev):
+        rc = call(_ptr(hidden), _ptr(W_lm), dt, *map(_ptr, side), _ptr(stats), _ptr(g), R, H, V,
+                  *sizes, _ptr(grad_hidden), _ptr(grad_W), _ptr(ws), ws.numel(), _stream(dev))
+    _check(rc, what)
+    return grad_hidden, grad_W
+
+
+def lmhead_ce(hidden: torch.Tensor, W_lm: torch.Tensor, targets: torch.Tensor):
+    """Softmax cross entropy of hidden [R,H] . W_lm [V,H]^T with targets [R] int32 (-1: none; loss
+    0), without the logits: -> (loss [R] f32, row_stats [R,3] f32, which lmhead_ce_backward takes).
+    hidden and W_lm share a dtype and start on 16 bytes; H % 8 == 0."""
+    R, H, V, dt = _head_args(hidden, W_lm)
+    t = _targets(targets, R, hidden)
+    return _head_forward(_lib.dflash2_lmhead_ce, "dflash2_lmhead_ce", hidden, W_lm, R, H, V, 1, dt,
+                         (t,), ())
+
+
+def lmhead_ce_backward(hidden: torch.Tensor, W_lm: torch.Tensor, targets: torch.Tensor,
+                       row_stats: torch.Tensor, grad_loss: torch.Tensor,
+                       need_hidden: bool = True, need_weight: bool = True):
+    """The gradients of sum_i grad_loss[i] * loss[i], from lmhead_ce()'s row_stats: ->
+    (grad_hidden [R,H], grad_W [V,H]) of the inputs' dtype, None for one that is not needed."""
+    R, H, V, dt = _head_args(hidden, W_lm)
+    t = _targets(targets, R, hidden)
+    return _head_backward(_lib.dflash2_lmhead_ce_backward, "dflash2_lmhead_ce_backward", hidden,
+                          W_lm, R, H, V, 1, dt, (t,), (), row_stats, grad_loss, need_hidden,
+                          need_weight)
+
+
+def lmhead_distill(hidden: torch.Tensor, W_lm: torch.Tensor, teacher_ids: torch.Tensor,
+                   teacher_logits: torch.Tensor, temperature: float = 1.0):
+    """distill() of the logits hidden [R,H] . W_lm [V,H]^T, without the logits: -> (loss [R] f32,
+    row_stats [R,K+2] f32, which lmhead_distill_backward takes). hidden and W_lm share a dtype and
+    start on 16 bytes; H % 8 == 0."""
+    R, H, V, dt = _head_args(hidden, W_lm)
+    K, ids, t = _teacher(teacher_ids, teacher_logits, R, hidden)
+    return _head_forward(_lib.dflash2_lmhead_distill, "dflash2_lmhead_distill", hidden, W_lm, R, H,
+                         V, K, dt, (ids, t), (K, float(temperature)))
+
+
+def lmhead_distill_backward(hidden: torch.Tensor, W_lm: torch.Tensor, teacher_ids: torch.Tensor,
+                            teacher_logits: torch.Tensor, row_stats: torch.Tensor,
+                            grad_loss: torch.Tensor, temperature: float = 1.0,
+                            need_hidden: bool = True, need_weight: bool = True):
+    """The gradients of sum_i grad_loss[i] * loss[i], from lmhead_distill()'s row_stats: ->
+    (grad_hidden [R,H], grad_W [V,H]) of the inputs' dtype, None for one that is not needed."""
+    R, H, V, dt = _head_args(hidden, W_lm)
+    K, ids, t = _teacher(teacher_ids, teacher_logits, R, hidden)
+    return _head_backward(_lib.dflash2_lmhead_distill_backward, "dflash2_lmhead_distill_backward",
+                          hidden, W_lm, R, H, V, K, dt, (ids, t), (K, float(temperature)),
+                          row_stats, grad_loss, need_hidden, need_weight)
+
+
+class _LmheadCeLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, W_lm, targets):
+        loss, row_stats = lmhead_ce(hidden, W_lm, targets)
+        ctx.save_for_backward(hidden, W_lm, targets, row_stats)
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        hidden, W_lm, targets, row_stats = ctx.saved_tensors
+        gh, gw = lmhead_ce_backward(hidden, W_lm, targets, row_stats, grad_loss.contiguous(),
+                                    ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return gh, gw, None
+
+
+def lmhead_ce_loss(hidden: torch.Tensor, W_lm: torch.Tensor, targets: torch.Tensor) -> torch.Tensor:
+    """lmhead_ce() under autograd: loss [R] f32, differentiable (once) in hidden and W_lm; a head
+    that needs no gradient (frozen) costs none."""
+    return _LmheadCeLoss.apply(hidden, W_lm, targets)
+
+
+class _LmheadDistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, W_lm, teacher_ids, teacher_logits, temperature):
+        loss, row_stats = lmhead_distill(hidden, W_lm, teacher_ids, teacher_logits, temperature)
+        ctx.save_for_backward(hidden, W_lm, teacher_ids, teacher_logits, row_stats)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        hidden, W_lm, teacher_ids, teacher_logits, row_stats = ctx.saved_tensors
+        gh, gw = lmhead_distill_backward(hidden, W_lm, teacher_ids, teacher_logits, row_stats,
+                                         grad_loss.contiguous(), ctx.temperature,
+                                         ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return gh, gw, None, None, None
+
+
+def lmhead_distill_loss(hidden: torch.Tensor, W_lm: torch.Tensor, teacher_ids: torch.Tensor,
+                        teacher_logits: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
+    """lmhead_distill() under autograd: loss [R] f32, differentiable (once) in hidden and W_lm. The
+    teacher's side is a constant."""
+    if teacher_logits.requires_grad:
+        raise ValueError("teacher_logits is a constant of the loss: detach it")
+    return _LmheadDistillLoss.apply(hidden, W_lm, teacher_ids, teacher_logits, float(temperature))
+
+
+# ---- the global gradient norm, and clipping ----------------------------------------------------
+
+def _addresses(ts: list) -> array:
+    return array("Q", [t.data_ptr() for t in ts])
+
+
+def _grads(grads):
+    """The gradients as a list, and their sizes and types as host arrays."""
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    _contig(*grads)
+    _same_device(grads[0].device, *grads)
+    return grads, array("q", [t.numel() for t in grads]), array("i", [_dtype(t) for t in grads])
+
+
+def _host(a: array) -> int:
+    return a.buffer_info()[0]
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The 2-norm over all gradients (a tensor, or tensors of float32 or bfloat16): a float32 scalar
+    on their device."""
+    grads, sizes, dtypes = _grads(grads)
+    dev = grads[0].device
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = _workspace(_lib.dflash2_grad_norm_workspace_bytes(), dev)
+    addresses = _addresses(grads)
+    with _on(dev):
+        rc = _lib.dflash2_grad_norm(_host(addresses), _host(sizes), _host(dtypes), len(grads),
+                                    _ptr(norm), _ptr(ws), ws.numel(), _stream(dev))
+    _check(rc, "dflash2_grad_norm")
+    return norm
+
+
+def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / norm), in place or into `out` (a tensor for each,
+    of its shape and type): -> their norm, as grad_norm() gives it. A norm that is not finite scales
+    nothing."""
+    grads, sizes, dtypes = _grads(grads)
+    dev = grads[0].device
+    if out is None:
+        outs = grads
+    else:
+        outs = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(outs) != len(grads) or any(o.shape != g.shape or o.dtype != g.dtype
+                                          for o, g in zip(outs, grads)):
+            raise ValueError("out must have the gradients' shapes and dtypes")
+        _contig(*outs)
+        _same_device(dev, *outs)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = _workspace(_lib.dflash2_grad_norm_workspace_bytes(), dev)
+    addresses = _addresses(grads)
+    out_addresses = addresses if outs is grads else _addresses(outs)
+    with _on(dev):
+        rc = _lib.dflash2_clip_grads(_host(addresses), _host(sizes), _host(dtypes), len(grads),
+                                     _host(out_addresses), float(max_norm), _ptr(norm), _ptr(ws),
+                                     ws.numel(), _stream(dev))
+    _check(rc, "dflash2_clip_grads")
+    return norm

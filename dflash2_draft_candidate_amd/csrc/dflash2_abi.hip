@@ -354,6 +354,161 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
                                           workspace, static_cast<hipStream_t>(stream)));
 }
 
+// Sizes shared by the losses of the LM head's product.
+static int check_lmhead_loss(int dtype, int R, int H, int V, int K, float temperature) {
+    if (!dtype_ok(dtype) || R < 1 || R > DFLASH2_MAX_LMHEAD_LOSS_ROWS || H < 8 || H % 8 != 0 ||
+        H > DFLASH2_MAX_LMHEAD_LOSS_H || V < 1 || V > DFLASH2_MAX_V || K < 1 ||
+        K > DFLASH2_MAX_K || !(temperature >= FLT_MIN) || !(temperature <= FLT_MAX))
+        return DFLASH2_ERR_INVALID_ARG;
+    return DFLASH2_OK;
+}
+
+static int elem_bytes(int dtype) { return dtype == DFLASH2_F32 ? 4 : 2; }
+
+size_t dflash2_lmhead_loss_workspace_bytes(int R, int H, int V, int dtype, int backward) {
+    if (check_lmhead_loss(dtype, R, H, V, 1, 1.f) != DFLASH2_OK) return 0;
+    return backward ? lmloss_backward_workspace_bytes(R, H, V, elem_bytes(dtype))
+                    : lmloss_workspace_bytes(R, H, V, elem_bytes(dtype));
+}
+
+static int lmhead_loss(const void *hidden, const void *W_lm, int dtype, const int32_t *ids,
+                       const float *teacher, int R, int H, int V, int K, float temperature,
+                       float *loss, float *row_stats, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+    int rc = check_workspace(workspace, workspace_bytes,
+                             dflash2_lmhead_loss_workspace_bytes(R, H, V, dtype, 0));
+    if (rc) return rc;
+    return hip_status(launch_lmloss(hidden, W_lm, elem_bytes(dtype), ids, teacher, R, H, V, K,
+                                    temperature, loss, row_stats, workspace,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+static int lmhead_loss_backward(const void *hidden, const void *W_lm, int dtype,
+                                const int32_t *ids, const float *teacher, const float *row_stats,
+                                const float *grad_loss, int R, int H, int V, int K,
+                                float temperature, void *grad_hidden, void *grad_W,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    if (!grad_hidden && !grad_W) return DFLASH2_ERR_INVALID_ARG;
+    const size_t hb = (size_t)R * H * elem_bytes(dtype), wb = (size_t)V * H * elem_bytes(dtype);
+    for (void *out : {grad_hidden, grad_W}) {
+        if (!out) continue;
+        if (!aligned16(out)) return DFLASH2_ERR_ALIGNMENT;
+        const size_t n = out == grad_hidden ? hb : wb;
+        if (overlap(out, n, hidden, hb) || overlap(out, n, W_lm, wb))
+            return DFLASH2_ERR_INVALID_ARG;
+    }
+    if (grad_hidden && grad_W && overlap(grad_hidden, hb, grad_W, wb))
+        return DFLASH2_ERR_INVALID_ARG;
+    const int rc = check_workspace(workspace, workspace_bytes,
+                                   dflash2_lmhead_loss_workspace_bytes(R, H, V, dtype, 1));
+    if (rc) return rc;
+    return hip_status(launch_lmloss_backward(
+        hidden, W_lm, elem_bytes(dtype), ids, teacher, row_stats, grad_loss, R, H, V, K,
+        temperature, grad_hidden, grad_W, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int dflash2_lmhead_ce(const void *hidden, const void *W_lm, int dtype, const int32_t *targets,
+                      int R, int H, int V, float *loss, float *row_stats, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    int rc = check_lmhead_loss(dtype, R, H, V, 1, 1.f);
+    if (rc) return rc;
+    if ((rc = check_ptrs({hidden, W_lm, targets, loss, row_stats}))) return rc;
+    return lmhead_loss(hidden, W_lm, dtype, targets, nullptr, R, H, V, 1, 1.f, loss, row_stats,
+                       workspace, workspace_bytes, stream);
+}
+
+int dflash2_lmhead_ce_backward(const void *hidden, const void *W_lm, int dtype,
+                               const int32_t *targets, const float *row_stats,
+                               const float *grad_loss, int R, int H, int V, void *grad_hidden,
+                               void *grad_W, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+    int rc = check_lmhead_loss(dtype, R, H, V, 1, 1.f);
+    if (rc) return rc;
+    if ((rc = check_ptrs({hidden, W_lm, targets, row_stats, grad_loss}))) return rc;
+    return lmhead_loss_backward(hidden, W_lm, dtype, targets, nullptr, row_stats, grad_loss, R, H,
+                                V, 1, 1.f, grad_hidden, grad_W, workspace, workspace_bytes,
+                                stream);
+}
+
+int dflash2_lmhead_distill(const void *hidden, const void *W_lm, int dtype,
+                           const int32_t *teacher_ids, const float *teacher_logits, int R, int H,
+                           int V, int K, float temperature, float *loss, float *row_stats,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_lmhead_loss(dtype, R, H, V, K, temperature);
+    if (rc) return rc;
+    if ((rc = check_ptrs({hidden, W_lm, teacher_ids, teacher_logits, loss, row_stats}))) return rc;
+    return lmhead_loss(hidden, W_lm, dtype, teacher_ids, teacher_logits, R, H, V, K, temperature,
+                       loss, row_stats, workspace, workspace_bytes, stream);
+}
+
+int dflash2_lmhead_distill_backward(const void *hidden, const void *W_lm, int dtype,
+                                    const int32_t *teacher_ids, const float *teacher_logits,
+                                    const float *row_stats, const float *grad_loss, int R, int H,
+                                    int V, int K, float temperature, void *grad_hidden,
+                                    void *grad_W, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    int rc = check_lmhead_loss(dtype, R, H, V, K, temperature);
+    if (rc) return rc;
+    if ((rc = check_ptrs({hidden, W_lm, teacher_ids, teacher_logits, row_stats, grad_loss})))
+        return rc;
+    return lmhead_loss_backward(hidden, W_lm, dtype, teacher_ids, teacher_logits, row_stats,
+                                grad_loss, R, H, V, K, temperature, grad_hidden, grad_W, workspace,
+                                workspace_bytes, stream);
+}
+
+// The gradients of dflash2_grad_norm and dflash2_clip_grads: types, sizes, addresses on an element.
+static int check_grads(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                       int count) {
+    if (count < 0 || count > DFLASH2_MAX_GRADS || (count > 0 && (!grads || !sizes || !dtypes)))
+        return DFLASH2_ERR_INVALID_ARG;
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) {
+        if (!dtype_ok(dtypes[i]) || sizes[i] < 0 || sizes[i] > DFLASH2_MAX_GRAD_ELEMENTS)
+            return DFLASH2_ERR_INVALID_ARG;
+        if (sizes[i] > 0 && !grads[i]) return DFLASH2_ERR_INVALID_ARG;
+        total += sizes[i];
+    }
+    if (total > DFLASH2_MAX_GRAD_ELEMENTS) return DFLASH2_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i)
+        if (sizes[i] > 0 && reinterpret_cast<uintptr_t>(grads[i]) % elem_bytes(dtypes[i]) != 0)
+            return DFLASH2_ERR_ALIGNMENT;
+    return DFLASH2_OK;
+}
+
+size_t dflash2_grad_norm_workspace_bytes(void) { return grad_norm_workspace_bytes(); }
+
+int dflash2_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                      int count, float *norm, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    int rc = check_grads(grads, sizes, dtypes, count);
+    if (rc) return rc;
+    if ((rc = check_ptrs({norm}))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, grad_norm_workspace_bytes()))) return rc;
+    return hip_status(launch_clip_grads(grads, sizes, dtypes, count, nullptr, 0.f, norm, workspace,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int dflash2_clip_grads(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                       int count, void *const *out, float max_norm, float *norm, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    int rc = check_grads(grads, sizes, dtypes, count);
+    if (rc) return rc;
+    if ((count > 0 && !out) || !(max_norm >= 0.f) || !(max_norm <= FLT_MAX))
+        return DFLASH2_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const size_t n = (size_t)sizes[i] * elem_bytes(dtypes[i]);
+        if (!out[i] || (out[i] != grads[i] && overlap(out[i], n, grads[i], n)))
+            return DFLASH2_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(out[i]) % elem_bytes(dtypes[i]) != 0)
+            return DFLASH2_ERR_ALIGNMENT;
+    }
+    if ((rc = check_ptrs({norm}))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, grad_norm_workspace_bytes()))) return rc;
+    return hip_status(launch_clip_grads(grads, sizes, dtypes, count, out, max_norm, norm, workspace,
+                                        static_cast<hipStream_t>(stream)));
+}
+
 size_t dflash2_workspace_bytes(int B, int L, int V, int H, int r, int k) {
     if (B < 1 || L < 1 || H < 1 || r < 1 || r > DFLASH2_MAX_R || rows_of(B, L) > INT_MAX ||
         check_rows((int)rows_of(B, L), V, k) != DFLASH2_OK)

@@ -122,4 +122,27 @@ hipError_t launch_distill_step(const void *student, int dtype, const int32_t *id
                                const float *teacher, const float *grad_loss, int R, int V, int K,
                                float tau, float *loss, void *grad, void *ws, hipStream_t stream);
 
+// ---- losses of the LM head's product, without its logits --------------------------------------
+// hidden [R, H] and W [V, H] of elem_bytes (2: bf16, 4: f32), H % 8 == 0; ids [R, K]; teacher [R, K]
+// or null (K = 1: a target token). row_stats [R, K + 2]. grad_hidden [R, H] and grad_W [V, H] of
+// the same type, either may be null. Workspaces: lmloss_workspace_bytes (forward),
+// lmloss_backward_workspace_bytes.
+size_t lmloss_workspace_bytes(int R, int H, int V, int elem_bytes);
+size_t lmloss_backward_workspace_bytes(int R, int H, int V, int elem_bytes);
+hipError_t launch_lmloss(const void *hidden, const void *W, int elem_bytes, const int32_t *ids,
+                         const float *teacher, int R, int H, int V, int K, float tau, float *loss,
+                         float *row_stats, void *ws, hipStream_t stream);
+hipError_t launch_lmloss_backward(const void *hidden, const void *W, int elem_bytes,
+                                  const int32_t *ids, const float *teacher, const float *row_stats,
+                                  const float *grad_loss, int R, int H, int V, int K, float tau,
+                                  void *grad_hidden, void *grad_W, void *ws, hipStream_t stream);
+
+// ---- the global gradient norm, and clipping -----------------------------------------------------
+// Host arrays of `count` tensors (dtypes: the C ABI's); out null: the norm alone. Workspace:
+// grad_norm_workspace_bytes.
+size_t grad_norm_workspace_bytes();
+hipError_t launch_clip_grads(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                             int count, void *const *out, float max_norm, float *norm, void *ws,
+                             hipStream_t stream);
+
 }  // namespace dflash2

@@ -52,6 +52,10 @@ extern "C" {
 #define DFLASH2_LMHEAD_MAX_ROWS 16 /* largest R of dflash2_lmhead_topk (one 16-row tile) */
 #define DFLASH2_MAX_SAMPLE_ROWS (1 << 21)  /* largest R of dflash2_sample */
 #define DFLASH2_MAX_DISTILL_ROWS (1 << 21) /* largest R of the dflash2_distill calls */
+#define DFLASH2_MAX_LMHEAD_LOSS_ROWS (1 << 16) /* largest R of the dflash2_lmhead_ce/_distill calls */
+#define DFLASH2_MAX_LMHEAD_LOSS_H (1 << 16)    /* and their largest H */
+#define DFLASH2_MAX_GRADS (1 << 16)                     /* most tensors of dflash2_clip_grads */
+#define DFLASH2_MAX_GRAD_ELEMENTS ((int64_t)1 << 40)    /* and their elements, all together */
 
 typedef enum dflash2_dtype {
     DFLASH2_F32 = 0,  /* IEEE binary32 */
@@ -365,6 +369,92 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
                          const float *teacher_logits, const float *grad_loss, int R, int V, int K,
                          float temperature, float *loss, void *grad_student, void *workspace,
                          size_t workspace_bytes, void *stream);
+
+/*
+ * dflash2_lmhead_ce, dflash2_lmhead_distill and their backward calls - losses of the LM head's
+ *   product, from the hidden states on: softmax cross entropy with target tokens, and the
+ *   distillation loss of dflash2_distill. The [R, V] logits are never in memory.
+ *
+ *   hidden         [R, H]  dtype, device, row-major.
+ *   W_lm           [V, H]  dtype, device, row-major (one row per vocabulary token).
+ *   targets        [R]     int32, device. An id outside [0, V) is no target (-1: ignored rows).
+ *   teacher_ids    [R, K]  int32, teacher_logits [R, K] float, device, as in dflash2_distill: an id
+ *                          outside [0, V) is no entry, one that occurs twice counts twice, -inf is
+ *                          an entry without mass.
+ *   temperature    tau > 0 (finite and normal).
+ *   With x = hidden . W_lm^T (products of the stored values, fp32 sums), q = softmax(x / tau) and
+ *   p = softmax(t / tau) over the row's entries (cross entropy: tau = 1, p = 1 at the target):
+ *   loss           [R]     float, device, out. tau^2 sum_j p_j (ln p_j - ln q[id_j]).
+ *   row_stats      [R, K + 2] float, device (cross entropy: K = 1). Out of the forward call, into
+ *                          the backward call: (max_v x_v, sum_v exp((x_v - max) / tau), the
+ *                          entries' x); a sum of -1 marks a row without an entry.
+ *   grad_loss      [R]     float, device. The gradient g of each row's loss.
+ *   grad_hidden    [R, H]  dtype, device, out, may be NULL. With
+ *                          G[r][v] = g_r tau (q_v - sum_{j: id_j = v} p_j): G . W_lm.
+ *   grad_W         [V, H]  dtype, device, out, may be NULL (a frozen head): G^T . hidden. Written
+ *                          in full. (At least one of the two is given; they overlap neither the
+ *                          inputs nor each other.)
+ *   bf16: G is rounded to bf16 before the two products; everything else is fp32, rounded once.
+ *   Rows without an entry, or without teacher mass: loss 0, gradient 0; their hidden states and
+ *   grad_loss are not read (padding may hold anything) and cost nothing in the products. NaN, or
+ *   +inf among a row's logits, makes the row's loss NaN and its gradient NaN, and with it grad_W;
+ *   a NaN or +inf teacher logit makes the loss NaN, and G at the row's entries.
+ *   1 <= R <= DFLASH2_MAX_LMHEAD_LOSS_ROWS (call again for more: the losses are per row, grad_W adds
+ *   up), 8 <= H <= DFLASH2_MAX_LMHEAD_LOSS_H and H % 8 == 0, 1 <= V <= DFLASH2_MAX_V,
+ *   1 <= K <= DFLASH2_MAX_K.
+ * Workspace: dflash2_lmhead_loss_workspace_bytes(R, H, V, dtype, backward) bytes (backward 0 or 1:
+ * of which call), contents need not be initialised. The backward call goes through the vocabulary
+ * in pieces and keeps G of one of them there: 128 MiB at most, or R times 256 columns.
+ * Errors: DFLASH2_ERR_INVALID_ARG, DFLASH2_ERR_ALIGNMENT, DFLASH2_ERR_WORKSPACE, DFLASH2_ERR_HIP.
+ */
+size_t dflash2_lmhead_loss_workspace_bytes(int R, int H, int V, int dtype, int backward);
+int dflash2_lmhead_ce(const void *hidden, const void *W_lm, int dtype, const int32_t *targets,
+                      int R, int H, int V, float *loss, float *row_stats, void *workspace,
+                      size_t workspace_bytes, void *stream);
+int dflash2_lmhead_ce_backward(const void *hidden, const void *W_lm, int dtype,
+                               const int32_t *targets, const float *row_stats,
+                               const float *grad_loss, int R, int H, int V, void *grad_hidden,
+                               void *grad_W, void *workspace, size_t workspace_bytes,
+                               void *stream);
+int dflash2_lmhead_distill(const void *hidden, const void *W_lm, int dtype,
+                           const int32_t *teacher_ids, const float *teacher_logits, int R, int H,
+                           int V, int K, float temperature, float *loss, float *row_stats,
+                           void *workspace, size_t workspace_bytes, void *stream);
+int dflash2_lmhead_distill_backward(const void *hidden, const void *W_lm, int dtype,
+                                    const int32_t *teacher_ids, const float *teacher_logits,
+                                    const float *row_stats, const float *grad_loss, int R, int H,
+                                    int V, int K, float temperature, void *grad_hidden,
+                                    void *grad_W, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * dflash2_grad_norm, dflash2_clip_grads - the global 2-norm over a training step's gradients, and
+ *   the gradients scaled down to a largest norm.
+ *
+ *   grads      [count]  host array of device pointers, each on an element of its type (16-byte
+ *                       alignment is not asked for: gradients may be views).
+ *   sizes      [count]  host array: elements of each tensor, >= 0 (an empty one's pointer is not
+ *                       looked at).
+ *   dtypes     [count]  host array of dflash2_dtype; types may be mixed.
+ *   norm       [1]      float, device, out. sqrt(sum g^2) over all tensors; squares are added in
+ *                       64 bits. 0 for no tensors.
+ *   out        [count]  host array of device pointers, the tensors' own type: g min(1, max_norm /
+ *                       norm), rounded to that type. out[i] = grads[i] scales in place; otherwise
+ *                       an output overlaps no gradient and no other output.
+ *   max_norm            >= 0, finite.
+ *   A norm that is not finite (NaN or infinity among the gradients, or a norm past the largest
+ *   float) scales nothing: the caller sees it in `norm` and drops the step.
+ *   The arrays are read during the call; a captured call keeps the pointers it was given.
+ *   count <= DFLASH2_MAX_GRADS, at most DFLASH2_MAX_GRAD_ELEMENTS elements in all.
+ * Workspace: dflash2_grad_norm_workspace_bytes() bytes, contents need not be initialised.
+ */
+size_t dflash2_grad_norm_workspace_bytes(void);
+int dflash2_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                      int count, float *norm, void *workspace, size_t workspace_bytes,
+                      void *stream);
+int dflash2_clip_grads(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                       int count, void *const *out, float max_norm, float *norm, void *workspace,
+                       size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
