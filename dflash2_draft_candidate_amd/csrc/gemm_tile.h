@@ -1,28 +1,32 @@
-// One workgroup's tile of a matrix product on the matrix cores: C[m][n] = sum_k A(m, k) B(n, k).
+// Matrix products on the matrix cores: tiles of C[m][n] = sum_k A(m, k) B(n, k).
 //
 // An operand lies in memory in one of two ways: its rows hold k (KC: element (m, k) at
 // base + m ld + k), or its rows hold m (KS: element (m, k) at base + k ld + m). The LM head's
 // logits take two KC operands, the hidden states' gradient KS x KC, the weight's KS x KS; no
 // operand is transposed in memory first.
 //
-// Design (gfx950, eight waves):
+// What both kernels below share (gfx950, eight waves):
 //   * A K step is 128 bytes of k per row (64 bf16, 32 f32), so a stage holds 128 B bytes of an
-//     operand of B rows in either layout. Two stages per operand: the loads of step t + 1 go from
-//     memory straight into LDS (16 bytes a lane) while step t is multiplied.
+//     operand of B rows in either layout. Loads go from memory straight into LDS, 16 bytes a lane.
 //   * The loads write LDS linearly, so the swizzle that keeps the fragment reads free of bank
 //     conflicts is in the addresses they read: KC stages keep chunk c (16 bytes) of row m at slot
 //     c ^ (m & 7); KS stages of bf16 keep the 32-byte piece s of row k at s ^ f(k), where f takes
-//     16 values over the 16 rows that one transposing read touches; KS stages of f32 keep the
-//     64-byte piece s at s ^ ((k >> 2) & 3).
+//     16 values (as many as fit the row) over the 16 rows that one transposing read touches; KS
+//     stages of f32 keep the 64-byte piece s at s ^ ((k >> 2) & 3).
 //   * bf16: v_mfma_f32_16x16x32_bf16. Lane (g = lane / 16, j = lane % 16) takes row j and
 //     k = 8 g .. 8 g + 7: one 16-byte LDS read from a KC stage, two transposing 8-byte reads
 //     (rows k = 8 g .. + 3 and + 4 .. + 7) from a KS stage. f32: v_mfma_f32_16x16x4_f32, a lane's
 //     16 bytes (k = 4 g .. 4 g + 3) feeding four of them; both operands agree on which k an
 //     instruction multiplies. Sums are fp32 and their order depends on k alone, not on the tile.
-//   * Out of range: a descriptor ends at the operand's last valid byte, so rows past the end read
-//     zeros; a KC operand whose k ends inside a step masks the chunks behind it. What lies behind
-//     the last column m of a KS row only reaches outputs that no caller stores.
+//   * Out of range: a load's descriptor ends at the operand's last valid byte, so rows past the end
+//     read zeros; a KC operand whose k ends inside a step masks the chunks behind it. What lies
+//     behind the last column m of a KS row only reaches outputs that no caller stores.
+//   * The loads into LDS are inline assembly (they have no output registers): the compiler, which
+//     cannot tell the stages apart, would wait for all of them before each read of LDS. Every wait
+//     for them is written out below.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.h"
 
@@ -34,47 +38,48 @@ constexpr int kStepBytes = 128;
 constexpr int kGemmOutside = 0x7FFFFFF0;  // an offset that no descriptor covers
 constexpr int kGemmWord3 = 0x00020000;    // gfx9-family buffer descriptor word 3 (raw data)
 
-constexpr int kWaitAll = 0x0070;          // s_waitcnt vmcnt(0) lgkmcnt(0)
-
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// An operand from the tile's first row (KC) or column (KS) and first k on.
+// A tile's operand: from its first row (KC) or column (KS) and first k on.
 struct GemmOperand {
     const char *base;
-    int64_t ld;     // bytes from one row to the next
-    int64_t bytes;  // valid bytes from base on
+    int64_t ld;  // bytes from one row to the next
+    int valid;   // KC: rows in range, counted from the tile's first; KS: bytes of a row before base
 };
 
-// The operand of rows [row0, rows) of a KC matrix, k in [k0, k1). (A row is a whole number of
-// 16-byte chunks in memory; what k1 leaves of the last one holds zeros.)
+// Rows from row0 on of a KC matrix of `rows` rows, k from k0 on. (A row is a whole number of 16-byte
+// chunks in memory; what the last k leaves of its chunk holds zeros.)
 template <typename T>
 __device__ __forceinline__ GemmOperand operand_kc(const void *p, int64_t ld, int row0, int rows,
-                                                  int most, int k0, int k1) {
-    const int n = min(rows - row0, most);
-    return {static_cast<const char *>(p) + row0 * ld + (int64_t)k0 * sizeof(T), ld,
-            n > 0 ? (int64_t)(n - 1) * ld + ((int64_t)(k1 - k0) * (int)sizeof(T) + 15) / 16 * 16 : 0};
+                                                  int k0) {
+    return {static_cast<const char *>(p) + row0 * ld + (int64_t)k0 * sizeof(T), ld, rows - row0};
 }
 
-// The operand of columns from col0 on of a KS matrix, k in [k0, k1).
+// Columns from col0 on of a KS matrix, k from k0 on.
 template <typename T>
-__device__ __forceinline__ GemmOperand operand_ks(const void *p, int64_t ld, int col0, int k0,
-                                                  int k1) {
+__device__ __forceinline__ GemmOperand operand_ks(const void *p, int64_t ld, int col0, int k0) {
     return {static_cast<const char *>(p) + (int64_t)k0 * ld + (int64_t)col0 * sizeof(T), ld,
-            (int64_t)(k1 - k0) * ld - (int64_t)col0 * (int)sizeof(T)};
+            col0 * (int)sizeof(T)};
 }
 
-// One operand's stages: B rows (m) of a K step.
-template <typename T, int B, bool KS> struct GemmSide {
+// One stage of an operand: B rows (KC) or columns (KS) of a K step. Where G is not 0 they are every
+// other run of G of the tile's: row i of the stage is row (i / G) 2 G + i % G.
+template <typename T, int B, bool KS, int G = 0> struct GemmSide {
     static constexpr int kBytes = B * kStepBytes;
     static constexpr int kStepK = kStepBytes / (int)sizeof(T);
     static constexpr int kLoads = kBytes / 1024;  // of 1 KB, one wave's
     static constexpr int kPerWave = (kLoads + kGemmWaves - 1) / kGemmWaves;
-    static constexpr int kRowChunks = B * (int)sizeof(T) / 16;  // KS: 16-byte chunks per stage row
+    static constexpr int kRowBytes = B * (int)sizeof(T);  // KS
+    static constexpr int kRowChunks = kRowBytes / 16;
 
     int voff[kPerWave];  // the lane's bytes within the operand's step
     int kbyte;           // KC: the first byte of k that the lane reads
+
+    static __device__ __forceinline__ int tile_row(int i) {
+        return G == 0 ? i : (i / (G ? G : 1)) * 2 * G + i % (G ? G : 1);
+    }
 
     __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
         kbyte = ((lane & 7) ^ (lane >> 3)) * 16;
@@ -82,7 +87,7 @@ template <typename T, int B, bool KS> struct GemmSide {
         for (int q = 0; q < kPerWave; ++q) {
             const int load = wave + kGemmWaves * q;
             if constexpr (!KS) {
-                voff[q] = (8 * load + (lane >> 3)) * (int)ld + kbyte;
+                voff[q] = tile_row(8 * load + (lane >> 3)) * (int)ld + kbyte;
             } else {
                 const int at = load * kWave + lane, k = at / kRowChunks, p = at % kRowChunks;
                 int c;
@@ -90,7 +95,7 @@ template <typename T, int B, bool KS> struct GemmSide {
                     c = (((p >> 1) ^ swizzle(k)) << 1) | (p & 1);
                 else
                     c = (((p >> 2) ^ ((k >> 2) & 3)) << 2) | (p & 3);
-                voff[q] = k * (int)ld + c * 16;
+                voff[q] = k * (int)ld + tile_row(c * (16 / (int)sizeof(T))) * (int)sizeof(T);
             }
         }
     }
@@ -105,21 +110,31 @@ template <typename T, int B, bool KS> struct GemmSide {
         return KS ? ld * kStepK : (int64_t)kStepBytes;
     }
 
-    // Starts the loads of a step whose first element is at `p`, with `bytes` valid bytes from there
-    // and (KC) `kleft` bytes of k left.
-    __device__ __forceinline__ void issue(char *stage, const char *p, int64_t bytes, int kleft,
+    // Starts the loads of a step into LDS at `to` (for this wave). p: the step's first byte of the
+    // operand; `valid` as the operand's, counted from p; kleft: values of k left.
+    __device__ __forceinline__ void issue(uint32_t to, const char *p, int ld, int valid, int kleft,
                                           int wave) const {
-        const int n = (int)(bytes < 0 ? 0 : bytes > kGemmOutside ? kGemmOutside : bytes);
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0, n, kGemmWord3);
+        const int ks = kleft < 0 ? 0 : kleft < kStepK ? kleft : kStepK;
+        int n;
+        if constexpr (KS)
+            n = ks * ld - valid;
+        else
+            n = ks == 0 ? 0 : (min(valid, 2 * B) - 1) * ld + (ks * (int)sizeof(T) + 15) / 16 * 16;
+        const uint64_t a = reinterpret_cast<uint64_t>(p);
+        u32x4 rs;
+        rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
+        rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
+        rs.z = __builtin_amdgcn_readfirstlane((uint32_t)(n < 0 ? 0 : n));
+        rs.w = kGemmWord3;
 #pragma unroll
         for (int q = 0; q < kPerWave; ++q) {
-            const int load = wave + kGemmWaves * q;
-            if (kLoads % kGemmWaves != 0 && load >= kLoads) break;
+            if (kLoads % kGemmWaves != 0 && wave + kGemmWaves * q >= kLoads) break;
             int off = voff[q];
-            if constexpr (!KS) off = kbyte < kleft ? off : kGemmOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(stage + load * 1024), 16, off,
-                                                     0, 0, 0);
+            if constexpr (!KS) off = kbyte < kleft * (int)sizeof(T) ? off : kGemmOutside;
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                             to + q * kGemmWaves * 1024),
+                         "v"(off), "s"(rs)
+                         : "memory");
         }
     }
 
@@ -138,11 +153,11 @@ template <typename T, int B, bool KS> struct GemmSide {
                 const int k = 8 * g + (j >> 2);
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    at[i] = k * (B * 2) + (((m0 / 16 + i) ^ swizzle(k)) << 5) + 8 * (j & 3);
+                    at[i] = k * kRowBytes + (((m0 / 16 + i) ^ swizzle(k)) << 5) + 8 * (j & 3);
             } else {
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    at[i] = 4 * g * (B * 4) + (((m0 / 16 + i) ^ g) << 6) + 4 * j;
+                    at[i] = 4 * g * kRowBytes + (((m0 / 16 + i) ^ g) << 6) + 4 * j;
             }
         }
         // half h of the step: bf16 k = 32 h .. 32 h + 31, f32 k = 16 h .. 16 h + 15
@@ -150,16 +165,16 @@ template <typename T, int B, bool KS> struct GemmSide {
             if constexpr (!KS) {
                 return *reinterpret_cast<const Frag *>(stage + at[h] + i * 16 * kStepBytes);
             } else if constexpr (sizeof(T) == 2) {
-                const char *p = stage + at[i] + 32 * h * (B * 2);
+                const char *p = stage + at[i] + 32 * h * kRowBytes;
                 struct { s16x4 lo, hi; } v;
                 v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
-                v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * (B * 2)));
+                v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * kRowBytes));
                 return __builtin_bit_cast(Frag, v);
             } else {
-                const char *p = stage + at[i] + 16 * h * (B * 4);
+                const char *p = stage + at[i] + 16 * h * kRowBytes;
                 Frag v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float *>(p + e * (B * 4));
+                for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float *>(p + e * kRowBytes);
                 return v;
             }
         }
@@ -175,24 +190,80 @@ __device__ __forceinline__ f32x4 gemm_mfma(f32x4 a, f32x4 b, f32x4 c) {
     return c;
 }
 
+__device__ __forceinline__ uint32_t lds_address(void *p) {
+    return (uint32_t)(uintptr_t)(lds_void *)p;
+}
+
+// ---- output --------------------------------------------------------------------------------------
+
+// Four values of type T, rounded to nearest even.
+template <typename T>
+__device__ __forceinline__ auto packed4(f32x4 x) {
+    if constexpr (sizeof(T) == 2) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(u32x2, bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2],
+                                                (__bf16)x[3]});
+    } else {
+        return __builtin_bit_cast(u32x4, x);
+    }
+}
+
+// Output rows as a descriptor and 32-bit offsets: `rows` rows of `ld` bytes from p on, the last
+// one `width` bytes long. A store at kGemmOutside, or behind the last row, is dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(void *p, int64_t ld, int rows,
+                                                           int64_t width) {
+    const int64_t n = rows > 0 ? (rows - 1) * ld + width : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(p, (short)0, (int)n, kGemmWord3);
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t rs, int off, f32x4 x) {
+    if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(packed4<T>(x), rs, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b128(packed4<T>(x), rs, off, 0, 0);
+}
+
+// vmcnt(VM) lgkmcnt(0), then the barrier; nothing moves across.
+template <int VM> __device__ __forceinline__ void gemm_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// `x` as a value of its own: what an epilogue computes from it is computed there, not kept in registers
+// through the products.
+__device__ __forceinline__ int anew(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// ---- one tile at a time ------------------------------------------------------------------------
 // A tile of BM x BN over WM x (8 / WM) waves. Wave (wm, wn) holds rows m = wm BM / WM + 16 mi +
-// 4 g + i and columns n = wn BN / WN + 16 ni + j in acc[mi][ni][i].
+// 4 g + i and columns n = wn BN / WN + 16 ni + j in acc[mi][ni][i]. Two stages per operand: the loads
+// of step t + 1 are in flight while step t is multiplied. For tiles below 256 x 256, and for f32,
+// where the matrix cores are the bound whatever feeds them (4096 x 4096 x 2048: 142 TFLOP/s; the
+// phases below: 132).
 template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile {
     static constexpr int WN = kGemmWaves / WM;
     static constexpr int MI = BM / (16 * WM), NI = BN / (16 * WN);
+    static constexpr int kCols = BN;
     static_assert(MI * 16 * WM == BM && NI * 16 * WN == BN, "whole fragments");
     typedef GemmSide<T, BM, AS> SideA;
     typedef GemmSide<T, BN, BS> SideB;
     static constexpr int kStepK = SideA::kStepK;
+    static constexpr int kLdsBytes = 2 * (SideA::kBytes + SideB::kBytes);
 
     f32x4 acc[MI][NI];
 
     static __device__ __forceinline__ int wave_m(int wave) { return (wave / WN) * (BM / WM); }
     static __device__ __forceinline__ int wave_n(int wave) { return (wave % WN) * (BN / WN); }
 
-    // The product over K values of k. a0/a1, b0/b1: the stages, objects of their own in LDS.
-    __device__ __forceinline__ void run(const GemmOperand &A, const GemmOperand &B, int K, char *a0,
-                                        char *a1, char *b0, char *b1, int wave, int lane) {
+    // The product over K values of k. lds: kLdsBytes.
+    __device__ __forceinline__ void run(const GemmOperand &A, const GemmOperand &B, int K, char *lds,
+                                        int wave, int lane) {
         SideA sa;
         SideB sb;
         sa.init(A.ld, wave, lane);
@@ -206,22 +277,20 @@ template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile 
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+        constexpr int kStage = SideA::kBytes + SideB::kBytes;
+        const uint32_t base = lds_address(lds) + wave * 1024;
         const int steps = (K + kStepK - 1) / kStepK;
         const char *pa = A.base, *pb = B.base;
-        int64_t na = A.bytes, nb = B.bytes;
-        int kleft = K * (int)sizeof(T);
-        auto issue = [&](char *sta, char *stb) {
-            sa.issue(sta, pa, na, kleft, wave);
-            sb.issue(stb, pb, nb, kleft, wave);
-            const int64_t da = SideA::stride(A.ld), db = SideB::stride(B.ld);
-            pa += da;
-            na -= da;
-            pb += db;
-            nb -= db;
-            kleft -= kStepBytes;
-            __builtin_amdgcn_sched_barrier(0);  // (the compiler would start them after the products)
+        int kleft = K;
+        auto issue = [&](int buf) {
+            sa.issue(base + buf * kStage, pa, (int)A.ld, A.valid, kleft, wave);
+            sb.issue(base + buf * kStage + SideA::kBytes, pb, (int)B.ld, B.valid, kleft, wave);
+            pa += SideA::stride(A.ld);
+            pb += SideB::stride(B.ld);
+            kleft -= kStepK;
         };
-        auto compute = [&](const char *sta, const char *stb) {
+        auto compute = [&](int buf) {
+            const char *sta = lds + buf * kStage, *stb = sta + SideA::kBytes;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 typename SideA::Frag fa[MI];
@@ -237,31 +306,240 @@ template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile 
                         acc[mi][ni] = gemm_mfma(fa[mi], fb[ni], acc[mi][ni]);
             }
         };
-        // The barrier at a step's start: this wave's loads have landed (vmcnt), so after it all
-        // waves' have, and every wave has read the other stage, which the next loads overwrite.
-        auto ready = [&]() {
-            __builtin_amdgcn_s_waitcnt(kWaitAll);
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-        };
-        // (Loads past the last step read nothing and write zeros: the loop stays free of branches.)
-        issue(a0, b0);
+        // At a step's barrier this wave's loads have landed, so after it all waves' have, and every
+        // wave has read the other stage, which the next loads overwrite. (Loads past the last step
+        // read nothing and write zeros: the loop stays free of branches.)
+        issue(0);
         for (int t = 0; t + 1 < steps; t += 2) {
-            ready();
-            issue(a1, b1);
-            compute(a0, b0);
-            ready();
-            issue(a0, b0);
-            compute(a1, b1);
+            gemm_barrier<0>();
+            issue(1);
+            compute(0);
+            gemm_barrier<0>();
+            issue(0);
+            compute(1);
         }
-        ready();
-        if (steps & 1) compute(a0, b0);
+        gemm_barrier<0>();
+        if (steps & 1) compute(0);
     }
 };
 
-// The tile of workgroup `id` of nm x nn tiles. Consecutive workgroups run on different XCDs, each
-// with an L2 of its own: XCD x takes a contiguous eighth of the tiles, in groups of `group` rows
-// of tiles, rows first, so that what it works on at a time shares operands.
+// ---- a stream of 256 x 256 tiles ---------------------------------------------------------------
+// The waves form two groups of four, one wave of each on every SIMD. A K step is four phases, each a
+// quarter of the wave's 128 x 64 (64 x 32: 16 matrix instructions); in a phase a wave first reads the
+// fragments of the quarter from LDS and starts two loads, then multiplies. The second group runs one
+// barrier behind the first, so on every SIMD one wave multiplies while the other one reads.
+//   * A and B are staged in halves of 128 rows (the rows of every wave's first and second half), each
+//     in a place of its own: 8 x 16 KB, two steps. Phases read A0 | B1 | A1 | B0 of the next step, and
+//     each starts the load of the half that the phase before has read, for two steps later: seven
+//     phases pass before it is read, so the waits leave six halves (12 loads a wave) in flight.
+//   * A wave's reads of a half are done (lgkmcnt) before the barrier that ends its reading; no wave
+//     starts a load into that half before that barrier, whichever group it is in.
+//   * The loads run ahead over the end of a tile into the next one of the workgroup, so a tile's
+//     epilogue, which uses no LDS, finds the next tile's first two steps on their way.
+//   * An epilogue's stores count in vmcnt like loads. kStores is how many a wave surely makes in one;
+//     the first six phases behind it, whose halves were asked for before them, do not wait for them.
+// 4096 x 4096 x 16384 bf16: 1314 TFLOP/s (KC x KC), 1319 (KS x KC), 1366 (KS x KS); one stage of
+// 64 KB ahead and a barrier per step (GemmTile): 1123, 1201, 1217.
+struct GemmWork {
+    GemmOperand a, b;
+    int K;  // <= 0: no tile
+};
+
+template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
+    static constexpr int WM = 2, WN = 4, MI = 8, NI = 4, BM = 256, BN = 256, kCols = BN;
+    typedef GemmSide<T, 128, AS, 64> SideA;
+    typedef GemmSide<T, 128, BS, 32> SideB;
+    static constexpr int kStepK = SideA::kStepK;
+    static constexpr int kHalf = SideA::kBytes;
+    static constexpr int kStageBytes = 8 * kHalf;  // per buffer: A0 A1 B0 B1
+    static constexpr int kScratch = 4096;          // a wave's, for its stores
+    static constexpr int kLdsBytes = kStageBytes + kGemmWaves * kScratch;
+    static_assert(12 + kStores < 64, "vmcnt");
+
+    f32x4 acc[MI][NI];
+
+    static __device__ __forceinline__ int wave_m(int wave) { return (wave / WN) * (BM / WM); }
+    static __device__ __forceinline__ int wave_n(int wave) { return (wave % WN) * (BN / WN); }
+
+    // steps of a tile: an even number, so that every tile starts in buffer 0
+    static __device__ __forceinline__ int steps_of(int K) {
+        return ((K + kStepK - 1) / kStepK + 1) & ~1;
+    }
+
+    // work(i): the workgroup's tile i, K = 0 behind the last; done(i): its epilogue, on acc.
+    // All tiles share the operands' ld.
+    template <typename Work, typename Done>
+    __device__ __forceinline__ void run(int64_t lda, int64_t ldb, Work work, Done done, char *lds,
+                                        int wave, int lane) {
+        SideA sa;
+        SideB sb;
+        sa.init(lda, wave, lane);
+        sb.init(ldb, wave, lane);
+        typename SideA::template Reader<4> ra;
+        typename SideB::template Reader<2> rb;
+        ra.init((wave / WN) * 64, lane);
+        rb.init((wave % WN) * 32, lane);
+
+        // what the loads are at: two steps ahead of the products
+        const uint32_t base = lds_address(lds) + wave * 1024;
+        const int64_t da = SideA::stride(lda), db = SideB::stride(ldb);
+        const int64_t half_a = AS ? 64 * (int)sizeof(T) : 64 * lda;
+        const int64_t half_b = BS ? 32 * (int)sizeof(T) : 32 * ldb;
+        constexpr int kPartA = AS ? 64 * (int)sizeof(T) : -64;  // on `valid`, for the second half
+        constexpr int kPartB = BS ? 32 * (int)sizeof(T) : -32;
+        GemmWork at = work(0);
+        if (at.K <= 0) return;
+        int next = 1, load_left = steps_of(at.K), kleft = at.K;
+        auto load_a = [&](int half, int buf) {
+            sa.issue(base + (buf * 4 + half) * kHalf, at.a.base + half * half_a, (int)lda,
+                     at.a.valid + half * kPartA, kleft, wave);
+        };
+        auto load_b = [&](int half, int buf) {
+            sb.issue(base + (buf * 4 + 2 + half) * kHalf, at.b.base + half * half_b, (int)ldb,
+                     at.b.valid + half * kPartB, kleft, wave);
+        };
+        auto advance = [&]() {
+            at.a.base += da;
+            at.b.base += db;
+            kleft -= kStepK;
+            if (--load_left == 0) {
+                at = work(next++);
+                kleft = at.K;
+                load_left = at.K > 0 ? steps_of(at.K) : -1;  // (behind the last tile: loads of nothing)
+            }
+        };
+        typename SideA::Frag fa[4][2];
+        typename SideB::Frag fb0[2][2], fb1[2][2], fbn[2][2];
+        auto read_a = [&](int buf, int half) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) fa[i][h] = ra.read(lds + (buf * 4 + half) * kHalf, i, h);
+        };
+        auto read_b = [&](int buf, int half, typename SideB::Frag(&f)[2][2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) f[i][h] = rb.read(lds + (buf * 4 + 2 + half) * kHalf, i, h);
+        };
+        auto multiply = [&](int ah, int bh, typename SideB::Frag(&f)[2][2]) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[4 * ah + i][2 * bh + j] =
+                            gemm_mfma(fa[i][h], f[j][h], acc[4 * ah + i][2 * bh + j]);
+            __builtin_amdgcn_s_setprio(0);
+        };
+        auto follow = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int buf = 0; buf < 2; ++buf) {
+            load_b(0, buf);
+            load_a(0, buf);
+            load_b(1, buf);
+            load_a(1, buf);
+            advance();
+        }
+        gemm_barrier<14>();  // the first of the 8 halves has landed
+        read_b(0, 0, fb0);
+        gemm_barrier<12>();  // the second
+        if (wave >= kGemmWaves / 2) follow();  // from here on this group runs one barrier behind
+        bool stored = false;  // an epilogue's stores are younger than what is waited for
+        auto landed = [&](bool may_be_young) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (kStores > 0 && may_be_young && stored)
+                gemm_barrier<12 + kStores>();
+            else
+                gemm_barrier<12>();
+        };
+        auto step = [&](int buf, typename SideB::Frag(&b0)[2][2], typename SideB::Frag(&bn)[2][2]) {
+            read_a(buf, 0);
+            load_b(0, buf);
+            landed(true);
+            multiply(0, 0, b0);
+            follow();
+            read_b(buf, 1, fb1);
+            load_a(0, buf);
+            landed(true);
+            multiply(0, 1, fb1);
+            follow();
+            read_a(buf, 1);
+            load_b(1, buf);
+            landed(buf == 0);
+            multiply(1, 1, fb1);
+            follow();
+            read_b(buf ^ 1, 0, bn);
+            load_a(1, buf);
+            advance();
+            landed(buf == 0);
+            multiply(1, 0, b0);
+            follow();
+        };
+        for (int i = 0;; ++i) {
+            const int K = work(i).K;
+            if (K <= 0) break;
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = steps_of(K); t > 0; t -= 2) {
+                step(0, fb0, fbn);
+                step(1, fbn, fb0);
+                stored = false;
+            }
+            done(i);
+            stored = true;
+        }
+        if (wave < kGemmWaves / 2) follow();  // (the other group's last barrier)
+        __builtin_amdgcn_s_waitcnt(0x0070);   // no load is in flight when the workgroup ends
+    }
+
+    // The tile as bf16 rows of output: row n of it at `out` + n ld, its columns m from byte `first` on,
+    // those from byte `end` of a row on left out. value(mi, ni): the wave's four values. A wave's
+    // accumulators hold 8 bytes of each of 16 rows; 16 rows of its 128 columns go through 4 KB of LDS
+    // (16-byte chunk c of row j at c ^ j), so that a store covers 256 bytes of each of 4 rows: a store
+    // takes its time by the lines it touches (4096 x 65536 x 1024: 630 us with 8-byte stores from the
+    // accumulators).
+    template <typename Value>
+    __device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t out, int ld, int first, int end,
+                                               char *lds, int wave, int lane, Value value) {
+        char *scratch = lds + kStageBytes + wave * kScratch;
+        lane = anew(lane);
+        const int g = lane >> 4, j = lane & 15;
+        const int put = j * 256 + (g & 1) * 8;
+        const int column = first + wave_m(wave) * 2 + j * 16;  // (in the second half lane j takes chunk j)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                const auto x = packed4<uint16_t>(value(mi, ni));
+                *reinterpret_cast<decltype(packed4<uint16_t>(f32x4{}))  *>(
+                    scratch + put + (((2 * mi + (g >> 1)) ^ j) << 4)) = x;
+                __builtin_amdgcn_sched_barrier(0);  // (all at once would not fit the registers)
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = 4 * q + g;
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(scratch + row * 256 + ((j ^ row) << 4));
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    x, out, column < end ? (wave_n(wave) + 16 * ni + row) * ld + column : kGemmOutside,
+                    0, 0);
+            }
+        }
+    }
+    static constexpr int kRowStores = 4 * NI;  // store_rows' stores
+};
+
+// The tile of place `id` of nm x nn tiles. Consecutive workgroups run on different XCDs, each with
+// an L2 of its own: XCD x takes a contiguous eighth of the tiles, in groups of `group` rows of tiles,
+// rows first, so that what it works on at a time shares operands.
 __device__ __forceinline__ void gemm_place(int id, int nm, int nn, int group, int &tm, int &tn) {
     constexpr int kXcds = 8;
     const int total = nm * nn, x = id % kXcds, q = total / kXcds, r = total % kXcds;

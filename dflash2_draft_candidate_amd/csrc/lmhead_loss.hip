@@ -197,76 +197,37 @@ struct LogitsJob {
     const int32_t *count;
     int H, V;
     int v0, v1;           // the piece of the vocabulary
-    int nv, nr;           // tiles
+    int nv, nr;           // tiles (of all R rows)
     float c;              // log2(e) / tau
-    float2 *parts;        // forward: per 16 rows, [nv WM][16] (max, sum)
+    float2 *parts;        // forward: per 16 rows, [nparts][16] (max, sum)
+    int64_t nparts;
     void *G;              // backward: [count][ldg]
     int64_t ldg;          // columns
     const float2 *scale;  // backward: [count]
 };
 
-// Four values of type T, rounded to nearest even.
-template <typename T>
-__device__ __forceinline__ auto packed4(f32x4 x) {
-    if constexpr (sizeof(T) == 2) {
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(u32x2, bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2],
-                                                (__bf16)x[3]});
-    } else {
-        return __builtin_bit_cast(u32x4, x);
-    }
-}
+// A tile's end: for GRAD G's values, else maxima and sums. Its vocabulary rows start at v0, its
+// kept rows at r0 (of R); `part`: the place of its (max, sum) pairs.
+template <typename T> using GradStream = GemmStream<T, false, false, 16>;
+template <typename T> using StatsStream = GemmStream<T, false, false, 0>;
 
-// Output rows as a descriptor and 32-bit offsets: `rows` rows of `ld` bytes from p on, the last
-// one `width` bytes long. A store at kGemmOutside, or behind the last row, is dropped.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(void *p, int64_t ld, int rows,
-                                                           int64_t width) {
-    const int64_t n = rows > 0 ? (rows - 1) * ld + width : 0;
-    return __builtin_amdgcn_make_buffer_rsrc(p, (short)0, (int)n, kGemmWord3);
-}
-
-template <typename T>
-__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t rs, int off, f32x4 x) {
-    if constexpr (sizeof(T) == 2)
-        __builtin_amdgcn_raw_buffer_store_b64(packed4<T>(x), rs, off, 0, 0);
-    else
-        __builtin_amdgcn_raw_buffer_store_b128(packed4<T>(x), rs, off, 0, 0);
-}
-
-// Tile of 256 vocabulary rows x BN kept rows. GRAD: G's values; else maxima and sums.
-template <typename T, int BN, int WM, bool GRAD>
-__global__ __launch_bounds__(kGemmThreads) void lmloss_logits_kernel(LogitsJob job) {
-    typedef GemmTile<T, kTile, BN, false, false, WM> Tile;
-    __shared__ __align__(1024) char a0[Tile::SideA::kBytes];
-    __shared__ __align__(1024) char a1[Tile::SideA::kBytes];
-    __shared__ __align__(1024) char b0[Tile::SideB::kBytes];
-    __shared__ __align__(1024) char b1[Tile::SideB::kBytes];
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count;
-    int tm, tn;
-    gemm_place(blockIdx.x, job.nv, job.nr, kPlaceGroup, tm, tn);
-    const int v0 = job.v0 + tm * kTile, r0 = tn * BN;
-    if (r0 >= R) return;
-    const int64_t ld = (int64_t)job.H * sizeof(T);
-    Tile tile;
-    tile.run(operand_kc<T>(job.W, ld, v0, job.v1, kTile, 0, job.H),
-             operand_kc<T>(job.rows, ld, r0, R, BN, 0, job.H), job.H, a0, a1, b0, b1, wave, lane);
-
+template <typename T, bool GRAD, typename Tile>
+__device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, int v0, int r0, int R,
+                                            int64_t part, char *lds, int wave, int lane) {
+    lane = anew(lane);
     const int g = lane >> 4, j = lane & 15;
     const int vw = v0 + Tile::wave_m(wave) + 4 * g;
     const float c = job.c;
     const int64_t ldg = job.ldg * (int64_t)sizeof(T);
-    const int valid = min(R - r0, BN);
     const __amdgpu_buffer_rsrc_t out = out_rows(
-        static_cast<char *>(job.G) + r0 * ldg + (int64_t)(v0 - job.v0) * sizeof(T), ldg, valid,
-        kTile * sizeof(T));
+        static_cast<char *>(job.G) + r0 * ldg + (int64_t)(v0 - job.v0) * sizeof(T), ldg,
+        min(R - r0, Tile::kCols), kTile * sizeof(T));
+    const bool ragged = v0 + kTile > job.v1;
 #pragma unroll
     for (int ni = 0; ni < Tile::NI; ++ni) {
         const int rn = Tile::wave_n(wave) + 16 * ni + j, r = r0 + rn;
         if constexpr (!GRAD) {
-            if (v0 + kTile > job.v1) {
+            if (ragged) {
 #pragma unroll
                 for (int mi = 0; mi < Tile::MI; ++mi)
 #pragma unroll
@@ -289,11 +250,11 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_kernel(LogitsJob j
                     sum += __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - ref) * c);
             sum += __shfl_xor(sum, 16, kWave);
             sum += __shfl_xor(sum, 32, kWave);
-            if (g == 0 && r < R) {
-                const int64_t parts = (int64_t)job.nv * WM;
-                job.parts[((r >> 4) * parts + tm * WM + wave / Tile::WN) * 16 + (r & 15)] =
+            if (g == 0 && r < R)
+                job.parts[((r >> 4) * job.nparts + part + wave / Tile::WN) * 16 + (r & 15)] =
                     float2{top, sum};
-            }
+        } else if constexpr (std::is_same<Tile, GradStream<T>>::value) {
+            break;  // (stored below)
         } else {
             const float2 s = job.scale[min(r, R - 1)];
             const int off = rn * (int)ldg + (vw - v0) * (int)sizeof(T);
@@ -303,13 +264,84 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_kernel(LogitsJob j
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     y[i] = s.y * __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - s.x) * c);
-                    if (vw + 16 * mi + i >= job.v1) y[i] = 0.f;
+                    if (ragged && vw + 16 * mi + i >= job.v1) y[i] = 0.f;
                 }
                 store4<T>(out, off + 16 * mi * (int)sizeof(T), y);
                 __builtin_amdgcn_sched_barrier(0);  // (all at once would not fit the registers)
             }
         }
     }
+    if constexpr (GRAD && std::is_same<Tile, GradStream<T>>::value) {
+        float2 s[Tile::NI];
+#pragma unroll
+        for (int ni = 0; ni < Tile::NI; ++ni)
+            s[ni] = job.scale[min(r0 + Tile::wave_n(wave) + 16 * ni + j, R - 1)];
+        tile.store_rows(out, (int)ldg, 0, kTile * 2, lds, wave, lane, [&](int mi, int ni) {
+            f32x4 y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = s[ni].y * __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - s[ni].x) * c);
+                if (ragged && vw + 16 * mi + i >= job.v1) y[i] = 0.f;
+            }
+            return y;
+        });
+    }
+}
+
+// Tiles of 256 vocabulary rows x BN kept rows, one a workgroup.
+template <typename T, int BN, int WM_, bool GRAD>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_logits_kernel(LogitsJob job) {
+    typedef GemmTile<T, kTile, BN, false, false, WM_> Tile;
+    __shared__ __align__(1024) char lds[Tile::kLdsBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count, nr = (R + BN - 1) / BN;
+    if ((int)blockIdx.x >= job.nv * nr) return;
+    int tm, tn;
+    gemm_place(blockIdx.x, job.nv, nr, kPlaceGroup, tm, tn);
+    const int v0 = job.v0 + tm * kTile, r0 = tn * BN;
+    const int64_t ld = (int64_t)job.H * sizeof(T);
+    Tile tile;
+    tile.run(operand_kc<T>(job.W, ld, v0, job.v1, 0), operand_kc<T>(job.rows, ld, r0, R, 0), job.H,
+             lds, wave, lane);
+    logits_done<T, GRAD>(job, tile, v0, r0, R, (int64_t)tm * WM_, lds, wave, lane);
+}
+
+// The same with 256 kept rows a tile, as a stream.
+template <typename T, bool GRAD>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(LogitsJob job) {
+    typedef typename std::conditional<GRAD, GradStream<T>, StatsStream<T>>::type Stream;
+    static_assert(!GRAD || Stream::kRowStores == 16, "the stores a tile's end makes");
+    __shared__ __align__(1024) char lds[Stream::kLdsBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count, nr = (R + kTile - 1) / kTile, tiles = job.nv * nr;
+    const int64_t ld = (int64_t)job.H * sizeof(T);
+    auto place = [&](int i, int &v0, int &r0) {
+        const int id = blockIdx.x + i * gridDim.x;
+        if (id >= tiles) return false;
+        int tm, tn;
+        gemm_place(id, job.nv, nr, kPlaceGroup, tm, tn);
+        v0 = job.v0 + tm * kTile;
+        r0 = tn * kTile;
+        return true;
+    };
+    Stream stream;
+    stream.run(
+        ld, ld,
+        [&](int i) -> GemmWork {
+            int v0, r0;
+            if (!place(i, v0, r0)) return {{job.W, ld, 0}, {job.rows, ld, 0}, 0};
+            return {operand_kc<T>(job.W, ld, v0, job.v1, 0), operand_kc<T>(job.rows, ld, r0, R, 0),
+                    job.H};
+        },
+        [&](int i) {
+            int v0 = 0, r0 = 0;
+            place(i, v0, r0);
+            logits_done<T, GRAD>(job, stream, v0, r0, R,
+                                 (int64_t)((v0 - job.v0) / kTile) * Stream::WM, lds, wave, lane);
+        },
+        lds, wave, lane);
 }
 
 // ---- forward's end -------------------------------------------------------------------------------
@@ -469,36 +501,19 @@ struct HiddenJob {
     const int32_t *count;
     int R, H, v0, v1;
     int64_t ldg;
-    int nh, nr, splits, per;  // tiles; splits of the piece, `per` columns each
+    int nh, nr, splits, per;  // tiles (of all R rows); splits of the piece, `per` columns each
     bool first;          // the first piece: nothing to add to
     float *sums;         // [splits][R][H]
 };
 
-// Tile of 256 columns of H x BN kept rows over a split of the piece.
-template <typename T, int BN, int WM>
-__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_kernel(HiddenJob job) {
-    typedef GemmTile<T, kTile, BN, true, false, WM> Tile;
-    __shared__ __align__(1024) char a0[Tile::SideA::kBytes];
-    __shared__ __align__(1024) char a1[Tile::SideA::kBytes];
-    __shared__ __align__(1024) char b0[Tile::SideB::kBytes];
-    __shared__ __align__(1024) char b1[Tile::SideB::kBytes];
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count;
-    int tm, tn;
-    const int tiles = job.nh * job.nr, split = blockIdx.x / tiles;
-    gemm_place(blockIdx.x % tiles, job.nh, job.nr, kPlaceGroup, tm, tn);
-    const int h0 = tm * kTile, r0 = tn * BN;
-    if (r0 >= R) return;
-    const int k0 = split * job.per, k1 = min(k0 + job.per, job.v1 - job.v0);
-    Tile tile;
-    tile.run(operand_ks<T>(job.W, (int64_t)job.H * sizeof(T), h0, job.v0 + k0, job.v0 + k1),
-             operand_kc<T>(job.G, job.ldg * (int64_t)sizeof(T), r0, R, BN, k0, k1), k1 - k0, a0, a1,
-             b0, b1, wave, lane);
+template <typename Tile>
+__device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, int split, int h0,
+                                            int r0, int R, int wave, int lane) {
+    lane = anew(lane);
     const int g = lane >> 4, j = lane & 15;
     const int ld = job.H * 4;
-    const __amdgpu_buffer_rsrc_t out =
-        out_rows(job.sums + ((int64_t)split * job.R + r0) * job.H, ld, min(R - r0, BN), ld);
+    const __amdgpu_buffer_rsrc_t out = out_rows(
+        job.sums + ((int64_t)split * job.R + r0) * job.H, ld, min(R - r0, Tile::kCols), ld);
 #pragma unroll
     for (int ni = 0; ni < Tile::NI; ++ni) {
         const int row = (Tile::wave_n(wave) + 16 * ni + j) * ld;
@@ -512,6 +527,62 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_kernel(HiddenJob j
             store4<float>(out, off, x);
         }
     }
+}
+
+// Tiles of 256 columns of H x BN kept rows over a split of the piece, one a workgroup.
+template <typename T, int BN, int WM>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_kernel(HiddenJob job) {
+    typedef GemmTile<T, kTile, BN, true, false, WM> Tile;
+    __shared__ __align__(1024) char lds[Tile::kLdsBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count, nr = (R + BN - 1) / BN;
+    if ((int)blockIdx.x >= job.nh * job.splits * nr) return;
+    int tm, tn;
+    gemm_place(blockIdx.x, job.nh * job.splits, nr, kPlaceGroup, tm, tn);
+    const int split = tm / job.nh, h0 = tm % job.nh * kTile, r0 = tn * BN;
+    const int k0 = split * job.per, k1 = min(k0 + job.per, job.v1 - job.v0);
+    Tile tile;
+    tile.run(operand_ks<T>(job.W, (int64_t)job.H * sizeof(T), h0, job.v0 + k0),
+             operand_kc<T>(job.G, job.ldg * (int64_t)sizeof(T), r0, R, k0), k1 - k0, lds, wave, lane);
+    hidden_done(job, tile, split, h0, r0, R, wave, lane);
+}
+
+// The same with 256 kept rows a tile, as a stream.
+template <typename T>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(HiddenJob job) {
+    typedef GemmStream<T, true, false, 32> Stream;  // (hidden_done: 32 stores)
+    __shared__ __align__(1024) char lds[Stream::kLdsBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count, nr = (R + kTile - 1) / kTile, tiles = job.nh * job.splits * nr;
+    const int64_t ldw = (int64_t)job.H * sizeof(T), ldg = job.ldg * (int64_t)sizeof(T);
+    auto place = [&](int i, int &split, int &h0, int &r0) {
+        const int id = blockIdx.x + i * gridDim.x;
+        if (id >= tiles) return false;
+        int tm, tn;
+        gemm_place(id, job.nh * job.splits, nr, kPlaceGroup, tm, tn);
+        split = tm / job.nh;
+        h0 = tm % job.nh * kTile;
+        r0 = tn * kTile;
+        return true;
+    };
+    Stream stream;
+    stream.run(
+        ldw, ldg,
+        [&](int i) -> GemmWork {
+            int split, h0, r0;
+            if (!place(i, split, h0, r0)) return {{job.W, ldw, 0}, {job.G, ldg, 0}, 0};
+            const int k0 = split * job.per, k1 = min(k0 + job.per, job.v1 - job.v0);
+            return {operand_ks<T>(job.W, ldw, h0, job.v0 + k0), operand_kc<T>(job.G, ldg, r0, R, k0),
+                    k1 - k0};
+        },
+        [&](int i) {
+            int split = 0, h0 = 0, r0 = 0;
+            place(i, split, h0, r0);
+            hidden_done(job, stream, split, h0, r0, R, wave, lane);
+        },
+        lds, wave, lane);
 }
 
 // grad_hidden from the splits' sums, in split order; zeros for the rows left out. One workgroup per
@@ -541,14 +612,18 @@ struct WeightJob {
     void *grad;          // [V, H]
 };
 
-// Tile of 256 columns of H x 256 vocabulary rows, over the kept rows.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_rows(const WeightJob &job, int v0) {
+    const int ld = job.H * (int)sizeof(T);
+    return out_rows(static_cast<char *>(job.grad) + (int64_t)(job.v0 + v0) * ld, ld,
+                    min(job.v1 - job.v0 - v0, kTile), ld);
+}
+
+// Tiles of 256 columns of H x 256 vocabulary rows, over the kept rows; one a workgroup.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob job) {
     typedef GemmTile<T, kTile, kTile, true, true, 2> Tile;
-    __shared__ __align__(1024) char a0[Tile::SideA::kBytes];
-    __shared__ __align__(1024) char a1[Tile::SideA::kBytes];
-    __shared__ __align__(1024) char b0[Tile::SideB::kBytes];
-    __shared__ __align__(1024) char b1[Tile::SideB::kBytes];
+    __shared__ __align__(1024) char lds[Tile::kLdsBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int R = *job.count;
@@ -556,17 +631,13 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
     gemm_place(blockIdx.x, job.nh, job.nv, kPlaceGroup, tm, tn);
     const int h0 = tm * kTile, v0 = tn * kTile;
     Tile tile;
-    tile.run(operand_ks<T>(job.rows, (int64_t)job.H * sizeof(T), h0, 0, R),
-             operand_ks<T>(job.G, job.ldg * (int64_t)sizeof(T), v0, 0, R), R, a0, a1, b0, b1, wave,
-             lane);
+    tile.run(operand_ks<T>(job.rows, (int64_t)job.H * sizeof(T), h0, 0),
+             operand_ks<T>(job.G, job.ldg * (int64_t)sizeof(T), v0, 0), R, lds, wave, lane);
     const int g = lane >> 4, j = lane & 15;
-    const int ld = job.H * (int)sizeof(T);
-    const __amdgpu_buffer_rsrc_t out =
-        out_rows(static_cast<char *>(job.grad) + (int64_t)(job.v0 + v0) * ld, ld,
-                 min(job.v1 - job.v0 - v0, kTile), ld);
+    const __amdgpu_buffer_rsrc_t out = weight_rows<T>(job, v0);
 #pragma unroll
     for (int ni = 0; ni < Tile::NI; ++ni) {
-        const int row = (Tile::wave_n(wave) + 16 * ni + j) * ld;
+        const int row = (Tile::wave_n(wave) + 16 * ni + j) * job.H * (int)sizeof(T);
 #pragma unroll
         for (int mi = 0; mi < Tile::MI; ++mi) {
             const int h = h0 + Tile::wave_m(wave) + 16 * mi + 4 * g;
@@ -574,6 +645,45 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+}
+
+// The same as a stream.
+template <typename T>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(WeightJob job) {
+    typedef GemmStream<T, true, true, 16> Stream;
+    static_assert(Stream::kRowStores == 16, "the stores a tile's end makes");
+    __shared__ __align__(1024) char lds[Stream::kLdsBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    // (without a kept row the products are over a row of zeros)
+    const int R = *job.count, K = max(R, 1), tiles = job.nh * job.nv;
+    const int64_t ldh = (int64_t)job.H * sizeof(T), ldg = job.ldg * (int64_t)sizeof(T);
+    auto place = [&](int i, int &h0, int &v0) {
+        const int id = blockIdx.x + i * gridDim.x;
+        if (id >= tiles) return false;
+        int tm, tn;
+        gemm_place(id, job.nh, job.nv, kPlaceGroup, tm, tn);
+        h0 = tm * kTile;
+        v0 = tn * kTile;
+        return true;
+    };
+    Stream stream;
+    stream.run(
+        ldh, ldg,
+        [&](int i) -> GemmWork {
+            int h0, v0;
+            if (!place(i, h0, v0)) return {{job.rows, ldh, 0}, {job.G, ldg, 0}, 0};
+            GemmWork w = {operand_ks<T>(job.rows, ldh, h0, 0), operand_ks<T>(job.G, ldg, v0, 0), K};
+            if (R == 0) w.a.valid = w.b.valid = 1 << 30;  // (past every row: nothing is read)
+            return w;
+        },
+        [&](int i) {
+            int h0 = 0, v0 = 0;
+            place(i, h0, v0);
+            stream.store_rows(weight_rows<T>(job, v0), (int)ldh, h0 * 2, (int)ldh, lds, wave, lane,
+                              [&](int mi, int ni) { return stream.acc[mi][ni]; });
+        },
+        lds, wave, lane);
 }
 
 // ---- plans and launches ------------------------------------------------------------------------
@@ -589,8 +699,11 @@ struct Plan {
     int nv;
     // backward
     int piece, pieces;       // columns (a multiple of 256), number
-    int splits, per;         // of a piece, for grad_hidden
+    int splits;              // of a piece, for grad_hidden: at most, all of them in the first one
     size_t rows, place, count, flags, parts, scale, G, sums, forward, backward;
+
+    // columns of a split in a piece of `width`
+    int per(int width) const { return ceil_div(ceil_div(width, splits), 64) * 64; }
 };
 
 int waves_m(int bn) { return bn == 256 ? 2 : bn == 128 ? 4 : 8; }
@@ -602,19 +715,20 @@ Plan plan(int R, int H, int V, int elem) {
     p.nr = ceil_div(R, p.bn);
     p.wm = waves_m(p.bn);
     p.nv = ceil_div(V, kTile);
-    int64_t most = kPieceBytes / ((int64_t)R * elem) / kTile * kTile;
-    most = most < kTile ? kTile : most > kPieceMost ? kPieceMost : most;
-    p.pieces = ceil_div(V, most);
-    p.piece = ceil_div(ceil_div(V, p.pieces), kTile) * kTile;  // (pieces of about one size)
+    // a piece: whole rounds of tiles over the CUs, if as many fit
+    int64_t most = kPieceBytes / ((int64_t)R * elem) / kTile;
+    most = most < 1 ? 1 : most > kPieceMost / kTile ? kPieceMost / kTile : most;
+    int round = kCus;
+    for (int n = p.nr; n % 2 == 0 && round > 1; n /= 2) round /= 2;
+    if (most > round) most = most / round * round;
+    p.piece = (int)(most < p.nv ? most : p.nv) * kTile;
     p.pieces = ceil_div(V, p.piece);
-    // grad_hidden: enough workgroups for every CU, a split of 1024 columns at least
-    const int tiles = ceil_div(H, kTile) * p.nr;
-    int s = kCus / tiles;
-    const int longest = p.piece / 1024;
-    s = s > longest ? longest : s;
-    s = s < 1 ? 1 : s;
-    p.per = ceil_div(ceil_div(p.piece, s), 64) * 64;
-    p.splits = ceil_div(p.piece < V ? p.piece : V, p.per);  // (every one has columns of piece 0)
+    // grad_hidden: a workgroup for every CU, splits of 1024 columns at least
+    const int tiles = ceil_div(H, kTile) * p.nr, width = p.piece < V ? p.piece : V;
+    const int longest = width / 1024;
+    p.splits = kCus / tiles < longest ? kCus / tiles : longest;
+    p.splits = p.splits < 1 ? 1 : p.splits;
+    p.splits = ceil_div(width, p.per(width));
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t a = at;
@@ -636,11 +750,21 @@ Plan plan(int R, int H, int V, int elem) {
     return p;
 }
 
+// (bf16 tiles of 256 rows go through a stream, one workgroup per CU.)
 template <typename T, bool GRAD>
 void launch_logits(int bn, const LogitsJob &job, hipStream_t s) {
-    const dim3 grid(job.nv * job.nr), block(kGemmThreads);
+    const int tiles = job.nv * job.nr;
+    const dim3 grid(tiles), block(kGemmThreads);
+    if constexpr (sizeof(T) == 2) {
+        if (bn == kTile) {
+            lmloss_logits_stream_kernel<T, GRAD><<<tiles < kCus ? tiles : kCus, block, 0, s>>>(job);
+            return;
+        }
+    } else if (bn == kTile) {
+        lmloss_logits_kernel<T, 256, 2, GRAD><<<grid, block, 0, s>>>(job);
+        return;
+    }
     switch (bn) {
-    case 256: lmloss_logits_kernel<T, 256, 2, GRAD><<<grid, block, 0, s>>>(job); break;
     case 128: lmloss_logits_kernel<T, 128, 4, GRAD><<<grid, block, 0, s>>>(job); break;
     case 64: lmloss_logits_kernel<T, 64, 8, GRAD><<<grid, block, 0, s>>>(job); break;
     default: lmloss_logits_kernel<T, 32, 8, GRAD><<<grid, block, 0, s>>>(job); break;
@@ -649,13 +773,32 @@ void launch_logits(int bn, const LogitsJob &job, hipStream_t s) {
 
 template <typename T>
 void launch_hidden(int bn, const HiddenJob &job, hipStream_t s) {
-    const dim3 grid(job.nh * job.nr * job.splits), block(kGemmThreads);
+    const int tiles = job.nh * job.nr * job.splits;
+    const dim3 grid(tiles), block(kGemmThreads);
+    if constexpr (sizeof(T) == 2) {
+        if (bn == kTile) {
+            lmloss_hidden_stream_kernel<T><<<tiles < kCus ? tiles : kCus, block, 0, s>>>(job);
+            return;
+        }
+    } else if (bn == kTile) {
+        lmloss_hidden_kernel<T, 256, 2><<<grid, block, 0, s>>>(job);
+        return;
+    }
     switch (bn) {
-    case 256: lmloss_hidden_kernel<T, 256, 2><<<grid, block, 0, s>>>(job); break;
     case 128: lmloss_hidden_kernel<T, 128, 4><<<grid, block, 0, s>>>(job); break;
     case 64: lmloss_hidden_kernel<T, 64, 8><<<grid, block, 0, s>>>(job); break;
     default: lmloss_hidden_kernel<T, 32, 8><<<grid, block, 0, s>>>(job); break;
     }
+}
+
+template <typename T>
+void launch_weight(const WeightJob &job, hipStream_t s) {
+    const int tiles = job.nh * job.nv;
+    if constexpr (sizeof(T) == 2)
+        lmloss_weight_stream_kernel<T>
+            <<<tiles < kCus ? tiles : kCus, kGemmThreads, 0, s>>>(job);
+    else
+        lmloss_weight_kernel<T><<<tiles, kGemmThreads, 0, s>>>(job);
 }
 
 template <typename T>
@@ -693,8 +836,9 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     lj.nr = p.nr;
     lj.c = c;
     lj.parts = reinterpret_cast<float2 *>(ws + p.parts);
+    lj.nparts = (int64_t)p.nv * p.wm;
     launch_logits<T, false>(p.bn, lj, s);
-    FinishJob fj = {lj.parts, (int64_t)p.nv * p.wm, gj.place, e, R, V, c, loss, stats};
+    FinishJob fj = {lj.parts, lj.nparts, gj.place, e, R, V, c, loss, stats};
     lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
     return hipGetLastError();
 }
@@ -738,14 +882,15 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
         EntriesJob ej = {e, stats, grad_loss, gj.place, R, V, v0, v1, c, lj.G, p.piece};
         lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
         if (grad_hidden) {
-            HiddenJob hj = {lj.W, ws + p.G, gj.count, R, H, v0, v1, p.piece, nh, p.nr, p.splits,
-                            p.per, i == 0, reinterpret_cast<float *>(ws + p.sums)};
-            hj.splits = ceil_div(v1 - v0, p.per);
+            const int per = p.per(v1 - v0);
+            HiddenJob hj = {lj.W, ws + p.G, gj.count, R, H, v0, v1, p.piece, nh, p.nr,
+                            ceil_div(v1 - v0, per), per, i == 0,
+                            reinterpret_cast<float *>(ws + p.sums)};
             launch_hidden<T>(p.bn, hj, s);
         }
         if (grad_W) {
             WeightJob wj = {gj.rows, ws + p.G, gj.count, H, v0, v1, p.piece, nh, lj.nv, grad_W};
-            lmloss_weight_kernel<T><<<nh * lj.nv, kGemmThreads, 0, s>>>(wj);
+            launch_weight<T>(wj, s);
         }
     }
     if (grad_hidden)
