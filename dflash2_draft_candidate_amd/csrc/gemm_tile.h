@@ -71,11 +71,17 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
     static constexpr int kStepK = kStepBytes / (int)sizeof(T);
     static constexpr int kLoads = kBytes / 1024;  // of 1 KB, one wave's
     static constexpr int kPerWave = (kLoads + kGemmWaves - 1) / kGemmWaves;
+    static_assert(kLoads % kGemmWaves == 0 || kGemmWaves % kLoads == 0, "the waves share the loads");
     static constexpr int kRowBytes = B * (int)sizeof(T);  // KS
     static constexpr int kRowChunks = kRowBytes / 16;
 
     int voff[kPerWave];  // the lane's bytes within the operand's step
     int kbyte;           // KC: the first byte of k that the lane reads
+
+    // Where the stage has fewer than 8 loads, some waves make the same one: every wave counts the same.
+    static __device__ __forceinline__ int load_of(int wave, int q) {
+        return kLoads < kGemmWaves ? wave % kLoads : wave + kGemmWaves * q;
+    }
 
     static __device__ __forceinline__ int tile_row(int i) {
         return G == 0 ? i : (i / (G ? G : 1)) * 2 * G + i % (G ? G : 1);
@@ -85,7 +91,7 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
         kbyte = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
         for (int q = 0; q < kPerWave; ++q) {
-            const int load = wave + kGemmWaves * q;
+            const int load = load_of(wave, q);
             if constexpr (!KS) {
                 voff[q] = tile_row(8 * load + (lane >> 3)) * (int)ld + kbyte;
             } else {
@@ -110,7 +116,7 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
         return KS ? ld * kStepK : (int64_t)kStepBytes;
     }
 
-    // Starts the loads of a step into LDS at `to` (for this wave). p: the step's first byte of the
+    // Starts this wave's loads of a step into the stage at `to`. p: the step's first byte of the
     // operand; `valid` as the operand's, counted from p; kleft: values of k left.
     __device__ __forceinline__ void issue(uint32_t to, const char *p, int ld, int valid, int kleft,
                                           int wave) const {
@@ -128,11 +134,10 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
         rs.w = kGemmWord3;
 #pragma unroll
         for (int q = 0; q < kPerWave; ++q) {
-            if (kLoads % kGemmWaves != 0 && wave + kGemmWaves * q >= kLoads) break;
             int off = voff[q];
             if constexpr (!KS) off = kbyte < kleft * (int)sizeof(T) ? off : kGemmOutside;
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
-                             to + q * kGemmWaves * 1024),
+                             to + load_of(wave, q) * 1024),
                          "v"(off), "s"(rs)
                          : "memory");
         }
@@ -278,7 +283,7 @@ template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile 
             for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
 
         constexpr int kStage = SideA::kBytes + SideB::kBytes;
-        const uint32_t base = lds_address(lds) + wave * 1024;
+        const uint32_t base = lds_address(lds);
         const int steps = (K + kStepK - 1) / kStepK;
         const char *pa = A.base, *pb = B.base;
         int kleft = K;
@@ -323,6 +328,103 @@ template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile 
     }
 };
 
+// ---- few columns: a ring of stages ---------------------------------------------------------------
+// Tiles of BM x BN where the read of A is the bound (BN <= 128): each wave takes BM / 8 rows and all
+// columns. A stage is SUB consecutive K steps; the ring holds as many as LDS does, and all but the one
+// that is read are on their way. The loads run ahead from one tile of the workgroup into the next.
+struct GemmWork {
+    GemmOperand a, b;
+    int K;  // <= 0: no tile
+};
+
+template <typename T, int BM_, int BN, int SUB, bool AS, bool BS> struct GemmRing {
+    static constexpr int BM = BM_, WM = 8, WN = 1, MI = BM / 128, NI = BN / 16, kCols = BN;
+    typedef GemmSide<T, BM, AS> SideA;
+    typedef GemmSide<T, BN, BS> SideB;
+    static constexpr int kStepK = SideA::kStepK;
+    static constexpr int kStep = SideA::kBytes + SideB::kBytes, kStage = SUB * kStep;
+    static constexpr int kStages = 163840 / kStage;
+    static constexpr int kLdsBytes = kStages * kStage;
+    static constexpr int kLoads = SUB * (SideA::kPerWave + SideB::kPerWave);  // a wave's, per stage
+    static_assert(kStages >= 3 && (kStages - 2) * kLoads < 64, "stages");
+
+    f32x4 acc[MI][NI];
+
+    static __device__ __forceinline__ int wave_m(int wave) { return wave * (BM / WM); }
+    static __device__ __forceinline__ int wave_n(int) { return 0; }
+
+    // work(i): the workgroup's tile i, K = 0 behind the last; done(i): its epilogue, on acc. All tiles
+    // share the operands' ld. Behind the last tile LDS is free.
+    template <typename Work, typename Done>
+    __device__ __forceinline__ void run(int64_t lda, int64_t ldb, Work work, Done done, char *lds,
+                                        int wave, int lane) {
+        SideA sa;
+        SideB sb;
+        sa.init(lda, wave, lane);
+        sb.init(ldb, wave, lane);
+        typename SideA::template Reader<MI> ra;
+        typename SideB::template Reader<NI> rb;
+        ra.init(wave_m(wave), lane);
+        rb.init(0, lane);
+        const uint32_t base = lds_address(lds);
+        const int64_t da = SideA::stride(lda), db = SideB::stride(ldb);
+        GemmWork at = work(0);
+        int next = 1, kleft = at.K;
+        auto issue = [&](int slot) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                const uint32_t to = base + slot * kStage + u * kStep;
+                sa.issue(to, at.a.base, (int)lda, at.a.valid, kleft, wave);
+                sb.issue(to + SideA::kBytes, at.b.base, (int)ldb, at.b.valid, kleft, wave);
+                at.a.base += da;
+                at.b.base += db;
+                kleft -= kStepK;
+            }
+            if (kleft <= 0 && at.K > 0) {  // (behind the last tile: loads of nothing)
+                at = work(next++);
+                kleft = at.K;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int slot = 0;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue(i);
+        for (int i = 0;; ++i) {
+            const int K = work(i).K;
+            if (K <= 0) break;
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < K; k += SUB * kStepK) {
+                // this stage has landed in every wave, and every wave has read the one before it
+                gemm_barrier<(kStages - 2) * kLoads>();
+                issue(slot == 0 ? kStages - 1 : slot - 1);
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const char *sta = lds + slot * kStage + u * kStep, *stb = sta + SideA::kBytes;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        typename SideA::Frag fa[MI];
+#pragma unroll
+                        for (int mi = 0; mi < MI; ++mi) fa[mi] = ra.read(sta, mi, h);
+#pragma unroll
+                        for (int ni = 0; ni < NI; ++ni) {
+                            const typename SideB::Frag fb = rb.read(stb, ni, h);
+#pragma unroll
+                            for (int mi = 0; mi < MI; ++mi)
+                                acc[mi][ni] = gemm_mfma(fa[mi], fb, acc[mi][ni]);
+                        }
+                    }
+                }
+                slot = slot == kStages - 1 ? 0 : slot + 1;
+            }
+            done(i);
+        }
+        gemm_barrier<0>();
+    }
+};
+
 // ---- a stream of 256 x 256 tiles ---------------------------------------------------------------
 // The waves form two groups of four, one wave of each on every SIMD. A K step is four phases, each a
 // quarter of the wave's 128 x 64 (64 x 32: 16 matrix instructions); in a phase a wave first reads the
@@ -340,11 +442,6 @@ template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile 
 //     the first six phases behind it, whose halves were asked for before them, do not wait for them.
 // 4096 x 4096 x 16384 bf16: 1314 TFLOP/s (KC x KC), 1319 (KS x KC), 1366 (KS x KS); one stage of
 // 64 KB ahead and a barrier per step (GemmTile): 1123, 1201, 1217.
-struct GemmWork {
-    GemmOperand a, b;
-    int K;  // <= 0: no tile
-};
-
 template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
     static constexpr int WM = 2, WN = 4, MI = 8, NI = 4, BM = 256, BN = 256, kCols = BN;
     typedef GemmSide<T, 128, AS, 64> SideA;
@@ -381,7 +478,7 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
         rb.init((wave % WN) * 32, lane);
 
         // what the loads are at: two steps ahead of the products
-        const uint32_t base = lds_address(lds) + wave * 1024;
+        const uint32_t base = lds_address(lds);
         const int64_t da = SideA::stride(lda), db = SideB::stride(ldb);
         const int64_t half_a = AS ? 64 * (int)sizeof(T) : 64 * lda;
         const int64_t half_b = BS ? 32 * (int)sizeof(T) : 32 * ldb;

@@ -38,10 +38,14 @@ constexpr int kPieceMost = 1 << 20;              // columns of a piece (32-bit o
 constexpr int kPlaceGroup = 8;                   // rows of tiles that share columns of tiles
 constexpr int kCus = 256;
 
-// Rows of a tile's hidden side for R rows.
-int row_tile(int R) { return R > 128 ? 256 : R > 64 ? 128 : R > 32 ? 64 : 32; }
-
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Few kept rows: ranges of the vocabulary (of `width` columns, 16 at least each) for nr tiles of kept
+// rows: a workgroup per CU.
+__host__ __device__ __forceinline__ int few_ranges(int width, int nr) {
+    const int units = (width + 15) / 16, most = nr > kCus ? 1 : kCus / (nr > 0 ? nr : 1);
+    return units < most ? units : most;
+}
 
 // What a row's kept statistics hold, [K + 2] floats: the maximum of its logits, the sum of
 // exp((x - max) / tau) (kLeftOut: a row without an entry), the entries' logits.
@@ -166,6 +170,7 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
             w[j] = job.W + (id_ok(id, job.V) ? id : 0) * row_bytes;
             sum[j] = 0.f;
         }
+#pragma unroll 4
         for (int64_t b = lane * 16; b < row_bytes; b += kWave * 16) {
             const u32x4 h = *reinterpret_cast<const u32x4 *>(src + b);
             if (copies) *reinterpret_cast<u32x4 *>(dst + b) = h;
@@ -191,6 +196,13 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
 
 // ---- the product's epilogues ---------------------------------------------------------------------
 
+// (ref, sum) pairs in natural units: sum counts exp((x - ref) / tau). NaN in either stays.
+__device__ __forceinline__ void join(float &m, float &s, float om, float os, float c) {
+    const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.f : top;
+    s = s * __builtin_amdgcn_exp2f((m - ref) * c) + os * __builtin_amdgcn_exp2f((om - ref) * c);
+    m = top;
+}
+
 struct LogitsJob {
     const char *rows;     // [count, H]
     const char *W;        // [V, H]
@@ -204,6 +216,7 @@ struct LogitsJob {
     void *G;              // backward: [count][ldg]
     int64_t ldg;          // columns
     const float2 *scale;  // backward: [count]
+    int low;              // few rows: the row of G where what rounding left of row 0 stands, or 0
 };
 
 // A tile's end: for GRAD G's values, else maxima and sums. Its vocabulary rows start at v0, its
@@ -253,25 +266,9 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
             if (g == 0 && r < R)
                 job.parts[((r >> 4) * job.nparts + part + wave / Tile::WN) * 16 + (r & 15)] =
                     float2{top, sum};
-        } else if constexpr (std::is_same<Tile, GradStream<T>>::value) {
-            break;  // (stored below)
-        } else {
-            const float2 s = job.scale[min(r, R - 1)];
-            const int off = rn * (int)ldg + (vw - v0) * (int)sizeof(T);
-#pragma unroll
-            for (int mi = 0; mi < Tile::MI; ++mi) {
-                f32x4 y;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[i] = s.y * __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - s.x) * c);
-                    if (ragged && vw + 16 * mi + i >= job.v1) y[i] = 0.f;
-                }
-                store4<T>(out, off + 16 * mi * (int)sizeof(T), y);
-                __builtin_amdgcn_sched_barrier(0);  // (all at once would not fit the registers)
-            }
         }
     }
-    if constexpr (GRAD && std::is_same<Tile, GradStream<T>>::value) {
+    if constexpr (GRAD) {
         float2 s[Tile::NI];
 #pragma unroll
         for (int ni = 0; ni < Tile::NI; ++ni)
@@ -288,26 +285,7 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
     }
 }
 
-// Tiles of 256 vocabulary rows x BN kept rows, one a workgroup.
-template <typename T, int BN, int WM_, bool GRAD>
-__global__ __launch_bounds__(kGemmThreads) void lmloss_logits_kernel(LogitsJob job) {
-    typedef GemmTile<T, kTile, BN, false, false, WM_> Tile;
-    __shared__ __align__(1024) char lds[Tile::kLdsBytes];
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count, nr = (R + BN - 1) / BN;
-    if ((int)blockIdx.x >= job.nv * nr) return;
-    int tm, tn;
-    gemm_place(blockIdx.x, job.nv, nr, kPlaceGroup, tm, tn);
-    const int v0 = job.v0 + tm * kTile, r0 = tn * BN;
-    const int64_t ld = (int64_t)job.H * sizeof(T);
-    Tile tile;
-    tile.run(operand_kc<T>(job.W, ld, v0, job.v1, 0), operand_kc<T>(job.rows, ld, r0, R, 0), job.H,
-             lds, wave, lane);
-    logits_done<T, GRAD>(job, tile, v0, r0, R, (int64_t)tm * WM_, lds, wave, lane);
-}
-
-// The same with 256 kept rows a tile, as a stream.
+// Tiles of 256 vocabulary rows x 256 kept rows, bf16.
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(LogitsJob job) {
     typedef typename std::conditional<GRAD, GradStream<T>, StatsStream<T>>::type Stream;
@@ -344,22 +322,133 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(Logi
         lds, wave, lane);
 }
 
-// ---- forward's end -------------------------------------------------------------------------------
-
-// (ref, sum) pairs in natural units: sum counts exp((x - ref) / tau). NaN in either stays.
-__device__ __forceinline__ void join(float &m, float &s, float om, float os, float c) {
-    const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.f : top;
-    s = s * __builtin_amdgcn_exp2f((m - ref) * c) + os * __builtin_amdgcn_exp2f((om - ref) * c);
-    m = top;
+// Few kept rows (BN <= 128 a tile), or f32: a workgroup takes a range of the vocabulary (a multiple of 16
+// rows of W) and goes through it in tiles of 128 or 256. Forward: each lane keeps its columns' (max, sum) over
+// the whole range. G of few bf16 rows is kept in two parts (rounded, and what that left): the products
+// that read it are bound by W and the gradient, and two parts cost them nothing.
+template <typename T, int BN, bool GRAD>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJob job) {
+    // bf16 of up to 64 rows: stages of two K steps, 256 bytes of each of 128 rows of W. f32: the matrix
+    // cores are the bound, and shorter tiles leave less of a range's last one unused.
+    constexpr int SUB = sizeof(T) == 2 && BN <= 64 ? 2 : 1, BM = sizeof(T) == 4 || SUB == 2 ? 128 : 256;
+    typedef GemmRing<T, BM, BN, SUB, false, false> Ring;
+    __shared__ __align__(1024) char lds[Ring::kLdsBytes];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count, nr = (R + BN - 1) / BN, ranges = few_ranges(job.v1 - job.v0, nr);
+    if ((int)blockIdx.x >= ranges * nr) return;
+    int range, tn;
+    gemm_place(blockIdx.x, ranges, nr, 1, range, tn);
+    const int units = (job.v1 - job.v0 + 15) / 16, r0 = tn * BN;
+    const int lo = job.v0 + 16 * (int)((int64_t)units * range / ranges);
+    const int hi = min(job.v0 + 16 * (int)((int64_t)units * (range + 1) / ranges), job.v1);
+    const int64_t ld = (int64_t)job.H * sizeof(T);
+    const float c = job.c;
+    float top[Ring::NI], sum[Ring::NI];
+#pragma unroll
+    for (int ni = 0; ni < Ring::NI; ++ni) {
+        top[ni] = -INFINITY;
+        sum[ni] = 0.f;
+    }
+    Ring ring;
+    ring.run(
+        ld, ld,
+        [&](int i) -> GemmWork {
+            const int v0 = lo + i * BM;
+            if (v0 >= hi) return {{job.W, ld, 0}, {job.rows, ld, 0}, 0};
+            return {operand_kc<T>(job.W, ld, v0, hi, 0), operand_kc<T>(job.rows, ld, r0, R, 0), job.H};
+        },
+        [&](int i) {
+            const int at = anew(lane), g = at >> 4, j = at & 15;
+            const int v0 = lo + i * BM, vw = v0 + Ring::wave_m(wave) + 4 * g;
+            const int64_t ldg = job.ldg * (int64_t)sizeof(T);
+            const bool ragged = v0 + BM > hi;
+            const __amdgpu_buffer_rsrc_t out = out_rows(
+                static_cast<char *>(job.G) + r0 * ldg + (int64_t)(v0 - job.v0) * sizeof(T), ldg,
+                job.low ? 2 * job.low : sizeof(T) == 2 ? BN : min(R - r0, BN), BM * sizeof(T));
+#pragma unroll
+            for (int ni = 0; ni < Ring::NI; ++ni) {
+                const int rn = 16 * ni + j, r = r0 + rn;
+                if constexpr (!GRAD) {
+                    float high = top[ni];
+#pragma unroll
+                    for (int mi = 0; mi < Ring::MI; ++mi)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (ragged && vw + 16 * mi + k >= hi) ring.acc[mi][ni][k] = -INFINITY;
+                            high = fmaxf(high, ring.acc[mi][ni][k]);
+                        }
+                    const float ref = high == -INFINITY ? 0.f : high;
+                    float s = sum[ni] * __builtin_amdgcn_exp2f((top[ni] - ref) * c);
+#pragma unroll
+                    for (int mi = 0; mi < Ring::MI; ++mi)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            s += __builtin_amdgcn_exp2f((ring.acc[mi][ni][k] - ref) * c);
+                    top[ni] = high;
+                    sum[ni] = s;
+                } else {
+                    const float2 sc = job.scale[min(r, R - 1)];
+#pragma unroll
+                    for (int mi = 0; mi < Ring::MI; ++mi) {
+                        const int v = vw + 16 * mi;
+                        f32x4 y;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            y[k] = sc.y * __builtin_amdgcn_exp2f((ring.acc[mi][ni][k] - sc.x) * c);
+                            if (r >= R || (ragged && v + k >= job.v1)) y[k] = 0.f;
+                        }
+                        // (hi is a multiple of 16 behind v0, or the piece's end)
+                        const int off = v - 4 * g < hi ? rn * (int)ldg + (v - v0) * (int)sizeof(T)
+                                                       : kGemmOutside;
+                        store4<T>(out, off, y);
+                        if (sizeof(T) == 2 && job.low) {
+                            f32x4 z;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) z[k] = y[k] - (float)(__bf16)y[k];
+                            store4<T>(out, off + (off == kGemmOutside ? 0 : job.low * (int)ldg), z);
+                        }
+                    }
+                }
+            }
+        },
+        lds, wave, lane);
+    if constexpr (!GRAD) {
+        float2 *pair = reinterpret_cast<float2 *>(lds);  // [waves][BN]
+        const int g = lane >> 4, j = lane & 15;
+#pragma unroll
+        for (int ni = 0; ni < Ring::NI; ++ni) {
+            float m = top[ni], s = sum[ni];
+#pragma unroll
+            for (int d = 16; d < kWave; d *= 2) {
+                const float om = __shfl_xor(m, d, kWave), os = __shfl_xor(s, d, kWave);
+                join(m, s, om, os, c);
+            }
+            if (g == 0) pair[wave * BN + 16 * ni + j] = float2{m, s};
+        }
+        __syncthreads();
+        const int n = threadIdx.x, r = r0 + n;
+        if (n < BN && r < R) {
+            float2 x = pair[n];
+            for (int w = 1; w < kGemmWaves; ++w) {
+                const float2 y = pair[w * BN + n];
+                join(x.x, x.y, y.x, y.y, c);
+            }
+            job.parts[((int64_t)(r >> 4) * ranges + range) * 16 + (r & 15)] = x;
+        }
+    }
 }
 
+// ---- forward's end -------------------------------------------------------------------------------
+
 constexpr int kFinishRows = 16;
-constexpr int kFinishThreads = 512;
+constexpr int kFinishThreads = 1024;
 
 struct FinishJob {
     const float2 *parts;
-    int64_t nparts;
-    const int32_t *place;
+    int64_t nparts;      // pairs of a row; or 0: few_ranges
+    const int32_t *place, *count;
+    int bn;
     Entries e;
     int R, V;
     float c;
@@ -370,15 +459,18 @@ struct FinishJob {
 // 16 rows: their tiles' pairs in a fixed order, then a wave per row over its entries.
 __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob job) {
     constexpr int kGroups = kFinishThreads / kFinishRows;
+    static_assert(kGroups == kWave, "a wave joins a row's groups");
     __shared__ float2 pair[kGroups][kFinishRows];
     const int first = blockIdx.x * kFinishRows;
+    const int64_t nparts = job.nparts ? job.nparts : few_ranges(job.V, (*job.count + job.bn - 1) / job.bn);
     {
         const int k = threadIdx.x % kFinishRows, grp = threadIdx.x / kFinishRows;
         const int r = first + k, p = r < job.R ? job.place[r] : -1;
         float m = -INFINITY, s = 0.f;
         if (p >= 0) {
-            const float2 *src = job.parts + (p >> 4) * job.nparts * 16 + (p & 15);
-            for (int64_t i = grp; i < job.nparts; i += kGroups) {
+            const float2 *src = job.parts + (p >> 4) * nparts * 16 + (p & 15);
+#pragma unroll 4
+            for (int64_t i = grp; i < nparts; i += kGroups) {
                 const float2 x = src[i * 16];
                 join(m, s, x.x, x.y, job.c);
             }
@@ -399,12 +491,10 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
             continue;
         }
         float m = -INFINITY, s = 0.f;
-        if (lane < kGroups) {
-            m = pair[lane][k].x;
-            s = pair[lane][k].y;
-        }
+        m = pair[lane][k].x;
+        s = pair[lane][k].y;
 #pragma unroll
-        for (int d = 1; d < kGroups; d *= 2) {
+        for (int d = 1; d < kWave; d *= 2) {
             const float om = __shfl_down(m, d, kWave), os = __shfl_down(s, d, kWave);
             if (lane % (2 * d) == 0) join(m, s, om, os, job.c);
         }
@@ -451,6 +541,7 @@ struct EntriesJob {
     float c;
     void *G;
     int64_t ldg;
+    int low;
 };
 
 // One wave per row: G at the row's entries, the masses of equal ids added in their order.
@@ -487,10 +578,13 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     // (fminf drops a NaN: a row whose sum is NaN keeps it)
     const float y = job.grad_loss[r] * job.e.tau * ((st[1] != st[1] ? st[1] : q) - total);
     T *out = static_cast<T *>(job.G) + p * job.ldg + (id - job.v0);
-    if constexpr (sizeof(T) == 2)
+    if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<__bf16 *>(out) = (__bf16)y;
-    else
+        if (job.low)
+            *reinterpret_cast<__bf16 *>(out + job.low * job.ldg) = (__bf16)(y - (float)(__bf16)y);
+    } else {
         *out = y;
+    }
 }
 
 // ---- the gradients' products -----------------------------------------------------------------------
@@ -499,14 +593,15 @@ struct HiddenJob {
     const char *W;       // [V, H]
     const char *G;       // [count][ldg]
     const int32_t *count;
-    int R, H, v0, v1;
+    int R, H, v0, v1;    // R: rows of G and of the sums
     int64_t ldg;
     int nh, nr, splits, per;  // tiles (of all R rows); splits of the piece, `per` columns each
     bool first;          // the first piece: nothing to add to
     float *sums;         // [splits][R][H]
+    int low;             // as the logits' job's
 };
 
-template <typename Tile>
+template <bool few, typename Tile>
 __device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, int split, int h0,
                                             int r0, int R, int wave, int lane) {
     lane = anew(lane);
@@ -516,11 +611,13 @@ __device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, in
         job.sums + ((int64_t)split * job.R + r0) * job.H, ld, min(R - r0, Tile::kCols), ld);
 #pragma unroll
     for (int ni = 0; ni < Tile::NI; ++ni) {
-        const int row = (Tile::wave_n(wave) + 16 * ni + j) * ld;
+        const int n = Tile::wave_n(wave) + 16 * ni + j, row = n * ld;
+        // (few rows: those that hold something)
+        const bool some = !few || (n >= job.low && job.low ? n - job.low : n) < *job.count;
 #pragma unroll
         for (int mi = 0; mi < Tile::MI; ++mi) {
             const int h = h0 + Tile::wave_m(wave) + 16 * mi + 4 * g;
-            const int off = h < job.H ? row + 4 * h : kGemmOutside;
+            const int off = some && h < job.H ? row + 4 * h : kGemmOutside;
             f32x4 x = tile.acc[mi][ni];
             if (!job.first)
                 x += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(out, off, 0, 0));
@@ -529,26 +626,33 @@ __device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, in
     }
 }
 
-// Tiles of 256 columns of H x BN kept rows over a split of the piece, one a workgroup.
-template <typename T, int BN, int WM>
-__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_kernel(HiddenJob job) {
-    typedef GemmTile<T, kTile, BN, true, false, WM> Tile;
-    __shared__ __align__(1024) char lds[Tile::kLdsBytes];
+// Few kept rows, or f32: tiles of 256 columns of H x BN rows of G over a split of the piece, one a
+// workgroup.
+template <typename T, int BN>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJob job) {
+    typedef GemmRing<T, kTile, BN, 1, true, false> Ring;
+    __shared__ __align__(1024) char lds[Ring::kLdsBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count, nr = (R + BN - 1) / BN;
+    const int R = sizeof(T) == 2 ? BN : *job.count, nr = (R + BN - 1) / BN;
     if ((int)blockIdx.x >= job.nh * job.splits * nr) return;
     int tm, tn;
     gemm_place(blockIdx.x, job.nh * job.splits, nr, kPlaceGroup, tm, tn);
     const int split = tm / job.nh, h0 = tm % job.nh * kTile, r0 = tn * BN;
     const int k0 = split * job.per, k1 = min(k0 + job.per, job.v1 - job.v0);
-    Tile tile;
-    tile.run(operand_ks<T>(job.W, (int64_t)job.H * sizeof(T), h0, job.v0 + k0),
-             operand_kc<T>(job.G, job.ldg * (int64_t)sizeof(T), r0, R, k0), k1 - k0, lds, wave, lane);
-    hidden_done(job, tile, split, h0, r0, R, wave, lane);
+    const int64_t ldw = (int64_t)job.H * sizeof(T), ldg = job.ldg * (int64_t)sizeof(T);
+    Ring ring;
+    ring.run(
+        ldw, ldg,
+        [&](int i) -> GemmWork {
+            if (i > 0) return {{job.W, ldw, 0}, {job.G, ldg, 0}, 0};
+            return {operand_ks<T>(job.W, ldw, h0, job.v0 + k0), operand_kc<T>(job.G, ldg, r0, R, k0),
+                    k1 - k0};
+        },
+        [&](int) { hidden_done<sizeof(T) == 2>(job, ring, split, h0, r0, R, wave, lane); }, lds, wave, lane);
 }
 
-// The same with 256 kept rows a tile, as a stream.
+// Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(HiddenJob job) {
     typedef GemmStream<T, true, false, 32> Stream;  // (hidden_done: 32 stores)
@@ -580,26 +684,37 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
         [&](int i) {
             int split = 0, h0 = 0, r0 = 0;
             place(i, split, h0, r0);
-            hidden_done(job, stream, split, h0, r0, R, wave, lane);
+            hidden_done<false>(job, stream, split, h0, r0, R, wave, lane);
         },
         lds, wave, lane);
 }
 
-// grad_hidden from the splits' sums, in split order; zeros for the rows left out. One workgroup per
-// row.
+// grad_hidden from the splits' sums, added in a fixed order (and from the two parts of G, `low` rows
+// apart); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per quarter of the
+// splits.
 template <typename T>
-__global__ __launch_bounds__(256) void lmloss_hidden_out_kernel(const float *sums, int splits,
-                                                                const int32_t *place, int R, int H,
+__global__ __launch_bounds__(256) void lmloss_hidden_out_kernel(const float *sums, int splits, int rows,
+                                                                int low, const int32_t *place, int H,
                                                                 T *grad) {
-    const int r = blockIdx.x, p = place[r];
-    for (int h = threadIdx.x * 4; h < H; h += 1024) {
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-        if (p >= 0)
-            for (int s = 0; s < splits; ++s)
-                x += *reinterpret_cast<const f32x4 *>(sums + ((int64_t)s * R + p) * H + h);
-        const auto y = packed4<T>(x);
-        *reinterpret_cast<decltype(packed4<T>(x)) *>(grad + (int64_t)r * H + h) = y;
+    __shared__ f32x4 part[3][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int r = blockIdx.x, p = place[r], h = (blockIdx.y * kWave + lane) * 4;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (p >= 0 && h < H) {
+#pragma unroll 4
+        for (int s = wave; s < splits; s += 4) {
+            const float *at = sums + ((int64_t)s * rows + p) * H + h;
+            x += *reinterpret_cast<const f32x4 *>(at);
+            if (low) x += *reinterpret_cast<const f32x4 *>(at + (int64_t)low * H);
+        }
     }
+    if (wave > 0) part[wave - 1][lane] = x;
+    __syncthreads();
+    if (wave > 0 || h >= H) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) x += part[w][lane];
+    const auto y = packed4<T>(x);
+    *reinterpret_cast<decltype(packed4<T>(x)) *>(grad + (int64_t)r * H + h) = y;
 }
 
 struct WeightJob {
@@ -613,28 +728,29 @@ struct WeightJob {
 };
 
 template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_rows(const WeightJob &job, int v0) {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_rows(const WeightJob &job, int v0,
+                                                              int most) {
     const int ld = job.H * (int)sizeof(T);
     return out_rows(static_cast<char *>(job.grad) + (int64_t)(job.v0 + v0) * ld, ld,
-                    min(job.v1 - job.v0 - v0, kTile), ld);
+                    min(job.v1 - job.v0 - v0, most), ld);
 }
 
-// Tiles of 256 columns of H x 256 vocabulary rows, over the kept rows; one a workgroup.
+// f32: tiles of 256 columns of H x 128 vocabulary rows, over the kept rows; one a workgroup.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob job) {
-    typedef GemmTile<T, kTile, kTile, true, true, 2> Tile;
+    typedef GemmTile<T, kTile, 128, true, true, 4> Tile;
     __shared__ __align__(1024) char lds[Tile::kLdsBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int R = *job.count;
     int tm, tn;
     gemm_place(blockIdx.x, job.nh, job.nv, kPlaceGroup, tm, tn);
-    const int h0 = tm * kTile, v0 = tn * kTile;
+    const int h0 = tm * kTile, v0 = tn * Tile::kCols;
     Tile tile;
     tile.run(operand_ks<T>(job.rows, (int64_t)job.H * sizeof(T), h0, 0),
              operand_ks<T>(job.G, job.ldg * (int64_t)sizeof(T), v0, 0), R, lds, wave, lane);
-    const int g = lane >> 4, j = lane & 15;
-    const __amdgpu_buffer_rsrc_t out = weight_rows<T>(job, v0);
+    const int at = anew(lane), g = at >> 4, j = at & 15;
+    const __amdgpu_buffer_rsrc_t out = weight_rows<T>(job, v0, Tile::kCols);
 #pragma unroll
     for (int ni = 0; ni < Tile::NI; ++ni) {
         const int row = (Tile::wave_n(wave) + 16 * ni + j) * job.H * (int)sizeof(T);
@@ -647,7 +763,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
     }
 }
 
-// The same as a stream.
+// bf16, more than 128 kept rows: tiles of 256 columns of H x 256 vocabulary rows.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(WeightJob job) {
     typedef GemmStream<T, true, true, 16> Stream;
@@ -680,10 +796,120 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
         [&](int i) {
             int h0 = 0, v0 = 0;
             place(i, h0, v0);
-            stream.store_rows(weight_rows<T>(job, v0), (int)ldh, h0 * 2, (int)ldh, lds, wave, lane,
+            stream.store_rows(weight_rows<T>(job, v0, kTile), (int)ldh, h0 * 2, (int)ldh, lds, wave, lane,
                               [&](int mi, int ni) { return stream.acc[mi][ni]; });
         },
         lds, wave, lane);
+}
+
+// bf16, few kept rows: 64 STEPS rows of G (with `low`, in two parts). The output is the bound. A wave
+// keeps the kept rows' values at 64 columns of H as fragments, for a workgroup's 512, and goes through a
+// range of the vocabulary, 64 rows at a time: G's columns come through LDS, two buffers, and the output
+// goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows).
+struct WeightFewJob {
+    const uint16_t *rows;  // [count, H]
+    const char *G;         // [64 STEPS][ldg]
+    const int32_t *count;
+    int H, v0, v1, low;
+    int64_t ldg;
+    int slabs, ranges;     // of 512 columns of H; of the vocabulary, a multiple of 8
+    uint16_t *grad;        // [V, H]
+};
+
+template <int STEPS>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightFewJob job) {
+    typedef uint16_t T;
+    typedef GemmSide<T, 64, true> Side;
+    constexpr int kBuffer = STEPS * Side::kBytes;
+    constexpr int kStores = 8;  // a wave's, for 64 rows
+    __shared__ __align__(1024) char lds[2 * kBuffer + kGemmWaves * 4096];
+    const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count;
+    // (the slabs of a range run on one XCD, whose L2 gives them G)
+    const int at = blockIdx.x / 8, slab = at % job.slabs;
+    const int range = blockIdx.x % 8 + 8 * (at / job.slabs);
+    const int units = (job.v1 - job.v0 + 63) / 64;
+    const int u0 = (int)((int64_t)units * range / job.ranges);
+    const int u1 = (int)((int64_t)units * (range + 1) / job.ranges);
+    if (u0 >= u1) return;
+    const int h0 = slab * 512 + wave * 64;
+
+    Side side;
+    const int64_t ldg = job.ldg * (int64_t)sizeof(T);
+    side.init(ldg, wave, lane);
+    const uint32_t base = lds_address(lds);
+    auto issue = [&](int u, int buf) {
+        const bool in = u < u1 && R > 0;  // (without a kept row nothing has written G: zeros)
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            side.issue(base + buf * kBuffer + s * Side::kBytes,
+                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? 64 : 0, wave);
+    };
+    issue(u0, 0);
+    bf16x8 fa[2 * STEPS][4];
+#pragma unroll
+    for (int s = 0; s < 2 * STEPS; ++s)
+#pragma unroll
+        for (int mi = 0; mi < 4; ++mi) {
+            const int h = h0 + 16 * mi + j;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int k = 32 * s + 8 * g + e, r = job.low && k >= job.low ? k - job.low : k;
+                const uint16_t x = r < R && h < job.H ? job.rows[(int64_t)r * job.H + h] : 0;
+                fa[s][mi][e] = __builtin_bit_cast(__bf16, x);
+            }
+        }
+    Side::template Reader<4> rb;
+    rb.init(0, lane);
+    char *scratch = lds + 2 * kBuffer + wave * 4096;
+    const int ld = job.H * (int)sizeof(T);
+    const int row_in = lane >> 3, chunk = lane & 7;  // of the stores
+    const int h_out = h0 + 8 * chunk;
+    for (int u = u0; u < u1; ++u) {
+        const int buf = (u - u0) & 1;
+        // the loads of this buffer are older than the last 64 rows' stores
+        if (u == u0) gemm_barrier<0>(); else gemm_barrier<kStores>();
+        issue(u + 1, buf ^ 1);
+        f32x4 acc[4][4];
+#pragma unroll
+        for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2 * STEPS; ++s)
+#pragma unroll
+            for (int ni = 0; ni < 4; ++ni) {
+                const bf16x8 fb = rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, ni, s % 2);
+#pragma unroll
+                for (int mi = 0; mi < 4; ++mi) acc[mi][ni] = gemm_mfma(fa[s][mi], fb, acc[mi][ni]);
+            }
+        const int v = job.v0 + u * 64;
+        const __amdgpu_buffer_rsrc_t out =
+            out_rows(reinterpret_cast<char *>(job.grad) + (int64_t)v * ld, ld, min(job.v1 - v, 64), ld);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < 4; ++mi) {
+                    const auto x = packed4<T>(acc[mi][2 * half + ni]);
+                    const int row = 16 * ni + j;
+                    *reinterpret_cast<decltype(packed4<T>(f32x4{})) *>(
+                        scratch + row * 128 + (((2 * mi + (g >> 1)) ^ (row & 7)) << 4) + (g & 1) * 8) = x;
+                }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = 8 * q + row_in;
+                const u32x4 x =
+                    *reinterpret_cast<const u32x4 *>(scratch + row * 128 + ((chunk ^ (row & 7)) << 4));
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    x, out,
+                    h_out < job.H ? (32 * half + row) * ld + h_out * (int)sizeof(T) : kGemmOutside, 0, 0);
+            }
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);  // no load is in flight when the workgroup ends
 }
 
 // ---- plans and launches ------------------------------------------------------------------------
@@ -691,12 +917,12 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
-    int elem;
-    int bn;                  // row_tile
-    int nr;                  // tiles of rows
-    int wm;                  // waves along the vocabulary in a logits tile
+    int bn, nr;              // kept rows of a tile, tiles
+    bool few;                // tiles of at most 128 rows: rings (f32: always)
+    int low;                 // few bf16 rows: G in two parts, this many rows apart; or 0
+    int grows;               // rows of G
     // forward
-    int nv;
+    int nv;                  // tiles of the vocabulary
     // backward
     int piece, pieces;       // columns (a multiple of 256), number
     int splits;              // of a piece, for grad_hidden: at most, all of them in the first one
@@ -706,26 +932,31 @@ struct Plan {
     int per(int width) const { return ceil_div(ceil_div(width, splits), 64) * 64; }
 };
 
-int waves_m(int bn) { return bn == 256 ? 2 : bn == 128 ? 4 : 8; }
+// Rows of a tile for R rows. bf16: 256 from 129 rows on (two tiles of 128 read W twice); f32: 128 at
+// most (the matrix cores are the bound there, and smaller tiles leave less of the last one unused).
+int row_tile(int R, int elem) {
+    return R > 128 && elem == 2 ? 256 : R > 64 ? 128 : R > 32 ? 64 : 32;
+}
 
 Plan plan(int R, int H, int V, int elem) {
     Plan p;
-    p.elem = elem;
-    p.bn = row_tile(R);
+    p.bn = row_tile(R, elem);
     p.nr = ceil_div(R, p.bn);
-    p.wm = waves_m(p.bn);
+    p.few = p.bn <= 128;
+    p.low = elem == 2 && p.bn <= 64 ? p.bn : 0;
+    p.grows = elem == 2 && p.few ? p.bn + p.low : R;
     p.nv = ceil_div(V, kTile);
     // a piece: whole rounds of tiles over the CUs, if as many fit
-    int64_t most = kPieceBytes / ((int64_t)R * elem) / kTile;
+    int64_t most = kPieceBytes / ((int64_t)p.grows * elem) / kTile;
     most = most < 1 ? 1 : most > kPieceMost / kTile ? kPieceMost / kTile : most;
     int round = kCus;
     for (int n = p.nr; n % 2 == 0 && round > 1; n /= 2) round /= 2;
     if (most > round) most = most / round * round;
     p.piece = (int)(most < p.nv ? most : p.nv) * kTile;
     p.pieces = ceil_div(V, p.piece);
-    // grad_hidden: a workgroup for every CU, splits of 1024 columns at least
+    // grad_hidden: a workgroup for every CU, splits of 256 columns at least
     const int tiles = ceil_div(H, kTile) * p.nr, width = p.piece < V ? p.piece : V;
-    const int longest = width / 1024;
+    const int longest = width / 256;
     p.splits = kCus / tiles < longest ? kCus / tiles : longest;
     p.splits = p.splits < 1 ? 1 : p.splits;
     p.splits = ceil_div(width, p.per(width));
@@ -740,65 +971,74 @@ Plan plan(int R, int H, int V, int elem) {
     p.count = take(4);
     const size_t common = at;
     p.flags = take((size_t)R * 4);
-    p.parts = take((size_t)ceil_div(R, 16) * 16 * p.nv * p.wm * sizeof(float2));
+    // (few_ranges of the kept rows' tiles: 256 bn pairs, or one for each of more rows than that)
+    const size_t rows16 = (size_t)ceil_div(R, 16) * 16, few_most = (size_t)kCus * p.bn;
+    const size_t pairs = p.few ? (rows16 > few_most ? rows16 : few_most) : rows16 * p.nv * 2;
+    p.parts = take(pairs * sizeof(float2));
     p.forward = at;
     at = common;
     p.scale = take((size_t)R * sizeof(float2));
-    p.G = take((size_t)R * p.piece * elem);
-    p.sums = take((size_t)p.splits * R * H * 4);
+    p.G = take((size_t)p.grows * p.piece * elem);
+    p.sums = take((size_t)p.splits * p.grows * H * 4);
     p.backward = at;
     return p;
 }
 
-// (bf16 tiles of 256 rows go through a stream, one workgroup per CU.)
 template <typename T, bool GRAD>
-void launch_logits(int bn, const LogitsJob &job, hipStream_t s) {
-    const int tiles = job.nv * job.nr;
-    const dim3 grid(tiles), block(kGemmThreads);
+void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
+    const dim3 block(kGemmThreads);
     if constexpr (sizeof(T) == 2) {
-        if (bn == kTile) {
+        if (!p.few) {
+            const int tiles = job.nv * job.nr;
             lmloss_logits_stream_kernel<T, GRAD><<<tiles < kCus ? tiles : kCus, block, 0, s>>>(job);
             return;
         }
-    } else if (bn == kTile) {
-        lmloss_logits_kernel<T, 256, 2, GRAD><<<grid, block, 0, s>>>(job);
-        return;
     }
-    switch (bn) {
-    case 128: lmloss_logits_kernel<T, 128, 4, GRAD><<<grid, block, 0, s>>>(job); break;
-    case 64: lmloss_logits_kernel<T, 64, 8, GRAD><<<grid, block, 0, s>>>(job); break;
-    default: lmloss_logits_kernel<T, 32, 8, GRAD><<<grid, block, 0, s>>>(job); break;
+    const dim3 grid(job.nr > kCus ? job.nr : kCus);  // (whatever few_ranges gives for the kept rows)
+    switch (p.bn) {
+    case 128: lmloss_logits_few_kernel<T, 128, GRAD><<<grid, block, 0, s>>>(job); break;
+    case 64: lmloss_logits_few_kernel<T, 64, GRAD><<<grid, block, 0, s>>>(job); break;
+    default: lmloss_logits_few_kernel<T, 32, GRAD><<<grid, block, 0, s>>>(job); break;
     }
 }
 
 template <typename T>
-void launch_hidden(int bn, const HiddenJob &job, hipStream_t s) {
+void launch_hidden(const Plan &p, const HiddenJob &job, hipStream_t s) {
     const int tiles = job.nh * job.nr * job.splits;
     const dim3 grid(tiles), block(kGemmThreads);
     if constexpr (sizeof(T) == 2) {
-        if (bn == kTile) {
+        if (!p.few) {
             lmloss_hidden_stream_kernel<T><<<tiles < kCus ? tiles : kCus, block, 0, s>>>(job);
             return;
         }
-    } else if (bn == kTile) {
-        lmloss_hidden_kernel<T, 256, 2><<<grid, block, 0, s>>>(job);
-        return;
     }
-    switch (bn) {
-    case 128: lmloss_hidden_kernel<T, 128, 4><<<grid, block, 0, s>>>(job); break;
-    case 64: lmloss_hidden_kernel<T, 64, 8><<<grid, block, 0, s>>>(job); break;
-    default: lmloss_hidden_kernel<T, 32, 8><<<grid, block, 0, s>>>(job); break;
+    switch (p.bn + p.low) {
+    case 128: lmloss_hidden_few_kernel<T, 128><<<grid, block, 0, s>>>(job); break;
+    case 64: lmloss_hidden_few_kernel<T, 64><<<grid, block, 0, s>>>(job); break;
+    default:
+        if constexpr (sizeof(T) == 4) lmloss_hidden_few_kernel<T, 32><<<grid, block, 0, s>>>(job);
+        break;
     }
 }
 
 template <typename T>
-void launch_weight(const WeightJob &job, hipStream_t s) {
-    const int tiles = job.nh * job.nv;
-    if constexpr (sizeof(T) == 2)
-        lmloss_weight_stream_kernel<T>
-            <<<tiles < kCus ? tiles : kCus, kGemmThreads, 0, s>>>(job);
-    else
-        lmloss_weight_kernel<T><<<tiles, kGemmThreads, 0, s>>>(job);
+void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
+    if constexpr (sizeof(T) == 4) {
+        lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
+    } else if (p.few) {
+        WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.H, job.v0,
+                          job.v1, p.low, job.ldg, ceil_div(job.H, 512), 0,
+                          static_cast<uint16_t *>(job.grad)};
+        w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
+        const int grid = w.slabs * w.ranges;
+        if (p.grows > 64)
+            lmloss_weight_few_kernel<2><<<grid, kGemmThreads, 0, s>>>(w);
+        else
+            lmloss_weight_few_kernel<1><<<grid, kGemmThreads, 0, s>>>(w);
+    } else {
+        const int tiles = job.nh * job.nv;
+        lmloss_weight_stream_kernel<T><<<tiles < kCus ? tiles : kCus, kGemmThreads, 0, s>>>(job);
+    }
 }
 
 template <typename T>
@@ -836,9 +1076,9 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     lj.nr = p.nr;
     lj.c = c;
     lj.parts = reinterpret_cast<float2 *>(ws + p.parts);
-    lj.nparts = (int64_t)p.nv * p.wm;
-    launch_logits<T, false>(p.bn, lj, s);
-    FinishJob fj = {lj.parts, lj.nparts, gj.place, e, R, V, c, loss, stats};
+    lj.nparts = p.few ? 0 : p.nv * 2;
+    launch_logits<T, false>(p, lj, s);
+    FinishJob fj = {lj.parts, lj.nparts, gj.place, gj.count, p.bn, e, R, V, c, loss, stats};
     lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
     return hipGetLastError();
 }
@@ -878,25 +1118,27 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
         lj.G = ws + p.G;
         lj.ldg = p.piece;
         lj.scale = gj.scale;
-        launch_logits<T, true>(p.bn, lj, s);
-        EntriesJob ej = {e, stats, grad_loss, gj.place, R, V, v0, v1, c, lj.G, p.piece};
+        lj.low = p.low;
+        launch_logits<T, true>(p, lj, s);
+        EntriesJob ej = {e, stats, grad_loss, gj.place, R, V, v0, v1, c, lj.G, p.piece, p.low};
         lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
         if (grad_hidden) {
             const int per = p.per(v1 - v0);
-            HiddenJob hj = {lj.W, ws + p.G, gj.count, R, H, v0, v1, p.piece, nh, p.nr,
+            HiddenJob hj = {lj.W, ws + p.G, gj.count, p.grows, H, v0, v1, p.piece, nh, p.nr,
                             ceil_div(v1 - v0, per), per, i == 0,
-                            reinterpret_cast<float *>(ws + p.sums)};
-            launch_hidden<T>(p.bn, hj, s);
+                            reinterpret_cast<float *>(ws + p.sums), p.low};
+            launch_hidden<T>(p, hj, s);
         }
         if (grad_W) {
-            WeightJob wj = {gj.rows, ws + p.G, gj.count, H, v0, v1, p.piece, nh, lj.nv, grad_W};
-            launch_weight<T>(wj, s);
+            WeightJob wj = {gj.rows, ws + p.G, gj.count, H, v0, v1, p.piece, nh,
+                            ceil_div(v1 - v0, sizeof(T) == 4 ? 128 : kTile), grad_W};
+            launch_weight<T>(p, wj, s);
         }
     }
     if (grad_hidden)
-        lmloss_hidden_out_kernel<T><<<R, 256, 0, s>>>(reinterpret_cast<float *>(ws + p.sums),
-                                                      p.splits, gj.place, R, H,
-                                                      static_cast<T *>(grad_hidden));
+        lmloss_hidden_out_kernel<T><<<dim3(R, ceil_div(H, 256)), 256, 0, s>>>(
+            reinterpret_cast<float *>(ws + p.sums), p.splits, p.grows, p.low, gj.place, H,
+            static_cast<T *>(grad_hidden));
     return hipGetLastError();
 }
 
