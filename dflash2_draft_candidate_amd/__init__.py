@@ -13,6 +13,7 @@ pred_cb / succ_cb [V, r] (one dtype), anchor_ids [B] int32. See include/dflash2.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from array import array
 
@@ -792,18 +793,32 @@ def lmhead_distill_loss(hidden: torch.Tensor, W_lm: torch.Tensor, teacher_ids: t
 
 # ---- the global gradient norm, and clipping ----------------------------------------------------
 
-def _addresses(ts: list) -> array:
-    return array("Q", [t.data_ptr() for t in ts])
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_dtype_of = operator.attrgetter("dtype")
 
 
-def _grads(grads):
-    """The gradients as a list, and their sizes and types as host arrays."""
-    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
-    if not grads:
-        raise ValueError("no gradients")
-    _contig(*grads)
-    _same_device(grads[0].device, *grads)
-    return grads, array("q", [t.numel() for t in grads]), array("i", [_dtype(t) for t in grads])
+class _Tensors:
+    """Tensors as the host arrays that the library takes. (A step has hundreds of gradients: what is
+    asked of each is asked by map, without a Python frame per tensor.)"""
+
+    def __init__(self, tensors):
+        self.list = ts = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+        if not ts:
+            raise ValueError("no gradients")
+        if not all(map(torch.Tensor.is_contiguous, ts)):
+            raise ValueError("tensors must be contiguous")
+        devices = set(map(torch.Tensor.get_device, ts))
+        if min(devices) < 0:
+            raise ValueError("tensors must live on the GPU")
+        if len(devices) > 1:
+            raise ValueError("tensors must share a device")
+        self.device = ts[0].device
+        try:
+            self.dtypes = array("i", map(_DTYPES.__getitem__, map(_dtype_of, ts)))
+        except KeyError as e:
+            raise TypeError(f"expected float32 or bfloat16, got {e.args[0]}") from None
+        self.sizes = array("q", map(torch.Tensor.numel, ts))
+        self.addresses = array("Q", map(torch.Tensor.data_ptr, ts))
 
 
 def _host(a: array) -> int:
@@ -813,40 +828,34 @@ def _host(a: array) -> int:
 def grad_norm(grads) -> torch.Tensor:
     """The 2-norm over all gradients (a tensor, or tensors of float32 or bfloat16): a float32 scalar
     on their device."""
-    grads, sizes, dtypes = _grads(grads)
-    dev = grads[0].device
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = _workspace(_lib.dflash2_grad_norm_workspace_bytes(), dev)
-    addresses = _addresses(grads)
-    with _on(dev):
-        rc = _lib.dflash2_grad_norm(_host(addresses), _host(sizes), _host(dtypes), len(grads),
-                                    _ptr(norm), _ptr(ws), ws.numel(), _stream(dev))
+    g = _Tensors(grads)
+    norm = torch.empty((), dtype=torch.float32, device=g.device)
+    ws = _workspace(_lib.dflash2_grad_norm_workspace_bytes(), g.device)
+    with _on(g.device):
+        rc = _lib.dflash2_grad_norm(_host(g.addresses), _host(g.sizes), _host(g.dtypes),
+                                    len(g.list), _ptr(norm), _ptr(ws), ws.numel(),
+                                    _stream(g.device))
     _check(rc, "dflash2_grad_norm")
     return norm
 
 
 def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
-    """Scales the gradients by min(1, max_norm / norm), in place or into `out` (a tensor for each,
-    of its shape and type): -> their norm, as grad_norm() gives it. A norm that is not finite scales
-    nothing."""
-    grads, sizes, dtypes = _grads(grads)
-    dev = grads[0].device
-    if out is None:
-        outs = grads
-    else:
-        outs = [out] if isinstance(out, torch.Tensor) else list(out)
-        if len(outs) != len(grads) or any(o.shape != g.shape or o.dtype != g.dtype
-                                          for o, g in zip(outs, grads)):
-            raise ValueError("out must have the gradients' shapes and dtypes")
-        _contig(*outs)
-        _same_device(dev, *outs)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = _workspace(_lib.dflash2_grad_norm_workspace_bytes(), dev)
-    addresses = _addresses(grads)
-    out_addresses = addresses if outs is grads else _addresses(outs)
-    with _on(dev):
-        rc = _lib.dflash2_clip_grads(_host(addresses), _host(sizes), _host(dtypes), len(grads),
-                                     _host(out_addresses), float(max_norm), _ptr(norm), _ptr(ws),
-                                     ws.numel(), _stream(dev))
+    """Scales the gradients by min(1, max_norm / norm), in place or into `out` (a tensor for each, of
+    its type and number of elements): -> their norm, as grad_norm() gives it. A norm that is not
+    finite scales nothing."""
+    g = _Tensors(grads)
+    o = g
+    if out is not None:
+        o = _Tensors(out)
+        if o.sizes != g.sizes or o.dtypes != g.dtypes:
+            raise ValueError("out must have the gradients' sizes and dtypes")
+        if o.device != g.device:
+            raise ValueError("tensors must share a device")
+    norm = torch.empty((), dtype=torch.float32, device=g.device)
+    ws = _workspace(_lib.dflash2_grad_norm_workspace_bytes(), g.device)
+    with _on(g.device):
+        rc = _lib.dflash2_clip_grads(_host(g.addresses), _host(g.sizes), _host(g.dtypes),
+                                     len(g.list), _host(o.addresses), float(max_norm), _ptr(norm),
+                                     _ptr(ws), ws.numel(), _stream(g.device))
     _check(rc, "dflash2_clip_grads")
     return norm
