@@ -230,12 +230,28 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t rs, int off, f32x4
         __builtin_amdgcn_raw_buffer_store_b128(packed4<T>(x), rs, off, 0, 0);
 }
 
-// vmcnt(VM) lgkmcnt(0), then the barrier; nothing moves across.
-template <int VM> __device__ __forceinline__ void gemm_barrier() {
+// The barrier with what it stands for: nothing moves across, for the compiler's passes over memory
+// (which take the barrier itself for an instruction that has none) and for its scheduler.
+__device__ __forceinline__ void bare_barrier() {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// vmcnt(VM) lgkmcnt(LGKM). 63 and 15: no wait.
+template <int VM, int LGKM> __device__ __forceinline__ void wait_for() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70 | (LGKM << 8));
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+template <int VM> __device__ __forceinline__ void gemm_barrier() {
+    wait_for<VM, 0>();
+    bare_barrier();
 }
 
 // `x` as a value of its own: what an epilogue computes from it is computed there, not kept in registers
@@ -531,11 +547,6 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
                             gemm_mfma(fa[i][h], f[j][h], acc[4 * ah + i][2 * bh + j]);
             __builtin_amdgcn_s_setprio(0);
         };
-        auto follow = [&]() {
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-        };
 #pragma unroll
         for (int buf = 0; buf < 2; ++buf) {
             load_b(0, buf);
@@ -547,10 +558,9 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
         gemm_barrier<14>();  // the first of the 8 halves has landed
         read_b(0, 0, fb0);
         gemm_barrier<12>();  // the second
-        if (wave >= kGemmWaves / 2) follow();  // from here on this group runs one barrier behind
+        if (wave >= kGemmWaves / 2) bare_barrier();  // from here on this group runs one barrier behind
         bool stored = false;  // an epilogue's stores are younger than what is waited for
         auto landed = [&](bool may_be_young) {
-            __builtin_amdgcn_sched_barrier(0);
             if (kStores > 0 && may_be_young && stored)
                 gemm_barrier<12 + kStores>();
             else
@@ -561,23 +571,23 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
             load_b(0, buf);
             landed(true);
             multiply(0, 0, b0);
-            follow();
+            bare_barrier();
             read_b(buf, 1, fb1);
             load_a(0, buf);
             landed(true);
             multiply(0, 1, fb1);
-            follow();
+            bare_barrier();
             read_a(buf, 1);
             load_b(1, buf);
             landed(buf == 0);
             multiply(1, 1, fb1);
-            follow();
+            bare_barrier();
             read_b(buf ^ 1, 0, bn);
             load_a(1, buf);
             advance();
             landed(buf == 0);
             multiply(1, 0, b0);
-            follow();
+            bare_barrier();
         };
         for (int i = 0;; ++i) {
             const int K = work(i).K;
@@ -594,8 +604,8 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
             done(i);
             stored = true;
         }
-        if (wave < kGemmWaves / 2) follow();  // (the other group's last barrier)
-        __builtin_amdgcn_s_waitcnt(0x0070);   // no load is in flight when the workgroup ends
+        if (wave < kGemmWaves / 2) bare_barrier();  // (the other group's last barrier)
+        wait_for<0, 0>();  // no load is in flight when the workgroup ends
     }
 
     // The tile as bf16 rows of output: row n of it at `out` + n ld, its columns m from byte `first` on,

@@ -105,6 +105,7 @@ struct GatherJob {
     int32_t *place;       // [R] where row r went, -1: left out
     int32_t *count;
     float2 *scale;        // kStats: [kept rows] (max, g tau / sum)
+    int32_t *from;        // kStats: [kept rows] the row that a kept one was
 };
 
 constexpr int kGatherRows = 4;     // rows per workgroup, one a wave
@@ -157,6 +158,7 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
         if (lane == 0) {
             const float *st = job.stats + (int64_t)r * (K + 2);
             job.scale[before] = float2{st[0], job.grad_loss[r] * job.e.tau / st[1]};
+            job.from[before] = r;
         }
         return;
     } else {
@@ -808,9 +810,9 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 // goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows).
 struct WeightFewJob {
     const uint16_t *rows;  // [count, H]
-    const char *G;         // [64 STEPS][ldg]
+    const char *G;         // [grows][ldg], grows <= 64 STEPS
     const int32_t *count;
-    int H, v0, v1, low;
+    int H, v0, v1, low, grows;
     int64_t ldg;
     int slabs, ranges;     // of 512 columns of H; of the vocabulary, a multiple of 8
     uint16_t *grad;        // [V, H]
@@ -844,7 +846,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
             side.issue(base + buf * kBuffer + s * Side::kBytes,
-                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? 64 : 0, wave);
+                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? job.grows - 64 * s : 0, wave);
     };
     issue(u0, 0);
     bf16x8 fa[2 * STEPS][4];
@@ -909,8 +911,16 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
             }
         }
     }
-    __builtin_amdgcn_s_waitcnt(0x0070);  // no load is in flight when the workgroup ends
+    wait_for<0, 0>();  // no load is in flight when the workgroup ends
 }
+
+}  // namespace
+}  // namespace dflash2
+
+#include "lmhead_rows.h"
+
+namespace dflash2 {
+namespace {
 
 // ---- plans and launches ------------------------------------------------------------------------
 
@@ -919,6 +929,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 struct Plan {
     int bn, nr;              // kept rows of a tile, tiles
     bool few;                // tiles of at most 128 rows: rings (f32: always)
+    int kc;                  // at most 32 bf16 rows, H <= 4096: columns of H a wave (lmhead_rows.h); or 0
     int low;                 // few bf16 rows: G in two parts, this many rows apart; or 0
     int grows;               // rows of G
     // forward
@@ -926,8 +937,15 @@ struct Plan {
     // backward
     int piece, pieces;       // columns (a multiple of 256), number
     int splits;              // of a piece, for grad_hidden: at most, all of them in the first one
-    size_t rows, place, count, flags, parts, scale, G, sums, forward, backward;
+    size_t rows, place, count, flags, parts, scale, from, G, sums, forward, backward;
 
+    // grad_hidden together with the logits
+    bool fused() const { return kc && bn == 16; }
+    // workgroups of a rows kernel
+    int rows_grid(int width) const {
+        const int units = ceil_div(width, kRowsTile);
+        return units < kCus ? units : kCus;
+    }
     // columns of a split in a piece of `width`
     int per(int width) const { return ceil_div(ceil_div(width, splits), 64) * 64; }
 };
@@ -943,6 +961,8 @@ Plan plan(int R, int H, int V, int elem) {
     p.bn = row_tile(R, elem);
     p.nr = ceil_div(R, p.bn);
     p.few = p.bn <= 128;
+    p.kc = elem != 2 || R > 32 || H > 4096 ? 0 : H <= 512 ? 64 : H <= 1024 ? 128 : H <= 2048 ? 256 : 512;
+    if (p.kc && R <= 16) p.bn = 16;
     p.low = elem == 2 && p.bn <= 64 ? p.bn : 0;
     p.grows = elem == 2 && p.few ? p.bn + p.low : R;
     p.nv = ceil_div(V, kTile);
@@ -978,10 +998,37 @@ Plan plan(int R, int H, int V, int elem) {
     p.forward = at;
     at = common;
     p.scale = take((size_t)R * sizeof(float2));
+    p.from = take((size_t)R * 4);
     p.G = take((size_t)p.grows * p.piece * elem);
-    p.sums = take((size_t)p.splits * p.grows * H * 4);
+    p.sums = take((size_t)(p.fused() ? p.rows_grid(width) * 16 : p.splits * p.grows) * H * 4);
     p.backward = at;
     return p;
+}
+
+template <int KC>
+void launch_rows_kc(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t s) {
+    const dim3 grid(p.rows_grid(job.v1 - job.v0)), block(kGemmThreads);
+    if (p.bn == 32) {
+        if (what == RowsDo::kStats)
+            lmloss_rows_kernel<KC, 32, RowsDo::kStats><<<grid, block, 0, s>>>(job);
+        else
+            lmloss_rows_kernel<KC, 32, RowsDo::kGrad><<<grid, block, 0, s>>>(job);
+        return;
+    }
+    switch (what) {
+    case RowsDo::kStats: lmloss_rows_kernel<KC, 16, RowsDo::kStats><<<grid, block, 0, s>>>(job); break;
+    case RowsDo::kGrad: lmloss_rows_kernel<KC, 16, RowsDo::kGrad><<<grid, block, 0, s>>>(job); break;
+    default: lmloss_rows_kernel<KC, 16, RowsDo::kHidden><<<grid, block, 0, s>>>(job); break;
+    }
+}
+
+void launch_rows(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t s) {
+    switch (p.kc) {
+    case 64: launch_rows_kc<64>(p, what, job, s); break;
+    case 128: launch_rows_kc<128>(p, what, job, s); break;
+    case 256: launch_rows_kc<256>(p, what, job, s); break;
+    default: launch_rows_kc<512>(p, what, job, s); break;
+    }
 }
 
 template <typename T, bool GRAD>
@@ -1027,7 +1074,7 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
         lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
     } else if (p.few) {
         WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.H, job.v0,
-                          job.v1, p.low, job.ldg, ceil_div(job.H, 512), 0,
+                          job.v1, p.low, p.grows, job.ldg, ceil_div(job.H, 512), 0,
                           static_cast<uint16_t *>(job.grad)};
         w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
         const int grid = w.slabs * w.ranges;
@@ -1064,6 +1111,21 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
         lmloss_gather_kernel<T, Rows::kTargets><<<grid, 256, 0, s>>>(gj);
     }
     const float c = kLog2e / e.tau;
+    if (p.kc) {
+        RowsJob rj = {};
+        rj.rows = reinterpret_cast<const uint16_t *>(gj.rows);
+        rj.W = reinterpret_cast<const uint16_t *>(gj.W);
+        rj.count = gj.count;
+        rj.H = H;
+        rj.V = V;
+        rj.v1 = V;
+        rj.c = c;
+        rj.parts = reinterpret_cast<float2 *>(ws + p.parts);
+        launch_rows(p, RowsDo::kStats, rj, s);
+        FinishJob fj = {rj.parts, p.rows_grid(V), gj.place, gj.count, p.bn, e, R, V, c, loss, stats};
+        lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
+        return hipGetLastError();
+    }
     LogitsJob lj = {};
     lj.rows = gj.rows;
     lj.W = gj.W;
@@ -1099,6 +1161,7 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
     gj.place = reinterpret_cast<int32_t *>(ws + p.place);
     gj.count = reinterpret_cast<int32_t *>(ws + p.count);
     gj.scale = reinterpret_cast<float2 *>(ws + p.scale);
+    gj.from = reinterpret_cast<int32_t *>(ws + p.from);
     lmloss_gather_kernel<T, Rows::kStats><<<ceil_div(R, kGatherRows), 256, 0, s>>>(gj);
     const float c = kLog2e / e.tau;
     const int nh = ceil_div(H, kTile);
@@ -1119,10 +1182,35 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
         lj.ldg = p.piece;
         lj.scale = gj.scale;
         lj.low = p.low;
-        launch_logits<T, true>(p, lj, s);
-        EntriesJob ej = {e, stats, grad_loss, gj.place, R, V, v0, v1, c, lj.G, p.piece, p.low};
-        lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
-        if (grad_hidden) {
+        const bool fused = p.fused() && grad_hidden;
+        if (p.kc) {
+            RowsJob rj = {};
+            rj.rows = reinterpret_cast<const uint16_t *>(gj.rows);
+            rj.W = static_cast<const uint16_t *>(W);
+            rj.count = gj.count;
+            rj.H = H;
+            rj.V = V;
+            rj.v0 = v0;
+            rj.v1 = v1;
+            rj.c = c;
+            rj.scale = gj.scale;
+            rj.G = fused && !grad_W ? nullptr : static_cast<uint16_t *>(lj.G);
+            rj.ldg = p.piece;
+            rj.low = p.low;
+            rj.from = gj.from;
+            rj.e = e;
+            rj.grad_loss = grad_loss;
+            rj.sums = reinterpret_cast<float *>(ws + p.sums);
+            rj.first = i == 0;
+            launch_rows(p, fused ? RowsDo::kHidden : RowsDo::kGrad, rj, s);
+        } else {
+            launch_logits<T, true>(p, lj, s);
+        }
+        if (!fused) {
+            EntriesJob ej = {e, stats, grad_loss, gj.place, R, V, v0, v1, c, lj.G, p.piece, p.low};
+            lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
+        }
+        if (grad_hidden && !fused) {
             const int per = p.per(v1 - v0);
             HiddenJob hj = {lj.W, ws + p.G, gj.count, p.grows, H, v0, v1, p.piece, nh, p.nr,
                             ceil_div(v1 - v0, per), per, i == 0,
@@ -1137,8 +1225,9 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
     }
     if (grad_hidden)
         lmloss_hidden_out_kernel<T><<<dim3(R, ceil_div(H, 256)), 256, 0, s>>>(
-            reinterpret_cast<float *>(ws + p.sums), p.splits, p.grows, p.low, gj.place, H,
-            static_cast<T *>(grad_hidden));
+            reinterpret_cast<float *>(ws + p.sums),
+            p.fused() ? p.rows_grid(p.piece < V ? p.piece : V) : p.splits, p.fused() ? 16 : p.grows,
+            p.fused() ? 0 : p.low, gj.place, H, static_cast<T *>(grad_hidden));
     return hipGetLastError();
 }
 

@@ -1,0 +1,271 @@
+// The LM head's losses for at most 32 kept rows (bf16, H <= 4096): one read of W a pass, at the rate of
+// its stream. Included by lmhead_loss.hip.
+//
+// Design:
+//   * A wave owns KC columns of H (an eighth, rounded up to 64 .. 512) for the whole pass: the kept rows'
+//     values there are matrix fragments in its registers. A workgroup takes a contiguous range of the
+//     vocabulary, 8 rows of W a tile: the waves together read whole rows (8 KB at H = 4096). Tiles of 256
+//     rows x 256 bytes, which the ring of stages reads, touch every row of the range over and over and
+//     ran at 5.0 - 5.4 TB/s; rows read whole, at 6.0.
+//   * A wave's part of a tile goes straight from memory into LDS that only it reads, two tiles deep, so
+//     the stream needs no barrier: it waits for its own loads.
+//   * The waves' partial logits (8 x 16 or 8 x 32) are added through LDS in a fixed order, one barrier a
+//     tile, by groups of threads that own an element (row, v) each and keep its running maximum and sum,
+//     or form G there.
+//   * With at most 16 rows the backward pass multiplies G, in two bf16 parts, with the tile of W while it
+//     is still in LDS (v_mfma_f32_16x16x16_bf16: 8 rows, two parts): 16 x KC sums a wave in registers.
+//     W is read once for the logits and grad_hidden (G and its product in passes of their own: 450 us for
+//     16 x 4096 x 151936).
+#pragma once
+
+#include "dflash2.h"
+
+namespace dflash2 {
+namespace {
+
+constexpr int kRowsTile = 8;
+
+enum class RowsDo { kStats, kGrad, kHidden };
+
+struct RowsJob {
+    const uint16_t *rows;  // [count, H]
+    const uint16_t *W;     // [V, H]
+    const int32_t *count;
+    int H, V, v0, v1;      // the piece
+    float c;               // log2(e) / tau
+    float2 *parts;         // kStats: per 16 rows, [workgroups][16] (max, sum)
+    const float2 *scale;   // kGrad, kHidden: [count] (max, g tau / sum)
+    uint16_t *G;           // [2 low][ldg], null: not kept
+    int64_t ldg;
+    int low;
+    // kHidden
+    const int32_t *from;   // [count] the kept rows' places among all
+    Entries e;
+    const float *grad_loss;
+    float *sums;           // [workgroups][16][H]
+    bool first;
+};
+
+template <int KC, int BN, RowsDo DO>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) {
+    static_assert(DO != RowsDo::kHidden || BN == 16, "the sums are a wave's registers");
+    constexpr int NI = BN / 16, kSlices = KC / 32, kRowBytes = KC * 2;
+    constexpr int kLoads = kRowsTile * kRowBytes / 1024;     // a wave's, per tile
+    constexpr int kPartRow = BN * kRowsTile + 8;             // floats of a wave's partial tile
+    constexpr int kOwners = kGemmThreads / (BN * kRowsTile); // threads per element
+    constexpr int kStores = DO == RowsDo::kStats ? 0 : 2;    // per tile, younger than what it waits for
+    constexpr int kList = DFLASH2_MAX_K;
+    __shared__ __align__(1024) char stage[kGemmWaves][2][kRowsTile * kRowBytes];
+    __shared__ __align__(16) float part[2][kGemmWaves][kPartRow];
+    __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 1];       // [row][hi of 8 v, lo of 8 v]
+    __shared__ int2 list[DO == RowsDo::kHidden ? 16 * kList : 1];      // [row] (v, mass g tau)
+    __shared__ int listed[DO == RowsDo::kHidden ? 16 : 1];
+
+    const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int R = *job.count, H = job.H, h0 = wave * KC;
+    if (R == 0) return;
+    const int units = (job.v1 - job.v0 + kRowsTile - 1) / kRowsTile;
+    const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
+    const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+    const int64_t ld = (int64_t)H * 2;
+
+    // Loads: lane `at` of a tile's KC / 8 chunks a row takes chunk p ^ (row & 7) for place p.
+    int voff[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int at = i * kWave + lane, row = at / (KC / 8), c = (at % (KC / 8)) ^ (row & 7);
+        voff[i] = h0 + 8 * c < H ? row * (int)ld + 16 * c : kGemmOutside;
+    }
+    auto issue = [&](int u) {
+        const int v = job.v0 + u * kRowsTile, n = u < u1 ? min(kRowsTile, job.v1 - v) : 0;
+        const int bytes = n > 0 && h0 < H ? (n - 1) * (int)ld + (H - h0) * 2 : 0;
+        const uint64_t a = reinterpret_cast<uint64_t>(job.W + (int64_t)v * H + h0);
+        u32x4 rs;
+        rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
+        rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
+        rs.z = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
+        rs.w = kGemmWord3;
+        const uint32_t to = lds_address(stage[wave][(u - u0) & 1]);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                             to + i * 1024),
+                         "v"(voff[i]), "s"(rs)
+                         : "memory");
+    };
+    issue(u0);
+    issue(u0 + 1);
+
+    // The kept rows as fragments: lane (j, g) of slice s holds row 16 ni + j at h0 + 32 s + 8 g .. + 7.
+    bf16x8 hid[NI][kSlices];
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+            const int r = 16 * ni + j, h = h0 + 32 * s + 8 * g;
+            u32x4 x = {0u, 0u, 0u, 0u};
+            if (r < R && h < H) x = *reinterpret_cast<const u32x4 *>(job.rows + (int64_t)r * H + h);
+            hid[ni][s] = __builtin_bit_cast(bf16x8, x);
+        }
+    // This thread's element of a tile: kept row er, vocabulary row ev; `owner` of kOwners threads.
+    constexpr int kMine = kWave / kOwners;  // elements of a wave
+    const int el = wave * kMine + lane % kMine, owner = lane / kMine, er = el / kRowsTile;
+    const int ev = el % kRowsTile;
+    float top = -INFINITY, sum = 0.f;
+    float2 sc = {0.f, 0.f};
+    if constexpr (DO != RowsDo::kStats) sc = job.scale[min(er, R - 1)];
+    if constexpr (DO == RowsDo::kHidden) {
+        // the rows' entries in this range, with their masses times g tau
+        for (int p = wave; p < 16; p += kGemmWaves) {
+            int n = 0;
+            if (p < R) {
+                const int r = job.from[p], K = job.e.K;
+                const int id = lane < K ? job.e.ids[(int64_t)r * K + lane] : -1;
+                const bool any = id_ok(id, job.V);
+                float mass = 1.f;
+                if (job.e.teacher) {
+                    const float t = any ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
+                    float high = wave_max(t);
+                    if (__ballot(any && t != t) != 0ull) high = NAN;
+                    const float w = any ? __builtin_amdgcn_exp2f((t - high) * job.c) : 0.f;
+                    mass = w / wave_sum(w);
+                }
+                const bool in = any && id >= job.v0 + u0 * kRowsTile && id < job.v0 + u1 * kRowsTile;
+                const uint64_t m = __ballot(in);
+                n = __popcll(m);
+                if (in)
+                    list[p * kList + __popcll(m & ((1ull << lane) - 1))] =
+                        int2{id, __float_as_int(mass * job.grad_loss[r] * job.e.tau)};
+            }
+            if (lane == 0) listed[p] = n;
+        }
+        __syncthreads();
+    }
+    const int nlist = DO == RowsDo::kHidden ? listed[min(er, 15)] : 0;
+
+    // Fragment addresses within a tile. Logits: row j & 7 (rows 8 .. 15 of the instruction repeat them),
+    // chunk 4 s + g. grad_hidden: the 4 rows 4 (g & 1) .. of 16 columns, transposed.
+    int xa[2], ta[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xa[i] = (j & 7) * kRowBytes + (((4 * i + g) ^ (j & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 4 * (g & 1) + (j >> 2), c = 2 * i + ((j & 3) >> 1);
+        ta[i] = row * kRowBytes + ((c ^ row) << 4) + 8 * (j & 1);
+    }
+    constexpr int kSums = DO == RowsDo::kHidden ? KC / 16 : 1;
+    f32x4 acc[kSums];
+#pragma unroll
+    for (int t = 0; t < kSums; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+        job.G, (short)0, job.G ? (int)(2 * job.low * job.ldg) * 2 : 0, kGemmWord3);
+
+    wait_for<0, 15>();  // the first two tiles, and what was read above
+    for (int u = u0; u < u1; ++u) {
+        const int buf = (u - u0) & 1;
+        const char *tile = stage[wave][buf];
+        // this tile's loads: all but the next one's, and the stores behind those
+        wait_for<kLoads + kStores, 15>();
+        f32x4 x[NI];
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) x[ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+            const bf16x8 w = *reinterpret_cast<const bf16x8 *>(tile + xa[s & 1] + (s >> 1) * 128);
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni) x[ni] = gemm_mfma(w, hid[ni][s], x[ni]);
+        }
+        // lane (j, g < 2) holds v = 4 g .. 4 g + 3 of row 16 ni + j
+        if (g < 2) {
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni)
+                *reinterpret_cast<f32x4 *>(&part[buf][wave][(16 * ni + j) * kRowsTile + 4 * g]) = x[ni];
+        }
+        if constexpr (DO != RowsDo::kHidden) {
+            wait_for<63, 0>();  // the tile is read
+            issue(u + 2);
+        }
+        wait_for<63, 0>();
+        bare_barrier();
+        // (the other buffer's partial tiles are written before the next barrier, this one's after it)
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGemmWaves / kOwners; ++w)
+            y += part[buf][owner * (kGemmWaves / kOwners) + w][el];
+#pragma unroll
+        for (int d = kMine; d < kWave; d *= 2) y += __shfl_xor(y, d, kWave);
+        const int v = job.v0 + u * kRowsTile + ev;
+        if constexpr (DO == RowsDo::kStats) {
+            if (v < job.v1) {
+                const float high = fmaxf(top, y), ref = high == -INFINITY ? 0.f : high;
+                sum = sum * __builtin_amdgcn_exp2f((top - ref) * job.c) +
+                      __builtin_amdgcn_exp2f((y - ref) * job.c);
+                top = high;
+            }
+        } else {
+            float z = sc.y * __builtin_amdgcn_exp2f((y - sc.x) * job.c);
+            if constexpr (DO == RowsDo::kHidden) {
+                for (int i = 0; i < nlist; ++i) {
+                    const int2 e = list[er * kList + i];
+                    if (e.x == v) z -= __int_as_float(e.y);
+                }
+            }
+            if (er >= R || v >= job.v1) z = 0.f;
+            const __bf16 hi = (__bf16)z, lo = (__bf16)(z - (float)hi);
+            const uint16_t hb = __builtin_bit_cast(uint16_t, hi), lb = __builtin_bit_cast(uint16_t, lo);
+            // (every wave makes both, whatever they write: the waits count them)
+            const int off = owner == 0 ? (int)(er * job.ldg + u * kRowsTile + ev) * 2 : kGemmOutside;
+            __builtin_amdgcn_raw_buffer_store_b16(hb, out, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16(
+                lb, out, owner == 0 ? off + (int)(job.low * job.ldg) * 2 : off, 0, 0);
+            if constexpr (DO == RowsDo::kHidden) {
+                if (owner == 0) {
+                    gt[er * 16 + ev] = hb;
+                    gt[er * 16 + 8 + ev] = lb;
+                }
+                wait_for<63, 0>();
+                bare_barrier();
+                // lane (j, g): row j, k = 4 g ..: hi of v 0 .. 7, then lo
+                const s16x4 ga = *reinterpret_cast<const s16x4 *>(&gt[j * 16 + 4 * g]);
+#pragma unroll
+                for (int t = 0; t < kSums; ++t) {
+                    const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_s16x4 *)(tile + ta[t & 3] + (t >> 2) * 128));
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(ga, w, acc[t], 0, 0, 0);
+                }
+                // the tile is read; (gt is written again behind the next tile's first barrier)
+                wait_for<63, 0>();
+                issue(u + 2);
+            }
+        }
+    }
+    wait_for<0, 0>();  // no load is in flight when the workgroup ends
+
+    if constexpr (DO == RowsDo::kStats) {
+#pragma unroll
+        for (int d = 1; d < kRowsTile; d *= 2) {
+            const float om = __shfl_xor(top, d, kWave), os = __shfl_xor(sum, d, kWave);
+            join(top, sum, om, os, job.c);
+        }
+        if (ev == 0 && owner == 0 && er < R)
+            job.parts[((int64_t)(er >> 4) * gridDim.x + blockIdx.x) * 16 + (er & 15)] = float2{top, sum};
+    }
+    if constexpr (DO == RowsDo::kHidden) {
+#pragma unroll
+        for (int t = 0; t < kSums; ++t) {
+            const int h = h0 + 16 * t + j;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * g + i;
+                if (r < R && h < H) {
+                    float *at = job.sums + ((int64_t)blockIdx.x * 16 + r) * H + h;
+                    *at = job.first ? acc[t][i] : *at + acc[t][i];
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+}  // namespace dflash2
