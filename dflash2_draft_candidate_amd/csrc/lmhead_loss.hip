@@ -692,29 +692,27 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
 }
 
 // grad_hidden from the splits' sums, added in a fixed order (and from the two parts of G, `low` rows
-// apart); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per quarter of the
-// splits.
-template <typename T>
-__global__ __launch_bounds__(256) void lmloss_hidden_out_kernel(const float *sums, int splits, int rows,
-                                                                int low, const int32_t *place, int H,
-                                                                T *grad) {
-    __shared__ f32x4 part[3][kWave];
+// apart); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per WAVES-th split.
+template <typename T, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void lmloss_hidden_out_kernel(
+    const float *sums, int splits, int rows, int low, const int32_t *place, int H, T *grad) {
+    __shared__ f32x4 part[WAVES][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int r = blockIdx.x, p = place[r], h = (blockIdx.y * kWave + lane) * 4;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (p >= 0 && h < H) {
-#pragma unroll 4
-        for (int s = wave; s < splits; s += 4) {
+#pragma unroll 8
+        for (int s = wave; s < splits; s += WAVES) {
             const float *at = sums + ((int64_t)s * rows + p) * H + h;
             x += *reinterpret_cast<const f32x4 *>(at);
             if (low) x += *reinterpret_cast<const f32x4 *>(at + (int64_t)low * H);
         }
     }
-    if (wave > 0) part[wave - 1][lane] = x;
+    if (wave > 0) part[wave][lane] = x;
     __syncthreads();
     if (wave > 0 || h >= H) return;
 #pragma unroll
-    for (int w = 0; w < 3; ++w) x += part[w][lane];
+    for (int w = 1; w < WAVES; ++w) x += part[w][lane];
     const auto y = packed4<T>(x);
     *reinterpret_cast<decltype(packed4<T>(x)) *>(grad + (int64_t)r * H + h) = y;
 }
@@ -1223,11 +1221,17 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             launch_weight<T>(p, wj, s);
         }
     }
-    if (grad_hidden)
-        lmloss_hidden_out_kernel<T><<<dim3(R, ceil_div(H, 256)), 256, 0, s>>>(
-            reinterpret_cast<float *>(ws + p.sums),
-            p.fused() ? p.rows_grid(p.piece < V ? p.piece : V) : p.splits, p.fused() ? 16 : p.grows,
-            p.fused() ? 0 : p.low, gj.place, H, static_cast<T *>(grad_hidden));
+    if (grad_hidden) {
+        const dim3 grid(R, ceil_div(H, 256));
+        float *sums = reinterpret_cast<float *>(ws + p.sums);
+        if (p.fused())
+            lmloss_hidden_out_kernel<T, 16><<<grid, 16 * kWave, 0, s>>>(
+                sums, p.rows_grid(p.piece < V ? p.piece : V), 16, 0, gj.place, H,
+                static_cast<T *>(grad_hidden));
+        else
+            lmloss_hidden_out_kernel<T, 4><<<grid, 4 * kWave, 0, s>>>(
+                sums, p.splits, p.grows, p.low, gj.place, H, static_cast<T *>(grad_hidden));
+    }
     return hipGetLastError();
 }
 

@@ -53,9 +53,12 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     constexpr int kLoads = kRowsTile * kRowBytes / 1024;     // a wave's, per tile
     constexpr int kPartRow = BN * kRowsTile + 8;             // floats of a wave's partial tile
     constexpr int kOwners = kGemmThreads / (BN * kRowsTile); // threads per element
-    constexpr int kStores = DO == RowsDo::kStats ? 0 : 2;    // per tile, younger than what it waits for
+    // per tile, younger than what it waits for: its stores, and two loads that run further ahead
+    constexpr bool kAhead = DO != RowsDo::kHidden;
+    constexpr int kYounger = (DO == RowsDo::kStats ? 0 : 2) + (kAhead ? 2 : 0);
     constexpr int kList = DFLASH2_MAX_K;
     __shared__ __align__(1024) char stage[kGemmWaves][2][kRowsTile * kRowBytes];
+    __shared__ __align__(16) uint32_t dump[kGemmWaves][kWave];
     __shared__ __align__(16) float part[2][kGemmWaves][kPartRow];
     __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 1];       // [row][hi of 8 v, lo of 8 v]
     __shared__ int2 list[DO == RowsDo::kHidden ? 16 * kList : 1];      // [row] (v, mass g tau)
@@ -94,8 +97,28 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
                          "v"(voff[i]), "s"(rs)
                          : "memory");
     };
+    // (Not for kHidden, which the products bound: 276 us without, 298 with.) One load that touches every 128-byte line of this wave's part of a tile: the tile comes to the L2
+    // while the two in LDS are still in use. (What it brings lands in `dump`.)
+    constexpr int kLines = kRowBytes / 128;  // per row
+    const int touch = lane < kRowsTile * kLines && h0 + (lane % kLines) * 64 < H
+                          ? (lane / kLines) * (int)ld + (lane % kLines) * 128 : kGemmOutside;
+    auto ahead = [&](int u) {
+        const int v = job.v0 + u * kRowsTile, n = u < u1 ? min(kRowsTile, job.v1 - v) : 0;
+        const int bytes = n > 0 && h0 < H ? (n - 1) * (int)ld + (H - h0) * 2 : 0;
+        const uint64_t a = reinterpret_cast<uint64_t>(job.W + (int64_t)v * H + h0);
+        u32x4 rs;
+        rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
+        rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
+        rs.z = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
+        rs.w = kGemmWord3;
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
+                         lds_address(dump[wave])),
+                     "v"(touch), "s"(rs)
+                     : "memory");
+    };
     issue(u0);
     issue(u0 + 1);
+    if constexpr (kAhead) ahead(u0 + 2);
 
     // The kept rows as fragments: lane (j, g) of slice s holds row 16 ni + j at h0 + 32 s + 8 g .. + 7.
     bf16x8 hid[NI][kSlices];
@@ -166,25 +189,36 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
         const int buf = (u - u0) & 1;
         const char *tile = stage[wave][buf];
         // this tile's loads: all but the next one's, and the stores behind those
-        wait_for<kLoads + kStores, 15>();
-        f32x4 x[NI];
+        wait_for<kLoads + kYounger, 15>();
+        // (two chains of sums; reads in batches, which the compiler would make and wait for one by one)
+        constexpr int kBatch = kSlices < 4 || DO == RowsDo::kHidden ? (kSlices < 4 ? kSlices : 4) : kSlices < 8 ? kSlices : 8;
+        f32x4 x[NI][2];
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) x[ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int ni = 0; ni < NI; ++ni) x[ni][0] = x[ni][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < kSlices; ++s) {
-            const bf16x8 w = *reinterpret_cast<const bf16x8 *>(tile + xa[s & 1] + (s >> 1) * 128);
+        for (int b = 0; b < kSlices; b += kBatch) {
+            bf16x8 w[kBatch];
 #pragma unroll
-            for (int ni = 0; ni < NI; ++ni) x[ni] = gemm_mfma(w, hid[ni][s], x[ni]);
+            for (int s = 0; s < kBatch; ++s)
+                w[s] = *reinterpret_cast<const bf16x8 *>(tile + xa[s & 1] + ((b + s) >> 1) * 128);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni)
+                    x[ni][s & 1] = gemm_mfma(w[s], hid[ni][b + s], x[ni][s & 1]);
         }
         // lane (j, g < 2) holds v = 4 g .. 4 g + 3 of row 16 ni + j
         if (g < 2) {
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
-                *reinterpret_cast<f32x4 *>(&part[buf][wave][(16 * ni + j) * kRowsTile + 4 * g]) = x[ni];
+                *reinterpret_cast<f32x4 *>(&part[buf][wave][(16 * ni + j) * kRowsTile + 4 * g]) =
+                    x[ni][0] + x[ni][1];
         }
         if constexpr (DO != RowsDo::kHidden) {
             wait_for<63, 0>();  // the tile is read
             issue(u + 2);
+            ahead(u + 3);
         }
         wait_for<63, 0>();
         bare_barrier();
@@ -193,8 +227,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
 #pragma unroll
         for (int w = 0; w < kGemmWaves / kOwners; ++w)
             y += part[buf][owner * (kGemmWaves / kOwners) + w][el];
-#pragma unroll
-        for (int d = kMine; d < kWave; d *= 2) y += __shfl_xor(y, d, kWave);
+        if constexpr (kOwners == 4) y += __uint_as_float(xor_lane<16>(__float_as_uint(y), lane));
+        y += __uint_as_float(xor_lane<32>(__float_as_uint(y), lane));
         const int v = job.v0 + u * kRowsTile + ev;
         if constexpr (DO == RowsDo::kStats) {
             if (v < job.v1) {
@@ -228,11 +262,25 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
                 bare_barrier();
                 // lane (j, g): row j, k = 4 g ..: hi of v 0 .. 7, then lo
                 const s16x4 ga = *reinterpret_cast<const s16x4 *>(&gt[j * 16 + 4 * g]);
+                constexpr int kGroup = 4;
+                s16x4 w[2][kGroup];
+                auto read = [&](int t0, s16x4(&f)[kGroup]) {
 #pragma unroll
-                for (int t = 0; t < kSums; ++t) {
-                    const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (lds_s16x4 *)(tile + ta[t & 3] + (t >> 2) * 128));
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(ga, w, acc[t], 0, 0, 0);
+                    for (int t = t0; t < t0 + kGroup; ++t)
+                        f[t - t0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_s16x4 *)(tile + ta[t & 3] + (t >> 2) * 128));
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                read(0, w[0]);
+#pragma unroll
+                for (int t0 = 0; t0 < kSums; t0 += kGroup) {
+                    const int b = t0 / kGroup & 1;
+                    if (t0 + kGroup < kSums) read(t0 + kGroup, w[b ^ 1]);
+#pragma unroll
+                    for (int t = t0; t < t0 + kGroup; ++t)
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(ga, w[b][t - t0], acc[t], 0,
+                                                                          0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 // the tile is read; (gt is written again behind the next tile's first barrier)
                 wait_for<63, 0>();
