@@ -33,7 +33,7 @@ namespace dflash2 {
 namespace {
 
 constexpr int kTile = 256;                       // rows of W (or columns of hidden) per tile
-constexpr int64_t kPieceBytes = 128ll << 20;     // of G
+constexpr int64_t kPieceBytes = 256ll << 20;     // of G
 constexpr int kPieceMost = 1 << 20;              // columns of a piece (32-bit offsets in it)
 constexpr int kPlaceGroup = 8;                   // rows of tiles that share columns of tiles
 constexpr int kCus = 256;
@@ -60,22 +60,34 @@ struct Entries {
 
 __device__ __forceinline__ bool id_ok(int id, int V) { return id >= 0 && id < V; }
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, kWave);
-    return x;
+// Over the wave's lanes, in every lane, in the VALU.
+template <typename F>
+__device__ __forceinline__ float wave_fold(float x, int lane, F f) {
+    x = f(x, __uint_as_float(xor_lane<1>(__float_as_uint(x), lane)));
+    x = f(x, __uint_as_float(xor_lane<2>(__float_as_uint(x), lane)));
+    x = f(x, __uint_as_float(xor_lane<4>(__float_as_uint(x), lane)));
+    x = f(x, __uint_as_float(xor_lane<8>(__float_as_uint(x), lane)));
+    x = f(x, __uint_as_float(xor_lane<16>(__float_as_uint(x), lane)));
+    return f(x, __uint_as_float(xor_lane<32>(__float_as_uint(x), lane)));
 }
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, kWave);
-    return x;
+__device__ __forceinline__ float wave_sum(float x, int lane) {
+    return wave_fold(x, lane, [](float a, float b) { return a + b; });
 }
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, kWave));
-    return x;
+__device__ __forceinline__ float wave_max(float x, int lane) {
+    return wave_fold(x, lane, [](float a, float b) { return fmaxf(a, b); });
+}
+
+template <int S>
+__device__ __forceinline__ double add_lane(double x, int lane) {
+    return x + __longlong_as_double((long long)xor_lane64<S>((uint64_t)__double_as_longlong(x), lane));
+}
+
+__device__ __forceinline__ double wave_sum(double x, int lane) {
+    x = add_lane<2>(add_lane<1>(x, lane), lane);
+    x = add_lane<8>(add_lane<4>(x, lane), lane);
+    return add_lane<32>(add_lane<16>(x, lane), lane);
 }
 
 // ---- rows with an entry ------------------------------------------------------------------------
@@ -91,7 +103,7 @@ __global__ __launch_bounds__(256) void lmloss_flags_kernel(Entries e, int R, int
     if (j == 0) flags[r] = has ? 1 : 0;
 }
 
-enum class Rows { kTargets, kFlags, kStats };
+enum class Rows { kTargets, kEntries, kFlags, kStats };
 
 struct GatherJob {
     const char *hidden;   // [R, H]
@@ -110,18 +122,28 @@ struct GatherJob {
 
 constexpr int kGatherRows = 4;     // rows per workgroup, one a wave
 constexpr int kGatherEntries = 8;  // entries per wave
+constexpr int kInlineEntries = 4096;  // up to so many the gather looks at them itself (a launch less)
 
 template <Rows M>
 __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
     if constexpr (M == Rows::kTargets) return id_ok(job.e.ids[r], job.V);
+    if constexpr (M == Rows::kEntries) {
+        const int32_t *ids = job.e.ids + (int64_t)r * job.e.K;
+        const float *t = job.e.teacher + (int64_t)r * job.e.K;
+        int has = 0;  // (no entry's loads wait for another's)
+#pragma unroll 8
+        for (int j = 0; j < job.e.K; ++j)
+            has |= (int)id_ok(ids[j], job.V) & (int)!(t[j] == -INFINITY);
+        return has != 0;
+    }
     if constexpr (M == Rows::kFlags) return job.flags[r] != 0;
     if constexpr (M == Rows::kStats) return !(job.stats[(int64_t)r * (job.e.K + 2) + 1] < 0.f);
 }
 
 // Workgroup (x, y): rows 4 x .. 4 x + 3; y = 0 copies them to their places, and (forward) each y
-// takes the dot products of 8 of the entries. A row's place is the number of kept rows before it,
+// takes the dot products of ENTRIES of the entries. A row's place is the number of kept rows before it,
 // which every workgroup of y = 0 counts for itself.
-template <typename T, Rows M>
+template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
     constexpr bool kForward = M != Rows::kStats;
     constexpr int kPer = 16 / (int)sizeof(T);
@@ -163,11 +185,12 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
         return;
     } else {
         char *dst = job.rows + before * row_bytes;
-        const int j0 = blockIdx.y * kGatherEntries, n = min(kGatherEntries, K - j0);
-        const char *w[kGatherEntries];
-        float sum[kGatherEntries];
+        // (past the last entry, and for ids that are none: row 0, whose product nothing reads)
+        const int j0 = blockIdx.y * ENTRIES, n = min(ENTRIES, K - j0);
+        const char *w[ENTRIES];
+        float sum[ENTRIES];
 #pragma unroll
-        for (int j = 0; j < kGatherEntries; ++j) {
+        for (int j = 0; j < ENTRIES; ++j) {
             const int id = j < n ? job.e.ids[(int64_t)r * K + j0 + j] : 0;
             w[j] = job.W + (id_ok(id, job.V) ? id : 0) * row_bytes;
             sum[j] = 0.f;
@@ -179,8 +202,7 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
             float x[kPer];
             Elem<T>::unpack(h, x);
 #pragma unroll
-            for (int j = 0; j < kGatherEntries; ++j) {
-                if (j >= n) break;
+            for (int j = 0; j < ENTRIES; ++j) {
                 float y[kPer];
                 Elem<T>::unpack(*reinterpret_cast<const u32x4 *>(w[j] + b), y);
 #pragma unroll
@@ -188,10 +210,9 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
             }
         }
 #pragma unroll
-        for (int j = 0; j < kGatherEntries; ++j) {
-            if (j >= n) break;
-            const float s = wave_sum(sum[j]);
-            if (lane == 0) job.stats[(int64_t)r * (K + 2) + 2 + j0 + j] = s;
+        for (int j = 0; j < ENTRIES; ++j) {
+            const float s = wave_sum(sum[j], lane);
+            if (lane == 0 && j < n) job.stats[(int64_t)r * (K + 2) + 2 + j0 + j] = s;
         }
     }
 }
@@ -203,6 +224,18 @@ __device__ __forceinline__ void join(float &m, float &s, float om, float os, flo
     const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.f : top;
     s = s * __builtin_amdgcn_exp2f((m - ref) * c) + os * __builtin_amdgcn_exp2f((om - ref) * c);
     m = top;
+}
+
+// With lane ^ S's pair, in the lower lane's order on both sides (a fused sum of products is not
+// symmetric): every lane ends with the same pair.
+template <int S>
+__device__ __forceinline__ void join_lane(float &m, float &s, int lane, float c) {
+    const float om = __uint_as_float(xor_lane<S>(__float_as_uint(m), lane));
+    const float os = __uint_as_float(xor_lane<S>(__float_as_uint(s), lane));
+    float lm = lane & S ? om : m, ls = lane & S ? os : s;
+    join(lm, ls, lane & S ? m : om, lane & S ? s : os, c);
+    m = lm;
+    s = ls;
 }
 
 struct LogitsJob {
@@ -254,8 +287,8 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
             for (int mi = 0; mi < Tile::MI; ++mi)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, tile.acc[mi][ni][i]);
-            top = fmaxf(top, __shfl_xor(top, 16, kWave));
-            top = fmaxf(top, __shfl_xor(top, 32, kWave));
+            top = fmaxf(top, __uint_as_float(xor_lane<16>(__float_as_uint(top), lane)));
+            top = fmaxf(top, __uint_as_float(xor_lane<32>(__float_as_uint(top), lane)));
             const float ref = top == -INFINITY ? 0.f : top;
             float sum = 0.f;
 #pragma unroll
@@ -263,8 +296,8 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     sum += __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - ref) * c);
-            sum += __shfl_xor(sum, 16, kWave);
-            sum += __shfl_xor(sum, 32, kWave);
+            sum += __uint_as_float(xor_lane<16>(__float_as_uint(sum), lane));
+            sum += __uint_as_float(xor_lane<32>(__float_as_uint(sum), lane));
             if (g == 0 && r < R)
                 job.parts[((r >> 4) * job.nparts + part + wave / Tile::WN) * 16 + (r & 15)] =
                     float2{top, sum};
@@ -421,11 +454,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
 #pragma unroll
         for (int ni = 0; ni < Ring::NI; ++ni) {
             float m = top[ni], s = sum[ni];
-#pragma unroll
-            for (int d = 16; d < kWave; d *= 2) {
-                const float om = __shfl_xor(m, d, kWave), os = __shfl_xor(s, d, kWave);
-                join(m, s, om, os, c);
-            }
+            join_lane<16>(m, s, lane, c);
+            join_lane<32>(m, s, lane, c);
             if (g == 0) pair[wave * BN + 16 * ni + j] = float2{m, s};
         }
         __syncthreads();
@@ -495,13 +525,12 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
         float m = -INFINITY, s = 0.f;
         m = pair[lane][k].x;
         s = pair[lane][k].y;
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const float om = __shfl_down(m, d, kWave), os = __shfl_down(s, d, kWave);
-            if (lane % (2 * d) == 0) join(m, s, om, os, job.c);
-        }
-        m = __shfl(m, 0, kWave);
-        s = __shfl(s, 0, kWave);
+        join_lane<1>(m, s, lane, job.c);
+        join_lane<2>(m, s, lane, job.c);
+        join_lane<4>(m, s, lane, job.c);
+        join_lane<8>(m, s, lane, job.c);
+        join_lane<16>(m, s, lane, job.c);
+        join_lane<32>(m, s, lane, job.c);
         const int id = lane < K ? job.e.ids[(int64_t)r * K + lane] : -1;
         const bool ok = id_ok(id, job.V);
         double term = 0.0;
@@ -509,11 +538,11 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
         double p = ok ? 1.0 : 0.0, ln_p = 0.0;
         if (job.e.teacher) {
             const float t = ok ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
-            float top = wave_max(t);
+            float top = wave_max(t, lane);
             if (__ballot(ok && t != t) != 0ull) top = NAN;
             ln_p = ((double)t - top) / tau;
             const double w = ok ? exp(ln_p) : 0.0;
-            const double all = wave_sum(w);
+            const double all = wave_sum(w, lane);
             p = w / all;
             ln_p -= log(all);
         }
@@ -523,7 +552,7 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
             ln_q = ln_q > 0.0 ? 0.0 : ln_q;
             term = p * (ln_p - ln_q);
         }
-        term = wave_sum(term);
+        term = wave_sum(term, lane);
         if (lane == 0) {
             job.loss[r] = (float)(tau * tau * term);
             st[0] = m;
@@ -559,10 +588,10 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     float mass = 1.f;
     if (job.e.teacher) {
         const float t = ok ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
-        float top = wave_max(t);
+        float top = wave_max(t, lane);
         if (__ballot(ok && t != t) != 0ull) top = NAN;
         const float w = ok ? __builtin_amdgcn_exp2f((t - top) * job.c) : 0.f;
-        mass = w / wave_sum(w);
+        mass = w / wave_sum(w, lane);
     }
     float total = 0.f;
     bool earlier = false;
@@ -591,6 +620,35 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
 
 // ---- the gradients' products -----------------------------------------------------------------------
 
+// Streams of tiles: splits of the vocabulary for grad_hidden, given how many tiles of kept rows there are
+// (known on the device only) and the width of the first piece. A tile's end, with its sums read and
+// written, takes as long as 17 K steps. Rounds of tiles over the CUs count as whole ones, but the card's
+// power is the limit from about three quarters of the CUs on (192 tiles as 192, or in 4 splits as 768,
+// take the same time; 160 tiles in 3 splits take 0.9 of the time of 160).
+constexpr int kSplitTiles = 768;  // splits x tiles, at most, where there is more than one split
+
+__host__ __device__ __forceinline__ int split_columns(int width, int splits) {
+    return ((width + splits - 1) / splits + 63) / 64 * 64;
+}
+
+__host__ __device__ __forceinline__ int stream_splits(int tiles, int width) {
+    int best = 1, least = 0x7FFFFFFF;
+    for (int rounds = 1; rounds <= kSplitTiles / kCus; ++rounds) {  // as many as fit the rounds
+        const int fit = rounds * kCus / tiles, most = width / 256;
+        const int s = fit < most ? fit : most;
+        if (s < 1) continue;
+        const int steps = split_columns(width, s) / 64 + 17;
+        const int all = (int)((int64_t)s * tiles * steps * 333 >> 16);  // 1.3 / 256: at 0.77 of the CUs
+        const int cost = rounds * steps > all ? rounds * steps : all;
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    const int per = split_columns(width, best);
+    return (width + per - 1) / per;
+}
+
 struct HiddenJob {
     const char *W;       // [V, H]
     const char *G;       // [count][ldg]
@@ -601,16 +659,17 @@ struct HiddenJob {
     bool first;          // the first piece: nothing to add to
     float *sums;         // [splits][R][H]
     int low;             // as the logits' job's
+    int width;           // streams: of the first piece (nr, splits, per and R come from the kept rows)
 };
 
 template <bool few, typename Tile>
-__device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, int split, int h0,
-                                            int r0, int R, int wave, int lane) {
+__device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, int split, int rows,
+                                            int h0, int r0, int R, int wave, int lane) {
     lane = anew(lane);
     const int g = lane >> 4, j = lane & 15;
     const int ld = job.H * 4;
     const __amdgpu_buffer_rsrc_t out = out_rows(
-        job.sums + ((int64_t)split * job.R + r0) * job.H, ld, min(R - r0, Tile::kCols), ld);
+        job.sums + ((int64_t)split * rows + r0) * job.H, ld, min(R - r0, Tile::kCols), ld);
 #pragma unroll
     for (int ni = 0; ni < Tile::NI; ++ni) {
         const int n = Tile::wave_n(wave) + 16 * ni + j, row = n * ld;
@@ -651,7 +710,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJ
             return {operand_ks<T>(job.W, ldw, h0, job.v0 + k0), operand_kc<T>(job.G, ldg, r0, R, k0),
                     k1 - k0};
         },
-        [&](int) { hidden_done<sizeof(T) == 2>(job, ring, split, h0, r0, R, wave, lane); }, lds, wave, lane);
+        [&](int) { hidden_done<sizeof(T) == 2>(job, ring, split, job.R, h0, r0, R, wave, lane); }, lds, wave, lane);
 }
 
 // Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16.
@@ -661,13 +720,17 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
     __shared__ __align__(1024) char lds[Stream::kLdsBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count, nr = (R + kTile - 1) / kTile, tiles = job.nh * job.splits * nr;
+    const int R = *job.count, nr = (R + kTile - 1) / kTile;
+    if (R == 0) return;
+    const int width = job.v1 - job.v0;
+    const int per = split_columns(width, stream_splits(job.nh * nr, job.width));
+    const int splits = (width + per - 1) / per, tiles = job.nh * splits * nr;
     const int64_t ldw = (int64_t)job.H * sizeof(T), ldg = job.ldg * (int64_t)sizeof(T);
     auto place = [&](int i, int &split, int &h0, int &r0) {
         const int id = blockIdx.x + i * gridDim.x;
         if (id >= tiles) return false;
         int tm, tn;
-        gemm_place(id, job.nh * job.splits, nr, kPlaceGroup, tm, tn);
+        gemm_place(id, job.nh * splits, nr, kPlaceGroup, tm, tn);
         split = tm / job.nh;
         h0 = tm % job.nh * kTile;
         r0 = tn * kTile;
@@ -679,14 +742,14 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
         [&](int i) -> GemmWork {
             int split, h0, r0;
             if (!place(i, split, h0, r0)) return {{job.W, ldw, 0}, {job.G, ldg, 0}, 0};
-            const int k0 = split * job.per, k1 = min(k0 + job.per, job.v1 - job.v0);
+            const int k0 = split * per, k1 = min(k0 + per, width);
             return {operand_ks<T>(job.W, ldw, h0, job.v0 + k0), operand_kc<T>(job.G, ldg, r0, R, k0),
                     k1 - k0};
         },
         [&](int i) {
             int split = 0, h0 = 0, r0 = 0;
             place(i, split, h0, r0);
-            hidden_done<false>(job, stream, split, h0, r0, R, wave, lane);
+            hidden_done<false>(job, stream, split, nr * kTile, h0, r0, R, wave, lane);
         },
         lds, wave, lane);
 }
@@ -695,8 +758,14 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
 // apart); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per WAVES-th split.
 template <typename T, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave) void lmloss_hidden_out_kernel(
-    const float *sums, int splits, int rows, int low, const int32_t *place, int H, T *grad) {
+    const float *sums, int splits, int rows, int low, const int32_t *count, int width,
+    const int32_t *place, int H, T *grad) {
     __shared__ f32x4 part[WAVES][kWave];
+    if (width > 0) {  // a stream's: as it has split them
+        const int nr = (*count + kTile - 1) / kTile, nh = (H + kTile - 1) / kTile;
+        splits = nr > 0 ? stream_splits(nh * nr, width) : 0;
+        rows = nr * kTile;
+    }
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int r = blockIdx.x, p = place[r], h = (blockIdx.y * kWave + lane) * 4;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -871,29 +940,30 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
         // the loads of this buffer are older than the last 64 rows' stores
         if (u == u0) gemm_barrier<0>(); else gemm_barrier<kStores>();
         issue(u + 1, buf ^ 1);
-        f32x4 acc[4][4];
-#pragma unroll
-        for (int mi = 0; mi < 4; ++mi)
-#pragma unroll
-            for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < 2 * STEPS; ++s)
-#pragma unroll
-            for (int ni = 0; ni < 4; ++ni) {
-                const bf16x8 fb = rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, ni, s % 2);
-#pragma unroll
-                for (int mi = 0; mi < 4; ++mi) acc[mi][ni] = gemm_mfma(fa[s][mi], fb, acc[mi][ni]);
-            }
         const int v = job.v0 + u * 64;
         const __amdgpu_buffer_rsrc_t out =
             out_rows(reinterpret_cast<char *>(job.grad) + (int64_t)v * ld, ld, min(job.v1 - v, 64), ld);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+            f32x4 acc[4][2];
+#pragma unroll
+            for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < 2; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 2 * STEPS; ++s)
+#pragma unroll
+                for (int ni = 0; ni < 2; ++ni) {
+                    const bf16x8 fb =
+                        rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, 2 * half + ni, s % 2);
+#pragma unroll
+                    for (int mi = 0; mi < 4; ++mi) acc[mi][ni] = gemm_mfma(fa[s][mi], fb, acc[mi][ni]);
+                }
 #pragma unroll
             for (int ni = 0; ni < 2; ++ni)
 #pragma unroll
                 for (int mi = 0; mi < 4; ++mi) {
-                    const auto x = packed4<T>(acc[mi][2 * half + ni]);
+                    const auto x = packed4<T>(acc[mi][ni]);
                     const int row = 16 * ni + j;
                     *reinterpret_cast<decltype(packed4<T>(f32x4{})) *>(
                         scratch + row * 128 + (((2 * mi + (g >> 1)) ^ (row & 7)) << 4) + (g & 1) * 8) = x;
@@ -945,7 +1015,7 @@ struct Plan {
         return units < kCus ? units : kCus;
     }
     // columns of a split in a piece of `width`
-    int per(int width) const { return ceil_div(ceil_div(width, splits), 64) * 64; }
+    int per(int width) const { return split_columns(width, splits); }
 };
 
 // Rows of a tile for R rows. bf16: 256 from 129 rows on (two tiles of 128 read W twice); f32: 128 at
@@ -972,7 +1042,7 @@ Plan plan(int R, int H, int V, int elem) {
     if (most > round) most = most / round * round;
     p.piece = (int)(most < p.nv ? most : p.nv) * kTile;
     p.pieces = ceil_div(V, p.piece);
-    // grad_hidden: a workgroup for every CU, splits of 256 columns at least
+    // grad_hidden (rings): a workgroup for every CU, splits of 256 columns at least
     const int tiles = ceil_div(H, kTile) * p.nr, width = p.piece < V ? p.piece : V;
     const int longest = width / 256;
     p.splits = kCus / tiles < longest ? kCus / tiles : longest;
@@ -998,7 +1068,12 @@ Plan plan(int R, int H, int V, int elem) {
     p.scale = take((size_t)R * sizeof(float2));
     p.from = take((size_t)R * 4);
     p.G = take((size_t)p.grows * p.piece * elem);
-    p.sums = take((size_t)(p.fused() ? p.rows_grid(width) * 16 : p.splits * p.grows) * H * 4);
+    const size_t split_rows = (size_t)kSplitTiles / ceil_div(H, kTile) * kTile;
+    const size_t stream_rows = (size_t)p.nr * kTile > split_rows ? (size_t)p.nr * kTile : split_rows;
+    const size_t sum_rows = p.fused() ? (size_t)p.rows_grid(width) * 16
+                            : p.few   ? (size_t)p.splits * p.grows
+                                      : stream_rows;
+    p.sums = take(sum_rows * H * 4);
     p.backward = at;
     return p;
 }
@@ -1053,7 +1128,7 @@ void launch_hidden(const Plan &p, const HiddenJob &job, hipStream_t s) {
     const dim3 grid(tiles), block(kGemmThreads);
     if constexpr (sizeof(T) == 2) {
         if (!p.few) {
-            lmloss_hidden_stream_kernel<T><<<tiles < kCus ? tiles : kCus, block, 0, s>>>(job);
+            lmloss_hidden_stream_kernel<T><<<kCus, block, 0, s>>>(job);
             return;
         }
     }
@@ -1070,13 +1145,15 @@ template <typename T>
 void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
         lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
-    } else if (p.few) {
+    } else if (p.grows <= kTile) {
         WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.H, job.v0,
                           job.v1, p.low, p.grows, job.ldg, ceil_div(job.H, 512), 0,
                           static_cast<uint16_t *>(job.grad)};
         w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
         const int grid = w.slabs * w.ranges;
-        if (p.grows > 64)
+        if (w.grows > 128)
+            lmloss_weight_few_kernel<4><<<grid, kGemmThreads, 0, s>>>(w);
+        else if (w.grows > 64)
             lmloss_weight_few_kernel<2><<<grid, kGemmThreads, 0, s>>>(w);
         else
             lmloss_weight_few_kernel<1><<<grid, kGemmThreads, 0, s>>>(w);
@@ -1101,12 +1178,14 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     gj.rows = ws + p.rows;
     gj.place = reinterpret_cast<int32_t *>(ws + p.place);
     gj.count = reinterpret_cast<int32_t *>(ws + p.count);
-    const dim3 grid(ceil_div(R, kGatherRows), ceil_div(e.K, kGatherEntries));
-    if (e.teacher) {
+    const dim3 grid(ceil_div(R, kGatherRows), e.teacher ? ceil_div(e.K, kGatherEntries) : 1);
+    if (e.teacher && (int64_t)R * e.K <= kInlineEntries) {
+        lmloss_gather_kernel<T, Rows::kEntries, kGatherEntries><<<grid, 256, 0, s>>>(gj);
+    } else if (e.teacher) {
         lmloss_flags_kernel<<<ceil_div(R, 4), 256, 0, s>>>(e, R, V, const_cast<int32_t *>(gj.flags));
-        lmloss_gather_kernel<T, Rows::kFlags><<<grid, 256, 0, s>>>(gj);
+        lmloss_gather_kernel<T, Rows::kFlags, kGatherEntries><<<grid, 256, 0, s>>>(gj);
     } else {
-        lmloss_gather_kernel<T, Rows::kTargets><<<grid, 256, 0, s>>>(gj);
+        lmloss_gather_kernel<T, Rows::kTargets, 1><<<grid, 256, 0, s>>>(gj);
     }
     const float c = kLog2e / e.tau;
     if (p.kc) {
@@ -1160,7 +1239,7 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
     gj.count = reinterpret_cast<int32_t *>(ws + p.count);
     gj.scale = reinterpret_cast<float2 *>(ws + p.scale);
     gj.from = reinterpret_cast<int32_t *>(ws + p.from);
-    lmloss_gather_kernel<T, Rows::kStats><<<ceil_div(R, kGatherRows), 256, 0, s>>>(gj);
+    lmloss_gather_kernel<T, Rows::kStats, 1><<<ceil_div(R, kGatherRows), 256, 0, s>>>(gj);
     const float c = kLog2e / e.tau;
     const int nh = ceil_div(H, kTile);
     for (int i = 0; i < p.pieces; ++i) {
@@ -1212,7 +1291,8 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             const int per = p.per(v1 - v0);
             HiddenJob hj = {lj.W, ws + p.G, gj.count, p.grows, H, v0, v1, p.piece, nh, p.nr,
                             ceil_div(v1 - v0, per), per, i == 0,
-                            reinterpret_cast<float *>(ws + p.sums), p.low};
+                            reinterpret_cast<float *>(ws + p.sums), p.low,
+                            p.piece < V ? p.piece : V};
             launch_hidden<T>(p, hj, s);
         }
         if (grad_W) {
@@ -1226,11 +1306,12 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
         float *sums = reinterpret_cast<float *>(ws + p.sums);
         if (p.fused())
             lmloss_hidden_out_kernel<T, 16><<<grid, 16 * kWave, 0, s>>>(
-                sums, p.rows_grid(p.piece < V ? p.piece : V), 16, 0, gj.place, H,
+                sums, p.rows_grid(p.piece < V ? p.piece : V), 16, 0, gj.count, 0, gj.place, H,
                 static_cast<T *>(grad_hidden));
         else
             lmloss_hidden_out_kernel<T, 4><<<grid, 4 * kWave, 0, s>>>(
-                sums, p.splits, p.grows, p.low, gj.place, H, static_cast<T *>(grad_hidden));
+                sums, p.splits, p.grows, p.low, gj.count, p.few ? 0 : p.piece < V ? p.piece : V,
+                gj.place, H, static_cast<T *>(grad_hidden));
     }
     return hipGetLastError();
 }

@@ -149,10 +149,10 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
                 float mass = 1.f;
                 if (job.e.teacher) {
                     const float t = any ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
-                    float high = wave_max(t);
+                    float high = wave_max(t, lane);
                     if (__ballot(any && t != t) != 0ull) high = NAN;
                     const float w = any ? __builtin_amdgcn_exp2f((t - high) * job.c) : 0.f;
-                    mass = w / wave_sum(w);
+                    mass = w / wave_sum(w, lane);
                 }
                 const bool in = any && id >= job.v0 + u0 * kRowsTile && id < job.v0 + u1 * kRowsTile;
                 const uint64_t m = __ballot(in);
@@ -291,11 +291,9 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     wait_for<0, 0>();  // no load is in flight when the workgroup ends
 
     if constexpr (DO == RowsDo::kStats) {
-#pragma unroll
-        for (int d = 1; d < kRowsTile; d *= 2) {
-            const float om = __shfl_xor(top, d, kWave), os = __shfl_xor(sum, d, kWave);
-            join(top, sum, om, os, job.c);
-        }
+        join_lane<1>(top, sum, lane, job.c);
+        join_lane<2>(top, sum, lane, job.c);
+        join_lane<4>(top, sum, lane, job.c);
         if (ev == 0 && owner == 0 && er < R)
             job.parts[((int64_t)(er >> 4) * gridDim.x + blockIdx.x) * 16 + (er & 15)] = float2{top, sum};
     }
