@@ -64,6 +64,31 @@ __device__ __forceinline__ GemmOperand operand_ks(const void *p, int64_t ld, int
             col0 * (int)sizeof(T)};
 }
 
+// A descriptor of `bytes` bytes from p on, in scalar registers.
+__device__ __forceinline__ u32x4 scalar_buffer(const void *p, int bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    u32x4 rs;
+    rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
+    rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
+    rs.z = __builtin_amdgcn_readfirstlane((uint32_t)(bytes < 0 ? 0 : bytes));
+    rs.w = kGemmWord3;
+    return rs;
+}
+
+// Starts a load of 16 (4) bytes a lane, from `off` bytes into the buffer, into LDS at `to` + 16 (4) lane.
+// (A memory instruction may read a scalar register that a vector instruction wrote 5 states later; the
+// compiler sees to that, but not inside assembly. M0 needs one state.)
+__device__ __forceinline__ void load_lds16(uint32_t to, int off, u32x4 rs) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+                 "v"(off), "s"(rs)
+                 : "memory");
+}
+__device__ __forceinline__ void load_lds4(uint32_t to, int off, u32x4 rs) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
+                 "v"(off), "s"(rs)
+                 : "memory");
+}
+
 // One stage of an operand: B rows (KC) or columns (KS) of a K step. Where G is not 0 they are every
 // other run of G of the tile's: row i of the stage is row (i / G) 2 G + i % G.
 template <typename T, int B, bool KS, int G = 0> struct GemmSide {
@@ -126,20 +151,12 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
             n = ks * ld - valid;
         else
             n = ks == 0 ? 0 : (min(valid, 2 * B) - 1) * ld + (ks * (int)sizeof(T) + 15) / 16 * 16;
-        const uint64_t a = reinterpret_cast<uint64_t>(p);
-        u32x4 rs;
-        rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
-        rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
-        rs.z = __builtin_amdgcn_readfirstlane((uint32_t)(n < 0 ? 0 : n));
-        rs.w = kGemmWord3;
+        const u32x4 rs = scalar_buffer(p, n);
 #pragma unroll
         for (int q = 0; q < kPerWave; ++q) {
             int off = voff[q];
             if constexpr (!KS) off = kbyte < kleft * (int)sizeof(T) ? off : kGemmOutside;
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
-                             to + load_of(wave, q) * 1024),
-                         "v"(off), "s"(rs)
-                         : "memory");
+            load_lds16(to + load_of(wave, q) * 1024, off, rs);
         }
     }
 

@@ -877,9 +877,10 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 // goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows).
 struct WeightFewJob {
     const uint16_t *rows;  // [count, H]
-    const char *G;         // [grows][ldg], grows <= 64 STEPS
+    const char *G;         // [grows][ldg], at most 64 STEPS rows
     const int32_t *count;
-    int H, v0, v1, low, grows;
+    int H, v0, v1, low;
+    int grows;             // rows of G, 0: the kept rows
     int64_t ldg;
     int slabs, ranges;     // of 512 columns of H; of the vocabulary, a multiple of 8
     uint16_t *grad;        // [V, H]
@@ -894,7 +895,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
     __shared__ __align__(1024) char lds[2 * kBuffer + kGemmWaves * 4096];
     const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count;
+    const int R = *job.count, rows = job.grows ? job.grows : R;
     // (the slabs of a range run on one XCD, whose L2 gives them G)
     const int at = blockIdx.x / 8, slab = at % job.slabs;
     const int range = blockIdx.x % 8 + 8 * (at / job.slabs);
@@ -913,7 +914,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
             side.issue(base + buf * kBuffer + s * Side::kBytes,
-                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? job.grows - 64 * s : 0, wave);
+                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? rows - 64 * s : 0, wave);
     };
     issue(u0, 0);
     bf16x8 fa[2 * STEPS][4];
@@ -1147,13 +1148,13 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
         lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
     } else if (p.grows <= kTile) {
         WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.H, job.v0,
-                          job.v1, p.low, p.grows, job.ldg, ceil_div(job.H, 512), 0,
+                          job.v1, p.low, p.few ? p.grows : 0, job.ldg, ceil_div(job.H, 512), 0,
                           static_cast<uint16_t *>(job.grad)};
         w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
         const int grid = w.slabs * w.ranges;
-        if (w.grows > 128)
+        if (p.grows > 128)
             lmloss_weight_few_kernel<4><<<grid, kGemmThreads, 0, s>>>(w);
-        else if (w.grows > 64)
+        else if (p.grows > 64)
             lmloss_weight_few_kernel<2><<<grid, kGemmThreads, 0, s>>>(w);
         else
             lmloss_weight_few_kernel<1><<<grid, kGemmThreads, 0, s>>>(w);

@@ -53,15 +53,15 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     constexpr int kLoads = kRowsTile * kRowBytes / 1024;     // a wave's, per tile
     constexpr int kPartRow = BN * kRowsTile + 8;             // floats of a wave's partial tile
     constexpr int kOwners = kGemmThreads / (BN * kRowsTile); // threads per element
-    // per tile, younger than what it waits for: its stores, and two loads that run further ahead
+    // per tile, younger than what it waits for (at least): its stores, two loads that run further ahead
     constexpr bool kAhead = DO != RowsDo::kHidden;
     constexpr int kYounger = (DO == RowsDo::kStats ? 0 : 2) + (kAhead ? 2 : 0);
     constexpr int kList = DFLASH2_MAX_K;
     __shared__ __align__(1024) char stage[kGemmWaves][2][kRowsTile * kRowBytes];
     __shared__ __align__(16) uint32_t dump[kGemmWaves][kWave];
     __shared__ __align__(16) float part[2][kGemmWaves][kPartRow];
-    __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 1];       // [row][hi of 8 v, lo of 8 v]
-    __shared__ int2 list[DO == RowsDo::kHidden ? 16 * kList : 1];      // [row] (v, mass g tau)
+    __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 1];  // [row][8 hi, 8 lo]
+    __shared__ int2 list[DO == RowsDo::kHidden ? 16 * kList : 1];  // [row] (v, mass g tau)
     __shared__ int listed[DO == RowsDo::kHidden ? 16 : 1];
 
     const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
@@ -80,42 +80,25 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
         const int at = i * kWave + lane, row = at / (KC / 8), c = (at % (KC / 8)) ^ (row & 7);
         voff[i] = h0 + 8 * c < H ? row * (int)ld + 16 * c : kGemmOutside;
     }
-    auto issue = [&](int u) {
+    // this wave's columns of tile u (of nothing behind the last)
+    auto buffer = [&](int u) {
         const int v = job.v0 + u * kRowsTile, n = u < u1 ? min(kRowsTile, job.v1 - v) : 0;
-        const int bytes = n > 0 && h0 < H ? (n - 1) * (int)ld + (H - h0) * 2 : 0;
-        const uint64_t a = reinterpret_cast<uint64_t>(job.W + (int64_t)v * H + h0);
-        u32x4 rs;
-        rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
-        rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
-        rs.z = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
-        rs.w = kGemmWord3;
+        return scalar_buffer(job.W + (int64_t)v * H + h0,
+                             n > 0 && h0 < H ? (n - 1) * (int)ld + (H - h0) * 2 : 0);
+    };
+    auto issue = [&](int u) {
+        const u32x4 rs = buffer(u);
         const uint32_t to = lds_address(stage[wave][(u - u0) & 1]);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
-                             to + i * 1024),
-                         "v"(voff[i]), "s"(rs)
-                         : "memory");
+        for (int i = 0; i < kLoads; ++i) load_lds16(to + i * 1024, voff[i], rs);
     };
-    // (Not for kHidden, which the products bound: 276 us without, 298 with.) One load that touches every 128-byte line of this wave's part of a tile: the tile comes to the L2
-    // while the two in LDS are still in use. (What it brings lands in `dump`.)
+    // One load that touches every 128-byte line of this wave's part of a tile: the tile comes to the L2
+    // while the two in LDS are still in use (16 x 4096 x 151936: 209 us without, 202 with). What it
+    // brings lands in `dump`. Not for kHidden (276 us without, 298 with).
     constexpr int kLines = kRowBytes / 128;  // per row
     const int touch = lane < kRowsTile * kLines && h0 + (lane % kLines) * 64 < H
                           ? (lane / kLines) * (int)ld + (lane % kLines) * 128 : kGemmOutside;
-    auto ahead = [&](int u) {
-        const int v = job.v0 + u * kRowsTile, n = u < u1 ? min(kRowsTile, job.v1 - v) : 0;
-        const int bytes = n > 0 && h0 < H ? (n - 1) * (int)ld + (H - h0) * 2 : 0;
-        const uint64_t a = reinterpret_cast<uint64_t>(job.W + (int64_t)v * H + h0);
-        u32x4 rs;
-        rs.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
-        rs.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
-        rs.z = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
-        rs.w = kGemmWord3;
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
-                         lds_address(dump[wave])),
-                     "v"(touch), "s"(rs)
-                     : "memory");
-    };
+    auto ahead = [&](int u) { load_lds4(lds_address(dump[wave]), touch, buffer(u)); };
     issue(u0);
     issue(u0 + 1);
     if constexpr (kAhead) ahead(u0 + 2);

@@ -181,7 +181,39 @@ def test_pieces(d2, R, H, V, dt):
     check(ref, *run(d2, *x, 1.0), dtype, 1.0)
 
 
-WAYS = [(20, 64, 700), (90, 72, 1030), (400, 136, 515)]
+# each way through the kernels, at its ends: rows read whole (up to 16 and 32 rows, by H), rings of 64 and
+# 128 rows, the weight gradient from held rows (up to 256), streams
+EDGES = [(R, H, V) for R, V in ((15, 2053), (16, 300), (17, 1031), (32, 4099), (33, 700), (64, 1500),
+                                (65, 513), (128, 2049), (129, 1025), (256, 777), (257, 1300))
+         for H in (128, 520, 1000, 2056)] + \
+    [(16, 3000, 5000), (31, 4096, 3001), (9, 4104, 2003), (48, 4096, 3001), (130, 4096, 1700),
+     (600, 2048, 2500), (300, 1544, 40001)]
+
+
+@pytest.mark.parametrize("R,H,V", EDGES)
+def test_edges(d2, R, H, V):
+    log(f"lmhead loss edges R={R} H={H} V={V}")
+    x = inputs(R, H, V, 0 if (R + H) % 2 else 3, torch.bfloat16, R + H)
+    x[2][R // 2] = -1
+    ref = reference(*x, 1.0)
+    check(ref, *run(d2, *x, 1.0), torch.bfloat16, 1.0)
+
+
+@pytest.mark.parametrize("R,H,V,dt", [(3, 8, 2200001, "bf16"), (20, 8, 1100003, "bf16"),
+                                      (40, 8, 1100003, "bf16"), (2, 8, 1100003, "f32")])
+def test_long_vocabulary(d2, R, H, V, dt):
+    """More columns than a piece may have."""
+    log(f"lmhead loss long vocabulary R={R} V={V} {dt}")
+    dtype = torch.float32 if dt == "f32" else torch.bfloat16
+    x = inputs(R, H, V, 4, dtype, 17)
+    x[2][:, 0] = V - 1
+    x[2][:, 1] = (1 << 20) - 1
+    x[2][:, 2] = 1 << 20
+    ref = reference(*x, 1.0)
+    check(ref, *run(d2, *x, 1.0), dtype, 1.0)
+
+
+WAYS = [(14, 1000, 700), (20, 64, 700), (90, 72, 1030), (400, 136, 515)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
