@@ -117,7 +117,6 @@ struct GatherJob {
     int32_t *place;       // [R] where row r went, -1: left out
     int32_t *count;
     float2 *scale;        // kStats: [kept rows] (max, g tau / sum)
-    int32_t *from;        // kStats: [kept rows] the row that a kept one was
 };
 
 constexpr int kGatherRows = 4;     // rows per workgroup, one a wave
@@ -180,7 +179,6 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
         if (lane == 0) {
             const float *st = job.stats + (int64_t)r * (K + 2);
             job.scale[before] = float2{st[0], job.grad_loss[r] * job.e.tau / st[1]};
-            job.from[before] = r;
         }
         return;
     } else {
@@ -533,6 +531,7 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
         join_lane<32>(m, s, lane, job.c);
         const int id = lane < K ? job.e.ids[(int64_t)r * K + lane] : -1;
         const bool ok = id_ok(id, job.V);
+        if (lane < K && !ok) st[2 + lane] = 0.f;
         double term = 0.0;
         const double tau = job.e.tau;
         double p = ok ? 1.0 : 0.0, ln_p = 0.0;
@@ -790,6 +789,7 @@ struct WeightJob {
     const char *rows;    // [count, H]
     const char *G;       // [count][ldg]
     const int32_t *count;
+    const int32_t *from; // null, or where in `rows` each kept row is (lmloss_weight_few_kernel)
     int H, v0, v1;
     int64_t ldg;
     int nh, nv;
@@ -876,9 +876,9 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 // range of the vocabulary, 64 rows at a time: G's columns come through LDS, two buffers, and the output
 // goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows).
 struct WeightFewJob {
-    const uint16_t *rows;  // [count, H]
+    const uint16_t *rows;  // [count, H], or with `from` all rows
     const char *G;         // [grows][ldg], at most 64 STEPS rows
-    const int32_t *count;
+    const int32_t *count, *from;
     int H, v0, v1, low;
     int grows;             // rows of G, 0: the kept rows
     int64_t ldg;
@@ -926,7 +926,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int k = 32 * s + 8 * g + e, r = job.low && k >= job.low ? k - job.low : k;
-                const uint16_t x = r < R && h < job.H ? job.rows[(int64_t)r * job.H + h] : 0;
+                uint16_t x = 0;
+                if (r < R && h < job.H) x = job.rows[(int64_t)(job.from ? job.from[r] : r) * job.H + h];
                 fa[s][mi][e] = __builtin_bit_cast(__bf16, x);
             }
         }
@@ -998,7 +999,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 struct Plan {
     int bn, nr;              // kept rows of a tile, tiles
     bool few;                // tiles of at most 128 rows: rings (f32: always)
-    int kc;                  // at most 32 bf16 rows, H <= 4096: columns of H a wave (lmhead_rows.h); or 0
+    int kc;                  // few bf16 rows, H <= 4096: columns of H a wave (lmhead_rows.h); or 0
     int low;                 // few bf16 rows: G in two parts, this many rows apart; or 0
     int grows;               // rows of G
     // forward
@@ -1030,7 +1031,11 @@ Plan plan(int R, int H, int V, int elem) {
     p.bn = row_tile(R, elem);
     p.nr = ceil_div(R, p.bn);
     p.few = p.bn <= 128;
-    p.kc = elem != 2 || R > 32 || H > 4096 ? 0 : H <= 512 ? 64 : H <= 1024 ? 128 : H <= 2048 ? 256 : 512;
+    // rows read whole: as many as a wave's registers hold of its columns
+    if (elem == 2 && (R <= 32 ? H <= 4096 : R <= 64 && H <= 2048))
+        p.kc = H <= 512 ? 64 : H <= 1024 ? 128 : H <= 2048 ? 256 : 512;
+    else
+        p.kc = 0;
     if (p.kc && R <= 16) p.bn = 16;
     p.low = elem == 2 && p.bn <= 64 ? p.bn : 0;
     p.grows = elem == 2 && p.few ? p.bn + p.low : R;
@@ -1058,6 +1063,7 @@ Plan plan(int R, int H, int V, int elem) {
     p.rows = take((size_t)R * H * elem);
     p.place = take((size_t)R * 4);
     p.count = take(4);
+    p.from = take((size_t)R * 4);
     const size_t common = at;
     p.flags = take((size_t)R * 4);
     // (few_ranges of the kept rows' tiles: 256 bn pairs, or one for each of more rows than that)
@@ -1067,7 +1073,6 @@ Plan plan(int R, int H, int V, int elem) {
     p.forward = at;
     at = common;
     p.scale = take((size_t)R * sizeof(float2));
-    p.from = take((size_t)R * 4);
     p.G = take((size_t)p.grows * p.piece * elem);
     const size_t split_rows = (size_t)kSplitTiles / ceil_div(H, kTile) * kTile;
     const size_t stream_rows = (size_t)p.nr * kTile > split_rows ? (size_t)p.nr * kTile : split_rows;
@@ -1082,6 +1087,15 @@ Plan plan(int R, int H, int V, int elem) {
 template <int KC>
 void launch_rows_kc(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t s) {
     const dim3 grid(p.rows_grid(job.v1 - job.v0)), block(kGemmThreads);
+    if constexpr (KC <= 256) {
+        if (p.bn == 64) {
+            if (what == RowsDo::kStats)
+                lmloss_rows_kernel<KC, 64, RowsDo::kStats><<<grid, block, 0, s>>>(job);
+            else
+                lmloss_rows_kernel<KC, 64, RowsDo::kGrad><<<grid, block, 0, s>>>(job);
+            return;
+        }
+    }
     if (p.bn == 32) {
         if (what == RowsDo::kStats)
             lmloss_rows_kernel<KC, 32, RowsDo::kStats><<<grid, block, 0, s>>>(job);
@@ -1147,8 +1161,8 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
         lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
     } else if (p.grows <= kTile) {
-        WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.H, job.v0,
-                          job.v1, p.low, p.few ? p.grows : 0, job.ldg, ceil_div(job.H, 512), 0,
+        WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.from, job.H,
+                          job.v0, job.v1, p.low, p.few ? p.grows : 0, job.ldg, ceil_div(job.H, 512), 0,
                           static_cast<uint16_t *>(job.grad)};
         w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
         const int grid = w.slabs * w.ranges;
@@ -1164,9 +1178,42 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
     }
 }
 
+RowsJob rows_job(const Plan &p, const void *hidden, const void *W, const Entries &e, int R, int H, int V,
+                 float *stats, char *ws) {
+    RowsJob job = {};
+    job.hidden = static_cast<const uint16_t *>(hidden);
+    job.W = static_cast<const uint16_t *>(W);
+    job.R = R;
+    job.H = H;
+    job.V = V;
+    job.c = kLog2e / e.tau;
+    job.e = e;
+    job.stats = stats;
+    job.place = reinterpret_cast<int32_t *>(ws + p.place);
+    job.from = reinterpret_cast<int32_t *>(ws + p.from);
+    job.count = reinterpret_cast<int32_t *>(ws + p.count);
+    return job;
+}
+
 template <typename T>
 hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, int R, int H, int V,
                    float *loss, float *stats, char *ws, hipStream_t s) {
+    const float c = kLog2e / e.tau;
+    int32_t *place = reinterpret_cast<int32_t *>(ws + p.place);
+    int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
+    float2 *parts = reinterpret_cast<float2 *>(ws + p.parts);
+    const auto finish = [&](int64_t nparts) {
+        FinishJob fj = {parts, nparts, place, count, p.bn, e, R, V, c, loss, stats};
+        lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
+        return hipGetLastError();
+    };
+    if (p.kc) {
+        RowsJob rj = rows_job(p, hidden, W, e, R, H, V, stats, ws);
+        rj.v1 = V;
+        rj.parts = parts;
+        launch_rows(p, RowsDo::kStats, rj, s);
+        return finish(p.rows_grid(V));
+    }
     GatherJob gj = {};
     gj.hidden = static_cast<const char *>(hidden);
     gj.W = static_cast<const char *>(W);
@@ -1177,8 +1224,8 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     gj.H = H;
     gj.V = V;
     gj.rows = ws + p.rows;
-    gj.place = reinterpret_cast<int32_t *>(ws + p.place);
-    gj.count = reinterpret_cast<int32_t *>(ws + p.count);
+    gj.place = place;
+    gj.count = count;
     const dim3 grid(ceil_div(R, kGatherRows), e.teacher ? ceil_div(e.K, kGatherEntries) : 1);
     if (e.teacher && (int64_t)R * e.K <= kInlineEntries) {
         lmloss_gather_kernel<T, Rows::kEntries, kGatherEntries><<<grid, 256, 0, s>>>(gj);
@@ -1187,22 +1234,6 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
         lmloss_gather_kernel<T, Rows::kFlags, kGatherEntries><<<grid, 256, 0, s>>>(gj);
     } else {
         lmloss_gather_kernel<T, Rows::kTargets, 1><<<grid, 256, 0, s>>>(gj);
-    }
-    const float c = kLog2e / e.tau;
-    if (p.kc) {
-        RowsJob rj = {};
-        rj.rows = reinterpret_cast<const uint16_t *>(gj.rows);
-        rj.W = reinterpret_cast<const uint16_t *>(gj.W);
-        rj.count = gj.count;
-        rj.H = H;
-        rj.V = V;
-        rj.v1 = V;
-        rj.c = c;
-        rj.parts = reinterpret_cast<float2 *>(ws + p.parts);
-        launch_rows(p, RowsDo::kStats, rj, s);
-        FinishJob fj = {rj.parts, p.rows_grid(V), gj.place, gj.count, p.bn, e, R, V, c, loss, stats};
-        lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
-        return hipGetLastError();
     }
     LogitsJob lj = {};
     lj.rows = gj.rows;
@@ -1215,90 +1246,85 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     lj.nv = p.nv;
     lj.nr = p.nr;
     lj.c = c;
-    lj.parts = reinterpret_cast<float2 *>(ws + p.parts);
+    lj.parts = parts;
     lj.nparts = p.few ? 0 : p.nv * 2;
     launch_logits<T, false>(p, lj, s);
-    FinishJob fj = {lj.parts, lj.nparts, gj.place, gj.count, p.bn, e, R, V, c, loss, stats};
-    lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
-    return hipGetLastError();
+    return finish(lj.nparts);
 }
 
 template <typename T>
 hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
                     const float *stats, const float *grad_loss, int R, int H, int V,
                     void *grad_hidden, void *grad_W, char *ws, hipStream_t s) {
-    GatherJob gj = {};
-    gj.hidden = static_cast<const char *>(hidden);
-    gj.stats = const_cast<float *>(stats);
-    gj.grad_loss = grad_loss;
-    gj.e = e;
-    gj.R = R;
-    gj.H = H;
-    gj.V = V;
-    gj.rows = ws + p.rows;
-    gj.place = reinterpret_cast<int32_t *>(ws + p.place);
-    gj.count = reinterpret_cast<int32_t *>(ws + p.count);
-    gj.scale = reinterpret_cast<float2 *>(ws + p.scale);
-    gj.from = reinterpret_cast<int32_t *>(ws + p.from);
-    lmloss_gather_kernel<T, Rows::kStats, 1><<<ceil_div(R, kGatherRows), 256, 0, s>>>(gj);
     const float c = kLog2e / e.tau;
+    int32_t *place = reinterpret_cast<int32_t *>(ws + p.place);
+    int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
+    int32_t *from = reinterpret_cast<int32_t *>(ws + p.from);
+    float2 *scale = reinterpret_cast<float2 *>(ws + p.scale);
+    if (!p.kc) {
+        GatherJob gj = {};
+        gj.hidden = static_cast<const char *>(hidden);
+        gj.stats = const_cast<float *>(stats);
+        gj.grad_loss = grad_loss;
+        gj.e = e;
+        gj.R = R;
+        gj.H = H;
+        gj.V = V;
+        gj.rows = ws + p.rows;
+        gj.place = place;
+        gj.count = count;
+        gj.scale = scale;
+        lmloss_gather_kernel<T, Rows::kStats, 1><<<ceil_div(R, kGatherRows), 256, 0, s>>>(gj);
+    }
+    const bool fused = p.fused() && grad_hidden;
     const int nh = ceil_div(H, kTile);
     for (int i = 0; i < p.pieces; ++i) {
         const int v0 = i * p.piece, v1 = v0 + p.piece < V ? v0 + p.piece : V;
-        LogitsJob lj = {};
-        lj.rows = gj.rows;
-        lj.W = static_cast<const char *>(W);
-        lj.count = gj.count;
-        lj.H = H;
-        lj.V = V;
-        lj.v0 = v0;
-        lj.v1 = v1;
-        lj.nv = ceil_div(v1 - v0, kTile);
-        lj.nr = p.nr;
-        lj.c = c;
-        lj.G = ws + p.G;
-        lj.ldg = p.piece;
-        lj.scale = gj.scale;
-        lj.low = p.low;
-        const bool fused = p.fused() && grad_hidden;
+        const char *Wb = static_cast<const char *>(W);
+        const int nv = ceil_div(v1 - v0, kTile);
         if (p.kc) {
-            RowsJob rj = {};
-            rj.rows = reinterpret_cast<const uint16_t *>(gj.rows);
-            rj.W = static_cast<const uint16_t *>(W);
-            rj.count = gj.count;
-            rj.H = H;
-            rj.V = V;
+            RowsJob rj = rows_job(p, hidden, W, e, R, H, V, const_cast<float *>(stats), ws);
             rj.v0 = v0;
             rj.v1 = v1;
-            rj.c = c;
-            rj.scale = gj.scale;
-            rj.G = fused && !grad_W ? nullptr : static_cast<uint16_t *>(lj.G);
+            rj.grad_loss = grad_loss;
+            rj.G = fused && !grad_W ? nullptr : reinterpret_cast<uint16_t *>(ws + p.G);
             rj.ldg = p.piece;
             rj.low = p.low;
-            rj.from = gj.from;
-            rj.e = e;
-            rj.grad_loss = grad_loss;
             rj.sums = reinterpret_cast<float *>(ws + p.sums);
             rj.first = i == 0;
             launch_rows(p, fused ? RowsDo::kHidden : RowsDo::kGrad, rj, s);
         } else {
+            LogitsJob lj = {};
+            lj.rows = ws + p.rows;
+            lj.W = Wb;
+            lj.count = count;
+            lj.H = H;
+            lj.V = V;
+            lj.v0 = v0;
+            lj.v1 = v1;
+            lj.nv = nv;
+            lj.nr = p.nr;
+            lj.c = c;
+            lj.G = ws + p.G;
+            lj.ldg = p.piece;
+            lj.scale = scale;
+            lj.low = p.low;
             launch_logits<T, true>(p, lj, s);
-        }
-        if (!fused) {
-            EntriesJob ej = {e, stats, grad_loss, gj.place, R, V, v0, v1, c, lj.G, p.piece, p.low};
+            EntriesJob ej = {e, stats, grad_loss, place, R, V, v0, v1, c, lj.G, p.piece, p.low};
             lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
         }
         if (grad_hidden && !fused) {
             const int per = p.per(v1 - v0);
-            HiddenJob hj = {lj.W, ws + p.G, gj.count, p.grows, H, v0, v1, p.piece, nh, p.nr,
+            HiddenJob hj = {Wb, ws + p.G, count, p.grows, H, v0, v1, p.piece, nh, p.nr,
                             ceil_div(v1 - v0, per), per, i == 0,
                             reinterpret_cast<float *>(ws + p.sums), p.low,
                             p.piece < V ? p.piece : V};
             launch_hidden<T>(p, hj, s);
         }
         if (grad_W) {
-            WeightJob wj = {gj.rows, ws + p.G, gj.count, H, v0, v1, p.piece, nh,
-                            ceil_div(v1 - v0, sizeof(T) == 4 ? 128 : kTile), grad_W};
+            WeightJob wj = {p.kc ? static_cast<const char *>(hidden) : ws + p.rows, ws + p.G, count,
+                            p.kc ? from : nullptr, H, v0, v1, p.piece, nh,
+                            sizeof(T) == 4 ? ceil_div(v1 - v0, 128) : nv, grad_W};
             launch_weight<T>(p, wj, s);
         }
     }
@@ -1307,12 +1333,12 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
         float *sums = reinterpret_cast<float *>(ws + p.sums);
         if (p.fused())
             lmloss_hidden_out_kernel<T, 16><<<grid, 16 * kWave, 0, s>>>(
-                sums, p.rows_grid(p.piece < V ? p.piece : V), 16, 0, gj.count, 0, gj.place, H,
+                sums, p.rows_grid(p.piece < V ? p.piece : V), 16, 0, count, 0, place, H,
                 static_cast<T *>(grad_hidden));
         else
             lmloss_hidden_out_kernel<T, 4><<<grid, 4 * kWave, 0, s>>>(
-                sums, p.splits, p.grows, p.low, gj.count, p.few ? 0 : p.piece < V ? p.piece : V,
-                gj.place, H, static_cast<T *>(grad_hidden));
+                sums, p.splits, p.grows, p.low, count, p.few ? 0 : p.piece < V ? p.piece : V,
+                place, H, static_cast<T *>(grad_hidden));
     }
     return hipGetLastError();
 }

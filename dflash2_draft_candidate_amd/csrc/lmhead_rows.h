@@ -1,5 +1,5 @@
-// The LM head's losses for at most 32 kept rows (bf16, H <= 4096): one read of W a pass, at the rate of
-// its stream. Included by lmhead_loss.hip.
+// The LM head's losses for at most 32 rows (64 where H <= 2048), bf16, H <= 4096: one read of W a pass, at
+// the rate of its stream, and few launches. Included by lmhead_loss.hip.
 //
 // Design:
 //   * A wave owns KC columns of H (an eighth, rounded up to 64 .. 512) for the whole pass: the kept rows'
@@ -12,6 +12,9 @@
 //   * The waves' partial logits (8 x 16 or 8 x 32) are added through LDS in a fixed order, one barrier a
 //     tile, by groups of threads that own an element (row, v) each and keep its running maximum and sum,
 //     or form G there.
+//   * Every workgroup finds the kept rows and their entries in its range by itself, while its first tiles
+//     are on their way; the first one leaves the rows' places for the kernels that follow. The entries'
+//     logits are taken, and their masses subtracted, where their columns come by.
 //   * With at most 16 rows the backward pass multiplies G, in two bf16 parts, with the tile of W while it
 //     is still in LDS (v_mfma_f32_16x16x16_bf16: 8 rows, two parts): 16 x KC sums a wave in registers.
 //     W is read once for the logits and grad_hidden (G and its product in passes of their own: 450 us for
@@ -28,21 +31,20 @@ constexpr int kRowsTile = 8;
 enum class RowsDo { kStats, kGrad, kHidden };
 
 struct RowsJob {
-    const uint16_t *rows;  // [count, H]
-    const uint16_t *W;     // [V, H]
-    const int32_t *count;
-    int H, V, v0, v1;      // the piece
-    float c;               // log2(e) / tau
-    float2 *parts;         // kStats: per 16 rows, [workgroups][16] (max, sum)
-    const float2 *scale;   // kGrad, kHidden: [count] (max, g tau / sum)
-    uint16_t *G;           // [2 low][ldg], null: not kept
+    const uint16_t *hidden;  // [R, H]
+    const uint16_t *W;       // [V, H]
+    int R, H, V, v0, v1;     // the piece
+    float c;                 // log2(e) / tau
+    Entries e;
+    float *stats;            // [R, K + 2]: kStats: the entries' logits out; else in
+    const float *grad_loss;  // kGrad, kHidden
+    int32_t *place;          // out: [R] a row's place among the kept ones, -1: left out
+    int32_t *from, *count;   // out: [kept rows] the row, their number
+    float2 *parts;           // kStats: per 16 rows, [workgroups][16] (max, sum)
+    uint16_t *G;             // [2 low][ldg], null: not kept
     int64_t ldg;
     int low;
-    // kHidden
-    const int32_t *from;   // [count] the kept rows' places among all
-    Entries e;
-    const float *grad_loss;
-    float *sums;           // [workgroups][16][H]
+    float *sums;             // kHidden: [workgroups][16][H]
     bool first;
 };
 
@@ -58,16 +60,17 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     constexpr int kYounger = (DO == RowsDo::kStats ? 0 : 2) + (kAhead ? 2 : 0);
     constexpr int kList = DFLASH2_MAX_K;
     __shared__ __align__(1024) char stage[kGemmWaves][2][kRowsTile * kRowBytes];
-    __shared__ __align__(16) uint32_t dump[kGemmWaves][kWave];
+    __shared__ __align__(16) uint32_t dump[kAhead ? kGemmWaves : 1][kWave];
     __shared__ __align__(16) float part[2][kGemmWaves][kPartRow];
-    __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 1];  // [row][8 hi, 8 lo]
-    __shared__ int2 list[DO == RowsDo::kHidden ? 16 * kList : 1];  // [row] (v, mass g tau)
-    __shared__ int listed[DO == RowsDo::kHidden ? 16 : 1];
+    __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 8];  // [row][8 hi, 8 lo]
+    // the kept rows' entries in this range: column (from its first on); mass times g tau, or which entry
+    __shared__ uint16_t list_v[BN * kList];
+    __shared__ float list_x[BN * kList];
+    __shared__ int listed[BN], from[BN], keeps[BN];
 
     const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count, H = job.H, h0 = wave * KC;
-    if (R == 0) return;
+    const int H = job.H, h0 = wave * KC, K = job.e.K;
     const int units = (job.v1 - job.v0 + kRowsTile - 1) / kRowsTile;
     const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
     const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
@@ -103,52 +106,100 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     issue(u0 + 1);
     if constexpr (kAhead) ahead(u0 + 2);
 
+    // The kept rows. A wave looks at rows wave, wave + 8, .., a lane at an entry; all loads at once.
+    constexpr int kRounds = BN / kGemmWaves;
+    int ids[kRounds];
+    float teacher[kRounds], sums[kRounds], grads[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int r = min(wave + kGemmWaves * i, job.R - 1);
+        const int64_t at = (int64_t)r * K + min(lane, K - 1);
+        ids[i] = job.e.ids[at];
+        teacher[i] = job.e.teacher ? job.e.teacher[at] : 0.f;
+        if constexpr (DO != RowsDo::kStats) {
+            sums[i] = job.stats[(int64_t)r * (K + 2) + 1];
+            grads[i] = job.grad_loss[r];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int r = wave + kGemmWaves * i;
+        bool has;
+        if constexpr (DO == RowsDo::kStats)
+            has = __ballot(lane < K && id_ok(ids[i], job.V) && !(teacher[i] == -INFINITY)) != 0ull;
+        else
+            has = !(sums[i] < 0.f);
+        if (lane == 0) keeps[r] = has && r < job.R ? 1 : 0;
+    }
+    __syncthreads();
+    const uint64_t mask = __ballot(lane < BN && keeps[min(lane, BN - 1)] != 0);
+    const int R = __popcll(mask), mine = __popcll(mask & ((1ull << lane) - 1));
+    const bool is_kept = (mask >> lane) & 1ull;
+    if (wave == 0) {
+        if (is_kept) from[mine] = lane;
+        if (blockIdx.x == 0) {
+            if (lane < job.R) job.place[lane] = is_kept ? mine : -1;
+            if (is_kept) job.from[mine] = lane;
+            if (lane == 0) *job.count = R;
+        }
+    }
+    __syncthreads();
+    if (R == 0) {  // (the loads in flight end before the workgroup does)
+        wait_for<0, 0>();
+        return;
+    }
+
     // The kept rows as fragments: lane (j, g) of slice s holds row 16 ni + j at h0 + 32 s + 8 g .. + 7.
     bf16x8 hid[NI][kSlices];
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
+    for (int ni = 0; ni < NI; ++ni) {
+        const int p = 16 * ni + j;
+        const uint16_t *row = job.hidden + (int64_t)from[min(p, R - 1)] * H;
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
-            const int r = 16 * ni + j, h = h0 + 32 * s + 8 * g;
+            const int h = h0 + 32 * s + 8 * g;
             u32x4 x = {0u, 0u, 0u, 0u};
-            if (r < R && h < H) x = *reinterpret_cast<const u32x4 *>(job.rows + (int64_t)r * H + h);
+            if (p < R && h < H) x = *reinterpret_cast<const u32x4 *>(row + h);
             hid[ni][s] = __builtin_bit_cast(bf16x8, x);
         }
+    }
     // This thread's element of a tile: kept row er, vocabulary row ev; `owner` of kOwners threads.
     constexpr int kMine = kWave / kOwners;  // elements of a wave
     const int el = wave * kMine + lane % kMine, owner = lane / kMine, er = el / kRowsTile;
-    const int ev = el % kRowsTile;
+    const int ev = el % kRowsTile, r_mine = from[min(er, R - 1)];
     float top = -INFINITY, sum = 0.f;
     float2 sc = {0.f, 0.f};
-    if constexpr (DO != RowsDo::kStats) sc = job.scale[min(er, R - 1)];
-    if constexpr (DO == RowsDo::kHidden) {
-        // the rows' entries in this range, with their masses times g tau
-        for (int p = wave; p < 16; p += kGemmWaves) {
-            int n = 0;
-            if (p < R) {
-                const int r = job.from[p], K = job.e.K;
-                const int id = lane < K ? job.e.ids[(int64_t)r * K + lane] : -1;
-                const bool any = id_ok(id, job.V);
-                float mass = 1.f;
-                if (job.e.teacher) {
-                    const float t = any ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
-                    float high = wave_max(t, lane);
-                    if (__ballot(any && t != t) != 0ull) high = NAN;
-                    const float w = any ? __builtin_amdgcn_exp2f((t - high) * job.c) : 0.f;
-                    mass = w / wave_sum(w, lane);
-                }
-                const bool in = any && id >= job.v0 + u0 * kRowsTile && id < job.v0 + u1 * kRowsTile;
-                const uint64_t m = __ballot(in);
-                n = __popcll(m);
-                if (in)
-                    list[p * kList + __popcll(m & ((1ull << lane) - 1))] =
-                        int2{id, __float_as_int(mass * job.grad_loss[r] * job.e.tau)};
+    float *stats = job.stats + (int64_t)r_mine * (K + 2);
+    if constexpr (DO != RowsDo::kStats)
+        sc = float2{stats[0], job.grad_loss[r_mine] * job.e.tau / stats[1]};
+    const int first = job.v0 + u0 * kRowsTile, end = job.v0 + u1 * kRowsTile;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int r = wave + kGemmWaves * i, p = __popcll(mask & ((1ull << r) - 1));
+        if (!((mask >> r) & 1ull)) continue;
+        const bool any = lane < K && id_ok(ids[i], job.V);
+        float x = __int_as_float(lane);
+        if constexpr (DO != RowsDo::kStats) {
+            x = 1.f;
+            if (job.e.teacher) {
+                const float t = any ? teacher[i] : -INFINITY;
+                float high = wave_max(t, lane);
+                if (__ballot(any && t != t) != 0ull) high = NAN;
+                const float w = any ? __builtin_amdgcn_exp2f((t - high) * job.c) : 0.f;
+                x = w / wave_sum(w, lane);
             }
-            if (lane == 0) listed[p] = n;
+            x *= grads[i] * job.e.tau;
         }
-        __syncthreads();
+        const uint64_t m = __ballot(any && ids[i] >= first && ids[i] < end);
+        if ((m >> lane) & 1ull) {
+            const int at = p * kList + __popcll(m & ((1ull << lane) - 1));
+            list_v[at] = (uint16_t)(ids[i] - first);  // (a range has at most 2^20 / 256 columns, or 8)
+            list_x[at] = x;
+        }
+        if (lane == 0) listed[p] = __popcll(m);
     }
-    const int nlist = DO == RowsDo::kHidden ? listed[min(er, 15)] : 0;
+    __syncthreads();
+    const int nlist = er < R ? listed[er] : 0;
 
     // Fragment addresses within a tile. Logits: row j & 7 (rows 8 .. 15 of the instruction repeat them),
     // chunk 4 s + g. grad_hidden: the 4 rows 4 (g & 1) .. of 16 columns, transposed.
@@ -210,10 +261,13 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
 #pragma unroll
         for (int w = 0; w < kGemmWaves / kOwners; ++w)
             y += part[buf][owner * (kGemmWaves / kOwners) + w][el];
-        if constexpr (kOwners == 4) y += __uint_as_float(xor_lane<16>(__float_as_uint(y), lane));
-        y += __uint_as_float(xor_lane<32>(__float_as_uint(y), lane));
-        const int v = job.v0 + u * kRowsTile + ev;
+        if constexpr (kOwners >= 4) y += __uint_as_float(xor_lane<16>(__float_as_uint(y), lane));
+        if constexpr (kOwners >= 2) y += __uint_as_float(xor_lane<32>(__float_as_uint(y), lane));
+        const int v = job.v0 + u * kRowsTile + ev, in_range = (u - u0) * kRowsTile + ev;
         if constexpr (DO == RowsDo::kStats) {
+            for (int i = 0; i < nlist; ++i)
+                if (list_v[er * kList + i] == in_range && owner == 0)
+                    stats[2 + __float_as_int(list_x[er * kList + i])] = y;
             if (v < job.v1) {
                 const float high = fmaxf(top, y), ref = high == -INFINITY ? 0.f : high;
                 sum = sum * __builtin_amdgcn_exp2f((top - ref) * job.c) +
@@ -222,12 +276,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
             }
         } else {
             float z = sc.y * __builtin_amdgcn_exp2f((y - sc.x) * job.c);
-            if constexpr (DO == RowsDo::kHidden) {
-                for (int i = 0; i < nlist; ++i) {
-                    const int2 e = list[er * kList + i];
-                    if (e.x == v) z -= __int_as_float(e.y);
-                }
-            }
+            for (int i = 0; i < nlist; ++i)
+                if (list_v[er * kList + i] == in_range) z -= list_x[er * kList + i];
             if (er >= R || v >= job.v1) z = 0.f;
             const __bf16 hi = (__bf16)z, lo = (__bf16)(z - (float)hi);
             const uint16_t hb = __builtin_bit_cast(uint16_t, hi), lb = __builtin_bit_cast(uint16_t, lo);
