@@ -131,6 +131,16 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
         }
     }
 
+    // KC: the stage's row i is row rows[i] of the operand, for i < n.
+    __device__ __forceinline__ void take_rows(const int *rows, int n, int ld, int wave, int lane) {
+        static_assert(!KS, "rows that hold k");
+#pragma unroll
+        for (int q = 0; q < kPerWave; ++q) {
+            const int i = tile_row(8 * load_of(wave, q) + (lane >> 3));
+            voff[q] = i < n ? rows[i] * ld + kbyte : kGemmOutside;
+        }
+    }
+
     // KS, bf16: f(k) for the 32-byte pieces of row k
     static __device__ __forceinline__ int swizzle(int k) {
         return ((((k >> 3) & 3) << 2) | (k & 3)) & (kRowChunks / 2 - 1);
@@ -370,13 +380,14 @@ struct GemmWork {
     int K;  // <= 0: no tile
 };
 
-template <typename T, int BM_, int BN, int SUB, bool AS, bool BS> struct GemmRing {
+// RESERVE: bytes of LDS that are not the ring's.
+template <typename T, int BM_, int BN, int SUB, bool AS, bool BS, int RESERVE = 0> struct GemmRing {
     static constexpr int BM = BM_, WM = 8, WN = 1, MI = BM / 128, NI = BN / 16, kCols = BN;
     typedef GemmSide<T, BM, AS> SideA;
     typedef GemmSide<T, BN, BS> SideB;
     static constexpr int kStepK = SideA::kStepK;
     static constexpr int kStep = SideA::kBytes + SideB::kBytes, kStage = SUB * kStep;
-    static constexpr int kStages = 163840 / kStage;
+    static constexpr int kStages = (163840 - RESERVE) / kStage;
     static constexpr int kLdsBytes = kStages * kStage;
     static constexpr int kLoads = SUB * (SideA::kPerWave + SideB::kPerWave);  // a wave's, per stage
     static_assert(kStages >= 3 && (kStages - 2) * kLoads < 64, "stages");
@@ -387,14 +398,16 @@ template <typename T, int BM_, int BN, int SUB, bool AS, bool BS> struct GemmRin
     static __device__ __forceinline__ int wave_n(int) { return 0; }
 
     // work(i): the workgroup's tile i, K = 0 behind the last; done(i): its epilogue, on acc. All tiles
-    // share the operands' ld. Behind the last tile LDS is free.
+    // share the operands' ld. Behind the last tile LDS is free. b_rows: null, or (in LDS) the rows of B's
+    // matrix that the tile's columns are, nb of them.
     template <typename Work, typename Done>
     __device__ __forceinline__ void run(int64_t lda, int64_t ldb, Work work, Done done, char *lds,
-                                        int wave, int lane) {
+                                        int wave, int lane, const int *b_rows = nullptr, int nb = 0) {
         SideA sa;
         SideB sb;
         sa.init(lda, wave, lane);
         sb.init(ldb, wave, lane);
+        if (b_rows) sb.take_rows(b_rows, nb, (int)ldb, wave, lane);
         typename SideA::template Reader<MI> ra;
         typename SideB::template Reader<NI> rb;
         ra.init(wave_m(wave), lane);

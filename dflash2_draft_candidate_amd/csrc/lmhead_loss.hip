@@ -26,6 +26,7 @@
 //     throughout.
 #include <type_traits>
 
+#include "dflash2.h"
 #include "gemm_tile.h"
 #include "kernels.h"
 
@@ -121,6 +122,11 @@ struct GatherJob {
 
 constexpr int kGatherRows = 4;     // rows per workgroup, one a wave
 constexpr int kGatherEntries = 8;  // entries per wave
+// Rows of W read whole from this H on, rings below it. V = 152000, loss and gradients: H = 520, 16 rows 176 us
+// and 178, 32 rows 220 and 192; H = 1032, 16 rows 278 and 343, 32 rows 346 and 355; H = 2048, 16 rows 448
+// and 586, 32 rows 576 and 597. (More than 32 rows: 64 of H = 1032, rings 432, whole rows 428; H = 520, 229
+// and 269.)
+constexpr int kRowsFrom = 1024;
 constexpr int kInlineEntries = 4096;  // up to so many the gather looks at them itself (a launch less)
 
 template <Rows M>
@@ -250,6 +256,12 @@ struct LogitsJob {
     int64_t ldg;          // columns
     const float2 *scale;  // backward: [count]
     int low;              // few rows: the row of G where what rounding left of row 0 stands, or 0
+    // few rows that the workgroups find themselves (`rows` are all R of them, count and scale are not read)
+    int R;
+    Entries e;
+    float *stats;         // [R, K + 2]: forward: the entries' logits out; else in
+    const float *grad_loss;
+    int32_t *place, *from, *kept;  // out: FewRows
 };
 
 // A tile's end: for GRAD G's values, else maxima and sums. Its vocabulary rows start at v0, its
@@ -355,33 +367,166 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(Logi
         lds, wave, lane);
 }
 
+// ---- few rows ---------------------------------------------------------------------------------------
+// Up to BN <= 64 rows: every workgroup finds the kept ones and their entries in its range of the
+// vocabulary by itself (a launch and a pass over the rows less); the first one leaves the rows' places for
+// the kernels that follow. The entries' logits are taken, and their masses subtracted, where their columns
+// come by. All eight waves take part: a wave looks at rows wave, wave + 8, .., a lane at an entry.
+template <int BN, int LIST> struct FewRowsLds {
+    float x[BN * LIST];     // backward: an entry's mass times g tau; forward: its column and which it is
+    uint16_t v[BN * LIST];  // backward: its column. Columns count from the range's first on; a forward
+                            // range has up to 2^20 of them, one of a piece 2^12
+    int listed[BN];         // entries of a kept row in the range
+    int from[BN], keeps[BN];  // the row that a kept one is; whether a row is kept
+
+    static constexpr int kWhich = 64;  // x = column * kWhich + entry
+    __device__ __forceinline__ int column(int at, bool forward) const {
+        return forward ? (int)(__float_as_uint(x[at]) / kWhich) : v[at];
+    }
+    __device__ __forceinline__ int entry(int at) const { return (int)(__float_as_uint(x[at]) % kWhich); }
+};
+static_assert(DFLASH2_MAX_K <= 64 && DFLASH2_MAX_V / kCus <= 1 << 20, "FewRowsLds::x");
+
+template <int BN, int LIST, bool FORWARD> struct FewRows {
+    typedef FewRowsLds<BN, LIST> Lds;
+    static constexpr int kRounds = BN / kGemmWaves;
+    int ids[kRounds];
+    float teacher[kRounds], sums[kRounds], grads[kRounds];
+    uint64_t mask;  // the kept rows
+    int R;          // their number
+
+    __device__ __forceinline__ void find(const Entries &e, int rows, int V, const float *stats,
+                                         const float *grad_loss, Lds &lds, int32_t *place,
+                                         int32_t *from, int32_t *kept, int wave, int lane) {
+        const int K = e.K;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {  // (all loads at once)
+            const int r = min(wave + kGemmWaves * i, rows - 1);
+            const int64_t at = (int64_t)r * K + min(lane, K - 1);
+            ids[i] = e.ids[at];
+            teacher[i] = e.teacher ? e.teacher[at] : 0.f;
+            if constexpr (!FORWARD) {
+                sums[i] = stats[(int64_t)r * (K + 2) + 1];
+                grads[i] = grad_loss[r];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int r = wave + kGemmWaves * i;
+            bool has;
+            if constexpr (FORWARD)
+                has = __ballot(lane < K && id_ok(ids[i], V) && !(teacher[i] == -INFINITY)) != 0ull;
+            else
+                has = !(sums[i] < 0.f);
+            if (lane == 0) lds.keeps[r] = has && r < rows ? 1 : 0;
+        }
+        __syncthreads();
+        mask = __ballot(lane < BN && lds.keeps[min(lane, BN - 1)] != 0);
+        R = __popcll(mask);
+        if (wave == 0) {
+            const int mine = __popcll(mask & ((1ull << lane) - 1));
+            const bool is_kept = (mask >> lane) & 1ull;
+            if (is_kept) lds.from[mine] = lane;
+            if (blockIdx.x == 0) {
+                if (lane < rows) place[lane] = is_kept ? mine : -1;
+                if (is_kept) from[mine] = lane;
+                if (lane == 0) *kept = R;
+            }
+        }
+        __syncthreads();
+    }
+
+    // The entries in columns [first, end), in their order.
+    __device__ __forceinline__ void list(const Entries &e, int V, float c, int first, int end, Lds &lds,
+                                         int wave, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int r = wave + kGemmWaves * i, p = __popcll(mask & ((1ull << r) - 1));
+            if (!((mask >> r) & 1ull)) continue;
+            const bool any = lane < e.K && id_ok(ids[i], V);
+            float x;
+            if constexpr (FORWARD) {
+                x = __uint_as_float((uint32_t)(ids[i] - first) * Lds::kWhich + lane);
+            } else {
+                x = 1.f;
+                if (e.teacher) {
+                    const float t = any ? teacher[i] : -INFINITY;
+                    float high = wave_max(t, lane);
+                    if (__ballot(any && t != t) != 0ull) high = NAN;
+                    const float w = any ? __builtin_amdgcn_exp2f((t - high) * c) : 0.f;
+                    x = w / wave_sum(w, lane);
+                }
+                x *= grads[i] * e.tau;
+            }
+            const uint64_t m = __ballot(any && ids[i] >= first && ids[i] < end);
+            if ((m >> lane) & 1ull) {
+                const int at = p * LIST + __popcll(m & ((1ull << lane) - 1));
+                if constexpr (!FORWARD) lds.v[at] = (uint16_t)(ids[i] - first);
+                lds.x[at] = x;
+            }
+            if (lane == 0) lds.listed[p] = __popcll(m);
+        }
+        __syncthreads();
+    }
+};
+
+// Entries a row that a ring's workgroup has a list for.
+template <int BN> constexpr int ring_list() { return BN <= 32 ? 32 : 16; }
+
 // Few kept rows (BN <= 128 a tile), or f32: a workgroup takes a range of the vocabulary (a multiple of 16
-// rows of W) and goes through it in tiles of 128 or 256. Forward: each lane keeps its columns' (max, sum) over
-// the whole range. G of few bf16 rows is kept in two parts (rounded, and what that left): the products
-// that read it are bound by W and the gradient, and two parts cost them nothing.
-template <typename T, int BN, bool GRAD>
+// rows of W) and goes through it in tiles of 128 or 256. Forward: each lane keeps its columns' (max, sum)
+// over the whole range. G of few bf16 rows is kept in two parts (rounded, and what that left): the
+// products that read it are bound by W and the gradient, and two parts cost them nothing. FIND: the
+// workgroups find the kept rows (one tile of them) and take care of their entries.
+template <typename T, int BN, bool GRAD, bool FIND>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJob job) {
     // bf16 of up to 64 rows: stages of two K steps, 256 bytes of each of 128 rows of W. f32: the matrix
     // cores are the bound, and shorter tiles leave less of a range's last one unused.
     constexpr int SUB = sizeof(T) == 2 && BN <= 64 ? 2 : 1, BM = sizeof(T) == 4 || SUB == 2 ? 128 : 256;
-    typedef GemmRing<T, BM, BN, SUB, false, false> Ring;
+    constexpr int kFind = FIND ? BN : 8, kList = ring_list<BN>();
+    typedef FewRows<kFind, kList, !GRAD> Few;
+    typedef GemmRing<T, BM, BN, SUB, false, false, FIND ? sizeof(typename Few::Lds) : 0> Ring;
     __shared__ __align__(1024) char lds[Ring::kLdsBytes];
+    __shared__ typename std::conditional<FIND, typename Few::Lds, int>::type few_lds;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int R = *job.count, nr = (R + BN - 1) / BN, ranges = few_ranges(job.v1 - job.v0, nr);
+    Few few;
+    const int *from = nullptr;
+    int R;
+    if constexpr (FIND) {
+        few.find(job.e, job.R, job.V, job.stats, job.grad_loss, few_lds, job.place, job.from, job.kept,
+                 wave, lane);
+        R = few.R;
+        from = few_lds.from;
+    } else {
+        R = *job.count;
+    }
+    const int nr = (R + BN - 1) / BN, ranges = few_ranges(job.v1 - job.v0, nr);
     if ((int)blockIdx.x >= ranges * nr) return;
     int range, tn;
     gemm_place(blockIdx.x, ranges, nr, 1, range, tn);
     const int units = (job.v1 - job.v0 + 15) / 16, r0 = tn * BN;
     const int lo = job.v0 + 16 * (int)((int64_t)units * range / ranges);
     const int hi = min(job.v0 + 16 * (int)((int64_t)units * (range + 1) / ranges), job.v1);
+    if constexpr (FIND) few.list(job.e, job.V, job.c, lo, hi, few_lds, wave, lane);
     const int64_t ld = (int64_t)job.H * sizeof(T);
     const float c = job.c;
+    const int rows = FIND ? job.R : R;  // of `rows`
     float top[Ring::NI], sum[Ring::NI];
+    float2 scale[Ring::NI];  // (read here: a load in a tile's end would wait for all that are in flight)
 #pragma unroll
     for (int ni = 0; ni < Ring::NI; ++ni) {
         top[ni] = -INFINITY;
         sum[ni] = 0.f;
+        if constexpr (GRAD) {
+            const int r = min(r0 + 16 * ni + (lane & 15), R - 1);
+            if constexpr (FIND) {
+                const float *st = job.stats + (int64_t)from[r] * (job.e.K + 2);
+                scale[ni] = float2{st[0], job.grad_loss[from[r]] * job.e.tau / st[1]};
+            } else {
+                scale[ni] = job.scale[r];
+            }
+        }
     }
     Ring ring;
     ring.run(
@@ -389,7 +534,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
         [&](int i) -> GemmWork {
             const int v0 = lo + i * BM;
             if (v0 >= hi) return {{job.W, ld, 0}, {job.rows, ld, 0}, 0};
-            return {operand_kc<T>(job.W, ld, v0, hi, 0), operand_kc<T>(job.rows, ld, r0, R, 0), job.H};
+            return {operand_kc<T>(job.W, ld, v0, hi, 0), operand_kc<T>(job.rows, ld, r0, rows, 0), job.H};
         },
         [&](int i) {
             const int at = anew(lane), g = at >> 4, j = at & 15;
@@ -402,7 +547,22 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
 #pragma unroll
             for (int ni = 0; ni < Ring::NI; ++ni) {
                 const int rn = 16 * ni + j, r = r0 + rn;
+                int listed = 0;
+                if constexpr (FIND) listed = r < R ? few_lds.listed[min(r, kFind - 1)] : 0;
                 if constexpr (!GRAD) {
+                    if constexpr (FIND) {
+                        for (int n = 0; n < listed; ++n) {
+                            const int dv = lo + few_lds.column(r * kList + n, true) - vw;
+                            const int j = few_lds.entry(r * kList + n);
+#pragma unroll
+                            for (int mi = 0; mi < Ring::MI; ++mi)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (dv == 16 * mi + k)
+                                        job.stats[(int64_t)from[r] * (job.e.K + 2) + 2 + j] =
+                                            ring.acc[mi][ni][k];
+                        }
+                    }
                     float high = top[ni];
 #pragma unroll
                     for (int mi = 0; mi < Ring::MI; ++mi)
@@ -421,31 +581,44 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
                     top[ni] = high;
                     sum[ni] = s;
                 } else {
-                    const float2 sc = job.scale[min(r, R - 1)];
+                    f32x4 y[Ring::MI];
+#pragma unroll
+                    for (int mi = 0; mi < Ring::MI; ++mi)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[mi][k] = scale[ni].y *
+                                       __builtin_amdgcn_exp2f((ring.acc[mi][ni][k] - scale[ni].x) * c);
+                    if constexpr (FIND) {
+                        for (int n = 0; n < listed; ++n) {
+                            const int dv = lo + few_lds.column(r * kList + n, false) - vw;
+                            const float x = few_lds.x[r * kList + n];
+#pragma unroll
+                            for (int mi = 0; mi < Ring::MI; ++mi)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) y[mi][k] -= dv == 16 * mi + k ? x : 0.f;
+                        }
+                    }
 #pragma unroll
                     for (int mi = 0; mi < Ring::MI; ++mi) {
                         const int v = vw + 16 * mi;
-                        f32x4 y;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            y[k] = sc.y * __builtin_amdgcn_exp2f((ring.acc[mi][ni][k] - sc.x) * c);
-                            if (r >= R || (ragged && v + k >= job.v1)) y[k] = 0.f;
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            if (r >= R || (ragged && v + k >= job.v1)) y[mi][k] = 0.f;
                         // (hi is a multiple of 16 behind v0, or the piece's end)
                         const int off = v - 4 * g < hi ? rn * (int)ldg + (v - v0) * (int)sizeof(T)
                                                        : kGemmOutside;
-                        store4<T>(out, off, y);
+                        store4<T>(out, off, y[mi]);
                         if (sizeof(T) == 2 && job.low) {
                             f32x4 z;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) z[k] = y[k] - (float)(__bf16)y[k];
+                            for (int k = 0; k < 4; ++k) z[k] = y[mi][k] - (float)(__bf16)y[mi][k];
                             store4<T>(out, off + (off == kGemmOutside ? 0 : job.low * (int)ldg), z);
                         }
                     }
                 }
             }
         },
-        lds, wave, lane);
+        lds, wave, lane, from, R);
     if constexpr (!GRAD) {
         float2 *pair = reinterpret_cast<float2 *>(lds);  // [waves][BN]
         const int g = lane >> 4, j = lane & 15;
@@ -886,7 +1059,8 @@ struct WeightFewJob {
     uint16_t *grad;        // [V, H]
 };
 
-template <int STEPS>
+// TWO: G in two parts of 32 STEPS rows, which meet the same rows of hidden.
+template <int STEPS, bool TWO>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightFewJob job) {
     typedef uint16_t T;
     typedef GemmSide<T, 64, true> Side;
@@ -917,20 +1091,42 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
                        job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? rows - 64 * s : 0, wave);
     };
     issue(u0, 0);
-    bf16x8 fa[2 * STEPS][4];
+    constexpr int kHeld = TWO ? STEPS : 2 * STEPS;
+    bf16x8 fa[kHeld][4];
+    // Where the rows are (`from` has 64 places, of which the kept rows' are used). Loads are of the first kept
+    // row where there is none.
+    typedef int __attribute__((ext_vector_type(4))) i32x4;
+    i32x4 at_row[kHeld][2];
 #pragma unroll
-    for (int s = 0; s < 2 * STEPS; ++s)
+    for (int s = 0; s < kHeld; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = 32 * s + 8 * g + 4 * i, r = !TWO && job.low && k >= job.low ? k - job.low : k;
+            at_row[s][i] = job.from ? *reinterpret_cast<const i32x4 *>(job.from + r)
+                                    : i32x4{r, r + 1, r + 2, r + 3};
+        }
+    const int first = R > 0 && job.from ? job.from[0] : 0;
+#pragma unroll
+    for (int s = 0; s < kHeld; ++s) {
+        uint32_t src[8];  // (bytes: at most 256 rows of 128 KiB)
+        bool in[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = 32 * s + 8 * g + e, r = !TWO && job.low && k >= job.low ? k - job.low : k;
+            in[e] = r < R;
+            src[e] = (uint32_t)(in[e] ? at_row[s][e / 4][e % 4] : first) * (uint32_t)job.H * 2u;
+        }
 #pragma unroll
         for (int mi = 0; mi < 4; ++mi) {
             const int h = h0 + 16 * mi + j;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int k = 32 * s + 8 * g + e, r = job.low && k >= job.low ? k - job.low : k;
-                uint16_t x = 0;
-                if (r < R && h < job.H) x = job.rows[(int64_t)(job.from ? job.from[r] : r) * job.H + h];
-                fa[s][mi][e] = __builtin_bit_cast(__bf16, x);
+                const uint16_t x = *reinterpret_cast<const uint16_t *>(
+                    reinterpret_cast<const char *>(job.rows) + src[e] + 2u * (uint32_t)min(h, job.H - 1));
+                fa[s][mi][e] = __builtin_bit_cast(__bf16, in[e] && h < job.H ? x : (uint16_t)0);
             }
         }
+    }
     Side::template Reader<4> rb;
     rb.init(0, lane);
     char *scratch = lds + 2 * kBuffer + wave * 4096;
@@ -959,7 +1155,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
                     const bf16x8 fb =
                         rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, 2 * half + ni, s % 2);
 #pragma unroll
-                    for (int mi = 0; mi < 4; ++mi) acc[mi][ni] = gemm_mfma(fa[s][mi], fb, acc[mi][ni]);
+                    for (int mi = 0; mi < 4; ++mi) acc[mi][ni] = gemm_mfma(fa[s % kHeld][mi], fb, acc[mi][ni]);
                 }
 #pragma unroll
             for (int ni = 0; ni < 2; ++ni)
@@ -1000,6 +1196,7 @@ struct Plan {
     int bn, nr;              // kept rows of a tile, tiles
     bool few;                // tiles of at most 128 rows: rings (f32: always)
     int kc;                  // few bf16 rows, H <= 4096: columns of H a wave (lmhead_rows.h); or 0
+    bool find;               // few bf16 rows: rings whose workgroups find the kept rows
     int low;                 // few bf16 rows: G in two parts, this many rows apart; or 0
     int grows;               // rows of G
     // forward
@@ -1026,17 +1223,15 @@ int row_tile(int R, int elem) {
     return R > 128 && elem == 2 ? 256 : R > 64 ? 128 : R > 32 ? 64 : 32;
 }
 
-Plan plan(int R, int H, int V, int elem) {
+Plan plan(int R, int H, int V, int K, int elem) {
     Plan p;
     p.bn = row_tile(R, elem);
     p.nr = ceil_div(R, p.bn);
     p.few = p.bn <= 128;
     // rows read whole: as many as a wave's registers hold of its columns
-    if (elem == 2 && (R <= 32 ? H <= 4096 : R <= 64 && H <= 2048))
-        p.kc = H <= 512 ? 64 : H <= 1024 ? 128 : H <= 2048 ? 256 : 512;
-    else
-        p.kc = 0;
+    p.kc = elem == 2 && R <= 32 && H <= 4096 && H > kRowsFrom ? H <= 2048 ? 256 : 512 : 0;
     if (p.kc && R <= 16) p.bn = 16;
+    p.find = elem == 2 && !p.kc && p.bn <= 64 && K <= (p.bn <= 32 ? ring_list<32>() : ring_list<64>());
     p.low = elem == 2 && p.bn <= 64 ? p.bn : 0;
     p.grows = elem == 2 && p.few ? p.bn + p.low : R;
     p.nv = ceil_div(V, kTile);
@@ -1063,7 +1258,7 @@ Plan plan(int R, int H, int V, int elem) {
     p.rows = take((size_t)R * H * elem);
     p.place = take((size_t)R * 4);
     p.count = take(4);
-    p.from = take((size_t)R * 4);
+    p.from = take(64 * 4);  // (of at most 64 rows)
     const size_t common = at;
     p.flags = take((size_t)R * 4);
     // (few_ranges of the kept rows' tiles: 256 bn pairs, or one for each of more rows than that)
@@ -1087,15 +1282,6 @@ Plan plan(int R, int H, int V, int elem) {
 template <int KC>
 void launch_rows_kc(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t s) {
     const dim3 grid(p.rows_grid(job.v1 - job.v0)), block(kGemmThreads);
-    if constexpr (KC <= 256) {
-        if (p.bn == 64) {
-            if (what == RowsDo::kStats)
-                lmloss_rows_kernel<KC, 64, RowsDo::kStats><<<grid, block, 0, s>>>(job);
-            else
-                lmloss_rows_kernel<KC, 64, RowsDo::kGrad><<<grid, block, 0, s>>>(job);
-            return;
-        }
-    }
     if (p.bn == 32) {
         if (what == RowsDo::kStats)
             lmloss_rows_kernel<KC, 32, RowsDo::kStats><<<grid, block, 0, s>>>(job);
@@ -1111,12 +1297,10 @@ void launch_rows_kc(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t 
 }
 
 void launch_rows(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t s) {
-    switch (p.kc) {
-    case 64: launch_rows_kc<64>(p, what, job, s); break;
-    case 128: launch_rows_kc<128>(p, what, job, s); break;
-    case 256: launch_rows_kc<256>(p, what, job, s); break;
-    default: launch_rows_kc<512>(p, what, job, s); break;
-    }
+    if (p.kc == 256)
+        launch_rows_kc<256>(p, what, job, s);
+    else
+        launch_rows_kc<512>(p, what, job, s);
 }
 
 template <typename T, bool GRAD>
@@ -1130,10 +1314,19 @@ void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
         }
     }
     const dim3 grid(job.nr > kCus ? job.nr : kCus);  // (whatever few_ranges gives for the kept rows)
+    if constexpr (sizeof(T) == 2) {
+        if (p.find) {
+            if (p.bn == 64)
+                lmloss_logits_few_kernel<T, 64, GRAD, true><<<grid, block, 0, s>>>(job);
+            else
+                lmloss_logits_few_kernel<T, 32, GRAD, true><<<grid, block, 0, s>>>(job);
+            return;
+        }
+    }
     switch (p.bn) {
-    case 128: lmloss_logits_few_kernel<T, 128, GRAD><<<grid, block, 0, s>>>(job); break;
-    case 64: lmloss_logits_few_kernel<T, 64, GRAD><<<grid, block, 0, s>>>(job); break;
-    default: lmloss_logits_few_kernel<T, 32, GRAD><<<grid, block, 0, s>>>(job); break;
+    case 128: lmloss_logits_few_kernel<T, 128, GRAD, false><<<grid, block, 0, s>>>(job); break;
+    case 64: lmloss_logits_few_kernel<T, 64, GRAD, false><<<grid, block, 0, s>>>(job); break;
+    default: lmloss_logits_few_kernel<T, 32, GRAD, false><<<grid, block, 0, s>>>(job); break;
     }
 }
 
@@ -1166,12 +1359,16 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
                           static_cast<uint16_t *>(job.grad)};
         w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
         const int grid = w.slabs * w.ranges;
-        if (p.grows > 128)
-            lmloss_weight_few_kernel<4><<<grid, kGemmThreads, 0, s>>>(w);
-        else if (p.grows > 64)
-            lmloss_weight_few_kernel<2><<<grid, kGemmThreads, 0, s>>>(w);
-        else
-            lmloss_weight_few_kernel<1><<<grid, kGemmThreads, 0, s>>>(w);
+        switch (p.low) {
+        case 64: lmloss_weight_few_kernel<2, true><<<grid, kGemmThreads, 0, s>>>(w); break;
+        case 32: lmloss_weight_few_kernel<1, true><<<grid, kGemmThreads, 0, s>>>(w); break;
+        case 16: lmloss_weight_few_kernel<1, false><<<grid, kGemmThreads, 0, s>>>(w); break;
+        default:
+            if (p.grows > 128)
+                lmloss_weight_few_kernel<4, false><<<grid, kGemmThreads, 0, s>>>(w);
+            else
+                lmloss_weight_few_kernel<2, false><<<grid, kGemmThreads, 0, s>>>(w);
+        }
     } else {
         const int tiles = job.nh * job.nv;
         lmloss_weight_stream_kernel<T><<<tiles < kCus ? tiles : kCus, kGemmThreads, 0, s>>>(job);
@@ -1195,6 +1392,17 @@ RowsJob rows_job(const Plan &p, const void *hidden, const void *W, const Entries
     return job;
 }
 
+void few_rows(const Plan &p, const Entries &e, int R, float *stats, const float *grad_loss, char *ws,
+              LogitsJob &job) {
+    job.R = R;
+    job.e = e;
+    job.stats = stats;
+    job.grad_loss = grad_loss;
+    job.place = reinterpret_cast<int32_t *>(ws + p.place);
+    job.from = reinterpret_cast<int32_t *>(ws + p.from);
+    job.kept = reinterpret_cast<int32_t *>(ws + p.count);
+}
+
 template <typename T>
 hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, int R, int H, int V,
                    float *loss, float *stats, char *ws, hipStream_t s) {
@@ -1214,31 +1422,34 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
         launch_rows(p, RowsDo::kStats, rj, s);
         return finish(p.rows_grid(V));
     }
-    GatherJob gj = {};
-    gj.hidden = static_cast<const char *>(hidden);
-    gj.W = static_cast<const char *>(W);
-    gj.flags = reinterpret_cast<int32_t *>(ws + p.flags);
-    gj.stats = stats;
-    gj.e = e;
-    gj.R = R;
-    gj.H = H;
-    gj.V = V;
-    gj.rows = ws + p.rows;
-    gj.place = place;
-    gj.count = count;
-    const dim3 grid(ceil_div(R, kGatherRows), e.teacher ? ceil_div(e.K, kGatherEntries) : 1);
-    if (e.teacher && (int64_t)R * e.K <= kInlineEntries) {
-        lmloss_gather_kernel<T, Rows::kEntries, kGatherEntries><<<grid, 256, 0, s>>>(gj);
-    } else if (e.teacher) {
-        lmloss_flags_kernel<<<ceil_div(R, 4), 256, 0, s>>>(e, R, V, const_cast<int32_t *>(gj.flags));
-        lmloss_gather_kernel<T, Rows::kFlags, kGatherEntries><<<grid, 256, 0, s>>>(gj);
-    } else {
-        lmloss_gather_kernel<T, Rows::kTargets, 1><<<grid, 256, 0, s>>>(gj);
+    if (!p.find) {
+        GatherJob gj = {};
+        gj.hidden = static_cast<const char *>(hidden);
+        gj.W = static_cast<const char *>(W);
+        gj.flags = reinterpret_cast<int32_t *>(ws + p.flags);
+        gj.stats = stats;
+        gj.e = e;
+        gj.R = R;
+        gj.H = H;
+        gj.V = V;
+        gj.rows = ws + p.rows;
+        gj.place = place;
+        gj.count = count;
+        const dim3 grid(ceil_div(R, kGatherRows), e.teacher ? ceil_div(e.K, kGatherEntries) : 1);
+        if (e.teacher && (int64_t)R * e.K <= kInlineEntries) {
+            lmloss_gather_kernel<T, Rows::kEntries, kGatherEntries><<<grid, 256, 0, s>>>(gj);
+        } else if (e.teacher) {
+            lmloss_flags_kernel<<<ceil_div(R, 4), 256, 0, s>>>(e, R, V, const_cast<int32_t *>(gj.flags));
+            lmloss_gather_kernel<T, Rows::kFlags, kGatherEntries><<<grid, 256, 0, s>>>(gj);
+        } else {
+            lmloss_gather_kernel<T, Rows::kTargets, 1><<<grid, 256, 0, s>>>(gj);
+        }
     }
     LogitsJob lj = {};
-    lj.rows = gj.rows;
-    lj.W = gj.W;
-    lj.count = gj.count;
+    lj.rows = p.find ? static_cast<const char *>(hidden) : ws + p.rows;
+    lj.W = static_cast<const char *>(W);
+    lj.count = count;
+    few_rows(p, e, R, stats, nullptr, ws, lj);
     lj.H = H;
     lj.V = V;
     lj.v0 = 0;
@@ -1261,7 +1472,7 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
     int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
     int32_t *from = reinterpret_cast<int32_t *>(ws + p.from);
     float2 *scale = reinterpret_cast<float2 *>(ws + p.scale);
-    if (!p.kc) {
+    if (!p.kc && !p.find) {
         GatherJob gj = {};
         gj.hidden = static_cast<const char *>(hidden);
         gj.stats = const_cast<float *>(stats);
@@ -1295,9 +1506,10 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             launch_rows(p, fused ? RowsDo::kHidden : RowsDo::kGrad, rj, s);
         } else {
             LogitsJob lj = {};
-            lj.rows = ws + p.rows;
+            lj.rows = p.find ? static_cast<const char *>(hidden) : ws + p.rows;
             lj.W = Wb;
             lj.count = count;
+            few_rows(p, e, R, const_cast<float *>(stats), grad_loss, ws, lj);
             lj.H = H;
             lj.V = V;
             lj.v0 = v0;
@@ -1310,8 +1522,10 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             lj.scale = scale;
             lj.low = p.low;
             launch_logits<T, true>(p, lj, s);
-            EntriesJob ej = {e, stats, grad_loss, place, R, V, v0, v1, c, lj.G, p.piece, p.low};
-            lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
+            if (!p.find) {
+                EntriesJob ej = {e, stats, grad_loss, place, R, V, v0, v1, c, lj.G, p.piece, p.low};
+                lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
+            }
         }
         if (grad_hidden && !fused) {
             const int per = p.per(v1 - v0);
@@ -1322,8 +1536,9 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             launch_hidden<T>(p, hj, s);
         }
         if (grad_W) {
-            WeightJob wj = {p.kc ? static_cast<const char *>(hidden) : ws + p.rows, ws + p.G, count,
-                            p.kc ? from : nullptr, H, v0, v1, p.piece, nh,
+            const bool found = p.kc || p.find;  // (the kept rows are where they were)
+            WeightJob wj = {found ? static_cast<const char *>(hidden) : ws + p.rows, ws + p.G, count,
+                            found ? from : nullptr, H, v0, v1, p.piece, nh,
                             sizeof(T) == 4 ? ceil_div(v1 - v0, 128) : nv, grad_W};
             launch_weight<T>(p, wj, s);
         }
@@ -1346,19 +1561,19 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
 }  // namespace
 
 size_t lmloss_workspace_bytes(int R, int H, int V, int elem_bytes) {
-    const Plan p = plan(R, H, V, elem_bytes);
+    const Plan p = plan(R, H, V, 1, elem_bytes);  // (K decides nothing that takes space)
     return p.forward;
 }
 
 size_t lmloss_backward_workspace_bytes(int R, int H, int V, int elem_bytes) {
-    const Plan p = plan(R, H, V, elem_bytes);
+    const Plan p = plan(R, H, V, 1, elem_bytes);  // (K decides nothing that takes space)
     return p.backward;
 }
 
 hipError_t launch_lmloss(const void *hidden, const void *W, int elem_bytes, const int32_t *ids,
                          const float *teacher, int R, int H, int V, int K, float tau, float *loss,
                          float *row_stats, void *ws, hipStream_t stream) {
-    const Plan p = plan(R, H, V, elem_bytes);
+    const Plan p = plan(R, H, V, K, elem_bytes);
     const Entries e = {ids, teacher, K, tau};
     char *w = static_cast<char *>(ws);
     return elem_bytes == 2
@@ -1370,7 +1585,7 @@ hipError_t launch_lmloss_backward(const void *hidden, const void *W, int elem_by
                                   const int32_t *ids, const float *teacher, const float *row_stats,
                                   const float *grad_loss, int R, int H, int V, int K, float tau,
                                   void *grad_hidden, void *grad_W, void *ws, hipStream_t stream) {
-    const Plan p = plan(R, H, V, elem_bytes);
+    const Plan p = plan(R, H, V, K, elem_bytes);
     const Entries e = {ids, teacher, K, tau};
     char *w = static_cast<char *>(ws);
     return elem_bytes == 2 ? backward<uint16_t>(p, hidden, W, e, row_stats, grad_loss, R, H, V,

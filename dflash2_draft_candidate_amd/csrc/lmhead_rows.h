@@ -1,5 +1,5 @@
-// The LM head's losses for at most 32 rows (64 where H <= 2048), bf16, H <= 4096: one read of W a pass, at
-// the rate of its stream, and few launches. Included by lmhead_loss.hip.
+// The LM head's losses for at most 32 rows (bf16, kRowsFrom < H <= 4096): one read of W a pass, at the rate
+// of its stream. Included by lmhead_loss.hip.
 //
 // Design:
 //   * A wave owns KC columns of H (an eighth, rounded up to 64 .. 512) for the whole pass: the kept rows'
@@ -12,9 +12,8 @@
 //   * The waves' partial logits (8 x 16 or 8 x 32) are added through LDS in a fixed order, one barrier a
 //     tile, by groups of threads that own an element (row, v) each and keep its running maximum and sum,
 //     or form G there.
-//   * Every workgroup finds the kept rows and their entries in its range by itself, while its first tiles
-//     are on their way; the first one leaves the rows' places for the kernels that follow. The entries'
-//     logits are taken, and their masses subtracted, where their columns come by.
+//   * The workgroups find the kept rows and their entries (FewRows) while their first tiles are on their
+//     way.
 //   * With at most 16 rows the backward pass multiplies G, in two bf16 parts, with the tile of W while it
 //     is still in LDS (v_mfma_f32_16x16x16_bf16: 8 rows, two parts): 16 x KC sums a wave in registers.
 //     W is read once for the logits and grad_hidden (G and its product in passes of their own: 450 us for
@@ -59,14 +58,12 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     constexpr bool kAhead = DO != RowsDo::kHidden;
     constexpr int kYounger = (DO == RowsDo::kStats ? 0 : 2) + (kAhead ? 2 : 0);
     constexpr int kList = DFLASH2_MAX_K;
+    typedef FewRows<BN, kList, DO == RowsDo::kStats> Few;
     __shared__ __align__(1024) char stage[kGemmWaves][2][kRowsTile * kRowBytes];
     __shared__ __align__(16) uint32_t dump[kAhead ? kGemmWaves : 1][kWave];
     __shared__ __align__(16) float part[2][kGemmWaves][kPartRow];
     __shared__ __align__(16) uint16_t gt[DO == RowsDo::kHidden ? 16 * 16 : 8];  // [row][8 hi, 8 lo]
-    // the kept rows' entries in this range: column (from its first on); mass times g tau, or which entry
-    __shared__ uint16_t list_v[BN * kList];
-    __shared__ float list_x[BN * kList];
-    __shared__ int listed[BN], from[BN], keeps[BN];
+    __shared__ typename Few::Lds few_lds;
 
     const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -106,44 +103,11 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     issue(u0 + 1);
     if constexpr (kAhead) ahead(u0 + 2);
 
-    // The kept rows. A wave looks at rows wave, wave + 8, .., a lane at an entry; all loads at once.
-    constexpr int kRounds = BN / kGemmWaves;
-    int ids[kRounds];
-    float teacher[kRounds], sums[kRounds], grads[kRounds];
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int r = min(wave + kGemmWaves * i, job.R - 1);
-        const int64_t at = (int64_t)r * K + min(lane, K - 1);
-        ids[i] = job.e.ids[at];
-        teacher[i] = job.e.teacher ? job.e.teacher[at] : 0.f;
-        if constexpr (DO != RowsDo::kStats) {
-            sums[i] = job.stats[(int64_t)r * (K + 2) + 1];
-            grads[i] = job.grad_loss[r];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int r = wave + kGemmWaves * i;
-        bool has;
-        if constexpr (DO == RowsDo::kStats)
-            has = __ballot(lane < K && id_ok(ids[i], job.V) && !(teacher[i] == -INFINITY)) != 0ull;
-        else
-            has = !(sums[i] < 0.f);
-        if (lane == 0) keeps[r] = has && r < job.R ? 1 : 0;
-    }
-    __syncthreads();
-    const uint64_t mask = __ballot(lane < BN && keeps[min(lane, BN - 1)] != 0);
-    const int R = __popcll(mask), mine = __popcll(mask & ((1ull << lane) - 1));
-    const bool is_kept = (mask >> lane) & 1ull;
-    if (wave == 0) {
-        if (is_kept) from[mine] = lane;
-        if (blockIdx.x == 0) {
-            if (lane < job.R) job.place[lane] = is_kept ? mine : -1;
-            if (is_kept) job.from[mine] = lane;
-            if (lane == 0) *job.count = R;
-        }
-    }
-    __syncthreads();
+    Few few;
+    few.find(job.e, job.R, job.V, job.stats, job.grad_loss, few_lds, job.place, job.from, job.count, wave,
+             lane);
+    const int R = few.R;
+    const int *from = few_lds.from;
     if (R == 0) {  // (the loads in flight end before the workgroup does)
         wait_for<0, 0>();
         return;
@@ -172,34 +136,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     float *stats = job.stats + (int64_t)r_mine * (K + 2);
     if constexpr (DO != RowsDo::kStats)
         sc = float2{stats[0], job.grad_loss[r_mine] * job.e.tau / stats[1]};
-    const int first = job.v0 + u0 * kRowsTile, end = job.v0 + u1 * kRowsTile;
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int r = wave + kGemmWaves * i, p = __popcll(mask & ((1ull << r) - 1));
-        if (!((mask >> r) & 1ull)) continue;
-        const bool any = lane < K && id_ok(ids[i], job.V);
-        float x = __int_as_float(lane);
-        if constexpr (DO != RowsDo::kStats) {
-            x = 1.f;
-            if (job.e.teacher) {
-                const float t = any ? teacher[i] : -INFINITY;
-                float high = wave_max(t, lane);
-                if (__ballot(any && t != t) != 0ull) high = NAN;
-                const float w = any ? __builtin_amdgcn_exp2f((t - high) * job.c) : 0.f;
-                x = w / wave_sum(w, lane);
-            }
-            x *= grads[i] * job.e.tau;
-        }
-        const uint64_t m = __ballot(any && ids[i] >= first && ids[i] < end);
-        if ((m >> lane) & 1ull) {
-            const int at = p * kList + __popcll(m & ((1ull << lane) - 1));
-            list_v[at] = (uint16_t)(ids[i] - first);  // (a range has at most 2^20 / 256 columns, or 8)
-            list_x[at] = x;
-        }
-        if (lane == 0) listed[p] = __popcll(m);
-    }
-    __syncthreads();
-    const int nlist = er < R ? listed[er] : 0;
+    few.list(job.e, job.V, job.c, job.v0 + u0 * kRowsTile, job.v0 + u1 * kRowsTile, few_lds, wave, lane);
+    const int nlist = er < R ? few_lds.listed[er] : 0;
 
     // Fragment addresses within a tile. Logits: row j & 7 (rows 8 .. 15 of the instruction repeat them),
     // chunk 4 s + g. grad_hidden: the 4 rows 4 (g & 1) .. of 16 columns, transposed.
@@ -266,8 +204,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
         const int v = job.v0 + u * kRowsTile + ev, in_range = (u - u0) * kRowsTile + ev;
         if constexpr (DO == RowsDo::kStats) {
             for (int i = 0; i < nlist; ++i)
-                if (list_v[er * kList + i] == in_range && owner == 0)
-                    stats[2 + __float_as_int(list_x[er * kList + i])] = y;
+                if (few_lds.column(er * kList + i, true) == in_range && owner == 0)
+                    stats[2 + few_lds.entry(er * kList + i)] = y;
             if (v < job.v1) {
                 const float high = fmaxf(top, y), ref = high == -INFINITY ? 0.f : high;
                 sum = sum * __builtin_amdgcn_exp2f((top - ref) * job.c) +
@@ -277,7 +215,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
         } else {
             float z = sc.y * __builtin_amdgcn_exp2f((y - sc.x) * job.c);
             for (int i = 0; i < nlist; ++i)
-                if (list_v[er * kList + i] == in_range) z -= list_x[er * kList + i];
+                if (few_lds.v[er * kList + i] == in_range) z -= few_lds.x[er * kList + i];
             if (er >= R || v >= job.v1) z = 0.f;
             const __bf16 hi = (__bf16)z, lo = (__bf16)(z - (float)hi);
             const uint16_t hb = __builtin_bit_cast(uint16_t, hi), lb = __builtin_bit_cast(uint16_t, lo);

@@ -181,8 +181,8 @@ def test_pieces(d2, R, H, V, dt):
     check(ref, *run(d2, *x, 1.0), dtype, 1.0)
 
 
-# each way through the kernels, at its ends: rows read whole (up to 16 and 32 rows, by H), rings of 64 and
-# 128 rows, the weight gradient from held rows (up to 256), streams
+# each way through the kernels, at its ends: rows read whole (up to 16 and 32 rows, by H), rings of 32, 64
+# and 128 rows, the weight gradient from held rows (up to 256), streams
 EDGES = [(R, H, V) for R, V in ((15, 2053), (16, 300), (17, 1031), (32, 4099), (33, 700), (64, 1500),
                                 (65, 513), (128, 2049), (129, 1025), (256, 777), (257, 1300))
          for H in (128, 520, 1000, 2056)] + \
@@ -199,6 +199,20 @@ def test_edges(d2, R, H, V):
     check(ref, *run(d2, *x, 1.0), torch.bfloat16, 1.0)
 
 
+@pytest.mark.parametrize("K", [16, 17, 32, 33, 64])
+@pytest.mark.parametrize("R,H", [(30, 264), (50, 264), (14, 1200), (25, 1200)])
+def test_entries_a_ring_lists(d2, R, H, K):
+    """As many entries as the workgroups of few rows look after by themselves, and one more; all of a row's
+    in one range of the vocabulary."""
+    log(f"lmhead loss R={R} H={H} K={K}")
+    V = 20011
+    x = inputs(R, H, V, K, torch.bfloat16, R + K)
+    x[2][::3] = 5000 + torch.arange(K, device=DEV).int()
+    x[2][R - 1] = -1
+    ref = reference(*x, 1.0)
+    check(ref, *run(d2, *x, 1.0), torch.bfloat16, 1.0)
+
+
 @pytest.mark.parametrize("R,H,V,dt", [(3, 8, 2200001, "bf16"), (20, 8, 1100003, "bf16"),
                                       (40, 8, 1100003, "bf16"), (2, 8, 1100003, "f32")])
 def test_long_vocabulary(d2, R, H, V, dt):
@@ -211,6 +225,27 @@ def test_long_vocabulary(d2, R, H, V, dt):
     x[2][:, 2] = 1 << 20
     ref = reference(*x, 1.0)
     check(ref, *run(d2, *x, 1.0), dtype, 1.0)
+
+
+@pytest.mark.parametrize("R,H", [(3, 8), (40, 8), (3, 1032)])
+def test_longest_ranges(d2, R, H):
+    """A workgroup's range of the vocabulary is past 2^16 columns: the entries' logits are exact there."""
+    log(f"lmhead loss, long ranges R={R} H={H}")
+    V = 2 ** 24 + 70001
+    gen = torch.Generator(device=DEV).manual_seed(51)
+    h = (torch.randint(-5, 6, (R, H), generator=gen, device=DEV) / 4).bfloat16()
+    at = torch.tensor([0, 65534, 65535, 65536, 65790, 2 ** 23 + 9, 2 ** 24 + 1, V - 2, V - 1], device=DEV)
+    W = torch.zeros(V, H, dtype=torch.bfloat16, device=DEV)
+    W[at] = (torch.randint(-2, 3, (at.numel(), H), generator=gen, device=DEV) / 8).bfloat16()
+    ids = at.int().expand(R, -1).contiguous()
+    t = torch.zeros(R, at.numel(), device=DEV)
+    loss, stats = d2.lmhead_distill(h, W, ids, t)
+    x = torch.mm(h.double(), W[at].double().t())
+    assert torch.equal(stats[:, 2:].double(), x)
+    assert torch.equal(stats[:, 0].double(), x.amax(dim=1).clamp(min=0))
+    lse = (x.exp().sum(dim=1) + (V - at.numel())).log()
+    want = (lse[:, None] - x).mean(dim=1) - math.log(at.numel())
+    assert bool(((loss - want).abs() <= eps(V)[0] + U * want.abs()).all())
 
 
 WAYS = [(14, 1000, 700), (20, 64, 700), (90, 72, 1030), (400, 136, 515)]
