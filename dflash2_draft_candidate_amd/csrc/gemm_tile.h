@@ -96,16 +96,17 @@ template <typename T, int B, bool KS, int G = 0> struct GemmSide {
     static constexpr int kStepK = kStepBytes / (int)sizeof(T);
     static constexpr int kLoads = kBytes / 1024;  // of 1 KB, one wave's
     static constexpr int kPerWave = (kLoads + kGemmWaves - 1) / kGemmWaves;
-    static_assert(kLoads % kGemmWaves == 0 || kGemmWaves % kLoads == 0, "the waves share the loads");
+    static_assert(kLoads % kGemmWaves == 0 || kGemmWaves % kLoads == 0 || !KS, "the waves share the loads");
     static constexpr int kRowBytes = B * (int)sizeof(T);  // KS
     static constexpr int kRowChunks = kRowBytes / 16;
 
     int voff[kPerWave];  // the lane's bytes within the operand's step
     int kbyte;           // KC: the first byte of k that the lane reads
 
-    // Where the stage has fewer than 8 loads, some waves make the same one: every wave counts the same.
+    // Where the loads are no multiple of 8, some waves make the same one: every wave counts the same.
     static __device__ __forceinline__ int load_of(int wave, int q) {
-        return kLoads < kGemmWaves ? wave % kLoads : wave + kGemmWaves * q;
+        const int i = wave + kGemmWaves * q;
+        return kLoads < kGemmWaves ? wave % kLoads : i < kLoads ? i : i - kGemmWaves;
     }
 
     static __device__ __forceinline__ int tile_row(int i) {
@@ -449,19 +450,24 @@ template <typename T, int BM_, int BN, int SUB, bool AS, bool BS, int RESERVE = 
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     const char *sta = lds + slot * kStage + u * kStep, *stb = sta + SideA::kBytes;
+                    // (all reads first: the products wait for theirs only, and cover the others)
+                    typename SideA::Frag fa[2][MI];
+                    typename SideB::Frag fb[2][NI];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        typename SideA::Frag fa[MI];
 #pragma unroll
-                        for (int mi = 0; mi < MI; ++mi) fa[mi] = ra.read(sta, mi, h);
+                        for (int mi = 0; mi < MI; ++mi) fa[h][mi] = ra.read(sta, mi, h);
 #pragma unroll
-                        for (int ni = 0; ni < NI; ++ni) {
-                            const typename SideB::Frag fb = rb.read(stb, ni, h);
+                        for (int ni = 0; ni < NI; ++ni) fb[h][ni] = rb.read(stb, ni, h);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
                             for (int mi = 0; mi < MI; ++mi)
-                                acc[mi][ni] = gemm_mfma(fa[mi], fb, acc[mi][ni]);
-                        }
-                    }
+                                acc[mi][ni] = gemm_mfma(fa[h][mi], fb[h][ni], acc[mi][ni]);
                 }
                 slot = slot == kStages - 1 ? 0 : slot + 1;
             }

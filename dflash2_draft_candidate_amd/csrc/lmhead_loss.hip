@@ -223,21 +223,37 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
 
 // ---- the product's epilogues ---------------------------------------------------------------------
 
+// log2(e) / tau: rounded, and what that left.
+struct Coef {
+    float c, low;
+};
+
+// exp(d / tau), d <= 0. The rounded product d c errs by up to |d c| 2^-24 (and as much from c), which is the
+// result's relative error: nothing to what is rounded to bf16; in f32 a correction of first order brings it
+// back (EXACT).
+template <bool EXACT> __device__ __forceinline__ float scaled_exp(float d, Coef k) {
+    const float t = d * k.c, e = __builtin_amdgcn_exp2f(t);
+    if constexpr (!EXACT) return e;
+    const float left = fmaf(d, k.c, -t) + d * k.low;
+    return t > -150.f ? fmaf(e, left * (float)kLn2, e) : e;  // (also where d is infinite, or NaN)
+}
+
 // (ref, sum) pairs in natural units: sum counts exp((x - ref) / tau). NaN in either stays.
-__device__ __forceinline__ void join(float &m, float &s, float om, float os, float c) {
+template <bool EXACT>
+__device__ __forceinline__ void join(float &m, float &s, float om, float os, Coef k) {
     const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.f : top;
-    s = s * __builtin_amdgcn_exp2f((m - ref) * c) + os * __builtin_amdgcn_exp2f((om - ref) * c);
+    s = s * scaled_exp<EXACT>(m - ref, k) + os * scaled_exp<EXACT>(om - ref, k);
     m = top;
 }
 
 // With lane ^ S's pair, in the lower lane's order on both sides (a fused sum of products is not
 // symmetric): every lane ends with the same pair.
-template <int S>
-__device__ __forceinline__ void join_lane(float &m, float &s, int lane, float c) {
+template <bool EXACT, int S>
+__device__ __forceinline__ void join_lane(float &m, float &s, int lane, Coef k) {
     const float om = __uint_as_float(xor_lane<S>(__float_as_uint(m), lane));
     const float os = __uint_as_float(xor_lane<S>(__float_as_uint(s), lane));
     float lm = lane & S ? om : m, ls = lane & S ? os : s;
-    join(lm, ls, lane & S ? m : om, lane & S ? s : os, c);
+    join<EXACT>(lm, ls, lane & S ? m : om, lane & S ? s : os, k);
     m = lm;
     s = ls;
 }
@@ -249,7 +265,7 @@ struct LogitsJob {
     int H, V;
     int v0, v1;           // the piece of the vocabulary
     int nv, nr;           // tiles (of all R rows)
-    float c;              // log2(e) / tau
+    Coef c;               // log2(e) / tau
     float2 *parts;        // forward: per 16 rows, [nparts][16] (max, sum)
     int64_t nparts;
     void *G;              // backward: [count][ldg]
@@ -275,7 +291,7 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
     lane = anew(lane);
     const int g = lane >> 4, j = lane & 15;
     const int vw = v0 + Tile::wave_m(wave) + 4 * g;
-    const float c = job.c;
+    const Coef c = job.c;
     const int64_t ldg = job.ldg * (int64_t)sizeof(T);
     const __amdgpu_buffer_rsrc_t out = out_rows(
         static_cast<char *>(job.G) + r0 * ldg + (int64_t)(v0 - job.v0) * sizeof(T), ldg,
@@ -305,7 +321,7 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
             for (int mi = 0; mi < Tile::MI; ++mi)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum += __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - ref) * c);
+                    sum += scaled_exp<false>(tile.acc[mi][ni][i] - ref, c);
             sum += __uint_as_float(xor_lane<16>(__float_as_uint(sum), lane));
             sum += __uint_as_float(xor_lane<32>(__float_as_uint(sum), lane));
             if (g == 0 && r < R)
@@ -322,7 +338,7 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
             f32x4 y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                y[i] = s[ni].y * __builtin_amdgcn_exp2f((tile.acc[mi][ni][i] - s[ni].x) * c);
+                y[i] = s[ni].y * scaled_exp<false>(tile.acc[mi][ni][i] - s[ni].x, c);
                 if (ragged && vw + 16 * mi + i >= job.v1) y[i] = 0.f;
             }
             return y;
@@ -437,7 +453,7 @@ template <int BN, int LIST, bool FORWARD> struct FewRows {
     }
 
     // The entries in columns [first, end), in their order.
-    __device__ __forceinline__ void list(const Entries &e, int V, float c, int first, int end, Lds &lds,
+    __device__ __forceinline__ void list(const Entries &e, int V, Coef c, int first, int end, Lds &lds,
                                          int wave, int lane) const {
 #pragma unroll
         for (int i = 0; i < kRounds; ++i) {
@@ -453,7 +469,7 @@ template <int BN, int LIST, bool FORWARD> struct FewRows {
                     const float t = any ? teacher[i] : -INFINITY;
                     float high = wave_max(t, lane);
                     if (__ballot(any && t != t) != 0ull) high = NAN;
-                    const float w = any ? __builtin_amdgcn_exp2f((t - high) * c) : 0.f;
+                    const float w = any ? scaled_exp<false>(t - high, c) : 0.f;
                     x = w / wave_sum(w, lane);
                 }
                 x *= grads[i] * e.tau;
@@ -483,6 +499,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
     // bf16 of up to 64 rows: stages of two K steps, 256 bytes of each of 128 rows of W. f32: the matrix
     // cores are the bound, and shorter tiles leave less of a range's last one unused.
     constexpr int SUB = sizeof(T) == 2 && BN <= 64 ? 2 : 1, BM = sizeof(T) == 4 || SUB == 2 ? 128 : 256;
+    constexpr bool kExact = sizeof(T) == 4;
     constexpr int kFind = FIND ? BN : 8, kList = ring_list<BN>();
     typedef FewRows<kFind, kList, !GRAD> Few;
     typedef GemmRing<T, BM, BN, SUB, false, false, FIND ? sizeof(typename Few::Lds) : 0> Ring;
@@ -510,7 +527,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
     const int hi = min(job.v0 + 16 * (int)((int64_t)units * (range + 1) / ranges), job.v1);
     if constexpr (FIND) few.list(job.e, job.V, job.c, lo, hi, few_lds, wave, lane);
     const int64_t ld = (int64_t)job.H * sizeof(T);
-    const float c = job.c;
+    const Coef c = job.c;
     const int rows = FIND ? job.R : R;  // of `rows`
     float top[Ring::NI], sum[Ring::NI];
     float2 scale[Ring::NI];  // (read here: a load in a tile's end would wait for all that are in flight)
@@ -572,12 +589,12 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
                             high = fmaxf(high, ring.acc[mi][ni][k]);
                         }
                     const float ref = high == -INFINITY ? 0.f : high;
-                    float s = sum[ni] * __builtin_amdgcn_exp2f((top[ni] - ref) * c);
+                    float s = sum[ni] * scaled_exp<kExact>(top[ni] - ref, c);
 #pragma unroll
                     for (int mi = 0; mi < Ring::MI; ++mi)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            s += __builtin_amdgcn_exp2f((ring.acc[mi][ni][k] - ref) * c);
+                            s += scaled_exp<kExact>(ring.acc[mi][ni][k] - ref, c);
                     top[ni] = high;
                     sum[ni] = s;
                 } else {
@@ -586,8 +603,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
                     for (int mi = 0; mi < Ring::MI; ++mi)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            y[mi][k] = scale[ni].y *
-                                       __builtin_amdgcn_exp2f((ring.acc[mi][ni][k] - scale[ni].x) * c);
+                            y[mi][k] = scale[ni].y * scaled_exp<kExact>(ring.acc[mi][ni][k] - scale[ni].x, c);
                     if constexpr (FIND) {
                         for (int n = 0; n < listed; ++n) {
                             const int dv = lo + few_lds.column(r * kList + n, false) - vw;
@@ -625,8 +641,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
 #pragma unroll
         for (int ni = 0; ni < Ring::NI; ++ni) {
             float m = top[ni], s = sum[ni];
-            join_lane<16>(m, s, lane, c);
-            join_lane<32>(m, s, lane, c);
+            join_lane<kExact, 16>(m, s, lane, c);
+            join_lane<kExact, 32>(m, s, lane, c);
             if (g == 0) pair[wave * BN + 16 * ni + j] = float2{m, s};
         }
         __syncthreads();
@@ -635,7 +651,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
             float2 x = pair[n];
             for (int w = 1; w < kGemmWaves; ++w) {
                 const float2 y = pair[w * BN + n];
-                join(x.x, x.y, y.x, y.y, c);
+                join<kExact>(x.x, x.y, y.x, y.y, c);
             }
             job.parts[((int64_t)(r >> 4) * ranges + range) * 16 + (r & 15)] = x;
         }
@@ -654,7 +670,7 @@ struct FinishJob {
     int bn;
     Entries e;
     int R, V;
-    float c;
+    Coef c;
     float *loss;
     float *stats;
 };
@@ -675,7 +691,7 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
 #pragma unroll 4
             for (int64_t i = grp; i < nparts; i += kGroups) {
                 const float2 x = src[i * 16];
-                join(m, s, x.x, x.y, job.c);
+                join<true>(m, s, x.x, x.y, job.c);
             }
         }
         pair[grp][k] = float2{m, s};
@@ -696,12 +712,12 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
         float m = -INFINITY, s = 0.f;
         m = pair[lane][k].x;
         s = pair[lane][k].y;
-        join_lane<1>(m, s, lane, job.c);
-        join_lane<2>(m, s, lane, job.c);
-        join_lane<4>(m, s, lane, job.c);
-        join_lane<8>(m, s, lane, job.c);
-        join_lane<16>(m, s, lane, job.c);
-        join_lane<32>(m, s, lane, job.c);
+        join_lane<true, 1>(m, s, lane, job.c);
+        join_lane<true, 2>(m, s, lane, job.c);
+        join_lane<true, 4>(m, s, lane, job.c);
+        join_lane<true, 8>(m, s, lane, job.c);
+        join_lane<true, 16>(m, s, lane, job.c);
+        join_lane<true, 32>(m, s, lane, job.c);
         const int id = lane < K ? job.e.ids[(int64_t)r * K + lane] : -1;
         const bool ok = id_ok(id, job.V);
         if (lane < K && !ok) st[2 + lane] = 0.f;
@@ -741,7 +757,7 @@ struct EntriesJob {
     const float *grad_loss;
     const int32_t *place;
     int R, V, v0, v1;
-    float c;
+    Coef c;
     void *G;
     int64_t ldg;
     int low;
@@ -762,7 +778,7 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
         const float t = ok ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
         float top = wave_max(t, lane);
         if (__ballot(ok && t != t) != 0ull) top = NAN;
-        const float w = ok ? __builtin_amdgcn_exp2f((t - top) * job.c) : 0.f;
+        const float w = ok ? scaled_exp<true>(t - top, job.c) : 0.f;
         mass = w / wave_sum(w, lane);
     }
     float total = 0.f;
@@ -777,7 +793,7 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     }
     if (!ok || earlier || id < job.v0 || id >= job.v1) return;
     const float *st = job.stats + (int64_t)r * (K + 2);
-    const float q = fminf(__builtin_amdgcn_exp2f((st[2 + lane] - st[0]) * job.c) / st[1], 1.f);
+    const float q = fminf(scaled_exp<true>(st[2 + lane] - st[0], job.c) / st[1], 1.f);
     // (fminf drops a NaN: a row whose sum is NaN keeps it)
     const float y = job.grad_loss[r] * job.e.tau * ((st[1] != st[1] ? st[1] : q) - total);
     T *out = static_cast<T *>(job.G) + p * job.ldg + (id - job.v0);
@@ -1220,7 +1236,11 @@ struct Plan {
 // Rows of a tile for R rows. bf16: 256 from 129 rows on (two tiles of 128 read W twice); f32: 128 at
 // most (the matrix cores are the bound there, and smaller tiles leave less of the last one unused).
 int row_tile(int R, int elem) {
-    return R > 128 && elem == 2 ? 256 : R > 64 ? 128 : R > 32 ? 64 : 32;
+    if (elem == 2) return R > 128 ? 256 : R > 64 ? 128 : R > 32 ? 64 : 32;
+    // f32: the matrix cores are the bound, so tiles are as short as the rows allow (331 rows x 1016 x 32003,
+    // loss and gradients: tiles of 112 758 us, of 128 818; 96 rows x 1024 x 100000: 861 us, of 128 1012)
+    const int even = ceil_div(R, ceil_div(R, 128));
+    return even > 64 ? ceil_div(even, 16) * 16 : even > 32 ? 64 : 32;
 }
 
 Plan plan(int R, int H, int V, int K, int elem) {
@@ -1303,6 +1323,12 @@ void launch_rows(const Plan &p, RowsDo what, const RowsJob &job, hipStream_t s) 
         launch_rows_kc<512>(p, what, job, s);
 }
 
+template <typename T, int BN, bool GRAD>
+void launch_logits_f32(dim3 grid, const LogitsJob &job, hipStream_t s) {
+    if constexpr (sizeof(T) == 4)
+        lmloss_logits_few_kernel<T, BN, GRAD, false><<<grid, kGemmThreads, 0, s>>>(job);
+}
+
 template <typename T, bool GRAD>
 void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
     const dim3 block(kGemmThreads);
@@ -1326,8 +1352,16 @@ void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
     switch (p.bn) {
     case 128: lmloss_logits_few_kernel<T, 128, GRAD, false><<<grid, block, 0, s>>>(job); break;
     case 64: lmloss_logits_few_kernel<T, 64, GRAD, false><<<grid, block, 0, s>>>(job); break;
+    case 80: launch_logits_f32<T, 80, GRAD>(grid, job, s); break;
+    case 96: launch_logits_f32<T, 96, GRAD>(grid, job, s); break;
+    case 112: launch_logits_f32<T, 112, GRAD>(grid, job, s); break;
     default: lmloss_logits_few_kernel<T, 32, GRAD, false><<<grid, block, 0, s>>>(job); break;
     }
+}
+
+template <typename T, int BN>
+void launch_hidden_f32(dim3 grid, const HiddenJob &job, hipStream_t s) {
+    if constexpr (sizeof(T) == 4) lmloss_hidden_few_kernel<T, BN><<<grid, kGemmThreads, 0, s>>>(job);
 }
 
 template <typename T>
@@ -1343,9 +1377,10 @@ void launch_hidden(const Plan &p, const HiddenJob &job, hipStream_t s) {
     switch (p.bn + p.low) {
     case 128: lmloss_hidden_few_kernel<T, 128><<<grid, block, 0, s>>>(job); break;
     case 64: lmloss_hidden_few_kernel<T, 64><<<grid, block, 0, s>>>(job); break;
-    default:
-        if constexpr (sizeof(T) == 4) lmloss_hidden_few_kernel<T, 32><<<grid, block, 0, s>>>(job);
-        break;
+    case 112: launch_hidden_f32<T, 112>(grid, job, s); break;
+    case 96: launch_hidden_f32<T, 96>(grid, job, s); break;
+    case 80: launch_hidden_f32<T, 80>(grid, job, s); break;
+    default: launch_hidden_f32<T, 32>(grid, job, s); break;
     }
 }
 
@@ -1375,6 +1410,12 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
     }
 }
 
+Coef coef(float tau) {
+    const double exact = 1.4426950408889634 / (double)tau;
+    const float c = (float)exact;
+    return {c, (float)(exact - (double)c)};
+}
+
 RowsJob rows_job(const Plan &p, const void *hidden, const void *W, const Entries &e, int R, int H, int V,
                  float *stats, char *ws) {
     RowsJob job = {};
@@ -1383,7 +1424,7 @@ RowsJob rows_job(const Plan &p, const void *hidden, const void *W, const Entries
     job.R = R;
     job.H = H;
     job.V = V;
-    job.c = kLog2e / e.tau;
+    job.c = coef(e.tau);
     job.e = e;
     job.stats = stats;
     job.place = reinterpret_cast<int32_t *>(ws + p.place);
@@ -1406,7 +1447,7 @@ void few_rows(const Plan &p, const Entries &e, int R, float *stats, const float 
 template <typename T>
 hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, int R, int H, int V,
                    float *loss, float *stats, char *ws, hipStream_t s) {
-    const float c = kLog2e / e.tau;
+    const Coef c = coef(e.tau);
     int32_t *place = reinterpret_cast<int32_t *>(ws + p.place);
     int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
     float2 *parts = reinterpret_cast<float2 *>(ws + p.parts);
@@ -1467,7 +1508,7 @@ template <typename T>
 hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
                     const float *stats, const float *grad_loss, int R, int H, int V,
                     void *grad_hidden, void *grad_W, char *ws, hipStream_t s) {
-    const float c = kLog2e / e.tau;
+    const Coef c = coef(e.tau);
     int32_t *place = reinterpret_cast<int32_t *>(ws + p.place);
     int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
     int32_t *from = reinterpret_cast<int32_t *>(ws + p.from);

@@ -33,7 +33,7 @@ struct RowsJob {
     const uint16_t *hidden;  // [R, H]
     const uint16_t *W;       // [V, H]
     int R, H, V, v0, v1;     // the piece
-    float c;                 // log2(e) / tau
+    Coef c;                  // log2(e) / tau
     Entries e;
     float *stats;            // [R, K + 2]: kStats: the entries' logits out; else in
     const float *grad_loss;  // kGrad, kHidden
@@ -208,12 +208,11 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
                     stats[2 + few_lds.entry(er * kList + i)] = y;
             if (v < job.v1) {
                 const float high = fmaxf(top, y), ref = high == -INFINITY ? 0.f : high;
-                sum = sum * __builtin_amdgcn_exp2f((top - ref) * job.c) +
-                      __builtin_amdgcn_exp2f((y - ref) * job.c);
+                sum = sum * scaled_exp<false>(top - ref, job.c) + scaled_exp<false>(y - ref, job.c);
                 top = high;
             }
         } else {
-            float z = sc.y * __builtin_amdgcn_exp2f((y - sc.x) * job.c);
+            float z = sc.y * scaled_exp<false>(y - sc.x, job.c);
             for (int i = 0; i < nlist; ++i)
                 if (few_lds.v[er * kList + i] == in_range) z -= few_lds.x[er * kList + i];
             if (er >= R || v >= job.v1) z = 0.f;
@@ -262,9 +261,9 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     wait_for<0, 0>();  // no load is in flight when the workgroup ends
 
     if constexpr (DO == RowsDo::kStats) {
-        join_lane<1>(top, sum, lane, job.c);
-        join_lane<2>(top, sum, lane, job.c);
-        join_lane<4>(top, sum, lane, job.c);
+        join_lane<false, 1>(top, sum, lane, job.c);
+        join_lane<false, 2>(top, sum, lane, job.c);
+        join_lane<false, 4>(top, sum, lane, job.c);
         if (ev == 0 && owner == 0 && er < R)
             job.parts[((int64_t)(er >> 4) * gridDim.x + blockIdx.x) * 16 + (er & 15)] = float2{top, sum};
     }

@@ -199,6 +199,14 @@ def test_edges(d2, R, H, V):
     check(ref, *run(d2, *x, 1.0), torch.bfloat16, 1.0)
 
 
+@pytest.mark.parametrize("R", [65, 80, 81, 96, 97, 112, 113, 128, 129, 160, 225, 270, 331])
+def test_f32_row_tiles(d2, R):
+    log(f"lmhead loss f32 R={R}")
+    x = inputs(R, 264, 1203, 0 if R % 2 else 4, torch.float32, R)
+    x[2][R // 3] = -1
+    check(reference(*x, 1.0), *run(d2, *x, 1.0), torch.float32, 1.0)
+
+
 @pytest.mark.parametrize("K", [16, 17, 32, 33, 64])
 @pytest.mark.parametrize("R,H", [(30, 264), (50, 264), (14, 1200), (25, 1200)])
 def test_entries_a_ring_lists(d2, R, H, K):
