@@ -532,3 +532,26 @@ def test_a_training_step(d2):
     assert abs(float(norm) - whole) <= 4 * U * whole
     for x, y in zip(grads, want):
         assert bool(((x.double() - y).abs() <= (2.0 ** -8 + 8 * U) * y.abs() + 1e-37).all())
+
+
+WORKSPACES = [(3, 64, 700), (14, 1200, 900), (25, 1200, 900), (30, 264, 1000), (50, 264, 1000), (100, 72, 1030),
+              (140, 136, 515), (250, 136, 515), (600, 264, 3000)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("R,H,V", WORKSPACES)
+def test_workspace_as_it_comes(d2, monkeypatch, R, H, V, dt):
+    """Nothing is taken from a workspace that the call has not written: it starts as NaN. All rows, a
+    few, one, none."""
+    log(f"lmhead loss workspace R={R} H={H} V={V} {dt}")
+    monkeypatch.setattr(d2, "_workspace", lambda n, device: torch.full((max(int(n), 16),), 255,
+                                                                       dtype=torch.uint8, device=device))
+    dtype = torch.float32 if dt == "f32" else torch.bfloat16
+    for K, step in ((0, 1), (3, 1), (0, 7), (20, 7), (0, R + 1), (2, R + 1), (0, 0)):
+        x = inputs(R, H, V, K, dtype, R + step)
+        if step != 1:
+            out = torch.ones(R, dtype=torch.bool, device=DEV)
+            if step:
+                out[R // 2::step] = False
+            x[2][out] = -1
+        check(reference(*x, 1.0), *run(d2, *x, 1.0), dtype, 1.0)
