@@ -763,7 +763,9 @@ struct EntriesJob {
     int low;
 };
 
-// One wave per row: G at the row's entries, the masses of equal ids added in their order.
+// One wave per row: G at the row's entries, the masses of equal ids added in their order. f32: taken from
+// what the product has written, whose logit is the one in the row's sum (q - 1 of a confident row keeps its
+// digits so); bf16: from the kept logit, rounded once.
 template <typename T>
 __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     const int r = blockIdx.x * 4 + threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -792,11 +794,17 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
         }
     }
     if (!ok || earlier || id < job.v0 || id >= job.v1) return;
-    const float *st = job.stats + (int64_t)r * (K + 2);
-    const float q = fminf(scaled_exp<true>(st[2 + lane] - st[0], job.c) / st[1], 1.f);
-    // (fminf drops a NaN: a row whose sum is NaN keeps it)
-    const float y = job.grad_loss[r] * job.e.tau * ((st[1] != st[1] ? st[1] : q) - total);
     T *out = static_cast<T *>(job.G) + p * job.ldg + (id - job.v0);
+    const float scale = job.grad_loss[r] * job.e.tau;
+    float y;
+    if constexpr (sizeof(T) == 4) {
+        y = *out - scale * total;
+    } else {
+        const float *st = job.stats + (int64_t)r * (K + 2);
+        const float q = fminf(scaled_exp<true>(st[2 + lane] - st[0], job.c) / st[1], 1.f);
+        // (fminf drops a NaN: a row whose sum is NaN keeps it)
+        y = scale * ((st[1] != st[1] ? st[1] : q) - total);
+    }
     if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<__bf16 *>(out) = (__bf16)y;
         if (job.low)

@@ -534,6 +534,30 @@ def test_a_training_step(d2):
         assert bool(((x.double() - y).abs() <= (2.0 ** -8 + 8 * U) * y.abs() + 1e-37).all())
 
 
+@pytest.mark.parametrize("R", [5, 100, 331])
+def test_f32_rows_sum_to_zero(d2, R):
+    """sum_v G[r][v] is 0 whatever the logits' own rounding: the entry's part is taken from the logit that
+    is in the row's sum. Logits of about 1000 that differ by a few (an error of 1e-4 each); grad_hidden's
+    first column is the sum, W's first being 1. With u = 2^-24: an exponential errs by 4 u, forward's
+    pairs are joined at most 12 times with 7 u each, g / sum, the products and the subtraction by 5 u,
+    the sum of 16 terms (whose magnitudes add up to 2) by 32 u, twice that if it truncates:
+    4 + 4 + 84 + 5 + 64 < 192."""
+    log(f"lmhead loss rows sum to zero R={R}")
+    H, V = 2048, 16
+    gen = torch.Generator(device=DEV).manual_seed(R)
+    h = torch.randn(R, H, generator=gen, device=DEV)
+    base = torch.randn(H, generator=gen, device=DEV)
+    W = base + torch.randn(V, H, generator=gen, device=DEV) * 0.05
+    h = h * 0.3 + base * 0.5
+    h[:, 0], W[:, 0] = 0.0, 1.0
+    ids = torch.mm(h, W.t()).argmax(dim=1).int()
+    g = torch.ones(R, device=DEV)
+    loss, stats = d2.lmhead_ce(h, W, ids)
+    gh, _ = d2.lmhead_ce_backward(h, W, ids, stats, g, need_weight=False)
+    assert float(stats[:, 0].min()) > 500.0
+    assert float(gh[:, 0].abs().max()) <= 192 * U
+
+
 WORKSPACES = [(3, 64, 700), (14, 1200, 900), (25, 1200, 900), (30, 264, 1000), (50, 264, 1000), (100, 72, 1030),
               (140, 136, 515), (250, 136, 515), (600, 264, 3000)]
 
