@@ -12,18 +12,23 @@
 //   * Rows without an entry (prompts, padding) are left out: a first kernel copies the other rows'
 //     hidden states behind one another (what stands in the rows left out, NaN among it, is never
 //     read), and the products run over those alone. Their number stays on the device; workgroups
-//     whose tile lies behind it end at once.
+//     whose tile lies behind it end at once. Up to 64 bf16 rows stay where they are: the product's
+//     workgroups look the kept ones up.
 //   * Forward: the product's tiles (W's rows x hidden rows) end in a maximum and a sum of
 //     exponentials per hidden row, 8 bytes instead of a tile of logits; a second kernel joins
-//     them. The logits of the entries come from dot products of their own, in the first kernel.
+//     them. The logits of the entries come from dot products of their own, in the first kernel, or
+//     (up to 64 bf16 rows) out of the product.
 //   * Backward: for a piece of the vocabulary at a time, the product again (the same sums in the
-//     same order) with G as its epilogue, in a buffer of at most kPieceBytes that stays in the
-//     last-level cache; then the entries of the piece, whose value is formed from the kept logit
-//     and rounded once; then the two products that read the piece. grad_hidden is summed over the
-//     pieces in fp32, split along the vocabulary where it has few tiles.
+//     same order) with G as its epilogue, in a buffer of at most kPieceBytes; then the entries of
+//     the piece; then the two products that read the piece. grad_hidden is summed over the pieces
+//     in fp32, split along the vocabulary where it has few tiles.
+//   * Three ways through the products. bf16, more than 128 rows: streams of 256 x 256 tiles, bound
+//     by the matrix cores (and by the card's power). Fewer rows, and f32: rings, which read W in
+//     tiles as narrow as the rows. At most 32 bf16 rows of 1024 < H <= 4096: W in whole rows
+//     (lmhead_rows.h), bound by its bytes.
 //   * bf16: G is rounded to bf16 for the matrix cores (2^-9 of each entry, as a bf16 gradient of
-//     logits would be); everything else is fp32. f32 inputs take the f32 matrix instructions
-//     throughout.
+//     logits would be; kept in two parts for few rows); everything else is fp32. f32 inputs take the
+//     f32 matrix instructions throughout.
 #include <type_traits>
 
 #include "dflash2.h"
@@ -122,10 +127,10 @@ struct GatherJob {
 
 constexpr int kGatherRows = 4;     // rows per workgroup, one a wave
 constexpr int kGatherEntries = 8;  // entries per wave
-// Rows of W read whole from this H on, rings below it. V = 152000, loss and gradients: H = 520, 16 rows 176 us
-// and 178, 32 rows 220 and 192; H = 1032, 16 rows 278 and 343, 32 rows 346 and 355; H = 2048, 16 rows 448
-// and 586, 32 rows 576 and 597. (More than 32 rows: 64 of H = 1032, rings 432, whole rows 428; H = 520, 229
-// and 269.)
+// Rows of W read whole above this H, rings up to it. V = 152000, loss and gradients, whole rows and rings:
+// H = 520, 16 rows 176 us and 178, 32 rows 220 and 192; H = 1032, 16 rows 278 and 343, 32 rows 346 and
+// 355; H = 2048, 16 rows 448 and 586, 32 rows 576 and 597. (More than 32 rows: 64 of H = 1032, 428 and
+// 432; H = 520, 269 and 229.)
 constexpr int kRowsFrom = 1024;
 constexpr int kInlineEntries = 4096;  // up to so many the gather looks at them itself (a launch less)
 
@@ -147,7 +152,8 @@ __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
 
 // Workgroup (x, y): rows 4 x .. 4 x + 3; y = 0 copies them to their places, and (forward) each y
 // takes the dot products of ENTRIES of the entries. A row's place is the number of kept rows before it,
-// which every workgroup of y = 0 counts for itself.
+// which every workgroup of y = 0 counts for itself. Bound by the rows of W that the entries name: 64 of each
+// of 1024 rows, H = 4096 (537 MB), 89 us; one of each, 12 us.
 template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
     constexpr bool kForward = M != Rows::kStats;
@@ -228,9 +234,9 @@ struct Coef {
     float c, low;
 };
 
-// exp(d / tau), d <= 0. The rounded product d c errs by up to |d c| 2^-24 (and as much from c), which is the
-// result's relative error: nothing to what is rounded to bf16; in f32 a correction of first order brings it
-// back (EXACT).
+// exp(d / tau), d <= 0. The rounded product d c errs by up to |d c| 2^-24 (and as much from c), which is
+// the result's relative error: nothing to what is rounded to bf16; in f32 a correction of first order
+// brings it back (EXACT).
 template <bool EXACT> __device__ __forceinline__ float scaled_exp(float d, Coef k) {
     const float t = d * k.c, e = __builtin_amdgcn_exp2f(t);
     if constexpr (!EXACT) return e;
@@ -272,7 +278,7 @@ struct LogitsJob {
     int64_t ldg;          // columns
     const float2 *scale;  // backward: [count]
     int low;              // few rows: the row of G where what rounding left of row 0 stands, or 0
-    // few rows that the workgroups find themselves (`rows` are all R of them, count and scale are not read)
+    // few rows that the workgroups find themselves (`rows`: all R; count and scale are not read)
     int R;
     Entries e;
     float *stats;         // [R, K + 2]: forward: the entries' logits out; else in
@@ -346,7 +352,9 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
     }
 }
 
-// Tiles of 256 vocabulary rows x 256 kept rows, bf16.
+// Tiles of 256 vocabulary rows x 256 kept rows, bf16. Bound by the matrix cores at the clock that the
+// card's power leaves: 4096 rows x 4096 x 151936, forward 4.02 ms (1267 TFLOP/s); 1024 rows, 1.06 - 1.09 ms
+// (1190: 2376 tiles are 9.3 rounds of the CUs).
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(LogitsJob job) {
     typedef typename std::conditional<GRAD, GradStream<T>, StatsStream<T>>::type Stream;
@@ -385,9 +393,10 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(Logi
 
 // ---- few rows ---------------------------------------------------------------------------------------
 // Up to BN <= 64 rows: every workgroup finds the kept ones and their entries in its range of the
-// vocabulary by itself (a launch and a pass over the rows less); the first one leaves the rows' places for
-// the kernels that follow. The entries' logits are taken, and their masses subtracted, where their columns
-// come by. All eight waves take part: a wave looks at rows wave, wave + 8, .., a lane at an entry.
+// vocabulary by itself (a launch and a pass over the rows less: 8 - 12 us of a call); the first one leaves
+// the rows' places for the kernels that follow. The entries' logits are taken, and their masses
+// subtracted, where their columns come by. All eight waves take part: a wave looks at rows wave,
+// wave + 8, .., a lane at an entry.
 template <int BN, int LIST> struct FewRowsLds {
     float x[BN * LIST];     // backward: an entry's mass times g tau; forward: its column and which it is
     uint16_t v[BN * LIST];  // backward: its column. Columns count from the range's first on; a forward
@@ -494,6 +503,10 @@ template <int BN> constexpr int ring_list() { return BN <= 32 ? 32 : 16; }
 // over the whole range. G of few bf16 rows is kept in two parts (rounded, and what that left): the
 // products that read it are bound by W and the gradient, and two parts cost them nothing. FIND: the
 // workgroups find the kept rows (one tile of them) and take care of their entries.
+// bf16 is bound by W: 64 rows x 4096 x 152000, 237 us a forward call (5.3 TB/s), 128 rows 268 us. f32 by
+// the matrix cores: 298 rows x 1016 x 32003 215 us, 90 TFLOP/s of 154 (the cores are busy 0.72 of the time;
+// reading a stage's fragments before its products, starting loads behind half of them, or one half of the
+// waves behind the other moved nothing).
 template <typename T, int BN, bool GRAD, bool FIND>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJob job) {
     // bf16 of up to 64 rows: stages of two K steps, 256 bytes of each of 128 rows of W. f32: the matrix
@@ -675,7 +688,8 @@ struct FinishJob {
     float *stats;
 };
 
-// 16 rows: their tiles' pairs in a fixed order, then a wave per row over its entries.
+// 16 rows: their tiles' pairs in a fixed order, then a wave per row over its entries. 5 - 7 us for 16 rows (the
+// latency of its loads), 12 us for 1024.
 __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob job) {
     constexpr int kGroups = kFinishThreads / kFinishRows;
     static_assert(kGroups == kWave, "a wave joins a row's groups");
@@ -764,8 +778,8 @@ struct EntriesJob {
 };
 
 // One wave per row: G at the row's entries, the masses of equal ids added in their order. f32: taken from
-// what the product has written, whose logit is the one in the row's sum (q - 1 of a confident row keeps its
-// digits so); bf16: from the kept logit, rounded once.
+// what the product has written, whose logit is the one in the row's sum (q - 1 of a confident row keeps
+// its digits so); bf16: from the kept logit, rounded once. 5 us for 1024 rows of one entry, 10 of 64.
 template <typename T>
 __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     const int r = blockIdx.x * 4 + threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -884,7 +898,8 @@ __device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, in
 }
 
 // Few kept rows, or f32: tiles of 256 columns of H x BN rows of G over a split of the piece, one a
-// workgroup.
+// workgroup. bf16 is bound by the read of W (64 rows x 4096 x 152000, G and this: 472 us), f32 by the matrix
+// cores (298 rows x 1016 x 32003: 197 us, 98 TFLOP/s).
 template <typename T, int BN>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJob job) {
     typedef GemmRing<T, kTile, BN, 1, true, false> Ring;
@@ -906,10 +921,12 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJ
             return {operand_ks<T>(job.W, ldw, h0, job.v0 + k0), operand_kc<T>(job.G, ldg, r0, R, k0),
                     k1 - k0};
         },
-        [&](int) { hidden_done<sizeof(T) == 2>(job, ring, split, job.R, h0, r0, R, wave, lane); }, lds, wave, lane);
+        [&](int) { hidden_done<sizeof(T) == 2>(job, ring, split, job.R, h0, r0, R, wave, lane); }, lds,
+        wave, lane);
 }
 
-// Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16.
+// Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16. 4096 rows x 4096 x 151936: 3.8 ms
+// (1330 TFLOP/s); 1024 rows, 64 tiles in splits, 1.0 ms (1270).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(HiddenJob job) {
     typedef GemmStream<T, true, false, 32> Stream;  // (hidden_done: 32 stores)
@@ -1001,7 +1018,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_rows(const WeightJob &j
                     min(job.v1 - job.v0 - v0, most), ld);
 }
 
-// f32: tiles of 256 columns of H x 128 vocabulary rows, over the kept rows; one a workgroup.
+// f32: tiles of 256 columns of H x 128 vocabulary rows, over the kept rows; one a workgroup. 298 rows x 1016
+// x 32003: 195 us, 99 TFLOP/s (10 K steps a tile, whose end no product covers).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob job) {
     typedef GemmTile<T, kTile, 128, true, true, 4> Tile;
@@ -1029,7 +1047,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
     }
 }
 
-// bf16, more than 128 kept rows: tiles of 256 columns of H x 256 vocabulary rows.
+// bf16, more rows than that: tiles of 256 columns of H x 256 vocabulary rows. 4096 rows x 4096 x 151936: 3.86
+// ms (1320 TFLOP/s); 1024 rows 1.1 ms (1150): of 16 K steps a tile, the end takes a sixth.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(WeightJob job) {
     typedef GemmStream<T, true, true, 16> Stream;
@@ -1071,7 +1090,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 // bf16, few kept rows: 64 STEPS rows of G (with `low`, in two parts). The output is the bound. A wave
 // keeps the kept rows' values at 64 columns of H as fragments, for a workgroup's 512, and goes through a
 // range of the vocabulary, 64 rows at a time: G's columns come through LDS, two buffers, and the output
-// goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows).
+// goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows). 16 rows x 4096 x
+// 151936 (1.245 GB written): 231 us, 5.4 TB/s.
 struct WeightFewJob {
     const uint16_t *rows;  // [count, H], or with `from` all rows
     const char *G;         // [grows][ldg], at most 64 STEPS rows
@@ -1242,11 +1262,12 @@ struct Plan {
 };
 
 // Rows of a tile for R rows. bf16: 256 from 129 rows on (two tiles of 128 read W twice); f32: 128 at
-// most (the matrix cores are the bound there, and smaller tiles leave less of the last one unused).
+// most.
 int row_tile(int R, int elem) {
     if (elem == 2) return R > 128 ? 256 : R > 64 ? 128 : R > 32 ? 64 : 32;
-    // f32: the matrix cores are the bound, so tiles are as short as the rows allow (331 rows x 1016 x 32003,
-    // loss and gradients: tiles of 112 758 us, of 128 818; 96 rows x 1024 x 100000: 861 us, of 128 1012)
+    // f32: the matrix cores are the bound, so tiles are as short as the rows allow (331 rows x 1016 x
+    // 32003, loss and gradients: tiles of 112 758 us, of 128 818; 96 rows x 1024 x 100000: 861, of 128
+    // 1012)
     const int even = ceil_div(R, ceil_div(R, 128));
     return even > 64 ? ceil_div(even, 16) * 16 : even > 32 ? 64 : 32;
 }

@@ -1,9 +1,10 @@
-// The LM head's losses for at most 32 rows (bf16, kRowsFrom < H <= 4096): one read of W a pass, at the rate
-// of its stream. Included by lmhead_loss.hip.
+// The LM head's losses for at most 32 rows (bf16, kRowsFrom < H <= 4096): one read of W a pass, at the
+// rate of its stream. 16 rows x 4096 x 151936: loss 203 us in the kernel (6.1 TB/s), logits again and
+// grad_hidden 270 us (W, and 67 MB of sums). Included by lmhead_loss.hip.
 //
 // Design:
-//   * A wave owns KC columns of H (an eighth, rounded up to 64 .. 512) for the whole pass: the kept rows'
-//     values there are matrix fragments in its registers. A workgroup takes a contiguous range of the
+//   * A wave owns KC columns of H (an eighth, rounded up to 256 or 512) for the whole pass: the kept
+//     rows' values there are matrix fragments in its registers. A workgroup takes a contiguous range of the
 //     vocabulary, 8 rows of W a tile: the waves together read whole rows (8 KB at H = 4096). Tiles of 256
 //     rows x 256 bytes, which the ring of stages reads, touch every row of the range over and over and
 //     ran at 5.0 - 5.4 TB/s; rows read whole, at 6.0.

@@ -394,7 +394,8 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
  *   grad_W         [V, H]  dtype, device, out, may be NULL (a frozen head): G^T . hidden. Written
  *                          in full. (At least one of the two is given; they overlap neither the
  *                          inputs nor each other.)
- *   bf16: G is rounded to bf16 before the two products; everything else is fp32, rounded once.
+ *   bf16: G is rounded to bf16 before the two products (of at most 64 rows it is kept in two bf16
+ *   parts, 16 bits); everything else is fp32, rounded once.
  *   Rows without an entry, or without teacher mass: loss 0, gradient 0; their hidden states and
  *   grad_loss are not read (padding may hold anything) and cost nothing in the products. NaN, or
  *   +inf among a row's logits, makes the row's loss NaN and its gradient NaN, and with it grad_W;
@@ -404,7 +405,8 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
  *   1 <= K <= DFLASH2_MAX_K.
  * Workspace: dflash2_lmhead_loss_workspace_bytes(R, H, V, dtype, backward) bytes (backward 0 or 1:
  * of which call), contents need not be initialised. The backward call goes through the vocabulary
- * in pieces and keeps G of one of them there: 128 MiB at most, or R times 256 columns.
+ * in pieces and keeps G of one of them there: 256 MiB at most, or R times 256 columns; beside it fp32
+ * sums of grad_hidden, some 200 MiB at most or, where that is more, 4 R H bytes, and the kept rows.
  * Errors: DFLASH2_ERR_INVALID_ARG, DFLASH2_ERR_ALIGNMENT, DFLASH2_ERR_WORKSPACE, DFLASH2_ERR_HIP.
  */
 size_t dflash2_lmhead_loss_workspace_bytes(int R, int H, int V, int dtype, int backward);
