@@ -5,7 +5,10 @@
 #include <float.h>
 #include <limits.h>
 
+#include <algorithm>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "kernels.h"
 
@@ -488,6 +491,33 @@ int dflash2_grad_norm(const void *const *grads, const int64_t *sizes, const int3
                                         static_cast<hipStream_t>(stream)));
 }
 
+// No output overlaps another one, or a gradient that is not its own.
+static int check_clip_outputs(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                              int count, void *const *out) {
+    struct Range {
+        uintptr_t first, end;
+        bool operator<(const Range &o) const { return first < o.first; }
+    };
+    std::unique_ptr<Range[]> outs(new (std::nothrow) Range[count > 0 ? count : 1]);
+    if (!outs) return DFLASH2_ERR_UNSUPPORTED;
+    int n = 0;
+    for (int i = 0; i < count; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
+        if (sizes[i] > 0) outs[n++] = {at, at + (size_t)sizes[i] * elem_bytes(dtypes[i])};
+    }
+    if (!std::is_sorted(outs.get(), outs.get() + n)) std::sort(outs.get(), outs.get() + n);
+    for (int i = 1; i < n; ++i)
+        if (outs[i].first < outs[i - 1].end) return DFLASH2_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (sizes[i] == 0 || out[i] == grads[i]) continue;  // (in place: an output itself)
+        const uintptr_t at = reinterpret_cast<uintptr_t>(grads[i]);
+        const uintptr_t end = at + (size_t)sizes[i] * elem_bytes(dtypes[i]);
+        const Range *next = std::lower_bound(outs.get(), outs.get() + n, Range{end, end});
+        if (next != outs.get() && next[-1].end > at) return DFLASH2_ERR_INVALID_ARG;
+    }
+    return DFLASH2_OK;
+}
+
 int dflash2_clip_grads(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
                        int count, void *const *out, float max_norm, float *norm, void *workspace,
                        size_t workspace_bytes, void *stream) {
@@ -497,12 +527,11 @@ int dflash2_clip_grads(const void *const *grads, const int64_t *sizes, const int
         return DFLASH2_ERR_INVALID_ARG;
     for (int i = 0; i < count; ++i) {
         if (sizes[i] == 0) continue;
-        const size_t n = (size_t)sizes[i] * elem_bytes(dtypes[i]);
-        if (!out[i] || (out[i] != grads[i] && overlap(out[i], n, grads[i], n)))
-            return DFLASH2_ERR_INVALID_ARG;
+        if (!out[i]) return DFLASH2_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(out[i]) % elem_bytes(dtypes[i]) != 0)
             return DFLASH2_ERR_ALIGNMENT;
     }
+    if ((rc = check_clip_outputs(grads, sizes, dtypes, count, out))) return rc;
     if ((rc = check_ptrs({norm}))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, grad_norm_workspace_bytes()))) return rc;
     return hip_status(launch_clip_grads(grads, sizes, dtypes, count, out, max_norm, norm, workspace,

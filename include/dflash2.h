@@ -442,7 +442,8 @@ int dflash2_lmhead_distill_backward(const void *hidden, const void *W_lm, int dt
  *                       64 bits. 0 for no tensors.
  *   out        [count]  host array of device pointers, the tensors' own type: g min(1, max_norm /
  *                       norm), rounded to that type. out[i] = grads[i] scales in place; otherwise
- *                       an output overlaps no gradient and no other output.
+ *                       an output overlaps no gradient, and never another output: a tensor that is
+ *                       named twice is refused (DFLASH2_ERR_INVALID_ARG).
  *   max_norm            >= 0, finite.
  *   A norm that is not finite (NaN or infinity among the gradients, or a norm past the largest
  *   float) scales nothing: the caller sees it in `norm` and drops the step.

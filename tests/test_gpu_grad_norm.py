@@ -178,3 +178,25 @@ def test_streams(d2):
             gb = d2.grad_norm(b)
         torch.cuda.synchronize()
         assert torch.equal(ga, na) and torch.equal(gb, nb)
+
+
+def test_outputs_side_by_side(d2):
+    """Outputs that touch, in any order, and gradients named twice: fine; twice the same output: refused,
+    and nothing is written."""
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    flat = torch.zeros(1000, device=DEV)
+    g = [torch.randn(n, generator=gen, device=DEV) for n in (300, 1, 0, 699)]
+    out = [flat[700:], flat[699:700], flat[:0], flat[:699]]
+    norm = d2.clip_grads(g, 1.0, out=out)
+    want = math.sqrt(sum(float((x.double() ** 2).sum()) for x in g))
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want
+    for x, y in zip(g, out):
+        assert bool(((y.double() - x.double() / want).abs() <= 2.0 ** -22 * x.double().abs() / want).all())
+    twice = d2.clip_grads([g[0], g[0]], 1.0, out=[flat[:300], flat[300:600]])
+    want = math.sqrt(2.0 * float((g[0].double() ** 2).sum()))
+    assert abs(float(twice) - want) <= 2.0 ** -23 * want and torch.equal(flat[:300], flat[300:600])
+    before = g[0].clone()
+    for grads, o in (([g[0], g[0]], None), ([g[0], g[0][10:20]], None), ([g[0], g[3]], [g[3][:300], flat[:699]])):
+        with pytest.raises(d2.Dflash2Error):
+            d2.clip_grads(grads, 1e-3, out=o)
+    assert torch.equal(before, g[0])

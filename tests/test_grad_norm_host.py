@@ -52,6 +52,13 @@ def test_norm_rejects(d2, kw, status):
     (dict(out=None), EINVAL), (dict(out=[P, 0]), EINVAL), (dict(out=[P + 16, Q]), EINVAL),
     (dict(out=[P, P + 4096 - 2]), EINVAL), (dict(out=[P, Q + 1]), EALIGN),
     (dict(out=[Q + 2, Q]), EALIGN), (dict(max_norm=-1.0), EINVAL),
+    # an output that overlaps another one, or a gradient that is not its own
+    (dict(out=[Q, Q]), EINVAL), (dict(out=[Q, Q + 30]), EINVAL), (dict(out=[Q + 12, Q]), EINVAL),
+    (dict(out=[P + 4096, Q]), EINVAL), (dict(out=[P + 4096 - 28, Q]), EINVAL),
+    (dict(out=[Q, P + 30]), EINVAL), (dict(out=[P, P]), EINVAL),
+    (dict(grads=[P, P], dtypes=[F32, F32], out=[P, P]), EINVAL),
+    (dict(grads=[P, P], dtypes=[F32, F32], out=[Q, P]), EINVAL),
+    (dict(grads=[P, P + 16], dtypes=[F32, F32], out=[P, P + 16]), EINVAL),
     (dict(max_norm=float("nan")), EINVAL), (dict(max_norm=float("inf")), EINVAL)])
 def test_clip_rejects(d2, kw, status):
     a, keep = arrays(kw)
