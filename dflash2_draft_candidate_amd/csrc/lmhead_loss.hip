@@ -96,6 +96,14 @@ __device__ __forceinline__ double wave_sum(double x, int lane) {
     return add_lane<32>(add_lane<16>(x, lane), lane);
 }
 
+// g tau / sum, and g tau times a mass: g tau alone may pass the largest float.
+__device__ __forceinline__ float grad_scale(float g, float tau, float sum) {
+    return (float)((double)g * (double)tau / (double)sum);
+}
+__device__ __forceinline__ float grad_mass(float g, float tau, float mass) {
+    return (float)((double)g * (double)tau * (double)mass);
+}
+
 // ---- rows with an entry ------------------------------------------------------------------------
 
 // flags[r] = whether row r has an entry with mass (or NaN). One wave per row.
@@ -190,7 +198,7 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
             *reinterpret_cast<u32x4 *>(dst + b) = *reinterpret_cast<const u32x4 *>(src + b);
         if (lane == 0) {
             const float *st = job.stats + (int64_t)r * (K + 2);
-            job.scale[before] = float2{st[0], job.grad_loss[r] * job.e.tau / st[1]};
+            job.scale[before] = float2{st[0], grad_scale(job.grad_loss[r], job.e.tau, st[1])};
         }
         return;
     } else {
@@ -481,7 +489,7 @@ template <int BN, int LIST, bool FORWARD> struct FewRows {
                     const float w = any ? scaled_exp<false>(t - high, c) : 0.f;
                     x = w / wave_sum(w, lane);
                 }
-                x *= grads[i] * e.tau;
+                x = grad_mass(grads[i], e.tau, x);
             }
             const uint64_t m = __ballot(any && ids[i] >= first && ids[i] < end);
             if ((m >> lane) & 1ull) {
@@ -552,7 +560,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
             const int r = min(r0 + 16 * ni + (lane & 15), R - 1);
             if constexpr (FIND) {
                 const float *st = job.stats + (int64_t)from[r] * (job.e.K + 2);
-                scale[ni] = float2{st[0], job.grad_loss[from[r]] * job.e.tau / st[1]};
+                scale[ni] = float2{st[0], grad_scale(job.grad_loss[from[r]], job.e.tau, st[1])};
             } else {
                 scale[ni] = job.scale[r];
             }
@@ -809,15 +817,15 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     }
     if (!ok || earlier || id < job.v0 || id >= job.v1) return;
     T *out = static_cast<T *>(job.G) + p * job.ldg + (id - job.v0);
-    const float scale = job.grad_loss[r] * job.e.tau;
+    const float g = job.grad_loss[r];
     float y;
     if constexpr (sizeof(T) == 4) {
-        y = *out - scale * total;
+        y = *out - grad_mass(g, job.e.tau, total);
     } else {
         const float *st = job.stats + (int64_t)r * (K + 2);
         const float q = fminf(scaled_exp<true>(st[2 + lane] - st[0], job.c) / st[1], 1.f);
         // (fminf drops a NaN: a row whose sum is NaN keeps it)
-        y = scale * ((st[1] != st[1] ? st[1] : q) - total);
+        y = grad_mass(g, job.e.tau, (st[1] != st[1] ? st[1] : q) - total);
     }
     if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<__bf16 *>(out) = (__bf16)y;

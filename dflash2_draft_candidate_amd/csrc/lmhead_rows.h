@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
     float2 sc = {0.f, 0.f};
     float *stats = job.stats + (int64_t)r_mine * (K + 2);
     if constexpr (DO != RowsDo::kStats)
-        sc = float2{stats[0], job.grad_loss[r_mine] * job.e.tau / stats[1]};
+        sc = float2{stats[0], grad_scale(job.grad_loss[r_mine], job.e.tau, stats[1])};
     few.list(job.e, job.V, job.c, job.v0 + u0 * kRowsTile, job.v0 + u1 * kRowsTile, few_lds, wave, lane);
     const int nlist = er < R ? few_lds.listed[er] : 0;
 

@@ -558,6 +558,32 @@ def test_f32_rows_sum_to_zero(d2, R):
     assert float(gh[:, 0].abs().max()) <= 192 * U
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("R,H,V", [(12, 1200, 700), (25, 1200, 700), (30, 264, 700), (60, 264, 700),
+                                   (100, 264, 700), (200, 264, 700), (300, 264, 700)])
+def test_large_scale(d2, R, H, V, dt):
+    """g tau passes the largest fp32 number, the gradient does not: with K equal entries |G| < g tau / K
+    at an entry and g tau q elsewhere, and q is about 1 / V where tau is large. (Six rows of that scale: their
+    sums, at most 6 g tau / 16 * 5 / 4, are finite too.)"""
+    log(f"lmhead loss, large scale R={R} H={H} V={V} {dt}")
+    dtype = torch.float32 if dt == "f32" else torch.bfloat16
+    for K, tau, size in ((64, 1e20, 4e18), (16, 1e20, 4e18), (64, 1e38, 4.0), (16, 1e-20, 1e-10)):
+        tau = float(torch.tensor(tau, dtype=torch.float32))  # (it is passed in fp32)
+        h, W, ids, t, g = inputs(R, H, V, K, dtype, R + K)
+        t.zero_()
+        ids[:] = torch.arange(K, device=DEV)
+        ids[4] = -1
+        g = torch.where(g > 0, 1.0, -1.0) * size
+        g[6:] *= 1e-3
+        ref = reference(h, W, ids, t, g, tau)
+        loss, stats = forward(d2, h, W, ids, t, tau)
+        gh, gw = backward(d2, h, W, ids, t, stats, g, tau)
+        assert bool(torch.isfinite(gh).all()) and bool(torch.isfinite(gw).all())
+        loss.zero_()  # (tau^2 may pass the largest number in it, and it is not what is tested)
+        ref["loss"].zero_()
+        check(ref, loss, gh, gw, dtype, tau)
+
+
 WORKSPACES = [(3, 64, 700), (14, 1200, 900), (25, 1200, 900), (30, 264, 1000), (50, 264, 1000), (100, 72, 1030),
               (140, 136, 515), (250, 136, 515), (600, 264, 3000)]
 
