@@ -23,8 +23,8 @@
 //     the piece; then the two products that read the piece. grad_hidden is summed over the pieces
 //     in fp32, split along the vocabulary where it has few tiles.
 //   * Three ways through the products. bf16, more than 128 rows: streams of 256 x 256 tiles, bound
-//     by the matrix cores (and by the card's power). Fewer rows, and f32: rings, which read W in
-//     tiles as narrow as the rows. At most 32 bf16 rows of 1024 < H <= 4096: W in whole rows
+//     by the matrix cores (and by the card's power). Fewer rows, f32, and logits of few such tiles:
+//     rings, which read W in tiles as narrow as the rows, or of 128 rows. At most 32 bf16 rows of 1024 < H <= 4096: W in whole rows
 //     (lmhead_rows.h), bound by its bytes.
 //   * bf16: G is rounded to bf16 for the matrix cores (2^-9 of each entry, as a bf16 gradient of
 //     logits would be; kept in two parts for few rows); everything else is fp32. f32 inputs take the
@@ -43,6 +43,10 @@ constexpr int64_t kPieceBytes = 256ll << 20;     // of G
 constexpr int kPieceMost = 1 << 20;              // columns of a piece (32-bit offsets in it)
 constexpr int kPlaceGroup = 8;                   // rows of tiles that share columns of tiles
 constexpr int kCus = 256;
+// Up to so many 256 x 256 tiles of logits, the rings' tiles of half that size give every CU one at most.
+// Forward, H = 4096: 256 rows x 32000 (125 tiles) 90 us, as streams 111; 1024 rows x 8000 (128) 80 and 105;
+// 384 rows x 32000 (250) 148 and 118.
+constexpr int kRingTiles = kCus / 2;
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
@@ -286,6 +290,7 @@ struct LogitsJob {
     int64_t ldg;          // columns
     const float2 *scale;  // backward: [count]
     int low;              // few rows: the row of G where what rounding left of row 0 stands, or 0
+    bool whole;           // bf16 rings: all rows of a tile of G are written, zeros behind the kept ones
     // few rows that the workgroups find themselves (`rows`: all R; count and scale are not read)
     int R;
     Entries e;
@@ -581,7 +586,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_few_kernel(LogitsJ
             const bool ragged = v0 + BM > hi;
             const __amdgpu_buffer_rsrc_t out = out_rows(
                 static_cast<char *>(job.G) + r0 * ldg + (int64_t)(v0 - job.v0) * sizeof(T), ldg,
-                job.low ? 2 * job.low : sizeof(T) == 2 ? BN : min(R - r0, BN), BM * sizeof(T));
+                job.low ? 2 * job.low : sizeof(T) == 2 && job.whole ? BN : min(R - r0, BN), BM * sizeof(T));
 #pragma unroll
             for (int ni = 0; ni < Ring::NI; ++ni) {
                 const int rn = 16 * ni + j, r = r0 + rn;
@@ -1252,6 +1257,7 @@ struct Plan {
     bool few;                // tiles of at most 128 rows: rings (f32: always)
     int kc;                  // few bf16 rows, H <= 4096: columns of H a wave (lmhead_rows.h); or 0
     bool find;               // few bf16 rows: rings whose workgroups find the kept rows
+    bool ring;               // logits by rings of 128 rows though not few (bf16, few tiles of 256 x 256)
     int low;                 // few bf16 rows: G in two parts, this many rows apart; or 0
     int grows;               // rows of G
     // forward
@@ -1263,6 +1269,8 @@ struct Plan {
 
     // grad_hidden together with the logits
     bool fused() const { return kc && bn == 16; }
+    // the logits' tiles of rows
+    int logits_bn() const { return ring ? 128 : bn; }
     // workgroups of a rows kernel
     int rows_grid(int width) const {
         const int units = ceil_div(width, kRowsTile);
@@ -1295,6 +1303,7 @@ Plan plan(int R, int H, int V, int K, int elem) {
     p.low = elem == 2 && p.bn <= 64 ? p.bn : 0;
     p.grows = elem == 2 && p.few ? p.bn + p.low : R;
     p.nv = ceil_div(V, kTile);
+    p.ring = !p.few && p.nv * (int64_t)p.nr <= kRingTiles;
     // a piece: whole rounds of tiles over the CUs, if as many fit
     int64_t most = kPieceBytes / ((int64_t)p.grows * elem) / kTile;
     most = most < 1 ? 1 : most > kPieceMost / kTile ? kPieceMost / kTile : most;
@@ -1322,8 +1331,8 @@ Plan plan(int R, int H, int V, int K, int elem) {
     const size_t common = at;
     p.flags = take((size_t)R * 4);
     // (few_ranges of the kept rows' tiles: 256 bn pairs, or one for each of more rows than that)
-    const size_t rows16 = (size_t)ceil_div(R, 16) * 16, few_most = (size_t)kCus * p.bn;
-    const size_t pairs = p.few ? (rows16 > few_most ? rows16 : few_most) : rows16 * p.nv * 2;
+    const size_t rows16 = (size_t)ceil_div(R, 16) * 16, few_most = (size_t)kCus * p.logits_bn();
+    const size_t pairs = p.few || p.ring ? (rows16 > few_most ? rows16 : few_most) : rows16 * p.nv * 2;
     p.parts = take(pairs * sizeof(float2));
     p.forward = at;
     at = common;
@@ -1373,7 +1382,7 @@ template <typename T, bool GRAD>
 void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
     const dim3 block(kGemmThreads);
     if constexpr (sizeof(T) == 2) {
-        if (!p.few) {
+        if (!p.few && !p.ring) {
             const int tiles = job.nv * job.nr;
             lmloss_logits_stream_kernel<T, GRAD><<<tiles < kCus ? tiles : kCus, block, 0, s>>>(job);
             return;
@@ -1389,7 +1398,7 @@ void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
             return;
         }
     }
-    switch (p.bn) {
+    switch (p.logits_bn()) {
     case 128: lmloss_logits_few_kernel<T, 128, GRAD, false><<<grid, block, 0, s>>>(job); break;
     case 64: lmloss_logits_few_kernel<T, 64, GRAD, false><<<grid, block, 0, s>>>(job); break;
     case 80: launch_logits_f32<T, 80, GRAD>(grid, job, s); break;
@@ -1492,7 +1501,7 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
     float2 *parts = reinterpret_cast<float2 *>(ws + p.parts);
     const auto finish = [&](int64_t nparts) {
-        FinishJob fj = {parts, nparts, place, count, p.bn, e, R, V, c, loss, stats};
+        FinishJob fj = {parts, nparts, place, count, p.logits_bn(), e, R, V, c, loss, stats};
         lmloss_finish_kernel<<<ceil_div(R, kFinishRows), kFinishThreads, 0, s>>>(fj);
         return hipGetLastError();
     };
@@ -1536,10 +1545,10 @@ hipError_t forward(const Plan &p, const void *hidden, const void *W, Entries e, 
     lj.v0 = 0;
     lj.v1 = V;
     lj.nv = p.nv;
-    lj.nr = p.nr;
+    lj.nr = ceil_div(R, p.logits_bn());
     lj.c = c;
     lj.parts = parts;
-    lj.nparts = p.few ? 0 : p.nv * 2;
+    lj.nparts = p.few || p.ring ? 0 : p.nv * 2;
     launch_logits<T, false>(p, lj, s);
     return finish(lj.nparts);
 }
@@ -1596,12 +1605,13 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             lj.v0 = v0;
             lj.v1 = v1;
             lj.nv = nv;
-            lj.nr = p.nr;
+            lj.nr = ceil_div(R, p.logits_bn());
             lj.c = c;
             lj.G = ws + p.G;
             lj.ldg = p.piece;
             lj.scale = scale;
             lj.low = p.low;
+            lj.whole = p.few;
             launch_logits<T, true>(p, lj, s);
             if (!p.find) {
                 EntriesJob ej = {e, stats, grad_loss, place, R, V, v0, v1, c, lj.G, p.piece, p.low};

@@ -182,12 +182,14 @@ def test_pieces(d2, R, H, V, dt):
 
 
 # each way through the kernels, at its ends: rows read whole (up to 16 and 32 rows, by H), rings of 32, 64
-# and 128 rows, the weight gradient from held rows (up to 256), streams
+# and 128 rows, the weight gradient from held rows (up to 256), streams, rings for the logits of up to 128
+# tiles
 EDGES = [(R, H, V) for R, V in ((15, 2053), (16, 300), (17, 1031), (32, 4099), (33, 700), (64, 1500),
                                 (65, 513), (128, 2049), (129, 1025), (256, 777), (257, 1300))
          for H in (128, 520, 1000, 2056)] + \
     [(16, 3000, 5000), (31, 4096, 3001), (9, 4104, 2003), (48, 4096, 3001), (130, 4096, 1700),
-     (600, 2048, 2500), (300, 1544, 40001)]
+     (600, 2048, 2500), (300, 1544, 40001), (256, 64, 32768), (256, 64, 32769), (512, 72, 16384),
+     (512, 72, 16385), (1000, 136, 8191), (1000, 136, 8200), (2000, 64, 4000), (5000, 64, 1500)]
 
 
 @pytest.mark.parametrize("R,H,V", EDGES)
@@ -585,7 +587,7 @@ def test_large_scale(d2, R, H, V, dt):
 
 
 WORKSPACES = [(3, 64, 700), (14, 1200, 900), (25, 1200, 900), (30, 264, 1000), (50, 264, 1000), (100, 72, 1030),
-              (140, 136, 515), (250, 136, 515), (600, 264, 3000)]
+              (140, 136, 515), (250, 136, 515), (600, 264, 3000), (300, 64, 20000)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
