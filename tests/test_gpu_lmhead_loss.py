@@ -189,7 +189,8 @@ EDGES = [(R, H, V) for R, V in ((15, 2053), (16, 300), (17, 1031), (32, 4099), (
          for H in (128, 520, 1000, 2056)] + \
     [(16, 3000, 5000), (31, 4096, 3001), (9, 4104, 2003), (48, 4096, 3001), (130, 4096, 1700),
      (600, 2048, 2500), (300, 1544, 40001), (256, 64, 32768), (256, 64, 32769), (512, 72, 16384),
-     (512, 72, 16385), (1000, 136, 8191), (1000, 136, 8200), (2000, 64, 4000), (5000, 64, 1500)]
+     (512, 72, 16385), (1000, 136, 8191), (1000, 136, 8200), (2000, 64, 4000), (5000, 64, 1500),
+     (129, 64, 33001), (256, 72, 40000), (513, 200, 20000), (1300, 136, 9000), (2000, 264, 4500)]
 
 
 @pytest.mark.parametrize("R,H,V", EDGES)
@@ -258,7 +259,8 @@ def test_longest_ranges(d2, R, H):
     assert bool(((loss - want).abs() <= eps(V)[0] + U * want.abs()).all())
 
 
-WAYS = [(14, 1000, 700), (20, 64, 700), (90, 72, 1030), (400, 136, 515)]
+WAYS = [(14, 1000, 700), (20, 64, 700), (90, 72, 1030), (400, 136, 515), (14, 1200, 700), (25, 1200, 700),
+        (400, 136, 20001)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -587,7 +589,7 @@ def test_large_scale(d2, R, H, V, dt):
 
 
 WORKSPACES = [(3, 64, 700), (14, 1200, 900), (25, 1200, 900), (30, 264, 1000), (50, 264, 1000), (100, 72, 1030),
-              (140, 136, 515), (250, 136, 515), (600, 264, 3000), (300, 64, 20000)]
+              (140, 136, 515), (250, 136, 515), (600, 264, 3000), (300, 64, 20000), (140, 72, 34000)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
