@@ -157,7 +157,7 @@ __device__ __forceinline__ u32x4 scaled(u32x4 v, float f) {
     }
 }
 
-// (The product is rounded to fp32 and then to bf16: 2^-24 on top of the 2^-9.)
+// (The product is rounded to fp32 and then to bf16: 2^-24 on top of the 2^-8.)
 template <typename T>
 __device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, float f) {
     constexpr int kPer = 16 / (int)sizeof(T);

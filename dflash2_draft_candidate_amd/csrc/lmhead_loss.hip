@@ -24,9 +24,9 @@
 //     in fp32, split along the vocabulary where it has few tiles.
 //   * Three ways through the products. bf16, more than 128 rows: streams of 256 x 256 tiles, bound
 //     by the matrix cores (and by the card's power). Fewer rows, f32, and logits of few such tiles:
-//     rings, which read W in tiles as narrow as the rows, or of 128 rows. At most 32 bf16 rows of 1024 < H <= 4096: W in whole rows
-//     (lmhead_rows.h), bound by its bytes.
-//   * bf16: G is rounded to bf16 for the matrix cores (2^-9 of each entry, as a bf16 gradient of
+//     rings, which read W in tiles as narrow as the rows, or of 128 rows. At most 32 bf16 rows of
+//     1024 < H <= 4096: W in whole rows (lmhead_rows.h), bound by its bytes.
+//   * bf16: G is rounded to bf16 for the matrix cores (2^-8 of each entry, as a bf16 gradient of
 //     logits would be; kept in two parts for few rows); everything else is fp32. f32 inputs take the
 //     f32 matrix instructions throughout.
 #include <type_traits>
@@ -701,8 +701,8 @@ struct FinishJob {
     float *stats;
 };
 
-// 16 rows: their tiles' pairs in a fixed order, then a wave per row over its entries. 5 - 7 us for 16 rows (the
-// latency of its loads), 12 us for 1024.
+// 16 rows: their tiles' pairs in a fixed order, then a wave per row over its entries. 5 - 7 us for 16
+// rows (the latency of its loads), 12 us for 1024.
 __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob job) {
     constexpr int kGroups = kFinishThreads / kFinishRows;
     static_assert(kGroups == kWave, "a wave joins a row's groups");
@@ -938,8 +938,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJ
         wave, lane);
 }
 
-// Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16. 4096 rows x 4096 x 151936: 3.8 ms
-// (1330 TFLOP/s); 1024 rows, 64 tiles in splits, 1.0 ms (1270).
+// Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16. 4096 rows x 4096 x 151936:
+// 3.8 ms (1330 TFLOP/s); 1024 rows, 64 tiles in splits, 1.0 ms (1270).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(HiddenJob job) {
     typedef GemmStream<T, true, false, 32> Stream;  // (hidden_done: 32 stores)
@@ -1106,8 +1106,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 // bf16, few kept rows: 64 STEPS rows of G (with `low`, in two parts). The output is the bound. A wave
 // keeps the kept rows' values at 64 columns of H as fragments, for a workgroup's 512, and goes through a
 // range of the vocabulary, 64 rows at a time: G's columns come through LDS, two buffers, and the output
-// goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows). 16 rows x 4096 x
-// 151936 (1.245 GB written): 231 us, 5.4 TB/s.
+// goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows). 16 rows x
+// 4096 x 151936 (1.245 GB written): 231 us, 5.4 TB/s.
 struct WeightFewJob {
     const uint16_t *rows;  // [count, H], or with `from` all rows
     const char *G;         // [grows][ldg], at most 64 STEPS rows
@@ -1148,13 +1148,14 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
             side.issue(base + buf * kBuffer + s * Side::kBytes,
-                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128, in ? rows - 64 * s : 0, wave);
+                       job.G + 64 * s * ldg + (int64_t)u * 128, (int)ldg, u * 128,
+                       in ? rows - 64 * s : 0, wave);
     };
     issue(u0, 0);
     constexpr int kHeld = TWO ? STEPS : 2 * STEPS;
     bf16x8 fa[kHeld][4];
-    // Where the rows are (`from` has 64 places, of which the kept rows' are used). Loads are of the first kept
-    // row where there is none.
+    // Where the rows are (`from` has 64 places, of which the kept rows' are used). Loads are of the first
+    // kept row where there is none.
     typedef int __attribute__((ext_vector_type(4))) i32x4;
     i32x4 at_row[kHeld][2];
 #pragma unroll
@@ -1215,7 +1216,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
                     const bf16x8 fb =
                         rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, 2 * half + ni, s % 2);
 #pragma unroll
-                    for (int mi = 0; mi < 4; ++mi) acc[mi][ni] = gemm_mfma(fa[s % kHeld][mi], fb, acc[mi][ni]);
+                    for (int mi = 0; mi < 4; ++mi)
+                        acc[mi][ni] = gemm_mfma(fa[s % kHeld][mi], fb, acc[mi][ni]);
                 }
 #pragma unroll
             for (int ni = 0; ni < 2; ++ni)

@@ -164,7 +164,8 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_rows_kernel(RowsJob job) 
         // this tile's loads: all but the next one's, and the stores behind those
         wait_for<kLoads + kYounger, 15>();
         // (two chains of sums; reads in batches, which the compiler would make and wait for one by one)
-        constexpr int kBatch = kSlices < 4 || DO == RowsDo::kHidden ? (kSlices < 4 ? kSlices : 4) : kSlices < 8 ? kSlices : 8;
+        constexpr int kBatch = DO == RowsDo::kHidden ? 4 : 8;
+        static_assert(kSlices % kBatch == 0, "whole batches");
         f32x4 x[NI][2];
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) x[ni][0] = x[ni][1] = f32x4{0.f, 0.f, 0.f, 0.f};
