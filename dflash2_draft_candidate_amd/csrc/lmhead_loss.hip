@@ -47,6 +47,7 @@ constexpr int kCus = 256;
 // Forward, H = 4096: 256 rows x 32000 (125 tiles) 90 us, as streams 111; 1024 rows x 8000 (128) 80 and 105;
 // 384 rows x 32000 (250) 148 and 118.
 constexpr int kRingTiles = kCus / 2;
+constexpr int kBothGroups = kCus / 2;  // (launch_both)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
@@ -913,16 +914,17 @@ __device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, in
 // Few kept rows, or f32: tiles of 256 columns of H x BN rows of G over a split of the piece, one a
 // workgroup. bf16 is bound by the read of W (64 rows x 4096 x 152000, G and this: 472 us), f32 by the matrix
 // cores (298 rows x 1016 x 32003: 197 us, 98 TFLOP/s).
+template <typename T, int BN> using HiddenRing = GemmRing<T, kTile, BN, 1, true, false>;
+
 template <typename T, int BN>
-__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJob job) {
-    typedef GemmRing<T, kTile, BN, 1, true, false> Ring;
-    __shared__ __align__(1024) char lds[Ring::kLdsBytes];
+__device__ __forceinline__ void hidden_few(const HiddenJob &job, int block, char *lds) {
+    typedef HiddenRing<T, BN> Ring;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int R = sizeof(T) == 2 ? BN : *job.count, nr = (R + BN - 1) / BN;
-    if ((int)blockIdx.x >= job.nh * job.splits * nr) return;
+    if (block >= job.nh * job.splits * nr) return;
     int tm, tn;
-    gemm_place(blockIdx.x, job.nh * job.splits, nr, kPlaceGroup, tm, tn);
+    gemm_place(block, job.nh * job.splits, nr, kPlaceGroup, tm, tn);
     const int split = tm / job.nh, h0 = tm % job.nh * kTile, r0 = tn * BN;
     const int k0 = split * job.per, k1 = min(k0 + job.per, job.v1 - job.v0);
     const int64_t ldw = (int64_t)job.H * sizeof(T), ldg = job.ldg * (int64_t)sizeof(T);
@@ -936,6 +938,12 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJ
         },
         [&](int) { hidden_done<sizeof(T) == 2>(job, ring, split, job.R, h0, r0, R, wave, lane); }, lds,
         wave, lane);
+}
+
+template <typename T, int BN>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJob job) {
+    __shared__ __align__(1024) char lds[HiddenRing<T, BN>::kLdsBytes];
+    hidden_few<T, BN>(job, blockIdx.x, lds);
 }
 
 // Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16. 4096 rows x 4096 x 151936:
@@ -1120,19 +1128,22 @@ struct WeightFewJob {
 };
 
 // TWO: G in two parts of 32 STEPS rows, which meet the same rows of hidden.
+template <int STEPS> constexpr int weight_few_lds() {
+    return 2 * STEPS * GemmSide<uint16_t, 64, true>::kBytes + kGemmWaves * 4096;
+}
+
 template <int STEPS, bool TWO>
-__global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightFewJob job) {
+__device__ __forceinline__ void weight_few(const WeightFewJob &job, int block, char *lds) {
     typedef uint16_t T;
     typedef GemmSide<T, 64, true> Side;
     constexpr int kBuffer = STEPS * Side::kBytes;
     constexpr int kStores = 8;  // a wave's, for 64 rows
-    __shared__ __align__(1024) char lds[2 * kBuffer + kGemmWaves * 4096];
     const int lane = threadIdx.x % kWave, g = lane >> 4, j = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int R = *job.count, rows = job.grows ? job.grows : R;
     // (the slabs of a range run on one XCD, whose L2 gives them G)
-    const int at = blockIdx.x / 8, slab = at % job.slabs;
-    const int range = blockIdx.x % 8 + 8 * (at / job.slabs);
+    const int at = block / 8, slab = at % job.slabs;
+    const int range = block % 8 + 8 * (at / job.slabs);
     const int units = (job.v1 - job.v0 + 63) / 64;
     const int u0 = (int)((int64_t)units * range / job.ranges);
     const int u1 = (int)((int64_t)units * (range + 1) / job.ranges);
@@ -1240,6 +1251,25 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightF
         }
     }
     wait_for<0, 0>();  // no load is in flight when the workgroup ends
+}
+
+template <int STEPS, bool TWO>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_weight_few_kernel(WeightFewJob job) {
+    __shared__ __align__(1024) char lds[weight_few_lds<STEPS>()];
+    weight_few<STEPS, TWO>(job, blockIdx.x, lds);
+}
+
+// Both gradients of little work in one launch, whose two parts do not wait for each other: the first
+// `groups` workgroups take grad_hidden's tiles. 40 rows x 256 x 1024: 9 us, 19 as two launches.
+template <int BN, int STEPS, bool TWO>
+__global__ __launch_bounds__(kGemmThreads) void lmloss_both_few_kernel(HiddenJob hidden,
+                                                                       WeightFewJob weight, int groups) {
+    constexpr int kHidden = HiddenRing<uint16_t, BN>::kLdsBytes, kWeight = weight_few_lds<STEPS>();
+    __shared__ __align__(1024) char lds[kHidden > kWeight ? kHidden : kWeight];
+    if ((int)blockIdx.x < groups)
+        hidden_few<uint16_t, BN>(hidden, blockIdx.x, lds);
+    else
+        weight_few<STEPS, TWO>(weight, blockIdx.x - groups, lds);
 }
 
 }  // namespace
@@ -1390,7 +1420,9 @@ void launch_logits(const Plan &p, const LogitsJob &job, hipStream_t s) {
             return;
         }
     }
-    const dim3 grid(job.nr > kCus ? job.nr : kCus);  // (whatever few_ranges gives for the kept rows)
+    // (at least what few_ranges gives for the kept rows, whose tiles are job.nr at most)
+    const int64_t all = (int64_t)ceil_div(job.v1 - job.v0, 16) * job.nr;
+    const dim3 grid(job.nr > kCus ? job.nr : all < kCus ? (int)all : kCus);
     if constexpr (sizeof(T) == 2) {
         if (p.find) {
             if (p.bn == 64)
@@ -1435,15 +1467,21 @@ void launch_hidden(const Plan &p, const HiddenJob &job, hipStream_t s) {
     }
 }
 
+WeightFewJob weight_few_job(const Plan &p, const WeightJob &job, int groups) {
+    WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.from, job.H,
+                      job.v0, job.v1, p.low, p.few ? p.grows : 0, job.ldg, ceil_div(job.H, 512), 0,
+                      static_cast<uint16_t *>(job.grad)};
+    const int most = ceil_div(job.v1 - job.v0, 64);  // (a range has 64 columns at least)
+    w.ranges = 8 * ceil_div(groups < (int64_t)most * w.slabs ? groups : most * w.slabs, 8 * w.slabs);
+    return w;
+}
+
 template <typename T>
 void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
         lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
     } else if (p.grows <= kTile) {
-        WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.from, job.H,
-                          job.v0, job.v1, p.low, p.few ? p.grows : 0, job.ldg, ceil_div(job.H, 512), 0,
-                          static_cast<uint16_t *>(job.grad)};
-        w.ranges = 8 * ceil_div(kCus, 8 * w.slabs);
+        const WeightFewJob w = weight_few_job(p, job, kCus);
         const int grid = w.slabs * w.ranges;
         switch (p.low) {
         case 64: lmloss_weight_few_kernel<2, true><<<grid, kGemmThreads, 0, s>>>(w); break;
@@ -1459,6 +1497,22 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
         const int tiles = job.nh * job.nv;
         lmloss_weight_stream_kernel<T><<<tiles < kCus ? tiles : kCus, kGemmThreads, 0, s>>>(job);
     }
+}
+
+// Both gradients of up to 128 bf16 rows in one launch, where grad_hidden's tiles leave the weight half of
+// the CUs and more. The backward call in one launch and in two: 40 rows x 256 x 8000 28 us and 37, x 32000
+// (125 tiles) 49 and 49; 100 rows x 1000 x 8000 63 and 70. Whether they were launched.
+bool launch_both(const Plan &p, const HiddenJob &hj, const WeightJob &wj, hipStream_t s) {
+    const int groups = hj.nh * hj.nr * hj.splits;
+    if (!p.few || groups > kBothGroups) return false;
+    const WeightFewJob w = weight_few_job(p, wj, kCus - groups);
+    const dim3 grid(groups + w.slabs * w.ranges), block(kGemmThreads);
+    switch (p.low) {
+    case 64: lmloss_both_few_kernel<128, 2, true><<<grid, block, 0, s>>>(hj, w, groups); break;
+    case 32: lmloss_both_few_kernel<64, 1, true><<<grid, block, 0, s>>>(hj, w, groups); break;
+    default: lmloss_both_few_kernel<128, 2, false><<<grid, block, 0, s>>>(hj, w, groups); break;
+    }
+    return true;
 }
 
 Coef coef(float tau) {
@@ -1620,21 +1674,18 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
                 lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
             }
         }
-        if (grad_hidden && !fused) {
-            const int per = p.per(v1 - v0);
-            HiddenJob hj = {Wb, ws + p.G, count, p.grows, H, v0, v1, p.piece, nh, p.nr,
-                            ceil_div(v1 - v0, per), per, i == 0,
-                            reinterpret_cast<float *>(ws + p.sums), p.low,
-                            p.piece < V ? p.piece : V};
-            launch_hidden<T>(p, hj, s);
-        }
-        if (grad_W) {
-            const bool found = p.kc || p.find;  // (the kept rows are where they were)
-            WeightJob wj = {found ? static_cast<const char *>(hidden) : ws + p.rows, ws + p.G, count,
-                            found ? from : nullptr, H, v0, v1, p.piece, nh,
-                            sizeof(T) == 4 ? ceil_div(v1 - v0, 128) : nv, grad_W};
-            launch_weight<T>(p, wj, s);
-        }
+        const int per = p.per(v1 - v0);
+        const HiddenJob hj = {Wb, ws + p.G, count, p.grows, H, v0, v1, p.piece, nh, p.nr,
+                              ceil_div(v1 - v0, per), per, i == 0, reinterpret_cast<float *>(ws + p.sums),
+                              p.low, p.piece < V ? p.piece : V};
+        const bool found = p.kc || p.find;  // (the kept rows are where they were)
+        const WeightJob wj = {found ? static_cast<const char *>(hidden) : ws + p.rows, ws + p.G, count,
+                              found ? from : nullptr, H, v0, v1, p.piece, nh,
+                              sizeof(T) == 4 ? ceil_div(v1 - v0, 128) : nv, grad_W};
+        if constexpr (sizeof(T) == 2)
+            if (grad_hidden && !fused && grad_W && launch_both(p, hj, wj, s)) continue;
+        if (grad_hidden && !fused) launch_hidden<T>(p, hj, s);
+        if (grad_W) launch_weight<T>(p, wj, s);
     }
     if (grad_hidden) {
         const dim3 grid(R, ceil_div(H, 256));
