@@ -16,8 +16,8 @@
 //     workgroups look the kept ones up.
 //   * Forward: the product's tiles (W's rows x hidden rows) end in a maximum and a sum of
 //     exponentials per hidden row, 8 bytes instead of a tile of logits; a second kernel joins
-//     them. The logits of the entries come from dot products of their own, in the first kernel, or
-//     (up to 64 bf16 rows) out of the product.
+//     them. The logits of the entries come out of the product (up to 64 bf16 rows), or from the
+//     first kernel, which repeats the product's instructions for them.
 //   * Backward: for a piece of the vocabulary at a time, the product again (the same sums in the
 //     same order) with G as its epilogue, in a buffer of at most kPieceBytes; then the entries of
 //     the piece; then the two products that read the piece. grad_hidden is summed over the pieces
@@ -109,6 +109,13 @@ __device__ __forceinline__ float grad_mass(float g, float tau, float mass) {
     return (float)((double)g * (double)tau * (double)mass);
 }
 
+// Between a wave's writes of LDS and its other lanes' reads (LDS keeps a wave's order): for the compiler.
+__device__ __forceinline__ void wave_lds_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ---- rows with an entry ------------------------------------------------------------------------
 
 // flags[r] = whether row r has an entry with mass (or NaN). One wave per row.
@@ -164,14 +171,19 @@ __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
 }
 
 // Workgroup (x, y): rows 4 x .. 4 x + 3; y = 0 copies them to their places, and (forward) each y
-// takes the dot products of ENTRIES of the entries. A row's place is the number of kept rows before it,
-// which every workgroup of y = 0 counts for itself. Bound by the rows of W that the entries name: 64 of each
-// of 1024 rows, H = 4096 (537 MB), 89 us; one of each, 12 us.
+// takes the logits of ENTRIES of the entries. A row's place is the number of kept rows before it,
+// which every workgroup of y = 0 counts for itself.
+// An entry's logit is the same fp32 number as in the row's maximum and sum: the same matrix
+// instructions on the same values of k, one after the other, as the rings and streams make them
+// (another order of sums is 10^-4 off where logits are about 1000, which is all of a sure row's loss).
+// A wave reads 1 KB of its hidden row and of each entry's row of W at a time, through LDS of its own.
 template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
     constexpr bool kForward = M != Rows::kStats;
-    constexpr int kPer = 16 / (int)sizeof(T);
+    constexpr int kBlock = 16 * kWave;               // bytes of a row
+    constexpr int kAhead = ENTRIES == 1 ? 8 : 4;     // blocks asked for at once
     __shared__ int part[4];
+    __shared__ __align__(16) char stage[kForward ? kGatherRows : 1][kForward ? (ENTRIES + 1) * kBlock : 16];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int first = blockIdx.x * kGatherRows, r = first + wave;
@@ -211,31 +223,61 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
         // (past the last entry, and for ids that are none: row 0, whose product nothing reads)
         const int j0 = blockIdx.y * ENTRIES, n = min(ENTRIES, K - j0);
         const char *w[ENTRIES];
-        float sum[ENTRIES];
 #pragma unroll
-        for (int j = 0; j < ENTRIES; ++j) {
-            const int id = j < n ? job.e.ids[(int64_t)r * K + j0 + j] : 0;
-            w[j] = job.W + (id_ok(id, job.V) ? id : 0) * row_bytes;
-            sum[j] = 0.f;
+        for (int e = 0; e < ENTRIES; ++e) {
+            const int id = e < n ? job.e.ids[(int64_t)r * K + j0 + e] : 0;
+            w[e] = job.W + (id_ok(id, job.V) ? id : 0) * row_bytes;
         }
-#pragma unroll 4
-        for (int64_t b = lane * 16; b < row_bytes; b += kWave * 16) {
-            const u32x4 h = *reinterpret_cast<const u32x4 *>(src + b);
-            if (copies) *reinterpret_cast<u32x4 *>(dst + b) = h;
-            float x[kPer];
-            Elem<T>::unpack(h, x);
+        // LDS: 16-byte chunk c of entry e's block at c ^ e, behind them the hidden row's. Lane (g, j) of a
+        // step takes chunk g of its 64 bytes: of entry j (the rows of the instruction repeat them), of
+        // the hidden row in every column.
+        static_assert((ENTRIES & (ENTRIES - 1)) == 0 && ENTRIES <= 16, "rows of the instruction");
+        constexpr int kSteps = 4;  // whose fragments are read together
+        char *lds = stage[wave];
+        const int g = lane >> 4, m = lane % ENTRIES;
+        typedef typename GemmSide<T, kTile, false>::Frag Frag;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t b0 = 0; b0 < row_bytes; b0 += kAhead * kBlock) {
+            u32x4 h[kAhead], x[kAhead][ENTRIES];
 #pragma unroll
-            for (int j = 0; j < ENTRIES; ++j) {
-                float y[kPer];
-                Elem<T>::unpack(*reinterpret_cast<const u32x4 *>(w[j] + b), y);
+            for (int a = 0; a < kAhead; ++a) {  // (zeros behind the row, as in the product)
+                const int64_t b = b0 + a * kBlock + lane * 16;
+                const bool in = b < row_bytes;
+                h[a] = in ? *reinterpret_cast<const u32x4 *>(src + b) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) sum[j] = fmaf(x[i], y[i], sum[j]);
+                for (int e = 0; e < ENTRIES; ++e)
+                    x[a][e] = in ? *reinterpret_cast<const u32x4 *>(w[e] + b) : u32x4{0u, 0u, 0u, 0u};
+            }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const int64_t left = row_bytes - (b0 + a * kBlock);
+                if (left <= 0) break;
+                if (copies && lane * 16 < left)
+                    *reinterpret_cast<u32x4 *>(dst + b0 + a * kBlock + lane * 16) = h[a];
+                wave_lds_order();  // (the last block is read)
+                *reinterpret_cast<u32x4 *>(lds + ENTRIES * kBlock + lane * 16) = h[a];
+#pragma unroll
+                for (int e = 0; e < ENTRIES; ++e)
+                    *reinterpret_cast<u32x4 *>(lds + e * kBlock + ((lane ^ e) << 4)) = x[a][e];
+                wave_lds_order();
+                for (int s0 = 0; s0 < 16 && s0 * 64 < left; s0 += kSteps) {
+                    Frag fw[kSteps], fh[kSteps];
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const int c = 4 * (s0 + s) + g;
+                        fw[s] = *reinterpret_cast<const Frag *>(lds + m * kBlock + ((c ^ m) << 4));
+                        fh[s] = *reinterpret_cast<const Frag *>(lds + ENTRIES * kBlock + (c << 4));
+                    }
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) sum = gemm_mfma(fw[s], fh[s], sum);
+                }
             }
         }
+        // lane (g, j) holds entries 4 g .. 4 g + 3
+        if (lane % 16 == 0) {
 #pragma unroll
-        for (int j = 0; j < ENTRIES; ++j) {
-            const float s = wave_sum(sum[j], lane);
-            if (lane == 0 && j < n) job.stats[(int64_t)r * (K + 2) + 2 + j0 + j] = s;
+            for (int i = 0; i < 4; ++i)
+                if (4 * g + i < n) job.stats[(int64_t)r * (K + 2) + 2 + j0 + 4 * g + i] = sum[i];
         }
     }
 }
@@ -763,9 +805,8 @@ __global__ __launch_bounds__(kFinishThreads) void lmloss_finish_kernel(FinishJob
             ln_p -= log(all);
         }
         if (ok && !(p == 0.0)) {
-            // (the entry's logit comes from another order of sums than the row's: at most 0)
-            double ln_q = ((double)st[2 + lane] - m) / tau - log((double)s);
-            ln_q = ln_q > 0.0 ? 0.0 : ln_q;
+            // (at most 0: the entry's logit is the one in the maximum and the sum)
+            const double ln_q = ((double)st[2 + lane] - m) / tau - log((double)s);
             term = p * (ln_p - ln_q);
         }
         term = wave_sum(term, lane);
@@ -792,8 +833,8 @@ struct EntriesJob {
 };
 
 // One wave per row: G at the row's entries, the masses of equal ids added in their order. f32: taken from
-// what the product has written, whose logit is the one in the row's sum (q - 1 of a confident row keeps
-// its digits so); bf16: from the kept logit, rounded once. 5 us for 1024 rows of one entry, 10 of 64.
+// what the product has written; bf16: from the kept logit, rounded once. Either way the logit is the
+// one in the row's sum, so q - 1 of a sure row keeps its digits. 5 us for 1024 rows of one entry, 10 of 64.
 template <typename T>
 __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
     const int r = blockIdx.x * 4 + threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -829,9 +870,8 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
         y = *out - grad_mass(g, job.e.tau, total);
     } else {
         const float *st = job.stats + (int64_t)r * (K + 2);
-        const float q = fminf(scaled_exp<true>(st[2 + lane] - st[0], job.c) / st[1], 1.f);
-        // (fminf drops a NaN: a row whose sum is NaN keeps it)
-        y = grad_mass(g, job.e.tau, (st[1] != st[1] ? st[1] : q) - total);
+        const float q = scaled_exp<true>(st[2 + lane] - st[0], job.c) / st[1];
+        y = grad_mass(g, job.e.tau, q - total);
     }
     if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<__bf16 *>(out) = (__bf16)y;
