@@ -19,7 +19,10 @@
 //     409 us (5.4 TB/s), clipping 841 us (5.3 TB/s read and written). 400 tensors of 58 million: 46 and
 //     87 us in four launches each, less than the host needs to hand 800 tensors over; 20 of 8192: 4.1
 //     and 4.7 us, latency.
+#include <float.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "device_common.h"
 #include "kernels.h"
@@ -142,24 +145,27 @@ __global__ __launch_bounds__(kNormThreads) void grad_norm_out_kernel(const doubl
     if (threadIdx.x == 0) *norm = (float)x;
 }
 
-template <typename T>
-__device__ __forceinline__ u32x4 scaled(u32x4 v, float f) {
+// F: float, or double for factors below the normal floats (chunk_scale).
+template <typename T, typename F>
+__device__ __forceinline__ u32x4 scaled(u32x4 v, F f) {
+    float x[Elem<T>::kPerVec];
+    Elem<T>::unpack(v, x);
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kPerVec; ++e) x[e] = (float)((F)x[e] * f);
     if constexpr (sizeof(T) == 4) {
-        return u32x4{__float_as_uint(__uint_as_float(v.x) * f), __float_as_uint(__uint_as_float(v.y) * f),
-                     __float_as_uint(__uint_as_float(v.z) * f), __float_as_uint(__uint_as_float(v.w) * f)};
+        return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                     __float_as_uint(x[3])};
     } else {
-        float x[8];
-        Elem<T>::unpack(v, x);
         bf16x8 y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (__bf16)(x[e] * f);
+        for (int e = 0; e < 8; ++e) y[e] = (__bf16)x[e];
         return __builtin_bit_cast(u32x4, y);
     }
 }
 
 // (The product is rounded to fp32 and then to bf16: 2^-24 on top of the 2^-8.)
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, float f) {
+template <typename T, typename F>
+__device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, F f) {
     constexpr int kPer = 16 / (int)sizeof(T);
     constexpr int kAhead = 4;
     int i = threadIdx.x * kPer;
@@ -173,7 +179,7 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, float f) 
     }
     for (; i + kPer <= n; i += kNormThreads * kPer) store16(out + i, scaled<T>(load16(p + i), f));
     for (int e = i; e < n && e < i + kPer; ++e) {
-        const float y = Elem<T>::load(p, e) * f;
+        const float y = (float)((F)Elem<T>::load(p, e) * f);
         if constexpr (sizeof(T) == 4)
             out[e] = y;
         else
@@ -190,18 +196,25 @@ __global__ __launch_bounds__(kNormThreads) void clip_grads_kernel(NormBatch b, N
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = xf;
     // (a norm that is not finite scales nothing)
     const bool clips = xf > max_norm && xf < INFINITY;
-    const float f = clips ? (float)((double)max_norm / x) : 1.f;
+    const double f = clips ? (double)max_norm / x : 1.0;
     for (int i = blockIdx.x; i < b.chunks; i += gridDim.x) {
         const int c = b.chunks - 1 - i, t = tensor_of(b, c);
         if (!clips && o.out[t] == b.grad[t]) continue;
         const int64_t at = (int64_t)(c - b.first[t]) * b.length, left = b.size[t] - at;
         const int n = (int)(left < b.length ? left : b.length);
+        const auto scale = [&](auto *out) {
+            const auto *p = static_cast<const std::remove_pointer_t<decltype(out)> *>(b.grad[t]) + at;
+            // (a factor that is no normal float, as of a norm of 1e36 and a limit of 1e-9, would lose
+            // its digits as one, and every result with it)
+            if (f < (double)FLT_MIN)
+                chunk_scale(p, out + at, n, f);
+            else
+                chunk_scale(p, out + at, n, (float)f);
+        };
         if ((b.wide[t / 32] >> (t % 32)) & 1u)
-            chunk_scale(static_cast<const float *>(b.grad[t]) + at, static_cast<float *>(o.out[t]) + at,
-                        n, f);
+            scale(static_cast<float *>(o.out[t]));
         else
-            chunk_scale(static_cast<const uint16_t *>(b.grad[t]) + at,
-                        static_cast<uint16_t *>(o.out[t]) + at, n, f);
+            scale(static_cast<uint16_t *>(o.out[t]));
     }
 }
 
