@@ -842,7 +842,7 @@ def grad_norm(grads) -> torch.Tensor:
 def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     """Scales the gradients by min(1, max_norm / norm), in place or into `out` (a tensor for each, of
     its type and number of elements): -> their norm, as grad_norm() gives it. A norm that is not
-    finite scales nothing."""
+    finite scales nothing. What is written counts as modified in place for autograd."""
     g = _Tensors(grads)
     o = g
     if out is not None:
@@ -858,4 +858,5 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
                                      len(g.list), _host(o.addresses), float(max_norm), _ptr(norm),
                                      _ptr(ws), ws.numel(), _stream(g.device))
     _check(rc, "dflash2_clip_grads")
+    torch.autograd.graph.increment_version(o.list)  # (what autograd has saved of them is refused)
     return norm
