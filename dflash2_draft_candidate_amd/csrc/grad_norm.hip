@@ -17,8 +17,9 @@
 //   * Tensors may start at any element: 16-byte accesses need no alignment here.
 //   * Both passes are bound by the bytes: 68 bf16 and f32 tensors of 1.11 billion elements (2.2 GB), the norm
 //     409 us (5.4 TB/s), clipping 841 us (5.3 TB/s read and written). 400 tensors of 58 million: 46 and
-//     87 us in four launches each, less than the host needs to hand 800 tensors over; 20 of 8192: 4.1
-//     and 4.7 us, latency.
+//     82 us in four launches each, less than the host needs to hand 800 tensors over; 20 of 8192: 4.1
+//     and 4.7 us, latency. From about 1000 tensors on a launch has fewer workgroups than it could use
+//     (kNormPartials).
 #include <float.h>
 #include <math.h>
 
@@ -32,9 +33,15 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormTensors = 128;    // per launch
-constexpr int kNormPartials = 2048;  // partial sums, all launches together
+// Partial sums, all launches together, which share them evenly: a launch's workgroups in either pass. Norm, and
+// norm with clipping, with 1024, 2048 and 8192: 68 tensors of 16 million 367, 383, 375 us and 1219, 1228, 1194; 400
+// of 145 000, 48, 44, 41 and 102, 98, 95; 1000 of 100 000, 124, 82, 67 and 316, 229, 216; 2000 of 100 000, 510,
+// 296, 150 and 1132, 706, 517 (on the GPU; the host takes about 0.6 us a tensor beside it).
+constexpr int kNormPartials = 2048;
 constexpr int kNormUnit = 2048;      // elements: a workgroup's step
-constexpr int kNormLongest = 32768;  // a chunk
+// A chunk. Norm, and norm with clipping, with 8192, 32768 and 131072: 68 tensors of 16 million 385, 383, 380 us
+// and 1237, 1228, 1253; 1000 of 100 000, 106, 82, 88 and 272, 229, 276.
+constexpr int kNormLongest = 32768;
 
 struct NormBatch {
     const void *grad[kNormTensors];

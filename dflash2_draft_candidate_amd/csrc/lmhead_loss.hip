@@ -152,7 +152,10 @@ constexpr int kGatherEntries = 8;  // entries per wave
 // 355; H = 2048, 16 rows 448 and 586, 32 rows 576 and 597. (More than 32 rows: 64 of H = 1032, 428 and
 // 432; H = 520, 269 and 229.)
 constexpr int kRowsFrom = 1024;
-constexpr int kInlineEntries = 4096;  // up to so many the gather looks at them itself (a launch less)
+// Up to so many the gather looks at the entries itself (a launch less; every workgroup looks at all of the rows
+// before its own). Forward, H = 256, V = 2000, inline and by flags: 256 rows x 16, 31 us and 32; 512 x 16, 31 and
+// 32.5; 1024 x 16, 32.5 and 33; 1024 x 64, 57 and 42.
+constexpr int kInlineEntries = 4096;
 
 template <Rows M>
 __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
@@ -176,7 +179,9 @@ __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
 // An entry's logit is the same fp32 number as in the row's maximum and sum: the same matrix
 // instructions on the same values of k, one after the other, as the rings and streams make them
 // (another order of sums is 10^-4 off where logits are about 1000, which is all of a sure row's loss).
-// A wave reads 1 KB of its hidden row and of each entry's row of W at a time, through LDS of its own.
+// A wave reads 1 KB of its hidden row and of each entry's row of W at a time, through LDS of its own. H = 4096:
+// 64 entries of each of 1024 rows 93 us (537 MB, bound by these bytes), one of each 13 us. f32 waits for the chain
+// of its instructions, 4 us for every 1024 of H (15 us of a call more at H = 4096 than a free order of sums).
 template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
     constexpr bool kForward = M != Rows::kStats;
@@ -409,8 +414,8 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
 }
 
 // Tiles of 256 vocabulary rows x 256 kept rows, bf16. Bound by the matrix cores at the clock that the
-// card's power leaves: 4096 rows x 4096 x 151936, forward 4.02 ms (1267 TFLOP/s); 1024 rows, 1.06 - 1.09 ms
-// (1190: 2376 tiles are 9.3 rounds of the CUs).
+// card's power leaves: 4096 rows x 4096 x 151936, forward 4.02 ms (1267 TFLOP/s); 1024 rows, 1.01 - 1.09 ms
+// (1180 - 1200: 2376 tiles are 9.3 rounds of the CUs).
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(LogitsJob job) {
     typedef typename std::conditional<GRAD, GradStream<T>, StatsStream<T>>::type Stream;
@@ -560,7 +565,7 @@ template <int BN> constexpr int ring_list() { return BN <= 32 ? 32 : 16; }
 // products that read it are bound by W and the gradient, and two parts cost them nothing. FIND: the
 // workgroups find the kept rows (one tile of them) and take care of their entries.
 // bf16 is bound by W: 64 rows x 4096 x 152000, 237 us a forward call (5.3 TB/s), 128 rows 268 us. f32 by
-// the matrix cores: 298 rows x 1016 x 32003 215 us, 90 TFLOP/s of 154 (the cores are busy 0.72 of the time;
+// the matrix cores: 298 rows x 1016 x 32003 200 us, 97 TFLOP/s of 154 (the cores are busy 0.72 of the time;
 // reading a stage's fragments before its products, starting loads behind half of them, or one half of the
 // waves behind the other moved nothing).
 template <typename T, int BN, bool GRAD, bool FIND>
@@ -953,7 +958,7 @@ __device__ __forceinline__ void hidden_done(const HiddenJob &job, Tile &tile, in
 
 // Few kept rows, or f32: tiles of 256 columns of H x BN rows of G over a split of the piece, one a
 // workgroup. bf16 is bound by the read of W (64 rows x 4096 x 152000, G and this: 472 us), f32 by the matrix
-// cores (298 rows x 1016 x 32003: 197 us, 98 TFLOP/s).
+// cores (298 rows x 1016 x 32003: 182 us, 106 TFLOP/s, busy 0.76).
 template <typename T, int BN> using HiddenRing = GemmRing<T, kTile, BN, 1, true, false>;
 
 template <typename T, int BN>
@@ -987,7 +992,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_few_kernel(HiddenJ
 }
 
 // Tiles of 256 columns of H x 256 kept rows over a split of the piece, bf16. 4096 rows x 4096 x 151936:
-// 3.8 ms (1330 TFLOP/s); 1024 rows, 64 tiles in splits, 1.0 ms (1270).
+// 3.8 ms (1330 TFLOP/s); 1024 rows, 64 tiles in splits, 0.98 ms (1300).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(HiddenJob job) {
     typedef GemmStream<T, true, false, 32> Stream;  // (hidden_done: 32 stores)
@@ -1030,8 +1035,10 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
 
 // grad_hidden from the splits' sums, added in a fixed order (and from the two parts of G, `low` rows
 // apart); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per WAVES-th split.
-// Few rows leave few workgroups, and many splits a chain of loads: 7 rows x 72 in 256 splits, 31 us with 4
-// waves, 7 with 16; 1024 rows x 4096 in 12 splits, 43 us with 4 (bytes).
+// Bound by the latency of its loads: 1024 rows x 4096 in 4 splits, 37 us (75 MB, 2.0 TB/s). Few rows leave few
+// workgroups, and many splits a chain of loads; the calls for grad_hidden with 16 waves and with 4: 7 rows x 72 in
+// 256 splits, 29 us and 33; 40 x 256 x 50000, 38 and 41; 64 x 1024 x 50000 in 64, 62 and 63; 64 x 2048 in 32, 92
+// and 91; below that 4 are as fast or faster (331 x 1016 x 32003, f32: 385 us, with 16 waves 388).
 template <typename T, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave) void lmloss_hidden_out_kernel(
     const float *sums, int splits, int rows, int low, const int32_t *count, int width,
@@ -1083,7 +1090,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_rows(const WeightJob &j
 }
 
 // f32: tiles of 256 columns of H x 128 vocabulary rows, over the kept rows; one a workgroup. 298 rows x 1016
-// x 32003: 195 us, 99 TFLOP/s (10 K steps a tile, whose end no product covers).
+// x 32003: 181 us, 107 TFLOP/s, busy 0.74 (10 K steps a tile, whose end no product covers).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob job) {
     typedef GemmTile<T, kTile, 128, true, true, 4> Tile;
@@ -1112,7 +1119,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
 }
 
 // bf16, more rows than that: tiles of 256 columns of H x 256 vocabulary rows. 4096 rows x 4096 x 151936: 3.86
-// ms (1320 TFLOP/s); 1024 rows 1.1 ms (1150): of 16 K steps a tile, the end takes a sixth.
+// ms (1320 TFLOP/s); 1024 rows 1.15 ms (1100): of 16 K steps a tile, the end takes a sixth.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(WeightJob job) {
     typedef GemmStream<T, true, true, 16> Stream;
@@ -1155,7 +1162,7 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
 // keeps the kept rows' values at 64 columns of H as fragments, for a workgroup's 512, and goes through a
 // range of the vocabulary, 64 rows at a time: G's columns come through LDS, two buffers, and the output
 // goes through 4 KB of LDS, so that a store covers whole lines (128 bytes of each of 8 rows). 16 rows x
-// 4096 x 151936 (1.245 GB written): 231 us, 5.4 TB/s.
+// 4096 x 151936 (1.245 GB written): 231 us, 5.4 TB/s (a plain fill reaches 6.9).
 struct WeightFewJob {
     const uint16_t *rows;  // [count, H], or with `from` all rows
     const char *G;         // [grows][ldg], at most 64 STEPS rows

@@ -396,8 +396,9 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
  *                          inputs nor each other.)
  *   bf16: G is rounded to bf16 before the two products (of at most 64 rows it is kept in two bf16
  *   parts, 16 bits); everything else is fp32, rounded once.
- *   Rows without an entry, or without teacher mass: loss 0, gradient 0; their hidden states and
- *   grad_loss are not read (padding may hold anything) and cost nothing in the products. NaN, or
+ *   Rows without an entry, or without teacher mass: loss 0, gradient 0; their hidden states are not
+ *   read and their grad_loss counts for nothing (padding may hold anything, NaN too), and they cost
+ *   nothing in the products. NaN, or
  *   +inf among a row's logits, makes the row's loss NaN and its gradient NaN, and with it grad_W;
  *   a NaN or +inf teacher logit makes the loss NaN, and G at the row's entries.
  *   1 <= R <= DFLASH2_MAX_LMHEAD_LOSS_ROWS (call again for more: the losses are per row, grad_W adds
