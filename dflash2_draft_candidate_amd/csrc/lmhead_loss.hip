@@ -186,7 +186,7 @@ template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
     constexpr bool kForward = M != Rows::kStats;
     constexpr int kBlock = 16 * kWave;               // bytes of a row
-    constexpr int kAhead = ENTRIES == 1 ? 4 : 2;     // blocks asked for at once (8 and 4: 0 - 2 us more)
+    constexpr int kAhead = ENTRIES == 1 ? 4 : 2;     // blocks asked for at once (8 and 4: up to 8 us more)
     __shared__ int part[4];
     __shared__ __align__(16) char stage[kForward ? kGatherRows : 1][kForward ? (ENTRIES + 1) * kBlock : 16];
     const int lane = threadIdx.x % kWave;
@@ -415,7 +415,7 @@ __device__ __forceinline__ void logits_done(const LogitsJob &job, Tile &tile, in
 
 // Tiles of 256 vocabulary rows x 256 kept rows, bf16. Bound by the matrix cores at the clock that the
 // card's power leaves: 4096 rows x 4096 x 151936, forward 4.02 ms (1267 TFLOP/s); 1024 rows, 1.01 - 1.09 ms
-// (1180 - 1200: 2376 tiles are 9.3 rounds of the CUs).
+// (1170 - 1260: 2376 tiles are 9.3 rounds of the CUs).
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_logits_stream_kernel(LogitsJob job) {
     typedef typename std::conditional<GRAD, GradStream<T>, StatsStream<T>>::type Stream;
