@@ -379,6 +379,7 @@ template <typename T, int BM, int BN, bool AS, bool BS, int WM> struct GemmTile 
 struct GemmWork {
     GemmOperand a, b;
     int K;  // <= 0: no tile
+    bool more = false;  // a stream of PARTS: the next work's products are this tile's too
 };
 
 // RESERVE: bytes of LDS that are not the ring's.
@@ -494,7 +495,7 @@ template <typename T, int BM_, int BN, int SUB, bool AS, bool BS, int RESERVE = 
 //     the first six phases behind it, whose halves were asked for before them, do not wait for them.
 // 4096 x 4096 x 16384 bf16: 1314 TFLOP/s (KC x KC), 1319 (KS x KC), 1366 (KS x KS); one stage of
 // 64 KB ahead and a barrier per step (GemmTile): 1123, 1201, 1217.
-template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
+template <typename T, bool AS, bool BS, int kStores, bool PARTS = false> struct GemmStream {
     static constexpr int WM = 2, WN = 4, MI = 8, NI = 4, BM = 256, BN = 256, kCols = BN;
     typedef GemmSide<T, 128, AS, 64> SideA;
     typedef GemmSide<T, 128, BS, 32> SideB;
@@ -515,8 +516,8 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
         return ((K + kStepK - 1) / kStepK + 1) & ~1;
     }
 
-    // work(i): the workgroup's tile i, K = 0 behind the last; done(i): its epilogue, on acc.
-    // All tiles share the operands' ld.
+    // work(i): the workgroup's tile i (PARTS: or a part of its k), K = 0 behind the last; done(i): its epilogue,
+    // on acc. All tiles share the operands' ld.
     template <typename Work, typename Done>
     __device__ __forceinline__ void run(int64_t lda, int64_t ldb, Work work, Done done, char *lds,
                                         int wave, int lane) {
@@ -625,17 +626,24 @@ template <typename T, bool AS, bool BS, int kStores> struct GemmStream {
             multiply(1, 0, b0);
             bare_barrier();
         };
+        bool more = false;
         for (int i = 0;; ++i) {
             const int K = work(i).K;
             if (K <= 0) break;
+            if (!PARTS || !more) {
 #pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
+                for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-                for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
             for (int t = steps_of(K); t > 0; t -= 2) {
                 step(0, fb0, fbn);
                 step(1, fbn, fb0);
                 stored = false;
+            }
+            if constexpr (PARTS) {
+                more = work(i).more;
+                if (more) continue;
             }
             done(i);
             stored = true;

@@ -26,9 +26,10 @@
 //     by the matrix cores (and by the card's power). Fewer rows, f32, and logits of few such tiles:
 //     rings, which read W in tiles as narrow as the rows, or of 128 rows. At most 32 bf16 rows of
 //     1024 < H <= 4096: W in whole rows (lmhead_rows.h), bound by its bytes.
-//   * bf16: G is rounded to bf16 for the matrix cores (2^-8 of each entry, as a bf16 gradient of
-//     logits would be; kept in two parts for few rows); everything else is fp32. f32 inputs take the
-//     f32 matrix instructions throughout.
+//   * bf16: G is rounded to bf16 for the matrix cores (2^-8 of each value, as a bf16 gradient of logits
+//     would be). Up to 64 rows it is kept in two parts; above, what rounding left of it at the entries, its
+//     largest values, is added to both gradients. Everything else is fp32. f32 inputs take the f32 matrix
+//     instructions throughout.
 #include <type_traits>
 
 #include "dflash2.h"
@@ -116,6 +117,143 @@ __device__ __forceinline__ void wave_lds_order() {
     asm volatile("" ::: "memory");
 }
 
+// ---- the entries by columns ------------------------------------------------------------------------
+// G of more than 64 bf16 rows is in one bf16 part. Its largest values, and most of what their rounding costs the
+// gradients, are the entries' (q - p against a q): what rounding left of those is added to both gradients'
+// fp32 sums, to grad_hidden with the entry's row of W (lmloss_hidden_out_kernel), to grad_W with the
+// row's hidden state (add_listed). Entries of less than a 32nd of the row's largest mass are left as they are: even
+// 63 of them come to a quarter of that one's rounding (64 entries a row, as a teacher's top logits fall: a third of
+// them remain). For grad_W the entries are listed by units of 64 columns, in the order of the rows.
+// The gradients' error, relative and over all elements, with and without: 1024 rows x 4096 x 151936, 0.00167 and
+// 0.0024; rounded output alone 0.00166. It costs 1 - 2 % of a call with one entry a row (1024 rows: 4.23 ms and 4.31),
+// 5 % with 64 (4.29 and 4.51), more where the vocabulary is small (kMany).
+struct Listed {
+    uint32_t where;  // the row, the column in the unit << 16
+    int entry;       // of all rows' entries
+};
+static_assert(DFLASH2_MAX_LMHEAD_LOSS_ROWS <= 1 << 16, "Listed::where");
+constexpr int kUnit = 64, kListUnits = 16;  // columns; units a workgroup lists at most
+// From a quarter of the rows' number on (K entries a row of V / kMany columns) a unit's listed entries, 16 at a
+// time, take grad_W's tiles longer than a second part of G, all zeros but for the entries' rests. The backward call
+// with lists and with two parts: 2476 rows x 2592, 42 of 2575, 531 us and 335; 2048 x 512, 64 of 8000, 271 and 196;
+// 2476 x 2592, 42 of 10000, 654 and 631; 4096 x 1024, 8 of 2048, 296 and 277, 4 of 2048, 246 and 274; 1024 x 4096,
+// 64 of 16000, 562 and 565, of 40000, 1114 and 1231 (none of it kept: 233, 131, 443, 190, 189, 406 and 915).
+constexpr int kMany = 256;
+
+struct ListedRest {
+    const Listed *list;
+    const int2 *units;       // a unit's first entry in the list, and behind its last
+    const float *left;       // [R, K] what rounding left of G (entries that are none, rows left out: anything)
+    const uint16_t *hidden;  // [R, H], all rows
+};
+
+constexpr float kLn32 = 3.4657359f;  // (a 32nd of the largest mass)
+
+struct ListsJob {
+    const int32_t *ids;
+    const uint64_t *mask;  // null: all; a row's entries of a 32nd of its largest mass and more
+    int n, K, V;           // entries of all rows
+    uint32_t inverse;      // 2^32 / K rounded up; K = 1: 0
+    int per, groups;       // units a workgroup lists, workgroups
+    Listed *list;
+    int2 *units;
+};
+
+// A workgroup lists the entries of `per` units: it counts them, and those before its units (where its part of the
+// list starts), and puts them there. Each wave takes a contiguous part of the entries; what it has found waits
+// in LDS (of more than kWaiting it goes through all entries again).
+template <int THREADS> struct Lists {
+    static constexpr int kWaves = THREADS / kWave, kAhead = 8, kWaiting = 256;
+    struct Waiting {
+        int entry, column;
+    };
+    struct Lds {
+        Waiting waiting[kWaves][kWaiting];
+        int count[kWaves][kListUnits], total[kListUnits], before[kWaves];
+    };
+
+    static __device__ __forceinline__ void run(const ListsJob &job, int block, Lds &lds, int wave, int lane) {
+        const int first = block * job.per * kUnit, end = min(first + job.per * kUnit, job.V);
+        const int e0 = (int)((int64_t)job.n * wave / kWaves), e1 = (int)((int64_t)job.n * (wave + 1) / kWaves);
+        const uint64_t below = (1ull << lane) - 1;
+        // (exact below 2^22, and there are not more)
+        const auto row_of = [&](int e) { return job.inverse ? (int)__umulhi((uint32_t)e, job.inverse) : e; };
+        // f(entry, column, whether it is listed here, whether before) for a wave's entries, 64 at a time
+        const auto each = [&](auto f) {
+            for (int base = e0; base < e1; base += kAhead * kWave) {
+                int id[kAhead];
+                uint64_t takes[kAhead];
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const int e = min(base + a * kWave + lane, e1 - 1), r = row_of(e);
+                    id[a] = job.ids[e];
+                    takes[a] = job.mask ? job.mask[r] >> (e - r * job.K) : 1ull;
+                }
+                __builtin_amdgcn_sched_barrier(0);  // (all loads at once)
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const int e = base + a * kWave + lane;
+                    if (e >= e1) id[a] = -1;
+                    f(e, id[a] - first, id[a] >= first && id[a] < end && (takes[a] & 1ull) != 0ull,
+                      id[a] >= 0 && id[a] < first);
+                }
+            }
+        };
+        // g(unit, the lanes whose entries are listed in it, in one of these) for each unit among them
+        const auto each_unit = [&](int column, bool in, auto g) {
+            const int unit = column / kUnit;
+            for (uint64_t m = __ballot(in); m != 0ull;) {
+                const int u = __builtin_amdgcn_readlane(unit, __builtin_ctzll(m));
+                const uint64_t same = __ballot(in && unit == u);
+                g(u, same, in && unit == u);
+                m &= ~same;
+            }
+        };
+        int mine = 0, earlier = 0, found = 0;  // mine: lane u: entries of unit u
+        each([&](int e, int column, bool in, bool is_before) {
+            earlier += __popcll(__ballot(is_before));
+            const uint64_t m = __ballot(in);
+            if (m == 0ull) return;
+            const int at = found + __popcll(m & below);
+            if (in && at < kWaiting) lds.waiting[wave][at] = Waiting{e, column};
+            found += __popcll(m);
+            each_unit(column, in, [&](int u, uint64_t same, bool) { mine += lane == u ? __popcll(same) : 0; });
+        });
+        if (lane < kListUnits) lds.count[wave][lane] = mine;
+        if (lane == 0) lds.before[wave] = earlier;
+        __syncthreads();
+        if (threadIdx.x < kListUnits) {
+            int n = 0;
+            for (int w = 0; w < kWaves; ++w) n += lds.count[w][threadIdx.x];
+            lds.total[threadIdx.x] = n;
+        }
+        __syncthreads();
+        int at = 0;  // lane u: where the wave's next entry of unit u goes
+        if (lane < kListUnits) {
+            for (int w = 0; w < kWaves; ++w) at += lds.before[w];
+            for (int u = 0; u < lane; ++u) at += lds.total[u];
+            if (wave == 0 && lane < job.per) job.units[block * job.per + lane] = int2{at, at + lds.total[lane]};
+            for (int w = 0; w < wave; ++w) at += lds.count[w][lane];
+        }
+        const auto put = [&](int e, int column, bool in) {
+            each_unit(column, in, [&](int u, uint64_t same, bool here) {
+                const int to = __shfl(at, u, kWave) + __popcll(same & below);
+                if (here)
+                    job.list[to] = Listed{(uint32_t)row_of(e) | (uint32_t)(column % kUnit) << 16, e};
+                if (lane == u) at += __popcll(same);
+            });
+        };
+        if (found <= kWaiting) {
+            for (int i = 0; i < found; i += kWave) {
+                const Waiting x = lds.waiting[wave][min(i + lane, found - 1)];
+                put(x.entry, x.column, i + lane < found);
+            }
+        } else {
+            each([&](int e, int column, bool in, bool) { put(e, column, in); });
+        }
+    }
+};
+
 // ---- rows with an entry ------------------------------------------------------------------------
 
 // flags[r] = whether row r has an entry with mass (or NaN). One wave per row.
@@ -129,20 +267,18 @@ __global__ __launch_bounds__(256) void lmloss_flags_kernel(Entries e, int R, int
     if (j == 0) flags[r] = has ? 1 : 0;
 }
 
-enum class Rows { kTargets, kEntries, kFlags, kStats };
+enum class Rows { kTargets, kEntries, kFlags };
 
 struct GatherJob {
     const char *hidden;   // [R, H]
-    const char *W;        // [V, H] (forward: the entries' logits)
+    const char *W;        // [V, H]
     const int32_t *flags; // kFlags
-    float *stats;         // [R, K + 2]: forward: entries' logits out; kStats: in
-    const float *grad_loss;
+    float *stats;         // [R, K + 2]: entries' logits out
     Entries e;
     int R, H, V;
     char *rows;           // [R, H] the kept rows, behind one another
     int32_t *place;       // [R] where row r went, -1: left out
     int32_t *count;
-    float2 *scale;        // kStats: [kept rows] (max, g tau / sum)
 };
 
 constexpr int kGatherRows = 4;     // rows per workgroup, one a wave
@@ -170,10 +306,9 @@ __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
         return has != 0;
     }
     if constexpr (M == Rows::kFlags) return job.flags[r] != 0;
-    if constexpr (M == Rows::kStats) return !(job.stats[(int64_t)r * (job.e.K + 2) + 1] < 0.f);
 }
 
-// Workgroup (x, y): rows 4 x .. 4 x + 3; y = 0 copies them to their places, and (forward) each y
+// Forward. Workgroup (x, y): rows 4 x .. 4 x + 3; y = 0 copies them to their places, and each y
 // takes the logits of ENTRIES of the entries. A row's place is the number of kept rows before it,
 // which every workgroup of y = 0 counts for itself.
 // An entry's logit is the same fp32 number as in the row's maximum and sum: the same matrix
@@ -184,11 +319,10 @@ __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
 // of its instructions, 4 us for every 1024 of H (15 us of a call more at H = 4096 than a free order of sums).
 template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
-    constexpr bool kForward = M != Rows::kStats;
     constexpr int kBlock = 16 * kWave;               // bytes of a row
     constexpr int kAhead = ENTRIES == 1 ? 4 : 2;     // blocks asked for at once (8 and 4: up to 8 us more)
     __shared__ int part[4];
-    __shared__ __align__(16) char stage[kForward ? kGatherRows : 1][kForward ? (ENTRIES + 1) * kBlock : 16];
+    __shared__ __align__(16) char stage[kGatherRows][(ENTRIES + 1) * kBlock];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int first = blockIdx.x * kGatherRows, r = first + wave;
@@ -214,76 +348,125 @@ __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
     const int K = job.e.K;
     const int64_t row_bytes = (int64_t)job.H * sizeof(T);
     const char *src = job.hidden + r * row_bytes;
-    if constexpr (!kForward) {
-        char *dst = job.rows + before * row_bytes;
-        for (int64_t b = lane * 16; b < row_bytes; b += kWave * 16)
-            *reinterpret_cast<u32x4 *>(dst + b) = *reinterpret_cast<const u32x4 *>(src + b);
-        if (lane == 0) {
-            const float *st = job.stats + (int64_t)r * (K + 2);
-            job.scale[before] = float2{st[0], grad_scale(job.grad_loss[r], job.e.tau, st[1])};
+    char *dst = job.rows + before * row_bytes;
+    // (past the last entry, and for ids that are none: row 0, whose product nothing reads)
+    const int j0 = blockIdx.y * ENTRIES, n = min(ENTRIES, K - j0);
+    const char *w[ENTRIES];
+#pragma unroll
+    for (int e = 0; e < ENTRIES; ++e) {
+        const int id = e < n ? job.e.ids[(int64_t)r * K + j0 + e] : 0;
+        w[e] = job.W + (id_ok(id, job.V) ? id : 0) * row_bytes;
+    }
+    // LDS: 16-byte chunk c of entry e's block at c ^ e, behind them the hidden row's. Lane (g, j) of a
+    // step takes chunk g of its 64 bytes: of entry j (the rows of the instruction repeat them), of
+    // the hidden row in every column.
+    static_assert((ENTRIES & (ENTRIES - 1)) == 0 && ENTRIES <= 16, "rows of the instruction");
+    constexpr int kSteps = 4;  // whose fragments are read together
+    char *lds = stage[wave];
+    const int g = lane >> 4, m = lane % ENTRIES;
+    typedef typename GemmSide<T, kTile, false>::Frag Frag;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t b0 = 0; b0 < row_bytes; b0 += kAhead * kBlock) {
+        u32x4 h[kAhead], x[kAhead][ENTRIES];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {  // (zeros behind the row, as in the product)
+            const int64_t b = b0 + a * kBlock + lane * 16;
+            const bool in = b < row_bytes;
+            h[a] = in ? *reinterpret_cast<const u32x4 *>(src + b) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < ENTRIES; ++e)
+                x[a][e] = in ? *reinterpret_cast<const u32x4 *>(w[e] + b) : u32x4{0u, 0u, 0u, 0u};
         }
-        return;
-    } else {
-        char *dst = job.rows + before * row_bytes;
-        // (past the last entry, and for ids that are none: row 0, whose product nothing reads)
-        const int j0 = blockIdx.y * ENTRIES, n = min(ENTRIES, K - j0);
-        const char *w[ENTRIES];
 #pragma unroll
-        for (int e = 0; e < ENTRIES; ++e) {
-            const int id = e < n ? job.e.ids[(int64_t)r * K + j0 + e] : 0;
-            w[e] = job.W + (id_ok(id, job.V) ? id : 0) * row_bytes;
-        }
-        // LDS: 16-byte chunk c of entry e's block at c ^ e, behind them the hidden row's. Lane (g, j) of a
-        // step takes chunk g of its 64 bytes: of entry j (the rows of the instruction repeat them), of
-        // the hidden row in every column.
-        static_assert((ENTRIES & (ENTRIES - 1)) == 0 && ENTRIES <= 16, "rows of the instruction");
-        constexpr int kSteps = 4;  // whose fragments are read together
-        char *lds = stage[wave];
-        const int g = lane >> 4, m = lane % ENTRIES;
-        typedef typename GemmSide<T, kTile, false>::Frag Frag;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t b0 = 0; b0 < row_bytes; b0 += kAhead * kBlock) {
-            u32x4 h[kAhead], x[kAhead][ENTRIES];
+        for (int a = 0; a < kAhead; ++a) {
+            const int64_t left = row_bytes - (b0 + a * kBlock);
+            if (left <= 0) break;
+            if (copies && lane * 16 < left)
+                *reinterpret_cast<u32x4 *>(dst + b0 + a * kBlock + lane * 16) = h[a];
+            wave_lds_order();  // (the last block is read)
+            *reinterpret_cast<u32x4 *>(lds + ENTRIES * kBlock + lane * 16) = h[a];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {  // (zeros behind the row, as in the product)
-                const int64_t b = b0 + a * kBlock + lane * 16;
-                const bool in = b < row_bytes;
-                h[a] = in ? *reinterpret_cast<const u32x4 *>(src + b) : u32x4{0u, 0u, 0u, 0u};
+            for (int e = 0; e < ENTRIES; ++e)
+                *reinterpret_cast<u32x4 *>(lds + e * kBlock + ((lane ^ e) << 4)) = x[a][e];
+            wave_lds_order();
+            for (int s0 = 0; s0 < 16 && s0 * 64 < left; s0 += kSteps) {
+                Frag fw[kSteps], fh[kSteps];
 #pragma unroll
-                for (int e = 0; e < ENTRIES; ++e)
-                    x[a][e] = in ? *reinterpret_cast<const u32x4 *>(w[e] + b) : u32x4{0u, 0u, 0u, 0u};
-            }
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int64_t left = row_bytes - (b0 + a * kBlock);
-                if (left <= 0) break;
-                if (copies && lane * 16 < left)
-                    *reinterpret_cast<u32x4 *>(dst + b0 + a * kBlock + lane * 16) = h[a];
-                wave_lds_order();  // (the last block is read)
-                *reinterpret_cast<u32x4 *>(lds + ENTRIES * kBlock + lane * 16) = h[a];
-#pragma unroll
-                for (int e = 0; e < ENTRIES; ++e)
-                    *reinterpret_cast<u32x4 *>(lds + e * kBlock + ((lane ^ e) << 4)) = x[a][e];
-                wave_lds_order();
-                for (int s0 = 0; s0 < 16 && s0 * 64 < left; s0 += kSteps) {
-                    Frag fw[kSteps], fh[kSteps];
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        const int c = 4 * (s0 + s) + g;
-                        fw[s] = *reinterpret_cast<const Frag *>(lds + m * kBlock + ((c ^ m) << 4));
-                        fh[s] = *reinterpret_cast<const Frag *>(lds + ENTRIES * kBlock + (c << 4));
-                    }
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) sum = gemm_mfma(fw[s], fh[s], sum);
+                for (int s = 0; s < kSteps; ++s) {
+                    const int c = 4 * (s0 + s) + g;
+                    fw[s] = *reinterpret_cast<const Frag *>(lds + m * kBlock + ((c ^ m) << 4));
+                    fh[s] = *reinterpret_cast<const Frag *>(lds + ENTRIES * kBlock + (c << 4));
                 }
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) sum = gemm_mfma(fw[s], fh[s], sum);
             }
         }
-        // lane (g, j) holds entries 4 g .. 4 g + 3
-        if (lane % 16 == 0) {
+    }
+    // lane (g, j) holds entries 4 g .. 4 g + 3
+    if (lane % 16 == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (4 * g + i < n) job.stats[(int64_t)r * (K + 2) + 2 + j0 + 4 * g + i] = sum[i];
-        }
+        for (int i = 0; i < 4; ++i)
+            if (4 * g + i < n) job.stats[(int64_t)r * (K + 2) + 2 + j0 + 4 * g + i] = sum[i];
+    }
+}
+
+struct KeepJob {
+    const char *hidden;  // [R, H]
+    const float *stats;  // [R, K + 2]
+    const float *grad_loss;
+    int R, H, K;
+    float tau;
+    char *rows;          // as GatherJob's
+    int32_t *place, *count;
+    float2 *scale;       // [kept rows] (max, g tau / sum)
+    const int32_t *ids;  // with mask: [R, K]
+    const float *teacher;
+    int V;
+    uint64_t *mask;      // null, or out: ListsJob's
+};
+constexpr int kKeepThreads = 1024, kKeepRows = kKeepThreads / kWave;
+
+// Backward: the kept rows to their places, by the forward call's statistics, a wave per row.
+template <typename T>
+__global__ __launch_bounds__(kKeepThreads) void lmloss_keep_kernel(KeepJob job) {
+    __shared__ int part[kKeepRows];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const auto kept = [&](int r) { return !(job.stats[(int64_t)r * (job.K + 2) + 1] < 0.f); };
+    const int first = blockIdx.x * kKeepRows, r = first + wave;
+    int n = 0;
+    for (int i = threadIdx.x; i < first; i += kKeepThreads) n += kept(i) ? 1 : 0;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d, kWave);
+    if (lane == 0) part[wave] = n;
+    const uint64_t keeps = __ballot(lane < kKeepRows && first + lane < job.R && kept(min(first + lane, job.R - 1)));
+    __syncthreads();
+    if (r >= job.R) return;
+    int before = __popcll(keeps & ((1ull << wave) - 1));
+#pragma unroll
+    for (int w = 0; w < kKeepRows; ++w) before += part[w];
+    const bool is_kept = (keeps >> wave) & 1ull;
+    if (lane == 0) {
+        job.place[r] = is_kept ? before : -1;
+        if (r == job.R - 1) *job.count = before + (is_kept ? 1 : 0);
+    }
+    if (job.mask) {
+        const int64_t at = (int64_t)r * job.K + min(lane, job.K - 1);
+        const bool ok = lane < job.K && id_ok(job.ids[at], job.V);
+        const float t = ok ? job.teacher[at] : -INFINITY, least = wave_max(t, lane) - job.tau * kLn32;
+        const uint64_t takes = __ballot(is_kept && ok && t >= least);
+        if (lane == 0) job.mask[r] = takes;
+    }
+    if (!is_kept) return;
+    const int64_t row_bytes = (int64_t)job.H * sizeof(T);
+    const char *src = job.hidden + r * row_bytes;
+    char *dst = job.rows + before * row_bytes;
+#pragma unroll 4
+    for (int64_t b = lane * 16; b < row_bytes; b += kWave * 16)
+        *reinterpret_cast<u32x4 *>(dst + b) = *reinterpret_cast<const u32x4 *>(src + b);
+    if (lane == 0) {
+        const float *st = job.stats + (int64_t)r * (job.K + 2);
+        job.scale[before] = float2{st[0], grad_scale(job.grad_loss[r], job.tau, st[1])};
     }
 }
 
@@ -835,21 +1018,40 @@ struct EntriesJob {
     void *G;
     int64_t ldg;
     int low;
-    float *rest;  // [R, K] or null: what rounding to bf16 left of G at the entries (Listed)
+    float *rest;           // [R, K] or null: ListedRest::left
+    const uint64_t *mask;  // as ListsJob's
+    int groups;            // workgroups of 16 rows; those behind them make the lists
+    ListsJob lists;
 };
+
+__global__ __launch_bounds__(256) void lmloss_zero_kernel(u32x4 *p, int64_t n) {
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256)
+        p[i] = u32x4{0u, 0u, 0u, 0u};
+}
 
 // One wave per row: G at the row's entries, the masses of equal ids added in their order. f32: taken from
 // what the product has written; bf16: from the kept logit, rounded once. Either way the logit is the
-// one in the row's sum, so q - 1 of a sure row keeps its digits. 5 us for 1024 rows of one entry, 10 of 64.
+// one in the row's sum, so q - 1 of a sure row keeps its digits. The first piece's launch makes the lists of the
+// entries by columns too, in workgroups of their own. 1024 rows: 5 us of one entry, 10 of 64; with the lists 6 and 34.
 template <typename T>
-__global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
-    const int r = blockIdx.x * 4 + threadIdx.x / kWave, lane = threadIdx.x % kWave;
+__global__ __launch_bounds__(kKeepThreads) void lmloss_entries_kernel(EntriesJob job) {
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if constexpr (sizeof(T) == 2) {
+        typedef Lists<kKeepThreads> Listing;
+        __shared__ typename Listing::Lds lds;
+        if ((int)blockIdx.x >= job.groups) {
+            Listing::run(job.lists, blockIdx.x - job.groups, lds, wave, lane);
+            return;
+        }
+    }
+    const int r = blockIdx.x * kKeepRows + wave;
     if (r >= job.R) return;
     const int p = job.place[r];
-    if (p < 0) return;
     const int K = job.e.K;
     const int id = lane < K ? job.e.ids[(int64_t)r * K + lane] : -1;
-    const bool ok = id_ok(id, job.V);
+    const bool ok = id_ok(id, job.V), in_piece = ok && id >= job.v0 && id < job.v1;
+    if (p < 0) return;
     float mass = 1.f;
     if (job.e.teacher) {
         const float t = ok ? job.e.teacher[(int64_t)r * K + lane] : -INFINITY;
@@ -868,7 +1070,7 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
             earlier |= j < lane;
         }
     }
-    if (!ok || id < job.v0 || id >= job.v1) return;
+    if (!in_piece) return;
     if (earlier) {
         if (sizeof(T) == 2 && job.rest) job.rest[(int64_t)r * K + lane] = 0.f;
         return;
@@ -888,146 +1090,92 @@ __global__ __launch_bounds__(256) void lmloss_entries_kernel(EntriesJob job) {
         *reinterpret_cast<__bf16 *>(out) = (__bf16)y;
         if (job.low) *reinterpret_cast<__bf16 *>(out + job.low * job.ldg) = (__bf16)(y - high);
         // (nothing is added to what is infinite or NaN already)
-        if (job.rest) job.rest[(int64_t)r * K + lane] = fabsf(high) < INFINITY ? y - high : 0.f;
+        if (job.rest) {
+            const bool takes = !job.mask || ((job.mask[r] >> lane) & 1ull) != 0ull;
+            job.rest[(int64_t)r * K + lane] = takes && fabsf(high) < INFINITY ? y - high : 0.f;
+        }
     } else {
         *out = y;
     }
 }
 
 // ---- what rounding left of the entries ---------------------------------------------------------------
-// G of more than 64 bf16 rows is in one bf16 part. Its largest values, and most of what their rounding costs the
-// gradients, are the entries' (q - p against a q): what rounding left of those is added to both gradients'
-// fp32 sums, to grad_hidden with the entry's row of W (lmloss_hidden_out_kernel), to grad_W with the
-// row's hidden state. For the latter the entries are listed by units of 64 columns, in the order of the
-// rows. The gradients' error, relative and over all elements, with and without: 1024 rows x 4096 x 151936, 0.00167
-// and 0.0024; rounded output alone 0.00166.
-struct Listed {
-    uint32_t where;  // the row's place, the column in the unit << 16
-    float rest;
-};
-static_assert(DFLASH2_MAX_LMHEAD_LOSS_ROWS <= 1 << 16, "Listed::where");
-constexpr int kUnit = 64, kListUnits = 16, kListThreads = 1024;
-
-struct ListsJob {
-    const int32_t *ids, *place;
-    const float *rest;
-    int n, K, v0, v1;  // entries of all rows
-    Listed *list;
-    int2 *units;       // a unit's first entry in the list, and behind its last
-};
-
-// A workgroup lists the entries of 16 units: it counts them, and those of the piece before its units (where
-// its part of the list starts), and goes through all entries again to put them there. Each wave takes a
-// contiguous part of the entries.
-__global__ __launch_bounds__(kListThreads) void lmloss_lists_kernel(ListsJob job) {
-    constexpr int kWaves = kListThreads / kWave, kAhead = 8;
-    __shared__ int count[kWaves][kListUnits], total[kListUnits], before[kWaves];
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int first = job.v0 + blockIdx.x * kListUnits * kUnit;
-    const int end = min(first + kListUnits * kUnit, job.v1);
-    const int e0 = (int)((int64_t)job.n * wave / kWaves), e1 = (int)((int64_t)job.n * (wave + 1) / kWaves);
-    // f(entry, id, whether it is listed here) for a wave's entries, 64 at a time
-    const auto each = [&](auto f) {
-        for (int base = e0; base < e1; base += kAhead * kWave) {
-            int id[kAhead];
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int e = base + a * kWave + lane;
-                id[a] = e < e1 ? job.ids[e] : -1;
-            }
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int e = base + a * kWave + lane;
-                bool in = id[a] >= first && id[a] < end;
-                if (in) in = job.place[e / job.K] >= 0 && job.rest[e] != 0.f;
-                f(e, id[a], in);
-            }
-        }
-    };
-    // g(unit, the lanes whose entries are listed in it, in one of these) for each unit among them
-    const auto each_unit = [&](int id, bool in, auto g) {
-        const int unit = (id - first) / kUnit;
-        for (uint64_t m = __ballot(in); m != 0ull;) {
-            const int u = __builtin_amdgcn_readlane(unit, __builtin_ctzll(m));
-            const uint64_t same = __ballot(in && unit == u);
-            g(u, same, in && unit == u);
-            m &= ~same;
-        }
-    };
-    if (lane < kListUnits) count[wave][lane] = 0;
-    int earlier = 0;
-    each([&](int, int id, bool in) {
-        earlier += __popcll(__ballot(id >= job.v0 && id < first));
-        each_unit(id, in, [&](int u, uint64_t same, bool) {
-            if (lane == 0) count[wave][u] += __popcll(same);
-        });
-    });
-    if (lane == 0) before[wave] = earlier;
-    __syncthreads();
-    if (threadIdx.x < kListUnits) {
-        int n = 0;
-        for (int w = 0; w < kWaves; ++w) n += count[w][threadIdx.x];
-        total[threadIdx.x] = n;
-    }
-    __syncthreads();
-    int at = 0;  // lane u: where the wave's next entry of unit u goes
-    if (lane < kListUnits) {
-        for (int w = 0; w < kWaves; ++w) at += before[w];
-        for (int u = 0; u < lane; ++u) at += total[u];
-        if (wave == 0) job.units[blockIdx.x * kListUnits + lane] = int2{at, at + total[lane]};
-        for (int w = 0; w < wave; ++w) at += count[w][lane];
-    }
-    each([&](int e, int id, bool in) {
-        each_unit(id, in, [&](int u, uint64_t same, bool mine) {
-            const int to = __shfl(at, u, kWave);
-            if (mine)
-                job.list[to + __popcll(same & ((1ull << lane) - 1))] =
-                    Listed{(uint32_t)job.place[e / job.K] | (uint32_t)((id - first) % kUnit) << 16,
-                           job.rest[e]};
-            if (lane == u) at += __popcll(same);
-        });
-    });
-}
 
 // Adds a unit's listed entries to a wave's part of grad_W: acc[mi][ni][i] is column h0 + 16 mi + 4 g + i of the
-// unit's row c0 + 16 ni + j. 16 entries at a time as a product of their hidden states and what is left of G.
-// Offset: of bytes in `rows` (32 bits where they reach, for the registers).
-template <typename Offset, int MI, int NI>
-__device__ __forceinline__ void add_listed(f32x4 (&acc)[MI][NI], const Listed *list, const int2 *units,
-                                           int unit, int c0, const uint16_t *rows, int H, int h0, int lane) {
-    const int2 range = units[__builtin_amdgcn_readfirstlane(unit)];
-    const int g = lane >> 4, j = lane & 15;
-    for (int e = range.x; e < range.y; e += 16) {
-        Offset row[4];
-        int column[4];
-        float rest[4];
+// unit's row c0 + 16 ni + j. 16 entries at a time as a product of their hidden states and what is left of G, with
+// the next 16's loads and the places of those behind them on their way. scratch: 16 rows of 16 MI columns of
+// hidden in LDS (16-byte chunk c of row k at c ^ k), the wave's own, which transposing reads take them from.
+template <int MI, int NI>
+__device__ __forceinline__ void add_listed(f32x4 (&acc)[MI][NI], const ListedRest &rest, int unit, int c0, int H,
+                                           int h0, char *scratch, int lane) {
+    constexpr int kChunks = 2 * MI, kRows = 16 / kChunks, kLoads = 4 / kRows;  // of a row; of lanes' 4 rows
+    const int2 range = rest.units[__builtin_amdgcn_readfirstlane(unit)];
+    if (range.x >= range.y) return;
+    const int g = lane >> 4, j = lane & 15, chunk = j % kChunks, sub = j / kChunks;
+    const int column = min(h0 + 8 * chunk, H - 8);
+    const int k_put = 4 * g + sub, k_get = 4 * g + (j >> 2);
+    Listed x[4];
+    u32x4 h[kLoads];
+    float left[4];
+    int at[4];  // columns
+    const auto places = [&](int e) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // (behind the last: its row, of which nothing is left)
-            const int at = e + 4 * g + i;
-            const Listed x = list[min(at, range.y - 1)];
-            row[i] = (Offset)(x.where & 0xFFFFu) * (Offset)(2 * H);
-            column[i] = (int)(x.where >> 16) - c0;
-            rest[i] = at < range.y ? x.rest : 0.f;
+        for (int i = 0; i < 4; ++i) x[i] = rest.list[(uint32_t)min(e + 4 * g + i, range.y - 1)];
+    };
+    const auto load = [&](int e) {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const uint32_t where = sub == 0 ? x[q * kRows].where : x[q * kRows + kRows - 1].where;
+            h[q] = *reinterpret_cast<const u32x4 *>(rest.hidden + (int64_t)(where & 0xFFFFu) * H + column);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            left[i] = rest.left[(uint32_t)x[i].entry];
+            at[i] = e + 4 * g + i < range.y ? (int)(x[i].where >> 16) - c0 : -1;
+        }
+    };
+    places(range.x);
+    load(range.x);
+    places(range.x + 16);
+    for (int e = range.x; e < range.y; e += 16) {
+        wave_lds_order();
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int k = k_put + q * kRows;
+            *reinterpret_cast<u32x4 *>(scratch + k * (kChunks * 16) + ((chunk ^ (k % kChunks)) << 4)) = h[q];
         }
         s16x4 b[NI];
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                b[ni][i] = __builtin_bit_cast(short, (__bf16)(column[i] == 16 * ni + j ? rest[i] : 0.f));
+                b[ni][i] = __builtin_bit_cast(short, (__bf16)(at[i] == 16 * ni + j ? left[i] : 0.f));
+        wave_lds_order();
+        __builtin_amdgcn_sched_barrier(0);
+        if (e + 16 < range.y) {  // (on their way during the products)
+            load(e + 16);
+            places(e + 32);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
-            s16x4 a;
+        for (int m0 = 0; m0 < MI; m0 += 4) {
+            s16x4 a[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = *reinterpret_cast<const short *>(reinterpret_cast<const char *>(rows) + row[i] +
-                                                        (Offset)(2 * min(h0 + 16 * mi + j, H - 1)));
+            for (int mi = 0; mi < 4; ++mi) {
+                const int c = 2 * (m0 + mi) + ((j & 3) >> 1);
+                a[mi] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(
+                    scratch + k_get * (kChunks * 16) + ((c ^ (k_get % kChunks)) << 4) + 8 * (j & 1)));
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int ni = 0; ni < NI; ++ni)
-                acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b[ni], acc[mi][ni], 0, 0, 0);
+            for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni)
+                    acc[m0 + mi][ni] =
+                        __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a[mi], b[ni], acc[m0 + mi][ni], 0, 0, 0);
         }
     }
+    wave_lds_order();
 }
 
 // ---- the gradients' products -----------------------------------------------------------------------
@@ -1192,8 +1340,20 @@ __global__ __launch_bounds__(WAVES * kWave) void lmloss_hidden_out_kernel(
         splits = nr > 0 ? stream_splits(nh * nr, width) : 0;
         rows = nr * kTile;
     }
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = blockIdx.x, p = place[r], h = (blockIdx.y * kWave + lane) * 4;
+    // the entries of which something is left, every WAVES-th to a wave
+    int id = -1;
+    float left = 0.f;
+    uint64_t mine = 0ull;
+    if (sizeof(T) == 2 && rest && p >= 0) {
+        const int64_t at = (int64_t)r * e.K + min(lane, e.K - 1);
+        id = lane < e.K ? e.ids[at] : -1;
+        left = rest[at];
+        const bool some = id_ok(id, V) && left != 0.f;
+        mine = __ballot(some && __popcll(__ballot(some) & ((1ull << lane) - 1)) % WAVES == wave);
+    }
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (p >= 0 && h < H) {
         const auto add = [&](int row) {
@@ -1203,19 +1363,24 @@ __global__ __launch_bounds__(WAVES * kWave) void lmloss_hidden_out_kernel(
         };
         add(p);
         if (low) add(p + low);
-        if constexpr (sizeof(T) == 2) {
-            if (rest) {
-#pragma unroll 4
-                for (int j = wave; j < e.K; j += WAVES) {
-                    const int64_t at = (int64_t)r * e.K + j;
-                    const int id = e.ids[at];
-                    const float left = id_ok(id, V) ? rest[at] : 0.f;
-                    if (left == 0.f) continue;
-                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                    const u32x2 w = *reinterpret_cast<const u32x2 *>(W + (int64_t)id * H + h);
-                    x += left * f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-                }
+        while (sizeof(T) == 2 && mine != 0ull) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            constexpr int kAhead = 4;
+            u32x2 w[kAhead];
+            float of[kAhead];
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n) {  // (behind the last: the first row, for nothing)
+                const int j = mine != 0ull ? __builtin_ctzll(mine) : 0;
+                const int v = mine != 0ull ? __builtin_amdgcn_readlane(id, j) : 0;
+                const uint32_t bits = __builtin_amdgcn_readlane(__float_as_uint(left), j);
+                of[n] = mine != 0ull ? __uint_as_float(bits) : 0.f;
+                w[n] = *reinterpret_cast<const u32x2 *>(W + (int64_t)v * H + h);
+                if (mine == 0ull) w[n] = u32x2{0u, 0u};
+                mine &= mine - 1ull;
             }
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n)
+                x += of[n] * f32x4{bf16_lo(w[n].x), bf16_hi(w[n].x), bf16_lo(w[n].y), bf16_hi(w[n].y)};
         }
     }
     if (wave > 0) part[wave][lane] = x;
@@ -1236,8 +1401,8 @@ struct WeightJob {
     int64_t ldg;
     int nh, nv;
     void *grad;          // [V, H]
-    const Listed *list;  // and units: null, or what rounding left of G's entries
-    const int2 *units;
+    ListedRest rest;     // bf16 in one part
+    int low;             // bf16, many entries: the row of G where what rounding left of row 0 stands, or 0
 };
 
 template <typename T>
@@ -1277,20 +1442,20 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
     }
 }
 
-// bf16, more rows than that: tiles of 256 columns of H x 256 vocabulary rows. 4096 rows x 4096 x 151936: 3.86
+// bf16, more rows than that, or many entries: tiles of 256 columns of H x 256 vocabulary rows. 4096 rows x 4096 x 151936: 3.86
 // ms (1320 TFLOP/s); 1024 rows 1.15 ms (1100): of 16 K steps a tile, the end takes a sixth.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(WeightJob job) {
-    typedef GemmStream<T, true, true, 16> Stream;
+    typedef GemmStream<T, true, true, 16, true> Stream;
     static_assert(Stream::kRowStores == 16, "the stores a tile's end makes");
     __shared__ __align__(1024) char lds[Stream::kLdsBytes];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     // (without a kept row the products are over a row of zeros)
-    const int R = *job.count, K = max(R, 1), tiles = job.nh * job.nv;
+    const int R = *job.count, K = max(R, 1), tiles = job.nh * job.nv, parts = job.low ? 2 : 1;
     const int64_t ldh = (int64_t)job.H * sizeof(T), ldg = job.ldg * (int64_t)sizeof(T);
     auto place = [&](int i, int &h0, int &v0) {
-        const int id = blockIdx.x + i * gridDim.x;
+        const int id = blockIdx.x + i / parts * gridDim.x;
         if (id >= tiles) return false;
         int tm, tn;
         gemm_place(id, job.nh, job.nv, kPlaceGroup, tm, tn);
@@ -1304,17 +1469,19 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(Weig
         [&](int i) -> GemmWork {
             int h0, v0;
             if (!place(i, h0, v0)) return {{job.rows, ldh, 0}, {job.G, ldg, 0}, 0};
-            GemmWork w = {operand_ks<T>(job.rows, ldh, h0, 0), operand_ks<T>(job.G, ldg, v0, 0), K};
+            const int low = i % parts;
+            GemmWork w = {operand_ks<T>(job.rows, ldh, h0, 0), operand_ks<T>(job.G, ldg, v0, low * job.low), K};
+            w.more = parts == 2 && low == 0;
             if (R == 0) w.a.valid = w.b.valid = 1 << 30;  // (past every row: nothing is read)
             return w;
         },
         [&](int i) {
             int h0 = 0, v0 = 0;
             place(i, h0, v0);
-            const int column = v0 + Stream::wave_n(wave);
-            add_listed<uint64_t>(stream.acc, job.list, job.units, column / kUnit, column % kUnit,
-                                 reinterpret_cast<const T *>(job.rows), job.H, h0 + Stream::wave_m(wave),
-                                 anew(lane));
+            static_assert(Stream::BN / Stream::WN == kUnit, "a wave's columns");
+            if (!job.low) add_listed(stream.acc, job.rest, (job.v0 + v0 + Stream::wave_n(wave)) / kUnit, 0, job.H,
+                       h0 + Stream::wave_m(wave), lds + Stream::kStageBytes + wave * Stream::kScratch,
+                       anew(lane));
             stream.store_rows(weight_rows<T>(job, v0, kTile), (int)ldh, h0 * 2, (int)ldh, lds, wave, lane,
                               [&](int mi, int ni) { return stream.acc[mi][ni]; });
         },
@@ -1335,8 +1502,7 @@ struct WeightFewJob {
     int64_t ldg;
     int slabs, ranges;     // of 512 columns of H; of the vocabulary, a multiple of 8
     uint16_t *grad;        // [V, H]
-    const Listed *list;    // more than one step and G in one part
-    const int2 *units;
+    ListedRest rest;       // more than one step and G in one part
 };
 
 // TWO: G in two parts of 32 STEPS rows, which meet the same rows of hidden.
@@ -1425,42 +1591,49 @@ __device__ __forceinline__ void weight_few(const WeightFewJob &job, int block, c
         const int v = job.v0 + u * 64;
         const __amdgpu_buffer_rsrc_t out =
             out_rows(reinterpret_cast<char *>(job.grad) + (int64_t)v * ld, ld, min(job.v1 - v, 64), ld);
+        // (of two steps in one part: all four 16 columns at once, so that listed entries are added once)
+        constexpr bool kListed = STEPS > 1 && !TWO;
+        constexpr int kOnce = STEPS == 2 && !TWO ? 4 : 2;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            f32x4 acc[4][2];
+        for (int n0 = 0; n0 < 4; n0 += kOnce) {
+            f32x4 acc[4][kOnce];
 #pragma unroll
             for (int mi = 0; mi < 4; ++mi)
 #pragma unroll
-                for (int ni = 0; ni < 2; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int ni = 0; ni < kOnce; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < 2 * STEPS; ++s)
 #pragma unroll
-                for (int ni = 0; ni < 2; ++ni) {
-                    const bf16x8 fb =
-                        rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, 2 * half + ni, s % 2);
+                for (int ni = 0; ni < kOnce; ++ni) {
+                    const bf16x8 fb = rb.read(lds + buf * kBuffer + (s / 2) * Side::kBytes, n0 + ni, s % 2);
 #pragma unroll
                     for (int mi = 0; mi < 4; ++mi)
                         acc[mi][ni] = gemm_mfma(fa[s % kHeld][mi], fb, acc[mi][ni]);
                 }
-            if constexpr (STEPS > 1 && !TWO)
-                add_listed<uint32_t>(acc, job.list, job.units, u, 32 * half, job.rows, job.H, h0, anew(lane));
+            if constexpr (kListed)
+                add_listed(acc, job.rest, job.v0 / kUnit + u, 16 * n0, job.H, h0, scratch, anew(lane));
 #pragma unroll
-            for (int ni = 0; ni < 2; ++ni)
+            for (int half = 0; half < kOnce / 2; ++half) {
 #pragma unroll
-                for (int mi = 0; mi < 4; ++mi) {
-                    const auto x = packed4<T>(acc[mi][ni]);
-                    const int row = 16 * ni + j;
-                    *reinterpret_cast<decltype(packed4<T>(f32x4{})) *>(
-                        scratch + row * 128 + (((2 * mi + (g >> 1)) ^ (row & 7)) << 4) + (g & 1) * 8) = x;
+                for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+                    for (int mi = 0; mi < 4; ++mi) {
+                        const auto x = packed4<T>(acc[mi][2 * half + ni]);
+                        const int row = 16 * ni + j;
+                        *reinterpret_cast<decltype(packed4<T>(f32x4{})) *>(
+                            scratch + row * 128 + (((2 * mi + (g >> 1)) ^ (row & 7)) << 4) + (g & 1) * 8) = x;
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int row = 8 * q + row_in;
+                    const u32x4 x =
+                        *reinterpret_cast<const u32x4 *>(scratch + row * 128 + ((chunk ^ (row & 7)) << 4));
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        x, out,
+                        h_out < job.H ? (16 * n0 + 32 * half + row) * ld + h_out * (int)sizeof(T)
+                                      : kGemmOutside,
+                        0, 0);
                 }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = 8 * q + row_in;
-                const u32x4 x =
-                    *reinterpret_cast<const u32x4 *>(scratch + row * 128 + ((chunk ^ (row & 7)) << 4));
-                __builtin_amdgcn_raw_buffer_store_b128(
-                    x, out,
-                    h_out < job.H ? (32 * half + row) * ld + h_out * (int)sizeof(T) : kGemmOutside, 0, 0);
             }
         }
     }
@@ -1511,10 +1684,14 @@ struct Plan {
     // backward
     int piece, pieces;       // columns (a multiple of 256), number
     int splits;              // of a piece, for grad_hidden: at most, all of them in the first one
-    size_t rows, place, count, flags, parts, scale, from, G, sums, rest, list, units, forward, backward;
+    size_t rows, place, count, flags, parts, scale, from, G, sums, rest, mask, list, units, forward, backward;
 
     // what rounding left of G's entries is added to the gradients
     bool listed(int elem) const { return elem == 2 && !low; }
+    // G has room for its second part
+    bool pair;
+    // a unit's entries are as many as a quarter of the rows (kMany)
+    bool many(int K, int V) const { return pair && (int64_t)K * kMany > V; }
 
     // grad_hidden together with the logits
     bool fused() const { return kc && bn == 16; }
@@ -1551,10 +1728,12 @@ Plan plan(int R, int H, int V, int K, int elem) {
     p.find = elem == 2 && !p.kc && p.bn <= 64 && K <= (p.bn <= 32 ? ring_list<32>() : ring_list<64>());
     p.low = elem == 2 && p.bn <= 64 ? p.bn : 0;
     p.grows = elem == 2 && p.few ? p.bn + p.low : R;
+    p.pair = p.listed(elem) && V < DFLASH2_MAX_K * kMany;
+    const int g_rows = p.pair ? 2 * p.grows : p.grows;
     p.nv = ceil_div(V, kTile);
     p.ring = !p.few && p.nv * (int64_t)p.nr <= kRingTiles;
     // a piece: whole rounds of tiles over the CUs, if as many fit
-    int64_t most = kPieceBytes / ((int64_t)p.grows * elem) / kTile;
+    int64_t most = kPieceBytes / ((int64_t)g_rows * elem) / kTile;
     most = most < 1 ? 1 : most > kPieceMost / kTile ? kPieceMost / kTile : most;
     int round = kCus;
     for (int n = p.nr; n % 2 == 0 && round > 1; n /= 2) round /= 2;
@@ -1586,7 +1765,7 @@ Plan plan(int R, int H, int V, int K, int elem) {
     p.forward = at;
     at = common;
     p.scale = take((size_t)R * sizeof(float2));
-    p.G = take((size_t)p.grows * p.piece * elem);
+    p.G = take((size_t)g_rows * p.piece * elem);
     const size_t split_rows = (size_t)kSplitTiles / ceil_div(H, kTile) * kTile;
     const size_t stream_rows = (size_t)p.nr * kTile > split_rows ? (size_t)p.nr * kTile : split_rows;
     const size_t sum_rows = p.fused() ? (size_t)p.rows_grid(width) * 16
@@ -1595,8 +1774,9 @@ Plan plan(int R, int H, int V, int K, int elem) {
     p.sums = take(sum_rows * H * 4);
     if (p.listed(elem)) {
         p.rest = take((size_t)R * DFLASH2_MAX_K * sizeof(float));
+        p.mask = take((size_t)R * sizeof(uint64_t));
         p.list = take((size_t)R * DFLASH2_MAX_K * sizeof(Listed));
-        p.units = take((size_t)(p.piece / kUnit + kListUnits) * sizeof(int2));
+        p.units = take((size_t)((int64_t)p.nv * kTile / kUnit + kListUnits) * sizeof(int2));
     }
     p.backward = at;
     return p;
@@ -1692,7 +1872,7 @@ void launch_hidden(const Plan &p, const HiddenJob &job, hipStream_t s) {
 WeightFewJob weight_few_job(const Plan &p, const WeightJob &job, int groups) {
     WeightFewJob w = {reinterpret_cast<const uint16_t *>(job.rows), job.G, job.count, job.from, job.H,
                       job.v0, job.v1, p.low, p.few ? p.grows : 0, job.ldg, ceil_div(job.H, 512), 0,
-                      static_cast<uint16_t *>(job.grad), job.list, job.units};
+                      static_cast<uint16_t *>(job.grad), job.rest};
     const int most = ceil_div(job.v1 - job.v0, 64);  // (a range has 64 columns at least)
     w.ranges = 8 * ceil_div(groups < (int64_t)most * w.slabs ? groups : most * w.slabs, 8 * w.slabs);
     return w;
@@ -1702,7 +1882,7 @@ template <typename T>
 void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
         lmloss_weight_kernel<T><<<job.nh * job.nv, kGemmThreads, 0, s>>>(job);
-    } else if (p.grows <= kTile) {
+    } else if (p.grows <= kTile && !job.low) {
         const WeightFewJob w = weight_few_job(p, job, kCus);
         const int grid = w.slabs * w.ranges;
         switch (p.low) {
@@ -1726,7 +1906,7 @@ void launch_weight(const Plan &p, const WeightJob &job, hipStream_t s) {
 // (125 tiles) 49 and 49; 100 rows x 1000 x 8000 63 and 70. Whether they were launched.
 bool launch_both(const Plan &p, const HiddenJob &hj, const WeightJob &wj, hipStream_t s) {
     const int groups = hj.nh * hj.nr * hj.splits;
-    if (!p.few || groups > kBothGroups) return false;
+    if (!p.few || groups > kBothGroups || wj.low) return false;
     const WeightFewJob w = weight_few_job(p, wj, kCus - groups);
     const dim3 grid(groups + w.slabs * w.ranges), block(kGemmThreads);
     switch (p.low) {
@@ -1840,25 +2020,46 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
     int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
     int32_t *from = reinterpret_cast<int32_t *>(ws + p.from);
     float2 *scale = reinterpret_cast<float2 *>(ws + p.scale);
-    if (!p.kc && !p.find) {
-        GatherJob gj = {};
-        gj.hidden = static_cast<const char *>(hidden);
-        gj.stats = const_cast<float *>(stats);
-        gj.grad_loss = grad_loss;
-        gj.e = e;
-        gj.R = R;
-        gj.H = H;
-        gj.V = V;
-        gj.rows = ws + p.rows;
-        gj.place = place;
-        gj.count = count;
-        gj.scale = scale;
-        lmloss_gather_kernel<T, Rows::kStats, 1><<<ceil_div(R, kGatherRows), 256, 0, s>>>(gj);
-    }
-    const bool fused = p.fused() && grad_hidden, listed = p.listed(sizeof(T));
+    const bool listed = p.listed(sizeof(T)), many = listed && grad_W && p.many(e.K, V);
     float *rest = listed ? reinterpret_cast<float *>(ws + p.rest) : nullptr;
-    Listed *list = listed ? reinterpret_cast<Listed *>(ws + p.list) : nullptr;
-    int2 *units = listed ? reinterpret_cast<int2 *>(ws + p.units) : nullptr;
+    uint64_t *mask = listed && e.teacher ? reinterpret_cast<uint64_t *>(ws + p.mask) : nullptr;
+    if (!p.kc && !p.find) {
+        KeepJob kj = {};
+        kj.hidden = static_cast<const char *>(hidden);
+        kj.stats = stats;
+        kj.grad_loss = grad_loss;
+        kj.R = R;
+        kj.H = H;
+        kj.K = e.K;
+        kj.tau = e.tau;
+        kj.rows = ws + p.rows;
+        kj.place = place;
+        kj.count = count;
+        kj.scale = scale;
+        if (listed && e.teacher) {
+            kj.ids = e.ids;
+            kj.teacher = e.teacher;
+            kj.V = V;
+            kj.mask = mask;
+        }
+        lmloss_keep_kernel<T><<<ceil_div(R, kKeepRows), kKeepThreads, 0, s>>>(kj);
+    }
+    ListsJob lists = {};
+    if (listed && grad_W && !many) {
+        const int units = p.nv * (kTile / kUnit), per = ceil_div(units, kCus / 2);
+        lists.ids = e.ids;
+        lists.mask = mask;
+        lists.n = R * e.K;
+        lists.K = e.K;
+        lists.V = V;
+        lists.inverse = e.K == 1 ? 0u : (uint32_t)(((1ull << 32) + e.K - 1) / e.K);
+        lists.per = per < kListUnits ? per : kListUnits;
+        lists.groups = ceil_div(units, lists.per);
+        lists.list = reinterpret_cast<Listed *>(ws + p.list);
+        lists.units = reinterpret_cast<int2 *>(ws + p.units);
+    }
+    const ListedRest left = {lists.list, lists.units, rest, static_cast<const uint16_t *>(hidden)};
+    const bool fused = p.fused() && grad_hidden;
     const int nh = ceil_div(H, kTile);
     for (int i = 0; i < p.pieces; ++i) {
         const int v0 = i * p.piece, v1 = v0 + p.piece < V ? v0 + p.piece : V;
@@ -1895,12 +2096,16 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
             lj.whole = p.few;
             launch_logits<T, true>(p, lj, s);
             if (!p.find) {
-                EntriesJob ej = {e, stats, grad_loss, place, R, V, v0, v1, c, lj.G, p.piece, p.low, rest};
-                lmloss_entries_kernel<T><<<ceil_div(R, 4), 256, 0, s>>>(ej);
-            }
-            if (rest && grad_W) {
-                ListsJob job = {e.ids, place, rest, R * e.K, e.K, v0, v1, list, units};
-                lmloss_lists_kernel<<<ceil_div(v1 - v0, kListUnits * kUnit), kListThreads, 0, s>>>(job);
+                const int low = many ? p.grows : p.low;
+                if (many) {
+                    const int64_t n = (int64_t)p.grows * p.piece / 8;  // (of bf16 rows of whole vectors)
+                    lmloss_zero_kernel<<<(int)(n / 1024 < 8 * kCus ? n / 1024 + 1 : 8 * kCus), 256, 0, s>>>(
+                        reinterpret_cast<u32x4 *>(ws + p.G) + n, n);
+                }
+                EntriesJob ej = {e, stats, grad_loss, place, R, V, v0, v1, c, lj.G, p.piece, low, rest, mask,
+                                 ceil_div(R, kKeepRows), lists};
+                lmloss_entries_kernel<T>
+                    <<<ej.groups + (i == 0 ? lists.groups : 0), kKeepThreads, 0, s>>>(ej);
             }
         }
         const int per = p.per(v1 - v0);
@@ -1910,7 +2115,7 @@ hipError_t backward(const Plan &p, const void *hidden, const void *W, Entries e,
         const bool found = p.kc || p.find;  // (the kept rows are where they were)
         const WeightJob wj = {found ? static_cast<const char *>(hidden) : ws + p.rows, ws + p.G, count,
                               found ? from : nullptr, H, v0, v1, p.piece, nh,
-                              sizeof(T) == 4 ? ceil_div(v1 - v0, 128) : nv, grad_W, list, units};
+                              sizeof(T) == 4 ? ceil_div(v1 - v0, 128) : nv, grad_W, left, many ? p.grows : 0};
         if constexpr (sizeof(T) == 2)
             if (grad_hidden && !fused && grad_W && launch_both(p, hj, wj, s)) continue;
         if (grad_hidden && !fused) launch_hidden<T>(p, hj, s);

@@ -394,8 +394,9 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
  *   grad_W         [V, H]  dtype, device, out, may be NULL (a frozen head): G^T . hidden. Written
  *                          in full. (At least one of the two is given; they overlap neither the
  *                          inputs nor each other.)
- *   bf16: G is rounded to bf16 before the two products (of at most 64 rows it is kept in two bf16
- *   parts, 16 bits); everything else is fp32, rounded once.
+ *   bf16: G is rounded to bf16 before the two products; of at most 64 rows it is kept in two bf16
+ *   parts, 16 bits, and of more at the row's entries of a 32nd of its largest mass and more.
+ *   Everything else is fp32, rounded once.
  *   Rows without an entry, or without teacher mass: loss 0, gradient 0; their hidden states are not
  *   read and their grad_loss counts for nothing (padding may hold anything, NaN too), and they cost
  *   nothing in the products. NaN, or
@@ -406,8 +407,9 @@ int dflash2_distill_step(const void *student, int student_dtype, const int32_t *
  *   1 <= K <= DFLASH2_MAX_K.
  * Workspace: dflash2_lmhead_loss_workspace_bytes(R, H, V, dtype, backward) bytes (backward 0 or 1:
  * of which call), contents need not be initialised. The backward call goes through the vocabulary
- * in pieces and keeps G of one of them there: 256 MiB at most, or R times 256 columns; beside it fp32
- * sums of grad_hidden, some 200 MiB at most or, where that is more, 4 R H bytes, and the kept rows.
+ * in pieces and keeps G of one of them there: 256 MiB at most, or R times 256 columns (512 where V
+ * is small); beside it fp32 sums of grad_hidden, some 200 MiB at most or, where that is more, 4 R H
+ * bytes, the kept rows, and below 1 KiB a row of entries.
  * Errors: DFLASH2_ERR_INVALID_ARG, DFLASH2_ERR_ALIGNMENT, DFLASH2_ERR_WORKSPACE, DFLASH2_ERR_HIP.
  */
 size_t dflash2_lmhead_loss_workspace_bytes(int R, int H, int V, int dtype, int backward);
