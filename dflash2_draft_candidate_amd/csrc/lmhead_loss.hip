@@ -315,7 +315,7 @@ __device__ __forceinline__ bool row_kept(const GatherJob &job, int r) {
 // instructions on the same values of k, one after the other, as the rings and streams make them
 // (another order of sums is 10^-4 off where logits are about 1000, which is all of a sure row's loss).
 // A wave reads 1 KB of its hidden row and of each entry's row of W at a time, through LDS of its own. H = 4096:
-// 64 entries of each of 1024 rows 93 us (537 MB, bound by these bytes), one of each 13 us. f32 waits for the chain
+// 64 entries of each of 1024 rows 76 - 93 us (537 MB, bound by these bytes), one of each 12 us. f32 waits for the chain
 // of its instructions, 4 us for every 1024 of H (15 us of a call more at H = 4096 than a free order of sums).
 template <typename T, Rows M, int ENTRIES>
 __global__ __launch_bounds__(256) void lmloss_gather_kernel(GatherJob job) {
@@ -1325,9 +1325,9 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_hidden_stream_kernel(Hidd
 }
 
 // grad_hidden from the splits' sums, added in a fixed order (and from the two parts of G, `low` rows
-// apart); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per WAVES-th split.
-// Bound by the latency of its loads: 1024 rows x 4096 in 4 splits, 37 us (75 MB, 2.0 TB/s). Few rows leave few
-// workgroups, and many splits a chain of loads; the calls for grad_hidden with 16 waves and with 4: 7 rows x 72 in
+// apart, or the entries' rests); zeros for the rows left out. Workgroup (x, y): 256 columns of row x, a wave per
+// WAVES-th split and entry. Bound by the latency of its loads: 1024 rows x 4096 in 4 splits, 37 us (75 MB, 2.0 TB/s),
+// 44 with an entry's rest a row, 58 with those of 64. Few rows leave few workgroups, and many splits a chain of loads; the calls for grad_hidden with 16 waves and with 4: 7 rows x 72 in
 // 256 splits, 29 us and 33; 40 x 256 x 50000, 38 and 41; 64 x 1024 x 50000 in 64, 62 and 63; 64 x 2048 in 32, 92
 // and 91; below that 4 are as fast or faster (331 x 1016 x 32003, f32: 385 us, with 16 waves 388).
 template <typename T, int WAVES>
@@ -1442,8 +1442,9 @@ __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_kernel(WeightJob j
     }
 }
 
-// bf16, more rows than that, or many entries: tiles of 256 columns of H x 256 vocabulary rows. 4096 rows x 4096 x 151936: 3.86
-// ms (1320 TFLOP/s); 1024 rows 1.15 ms (1100): of 16 K steps a tile, the end takes a sixth.
+// bf16, more rows than that, or many entries: tiles of 256 columns of H x 256 vocabulary rows. 4096 rows x 4096 x
+// 151936: 3.86 ms (1320 TFLOP/s); 1024 rows 1.15 ms (1100): of 16 K steps a tile, the end takes a sixth; with listed
+// entries, one a row, 1.21, with 64, 1.31.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void lmloss_weight_stream_kernel(WeightJob job) {
     typedef GemmStream<T, true, true, 16, true> Stream;

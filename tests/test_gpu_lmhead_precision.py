@@ -89,7 +89,7 @@ def compare(h, W, g, out, at, p, got_h, got_w, tau, columns):
 
 SIZES = [(65, 64, 64), (65, 1000, 700), (100, 2056, 3001), (128, 264, 64), (128, 4104, 1000), (129, 200, 700),
          (200, 1000, 2049), (256, 264, 513), (257, 264, 513), (331, 136, 20001), (600, 2056, 1500),
-         (700, 64, 300), (1024, 72, 140001), (3000, 64, 30001), (5000, 72, 1100)]
+         (700, 64, 300), (1024, 72, 140001), (3000, 64, 30001), (5000, 72, 1100), (65536, 8, 20001), (65536, 8, 900)]
 
 
 @pytest.mark.parametrize("R,H,V", SIZES)
